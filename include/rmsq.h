@@ -182,6 +182,79 @@ rmsq_status rmsnorm_quant_fp8_static_scratch(const void* input, const void* resi
                                              void* output, void* scale_output, int scale_dtype,
                                              void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * layernorm -- residual add + layer norm, in the input's type.
+ *
+ *   s    = RN_dtype(input + residual)                                  (or s = input)
+ *   mean = sum s / hidden;  rstd = 1 / sqrt(sum (s - mean)^2 / hidden + epsilon)     (fp32)
+ *   output = RN_dtype((s - mean) * rstd * (gamma + weight_offset) + beta)
+ *
+ *   beta             [hidden] of `dtype`, or NULL (0)
+ *   output           [rows x hidden] of `dtype`
+ *   mean, rstd       [rows] fp32, each NULL or what layernorm_backward reads
+ * Other arguments as for rmsnorm_quant_fp8, but hidden may be any number from 1 to
+ * RMSQ_MAX_HIDDEN (fp32: half of it), rows at most 2^27 - 1. output may be input, and residual_output
+ * may be residual or input (each element is read before it is written).
+ * A row with a NaN or an infinity gives NaN in that row alone.
+ * ------------------------------------------------------------------------------------------- */
+rmsq_status layernorm(const void* input, const void* residual, void* residual_output,
+                      const void* gamma, const void* beta, int64_t rows, int64_t hidden, int dtype,
+                      float epsilon, float weight_offset, void* output, float* mean, float* rstd,
+                      void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * layernorm_backward -- the gradients of layernorm.
+ *
+ *   xhat = (s - mean) * rstd;  g = grad_output * (gamma + weight_offset)
+ *   grad_input = RN_dtype(rstd * (g - <g> - xhat * <g * xhat>) + grad_residual)   (<.>: row mean)
+ *   grad_gamma = sum over rows of grad_output * xhat;  grad_beta = sum over rows of grad_output
+ *
+ *   grad_output      [rows x hidden] of `dtype`
+ *   grad_residual    [rows x hidden] of `dtype`: the gradient of residual_output, or NULL
+ *   input            [rows x hidden] of `dtype`: s, that is layernorm's residual_output where it
+ *                    had a residual and its input where not
+ *   mean, rstd       [rows] fp32, from layernorm
+ *   grad_input       [rows x hidden] of `dtype`: the gradient of s, so of input and of residual. It
+ *                    may be grad_output, grad_residual or input.
+ *   grad_gamma       [hidden] of `param_grad_dtype` (`dtype` or RMSQ_F32)
+ *   grad_beta        [hidden] of `param_grad_dtype`, or NULL
+ *   workspace        device memory of at least layernorm_backward_workspace(rows, hidden) bytes,
+ *                    16-byte aligned, used by this call alone until it ends on the stream (calls
+ *                    that may overlap need one each). Its contents before do not matter.
+ * Sums are held in fp32 and added in a fixed order: the same inputs give the same bits.
+ * rows == 0 writes zeros to grad_gamma and grad_beta. Sizes as for layernorm; RMSQ_ERR_SHAPE also for
+ * a workspace that is too small.
+ * ------------------------------------------------------------------------------------------- */
+#define RMSQ_LAYERNORM_PARTS 152
+int64_t layernorm_backward_workspace(int64_t rows, int64_t hidden);
+rmsq_status layernorm_backward(const void* grad_output, const void* grad_residual,
+                               const void* input, const void* gamma, const float* mean,
+                               const float* rstd, int64_t rows, int64_t hidden, int dtype,
+                               float weight_offset, void* grad_input, void* grad_gamma,
+                               void* grad_beta, int param_grad_dtype, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * layernorm_quant_int8, rmsnorm_quant_int8 -- residual add + norm + int8 codes with one scale per
+ * row, the form matmul_int8 reads.
+ *
+ *   y = the norm's fp32 value (layernorm above, or RMS norm as in this header's first lines)
+ *   scale = max_i |y_i| / 127;  q_i = RN_even(y_i / scale), in [-127, 127]
+ *
+ *   output           [rows x hidden] int8
+ *   scale_output     [rows] fp32; a row whose y is all zero gets codes 0 and scale 0
+ * Other arguments and sizes as for layernorm. Codes are formed with a reciprocal in fp32: one whose
+ * y_i / scale lies within 1e-4 of a half may be either neighbour.
+ * ------------------------------------------------------------------------------------------- */
+rmsq_status layernorm_quant_int8(const void* input, const void* residual, void* residual_output,
+                                 const void* gamma, const void* beta, int64_t rows, int64_t hidden,
+                                 int dtype, float epsilon, float weight_offset, void* output,
+                                 float* scale_output, void* stream);
+rmsq_status rmsnorm_quant_int8(const void* input, const void* residual, void* residual_output,
+                               const void* gamma, int64_t rows, int64_t hidden, int dtype,
+                               float epsilon, float weight_offset, void* output, float* scale_output,
+                               void* stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* rmsq_status_string(rmsq_status status);
 

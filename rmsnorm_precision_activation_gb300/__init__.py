@@ -12,7 +12,9 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 import os
 
 import torch
@@ -41,6 +43,11 @@ SIGNATURES = {
     "rmsnorm_quant_nvfp4": ([_P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _P, _I, _P], _I),
     "rmsnorm_quant_mxfp4": ([_P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _I, _P], _I),
     "rmsnorm_nvfp4_global_scale": ([_P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P], _I),
+    "layernorm": ([_P, _P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _P, _P], _I),
+    "layernorm_backward_workspace": ([_I64, _I64], _I64),
+    "layernorm_backward": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I, _F, _P, _P, _P, _I, _P, _I64, _P], _I),
+    "layernorm_quant_int8": ([_P, _P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _P], _I),
+    "rmsnorm_quant_int8": ([_P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _P], _I),
     "rmsq_status_string": ([_I], ctypes.c_char_p),
     "rmsq_device_status": ([], _I),
     "rmsq_set_schedule": ([_I], _I),
@@ -234,6 +241,138 @@ def rmsnorm_nvfp4_global_scale(input, gamma, *, residual=None, epsilon=1e-6, wei
                                               _stream(input.device, stream))
     _check(st, "rmsnorm_nvfp4_global_scale")
     return out
+
+
+def _given(t, name, shape, dtype, device):
+    """t, or a new tensor; a given one must be exactly what the kernel writes."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.numel() != math.prod(shape):
+        raise ValueError("%s must be a contiguous %s tensor of %d elements on %s"
+                         % (name, dtype, math.prod(shape), device))
+    return t
+
+
+def _prepare_norm(input, gamma, beta, residual, residual_output):
+    x, r, ro, residual_output, H = _prepare(input, gamma, residual, residual_output)
+    if beta is not None and (beta.shape != (H,) or not beta.is_contiguous()
+                             or beta.dtype != input.dtype or beta.device != input.device):
+        raise ValueError("beta must be a contiguous %s tensor of shape (%d,) on %s"
+                         % (input.dtype, H, input.device))
+    if residual_output is not None:
+        _given(residual_output, "residual_output", input.shape, input.dtype, input.device)
+    return x, r, ro, residual_output, H
+
+
+@contextlib.contextmanager
+def _queue(device, stream):
+    """The device and the stream the call is queued on; tensors made inside belong to the stream."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device)
+        else:
+            with torch.cuda.stream(stream):
+                yield stream
+
+
+def layernorm(input, gamma, beta=None, *, residual=None, residual_output=None, epsilon=1e-5,
+              weight_offset=0.0, output=None, stats=False, stream=None):
+    """Residual add + layer norm, in the input's type; any hidden size up to MAX_HIDDEN.
+
+    Returns (output [..., H], residual_output, mean [...], rstd [...]); mean and rstd are the fp32
+    statistics layernorm_backward reads, None unless stats is true."""
+    with _queue(input.device, stream) as queue:
+        x, r, ro, residual_output, H = _prepare_norm(input, gamma, beta, residual, residual_output)
+        output = _given(output, "output", input.shape, input.dtype, input.device)
+        mean = rstd = None
+        if stats:
+            mean = torch.empty(input.shape[:-1], dtype=torch.float32, device=input.device)
+            rstd = torch.empty(input.shape[:-1], dtype=torch.float32, device=input.device)
+        st = lib().layernorm(_ptr(x), _ptr(r), _ptr(ro), _ptr(gamma), _ptr(beta), x.shape[0], H,
+                             _DT[input.dtype], float(epsilon), float(weight_offset), _ptr(output),
+                             _ptr(mean), _ptr(rstd), _stream(input.device, queue))
+    _check(st, "layernorm")
+    return output, residual_output, mean, rstd
+
+
+def layernorm_backward_workspace(rows: int, hidden: int) -> int:
+    """Bytes of workspace layernorm_backward needs."""
+    return lib().layernorm_backward_workspace(int(rows), int(hidden))
+
+
+def layernorm_backward(grad_output, input, gamma, mean, rstd, *, grad_residual=None,
+                       weight_offset=0.0, grad_input=None, grad_gamma=None, grad_beta=None,
+                       param_grad_dtype=None, workspace=None, stream=None):
+    """The gradients of layernorm. input: what was normalised (layernorm's residual_output where it
+    had a residual); grad_residual: the gradient that reaches residual_output from elsewhere.
+    param_grad_dtype: type of grad_gamma and grad_beta, the input's (default) or torch.float32.
+    workspace: a CUDA uint8 tensor of layernorm_backward_workspace(rows, H) bytes, allocated when
+    not passed.
+
+    Returns (grad_input [..., H], grad_gamma [H], grad_beta [H])."""
+    with _queue(input.device, stream) as queue:
+        x, _, _, _, H = _prepare(input, gamma, None, None)
+        rows = x.shape[0]
+        for name, t in (("grad_output", grad_output), ("grad_residual", grad_residual)):
+            if t is not None and (t.shape != input.shape or not t.is_contiguous()
+                                  or t.dtype != input.dtype or t.device != input.device):
+                raise ValueError("%s must be a contiguous tensor of the input's shape, type and device" % name)
+        for name, t in (("mean", mean), ("rstd", rstd)):
+            if (t.dtype != torch.float32 or t.device != input.device or not t.is_contiguous()
+                    or t.numel() != rows):
+                raise ValueError("%s must be a contiguous float32 tensor of %d elements" % (name, rows))
+        pdt = param_grad_dtype or input.dtype
+        if pdt not in (input.dtype, torch.float32):
+            raise TypeError("param_grad_dtype must be the input's dtype or float32")
+        grad_input = _given(grad_input, "grad_input", input.shape, input.dtype, input.device)
+        grad_gamma = _given(grad_gamma, "grad_gamma", (H,), pdt, input.device)
+        grad_beta = _given(grad_beta, "grad_beta", (H,), pdt, input.device)
+        need = layernorm_backward_workspace(rows, H)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=input.device)
+        if workspace.device != input.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % input.device)
+        st = lib().layernorm_backward(
+            _ptr(grad_output), _ptr(grad_residual), _ptr(x), _ptr(gamma), _ptr(mean), _ptr(rstd),
+            rows, H, _DT[input.dtype], float(weight_offset), _ptr(grad_input), _ptr(grad_gamma),
+            _ptr(grad_beta), _DT[pdt], _ptr(workspace), workspace.numel() * workspace.element_size(),
+            _stream(input.device, queue))
+    _check(st, "layernorm_backward")
+    return grad_input, grad_gamma, grad_beta
+
+
+def _norm_quant_int8(name, input, gamma, beta, residual, residual_output, epsilon, weight_offset,
+                     output, scale_output, stream):
+    with _queue(input.device, stream) as queue:
+        x, r, ro, residual_output, H = _prepare_norm(input, gamma, beta, residual, residual_output)
+        output = _given(output, "output", input.shape, torch.int8, input.device)
+        scale_output = _given(scale_output, "scale_output", input.shape[:-1], torch.float32, input.device)
+        head = (_ptr(x), _ptr(r), _ptr(ro), _ptr(gamma))
+        if name == "layernorm_quant_int8":
+            head += (_ptr(beta),)
+        st = getattr(lib(), name)(*head, x.shape[0], H, _DT[input.dtype], float(epsilon),
+                                  float(weight_offset), _ptr(output), _ptr(scale_output),
+                                  _stream(input.device, queue))
+    _check(st, name)
+    return output, scale_output, residual_output
+
+
+def layernorm_quant_int8(input, gamma, beta=None, *, residual=None, residual_output=None,
+                         epsilon=1e-5, weight_offset=0.0, output=None, scale_output=None, stream=None):
+    """Residual add + layer norm + int8 codes with one fp32 scale per row (max |y| / 127).
+
+    Returns (output int8 [..., H], scale_output float32 [...], residual_output)."""
+    return _norm_quant_int8("layernorm_quant_int8", input, gamma, beta, residual, residual_output,
+                            epsilon, weight_offset, output, scale_output, stream)
+
+
+def rmsnorm_quant_int8(input, gamma, *, residual=None, residual_output=None, epsilon=1e-6,
+                       weight_offset=0.0, output=None, scale_output=None, stream=None):
+    """Residual add + RMSNorm + int8 codes with one fp32 scale per row (max |y| / 127).
+
+    Returns (output int8 [..., H], scale_output float32 [...], residual_output)."""
+    return _norm_quant_int8("rmsnorm_quant_int8", input, gamma, None, residual, residual_output,
+                            epsilon, weight_offset, output, scale_output, stream)
 
 
 def rmsq_device_status() -> int:

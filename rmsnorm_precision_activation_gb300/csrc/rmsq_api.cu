@@ -9,6 +9,7 @@
 
 #include "rmsq.h"
 #include "rmsq_host.h"
+#include "rmsq_ops.h"
 
 namespace rmsq {
 
@@ -206,6 +207,71 @@ cudaError_t run_kernel(const void* fn, const Plan& pl, const Params& p, cudaStre
         cfg.numAttrs = 2;
     }
     cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
+    if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
+    return e;
+}
+
+// ------------------------------------------------------------------------------------------
+// What the layer-norm and int8 operators share (rmsq_ops.h)
+// ------------------------------------------------------------------------------------------
+
+bool device_view(DeviceView* v)
+{
+    const DeviceInfo* di = device_info();
+    if (!di) return false;
+    v->sms = di->sms;
+    v->smem_optin = di->smem_optin;
+    v->err = di->err;
+    v->timeout_ns = g_timeout_ns.load();
+    return true;
+}
+
+struct ReadyFn {
+    const void* fn;
+    int dev;
+};
+static ReadyFn g_ready[512];
+static int g_nready = 0;
+
+cudaError_t launch_kernel(const void* fn, unsigned grid, unsigned threads, int smem, int cluster,
+                          cudaStream_t stream, void** args)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        int i = 0;
+        while (i < g_nready && !(g_ready[i].fn == fn && g_ready[i].dev == dev)) ++i;
+        if (i == g_nready) {
+            cudaFuncAttributes fa;
+            e = cudaFuncGetAttributes(&fa, fn);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     g_dev[dev].smem_optin - static_cast<int>(fa.sharedSizeBytes));
+            // clusters of 16 CTAs are beyond the portable size of 8
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            if (g_nready < static_cast<int>(sizeof(g_ready) / sizeof(g_ready[0])))
+                g_ready[g_nready++] = ReadyFn{fn, dev};
+        }
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = g_pdl.load() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    e = cudaLaunchKernelExC(&cfg, fn, args);
     if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
     return e;
 }

@@ -1,0 +1,78 @@
+// rmsq_ops.h -- host-side plumbing of the layer-norm and int8 operators: what they share with the
+// quantising RMS-norm entry points (device facts, launches), and their dispatch.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "rmsq.h"
+#include "rmsq_norm.cuh"
+
+namespace rmsq {
+
+// Facts about the current device and the process's settings (rmsq_api.cu).
+struct DeviceView {
+    int sms;
+    int smem_optin;
+    unsigned int* err;                // device error word
+    unsigned long long timeout_ns;    // bound of device-side waits
+};
+// False: no usable device.
+bool device_view(DeviceView* v);
+
+// Launches fn on the stream with programmatic dependent launch (as rmsq_set_pdl says), in clusters
+// of `cluster` CTAs when that is over 1, and counts the launch. Sets the function's attributes on
+// its first launch on a device.
+cudaError_t launch_kernel(const void* fn, unsigned grid, unsigned threads, int smem, int cluster,
+                          cudaStream_t stream, void** args);
+
+struct NormPlan {
+    int dt;
+    int elems;      // per thread: 8, 16 or 32
+    bool vec;
+    int scope;
+    int threads;
+    unsigned grid;
+    int cluster;
+};
+
+cudaError_t norm_layer(const NormPlan& pl, const NormParams& p, cudaStream_t stream);
+cudaError_t norm_layer_int8(const NormPlan& pl, const NormParams& p, cudaStream_t stream);
+cudaError_t norm_rms_int8(const NormPlan& pl, const NormParams& p, cudaStream_t stream);
+
+// Backward pass (rmsq_norm_bwd.cu): the row kernel for a type, elements per thread (8 or 16) and
+// alignment, and the column reduction.
+struct NormBwdParams;
+const void* norm_bwd_fn(int dt, int elems, bool vec);
+const void* norm_bwd_reduce_fn();
+
+#define RMSQ_DEFINE_NORM_DISPATCH(NAME, KIND)                                                     \
+    template <int DT, bool VEC> static const void* NAME##_fn(const NormPlan& pl)                  \
+    {                                                                                             \
+        switch (pl.scope * 64 + pl.elems) {                                                       \
+        case SCOPE_WARP * 64 + 8:                                                                 \
+            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 8, VEC, SCOPE_WARP, KIND>); \
+        case SCOPE_WARP * 64 + 16:                                                                \
+            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 16, VEC, SCOPE_WARP, KIND>); \
+        case SCOPE_WARP * 64 + 32:                                                                \
+            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 32, VEC, SCOPE_WARP, KIND>); \
+        case SCOPE_CTA * 64 + 16:                                                                 \
+            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 16, VEC, SCOPE_CTA, KIND>); \
+        case SCOPE_CTA * 64 + 32:                                                                 \
+            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 32, VEC, SCOPE_CTA, KIND>); \
+        case SCOPE_CLUSTER * 64 + 32:                                                             \
+            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 32, VEC, SCOPE_CLUSTER, KIND>); \
+        }                                                                                         \
+        return nullptr;                                                                           \
+    }                                                                                             \
+    cudaError_t NAME(const NormPlan& pl, const NormParams& p, cudaStream_t stream)                \
+    {                                                                                             \
+        const void* fn = pl.dt == DT_BF16 ? (pl.vec ? NAME##_fn<DT_BF16, true>(pl) : NAME##_fn<DT_BF16, false>(pl)) \
+                       : pl.dt == DT_FP16 ? (pl.vec ? NAME##_fn<DT_FP16, true>(pl) : NAME##_fn<DT_FP16, false>(pl)) \
+                                          : (pl.vec ? NAME##_fn<DT_F32, true>(pl) : NAME##_fn<DT_F32, false>(pl)); \
+        if (fn == nullptr) return cudaErrorInvalidConfiguration;                                  \
+        NormParams q = p;                                                                         \
+        void* args[] = {&q};                                                                      \
+        return launch_kernel(fn, pl.grid, pl.threads, 0, pl.cluster, stream, args);               \
+    }
+
+}  // namespace rmsq
