@@ -255,6 +255,27 @@ rmsq_status rmsnorm_quant_int8(const void* input, const void* residual, void* re
                                float epsilon, float weight_offset, void* output, float* scale_output,
                                void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * matmul_int8 -- product of int8 codes with a scale per token and per output channel.
+ *
+ *   output[i][j] = RN((sum_c input[i][c] * weight[j][c]) * input_scale[i] * weight_scale[j] + bias[j])
+ *
+ *   input            [m x k] int8, input_scale [m] fp32: the codes and scales of
+ *                    layernorm_quant_int8 / rmsnorm_quant_int8, or any others
+ *   weight           [n x k] int8 (a row per output channel), weight_scale [n] fp32
+ *   bias             [n] of `output_dtype`, or NULL
+ *   output           [m x n] of `output_dtype` (an rmsq_dtype)
+ * k is a multiple of 16 up to RMSQ_MATMUL_MAX_K (up to there no sum leaves 32 bits, whatever the
+ * codes); m and n are at most RMSQ_MATMUL_MAX_ROWS, any numbers; RMSQ_ERR_SHAPE otherwise. m == 0 or
+ * n == 0 launches nothing. The integer sums are exact, so outputs do not depend on how the work is
+ * split; the scales are applied in fp32 and the result is rounded once.
+ * ------------------------------------------------------------------------------------------- */
+#define RMSQ_MATMUL_MAX_K 131056
+#define RMSQ_MATMUL_MAX_ROWS 8388608
+rmsq_status matmul_int8(const void* input, const float* input_scale, const void* weight,
+                        const float* weight_scale, const void* bias, int64_t m, int64_t n, int64_t k,
+                        void* output, int output_dtype, void* stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* rmsq_status_string(rmsq_status status);
 

@@ -48,6 +48,7 @@ SIGNATURES = {
     "layernorm_backward": ([_P, _P, _P, _P, _P, _P, _I64, _I64, _I, _F, _P, _P, _P, _I, _P, _I64, _P], _I),
     "layernorm_quant_int8": ([_P, _P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _P], _I),
     "rmsnorm_quant_int8": ([_P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _P], _I),
+    "matmul_int8": ([_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _P], _I),
     "rmsq_status_string": ([_I], ctypes.c_char_p),
     "rmsq_device_status": ([], _I),
     "rmsq_set_schedule": ([_I], _I),
@@ -373,6 +374,41 @@ def rmsnorm_quant_int8(input, gamma, *, residual=None, residual_output=None, eps
     Returns (output int8 [..., H], scale_output float32 [...], residual_output)."""
     return _norm_quant_int8("rmsnorm_quant_int8", input, gamma, None, residual, residual_output,
                             epsilon, weight_offset, output, scale_output, stream)
+
+
+def matmul_int8(input, input_scale, weight, weight_scale, *, bias=None, out_dtype=torch.bfloat16,
+                output=None, stream=None):
+    """(input @ weight.T) * input_scale * weight_scale + bias on int8 codes, integer sums exact.
+
+    input int8 [..., K] with one fp32 scale per row, weight int8 [N, K] with one fp32 scale per
+    output channel, bias [N] of out_dtype. K must be a multiple of 16.
+
+    Returns output [..., N] of out_dtype."""
+    with _queue(input.device, stream) as queue:
+        if not input.is_cuda:
+            raise ValueError("input must be a CUDA tensor")
+        if input.dtype != torch.int8 or weight.dtype != torch.int8:
+            raise TypeError("input and weight must be int8")
+        if out_dtype not in _DT:
+            raise TypeError("out_dtype must be bfloat16, float16 or float32")
+        K = input.shape[-1]
+        if weight.dim() != 2 or weight.shape[1] != K:
+            raise ValueError("weight must have shape (N, %d)" % K)
+        N, M = weight.shape[0], math.prod(input.shape[:-1])
+        for name, t, n, dtype in (("input", input, M * K, torch.int8), ("weight", weight, N * K, torch.int8),
+                                  ("input_scale", input_scale, M, torch.float32),
+                                  ("weight_scale", weight_scale, N, torch.float32),
+                                  ("bias", bias, N, out_dtype)):
+            if t is not None and (not t.is_contiguous() or t.dtype != dtype or t.device != input.device
+                                  or t.numel() != n):
+                raise ValueError("%s must be a contiguous %s tensor of %d elements on %s"
+                                 % (name, dtype, n, input.device))
+        output = _given(output, "output", input.shape[:-1] + (N,), out_dtype, input.device)
+        st = lib().matmul_int8(_ptr(input), _ptr(input_scale), _ptr(weight), _ptr(weight_scale),
+                               _ptr(bias), M, N, K, _ptr(output), _DT[out_dtype],
+                               _stream(input.device, queue))
+    _check(st, "matmul_int8")
+    return output
 
 
 def rmsq_device_status() -> int:

@@ -233,7 +233,7 @@ struct ReadyFn {
 static ReadyFn g_ready[512];
 static int g_nready = 0;
 
-cudaError_t launch_kernel(const void* fn, unsigned grid, unsigned threads, int smem, int cluster,
+cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem, int cluster,
                           cudaStream_t stream, void** args)
 {
     int dev = 0;
@@ -258,7 +258,7 @@ cudaError_t launch_kernel(const void* fn, unsigned grid, unsigned threads, int s
         }
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;

@@ -22,7 +22,7 @@ bool device_view(DeviceView* v);
 // Launches fn on the stream with programmatic dependent launch (as rmsq_set_pdl says), in clusters
 // of `cluster` CTAs when that is over 1, and counts the launch. Sets the function's attributes on
 // its first launch on a device.
-cudaError_t launch_kernel(const void* fn, unsigned grid, unsigned threads, int smem, int cluster,
+cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem, int cluster,
                           cudaStream_t stream, void** args);
 
 struct NormPlan {
