@@ -1,7 +1,8 @@
 // rmsq_matmul.cu -- C ABI of the int8 product: argument checks and the choice of kernel.
+#include <atomic>
 #include <cstdint>
 
-#include "rmsq_matmul.cuh"
+#include "rmsq_matmul_tc.cuh"
 #include "rmsq_ops.h"
 
 namespace rmsq {
@@ -23,6 +24,65 @@ static cudaError_t launch_few(MatmulParams& p, const DeviceView& dv, cudaStream_
     void* args[] = {&p};
     return launch_kernel(fn, dim3(static_cast<unsigned>((tiles + per - 1) / per), static_cast<unsigned>(mtiles)),
                          kFewWarps * 32, 0, 1, stream, args);
+}
+
+// cuTensorMapEncodeTiled from the driver (the library does not link it).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn encode_fn()
+{
+    static std::atomic<void*> fn{nullptr};
+    void* f = fn.load();
+    if (f == nullptr) {
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess || found != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(f);
+    }
+    return reinterpret_cast<EncodeFn>(f);
+}
+
+// Codes [rows x k], read in boxes of box_rows x 64 elements; what lies outside reads as 0.
+static bool encode(CUtensorMap* map, const void* codes, long long rows, int k, int box_rows)
+{
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k)};
+    const cuuint32_t box[2] = {kTcStep, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, step,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT> static cudaError_t launch_tc(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
+{
+    CUtensorMap map_w, map_a;
+    if (!encode(&map_w, p.w, p.n, p.k, kTcRows) || !encode(&map_a, p.a, p.m, p.k, NT)) return cudaErrorUnknown;
+    TcTiles t;
+    t.n_tiles = static_cast<int>((p.n + kTcRows - 1) / kTcRows);
+    t.m_tiles = static_cast<int>((p.m + NT - 1) / NT);
+    const long long tiles = static_cast<long long>(t.n_tiles) * t.m_tiles;
+    // CTAs that share a tile's k: while that leaves no SM with two tiles and each CTA 4 stages
+    int cluster = 1;
+    const int steps = (p.k + kTcStep - 1) / kTcStep;
+    while (cluster < 8 && tiles * cluster * 2 <= dv.sms && steps >= 8 * cluster) cluster *= 2;
+    const long long grid = cluster > 1 ? tiles * cluster : tiles < dv.sms ? tiles : dv.sms;
+    void* args[] = {&map_w, &map_a, &p, &t};
+    return launch_kernel(reinterpret_cast<const void*>(&rmsq_matmul_tc_kernel<NT>),
+                         dim3(static_cast<unsigned>(grid)), kTcThreads, TcShape<NT>::SMEM, cluster, stream, args);
+}
+
+static cudaError_t launch_matmul(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
+{
+    if (p.m <= 8) return launch_few(p, dv, stream);
+    if (p.m <= 16) return launch_tc<16>(p, dv, stream);
+    if (p.m <= 32) return launch_tc<32>(p, dv, stream);
+    if (p.m <= 64) return launch_tc<64>(p, dv, stream);
+    return launch_tc<128>(p, dv, stream);
 }
 
 }  // namespace rmsq
@@ -58,7 +118,7 @@ extern "C" rmsq_status matmul_int8(const void* input, const float* input_scale, 
     p.k = static_cast<int>(k);
     p.dt = output_dtype;
     p.timeout_ns = dv.timeout_ns;
-    const cudaError_t e = launch_few(p, dv, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_matmul(p, dv, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) return RMSQ_OK;
     cudaGetLastError();
     return RMSQ_ERR_LAUNCH;

@@ -37,6 +37,13 @@ __device__ __forceinline__ void store_as(void* p, long long i, int dt, float v)
     else static_cast<uint16_t*>(p)[i] = dt == DT_BF16 ? Scalar<DT_BF16>::put(v) : Scalar<DT_FP16>::put(v);
 }
 
+// A sum to the output's fp32 value: one rounding each, in the same order in every kernel.
+__device__ __forceinline__ float scaled(int sum, float a_scale, float w_scale, float bias, bool has_bias)
+{
+    const float v = __fmul_rn(__fmul_rn(__int2float_rn(sum), a_scale), w_scale);
+    return has_bias ? __fadd_rn(v, bias) : v;
+}
+
 __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc)
 {
     acc = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), acc);
@@ -99,9 +106,8 @@ __global__ void __launch_bounds__(kFewWarps * 32) rmsq_matmul_few_kernel(const M
         if (n < p.n && m < p.m) {
             int s = 0;
             for (int q = 0; q < p.ksplit; ++q) s += part[row / kFewRows * p.ksplit + q][row % kFewRows * MT + i];
-            float v = static_cast<float>(s) * p.a_scale[m] * p.w_scale[n];
-            if (p.bias) v += load_as(p.bias, n, p.dt);
-            store_as(p.out, m * p.n + n, p.dt, v);
+            store_as(p.out, m * p.n + n, p.dt,
+                     scaled(s, p.a_scale[m], p.w_scale[n], p.bias ? load_as(p.bias, n, p.dt) : 0.f, p.bias));
         }
     }
 }

@@ -1,0 +1,386 @@
+// rmsq_matmul_tc.cuh -- the int8 product on the tensor cores.
+//
+// sm_103a's tcgen05 has no 8-bit-integer kind, so the codes go through its fp16 kind: a code is
+// exact in fp16, a product of two is at most 2^14, and fp32 sums of up to 1024 products are whole
+// numbers of at most 2^24, so exact. The fp32 accumulator is therefore read out and added to 32-bit
+// integers every 1024 elements of k (kChunk stages), which makes every sum exact.
+//
+// A CTA takes 128 output channels (the MMA's rows) and NT tokens (its columns). Per stage of 64
+// elements of k:
+//   warp 0       TMA loads the codes of both tiles into a ring (64-byte swizzle)
+//   warps 4-11   two warpgroups, stages in turn, turn codes into fp16: the channels' straight into
+//                TMEM (the MMA takes its first operand from there, which spares shared memory a
+//                write and a read), the tokens' into shared memory (128-byte swizzle)
+//   warp 1       one thread issues tcgen05.mma, four per stage
+//   warps 12-19  two warpgroups read the accumulator out, half of the tokens each, and write the
+//                output
+// The weight is read as codes, so a call with few tokens streams one byte per weight; CTAs of a
+// cluster then share a tile's k and add their integer sums through distributed shared memory.
+//
+// Every wait is bounded: a role whose wait runs out leaves its loop, the MMA and copy roles wait
+// (bounded again) for what they have in flight, and the CTA frees its TMEM and ends.
+#pragma once
+
+#include <cuda.h>
+
+#include "rmsq_matmul.cuh"
+
+namespace rmsq {
+
+constexpr int kTcThreads = 640;
+constexpr int kTcStep = 64;              // elements of k per stage
+constexpr int kTcChunk = 1024 / kTcStep; // stages per read-out of the accumulator
+constexpr int kTcRows = 128;             // output channels per CTA
+
+template <int NT> struct TcShape {
+    static constexpr int RAW_A = kTcRows * kTcStep;
+    static constexpr int RAW_B = (NT * kTcStep + 1023) / 1024 * 1024;
+    static constexpr int RAW = RAW_A + RAW_B;
+    static constexpr int OP = NT * kTcStep * 2;
+    static constexpr int OPS = 4;                                     // operand stages
+    static constexpr int RAWS = NT >= 128 ? 8 : NT >= 64 ? 12 : 14;   // code stages
+    // 1024 bytes to align the ring, 1024 for barriers; over half of an SM's shared memory, so one
+    // CTA per SM, which may take all of TMEM
+    static constexpr int SMEM = 2048 + RAWS * RAW + OPS * OP;
+    static_assert(SMEM > 116 * 1024 && SMEM <= 232448, "one CTA per SM");
+    static_assert(RAWS * RAW + OPS * OP >= NT * kTcRows * 4, "the cluster's sums reuse the ring");
+};
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Arrives on bar when every MMA this thread has issued is done.
+__device__ __forceinline__ void tc_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// d (+)= a b^T: a fp16 in TMEM (128 lanes, 8 columns), b fp16 in shared memory (K-major).
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+// K-major operand with 128-byte swizzle: groups of 8 rows are 1024 bytes apart.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr)
+{
+    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Four codes to four fp16: with the sign bit flipped a code is b = code + 128; the fp16 with high
+// byte 0x64 and low byte b is 1024 + b, from which 1152 is subtracted exactly.
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    lo = __byte_perm(u, 0x64646464u, 0x4140);
+    hi = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
+}
+
+__device__ __forceinline__ void tmem_st_x8(uint32_t addr, const uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                 ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// 8 columns of this warp's lanes; values are valid after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld_x8(uint32_t addr, uint32_t* v)
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ int4 ld_cluster_i4(uint32_t addr, uint32_t rank)
+{
+    uint32_t raddr;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(raddr) : "r"(addr), "r"(rank));
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(raddr) : "memory");
+    return v;
+}
+
+struct TcTiles {
+    int n_tiles, m_tiles;
+};
+
+// Tiles in groups of 8 channel tiles, tokens fastest within a group's column, so that the CTAs
+// running at one time share both operands in L2.
+__device__ __forceinline__ void tc_tile(long long i, const TcTiles& t, int& n, int& m)
+{
+    const long long per = 8LL * t.m_tiles;
+    const int group = static_cast<int>(i / per), in = static_cast<int>(i % per);
+    const int first = group * 8, width = t.n_tiles - first < 8 ? t.n_tiles - first : 8;
+    n = first + in % width;
+    m = in / width;
+}
+
+template <int NT>
+__global__ void __launch_bounds__(kTcThreads, 1)
+rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                      const MatmulParams p, const TcTiles tiles)
+{
+    using S = TcShape<NT>;
+    constexpr int OPS = S::OPS, RAWS = S::RAWS;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint32_t tmem_slot;
+
+    unsigned char* const smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char* const raw = smem;
+    unsigned char* const ops = smem + RAWS * S::RAW;
+    const uint32_t bars = smem_u32(ops + OPS * S::OP);
+    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * RAWS;
+    const uint32_t op_full = raw_empty + 8 * RAWS, op_empty = op_full + 8 * OPS;
+    const uint32_t acc_full = op_empty + 8 * OPS, acc_empty = acc_full + 8, drain = acc_empty + 8;
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t nc = cluster_size(), rank = cluster_rank();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < RAWS; ++i) {
+            mbar_init(raw_full + 8 * i, 1);
+            mbar_init(raw_empty + 8 * i, 4);
+        }
+        for (int i = 0; i < OPS; ++i) {
+            mbar_init(op_full + 8 * i, 4);
+            mbar_init(op_empty + 8 * i, 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 8);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem_a = tmem + 256;      // operand stages of 32 columns behind the accumulator
+    pdl_wait();
+
+    const int steps_all = (p.k + kTcStep - 1) / kTcStep;
+    const int k0 = static_cast<int>(static_cast<long long>(steps_all) * rank / nc);
+    const int steps = static_cast<int>(static_cast<long long>(steps_all) * (rank + 1) / nc) - k0;
+    const long long ntiles = static_cast<long long>(tiles.n_tiles) * tiles.m_tiles;
+    const long long first = cluster_id(), stride = cluster_count();
+    const unsigned long long limit = p.timeout_ns;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            long long it = 0;
+            for (long long tile = first; tile < ntiles && ok; tile += stride) {
+                int tn, tm;
+                tc_tile(tile, tiles, tn, tm);
+                for (int s = 0; s < steps; ++s, ++it) {
+                    const int slot = static_cast<int>(it % RAWS);
+                    const uint32_t phase = static_cast<uint32_t>(it / RAWS) & 1u;
+                    ok = mbar_wait_bounded(raw_empty + 8 * slot, phase ^ 1u, limit);
+                    if (!ok) break;
+                    const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw + slot * S::RAW);
+                    mbar_arrive_expect_tx(full, S::RAW_A + NT * kTcStep);
+                    tma_load_2d(dst, &map_w, (k0 + s) * kTcStep, tn * kTcRows, full);
+                    tma_load_2d(dst + S::RAW_A, &map_a, (k0 + s) * kTcStep, tm * NT, full);
+                }
+            }
+            if (!ok) {
+                // the copies in flight end before the CTA does
+                bool drained = true;
+                for (long long i = it > RAWS ? it - RAWS : 0; i < it; ++i)
+                    drained &= mbar_wait_bounded(raw_full + 8 * static_cast<int>(i % RAWS),
+                                                 static_cast<uint32_t>(i / RAWS) & 1u, 4 * limit);
+                atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(NT / 8) << 17) | ((kTcRows / 16u) << 24);
+            long long it = 0, chunks = 0;
+            for (long long tile = first; tile < ntiles && ok; tile += stride) {
+                for (int s = 0; s < steps && ok; ++s, ++it) {
+                    const int slot = static_cast<int>(it % OPS);
+                    const bool head = s % kTcChunk == 0, tail = s % kTcChunk == kTcChunk - 1 || s == steps - 1;
+                    if (head) ok = mbar_wait_bounded(acc_empty, static_cast<uint32_t>(chunks & 1) ^ 1u, limit);
+                    ok = ok && mbar_wait_bounded(op_full + 8 * slot, static_cast<uint32_t>(it / OPS) & 1u, limit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t desc = tc_desc(smem_u32(ops + slot * S::OP));
+#pragma unroll
+                    for (int k = 0; k < kTcStep / 16; ++k)
+                        tc_mma(tmem, tmem_a + slot * 32 + k * 8, desc + 2 * k, idesc, !(head && k == 0));
+                    tc_commit(op_empty + 8 * slot);
+                    if (tail) {
+                        tc_commit(acc_full);
+                        ++chunks;
+                    }
+                }
+            }
+            if (!ok) {
+                // the MMAs in flight end before TMEM is freed
+                tc_commit(drain);
+                const bool drained = mbar_wait_bounded(drain, 0, 4 * limit);
+                atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4 && warp < 12) {
+        const int wg = (warp - 4) >> 2, t = (threadIdx.x - 128) & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;     // this warp's TMEM lanes, in bits 16+
+        long long it = 0;
+        for (long long tile = first; tile < ntiles && ok; tile += stride) {
+            for (int s = 0; s < steps; ++s, ++it) {
+                if ((it & 1) != wg) continue;
+                const int rs = static_cast<int>(it % RAWS), os = static_cast<int>(it % OPS);
+                ok = mbar_wait_bounded(raw_full + 8 * rs, static_cast<uint32_t>(it / RAWS) & 1u, limit) &&
+                     mbar_wait_bounded(op_empty + 8 * os, (static_cast<uint32_t>(it / OPS) & 1u) ^ 1u, limit);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ra = smem_u32(raw + rs * S::RAW), rb = ra + S::RAW_A;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = ld_shared_v4(ra + t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
+                    uint32_t h[8];
+                    codes_to_half(v.x, h[0], h[1]);
+                    codes_to_half(v.y, h[2], h[3]);
+                    codes_to_half(v.z, h[4], h[5]);
+                    codes_to_half(v.w, h[6], h[7]);
+                    tmem_st_x8(tmem_a + lanes + os * 32 + c * 8, h);
+                }
+                const uint32_t ob = smem_u32(ops + os * S::OP);
+#pragma unroll
+                for (int j = 0; j < (NT * 4 + 127) / 128; ++j) {
+                    const int i = j * 128 + t, r = i % NT, c = i / NT;
+                    if (c < 4) {
+                        const uint4 v = ld_shared_v4(rb + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+                        uint4 lo, hi;
+                        codes_to_half(v.x, lo.x, lo.y);
+                        codes_to_half(v.y, lo.z, lo.w);
+                        codes_to_half(v.z, hi.x, hi.y);
+                        codes_to_half(v.w, hi.z, hi.w);
+                        st_shared_v4(ob + r * 128 + (((2 * c) ^ (r & 7)) << 4), lo);
+                        st_shared_v4(ob + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4), hi);
+                    }
+                }
+                fence_proxy_async_smem();
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(raw_empty + 8 * rs);
+                    mbar_arrive(op_full + 8 * os);
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
+    } else if (warp >= 12) {
+        constexpr int HALF = NT / 2;
+        const int wg = (warp - 12) >> 2, row = threadIdx.x & 127;
+        const uint32_t base = tmem + (static_cast<uint32_t>(warp & 3) << 21) + wg * HALF;
+        long long chunks = 0;
+        for (long long tile = first; tile < ntiles && ok; tile += stride) {
+            int acc[HALF];
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) acc[i] = 0;
+            for (int s = 0; s < steps; s += kTcChunk, ++chunks) {
+                ok = mbar_wait_bounded(acc_full, static_cast<uint32_t>(chunks & 1), limit);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < HALF; c += 8) {
+                    uint32_t v[8];
+                    tmem_ld_x8(base + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(acc_empty);
+            }
+            if (!ok) break;
+            int tn, tm;
+            tc_tile(tile, tiles, tn, tm);
+            if (nc == 1) {
+                const long long n = static_cast<long long>(tn) * kTcRows + row;
+                if (n < p.n) {
+                    const float ws = p.w_scale[n], b = p.bias ? load_as(p.bias, n, p.dt) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < HALF; ++i) {
+                        const long long m = static_cast<long long>(tm) * NT + wg * HALF + i;
+                        if (m < p.m) store_as(p.out, m * p.n + n, p.dt, scaled(acc[i], p.a_scale[m], ws, b, p.bias));
+                    }
+                }
+            } else {
+                // one tile per cluster: the ring is free, and takes the sums, [token][channel]
+                int* const sums = reinterpret_cast<int*>(raw);
+#pragma unroll
+                for (int i = 0; i < HALF; ++i) sums[(wg * HALF + i) * kTcRows + row] = acc[i];
+            }
+        }
+        if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
+    }
+
+    if (nc > 1) {
+        // tokens rank, rank + nc, ... of the tile: add the CTAs' sums and write
+        cluster_sync();
+        int tn, tm;
+        tc_tile(first, tiles, tn, tm);
+        const uint32_t sums = smem_u32(raw);
+        for (int e = threadIdx.x; e < (NT + static_cast<int>(nc) - 1) / static_cast<int>(nc) * 32; e += kTcThreads) {
+            const int i = (e >> 5) * static_cast<int>(nc) + static_cast<int>(rank);
+            const long long m = static_cast<long long>(tm) * NT + i, n = static_cast<long long>(tn) * kTcRows + lane * 4;
+            if (i >= NT || m >= p.m || n >= p.n) continue;
+            int4 v = make_int4(0, 0, 0, 0);
+            for (uint32_t r = 0; r < nc; ++r) {
+                const int4 o = ld_cluster_i4(sums + (i * kTcRows + lane * 4) * 4, r);
+                v.x += o.x;
+                v.y += o.y;
+                v.z += o.z;
+                v.w += o.w;
+            }
+            const int a[4] = {v.x, v.y, v.z, v.w};
+            const float as = p.a_scale[m];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < p.n)
+                    store_as(p.out, m * p.n + n + j, p.dt,
+                             scaled(a[j], as, p.w_scale[n + j], p.bias ? load_as(p.bias, n + j, p.dt) : 0.f, p.bias));
+        }
+        cluster_sync();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+}  // namespace rmsq
