@@ -2,7 +2,7 @@
 #include <atomic>
 #include <cstdint>
 
-#include "rmsq_matmul_tc.cuh"
+#include "rmsq_matmul_pair.cuh"
 #include "rmsq_ops.h"
 
 namespace rmsq {
@@ -76,13 +76,37 @@ template <int NT> static cudaError_t launch_tc(MatmulParams& p, const DeviceView
                          dim3(static_cast<unsigned>(grid)), kTcThreads, TcShape<NT>::SMEM, cluster, stream, args);
 }
 
+static cudaError_t launch_pair(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
+{
+    // setmaxnreg moves registers that the launch must have
+    static std::atomic<int> regs{0};
+    const void* fn = reinterpret_cast<const void*>(&rmsq_matmul_pair_kernel);
+    if (regs.load() == 0) {
+        cudaFuncAttributes fa;
+        const cudaError_t e = cudaFuncGetAttributes(&fa, fn);
+        if (e != cudaSuccess) return e;
+        regs.store(fa.numRegs);
+    }
+    if (regs.load() < kPairRegs) return cudaErrorInvalidConfiguration;
+    CUtensorMap map_w, map_a;
+    if (!encode(&map_w, p.w, p.n, p.k, kTcRows) || !encode(&map_a, p.a, p.m, p.k, kTcRows)) return cudaErrorUnknown;
+    TcTiles t;
+    t.n_tiles = static_cast<int>((p.n + 2 * kTcRows - 1) / (2 * kTcRows));
+    t.m_tiles = static_cast<int>((p.m + kPairTokens - 1) / kPairTokens);
+    const long long tiles = static_cast<long long>(t.n_tiles) * t.m_tiles;
+    const long long pairs = tiles < dv.sms / 2 ? tiles : dv.sms / 2;
+    void* args[] = {&map_w, &map_a, &p, &t};
+    return launch_kernel(fn, dim3(static_cast<unsigned>(2 * pairs)), kTcThreads, kPairSmem, 2, stream, args);
+}
+
 static cudaError_t launch_matmul(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
 {
     if (p.m <= 8) return launch_few(p, dv, stream);
     if (p.m <= 16) return launch_tc<16>(p, dv, stream);
     if (p.m <= 32) return launch_tc<32>(p, dv, stream);
     if (p.m <= 64) return launch_tc<64>(p, dv, stream);
-    return launch_tc<128>(p, dv, stream);
+    if (p.m <= 256 || p.n <= 128) return launch_tc<128>(p, dv, stream);
+    return launch_pair(p, dv, stream);
 }
 
 }  // namespace rmsq

@@ -1,0 +1,287 @@
+// rmsq_matmul_pair.cuh -- the int8 product on the tensor cores for many tokens: a CTA pair per tile.
+//
+// As rmsq_matmul_tc_kernel, but two CTAs (a cluster of 2) share one MMA (cta_group::2) of 256 output
+// channels by 256 tokens: each converts its own 128 channels into its TMEM and half of the tokens
+// into its shared memory, and holds the sums of its channels for all 256 tokens. Per product that
+// halves the codes a CTA turns into fp16 and the shared memory the MMA reads, which bound the
+// one-CTA kernel (shared memory moves 16-bit and 8-bit copies of both operands through one port).
+//
+// The leader (rank 0) issues the MMAs. Its op_full and acc_empty barriers count arrivals of both
+// CTAs; its commits arrive in both. Copy rings are each CTA's own. The reading warps hold 128 sums
+// per thread, so registers move to them from the other warps (setmaxnreg).
+#pragma once
+
+#include "rmsq_matmul_tc.cuh"
+
+namespace rmsq {
+
+constexpr int kPairTokens = 256;
+constexpr int kPairRaws = 8, kPairOps = 5;
+constexpr int kPairRaw = 2 * kTcRows * kTcStep;       // codes of 128 channels and 128 tokens
+constexpr int kPairOp = kTcRows * kTcStep * 2;        // 128 tokens in fp16
+constexpr int kPairSmem = 2048 + kPairRaws * kPairRaw + kPairOps * kPairOp;
+static_assert(kPairSmem > 116 * 1024 && kPairSmem <= 232448, "one CTA per SM");
+// registers: 12 warps give up what 8 take; the launch has kPairRegs for every thread
+constexpr int kPairRegs = 96, kPairRegsLow = 56, kPairRegsHigh = 152;
+static_assert(384 * kPairRegsLow + 256 * kPairRegsHigh <= kTcThreads * kPairRegs, "within the launch's registers");
+
+// Arrive on the leader's barrier at this CTA's address bar, ordering this thread's writes before.
+__device__ __forceinline__ void mbar_arrive_leader(uint32_t bar)
+{
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return done != 0;
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned long long timeout_ns)
+{
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    while (true) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (globaltimer_ns() - t0 > timeout_ns) return false;
+    }
+}
+
+// Arrives on bar in both CTAs when every MMA this thread has issued is done.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_pair(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+        : "memory");
+}
+
+__global__ void __launch_bounds__(kTcThreads, 1) __cluster_dims__(2, 1, 1)
+rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                        const MatmulParams p, const TcTiles tiles)
+{
+    constexpr int RAWS = kPairRaws, OPS = kPairOps;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint32_t tmem_slot;
+
+    unsigned char* const smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    unsigned char* const raw = smem;
+    unsigned char* const ops = smem + RAWS * kPairRaw;
+    const uint32_t bars = smem_u32(ops + OPS * kPairOp);
+    const uint32_t raw_full = bars, raw_empty = raw_full + 8 * RAWS;
+    const uint32_t op_full = raw_empty + 8 * RAWS, op_empty = op_full + 8 * OPS;
+    const uint32_t acc_full = op_empty + 8 * OPS, acc_empty = acc_full + 8, drain = acc_empty + 8;
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rank = static_cast<int>(cluster_rank());
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < RAWS; ++i) {
+            mbar_init(raw_full + 8 * i, 1);
+            mbar_init(raw_empty + 8 * i, 4);
+        }
+        for (int i = 0; i < OPS; ++i) {
+            mbar_init(op_full + 8 * i, 8);
+            mbar_init(op_empty + 8 * i, 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 16);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        tc_fence_before();
+    }
+    __syncthreads();
+    cluster_sync();                          // the other CTA's barriers are set up
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem_a = tmem + 256;      // operand stages of 32 columns behind the accumulator
+    pdl_wait();
+
+    const int steps = (p.k + kTcStep - 1) / kTcStep;
+    const long long ntiles = static_cast<long long>(tiles.n_tiles) * tiles.m_tiles;
+    const long long first = cluster_id(), stride = cluster_count();
+    const unsigned long long limit = p.timeout_ns;
+    bool ok = true;
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsLow));
+        if (warp == 0 && lane == 0) {
+            long long it = 0;
+            for (long long tile = first; tile < ntiles && ok; tile += stride) {
+                int tn, tm;
+                tc_tile(tile, tiles, tn, tm);
+                for (int s = 0; s < steps; ++s, ++it) {
+                    const int slot = static_cast<int>(it % RAWS);
+                    const uint32_t phase = static_cast<uint32_t>(it / RAWS) & 1u;
+                    ok = mbar_wait_bounded(raw_empty + 8 * slot, phase ^ 1u, limit);
+                    if (!ok) break;
+                    const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw + slot * kPairRaw);
+                    mbar_arrive_expect_tx(full, kPairRaw);
+                    tma_load_2d(dst, &map_w, s * kTcStep, (tn * 2 + rank) * kTcRows, full);
+                    tma_load_2d(dst + kTcRows * kTcStep, &map_a, s * kTcStep, (tm * 2 + rank) * kTcRows, full);
+                }
+            }
+            if (!ok) {
+                // the copies in flight end before the CTA does
+                bool drained = true;
+                for (long long i = it > RAWS ? it - RAWS : 0; i < it; ++i)
+                    drained &= mbar_wait_bounded(raw_full + 8 * static_cast<int>(i % RAWS),
+                                                 static_cast<uint32_t>(i / RAWS) & 1u, 4 * limit);
+                atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = (1u << 4) | ((kPairTokens / 8u) << 17) | ((2u * kTcRows / 16u) << 24);
+            long long it = 0, chunks = 0;
+            for (long long tile = first; tile < ntiles && ok; tile += stride) {
+                for (int s = 0; s < steps && ok; ++s, ++it) {
+                    const int slot = static_cast<int>(it % OPS);
+                    const bool head = s % kTcChunk == 0, tail = s % kTcChunk == kTcChunk - 1 || s == steps - 1;
+                    if (head) ok = mbar_wait_cluster(acc_empty, static_cast<uint32_t>(chunks & 1) ^ 1u, limit);
+                    ok = ok && mbar_wait_cluster(op_full + 8 * slot, static_cast<uint32_t>(it / OPS) & 1u, limit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t desc = tc_desc(smem_u32(ops + slot * kPairOp));
+#pragma unroll
+                    for (int k = 0; k < kTcStep / 16; ++k)
+                        tc_mma_pair(tmem, tmem_a + slot * 32 + k * 8, desc + 2 * k, idesc, !(head && k == 0));
+                    tc_commit_pair(op_empty + 8 * slot);
+                    if (tail) {
+                        tc_commit_pair(acc_full);
+                        ++chunks;
+                    }
+                }
+            }
+            if (!ok) {
+                // the MMAs in flight end before either CTA frees its TMEM (the barrier below)
+                tc_commit_pair(drain);
+                const bool drained = mbar_wait_bounded(drain, 0, 4 * limit);
+                atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsLow));
+        const int wg = (warp - 4) >> 2, t = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;     // this warp's TMEM lanes, in bits 16+
+        long long it = 0;
+        for (long long tile = first; tile < ntiles && ok; tile += stride) {
+            for (int s = 0; s < steps; ++s, ++it) {
+                if ((it & 1) != wg) continue;
+                const int rs = static_cast<int>(it % RAWS), os = static_cast<int>(it % OPS);
+                ok = mbar_wait_bounded(raw_full + 8 * rs, static_cast<uint32_t>(it / RAWS) & 1u, limit) &&
+                     mbar_wait_bounded(op_empty + 8 * os, (static_cast<uint32_t>(it / OPS) & 1u) ^ 1u, limit);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ra = smem_u32(raw + rs * kPairRaw), rb = ra + kTcRows * kTcStep;
+                const uint32_t ob = smem_u32(ops + os * kPairOp);
+                // thread t: channel t and token t of this CTA
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = ld_shared_v4(ra + t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
+                    uint32_t h[8];
+                    codes_to_half(v.x, h[0], h[1]);
+                    codes_to_half(v.y, h[2], h[3]);
+                    codes_to_half(v.z, h[4], h[5]);
+                    codes_to_half(v.w, h[6], h[7]);
+                    tmem_st_x8(tmem_a + lanes + os * 32 + c * 8, h);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const uint4 v = ld_shared_v4(rb + t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
+                    uint4 lo, hi;
+                    codes_to_half(v.x, lo.x, lo.y);
+                    codes_to_half(v.y, lo.z, lo.w);
+                    codes_to_half(v.z, hi.x, hi.y);
+                    codes_to_half(v.w, hi.z, hi.w);
+                    st_shared_v4(ob + t * 128 + (((2 * c) ^ (t & 7)) << 4), lo);
+                    st_shared_v4(ob + t * 128 + (((2 * c + 1) ^ (t & 7)) << 4), hi);
+                }
+                fence_proxy_async_smem();
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(raw_empty + 8 * rs);
+                    mbar_arrive_leader(op_full + 8 * os);
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsHigh));
+        constexpr int HALF = kPairTokens / 2;
+        const int wg = (warp - 12) >> 2, row = threadIdx.x & 127;
+        const uint32_t base = tmem + (static_cast<uint32_t>(warp & 3) << 21) + wg * HALF;
+        long long chunks = 0;
+        for (long long tile = first; tile < ntiles && ok; tile += stride) {
+            int acc[HALF];
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) acc[i] = 0;
+            for (int s = 0; s < steps; s += kTcChunk, ++chunks) {
+                ok = mbar_wait_bounded(acc_full, static_cast<uint32_t>(chunks & 1), limit);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < HALF; c += 8) {
+                    uint32_t v[8];
+                    tmem_ld_x8(base + c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_leader(acc_empty);
+            }
+            if (!ok) break;
+            int tn, tm;
+            tc_tile(tile, tiles, tn, tm);
+            const int n = (tn * 2 + rank) * kTcRows + row, m0 = tm * kPairTokens + wg * HALF;
+            if (n < p.n) {
+                const float ws = p.w_scale[n], b = p.bias ? load_as(p.bias, n, p.dt) : 0.f;
+                const float* const as = p.a_scale + m0;
+                const int left = static_cast<int>(p.m) - m0, es = p.dt == DT_F32 ? 4 : 2;
+                char* out = static_cast<char*>(p.out) + (m0 * p.n + n) * es;
+                const long long pitch = p.n * es;
+#pragma unroll
+                for (int i = 0; i < HALF; ++i, out += pitch)
+                    if (i < left) store_as(out, 0, p.dt, scaled(acc[i], as[i], ws, b, p.bias));
+            }
+        }
+        if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                          // no CTA leaves while the other arrives on its barriers
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+}  // namespace rmsq
