@@ -45,16 +45,16 @@ static EncodeFn encode_fn()
     return reinterpret_cast<EncodeFn>(f);
 }
 
-// Codes [rows x k], read in boxes of box_rows x 64 elements; what lies outside reads as 0.
+// Codes [rows x k], read in boxes of box_rows x 128 elements; what lies outside reads as 0.
 static bool encode(CUtensorMap* map, const void* codes, long long rows, int k, int box_rows)
 {
     const EncodeFn fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k)};
-    const cuuint32_t box[2] = {kTcStep, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {kTcCodes, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, step,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -66,10 +66,10 @@ template <int NT> static cudaError_t launch_tc(MatmulParams& p, const DeviceView
     t.n_tiles = static_cast<int>((p.n + kTcRows - 1) / kTcRows);
     t.m_tiles = static_cast<int>((p.m + NT - 1) / NT);
     const long long tiles = static_cast<long long>(t.n_tiles) * t.m_tiles;
-    // CTAs that share a tile's k: while that leaves no SM with two tiles and each CTA 4 stages
+    // CTAs that share a tile's k: while that leaves no SM with two tiles and each CTA 2 code stages
     int cluster = 1;
-    const int steps = (p.k + kTcStep - 1) / kTcStep;
-    while (cluster < 8 && tiles * cluster * 2 <= dv.sms && steps >= 8 * cluster) cluster *= 2;
+    const int steps = (p.k + kTcCodes - 1) / kTcCodes;
+    while (cluster < 8 && tiles * cluster * 2 <= dv.sms && steps >= 4 * cluster) cluster *= 2;
     const long long grid = cluster > 1 ? tiles * cluster : tiles < dv.sms ? tiles : dv.sms;
     void* args[] = {&map_w, &map_a, &p, &t};
     return launch_kernel(reinterpret_cast<const void*>(&rmsq_matmul_tc_kernel<NT>),

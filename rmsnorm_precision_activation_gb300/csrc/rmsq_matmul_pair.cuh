@@ -7,7 +7,7 @@
 // one-CTA kernel (shared memory moves 16-bit and 8-bit copies of both operands through one port).
 //
 // The leader (rank 0) issues the MMAs. Its op_full and acc_empty barriers count arrivals of both
-// CTAs; its commits arrive in both. Copy rings are each CTA's own. The reading warps hold 128 sums
+// CTAs (the follower's stages are passed on by two of its idle warps); its commits arrive in both. Copy rings are each CTA's own. The reading warps hold 128 sums
 // per thread, so registers move to them from the other warps (setmaxnreg).
 #pragma once
 
@@ -16,14 +16,14 @@
 namespace rmsq {
 
 constexpr int kPairTokens = 256;
-constexpr int kPairRaws = 8, kPairOps = 5;
-constexpr int kPairRaw = 2 * kTcRows * kTcStep;       // codes of 128 channels and 128 tokens
+constexpr int kPairRaws = 4, kPairOps = 5;
+constexpr int kPairRaw = 2 * kTcRows * kTcCodes;       // codes of 128 channels and 128 tokens
 constexpr int kPairOp = kTcRows * kTcStep * 2;        // 128 tokens in fp16
 constexpr int kPairSmem = 2048 + kPairRaws * kPairRaw + kPairOps * kPairOp;
 static_assert(kPairSmem > 116 * 1024 && kPairSmem <= 232448, "one CTA per SM");
 // registers: 12 warps give up what 8 take; the launch has kPairRegs for every thread
-constexpr int kPairRegs = 96, kPairRegsLow = 56, kPairRegsHigh = 152;
-static_assert(384 * kPairRegsLow + 256 * kPairRegsHigh <= kTcThreads * kPairRegs, "within the launch's registers");
+constexpr int kPairRegs = 96, kPairRegsIssue = 32, kPairRegsConvert = 64, kPairRegsRead = 160;
+static_assert(128 * kPairRegsIssue + 256 * (kPairRegsConvert + kPairRegsRead) <= kTcThreads * kPairRegs, "within the launch's registers");
 
 // Arrive on the leader's barrier at this CTA's address bar, ordering this thread's writes before.
 __device__ __forceinline__ void mbar_arrive_leader(uint32_t bar)
@@ -33,25 +33,12 @@ __device__ __forceinline__ void mbar_arrive_leader(uint32_t bar)
         "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
+// The same after tcgen05 operations alone, which tcgen05.fence orders: nothing else to release.
+__device__ __forceinline__ void mbar_arrive_leader_relaxed(uint32_t bar)
 {
-    uint32_t done;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(done) : "r"(bar), "r"(parity) : "memory");
-    return done != 0;
-}
-
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned long long timeout_ns)
-{
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const unsigned long long t0 = globaltimer_ns();
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (globaltimer_ns() - t0 > timeout_ns) return false;
-    }
+        "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar) : "memory");
 }
 
 // Arrives on bar in both CTAs when every MMA this thread has issued is done.
@@ -94,10 +81,10 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
     if (threadIdx.x == 0) {
         for (int i = 0; i < RAWS; ++i) {
             mbar_init(raw_full + 8 * i, 1);
-            mbar_init(raw_empty + 8 * i, 4);
+            mbar_init(raw_empty + 8 * i, 8);
         }
         for (int i = 0; i < OPS; ++i) {
-            mbar_init(op_full + 8 * i, 8);
+            mbar_init(op_full + 8 * i, rank == 0 ? 5 : 4);   // leader: its 4 warps and the follower
             mbar_init(op_empty + 8 * i, 1);
         }
         mbar_init(acc_full, 1);
@@ -119,14 +106,14 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
     const uint32_t tmem_a = tmem + 256;      // operand stages of 32 columns behind the accumulator
     pdl_wait();
 
-    const int steps = (p.k + kTcStep - 1) / kTcStep;
+    const int steps = (p.k + kTcCodes - 1) / kTcCodes;      // code stages
     const long long ntiles = static_cast<long long>(tiles.n_tiles) * tiles.m_tiles;
     const long long first = cluster_id(), stride = cluster_count();
-    const unsigned long long limit = p.timeout_ns;
+    const uint32_t limit = wait_limit(p.timeout_ns), drain_limit = wait_limit(4 * p.timeout_ns);
     bool ok = true;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsLow));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsIssue));
         if (warp == 0 && lane == 0) {
             long long it = 0;
             for (long long tile = first; tile < ntiles && ok; tile += stride) {
@@ -135,87 +122,118 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                 for (int s = 0; s < steps; ++s, ++it) {
                     const int slot = static_cast<int>(it % RAWS);
                     const uint32_t phase = static_cast<uint32_t>(it / RAWS) & 1u;
-                    ok = mbar_wait_bounded(raw_empty + 8 * slot, phase ^ 1u, limit);
+                    ok = mbar_wait<SCOPE_CTA>(raw_empty + 8 * slot, phase ^ 1u, limit);
                     if (!ok) break;
                     const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw + slot * kPairRaw);
                     mbar_arrive_expect_tx(full, kPairRaw);
-                    tma_load_2d(dst, &map_w, s * kTcStep, (tn * 2 + rank) * kTcRows, full);
-                    tma_load_2d(dst + kTcRows * kTcStep, &map_a, s * kTcStep, (tm * 2 + rank) * kTcRows, full);
+                    tma_load_2d(dst, &map_w, s * kTcCodes, (tn * 2 + rank) * kTcRows, full);
+                    tma_load_2d(dst + kTcRows * kTcCodes, &map_a, s * kTcCodes, (tm * 2 + rank) * kTcRows, full);
                 }
             }
             if (!ok) {
                 // the copies in flight end before the CTA does
                 bool drained = true;
                 for (long long i = it > RAWS ? it - RAWS : 0; i < it; ++i)
-                    drained &= mbar_wait_bounded(raw_full + 8 * static_cast<int>(i % RAWS),
-                                                 static_cast<uint32_t>(i / RAWS) & 1u, 4 * limit);
+                    drained &= mbar_wait<SCOPE_CTA>(raw_full + 8 * static_cast<int>(i % RAWS),
+                                                 static_cast<uint32_t>(i / RAWS) & 1u, drain_limit);
                 atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             constexpr uint32_t idesc = (1u << 4) | ((kPairTokens / 8u) << 17) | ((2u * kTcRows / 16u) << 24);
-            long long it = 0, chunks = 0;
+            const bool one = elect_one();
+            uint32_t slot = 0, phase = 0, chunks = 0;
             for (long long tile = first; tile < ntiles && ok; tile += stride) {
-                for (int s = 0; s < steps && ok; ++s, ++it) {
-                    const int slot = static_cast<int>(it % OPS);
-                    const bool head = s % kTcChunk == 0, tail = s % kTcChunk == kTcChunk - 1 || s == steps - 1;
-                    if (head) ok = mbar_wait_cluster(acc_empty, static_cast<uint32_t>(chunks & 1) ^ 1u, limit);
-                    ok = ok && mbar_wait_cluster(op_full + 8 * slot, static_cast<uint32_t>(it / OPS) & 1u, limit);
+                for (int s = 0; s < 2 * steps; ++s) {
+                    const bool head = s % (2 * kTcChunk) == 0;
+                    const bool tail = s % (2 * kTcChunk) == 2 * kTcChunk - 1 || s == 2 * steps - 1;
+                    if (head) ok = mbar_wait<SCOPE_CLUSTER>(acc_empty, (chunks & 1u) ^ 1u, limit);
+                    ok = ok && mbar_wait<SCOPE_CLUSTER>(op_full + 8 * slot, phase, limit);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t desc = tc_desc(smem_u32(ops + slot * kPairOp));
+                    const uint64_t desc = tc_desc(smem_u32(ops) + slot * kPairOp);
+                    if (one) {
 #pragma unroll
-                    for (int k = 0; k < kTcStep / 16; ++k)
-                        tc_mma_pair(tmem, tmem_a + slot * 32 + k * 8, desc + 2 * k, idesc, !(head && k == 0));
-                    tc_commit_pair(op_empty + 8 * slot);
-                    if (tail) {
-                        tc_commit_pair(acc_full);
-                        ++chunks;
+                        for (int k = 0; k < kTcStep / 16; ++k)
+                            tc_mma_pair(tmem, tmem_a + slot * 32 + k * 8, desc + 2 * k, idesc, !(head && k == 0));
+                        tc_commit_pair(op_empty + 8 * slot);
+                        if (tail) tc_commit_pair(acc_full);
+                    }
+                    __syncwarp();
+                    chunks += tail;
+                    if (++slot == OPS) {
+                        slot = 0;
+                        phase ^= 1u;
                     }
                 }
             }
-            if (!ok) {
+            if (!ok && one) {
                 // the MMAs in flight end before either CTA frees its TMEM (the barrier below)
                 tc_commit_pair(drain);
-                const bool drained = mbar_wait_bounded(drain, 0, 4 * limit);
+                const bool drained = mbar_wait<SCOPE_CTA>(drain, 0, drain_limit);
                 atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
             }
+        } else if (warp >= 2 && rank == 1 && lane == 0) {
+            // Passes the follower's finished operand stages on to the leader, stages in turn with the
+            // other such warp: an arrival that releases at cluster scope takes about 1000 cycles,
+            // which the converting warps do not wait for.
+            long long n = 0;
+            uint32_t slot = static_cast<uint32_t>(warp - 2), phase = 0;
+            for (long long tile = first; tile < ntiles; tile += stride) n += steps;
+            for (; n > 0; --n) {
+                ok = mbar_wait<SCOPE_CTA>(op_full + 8 * slot, phase, limit);
+                if (!ok) break;
+                mbar_arrive_leader(op_full + 8 * slot);
+                slot += 2;
+                if (slot >= OPS) {
+                    slot -= OPS;
+                    phase ^= 1u;
+                }
+            }
+            if (!ok) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
         }
         __syncwarp();
     } else if (warp < 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsLow));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsConvert));
         const int wg = (warp - 4) >> 2, t = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;     // this warp's TMEM lanes, in bits 16+
         long long it = 0;
         for (long long tile = first; tile < ntiles && ok; tile += stride) {
             for (int s = 0; s < steps; ++s, ++it) {
-                if ((it & 1) != wg) continue;
-                const int rs = static_cast<int>(it % RAWS), os = static_cast<int>(it % OPS);
-                ok = mbar_wait_bounded(raw_full + 8 * rs, static_cast<uint32_t>(it / RAWS) & 1u, limit) &&
-                     mbar_wait_bounded(op_empty + 8 * os, (static_cast<uint32_t>(it / OPS) & 1u) ^ 1u, limit);
+                const long long op = 2 * it + wg;
+                const int rs = static_cast<int>(it % RAWS), os = static_cast<int>(op % OPS);
+                ok = mbar_wait<SCOPE_CTA>(raw_full + 8 * rs, static_cast<uint32_t>(it / RAWS) & 1u, limit) &&
+                     mbar_wait<SCOPE_CTA>(op_empty + 8 * os, (static_cast<uint32_t>(op / OPS) & 1u) ^ 1u, limit);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t ra = smem_u32(raw + rs * kPairRaw), rb = ra + kTcRows * kTcStep;
+                const uint32_t ra = smem_u32(raw + rs * kPairRaw), rb = ra + kTcRows * kTcCodes;
                 const uint32_t ob = smem_u32(ops + os * kPairOp);
-                // thread t: channel t and token t of this CTA
+                // thread t: channel t and token t of this CTA; all loads first, to overlap
+                uint4 va[4], vb[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint4 v = ld_shared_v4(ra + t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
-                    uint32_t h[8];
-                    codes_to_half(v.x, h[0], h[1]);
-                    codes_to_half(v.y, h[2], h[3]);
-                    codes_to_half(v.z, h[4], h[5]);
-                    codes_to_half(v.w, h[6], h[7]);
-                    tmem_st_x8(tmem_a + lanes + os * 32 + c * 8, h);
+                for (int c = 0; c < 4; ++c) va[c] = ld_shared_v4(ra + t * 128 + (((4 * wg + c) ^ (t & 7)) << 4));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) vb[c] = ld_shared_v4(rb + t * 128 + (((4 * wg + c) ^ (t & 7)) << 4));
+#pragma unroll
+                for (int c = 0; c < 4; c += 2) {
+                    uint32_t h[16];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        codes_to_half(va[c + i].x, h[8 * i], h[8 * i + 1]);
+                        codes_to_half(va[c + i].y, h[8 * i + 2], h[8 * i + 3]);
+                        codes_to_half(va[c + i].z, h[8 * i + 4], h[8 * i + 5]);
+                        codes_to_half(va[c + i].w, h[8 * i + 6], h[8 * i + 7]);
+                    }
+                    tmem_st_x16(tmem_a + lanes + os * 32 + c * 8, h);
                 }
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint4 v = ld_shared_v4(rb + t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
                     uint4 lo, hi;
-                    codes_to_half(v.x, lo.x, lo.y);
-                    codes_to_half(v.y, lo.z, lo.w);
-                    codes_to_half(v.z, hi.x, hi.y);
-                    codes_to_half(v.w, hi.z, hi.w);
+                    codes_to_half(vb[c].x, lo.x, lo.y);
+                    codes_to_half(vb[c].y, lo.z, lo.w);
+                    codes_to_half(vb[c].z, hi.x, hi.y);
+                    codes_to_half(vb[c].w, hi.z, hi.w);
                     st_shared_v4(ob + t * 128 + (((2 * c) ^ (t & 7)) << 4), lo);
                     st_shared_v4(ob + t * 128 + (((2 * c + 1) ^ (t & 7)) << 4), hi);
                 }
@@ -225,13 +243,13 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(raw_empty + 8 * rs);
-                    mbar_arrive_leader(op_full + 8 * os);
+                    mbar_arrive(op_full + 8 * os);
                 }
             }
         }
         if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsHigh));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsRead));
         constexpr int HALF = kPairTokens / 2;
         const int wg = (warp - 12) >> 2, row = threadIdx.x & 127;
         const uint32_t base = tmem + (static_cast<uint32_t>(warp & 3) << 21) + wg * HALF;
@@ -241,21 +259,21 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
 #pragma unroll
             for (int i = 0; i < HALF; ++i) acc[i] = 0;
             for (int s = 0; s < steps; s += kTcChunk, ++chunks) {
-                ok = mbar_wait_bounded(acc_full, static_cast<uint32_t>(chunks & 1), limit);
+                ok = mbar_wait<SCOPE_CTA>(acc_full, static_cast<uint32_t>(chunks & 1), limit);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < HALF; c += 8) {
-                    uint32_t v[8];
-                    tmem_ld_x8(base + c, v);
+                for (int c = 0; c < HALF; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld_x16(base + c, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+                    for (int j = 0; j < 16; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_leader(acc_empty);
+                if (lane == 0) mbar_arrive_leader_relaxed(acc_empty);
             }
             if (!ok) break;
             int tn, tm;

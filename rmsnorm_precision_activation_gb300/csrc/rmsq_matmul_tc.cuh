@@ -3,15 +3,16 @@
 // sm_103a's tcgen05 has no 8-bit-integer kind, so the codes go through its fp16 kind: a code is
 // exact in fp16, a product of two is at most 2^14, and fp32 sums of up to 1024 products are whole
 // numbers of at most 2^24, so exact. The fp32 accumulator is therefore read out and added to 32-bit
-// integers every 1024 elements of k (kChunk stages), which makes every sum exact.
+// integers every 1024 elements of k (kTcChunk code stages), which makes every sum exact.
 //
-// A CTA takes 128 output channels (the MMA's rows) and NT tokens (its columns). Per stage of 64
-// elements of k:
-//   warp 0       TMA loads the codes of both tiles into a ring (64-byte swizzle)
-//   warps 4-11   two warpgroups, stages in turn, turn codes into fp16: the channels' straight into
-//                TMEM (the MMA takes its first operand from there, which spares shared memory a
-//                write and a read), the tokens' into shared memory (128-byte swizzle)
-//   warp 1       one thread issues tcgen05.mma, four per stage
+// A CTA takes 128 output channels (the MMA's rows) and NT tokens (its columns):
+//   warp 0       TMA loads the codes of both tiles into a ring, 128 elements of k per stage (boxes
+//                of 64 ran at half the rate: the copy engine's cost is per row of a box)
+//   warps 4-11   two warpgroups, each a half of every code stage, turn codes into fp16, one operand
+//                stage of 64 elements of k: the channels' straight into TMEM (the MMA takes its
+//                first operand from there, which spares shared memory a write and a read), the
+//                tokens' into shared memory
+//   warp 1       one thread issues tcgen05.mma, four per operand stage
 //   warps 12-19  two warpgroups read the accumulator out, half of the tokens each, and write the
 //                output
 // The weight is read as codes, so a call with few tokens streams one byte per weight; CTAs of a
@@ -28,17 +29,18 @@
 namespace rmsq {
 
 constexpr int kTcThreads = 640;
-constexpr int kTcStep = 64;              // elements of k per stage
-constexpr int kTcChunk = 1024 / kTcStep; // stages per read-out of the accumulator
+constexpr int kTcCodes = 128;            // elements of k per code stage
+constexpr int kTcStep = 64;              // elements of k per operand stage
+constexpr int kTcChunk = 1024 / kTcCodes; // code stages per read-out of the accumulator
 constexpr int kTcRows = 128;             // output channels per CTA
 
 template <int NT> struct TcShape {
-    static constexpr int RAW_A = kTcRows * kTcStep;
-    static constexpr int RAW_B = (NT * kTcStep + 1023) / 1024 * 1024;
+    static constexpr int RAW_A = kTcRows * kTcCodes;
+    static constexpr int RAW_B = NT * kTcCodes;
     static constexpr int RAW = RAW_A + RAW_B;
     static constexpr int OP = NT * kTcStep * 2;
-    static constexpr int OPS = 4;                                     // operand stages
-    static constexpr int RAWS = NT >= 128 ? 8 : NT >= 64 ? 12 : 14;   // code stages
+    static constexpr int OPS = NT >= 128 ? 6 : 8;                                   // operand stages
+    static constexpr int RAWS = NT >= 128 ? 4 : NT >= 64 ? 6 : 8;    // code stages
     // 1024 bytes to align the ring, 1024 for barriers; over half of an SM's shared memory, so one
     // CTA per SM, which may take all of TMEM
     static constexpr int SMEM = 2048 + RAWS * RAW + OPS * OP;
@@ -73,6 +75,14 @@ __device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // K-major operand with 128-byte swizzle: groups of 8 rows are 1024 bytes apart.
 __device__ __forceinline__ uint64_t tc_desc(uint32_t addr)
 {
@@ -97,6 +107,15 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t addr, const uint32_t (&v)[8]
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]),
+        "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
 // 8 columns of this warp's lanes; values are valid after tmem_wait_ld.
 __device__ __forceinline__ void tmem_ld_x8(uint32_t addr, uint32_t* v)
 {
@@ -104,6 +123,16 @@ __device__ __forceinline__ void tmem_ld_x8(uint32_t addr, uint32_t* v)
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "r"(addr)
                  : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t addr, uint32_t* v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(addr)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -158,7 +187,7 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     if (threadIdx.x == 0) {
         for (int i = 0; i < RAWS; ++i) {
             mbar_init(raw_full + 8 * i, 1);
-            mbar_init(raw_empty + 8 * i, 4);
+            mbar_init(raw_empty + 8 * i, 8);
         }
         for (int i = 0; i < OPS; ++i) {
             mbar_init(op_full + 8 * i, 4);
@@ -182,12 +211,12 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     const uint32_t tmem_a = tmem + 256;      // operand stages of 32 columns behind the accumulator
     pdl_wait();
 
-    const int steps_all = (p.k + kTcStep - 1) / kTcStep;
+    const int steps_all = (p.k + kTcCodes - 1) / kTcCodes;      // code stages
     const int k0 = static_cast<int>(static_cast<long long>(steps_all) * rank / nc);
     const int steps = static_cast<int>(static_cast<long long>(steps_all) * (rank + 1) / nc) - k0;
     const long long ntiles = static_cast<long long>(tiles.n_tiles) * tiles.m_tiles;
     const long long first = cluster_id(), stride = cluster_count();
-    const unsigned long long limit = p.timeout_ns;
+    const uint32_t limit = wait_limit(p.timeout_ns), drain_limit = wait_limit(4 * p.timeout_ns);
     bool ok = true;
 
     if (warp == 0) {
@@ -199,53 +228,60 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 for (int s = 0; s < steps; ++s, ++it) {
                     const int slot = static_cast<int>(it % RAWS);
                     const uint32_t phase = static_cast<uint32_t>(it / RAWS) & 1u;
-                    ok = mbar_wait_bounded(raw_empty + 8 * slot, phase ^ 1u, limit);
+                    ok = mbar_wait<SCOPE_CTA>(raw_empty + 8 * slot, phase ^ 1u, limit);
                     if (!ok) break;
                     const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw + slot * S::RAW);
-                    mbar_arrive_expect_tx(full, S::RAW_A + NT * kTcStep);
-                    tma_load_2d(dst, &map_w, (k0 + s) * kTcStep, tn * kTcRows, full);
-                    tma_load_2d(dst + S::RAW_A, &map_a, (k0 + s) * kTcStep, tm * NT, full);
+                    mbar_arrive_expect_tx(full, S::RAW);
+                    tma_load_2d(dst, &map_w, (k0 + s) * kTcCodes, tn * kTcRows, full);
+                    tma_load_2d(dst + S::RAW_A, &map_a, (k0 + s) * kTcCodes, tm * NT, full);
                 }
             }
             if (!ok) {
                 // the copies in flight end before the CTA does
                 bool drained = true;
                 for (long long i = it > RAWS ? it - RAWS : 0; i < it; ++i)
-                    drained &= mbar_wait_bounded(raw_full + 8 * static_cast<int>(i % RAWS),
-                                                 static_cast<uint32_t>(i / RAWS) & 1u, 4 * limit);
+                    drained &= mbar_wait<SCOPE_CTA>(raw_full + 8 * static_cast<int>(i % RAWS),
+                                                 static_cast<uint32_t>(i / RAWS) & 1u, drain_limit);
                 atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(NT / 8) << 17) | ((kTcRows / 16u) << 24);
-            long long it = 0, chunks = 0;
-            for (long long tile = first; tile < ntiles && ok; tile += stride) {
-                for (int s = 0; s < steps && ok; ++s, ++it) {
-                    const int slot = static_cast<int>(it % OPS);
-                    const bool head = s % kTcChunk == 0, tail = s % kTcChunk == kTcChunk - 1 || s == steps - 1;
-                    if (head) ok = mbar_wait_bounded(acc_empty, static_cast<uint32_t>(chunks & 1) ^ 1u, limit);
-                    ok = ok && mbar_wait_bounded(op_full + 8 * slot, static_cast<uint32_t>(it / OPS) & 1u, limit);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t desc = tc_desc(smem_u32(ops + slot * S::OP));
+        // The whole warp runs the loop and one lane issues: addresses and descriptors then stay in
+        // uniform registers (from divergent code an MMA took 60 cycles to issue).
+        constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(NT / 8) << 17) | ((kTcRows / 16u) << 24);
+        const bool one = elect_one();
+        uint32_t slot = 0, phase = 0, chunks = 0;
+        for (long long tile = first; tile < ntiles && ok; tile += stride) {
+            for (int s = 0; s < 2 * steps; ++s) {
+                const bool head = s % (2 * kTcChunk) == 0;
+                const bool tail = s % (2 * kTcChunk) == 2 * kTcChunk - 1 || s == 2 * steps - 1;
+                if (head) ok = mbar_wait<SCOPE_CTA>(acc_empty, (chunks & 1u) ^ 1u, limit);
+                ok = ok && mbar_wait<SCOPE_CTA>(op_full + 8 * slot, phase, limit);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t desc = tc_desc(smem_u32(ops) + slot * S::OP);
+                if (one) {
 #pragma unroll
                     for (int k = 0; k < kTcStep / 16; ++k)
                         tc_mma(tmem, tmem_a + slot * 32 + k * 8, desc + 2 * k, idesc, !(head && k == 0));
                     tc_commit(op_empty + 8 * slot);
-                    if (tail) {
-                        tc_commit(acc_full);
-                        ++chunks;
-                    }
+                    if (tail) tc_commit(acc_full);
+                }
+                __syncwarp();
+                chunks += tail;
+                if (++slot == OPS) {
+                    slot = 0;
+                    phase ^= 1u;
                 }
             }
-            if (!ok) {
-                // the MMAs in flight end before TMEM is freed
-                tc_commit(drain);
-                const bool drained = mbar_wait_bounded(drain, 0, 4 * limit);
-                atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
-            }
+        }
+        if (!ok && one) {
+            // the MMAs in flight end before TMEM is freed
+            tc_commit(drain);
+            const bool drained = mbar_wait<SCOPE_CTA>(drain, 0, drain_limit);
+            atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 12) {
@@ -254,17 +290,17 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         long long it = 0;
         for (long long tile = first; tile < ntiles && ok; tile += stride) {
             for (int s = 0; s < steps; ++s, ++it) {
-                if ((it & 1) != wg) continue;
-                const int rs = static_cast<int>(it % RAWS), os = static_cast<int>(it % OPS);
-                ok = mbar_wait_bounded(raw_full + 8 * rs, static_cast<uint32_t>(it / RAWS) & 1u, limit) &&
-                     mbar_wait_bounded(op_empty + 8 * os, (static_cast<uint32_t>(it / OPS) & 1u) ^ 1u, limit);
+                const long long op = 2 * it + wg;
+                const int rs = static_cast<int>(it % RAWS), os = static_cast<int>(op % OPS);
+                ok = mbar_wait<SCOPE_CTA>(raw_full + 8 * rs, static_cast<uint32_t>(it / RAWS) & 1u, limit) &&
+                     mbar_wait<SCOPE_CTA>(op_empty + 8 * os, (static_cast<uint32_t>(op / OPS) & 1u) ^ 1u, limit);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t ra = smem_u32(raw + rs * S::RAW), rb = ra + S::RAW_A;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const uint4 v = ld_shared_v4(ra + t * 64 + ((c ^ ((t >> 1) & 3)) << 4));
+                    const uint4 v = ld_shared_v4(ra + t * 128 + (((4 * wg + c) ^ (t & 7)) << 4));
                     uint32_t h[8];
                     codes_to_half(v.x, h[0], h[1]);
                     codes_to_half(v.y, h[2], h[3]);
@@ -277,7 +313,7 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 for (int j = 0; j < (NT * 4 + 127) / 128; ++j) {
                     const int i = j * 128 + t, r = i % NT, c = i / NT;
                     if (c < 4) {
-                        const uint4 v = ld_shared_v4(rb + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+                        const uint4 v = ld_shared_v4(rb + r * 128 + (((4 * wg + c) ^ (r & 7)) << 4));
                         uint4 lo, hi;
                         codes_to_half(v.x, lo.x, lo.y);
                         codes_to_half(v.y, lo.z, lo.w);
@@ -299,7 +335,7 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         }
         if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
     } else if (warp >= 12) {
-        constexpr int HALF = NT / 2;
+        constexpr int HALF = NT / 2, LD = HALF < 32 ? HALF : 32;     // columns of a warp, and of one read
         const int wg = (warp - 12) >> 2, row = threadIdx.x & 127;
         const uint32_t base = tmem + (static_cast<uint32_t>(warp & 3) << 21) + wg * HALF;
         long long chunks = 0;
@@ -308,17 +344,22 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
 #pragma unroll
             for (int i = 0; i < HALF; ++i) acc[i] = 0;
             for (int s = 0; s < steps; s += kTcChunk, ++chunks) {
-                ok = mbar_wait_bounded(acc_full, static_cast<uint32_t>(chunks & 1), limit);
+                ok = mbar_wait<SCOPE_CTA>(acc_full, static_cast<uint32_t>(chunks & 1), limit);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < HALF; c += 8) {
-                    uint32_t v[8];
-                    tmem_ld_x8(base + c, v);
+                for (int c = 0; c < HALF; c += LD) {
+                    uint32_t v[LD];
+                    if constexpr (LD == 8) {
+                        tmem_ld_x8(base + c, v);
+                    } else {
+                        tmem_ld_x16(base + c, v);
+                        if constexpr (LD == 32) tmem_ld_x16(base + c + 16, v + 16);
+                    }
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+                    for (int j = 0; j < LD; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
                 }
                 tc_fence_before();
                 __syncwarp();

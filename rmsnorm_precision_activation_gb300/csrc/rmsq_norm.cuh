@@ -127,6 +127,49 @@ __device__ __forceinline__ void pdl_wait()
     asm volatile("griddepcontrol.launch_dependents;");
 }
 
+// mbar_wait_bounded for kernels whose warps wait much of the time. The thread is suspended for up to
+// 10 us at a time, so waiting warps do not crowd the shared-memory pipe that the working ones need
+// (measured in the tensor-core product: polling made every ready wait take 350 cycles), and the
+// timer, which takes about a microsecond to read, is only read by waits that last. SCOPE_CLUSTER
+// also acquires what the cluster's other CTAs wrote before they arrived.
+template <int SCOPE> __device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    if constexpr (SCOPE == SCOPE_CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity), "r"(10000u) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity), "r"(10000u) : "memory");
+    return ok != 0;
+}
+
+// A timeout as mbar_wait takes it: 32 bits of nanoseconds (registers are scarce where it waits).
+__device__ __forceinline__ uint32_t wait_limit(unsigned long long timeout_ns)
+{
+    return timeout_ns < 4000000000ull ? static_cast<uint32_t>(timeout_ns) : 4000000000u;
+}
+
+__device__ __forceinline__ uint32_t globaltimer_lo()
+{
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+
+template <int SCOPE> __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t limit_ns)
+{
+    if (mbar_try_wait_long<SCOPE>(bar, parity)) return true;
+    const uint32_t t0 = globaltimer_lo();
+#pragma unroll 1
+    do {
+        if (mbar_try_wait_long<SCOPE>(bar, parity)) return true;
+    } while (globaltimer_lo() - t0 <= limit_ns);
+    return false;
+}
+
 // The thread's share of a slice of len elements, dealt to T threads. VEC: vector c of a thread is
 // vector c * T + t of the slice (rows start on 16-byte boundaries); otherwise element j is element
 // j * T + t, so that a warp's accesses are contiguous either way.

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kBwdThreads) rmsq_norm_bwd_kernel(const NormBw
     for (long long row = first; row < p.rows; row += stride) {
         const uint32_t bar = smem_u32(&bars[group * kBwdMaxStages + slot]);
         const float mean = p.mean[row], rstd = p.rstd[row];
-        if (!dead && !mbar_wait_bounded(bar, phase, p.timeout_ns)) dead = true;
+        if (!dead && !mbar_wait<SCOPE_CTA>(bar, phase, wait_limit(p.timeout_ns))) dead = true;
 
         const unsigned char* const sl = my_ring + slot * slot_bytes;
         const long long b0 = (row * p.hidden + c0) * ES;
@@ -242,9 +242,9 @@ __global__ void __launch_bounds__(kBwdThreads) rmsq_norm_bwd_kernel(const NormBw
             long long k = 0;
             for (long long r = first; r < issued; r += stride, ++k)
                 if (issued - r <= stride * p.stages)
-                    drained &= mbar_wait_bounded(
+                    drained &= mbar_wait<SCOPE_CTA>(
                         smem_u32(&bars[group * kBwdMaxStages + static_cast<int>(k % p.stages)]),
-                        static_cast<uint32_t>(k / p.stages) & 1u, 4 * p.timeout_ns);
+                        static_cast<uint32_t>(k / p.stages) & 1u, wait_limit(4 * p.timeout_ns));
             if (!drained) atomicOr(p.err, ERRF_DRAIN_TIMEOUT);
         }
     }
