@@ -89,7 +89,7 @@ static cudaError_t launch_pair(MatmulParams& p, const DeviceView& dv, cudaStream
     }
     if (regs.load() < kPairRegs) return cudaErrorInvalidConfiguration;
     CUtensorMap map_w, map_a;
-    if (!encode(&map_w, p.w, p.n, p.k, kTcRows) || !encode(&map_a, p.a, p.m, p.k, kTcRows)) return cudaErrorUnknown;
+    if (!encode(&map_w, p.w, p.n, p.k, kTcRows) || !encode(&map_a, p.a, p.m, p.k, kPairHalf)) return cudaErrorUnknown;
     TcTiles t;
     t.n_tiles = static_cast<int>((p.n + 2 * kTcRows - 1) / (2 * kTcRows));
     t.m_tiles = static_cast<int>((p.m + kPairTokens - 1) / kPairTokens);

@@ -1,13 +1,15 @@
 // rmsq_matmul_pair.cuh -- the int8 product on the tensor cores for many tokens: a CTA pair per tile.
 //
 // As rmsq_matmul_tc_kernel, but two CTAs (a cluster of 2) share one MMA (cta_group::2) of 256 output
-// channels by 256 tokens: each converts its own 128 channels into its TMEM and half of the tokens
-// into its shared memory, and holds the sums of its channels for all 256 tokens. Per product that
+// channels by 192 tokens: each converts its own 128 channels into its TMEM and half of the tokens
+// into its shared memory, and holds the sums of its channels for all 192 tokens. 192 rather than
+// 256, because two accumulators then fit TMEM beside the operand stages, and reading one out (2500
+// cycles per 8192 of MMA at 256, bound by the float-to-integer conversions) overlaps the next. Per product that
 // halves the codes a CTA turns into fp16 and the shared memory the MMA reads, which bound the
 // one-CTA kernel (shared memory moves 16-bit and 8-bit copies of both operands through one port).
 //
 // The leader (rank 0) issues the MMAs. Its op_full and acc_empty barriers count arrivals of both
-// CTAs (the follower's stages are passed on by two of its idle warps); its commits arrive in both. Copy rings are each CTA's own. The reading warps hold 128 sums
+// CTAs; its commits arrive in both. Copy rings are each CTA's own. The reading warps hold 96 sums
 // per thread, so registers move to them from the other warps (setmaxnreg).
 #pragma once
 
@@ -15,22 +17,28 @@
 
 namespace rmsq {
 
-constexpr int kPairTokens = 256;
-constexpr int kPairRaws = 4, kPairOps = 5;
-constexpr int kPairRaw = 2 * kTcRows * kTcCodes;       // codes of 128 channels and 128 tokens
-constexpr int kPairOp = kTcRows * kTcStep * 2;        // 128 tokens in fp16
+constexpr int kPairTokens = 192, kPairHalf = kPairTokens / 2;
+constexpr int kPairRaws = 6, kPairOps = 4;
+constexpr int kPairRawA = kTcRows * kTcCodes;                     // codes of 128 channels
+constexpr int kPairRaw = kPairRawA + kPairHalf * kTcCodes;        // and of 96 tokens
+constexpr int kPairOp = kPairHalf * kTcStep * 2;                  // 96 tokens in fp16
+static_assert(kPairRaw % 1024 == 0 && kPairOp % 1024 == 0 && kPairRawA % 1024 == 0, "swizzle atoms");
+static_assert(2 * kPairTokens + kPairOps * 32 <= 512, "two accumulators and the operand stages fill TMEM");
 constexpr int kPairSmem = 2048 + kPairRaws * kPairRaw + kPairOps * kPairOp;
 static_assert(kPairSmem > 116 * 1024 && kPairSmem <= 232448, "one CTA per SM");
 // registers: 12 warps give up what 8 take; the launch has kPairRegs for every thread
-constexpr int kPairRegs = 96, kPairRegsIssue = 32, kPairRegsConvert = 64, kPairRegsRead = 160;
+constexpr int kPairRegs = 96, kPairRegsIssue = 32, kPairRegsConvert = 80, kPairRegsRead = 144;
 static_assert(128 * kPairRegsIssue + 256 * (kPairRegsConvert + kPairRegsRead) <= kTcThreads * kPairRegs, "within the launch's registers");
 
-// Arrive on the leader's barrier at this CTA's address bar, ordering this thread's writes before.
+// Arrive on the leader's barrier at this CTA's address bar. What the arrival publishes stays in this
+// CTA's own shared memory and TMEM, where the MMA reads it: fence.proxy.async and tcgen05.fence before
+// the arrival make it visible there, so the arrival need not release at cluster scope (which takes
+// about 1000 cycles behind the converting warps' stores: 863 us against 768 at 8192^3).
 __device__ __forceinline__ void mbar_arrive_leader(uint32_t bar)
 {
     asm volatile(
         "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, 0;\n\t"
-        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar) : "memory");
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(bar) : "memory");
 }
 
 // The same after tcgen05 operations alone, which tcgen05.fence orders: nothing else to release.
@@ -73,7 +81,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
     const uint32_t bars = smem_u32(ops + OPS * kPairOp);
     const uint32_t raw_full = bars, raw_empty = raw_full + 8 * RAWS;
     const uint32_t op_full = raw_empty + 8 * RAWS, op_empty = op_full + 8 * OPS;
-    const uint32_t acc_full = op_empty + 8 * OPS, acc_empty = acc_full + 8, drain = acc_empty + 8;
+    const uint32_t acc_full = op_empty + 8 * OPS, acc_empty = acc_full + 16, drain = acc_empty + 16;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = static_cast<int>(cluster_rank());
@@ -84,11 +92,13 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
             mbar_init(raw_empty + 8 * i, 8);
         }
         for (int i = 0; i < OPS; ++i) {
-            mbar_init(op_full + 8 * i, rank == 0 ? 5 : 4);   // leader: its 4 warps and the follower
+            mbar_init(op_full + 8 * i, 8);
             mbar_init(op_empty + 8 * i, 1);
         }
-        mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 16);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + 8 * i, 1);
+            mbar_init(acc_empty + 8 * i, 16);
+        }
         mbar_init(drain, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -103,7 +113,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
     cluster_sync();                          // the other CTA's barriers are set up
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const uint32_t tmem_a = tmem + 256;      // operand stages of 32 columns behind the accumulator
+    const uint32_t tmem_a = tmem + 2 * kPairTokens;      // operand stages of 32 columns behind the accumulators
     pdl_wait();
 
     const int steps = (p.k + kTcCodes - 1) / kTcCodes;      // code stages
@@ -127,7 +137,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                     const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw + slot * kPairRaw);
                     mbar_arrive_expect_tx(full, kPairRaw);
                     tma_load_2d(dst, &map_w, s * kTcCodes, (tn * 2 + rank) * kTcRows, full);
-                    tma_load_2d(dst + kTcRows * kTcCodes, &map_a, s * kTcCodes, (tm * 2 + rank) * kTcRows, full);
+                    tma_load_2d(dst + kPairRawA, &map_a, s * kTcCodes, tm * kPairTokens + rank * kPairHalf, full);
                 }
             }
             if (!ok) {
@@ -146,7 +156,8 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                 for (int s = 0; s < 2 * steps; ++s) {
                     const bool head = s % (2 * kTcChunk) == 0;
                     const bool tail = s % (2 * kTcChunk) == 2 * kTcChunk - 1 || s == 2 * steps - 1;
-                    if (head) ok = mbar_wait<SCOPE_CLUSTER>(acc_empty, (chunks & 1u) ^ 1u, limit);
+                    const uint32_t buf = chunks & 1u;
+                    if (head) ok = mbar_wait<SCOPE_CLUSTER>(acc_empty + 8 * buf, ((chunks >> 1) & 1u) ^ 1u, limit);
                     ok = ok && mbar_wait<SCOPE_CLUSTER>(op_full + 8 * slot, phase, limit);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
@@ -155,9 +166,9 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                     if (one) {
 #pragma unroll
                         for (int k = 0; k < kTcStep / 16; ++k)
-                            tc_mma_pair(tmem, tmem_a + slot * 32 + k * 8, desc + 2 * k, idesc, !(head && k == 0));
+                            tc_mma_pair(tmem + buf * kPairTokens, tmem_a + slot * 32 + k * 8, desc + 2 * k, idesc, !(head && k == 0));
                         tc_commit_pair(op_empty + 8 * slot);
-                        if (tail) tc_commit_pair(acc_full);
+                        if (tail) tc_commit_pair(acc_full + 8 * buf);
                     }
                     __syncwarp();
                     chunks += tail;
@@ -173,24 +184,6 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                 const bool drained = mbar_wait<SCOPE_CTA>(drain, 0, drain_limit);
                 atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
             }
-        } else if (warp >= 2 && rank == 1 && lane == 0) {
-            // Passes the follower's finished operand stages on to the leader, stages in turn with the
-            // other such warp: an arrival that releases at cluster scope takes about 1000 cycles,
-            // which the converting warps do not wait for.
-            long long n = 0;
-            uint32_t slot = static_cast<uint32_t>(warp - 2), phase = 0;
-            for (long long tile = first; tile < ntiles; tile += stride) n += steps;
-            for (; n > 0; --n) {
-                ok = mbar_wait<SCOPE_CTA>(op_full + 8 * slot, phase, limit);
-                if (!ok) break;
-                mbar_arrive_leader(op_full + 8 * slot);
-                slot += 2;
-                if (slot >= OPS) {
-                    slot -= OPS;
-                    phase ^= 1u;
-                }
-            }
-            if (!ok) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
         }
         __syncwarp();
     } else if (warp < 12) {
@@ -207,14 +200,17 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t ra = smem_u32(raw + rs * kPairRaw), rb = ra + kTcRows * kTcCodes;
+                const uint32_t ra = smem_u32(raw + rs * kPairRaw), rb = ra + kPairRawA;
                 const uint32_t ob = smem_u32(ops + os * kPairOp);
-                // thread t: channel t and token t of this CTA; all loads first, to overlap
-                uint4 va[4], vb[4];
+                // thread t: channel t, and three of the 96 x 4 pieces of the tokens; all loads first, to overlap
+                uint4 va[4], vb[3];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) va[c] = ld_shared_v4(ra + t * 128 + (((4 * wg + c) ^ (t & 7)) << 4));
 #pragma unroll
-                for (int c = 0; c < 4; ++c) vb[c] = ld_shared_v4(rb + t * 128 + (((4 * wg + c) ^ (t & 7)) << 4));
+                for (int j = 0; j < 3; ++j) {
+                    const int i = j * 128 + t, r = i % kPairHalf, c = i / kPairHalf;
+                    vb[j] = ld_shared_v4(rb + r * 128 + (((4 * wg + c) ^ (r & 7)) << 4));
+                }
 #pragma unroll
                 for (int c = 0; c < 4; c += 2) {
                     uint32_t h[16];
@@ -228,14 +224,15 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                     tmem_st_x16(tmem_a + lanes + os * 32 + c * 8, h);
                 }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int j = 0; j < 3; ++j) {
+                    const int i = j * 128 + t, r = i % kPairHalf, c = i / kPairHalf;
                     uint4 lo, hi;
-                    codes_to_half(vb[c].x, lo.x, lo.y);
-                    codes_to_half(vb[c].y, lo.z, lo.w);
-                    codes_to_half(vb[c].z, hi.x, hi.y);
-                    codes_to_half(vb[c].w, hi.z, hi.w);
-                    st_shared_v4(ob + t * 128 + (((2 * c) ^ (t & 7)) << 4), lo);
-                    st_shared_v4(ob + t * 128 + (((2 * c + 1) ^ (t & 7)) << 4), hi);
+                    codes_to_half(vb[j].x, lo.x, lo.y);
+                    codes_to_half(vb[j].y, lo.z, lo.w);
+                    codes_to_half(vb[j].z, hi.x, hi.y);
+                    codes_to_half(vb[j].w, hi.z, hi.w);
+                    st_shared_v4(ob + r * 128 + (((2 * c) ^ (r & 7)) << 4), lo);
+                    st_shared_v4(ob + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4), hi);
                 }
                 fence_proxy_async_smem();
                 tmem_wait_st();
@@ -243,37 +240,39 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(raw_empty + 8 * rs);
-                    mbar_arrive(op_full + 8 * os);
+                    mbar_arrive_leader(op_full + 8 * os);
                 }
             }
         }
         if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsRead));
-        constexpr int HALF = kPairTokens / 2;
+        constexpr int HALF = kPairHalf;
         const int wg = (warp - 12) >> 2, row = threadIdx.x & 127;
         const uint32_t base = tmem + (static_cast<uint32_t>(warp & 3) << 21) + wg * HALF;
-        long long chunks = 0;
+        uint32_t chunks = 0;
         for (long long tile = first; tile < ntiles && ok; tile += stride) {
             int acc[HALF];
 #pragma unroll
             for (int i = 0; i < HALF; ++i) acc[i] = 0;
             for (int s = 0; s < steps; s += kTcChunk, ++chunks) {
-                ok = mbar_wait<SCOPE_CTA>(acc_full, static_cast<uint32_t>(chunks & 1), limit);
+                const uint32_t buf = chunks & 1u;
+                ok = mbar_wait<SCOPE_CTA>(acc_full + 8 * buf, (chunks >> 1) & 1u, limit);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < HALF; c += 16) {
-                    uint32_t v[16];
-                    tmem_ld_x16(base + c, v);
+                for (int c = 0; c < HALF; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld_x16(base + buf * kPairTokens + c, v);
+                    tmem_ld_x16(base + buf * kPairTokens + c + 16, v + 16);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+                    for (int j = 0; j < 32; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_leader_relaxed(acc_empty);
+                if (lane == 0) mbar_arrive_leader_relaxed(acc_empty + 8 * buf);
             }
             if (!ok) break;
             int tn, tm;
