@@ -57,15 +57,6 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar)
         ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
 }
 
-__device__ __forceinline__ void tc_mma_pair(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
-        : "memory");
-}
-
 __global__ void __launch_bounds__(kTcThreads, 1) __cluster_dims__(2, 1, 1)
 rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
                         const MatmulParams p, const TcTiles tiles)
@@ -151,31 +142,46 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
         } else if (warp == 1 && rank == 0) {
             constexpr uint32_t idesc = (1u << 4) | ((kPairTokens / 8u) << 17) | ((2u * kTcRows / 16u) << 24);
             const bool one = elect_one();
-            uint32_t slot = 0, phase = 0, chunks = 0;
+            const uint32_t desc0 = tc_desc_lo(smem_u32(ops));
+            uint32_t slot = 0, phase = 0, chunks = 0;    // a code stage fills operand stages slot and slot + 1
+            bool ready0 = false, ready1 = false;         // asked a stage ahead
             for (long long tile = first; tile < ntiles && ok; tile += stride) {
-                for (int s = 0; s < 2 * steps; ++s) {
-                    const bool head = s % (2 * kTcChunk) == 0;
-                    const bool tail = s % (2 * kTcChunk) == 2 * kTcChunk - 1 || s == 2 * steps - 1;
-                    const uint32_t buf = chunks & 1u;
-                    if (head) ok = mbar_wait<SCOPE_CLUSTER>(acc_empty + 8 * buf, ((chunks >> 1) & 1u) ^ 1u, limit);
-                    ok = ok && mbar_wait<SCOPE_CLUSTER>(op_full + 8 * slot, phase, limit);
+                int left = 0;                            // code stages until the read-out
+                for (int s = 0; s < steps; ++s) {
+                    const bool fresh = left == 0;
+                    if (fresh) {
+                        left = kTcChunk;
+                        ok = mbar_wait<SCOPE_CLUSTER>(acc_empty + 8 * (chunks & 1u), ((chunks >> 1) & 1u) ^ 1u, limit);
+                        ++chunks;
+                    }
+                    const uint32_t buf = (chunks - 1) & 1u, acc = tmem + buf * kPairTokens;
+                    const bool tail = --left == 0 || s == steps - 1;
+                    const uint32_t next = slot + 2 == OPS ? 0 : slot + 2, next_phase = slot + 2 == OPS ? phase ^ 1u : phase;
+                    if (!ready0) ok = ok && mbar_wait<SCOPE_CLUSTER>(op_full + 8 * slot, phase, limit);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t desc = tc_desc(smem_u32(ops) + slot * kPairOp);
                     if (one) {
-#pragma unroll
-                        for (int k = 0; k < kTcStep / 16; ++k)
-                            tc_mma_pair(tmem + buf * kPairTokens, tmem_a + slot * 32 + k * 8, desc + 2 * k, idesc, !(head && k == 0));
+                        tc_mma_step<true>(acc, tmem_a + slot * 32, desc0 + slot * (kPairOp / 16), idesc, fresh);
                         tc_commit_pair(op_empty + 8 * slot);
+                    }
+                    __syncwarp();
+                    if (!ready1) ok = mbar_wait<SCOPE_CLUSTER>(op_full + 8 * slot + 8, phase, limit);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const bool peek0 = mbar_test<SCOPE_CLUSTER>(op_full + 8 * next, next_phase);
+                    const bool peek1 = mbar_test<SCOPE_CLUSTER>(op_full + 8 * next + 8, next_phase);
+                    if (one) {
+                        tc_mma_step<true>(acc, tmem_a + slot * 32 + 32, desc0 + (slot + 1) * (kPairOp / 16), idesc, false);
+                        tc_commit_pair(op_empty + 8 * slot + 8);
                         if (tail) tc_commit_pair(acc_full + 8 * buf);
                     }
                     __syncwarp();
-                    chunks += tail;
-                    if (++slot == OPS) {
-                        slot = 0;
-                        phase ^= 1u;
-                    }
+                    ready0 = __all_sync(0xFFFFFFFFu, peek0);
+                    ready1 = __all_sync(0xFFFFFFFFu, peek1);
+                    slot = next;
+                    phase = next_phase;
                 }
             }
             if (!ok && one) {
@@ -190,18 +196,14 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsConvert));
         const int wg = (warp - 4) >> 2, t = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;     // this warp's TMEM lanes, in bits 16+
-        long long it = 0;
+        uint32_t rs = 0, rphase = 0, os = wg, ophase = 0;
+        bool ready = false;                  // the next code stage, asked ahead
         for (long long tile = first; tile < ntiles && ok; tile += stride) {
-            for (int s = 0; s < steps; ++s, ++it) {
-                const long long op = 2 * it + wg;
-                const int rs = static_cast<int>(it % RAWS), os = static_cast<int>(op % OPS);
-                ok = mbar_wait<SCOPE_CTA>(raw_full + 8 * rs, static_cast<uint32_t>(it / RAWS) & 1u, limit) &&
-                     mbar_wait<SCOPE_CTA>(op_empty + 8 * os, (static_cast<uint32_t>(op / OPS) & 1u) ^ 1u, limit);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t ra = smem_u32(raw + rs * kPairRaw), rb = ra + kPairRawA;
-                const uint32_t ob = smem_u32(ops + os * kPairOp);
+            for (int s = 0; s < steps; ++s) {
+                if (!ready) ok = mbar_wait<SCOPE_CTA>(raw_full + 8 * rs, rphase, limit);
+                const uint32_t rnext = rs + 1 == RAWS ? 0 : rs + 1, rnext_phase = rs + 1 == RAWS ? rphase ^ 1u : rphase;
+                const uint32_t ra = smem_u32(raw) + rs * kPairRaw, rb = ra + kPairRawA;
+                const uint32_t ob = smem_u32(ops) + os * kPairOp;
                 // thread t: channel t, and three of the 96 x 4 pieces of the tokens; all loads first, to overlap
                 uint4 va[4], vb[3];
 #pragma unroll
@@ -211,6 +213,11 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                     const int i = j * 128 + t, r = i % kPairHalf, c = i / kPairHalf;
                     vb[j] = ld_shared_v4(rb + r * 128 + (((4 * wg + c) ^ (r & 7)) << 4));
                 }
+                ok = ok && mbar_wait<SCOPE_CTA>(op_empty + 8 * os, ophase ^ 1u, limit);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                const bool peek = mbar_test<SCOPE_CTA>(raw_full + 8 * rnext, rnext_phase);
+                tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < 4; c += 2) {
                     uint32_t h[16];
@@ -241,6 +248,14 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                 if (lane == 0) {
                     mbar_arrive(raw_empty + 8 * rs);
                     mbar_arrive_leader(op_full + 8 * os);
+                }
+                ready = __all_sync(0xFFFFFFFFu, peek);
+                rs = rnext;
+                rphase = rnext_phase;
+                os += 2;
+                if (os >= OPS) {
+                    os -= OPS;
+                    ophase ^= 1u;
                 }
             }
         }

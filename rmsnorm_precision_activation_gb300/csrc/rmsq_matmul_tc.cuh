@@ -65,14 +65,27 @@ __device__ __forceinline__ void tc_commit(uint32_t bar)
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// d (+)= a b^T: a fp16 in TMEM (128 lanes, 8 columns), b fp16 in shared memory (K-major).
-__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+// One operand stage: d (+)= a b^T over 64 elements of k, four MMAs. a is fp16 in TMEM (128 lanes, 8
+// columns per MMA), b fp16 in shared memory (K-major, 32 bytes per MMA; desc_lo: the descriptor's
+// low word, which holds the address). fresh: overwrite d. PAIR: with the other CTA (cta_group::2).
+template <bool PAIR>
+__device__ __forceinline__ void tc_mma_step(uint32_t d, uint32_t a, uint32_t desc_lo, uint32_t idesc, bool fresh)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
-        : "memory");
+    constexpr uint32_t hi = 64u | (1u << 14) | (2u << 29);
+#pragma unroll
+    for (int k = 0; k < kTcStep / 16; ++k) {
+        const uint32_t add = k > 0 || !fresh;
+        if constexpr (PAIR)
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+                "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+                ::"r"(d), "r"(a + 8 * k), "r"(desc_lo + 2 * k), "r"(hi), "r"(idesc), "r"(add) : "memory");
+        else
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+                "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+                ::"r"(d), "r"(a + 8 * k), "r"(desc_lo + 2 * k), "r"(hi), "r"(idesc), "r"(add) : "memory");
+    }
 }
 
 // One lane of a converged warp.
@@ -83,11 +96,9 @@ __device__ __forceinline__ bool elect_one()
     return one != 0;
 }
 
-// K-major operand with 128-byte swizzle: groups of 8 rows are 1024 bytes apart.
-__device__ __forceinline__ uint64_t tc_desc(uint32_t addr)
-{
-    return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// Low word of the descriptor of a K-major operand with 128-byte swizzle, whose groups of 8 rows are
+// 1024 bytes apart (the high word is constant: that pitch, the version, the swizzle).
+__device__ __forceinline__ uint32_t tc_desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
 
 // Four codes to four fp16: with the sign bit flipped a code is b = code + 128; the fp16 with high
 // byte 0x64 and low byte b is 1024 + b, from which 1152 is subtracted exactly.
@@ -251,30 +262,45 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         // uniform registers (from divergent code an MMA took 60 cycles to issue).
         constexpr uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(NT / 8) << 17) | ((kTcRows / 16u) << 24);
         const bool one = elect_one();
-        uint32_t slot = 0, phase = 0, chunks = 0;
+        const uint32_t desc0 = tc_desc_lo(smem_u32(ops));
+        uint32_t slot = 0, phase = 0, chunks = 0;        // a code stage fills operand stages slot and slot + 1
+        bool ready0 = false, ready1 = false;             // asked a stage ahead
         for (long long tile = first; tile < ntiles && ok; tile += stride) {
-            for (int s = 0; s < 2 * steps; ++s) {
-                const bool head = s % (2 * kTcChunk) == 0;
-                const bool tail = s % (2 * kTcChunk) == 2 * kTcChunk - 1 || s == 2 * steps - 1;
-                if (head) ok = mbar_wait<SCOPE_CTA>(acc_empty, (chunks & 1u) ^ 1u, limit);
-                ok = ok && mbar_wait<SCOPE_CTA>(op_full + 8 * slot, phase, limit);
+            int left = 0;                                // code stages until the read-out
+            for (int s = 0; s < steps; ++s) {
+                const bool fresh = left == 0;
+                if (fresh) {
+                    left = kTcChunk;
+                    ok = mbar_wait<SCOPE_CTA>(acc_empty, (chunks & 1u) ^ 1u, limit);
+                    ++chunks;
+                }
+                const bool tail = --left == 0 || s == steps - 1;
+                const uint32_t next = slot + 2 == OPS ? 0 : slot + 2, next_phase = slot + 2 == OPS ? phase ^ 1u : phase;
+                if (!ready0) ok = ok && mbar_wait<SCOPE_CTA>(op_full + 8 * slot, phase, limit);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint64_t desc = tc_desc(smem_u32(ops) + slot * S::OP);
                 if (one) {
-#pragma unroll
-                    for (int k = 0; k < kTcStep / 16; ++k)
-                        tc_mma(tmem, tmem_a + slot * 32 + k * 8, desc + 2 * k, idesc, !(head && k == 0));
+                    tc_mma_step<false>(tmem, tmem_a + slot * 32, desc0 + slot * (S::OP / 16), idesc, fresh);
                     tc_commit(op_empty + 8 * slot);
+                }
+                __syncwarp();
+                if (!ready1) ok = mbar_wait<SCOPE_CTA>(op_full + 8 * slot + 8, phase, limit);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const bool peek0 = mbar_test<SCOPE_CTA>(op_full + 8 * next, next_phase);
+                const bool peek1 = mbar_test<SCOPE_CTA>(op_full + 8 * next + 8, next_phase);
+                if (one) {
+                    tc_mma_step<false>(tmem, tmem_a + slot * 32 + 32, desc0 + (slot + 1) * (S::OP / 16), idesc, false);
+                    tc_commit(op_empty + 8 * slot + 8);
                     if (tail) tc_commit(acc_full);
                 }
                 __syncwarp();
-                chunks += tail;
-                if (++slot == OPS) {
-                    slot = 0;
-                    phase ^= 1u;
-                }
+                ready0 = __all_sync(0xFFFFFFFFu, peek0);
+                ready1 = __all_sync(0xFFFFFFFFu, peek1);
+                slot = next;
+                phase = next_phase;
             }
         }
         if (!ok && one) {

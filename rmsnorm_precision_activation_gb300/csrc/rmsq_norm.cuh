@@ -146,6 +146,22 @@ template <int SCOPE> __device__ __forceinline__ bool mbar_try_wait_long(uint32_t
     return ok != 0;
 }
 
+// Whether the phase is over, without waiting: asked one step ahead, its latency (about 150 cycles,
+// which a wait for a finished phase costs too) passes behind other work.
+template <int SCOPE> __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    if constexpr (SCOPE == SCOPE_CLUSTER)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+
 // A timeout as mbar_wait takes it: 32 bits of nanoseconds (registers are scarce where it waits).
 __device__ __forceinline__ uint32_t wait_limit(unsigned long long timeout_ns)
 {
