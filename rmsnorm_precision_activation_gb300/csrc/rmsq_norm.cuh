@@ -177,6 +177,7 @@ __device__ __forceinline__ uint32_t globaltimer_lo()
 
 template <int SCOPE> __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t limit_ns)
 {
+    if (mbar_test<SCOPE>(bar, parity)) return true;
     if (mbar_try_wait_long<SCOPE>(bar, parity)) return true;
     const uint32_t t0 = globaltimer_lo();
 #pragma unroll 1
