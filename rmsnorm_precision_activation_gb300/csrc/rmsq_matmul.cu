@@ -66,14 +66,17 @@ template <int NT> static cudaError_t launch_tc(MatmulParams& p, const DeviceView
     t.n_tiles = static_cast<int>((p.n + kTcRows - 1) / kTcRows);
     t.m_tiles = static_cast<int>((p.m + NT - 1) / NT);
     const long long tiles = static_cast<long long>(t.n_tiles) * t.m_tiles;
-    // CTAs that share a tile's k: while that leaves no SM with two tiles and each CTA 2 code stages
-    int cluster = 1;
+    // CTAs that share a tile's k: as many as the SMs hold, each with at least 2 code stages
+    const long long slots = static_cast<long long>(dv.sms) * TcShape<NT>::CTAS;
     const int steps = (p.k + kTcCodes - 1) / kTcCodes;
-    while (cluster < 8 && tiles * cluster * 2 <= dv.sms && steps >= 4 * cluster) cluster *= 2;
-    const long long grid = cluster > 1 ? tiles * cluster : tiles < dv.sms ? tiles : dv.sms;
+    long long cluster = slots / tiles < 8 ? slots / tiles : 8;
+    if (cluster > steps / 2) cluster = steps / 2;
+    if (cluster < 1) cluster = 1;
+    const long long grid = cluster > 1 ? tiles * cluster : tiles < slots ? tiles : slots;
     void* args[] = {&map_w, &map_a, &p, &t};
     return launch_kernel(reinterpret_cast<const void*>(&rmsq_matmul_tc_kernel<NT>),
-                         dim3(static_cast<unsigned>(grid)), kTcThreads, TcShape<NT>::SMEM, cluster, stream, args);
+                         dim3(static_cast<unsigned>(grid)), TcShape<NT>::THREADS, TcShape<NT>::SMEM,
+                         static_cast<int>(cluster), stream, args);
 }
 
 static cudaError_t launch_pair(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)

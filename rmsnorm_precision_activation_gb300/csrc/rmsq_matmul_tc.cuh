@@ -13,8 +13,7 @@
 //                first operand from there, which spares shared memory a write and a read), the
 //                tokens' into shared memory
 //   warp 1       one thread issues tcgen05.mma, four per operand stage
-//   warps 12-19  two warpgroups read the accumulator out, half of the tokens each, and write the
-//                output
+//   warps 12-    one or two warpgroups read the accumulator out and write the output
 // The weight is read as codes, so a call with few tokens streams one byte per weight; CTAs of a
 // cluster then share a tile's k and add their integer sums through distributed shared memory.
 //
@@ -35,16 +34,25 @@ constexpr int kTcChunk = 1024 / kTcCodes; // code stages per read-out of the acc
 constexpr int kTcRows = 128;             // output channels per CTA
 
 template <int NT> struct TcShape {
+    // Few tokens leave room for two CTAs on an SM, each with half of TMEM: a stage's hand-overs from
+    // role to role take about 1000 cycles whatever its size, and a second CTA fills them (CTAS
+    // hold up to 32 tokens, so that one warpgroup reads the sums).
+    static constexpr int CTAS = NT <= 32 ? 2 : 1;
+    static constexpr int READERS = 8 / CTAS;                          // warps that read the accumulator
+    static constexpr int THREADS = 32 * (12 + READERS);
+    static constexpr int COLS = 512 / CTAS;                           // TMEM columns
+    static constexpr int ACC = NT <= 32 ? 64 : 256;                   // of these, before the operand stages
     static constexpr int RAW_A = kTcRows * kTcCodes;
     static constexpr int RAW_B = NT * kTcCodes;
     static constexpr int RAW = RAW_A + RAW_B;
     static constexpr int OP = NT * kTcStep * 2;
-    static constexpr int OPS = NT >= 128 ? 6 : 8;                                   // operand stages
-    static constexpr int RAWS = NT >= 128 ? 4 : NT >= 64 ? 6 : 8;    // code stages
-    // 1024 bytes to align the ring, 1024 for barriers; over half of an SM's shared memory, so one
-    // CTA per SM, which may take all of TMEM
+    static constexpr int OPS = NT >= 128 || NT <= 32 ? 6 : 8;         // operand stages
+    static constexpr int RAWS = NT >= 128 ? 4 : NT >= 64 ? 6 : NT >= 32 ? 4 : 5;    // code stages
+    // 1024 bytes to align the ring, 1024 for barriers
     static constexpr int SMEM = 2048 + RAWS * RAW + OPS * OP;
-    static_assert(SMEM > 116 * 1024 && SMEM <= 232448, "one CTA per SM");
+    // no more CTAs on an SM than TMEM has columns for, or its allocation would wait for one to end
+    static_assert(CTAS == 2 ? SMEM > 78 * 1024 && SMEM <= 112 * 1024 : SMEM > 116 * 1024 && SMEM <= 232448, "CTAs per SM");
+    static_assert(NT <= ACC && ACC + 32 * OPS <= COLS, "accumulator and operand stages in TMEM");
     static_assert(RAWS * RAW + OPS * OP >= NT * kTcRows * 4, "the cluster's sums reuse the ring");
 };
 
@@ -111,13 +119,6 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t
     asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
 }
 
-__device__ __forceinline__ void tmem_st_x8(uint32_t addr, const uint32_t (&v)[8])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 __device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t (&v)[16])
 {
     asm volatile(
@@ -127,14 +128,7 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t (&v)[1
         : "memory");
 }
 
-// 8 columns of this warp's lanes; values are valid after tmem_wait_ld.
-__device__ __forceinline__ void tmem_ld_x8(uint32_t addr, uint32_t* v)
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "r"(addr)
-                 : "memory");
-}
+// 16 columns of this warp's lanes; the values are valid after tmem_wait_ld.
 __device__ __forceinline__ void tmem_ld_x16(uint32_t addr, uint32_t* v)
 {
     asm volatile(
@@ -174,7 +168,7 @@ __device__ __forceinline__ void tc_tile(long long i, const TcTiles& t, int& n, i
 }
 
 template <int NT>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(TcShape<NT>::THREADS, TcShape<NT>::CTAS)
 rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
                       const MatmulParams p, const TcTiles tiles)
 {
@@ -205,13 +199,14 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
             mbar_init(op_empty + 8 * i, 1);
         }
         mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 8);
+        mbar_init(acc_empty, S::READERS);
         mbar_init(drain, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                     "r"(S::COLS)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
         tc_fence_before();
@@ -219,7 +214,7 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const uint32_t tmem_a = tmem + 256;      // operand stages of 32 columns behind the accumulator
+    const uint32_t tmem_a = tmem + S::ACC;   // operand stages of 32 columns behind the accumulator
     pdl_wait();
 
     const int steps_all = (p.k + kTcCodes - 1) / kTcCodes;      // code stages
@@ -313,38 +308,49 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     } else if (warp >= 4 && warp < 12) {
         const int wg = (warp - 4) >> 2, t = (threadIdx.x - 128) & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;     // this warp's TMEM lanes, in bits 16+
-        long long it = 0;
+        constexpr int PB = (NT * 4 + 127) / 128;      // a thread's pieces of the tokens' NT x 4
+        uint32_t rs = 0, rphase = 0, os = wg, ophase = 0;
+        bool ready = false;                  // the next code stage, asked ahead
         for (long long tile = first; tile < ntiles && ok; tile += stride) {
-            for (int s = 0; s < steps; ++s, ++it) {
-                const long long op = 2 * it + wg;
-                const int rs = static_cast<int>(it % RAWS), os = static_cast<int>(op % OPS);
-                ok = mbar_wait<SCOPE_CTA>(raw_full + 8 * rs, static_cast<uint32_t>(it / RAWS) & 1u, limit) &&
-                     mbar_wait<SCOPE_CTA>(op_empty + 8 * os, (static_cast<uint32_t>(op / OPS) & 1u) ^ 1u, limit);
+            for (int s = 0; s < steps; ++s) {
+                if (!ready) ok = mbar_wait<SCOPE_CTA>(raw_full + 8 * rs, rphase, limit);
+                const uint32_t rnext = rs + 1 == RAWS ? 0 : rs + 1, rnext_phase = rs + 1 == RAWS ? rphase ^ 1u : rphase;
+                const uint32_t ra = smem_u32(raw) + rs * S::RAW, rb = ra + S::RAW_A;
+                const uint32_t ob = smem_u32(ops) + os * S::OP;
+                uint4 va[4], vb[PB];                  // all loads first, to overlap
+#pragma unroll
+                for (int c = 0; c < 4; ++c) va[c] = ld_shared_v4(ra + t * 128 + (((4 * wg + c) ^ (t & 7)) << 4));
+#pragma unroll
+                for (int j = 0; j < PB; ++j) {
+                    const int i = j * 128 + t, r = i % NT, c = i / NT;
+                    if (c < 4) vb[j] = ld_shared_v4(rb + r * 128 + (((4 * wg + c) ^ (r & 7)) << 4));
+                }
+                ok = ok && mbar_wait<SCOPE_CTA>(op_empty + 8 * os, ophase ^ 1u, limit);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) break;
+                const bool peek = mbar_test<SCOPE_CTA>(raw_full + 8 * rnext, rnext_phase);
                 tc_fence_after();
-                const uint32_t ra = smem_u32(raw + rs * S::RAW), rb = ra + S::RAW_A;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const uint4 v = ld_shared_v4(ra + t * 128 + (((4 * wg + c) ^ (t & 7)) << 4));
-                    uint32_t h[8];
-                    codes_to_half(v.x, h[0], h[1]);
-                    codes_to_half(v.y, h[2], h[3]);
-                    codes_to_half(v.z, h[4], h[5]);
-                    codes_to_half(v.w, h[6], h[7]);
-                    tmem_st_x8(tmem_a + lanes + os * 32 + c * 8, h);
+                for (int c = 0; c < 4; c += 2) {
+                    uint32_t h[16];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        codes_to_half(va[c + i].x, h[8 * i], h[8 * i + 1]);
+                        codes_to_half(va[c + i].y, h[8 * i + 2], h[8 * i + 3]);
+                        codes_to_half(va[c + i].z, h[8 * i + 4], h[8 * i + 5]);
+                        codes_to_half(va[c + i].w, h[8 * i + 6], h[8 * i + 7]);
+                    }
+                    tmem_st_x16(tmem_a + lanes + os * 32 + c * 8, h);
                 }
-                const uint32_t ob = smem_u32(ops + os * S::OP);
 #pragma unroll
-                for (int j = 0; j < (NT * 4 + 127) / 128; ++j) {
+                for (int j = 0; j < PB; ++j) {
                     const int i = j * 128 + t, r = i % NT, c = i / NT;
                     if (c < 4) {
-                        const uint4 v = ld_shared_v4(rb + r * 128 + (((4 * wg + c) ^ (r & 7)) << 4));
                         uint4 lo, hi;
-                        codes_to_half(v.x, lo.x, lo.y);
-                        codes_to_half(v.y, lo.z, lo.w);
-                        codes_to_half(v.z, hi.x, hi.y);
-                        codes_to_half(v.w, hi.z, hi.w);
+                        codes_to_half(vb[j].x, lo.x, lo.y);
+                        codes_to_half(vb[j].y, lo.z, lo.w);
+                        codes_to_half(vb[j].z, hi.x, hi.y);
+                        codes_to_half(vb[j].w, hi.z, hi.w);
                         st_shared_v4(ob + r * 128 + (((2 * c) ^ (r & 7)) << 4), lo);
                         st_shared_v4(ob + r * 128 + (((2 * c + 1) ^ (r & 7)) << 4), hi);
                     }
@@ -357,11 +363,19 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     mbar_arrive(raw_empty + 8 * rs);
                     mbar_arrive(op_full + 8 * os);
                 }
+                ready = __all_sync(0xFFFFFFFFu, peek);
+                rs = rnext;
+                rphase = rnext_phase;
+                os += 2;
+                if (os >= OPS) {
+                    os -= OPS;
+                    ophase ^= 1u;
+                }
             }
         }
         if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
     } else if (warp >= 12) {
-        constexpr int HALF = NT / 2, LD = HALF < 32 ? HALF : 32;     // columns of a warp, and of one read
+        constexpr int HALF = NT * 4 / S::READERS, LD = HALF < 32 ? HALF : 32;     // columns of a warp, and of one read
         const int wg = (warp - 12) >> 2, row = threadIdx.x & 127;
         const uint32_t base = tmem + (static_cast<uint32_t>(warp & 3) << 21) + wg * HALF;
         long long chunks = 0;
@@ -377,12 +391,8 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
 #pragma unroll
                 for (int c = 0; c < HALF; c += LD) {
                     uint32_t v[LD];
-                    if constexpr (LD == 8) {
-                        tmem_ld_x8(base + c, v);
-                    } else {
-                        tmem_ld_x16(base + c, v);
-                        if constexpr (LD == 32) tmem_ld_x16(base + c + 16, v + 16);
-                    }
+                    tmem_ld_x16(base + c, v);
+                    if constexpr (LD == 32) tmem_ld_x16(base + c + 16, v + 16);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < LD; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
@@ -420,7 +430,7 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         int tn, tm;
         tc_tile(first, tiles, tn, tm);
         const uint32_t sums = smem_u32(raw);
-        for (int e = threadIdx.x; e < (NT + static_cast<int>(nc) - 1) / static_cast<int>(nc) * 32; e += kTcThreads) {
+        for (int e = threadIdx.x; e < (NT + static_cast<int>(nc) - 1) / static_cast<int>(nc) * 32; e += S::THREADS) {
             const int i = (e >> 5) * static_cast<int>(nc) + static_cast<int>(rank);
             const long long m = static_cast<long long>(tm) * NT + i, n = static_cast<long long>(tn) * kTcRows + lane * 4;
             if (i >= NT || m >= p.m || n >= p.n) continue;
@@ -446,7 +456,7 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::COLS));
     }
 }
 
