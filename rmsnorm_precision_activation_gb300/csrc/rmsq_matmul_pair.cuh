@@ -77,7 +77,22 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rank = static_cast<int>(cluster_rank());
 
+    const int steps = (p.k + kTcCodes - 1) / kTcCodes;      // code stages
+    const long long ntiles = static_cast<long long>(tiles.n_tiles) * tiles.m_tiles;
+    const long long first = cluster_id(), stride = cluster_count();
+
+    // Code stage s of a tile into this CTA's ring (one thread).
+    auto fetch = [&](uint32_t slot, int s, int tn, int tm) {
+        const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw) + slot * kPairRaw;
+        mbar_arrive_expect_tx(full, kPairRaw);
+        tma_load_2d(dst, &map_w, s * kTcCodes, (tn * 2 + rank) * kTcRows, full);
+        tma_load_2d(dst + kPairRawA, &map_a, s * kTcCodes, tm * kPairTokens + rank * kPairHalf, full);
+    };
+    int started = 0;                          // stages of the first tile fetched ahead
+
     if (threadIdx.x == 0) {
+        prefetch_map(&map_w);
+        prefetch_map(&map_a);
         for (int i = 0; i < RAWS; ++i) {
             mbar_init(raw_full + 8 * i, 1);
             mbar_init(raw_empty + 8 * i, 8);
@@ -93,6 +108,11 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
         mbar_init(drain, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
+        // the first loads run while the pair sets itself up
+        pdl_wait();
+        int tn, tm;
+        tc_tile(first, tiles, tn, tm);
+        for (; started < RAWS && started < steps; ++started) fetch(started, started, tn, tm);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem_slot))
@@ -107,9 +127,6 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
     const uint32_t tmem_a = tmem + 2 * kPairTokens;      // operand stages of 32 columns behind the accumulators
     pdl_wait();
 
-    const int steps = (p.k + kTcCodes - 1) / kTcCodes;      // code stages
-    const long long ntiles = static_cast<long long>(tiles.n_tiles) * tiles.m_tiles;
-    const long long first = cluster_id(), stride = cluster_count();
     const uint32_t limit = wait_limit(p.timeout_ns), drain_limit = wait_limit(4 * p.timeout_ns);
     bool ok = true;
 
@@ -121,14 +138,11 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                 int tn, tm;
                 tc_tile(tile, tiles, tn, tm);
                 for (int s = 0; s < steps; ++s, ++it) {
-                    const int slot = static_cast<int>(it % RAWS);
-                    const uint32_t phase = static_cast<uint32_t>(it / RAWS) & 1u;
-                    ok = mbar_wait<SCOPE_CTA>(raw_empty + 8 * slot, phase ^ 1u, limit);
+                    if (it < started) continue;
+                    const uint32_t slot = static_cast<uint32_t>(it % RAWS);
+                    ok = mbar_wait<SCOPE_CTA>(raw_empty + 8 * slot, (static_cast<uint32_t>(it / RAWS) & 1u) ^ 1u, limit);
                     if (!ok) break;
-                    const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw + slot * kPairRaw);
-                    mbar_arrive_expect_tx(full, kPairRaw);
-                    tma_load_2d(dst, &map_w, s * kTcCodes, (tn * 2 + rank) * kTcRows, full);
-                    tma_load_2d(dst + kPairRawA, &map_a, s * kTcCodes, tm * kPairTokens + rank * kPairHalf, full);
+                    fetch(slot, s, tn, tm);
                 }
             }
             if (!ok) {

@@ -64,6 +64,11 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -189,7 +194,24 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t nc = cluster_size(), rank = cluster_rank();
 
+    const int steps_all = (p.k + kTcCodes - 1) / kTcCodes;      // code stages
+    const int k0 = static_cast<int>(static_cast<long long>(steps_all) * rank / nc);
+    const int steps = static_cast<int>(static_cast<long long>(steps_all) * (rank + 1) / nc) - k0;
+    const long long ntiles = static_cast<long long>(tiles.n_tiles) * tiles.m_tiles;
+    const long long first = cluster_id(), stride = cluster_count();
+
+    // Code stage s of a tile into the ring (one thread).
+    auto fetch = [&](uint32_t slot, int s, int tn, int tm) {
+        const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw) + slot * S::RAW;
+        mbar_arrive_expect_tx(full, S::RAW);
+        tma_load_2d(dst, &map_w, (k0 + s) * kTcCodes, tn * kTcRows, full);
+        tma_load_2d(dst + S::RAW_A, &map_a, (k0 + s) * kTcCodes, tm * NT, full);
+    };
+    int started = 0;                          // stages of the first tile fetched ahead
+
     if (threadIdx.x == 0) {
+        prefetch_map(&map_w);
+        prefetch_map(&map_a);
         for (int i = 0; i < RAWS; ++i) {
             mbar_init(raw_full + 8 * i, 1);
             mbar_init(raw_empty + 8 * i, 8);
@@ -203,6 +225,11 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         mbar_init(drain, 1);
         fence_mbar_init();
         fence_proxy_async_smem();
+        // the first loads run while the CTA sets itself up
+        pdl_wait();
+        int tn, tm;
+        tc_tile(first, tiles, tn, tm);
+        for (; started < RAWS && started < steps; ++started) fetch(started, started, tn, tm);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
@@ -217,11 +244,6 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     const uint32_t tmem_a = tmem + S::ACC;   // operand stages of 32 columns behind the accumulator
     pdl_wait();
 
-    const int steps_all = (p.k + kTcCodes - 1) / kTcCodes;      // code stages
-    const int k0 = static_cast<int>(static_cast<long long>(steps_all) * rank / nc);
-    const int steps = static_cast<int>(static_cast<long long>(steps_all) * (rank + 1) / nc) - k0;
-    const long long ntiles = static_cast<long long>(tiles.n_tiles) * tiles.m_tiles;
-    const long long first = cluster_id(), stride = cluster_count();
     const uint32_t limit = wait_limit(p.timeout_ns), drain_limit = wait_limit(4 * p.timeout_ns);
     bool ok = true;
 
@@ -232,14 +254,11 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 int tn, tm;
                 tc_tile(tile, tiles, tn, tm);
                 for (int s = 0; s < steps; ++s, ++it) {
-                    const int slot = static_cast<int>(it % RAWS);
-                    const uint32_t phase = static_cast<uint32_t>(it / RAWS) & 1u;
-                    ok = mbar_wait<SCOPE_CTA>(raw_empty + 8 * slot, phase ^ 1u, limit);
+                    if (it < started) continue;
+                    const uint32_t slot = static_cast<uint32_t>(it % RAWS);
+                    ok = mbar_wait<SCOPE_CTA>(raw_empty + 8 * slot, (static_cast<uint32_t>(it / RAWS) & 1u) ^ 1u, limit);
                     if (!ok) break;
-                    const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw + slot * S::RAW);
-                    mbar_arrive_expect_tx(full, S::RAW);
-                    tma_load_2d(dst, &map_w, (k0 + s) * kTcCodes, tn * kTcRows, full);
-                    tma_load_2d(dst + S::RAW_A, &map_a, (k0 + s) * kTcCodes, tm * NT, full);
+                    fetch(slot, s, tn, tm);
                 }
             }
             if (!ok) {
