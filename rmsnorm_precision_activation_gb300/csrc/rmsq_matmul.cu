@@ -9,21 +9,12 @@ namespace rmsq {
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-static cudaError_t launch_few(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
+template <int NB> static cudaError_t launch_stream(MatmulParams& p, cudaStream_t stream)
 {
-    const int mt = p.m <= 1 ? 1 : p.m <= 2 ? 2 : p.m <= 4 ? 4 : 8;
-    const void* fn = mt == 1 ? reinterpret_cast<const void*>(&rmsq_matmul_few_kernel<1>)
-                   : mt == 2 ? reinterpret_cast<const void*>(&rmsq_matmul_few_kernel<2>)
-                   : mt == 4 ? reinterpret_cast<const void*>(&rmsq_matmul_few_kernel<4>)
-                             : reinterpret_cast<const void*>(&rmsq_matmul_few_kernel<8>);
-    const long long tiles = (p.n + kFewRows - 1) / kFewRows, mtiles = (p.m + mt - 1) / mt;
-    // warps sharing a channel: until there are 32 warps per SM, or a warp has two pieces left
-    p.ksplit = 1;
-    while (p.ksplit < kFewWarps && tiles * mtiles * p.ksplit < 32LL * dv.sms && p.k > 1024 * p.ksplit) p.ksplit *= 2;
-    const long long per = kFewWarps / p.ksplit;
     void* args[] = {&p};
-    return launch_kernel(fn, dim3(static_cast<unsigned>((tiles + per - 1) / per), static_cast<unsigned>(mtiles)),
-                         kFewWarps * 32, 0, 1, stream, args);
+    return launch_kernel(reinterpret_cast<const void*>(&rmsq_matmul_stream_kernel<NB>),
+                         dim3(static_cast<unsigned>((p.n + kStreamRows - 1) / kStreamRows)), kStreamWarps * 32, 0, 1,
+                         stream, args);
 }
 
 // cuTensorMapEncodeTiled from the driver (the library does not link it).
@@ -104,8 +95,8 @@ static cudaError_t launch_pair(MatmulParams& p, const DeviceView& dv, cudaStream
 
 static cudaError_t launch_matmul(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
 {
-    if (p.m <= 8) return launch_few(p, dv, stream);
-    if (p.m <= 16) return launch_tc<16>(p, dv, stream);
+    if (p.m <= 8) return launch_stream<1>(p, stream);
+    if (p.m <= 16) return launch_stream<2>(p, stream);
     if (p.m <= 32) return launch_tc<32>(p, dv, stream);
     if (p.m <= 64) return launch_tc<64>(p, dv, stream);
     if (p.m <= 256 || p.n <= 128) return launch_tc<128>(p, dv, stream);

@@ -20,7 +20,6 @@ struct MatmulParams {
     long long m, n;
     int k;
     int dt;                    // output's type
-    int ksplit;                // few-token kernel: warps that share a channel's sum
     unsigned long long timeout_ns;
 };
 
@@ -44,70 +43,131 @@ __device__ __forceinline__ float scaled(int sum, float a_scale, float w_scale, f
     return has_bias ? __fadd_rn(v, bias) : v;
 }
 
-__device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int acc)
+// Four codes to four fp16: with the sign bit flipped a code is b = code + 128; the fp16 with high
+// byte 0x64 and low byte b is 1024 + b, from which 1152 is subtracted exactly.
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi)
 {
-    acc = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), acc);
-    acc = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), acc);
-    acc = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), acc);
-    return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), acc);
+    const uint32_t u = w ^ 0x80808080u;
+    lo = __byte_perm(u, 0x64646464u, 0x4140);
+    hi = __byte_perm(u, 0x64646464u, 0x4342);
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
 }
 
-// Few tokens: bound by the weight's bytes. A warp takes kFewRows channels and MT tokens and walks
-// k in 512-byte pieces, 16 bytes per lane; ksplit warps of the CTA share a channel's k where there
-// are too few channels to fill the SMs. Sums by dp4a (four products per instruction, exact).
-constexpr int kFewRows = 4;
-constexpr int kFewWarps = 8;
+// Single tokens and decode batches (NB x 8 tokens): bound by the weight's bytes. A CTA takes 32
+// channels; its 8 warps take k in turn, 64 bytes of every row at a time, load the codes straight into
+// registers, turn them into fp16 there and multiply with mma.sync (fp32 sums of up to 1024 products
+// are exact, then they go to integers). No shared memory or barrier stands between a load and its
+// use, so a short call costs little more than its bytes, where the tcgen05 kernels' hand-overs cost
+// about 8 us. Measured (GB300, weights from HBM): 1 to 8 tokens x 7168 x 8192 13 us, 4.5 TB/s (a dp4a
+// kernel: 13 us for 1 token, 28 for 8; tcgen05: 16.6); 16 x 8192 x 8192 16.7 us (tcgen05: 18.4);
+// 32 tokens 23.9 us (tcgen05: 19.8, so those go there).
+// A fragment's k order is free as long as both operands share it: lane (g, t) loads 16 bytes of row
+// g at 16 t, and the j-th four of them are its elements in the j-th of four MMAs.
+constexpr int kStreamWarps = 8;
+constexpr int kStreamRows = 32;
 
-template <int MT>
-__global__ void __launch_bounds__(kFewWarps * 32) rmsq_matmul_few_kernel(const MatmulParams p)
+template <int NB>
+__global__ void __launch_bounds__(kStreamWarps * 32, 2) rmsq_matmul_stream_kernel(const MatmulParams p)
 {
-    __shared__ int part[kFewWarps][kFewRows * MT];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int piece = warp % p.ksplit;
-    const long long n0 = (static_cast<long long>(blockIdx.x) * (kFewWarps / p.ksplit) + warp / p.ksplit) * kFewRows;
-    const long long m0 = static_cast<long long>(blockIdx.y) * MT;
+    // steps of 64 elements held in registers: one is multiplied while the loads of the others run
+    constexpr int U = NB == 1 ? 4 : NB == 2 ? 3 : 2;
+    __shared__ int part[kStreamWarps][NB * 8][kStreamRows + 1];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const long long n0 = static_cast<long long>(blockIdx.x) * kStreamRows;
+    const signed char* wp[4];
+    const signed char* ap[NB];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const long long n = n0 + 8 * i + g;
+        wp[i] = p.w + (n < p.n ? n : p.n - 1) * p.k + 16 * t;
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const long long m = 8 * b + g;
+        ap[b] = p.a + (m < p.m ? m : p.m - 1) * p.k + 16 * t;
+    }
     pdl_wait();
 
-    int acc[kFewRows][MT];
+    float c[2][NB][4];
 #pragma unroll
-    for (int r = 0; r < kFewRows; ++r)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int i = 0; i < MT; ++i) acc[r][i] = 0;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) c[i][b][e] = 0.f;
+    bool fresh = true;                                     // nothing in part yet
+    auto flush = [&]() {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    int& sum = part[warp][8 * b + 2 * t + (e & 1)][16 * i + g + 8 * (e >> 1)];
+                    sum = (fresh ? 0 : sum) + __float2int_rn(c[i][b][e]);
+                    c[i][b][e] = 0.f;
+                }
+        fresh = false;
+    };
 
-    if (n0 < p.n) {
-#pragma unroll 2
-        for (int c = (piece * 32 + lane) * 16; c < p.k; c += p.ksplit * 512) {
-            uint4 w[kFewRows];
+    uint4 wv[U][4], av[U][NB];
+    auto load = [&](int u, int step) {                     // past the end: zeros, nothing is read
+        const int k = step * 64;
+        const bool in = k + 16 * t < p.k;
 #pragma unroll
-            for (int r = 0; r < kFewRows; ++r) {
-                const long long n = n0 + r < p.n ? n0 + r : p.n - 1;
-                w[r] = ld_stream_v4(reinterpret_cast<const uint4*>(p.w + n * p.k + c));
+        for (int i = 0; i < 4; ++i)
+            wv[u][i] = in ? ld_stream_v4(reinterpret_cast<const uint4*>(wp[i] + k)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) av[u][b] = in ? ld_v4(ap[b] + k) : make_uint4(0, 0, 0, 0);
+    };
+    const int steps = (p.k + 63) / 64;
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(u, warp + u * kStreamWarps);
+    int held = 0;                                          // steps in c: at most 16, 1024 products
+    for (int s = warp; s < steps; s += U * kStreamWarps) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t w[4][4] = {{wv[u][0].x, wv[u][0].y, wv[u][0].z, wv[u][0].w},
+                                      {wv[u][1].x, wv[u][1].y, wv[u][1].z, wv[u][1].w},
+                                      {wv[u][2].x, wv[u][2].y, wv[u][2].z, wv[u][2].w},
+                                      {wv[u][3].x, wv[u][3].y, wv[u][3].z, wv[u][3].w}};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t lo[4], hi[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) codes_to_half(w[i][j], lo[i], hi[i]);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    const uint32_t a[4] = {av[u][b].x, av[u][b].y, av[u][b].z, av[u][b].w};
+                    uint32_t b0, b1;
+                    codes_to_half(a[j], b0, b1);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                            "{%8, %9}, {%0, %1, %2, %3};"
+                            : "+f"(c[i][b][0]), "+f"(c[i][b][1]), "+f"(c[i][b][2]), "+f"(c[i][b][3])
+                            : "r"(lo[2 * i]), "r"(lo[2 * i + 1]), "r"(hi[2 * i]), "r"(hi[2 * i + 1]), "r"(b0), "r"(b1));
+                }
             }
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const long long m = m0 + i < p.m ? m0 + i : p.m - 1;
-                const uint4 a = ld_v4(p.a + m * p.k + c);
-#pragma unroll
-                for (int r = 0; r < kFewRows; ++r) acc[r][i] = dot16(w[r], a, acc[r][i]);
+            load(u, s + (u + U) * kStreamWarps);
+            if (++held == 16) {
+                flush();
+                held = 0;
             }
         }
     }
-#pragma unroll
-    for (int r = 0; r < kFewRows; ++r)
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int s = __reduce_add_sync(0xFFFFFFFFu, acc[r][i]);
-            if (lane == 0) part[warp][r * MT + i] = s;
-        }
+    flush();
     __syncthreads();
-    for (int e = threadIdx.x; e < kFewWarps / p.ksplit * kFewRows * MT; e += kFewWarps * 32) {
-        const int row = e / MT, i = e % MT;
-        const long long n = static_cast<long long>(blockIdx.x) * (kFewWarps / p.ksplit) * kFewRows + row, m = m0 + i;
+    for (int e = threadIdx.x; e < NB * 8 * kStreamRows; e += kStreamWarps * 32) {
+        const int row = e % kStreamRows, m = e / kStreamRows;
+        const long long n = n0 + row;
         if (n < p.n && m < p.m) {
-            int s = 0;
-            for (int q = 0; q < p.ksplit; ++q) s += part[row / kFewRows * p.ksplit + q][row % kFewRows * MT + i];
+            int v = 0;
+#pragma unroll
+            for (int q = 0; q < kStreamWarps; ++q) v += part[q][m][row];
             store_as(p.out, m * p.n + n, p.dt,
-                     scaled(s, p.a_scale[m], p.w_scale[n], p.bias ? load_as(p.bias, n, p.dt) : 0.f, p.bias));
+                     scaled(v, p.a_scale[m], p.w_scale[n], p.bias ? load_as(p.bias, n, p.dt) : 0.f, p.bias));
         }
     }
 }

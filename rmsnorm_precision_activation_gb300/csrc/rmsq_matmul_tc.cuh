@@ -47,7 +47,7 @@ template <int NT> struct TcShape {
     static constexpr int RAW = RAW_A + RAW_B;
     static constexpr int OP = NT * kTcStep * 2;
     static constexpr int OPS = NT >= 128 || NT <= 32 ? 6 : 8;         // operand stages
-    static constexpr int RAWS = NT >= 128 ? 4 : NT >= 64 ? 6 : NT >= 32 ? 4 : 5;    // code stages
+    static constexpr int RAWS = NT >= 128 ? 4 : NT >= 64 ? 6 : 4;    // code stages
     // 1024 bytes to align the ring, 1024 for barriers
     static constexpr int SMEM = 2048 + RAWS * RAW + OPS * OP;
     // no more CTAs on an SM than TMEM has columns for, or its allocation would wait for one to end
@@ -112,17 +112,6 @@ __device__ __forceinline__ bool elect_one()
 // Low word of the descriptor of a K-major operand with 128-byte swizzle, whose groups of 8 rows are
 // 1024 bytes apart (the high word is constant: that pitch, the version, the swizzle).
 __device__ __forceinline__ uint32_t tc_desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
-
-// Four codes to four fp16: with the sign bit flipped a code is b = code + 128; the fp16 with high
-// byte 0x64 and low byte b is 1024 + b, from which 1152 is subtracted exactly.
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi)
-{
-    const uint32_t u = w ^ 0x80808080u;
-    lo = __byte_perm(u, 0x64646464u, 0x4140);
-    hi = __byte_perm(u, 0x64646464u, 0x4342);
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
-}
 
 __device__ __forceinline__ void tmem_st_x16(uint32_t addr, const uint32_t (&v)[16])
 {
