@@ -252,6 +252,10 @@ cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem,
             // clusters of 16 CTAs are beyond the portable size of 8
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            // the rings of several CTAs fit on one SM
+            if (e == cudaSuccess && smem > 0)
+                e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared);
             if (e != cudaSuccess) return e;
             if (g_nready < static_cast<int>(sizeof(g_ready) / sizeof(g_ready[0])))
                 g_ready[g_nready++] = ReadyFn{fn, dev};

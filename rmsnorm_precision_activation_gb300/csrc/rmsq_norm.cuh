@@ -12,21 +12,36 @@
 //   M2 = sum_w M2_w + n_w (mean_w - mean)^2,
 // which costs one block barrier instead of two.
 //
-// Bound by HBM. A warp, a CTA or a cluster of CTAs owns a row (SCOPE_*); every row has its own
-// thread group and no loop, so the hardware's CTA scheduler evens out SMs of unequal bandwidth.
-// gamma and beta stay in L1.
+// Bound by HBM. A row group of T threads (a warp for rows of up to 512 elements, else 16 or 24
+// elements a thread) takes rows in turn; a group's next rows come through a ring of shared-memory slots filled
+// by bulk copies, so that loads run while a row is reduced, and gamma and beta stay in shared memory.
+// (Rows loaded straight into registers, by a CTA each, reached 0.65-0.8 of the copy rate without a
+// residual and 0.14-0.28 at odd widths.) A CTA takes several rows and ends, rather than all of a
+// persistent CTA's share: the hardware's CTA scheduler then evens out SMs of unequal bandwidth. Rows wider
+// than 8192 elements are split over a cluster whose CTAs exchange the row's sums.
 #pragma once
 
 #include "rmsq_device.cuh"
 
 namespace rmsq {
 
-enum { SCOPE_WARP = 0, SCOPE_CTA = 1, SCOPE_CLUSTER = 2 };
+enum { SCOPE_WARP = 0, SCOPE_CTA = 1, SCOPE_CLUSTER = 2 };    // threads of a row group, or that a wait acquires from
 enum { NORM_LAYER = 0, NORM_LAYER_INT8 = 1, NORM_RMS_INT8 = 2 };
 
+// The rows a kernel reads through its rings.
+struct RowTensors {
+    const void* in[3];     // tensors [rows x hidden]
+    long long total;       // bytes of one
+    int ntens;
+    int rows;
+    int hidden;
+    int slice;             // elements of a row per CTA
+    int stages;            // ring slots per row group
+    int slot;              // bytes of one tensor's row in a slot (multiple of 16)
+};
+
 struct NormParams {
-    const void* x;
-    const void* res;       // or null
+    RowTensors r;          // x, and the residual where there is one
     void* res_out;         // or null
     const void* gamma;
     const void* beta;      // or null
@@ -34,11 +49,13 @@ struct NormParams {
     float* scale;          // int8: one per row
     float* mean;           // or null
     float* rstd;           // or null
-    long long rows;
-    int hidden;
-    int slice;             // elements of a row per CTA (SCOPE_CLUSTER), else hidden
+    int T;                 // threads per row group
+    int groups;            // row groups per CTA
+    int rows_per_group;
     float eps;
     float offset;
+    unsigned int* err;
+    unsigned long long timeout_ns;
 };
 
 // One element of a 16-bit or 32-bit type, by type code.
@@ -99,16 +116,14 @@ template <> struct Scalar<DT_F32> {
     static __device__ __forceinline__ T add(T a, T b) { return __fadd_rn(a, b); }
 };
 
-// fp32 values -> one 16-byte vector of the type.
-template <int DT> __device__ __forceinline__ uint4 pack_vec(const float* f)
+// fp32 pairs -> one 16-byte vector of the type.
+template <int DT> __device__ __forceinline__ uint4 pack_pairs(const float2* f)
 {
-    if constexpr (DT == DT_F32) {
-        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                          __float_as_uint(f[3]));
-    } else {
-        return make_uint4(Scalar<DT>::put2(f[0], f[1]), Scalar<DT>::put2(f[2], f[3]),
-                          Scalar<DT>::put2(f[4], f[5]), Scalar<DT>::put2(f[6], f[7]));
-    }
+    if constexpr (DT == DT_F32)
+        return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+    else
+        return make_uint4(Scalar<DT>::put2(f[0].x, f[0].y), Scalar<DT>::put2(f[1].x, f[1].y),
+                          Scalar<DT>::put2(f[2].x, f[2].y), Scalar<DT>::put2(f[3].x, f[3].y));
 }
 
 __device__ __forceinline__ uint4 ld_v4(const void* p)
@@ -207,6 +222,61 @@ template <int DT, int E, bool VEC> struct Deal {
     }
 };
 
+// Two 16-bit elements of a word, exact.
+template <int DT> __device__ __forceinline__ float2 unpack2(uint32_t w)
+{
+    if constexpr (DT == DT_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else return make_float2(Scalar<DT>::get(static_cast<uint16_t>(w & 0xFFFFu)), Scalar<DT>::get(static_cast<uint16_t>(w >> 16)));
+}
+
+// A thread's share of gamma or beta over all rows, as raw 32-bit words (two 16-bit elements each).
+template <int DT, int E, bool VEC> struct Held {
+    using D = Deal<DT, E, VEC>;
+    using T = typename Scalar<DT>::T;
+    static constexpr int PER = 4 / sizeof(T), N = E / PER;
+    uint32_t w[N];
+
+    __device__ __forceinline__ void load(const T* p, int t, int threads, int len)     // p may be null: zeros
+    {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int c = 0; c < D::NC; ++c) {
+                const int k = D::col(c, t, threads);
+                const uint4 v = p != nullptr && k < len ? ld_v4(p + k) : make_uint4(0, 0, 0, 0);
+                w[4 * c] = v.x;
+                w[4 * c + 1] = v.y;
+                w[4 * c + 2] = v.z;
+                w[4 * c + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < E; e += PER) {
+                uint32_t v = 0;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const int k = D::col(e + j, t, threads);
+                    if (p != nullptr && k < len) {
+                        if constexpr (PER == 1) v = __float_as_uint(p[k]);
+                        else v |= static_cast<uint32_t>(p[k]) << (16 * j);
+                    }
+                }
+                w[e / PER] = v;
+            }
+        }
+    }
+    // Keeps the compiler from holding the words unpacked across rows, which the registers do not allow.
+    __device__ __forceinline__ void pin()
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm volatile("" : "+r"(w[i]));
+    }
+    __device__ __forceinline__ float2 pair(int i) const          // elements 2 i and 2 i + 1
+    {
+        if constexpr (PER == 1) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return unpack2<DT>(w[i]);
+    }
+};
+
 // int8 codes of values already scaled to [-127, 127]: adding 1.5 * 2^23 rounds to nearest even
 // and leaves the code in the low byte.
 __device__ __forceinline__ uint32_t code_bits(float v) { return __float_as_uint(__fadd_rn(v, 12582912.0f)); }
@@ -218,235 +288,437 @@ __device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float 
     return __byte_perm(lo, hi, 0x5410);
 }
 
+// ------------------------------------------------------------------------------------------
+// Rows through shared memory
+// ------------------------------------------------------------------------------------------
+
+constexpr int kRingStages = 8;      // slots per group at most
+constexpr int kRingGroups = 16;     // row groups per CTA at most
+constexpr int kRingBars = 2 * kRingStages * kRingGroups * 8;      // bytes of barriers
+
+// A row group's ring of slots: its next rows, brought by bulk copies while the group works. Rows that
+// do not start on 16-byte boundaries (VEC false) are copied from the boundary below; the tensors' last
+// bytes, which no whole 16-byte piece covers, are read directly.
+template <int DT, bool VEC> struct RowRing {
+    using S = Scalar<DT>;
+    using T = typename S::T;
+    static constexpr int ES = sizeof(T), VW = VEC ? Elem<DT>::EPV : 1;
+    const RowTensors& r;
+    int c0, len;                   // the CTA's slice of a row
+    uint32_t bars, base;           // shared addresses of the group's barriers (kRingStages full, as many
+                                   // empty) and slots
+    __device__ __forceinline__ uint32_t full(int stage) const { return bars + 8 * stage; }
+    __device__ __forceinline__ uint32_t empty(int stage) const { return bars + 8 * (kRingStages + stage); }
+
+    __device__ __forceinline__ uint32_t at(uint32_t stage, int i) const { return base + (stage * r.ntens + i) * r.slot; }
+    // Byte of the row's slice in a tensor.
+    __device__ __forceinline__ long long byte(int row) const { return (static_cast<long long>(row) * r.hidden + c0) * ES; }
+
+    // One row's pieces of every tensor into a slot (one thread).
+    __device__ __forceinline__ void fetch(int row, uint32_t stage, uint64_t policy) const
+    {
+        const long long b0 = byte(row), a0 = b0 & ~15LL;
+        long long a1 = (b0 + static_cast<long long>(len) * ES + 15) & ~15LL;
+        if (a1 > (r.total & ~15LL)) a1 = r.total & ~15LL;
+        const uint32_t bytes = len > 0 && a1 > a0 ? static_cast<uint32_t>(a1 - a0) : 0u;
+        mbar_arrive_expect_tx(full(stage), bytes * r.ntens);
+        if (bytes > 0)
+            for (int i = 0; i < r.ntens; ++i)
+                bulk_load(at(stage, i), static_cast<const unsigned char*>(r.in[i]) + a0, bytes, full(stage), policy);
+    }
+
+    // Vector (element, where VEC is false) k of tensor i of the row in a slot, as raw bits.
+    __device__ __forceinline__ uint4 vec(uint32_t stage, int i, int k) const { return ld_shared_v4(at(stage, i) + k * ES); }
+    __device__ __forceinline__ T elem(uint32_t stage, int i, int row, int k) const
+    {
+        const long long b0 = byte(row);
+        if (b0 + static_cast<long long>(k) * ES >= (r.total & ~15LL)) return static_cast<const T*>(r.in[i])[b0 / ES + k];
+        const uint32_t a = at(stage, i) + static_cast<uint32_t>(b0 & 15) + k * ES;
+        T v;
+        if constexpr (ES == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+        else asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+        return v;
+    }
+    // One thread sets the barriers up: a slot is empty when `warps` warps have left it.
+    __device__ __forceinline__ void init(int warps) const
+    {
+        for (int i = 0; i < r.stages; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), warps);
+        }
+    }
+    // Brings the group's n rows, first + i * stride (one thread of the CTA's copying warp: issuing a row's
+    // copies takes about 1000 cycles, which a working warp would keep its group waiting for). After a
+    // wait that ran out, waits (bounded) for the copies in flight, so that they end before the CTA does.
+    __device__ __forceinline__ void feed(int first, int stride, int n, unsigned long long timeout_ns, unsigned int* err) const
+    {
+        const uint64_t policy = l2_evict_normal_policy();
+        const uint32_t limit = wait_limit(timeout_ns);
+        int stage = 0, phase = 1, i = 0;
+        for (; i < n; ++i) {
+            if (!mbar_wait<SCOPE_CTA>(empty(stage), phase, limit)) break;
+            fence_proxy_async_smem();
+            fetch(first + i * stride, stage, policy);
+            if (++stage == r.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        if (i < n) {
+            bool drained = true;
+            for (int j = i > r.stages ? i - r.stages : 0; j < i; ++j)
+                drained &= mbar_wait<SCOPE_CTA>(full(j % r.stages), (j / r.stages) & 1, wait_limit(4 * timeout_ns));
+            atomicOr(err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
+        }
+    }
+};
+
+
+// The threads of a row group (T a multiple of 32).
+__device__ __forceinline__ void group_sync(int group, int T)
+{
+    if (T == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(T) : "memory");
+}
+
+// A row's sums among the CTAs of a cluster: each writes its own into a slot of every CTA, which counts
+// the bytes on its own barrier. Two sets in turn: a CTA sends a row's sums after it has read those of
+// the row before, so nobody writes a set that is still read. No cluster barrier, which the copying
+// warp would have to join; every wait is bounded.
+struct ClusterSums {
+    uint32_t bars, slots;          // shared addresses: 2 barriers, [2][16] float4
+    int nc, rank;
+    static constexpr int BYTES = 16 + 2 * 16 * 16;
+
+    __device__ __forceinline__ void init() const
+    {
+        mbar_init(bars, 1);
+        mbar_init(bars + 8, 1);
+    }
+    // By the lanes of one warp.
+    __device__ __forceinline__ void send(int lane, int flip, float4 v) const
+    {
+        const uint32_t bar = bars + 8 * flip, slot = slots + (flip * 16 + rank) * 16;
+        if (lane == 0) mbar_arrive_expect_tx(bar, nc * 16);
+        if (lane < nc)
+            asm volatile(
+                "{\n\t.reg .b32 a, b;\n\tmapa.shared::cluster.u32 a, %0, %2;\n\tmapa.shared::cluster.u32 b, %1, %2;\n\t"
+                "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [a], {%3, %4, %5, %6}, [b];\n\t}"
+                ::"r"(slot), "r"(bar), "r"(lane), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+    }
+    // Lane r of every warp gets rank r's (zeros past the cluster); false: the wait ran out.
+    __device__ __forceinline__ bool receive(int lane, int flip, int phase, uint32_t limit_ns, float4& v) const
+    {
+        const bool ok = mbar_wait<SCOPE_CLUSTER>(bars + 8 * flip, phase, limit_ns);
+        v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane < nc) {
+            const uint4 w = ld_shared_v4(slots + (flip * 16 + lane) * 16);
+            v = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+        }
+        return ok;
+    }
+};
+
+// Elements of a row per thread: 8, 16 or 24, and the warps of a CTA that work on rows then (one more
+// copies). Registers are dealt to a quarter of the SM's warps each, so 16 warps of 16 elements and 12 of
+// 24 are what two CTAs forward and one backward leave enough of them for.
+constexpr int row_warps(int elems) { return elems <= 16 ? 15 : 11; }
+constexpr int kRowSlice = 8192;               // elements of a row per CTA at most (11 warps of 24)
+
+// Shared memory before gamma, beta and the ring: barriers, the groups' warp sums and maxima (each for
+// two rows in turn: one barrier a row then keeps a row's from the next but one's), the cluster's sums.
+constexpr int kNormHead = (kRingBars + 2 * 16 * 8 + 2 * 16 * 4 + 2 * ClusterSums::BYTES + 127) / 128 * 128;
+
 template <int DT, int E, bool VEC, int SCOPE, int KIND>
-__global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512)
-rmsq_norm_kernel(const NormParams p)
+__global__ void __launch_bounds__(32 * row_warps(E) + 32, 2) rmsq_norm_kernel(const __grid_constant__ NormParams p)
 {
     using D = Deal<DT, E, VEC>;
     using S = Scalar<DT>;
+    using TT = typename S::T;
     constexpr bool RMS = KIND == NORM_RMS_INT8;
     constexpr bool INT8 = KIND != NORM_LAYER;
     constexpr int VW = D::VW, NC = D::NC;
+    extern __shared__ __align__(128) unsigned char smem[];
 
-    __shared__ float2 part[16];
-    __shared__ float part_max[16];
-    __shared__ float4 xch[2];
+    float2* const part = reinterpret_cast<float2*>(smem + kRingBars);
+    float* const part_max = reinterpret_cast<float*>(part + 32);
+    unsigned char* const cluster_part = reinterpret_cast<unsigned char*>(part_max + 32);
 
+    const int T = SCOPE == SCOPE_WARP ? 32 : p.T;
+    const int group = SCOPE == SCOPE_CLUSTER ? 0 : threadIdx.x / T, groups = p.groups;
+    const int t = threadIdx.x - group * T;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int T = SCOPE == SCOPE_WARP ? 32 : blockDim.x;
-    const int t = SCOPE == SCOPE_WARP ? lane : threadIdx.x;
-    const int nwarps = blockDim.x >> 5;
-    long long row;
-    int c0 = 0, len = p.hidden;
-    if constexpr (SCOPE == SCOPE_WARP) {
-        row = static_cast<long long>(blockIdx.x) * nwarps + warp;
-    } else if constexpr (SCOPE == SCOPE_CTA) {
-        row = blockIdx.x;
-    } else {
-        row = cluster_id();
-        c0 = static_cast<int>(cluster_rank()) * p.slice;
-        len = p.hidden - c0;
-        len = len < 0 ? 0 : len < p.slice ? len : p.slice;
+    const int group_warps = T >> 5, warp0 = group * group_warps;
+    const int nc = SCOPE == SCOPE_CLUSTER ? static_cast<int>(cluster_size()) : 1;
+    const int rank = SCOPE == SCOPE_CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+
+    const int c0 = rank * p.r.slice, left = p.r.hidden - c0;
+    const int len = left < 0 ? 0 : left < p.r.slice ? left : p.r.slice;
+    // a warp's lanes of the copying warp stand for the groups they feed
+    const bool copies = threadIdx.x >= T * groups;
+    const int mine = copies ? (lane < groups ? lane : 0) : group;
+    const RowRing<DT, VEC> ring{p.r, c0, len, smem_u32(smem) + mine * 2 * kRingStages * 8,
+                                smem_u32(smem + kNormHead) + (2 + mine * p.r.stages * p.r.ntens) * p.r.slot};
+    const ClusterSums sums{smem_u32(cluster_part), smem_u32(cluster_part + 16), nc, rank};
+    const ClusterSums maxima{sums.bars + ClusterSums::BYTES, sums.slots + ClusterSums::BYTES, nc, rank};
+
+    // this group's rows: every groups-th of the CTA's rows_per_cta * groups
+    const int first = static_cast<int>(SCOPE == SCOPE_CLUSTER ? cluster_id() : blockIdx.x) * p.rows_per_group * groups + mine;
+    int n = first < p.r.rows ? (p.r.rows - first + groups - 1) / groups : 0;
+    if (n > p.rows_per_group) n = p.rows_per_group;
+    const bool has_res = p.r.ntens == 2;
+
+    if (copies && lane < groups) {
+        ring.init(group_warps);
+        if (SCOPE == SCOPE_CLUSTER) {
+            sums.init();
+            maxima.init();
+        }
+        fence_mbar_init();
+        fence_proxy_async_smem();
     }
+    __syncthreads();
+    if constexpr (SCOPE == SCOPE_CLUSTER) cluster_sync();        // the other CTAs' barriers are set up
     pdl_wait();
-    if (SCOPE == SCOPE_WARP && row >= p.rows) return;
+    if (copies) {
+        if (lane < groups) ring.feed(first, groups, n, p.timeout_ns, p.err);
+        return;
+    }
 
-    const long long base = row * p.hidden + c0;
-    const typename S::T* const x = static_cast<const typename S::T*>(p.x) + base;
-    float v[E];
-
-    // ---- s into registers, fp32 (exact) ----
+    // gamma and beta of the slice stay in shared memory, in their own type
+    TT* const ws = reinterpret_cast<TT*>(smem + kNormHead);
+    TT* const bs = reinterpret_cast<TT*>(smem + kNormHead + p.r.slot);
+    const int workers = T * groups;
     if constexpr (VEC) {
-        uint4 raw[NC];
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int k = D::col(c, t, T);
-            raw[c] = k < len ? ld_stream_v4(reinterpret_cast<const uint4*>(x + k)) : make_uint4(0, 0, 0, 0);
-        }
-        if (p.res != nullptr) {
-            const typename S::T* const r = static_cast<const typename S::T*>(p.res) + base;
-            typename S::T* const ro = static_cast<typename S::T*>(p.res_out) + base;
-            uint4 add[NC];
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int k = D::col(c, t, T);
-                add[c] = k < len ? ld_stream_v4(reinterpret_cast<const uint4*>(r + k)) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int k = D::col(c, t, T);
-                raw[c] = Elem<DT>::add(raw[c], add[c]);
-                if (k < len) st_v4(ro + k, raw[c]);
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float f[VW];
-            Elem<DT>::unpack(raw[c], f);
-#pragma unroll
-            for (int j = 0; j < VW; ++j) v[c * VW + j] = f[j];
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        for (int k = threadIdx.x * VW; k < len; k += workers * VW) {
+            st_shared_v4(smem_u32(ws + k), ld_v4(static_cast<const TT*>(p.gamma) + c0 + k));
+            st_shared_v4(smem_u32(bs + k), p.beta != nullptr ? ld_v4(static_cast<const TT*>(p.beta) + c0 + k) : zero);
         }
     } else {
-        typename S::T raw[E];
-#pragma unroll
-        for (int c = 0; c < E; ++c) {
-            const int k = D::col(c, t, T);
-            raw[c] = k < len ? x[k] : typename S::T(0);
+#pragma unroll 4
+        for (int k = threadIdx.x; k < len; k += workers) {
+            const TT w = static_cast<const TT*>(p.gamma)[c0 + k], b = p.beta != nullptr ? static_cast<const TT*>(p.beta)[c0 + k] : TT(0);
+            ws[k] = w;
+            bs[k] = b;
         }
-        if (p.res != nullptr) {
-            const typename S::T* const r = static_cast<const typename S::T*>(p.res) + base;
-            typename S::T* const ro = static_cast<typename S::T*>(p.res_out) + base;
-            typename S::T add[E];
-#pragma unroll
-            for (int c = 0; c < E; ++c) {
-                const int k = D::col(c, t, T);
-                add[c] = k < len ? r[k] : typename S::T(0);
-            }
-#pragma unroll
-            for (int c = 0; c < E; ++c) {
-                const int k = D::col(c, t, T);
-                raw[c] = S::add(raw[c], add[c]);
-                if (k < len) ro[k] = raw[c];
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < E; ++c) v[c] = S::get(raw[c]);
     }
+    asm volatile("bar.sync 15, %0;" ::"r"(workers) : "memory");
 
-    // ---- mean and squares about it ----
-    float sum = 0.f, m2 = 0.f;
-    const int n_w = D::count(SCOPE == SCOPE_WARP ? 0 : warp * 32, T, len);
-    float mean = 0.f;
-    if constexpr (!RMS) {
+    // Counts of elements and their reciprocals: this warp's, lane's warp's of the group, the CTA's, lane's
+    // CTA's of the cluster. A count that is not a power of two makes a mean off by half a step more.
+    const uint32_t limit = wait_limit(p.timeout_ns);
+    const auto inverse = [](int k) { return k > 0 ? 1.0f / static_cast<float>(k) : 0.f; };
+    const int n_w = D::count((warp - warp0) * 32, T, len);
+    const int n_l = lane < group_warps ? D::count(lane * 32, T, len) : 0;
+    const int n_r = SCOPE == SCOPE_CLUSTER && lane < nc ? min(max(p.r.hidden - lane * p.r.slice, 0), p.r.slice) : 0;
+    const bool full = n_w == 32 * E;
+    const float inv_w = inverse(n_w), inv_l = inverse(n_l), inv_c = inverse(len), inv_r = inverse(n_r);
+    const float inv_h = 1.0f / static_cast<float>(p.r.hidden), f_l = static_cast<float>(n_l), f_r = static_cast<float>(n_r);
+    const float2 offset = splat(p.offset);
+    bool dead = false;                            // a wait ran out: finish without waiting again
+    int stage = 0, phase = 0;
+    int flip = 0;
+    for (int i = 0; i < n; ++i) {
+        const int row = first + i * groups;
+        if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage), phase, limit)) dead = true;
+        const long long at = static_cast<long long>(row) * p.r.hidden + c0;
+
+        // ---- s into registers, fp32 (exact), 0 outside the slice ----
+        float2 v[E / 2];
+        if constexpr (VEC) {
 #pragma unroll
-        for (int j = 0; j < E; ++j) sum += v[j];
-        sum = warp_sum(sum);
-        mean = n_w > 0 ? sum / static_cast<float>(n_w) : 0.f;
-    }
-    if (n_w == 32 * E) {
-#pragma unroll
-        for (int j = 0; j < E; ++j) {
-            const float d = v[j] - mean;
-            m2 = fmaf(d, d, m2);
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < NC; ++c)
-            if (D::col(c, t, T) < len) {
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    const float d = v[c * VW + j] - mean;
-                    m2 = fmaf(d, d, m2);
+            for (int c = 0; c < NC; ++c) {
+                const int k = D::col(c, t, T);
+                uint4 raw = make_uint4(0, 0, 0, 0);
+                if (k < len) {
+                    raw = ring.vec(stage, 0, k);
+                    if (has_res) {
+                        raw = Elem<DT>::add(raw, ring.vec(stage, 1, k));
+                        st_v4(static_cast<TT*>(p.res_out) + at + k, raw);
+                    }
                 }
+                float2 f[VW / 2];
+                Elem<DT>::pairs(raw, f);
+#pragma unroll
+                for (int j = 0; j < VW / 2; ++j) v[c * (VW / 2) + j] = f[j];
             }
-    }
-    m2 = warp_sum(m2);
-    if constexpr (SCOPE != SCOPE_WARP) {
-        if (lane == 0) part[warp] = make_float2(sum, m2);
-        __syncthreads();
-        const float2 q = lane < nwarps ? part[lane] : make_float2(0.f, 0.f);
-        if constexpr (RMS) {
-            m2 = warp_sum(q.y);
         } else {
-            const float n_l = lane < nwarps ? static_cast<float>(D::count(lane * 32, T, len)) : 0.f;
-            sum = warp_sum(q.x);
-            mean = len > 0 ? sum / static_cast<float>(len) : 0.f;
-            const float d = n_l > 0.f ? q.x / n_l - mean : 0.f;
-            m2 = warp_sum(fmaf(n_l * d, d, q.y));
+#pragma unroll
+            for (int c = 0; c < E; ++c) {
+                const int k = D::col(c, t, T);
+                TT raw = TT(0);
+                if (k < len) {
+                    raw = ring.elem(stage, 0, row, k);
+                    if (has_res) {
+                        raw = S::add(raw, ring.elem(stage, 1, row, k));
+                        static_cast<TT*>(p.res_out)[at + k] = raw;
+                    }
+                }
+                if (c & 1) v[c / 2].y = S::get(raw);
+                else v[c / 2].x = S::get(raw);
+            }
         }
-    }
-    if constexpr (SCOPE == SCOPE_CLUSTER) {
-        if (threadIdx.x == 0) xch[0] = make_float4(sum, m2, static_cast<float>(len), 0.f);
-        cluster_sync();
-        const uint32_t nc = cluster_size();
-        const float4 q = lane < static_cast<int>(nc) ? ld_cluster_f4(smem_u32(&xch[0]), lane)
-                                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-        if constexpr (RMS) {
-            m2 = warp_sum(q.y);
-        } else {
-            sum = warp_sum(q.x);
-            mean = sum / static_cast<float>(p.hidden);
-            const float d = q.z > 0.f ? q.x / q.z - mean : 0.f;
-            m2 = warp_sum(fmaf(q.z * d, d, q.y));
-        }
-    }
-    const float rstd = 1.0f / sqrtf(m2 / static_cast<float>(p.hidden) + p.eps);
 
-    // ---- y ----
-    const typename S::T* const gamma = static_cast<const typename S::T*>(p.gamma) + c0;
-    const typename S::T* const beta = p.beta ? static_cast<const typename S::T*>(p.beta) + c0 : nullptr;
-    float amax = 0.f;
+        // ---- mean and squares about it ----
+        float sum = 0.f, m2, mean = 0.f;
+        if constexpr (!RMS) {
+            float2 a = v[0];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int k = D::col(c, t, T);
-        if (k < len) {
-            float w[VW], b[VW];
-            if constexpr (VEC) {
-                Elem<DT>::unpack(ld_v4(gamma + k), w);
-                if (beta) {
-                    Elem<DT>::unpack(ld_v4(beta + k), b);
-                } else {
+            for (int j = 1; j < E / 2; ++j) a = add2(a, v[j]);
+            sum = warp_sum(a.x + a.y);
+            mean = sum * inv_w;
+        }
+        {
+            const float2 m = splat(-mean);
+            float2 a = make_float2(0.f, 0.f);
+            if (full) {
 #pragma unroll
-                    for (int j = 0; j < VW; ++j) b[j] = 0.f;
+                for (int j = 0; j < E / 2; ++j) {
+                    const float2 d = add2(v[j], m);
+                    a = fma2(d, d, a);
                 }
             } else {
-                w[0] = S::get(gamma[k]);
-                b[0] = beta ? S::get(beta[k]) : 0.f;
-            }
 #pragma unroll
-            for (int j = 0; j < VW; ++j) {
-                float& y = v[c * VW + j];
-                y = fmaf((y - mean) * rstd, w[j] + p.offset, b[j]);
-                if constexpr (INT8) amax = fmaxf(amax, fabsf(y));
+                for (int j = 0; j < E / 2; ++j) {
+                    float2 d = add2(v[j], m);
+                    if (D::col(2 * j / VW, t, T) >= len) d.x = 0.f;
+                    if (D::col((2 * j + 1) / VW, t, T) >= len) d.y = 0.f;
+                    a = fma2(d, d, a);
+                }
             }
-            if constexpr (!INT8) {
-                typename S::T* const o = static_cast<typename S::T*>(p.out) + base;
-                if constexpr (VEC) st_v4(o + k, pack_vec<DT>(&v[c * VW]));
-                else o[k] = S::put(v[c]);
-            }
+            m2 = warp_sum(a.x + a.y);
         }
-    }
-    const bool leader = SCOPE == SCOPE_WARP ? lane == 0
-                                            : threadIdx.x == 0 && (SCOPE == SCOPE_CTA || cluster_rank() == 0);
-    if constexpr (INT8) {
-        amax = warp_max(amax);
+        if (lane == 0) mbar_arrive(ring.empty(stage));       // the warp has read the slot
         if constexpr (SCOPE != SCOPE_WARP) {
-            if (lane == 0) part_max[warp] = amax;
-            __syncthreads();
-            amax = warp_max(lane < nwarps ? part_max[lane] : 0.f);
+            if (lane == 0) part[flip * 16 + warp] = make_float2(sum, m2);
+            group_sync(group, T);
+            const float2 q = lane < group_warps ? part[flip * 16 + warp0 + lane] : make_float2(0.f, 0.f);
+            float d = 0.f;
+            if constexpr (!RMS) {
+                sum = warp_sum(q.x);
+                mean = sum * inv_c;
+                d = f_l > 0.f ? q.x * inv_l - mean : 0.f;
+            }
+            m2 = warp_sum(fmaf(f_l * d, d, q.y));
         }
         if constexpr (SCOPE == SCOPE_CLUSTER) {
-            if (threadIdx.x == 0) xch[1] = make_float4(amax, 0.f, 0.f, 0.f);
-            cluster_sync();
-            amax = warp_max(lane < static_cast<int>(cluster_size())
-                                ? ld_cluster_f4(smem_u32(&xch[1]), lane).x : 0.f);
+            float4 q;
+            if (warp == 0) sums.send(lane, flip, make_float4(sum, m2, 0.f, 0.f));
+            if (!sums.receive(lane, flip, (i >> 1) & 1, dead ? 0 : limit, q)) dead = true;
+            float d = 0.f;
+            if constexpr (!RMS) {
+                mean = warp_sum(q.x) * inv_h;
+                d = f_r > 0.f ? q.x * inv_r - mean : 0.f;
+            }
+            m2 = warp_sum(fmaf(f_r * d, d, q.y));
         }
-        // 127 / amax overflows for rows of tiny y: those are scaled up by 2^100 first (exact).
-        const float pre = amax < 1e-30f ? 0x1p100f : 1.0f;
-        const float inv = amax > 0.f ? 127.0f / (amax * pre) : 0.f;
-        signed char* const o = static_cast<signed char*>(p.out) + base;
+        const float rstd = __frsqrt_rn(m2 * inv_h + p.eps);
+
+        // ---- y ----
+        const float2 m = splat(-mean), r2 = splat(rstd);
+        if constexpr (VEC) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int k = D::col(c, t, T);
-            if (k < len) {
-                float f[VW];
+            for (int c = 0; c < NC; ++c) {
+                const int k = D::col(c, t, T);
+                if (k < len) {
+                    float2 w[VW / 2], b[VW / 2];
+                    Elem<DT>::pairs(ld_shared_v4(smem_u32(ws + k)), w);
+                    Elem<DT>::pairs(ld_shared_v4(smem_u32(bs + k)), b);
 #pragma unroll
-                for (int j = 0; j < VW; ++j) f[j] = v[c * VW + j] * pre * inv;
-                if constexpr (VW == 8)
-                    st_v2(o + k, pack_codes(f[0], f[1], f[2], f[3]), pack_codes(f[4], f[5], f[6], f[7]));
-                else if constexpr (VW == 4)
-                    st_u32(o + k, pack_codes(f[0], f[1], f[2], f[3]));
-                else
-                    o[k] = static_cast<signed char>(code_bits(f[0]) & 0xFFu);
+                    for (int j = 0; j < VW / 2; ++j) {
+                        float2& y = v[c * (VW / 2) + j];
+                        y = fma2(mul2(add2(y, m), r2), add2(w[j], offset), b[j]);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j) {
+                const int k0 = D::col(2 * j, t, T), k1 = D::col(2 * j + 1, t, T);
+                const float2 w = make_float2(k0 < len ? S::get(ws[k0]) : 0.f, k1 < len ? S::get(ws[k1]) : 0.f);
+                const float2 b = make_float2(k0 < len ? S::get(bs[k0]) : 0.f, k1 < len ? S::get(bs[k1]) : 0.f);
+                v[j] = fma2(mul2(add2(v[j], m), r2), add2(w, offset), b);
             }
         }
-        if (leader) p.scale[row] = amax / 127.0f;
-    } else if (leader) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
+        if constexpr (!INT8) {
+            TT* const o = static_cast<TT*>(p.out) + at;
+            if constexpr (VEC) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+                    if (D::col(c, t, T) < len) st_v4(o + D::col(c, t, T), pack_pairs<DT>(&v[c * (VW / 2)]));
+            } else {
+#pragma unroll
+                for (int c = 0; c < E; ++c)
+                    if (D::col(c, t, T) < len) o[D::col(c, t, T)] = S::put(c & 1 ? v[c / 2].y : v[c / 2].x);
+            }
+        }
+        const bool leader = t == 0 && rank == 0;
+        if constexpr (INT8) {
+            float amax = 0.f;
+            if (full) {
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j) amax = max3(amax, fabsf(v[j].x), fabsf(v[j].y));
+            } else {
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j) {
+                    if (D::col(2 * j / VW, t, T) < len) amax = fmaxf(amax, fabsf(v[j].x));
+                    if (D::col((2 * j + 1) / VW, t, T) < len) amax = fmaxf(amax, fabsf(v[j].y));
+                }
+            }
+            amax = warp_max(amax);
+            if constexpr (SCOPE != SCOPE_WARP) {
+                if (lane == 0) part_max[flip * 16 + warp] = amax;
+                group_sync(group, T);
+                amax = warp_max(lane < group_warps ? part_max[flip * 16 + warp0 + lane] : 0.f);
+            }
+            if constexpr (SCOPE == SCOPE_CLUSTER) {
+                float4 q;
+                if (warp == 0) maxima.send(lane, flip, make_float4(amax, 0.f, 0.f, 0.f));
+                if (!maxima.receive(lane, flip, (i >> 1) & 1, dead ? 0 : limit, q)) dead = true;
+                amax = warp_max(q.x);
+            }
+            // 127 / amax overflows for rows of tiny y: those are scaled up by 2^100 first (exact).
+            const float pre = amax < 1e-30f ? 0x1p100f : 1.0f;
+            const float2 pre2 = splat(pre), inv = splat(amax > 0.f ? 127.0f / (amax * pre) : 0.f);
+            signed char* const o = static_cast<signed char*>(p.out) + at;
+            if (pre != 1.0f) {
+#pragma unroll
+                for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], pre2);
+            }
+#pragma unroll
+            for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], inv);
+            if constexpr (VEC) {
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const int k = D::col(c, t, T);
+                    const float2* const f = &v[c * (VW / 2)];
+                    if (k < len) {
+                        if constexpr (VW == 8)
+                            st_v2(o + k, pack_codes(f[0].x, f[0].y, f[1].x, f[1].y), pack_codes(f[2].x, f[2].y, f[3].x, f[3].y));
+                        else
+                            st_u32(o + k, pack_codes(f[0].x, f[0].y, f[1].x, f[1].y));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < E; ++c)
+                    if (D::col(c, t, T) < len)
+                        o[D::col(c, t, T)] = static_cast<signed char>(code_bits(c & 1 ? v[c / 2].y : v[c / 2].x) & 0xFFu);
+            }
+            if (leader) p.scale[row] = amax / 127.0f;
+        } else if (leader) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+        flip ^= 1;
+        if (++stage == p.r.stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
     }
-    // a CTA's exchange slots are read by the others of its cluster: none leaves before all have
-    if constexpr (SCOPE == SCOPE_CLUSTER) cluster_sync();
+    if (dead && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
+    if constexpr (SCOPE == SCOPE_CLUSTER) cluster_sync();        // nobody sends to a CTA that has left
 }
 
 }  // namespace rmsq

@@ -4,13 +4,16 @@
 
 namespace rmsq {
 
+template <int DT, bool VEC> static const void* pick(int elems)
+{
+    return elems == 8 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 8, VEC>)
+         : elems == 16 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 16, VEC>)
+                       : reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 24, VEC>);
+}
+
 template <int DT> static const void* pick(int elems, bool vec)
 {
-    if (elems == 8)
-        return vec ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 8, true>)
-                   : reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 8, false>);
-    return vec ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 16, true>)
-               : reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 16, false>);
+    return vec ? pick<DT, true>(elems) : pick<DT, false>(elems);
 }
 
 const void* norm_bwd_fn(int dt, int elems, bool vec)

@@ -9,39 +9,29 @@
 // registers until the end, when each CTA (cluster) writes one partial row of both. A second kernel
 // adds the partials in a fixed order: no atomics, the same bits every time.
 //
-// The rows come through a ring of shared-memory slots filled by bulk copies (cp.async.bulk +
-// mbarrier), so loads of the next rows run while a row is reduced. A row is read from its slot
-// twice (sums, then ds) rather than held in registers, which the column sums need. Rows that do
-// not start on 16-byte boundaries are copied from the boundary below; the last bytes of the
-// tensors, which no whole 16-byte piece covers, are read directly.
+// The rows come through a ring of shared-memory slots (RowRing), so loads of the next rows run while a
+// row is reduced. A row is read from its slot twice (sums, then ds) rather than held in registers,
+// which the column sums need.
 //
-// A CTA holds several row groups of T threads when rows are short; rows too wide for 512 threads
-// of 16 elements are split over a cluster whose CTAs exchange the two row sums.
+// A CTA holds several row groups of T threads when rows are short; rows wider than 16 KB are split
+// over a cluster whose CTAs exchange the two row sums.
 #pragma once
 
 #include "rmsq_norm.cuh"
 
 namespace rmsq {
 
-constexpr int kBwdThreads = 512;
-constexpr int kBwdMaxStages = 8;
-
 struct NormBwdParams {
-    const void* in[3];       // dy, s, dres (or null)
+    RowTensors r;            // dy, s, and dres where there is one
     const void* gamma;
     const float* mean;
     const float* rstd;
     void* ds;
     float* part;             // [parts][2][hidden]
     unsigned int* err;
-    long long rows;
-    int hidden;
-    int slice;               // elements per CTA of a row
     float offset;
     int T;                   // threads per row group
     int groups;              // row groups per CTA
-    int stages;              // ring slots per group
-    int slot;                // bytes of one tensor's row in a slot (multiple of 16)
     unsigned long long timeout_ns;
 };
 
@@ -54,204 +44,198 @@ struct NormBwdReduceParams {
     int dt;                  // type of dgamma and dbeta
 };
 
-// Shared memory before the ring: mbarriers of every slot, the groups' warp sums (two rows in
-// turn), the cluster's exchange slots (two rows in turn).
-constexpr int kBwdHead = kBwdMaxStages * 16 * 8 + 2 * 16 * 8 + 2 * 16;
-
-__device__ __forceinline__ void group_sync(int group, int T)
-{
-    if (T == 32) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(T) : "memory");
-}
+// Shared memory before the ring: barriers, the groups' warp sums (of two iterations in turn), the
+// cluster's sums.
+constexpr int kBwdHead = (kRingBars + 2 * 16 * 16 + ClusterSums::BYTES + 127) / 128 * 128;
 
 template <int DT, int E, bool VEC>
-__global__ void __launch_bounds__(kBwdThreads) rmsq_norm_bwd_kernel(const NormBwdParams p)
+__global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
 {
     using D = Deal<DT, E, VEC>;
     using S = Scalar<DT>;
     using TT = typename S::T;
-    constexpr int VW = D::VW, NC = D::NC, ES = sizeof(TT);
+    constexpr int VW = D::VW, NC = D::NC;
     extern __shared__ __align__(128) unsigned char smem[];
 
-    uint64_t* const bars = reinterpret_cast<uint64_t*>(smem);
-    float2* const red = reinterpret_cast<float2*>(smem + kBwdMaxStages * 16 * 8);
-    float4* const xch = reinterpret_cast<float4*>(smem + kBwdMaxStages * 16 * 8 + 2 * 16 * 8);
-    unsigned char* const ring = smem + kBwdHead;
+    float4* const red = reinterpret_cast<float4*>(smem + kRingBars);
+    unsigned char* const cluster_part = reinterpret_cast<unsigned char*>(red + 32);
 
     const int T = p.T, group = threadIdx.x / T, t = threadIdx.x % T;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group_warps = T >> 5, warp0 = group * group_warps;
-    const uint32_t nc = cluster_size(), rank = cluster_rank();
-    const int c0 = static_cast<int>(rank) * p.slice;
-    int len = p.hidden - c0;
-    len = len < 0 ? 0 : len < p.slice ? len : p.slice;
-    const int ntens = p.in[2] != nullptr ? 3 : 2;
-    const uint32_t slot_bytes = static_cast<uint32_t>(p.slot) * ntens;
-    unsigned char* const my_ring = ring + static_cast<size_t>(group) * p.stages * slot_bytes;
-    const long long first = static_cast<long long>(cluster_id()) * p.groups + group;
-    const long long stride = static_cast<long long>(cluster_count()) * p.groups;
-    const long long total = p.rows * p.hidden * ES;      // bytes of a tensor
+    const int nc = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
 
-    if (t == 0)
-        for (int i = 0; i < p.stages; ++i) mbar_init(smem_u32(&bars[group * kBwdMaxStages + i]), 1);
-    fence_mbar_init();
-    __syncthreads();
-    pdl_wait();
+    const int c0 = rank * p.r.slice, left = p.r.hidden - c0;
+    const int len = left < 0 ? 0 : left < p.r.slice ? left : p.r.slice;
+    // a lane of the copying warp stands for the group it feeds
+    const bool copies = threadIdx.x >= T * p.groups;
+    const int mine = copies ? (lane < p.groups ? lane : 0) : group;
+    const RowRing<DT, VEC> ring{p.r, c0, len, smem_u32(smem) + mine * 2 * kRingStages * 8,
+                                smem_u32(smem + kBwdHead) + mine * p.r.stages * p.r.ntens * p.r.slot};
+    const ClusterSums sums{smem_u32(cluster_part), smem_u32(cluster_part + 16), nc, rank};
+    const bool has_res = p.r.ntens == 3;
 
-    // One row's pieces of every tensor into a slot (one thread per group).
-    const uint64_t policy = l2_evict_normal_policy();
-    auto fetch = [&](long long row, int slot) {
-        const long long b0 = (row * p.hidden + c0) * ES;
-        const long long a0 = b0 & ~15LL;
-        long long a1 = (b0 + static_cast<long long>(len) * ES + 15) & ~15LL;
-        if (a1 > (total & ~15LL)) a1 = total & ~15LL;
-        const uint32_t bytes = len > 0 && a1 > a0 ? static_cast<uint32_t>(a1 - a0) : 0u;
-        const uint32_t bar = smem_u32(&bars[group * kBwdMaxStages + slot]);
-        mbar_arrive_expect_tx(bar, bytes * ntens);
-        if (bytes > 0)
-            for (int i = 0; i < ntens; ++i)
-                bulk_load(smem_u32(my_ring + slot * slot_bytes + i * p.slot),
-                          static_cast<const unsigned char*>(p.in[i]) + a0, bytes, bar, policy);
-    };
+    const int first = static_cast<int>(cluster_id()) * p.groups + mine;
+    const int stride = static_cast<int>(cluster_count()) * p.groups;
+    const int n = first < p.r.rows ? (p.r.rows - first + stride - 1) / stride : 0;      // this group's rows
 
-    float acc_g[E], acc_b[E], w[E];
-    const TT* const gamma = static_cast<const TT*>(p.gamma) + c0;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int k = D::col(c, t, T);
-#pragma unroll
-        for (int j = 0; j < VW; ++j) {
-            acc_g[c * VW + j] = acc_b[c * VW + j] = 0.f;
-            w[c * VW + j] = k < len ? S::get(gamma[k + j]) + p.offset : 0.f;
-        }
+    if (copies && lane < p.groups) {
+        ring.init(group_warps);
+        sums.init();
+        fence_mbar_init();
+        fence_proxy_async_smem();
     }
+    __syncthreads();
+    if (nc > 1) cluster_sync();                   // the other CTAs' barriers are set up
+    pdl_wait();
+    if (copies) {
+        if (lane < p.groups) ring.feed(first, stride, n, p.timeout_ns, p.err);
+        return;
+    }
+    const int workers = T * p.groups;
 
-    long long issued = first;                     // next row to fetch (thread t == 0)
-    if (t == 0)
-        for (int i = 0; i < p.stages && issued < p.rows; ++i, issued += stride) fetch(issued, i);
+    float2 acc_g[E / 2], acc_b[E / 2];
+    Held<DT, E, VEC> w;                           // gamma, in its own type
+    w.load(static_cast<const TT*>(p.gamma) + c0, t, T, len);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) acc_g[e] = acc_b[e] = make_float2(0.f, 0.f);
 
-    const float inv_h = 1.0f / static_cast<float>(p.hidden);
+    const uint32_t limit = wait_limit(p.timeout_ns);
+    const float inv_h = 1.0f / static_cast<float>(p.r.hidden);
     bool dead = false;                            // a wait ran out: finish without waiting again
-    int slot = 0, phase = 0, flip = 0;
-    long long done = 0;                           // rows finished by this group
-    // every CTA of a cluster, and every thread of a group, runs the same iterations
-    for (long long row = first; row < p.rows; row += stride) {
-        const uint32_t bar = smem_u32(&bars[group * kBwdMaxStages + slot]);
-        const float mean = p.mean[row], rstd = p.rstd[row];
-        if (!dead && !mbar_wait<SCOPE_CTA>(bar, phase, wait_limit(p.timeout_ns))) dead = true;
-
-        const unsigned char* const sl = my_ring + slot * slot_bytes;
-        const long long b0 = (row * p.hidden + c0) * ES;
-        const int shift = VEC ? 0 : static_cast<int>(b0 & 15);
-        // elements of the slice that the copies brought (all but the tensor's last few)
-        const int have = VEC ? len : static_cast<int>(((total & ~15LL) - b0) / ES);
-        // vector / element k of tensor i
-        auto get = [&](int i, int k, float* f) {
-            const unsigned char* const a = sl + i * p.slot + shift + k * ES;
-            if constexpr (VEC) {
-                Elem<DT>::unpack(ld_shared_v4(smem_u32(a)), *reinterpret_cast<float(*)[VW]>(f));
-            } else {
-                f[0] = S::get(k < have ? *reinterpret_cast<const TT*>(a)
-                                       : static_cast<const TT*>(p.in[i])[row * p.hidden + c0 + k]);
-            }
-        };
-
-        float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
+    int stage = 0, phase = 0;
+    int flip = 0;
+    // Elements 2 j and 2 j + 1 of the thread's share of tensor i, or all of its vector c (0 outside the slice).
+    auto load = [&](int slot, int i, int row, int c, float2* f) {
+        if constexpr (VEC) {
             const int k = D::col(c, t, T);
-            if (k < len) {
-                float dy[VW], s[VW];
-                get(0, k, dy);
-                get(1, k, s);
+            float2 g[VW / 2];
+            Elem<DT>::pairs(k < len ? ring.vec(slot, i, k) : make_uint4(0, 0, 0, 0), g);
 #pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    const int e = c * VW + j;
-                    const float xh = (s[j] - mean) * rstd, g = dy[j] * w[e];
-                    s1 += g;
-                    s2 = fmaf(g, xh, s2);
-                    acc_g[e] = fmaf(dy[j], xh, acc_g[e]);
-                    acc_b[e] += dy[j];
+            for (int j = 0; j < VW / 2; ++j) f[j] = g[j];
+        } else {
+            const int k0 = D::col(2 * c, t, T), k1 = D::col(2 * c + 1, t, T);
+            f[0].x = k0 < len ? S::get(ring.elem(slot, i, row, k0)) : 0.f;
+            f[0].y = k1 < len ? S::get(ring.elem(slot, i, row, k1)) : 0.f;
+        }
+    };
+    constexpr int PAIRS = VEC ? VW / 2 : 1, CHUNKS = E / 2 / PAIRS;
+    const float2 offset = splat(p.offset);
+    // Two rows at a time, so that one barrier and one round of shuffles serve both. Every CTA of a
+    // cluster, and every thread of a group, runs the same iterations.
+    for (int i = 0; i < n; i += 2) {
+        const int pair = n - i < 2 ? 1 : 2;
+        w.pin();
+        float mean[2], rstd[2], s1[2] = {0.f, 0.f}, s2[2] = {0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = first + (i + (r < pair ? r : 0)) * stride;
+            mean[r] = p.mean[row];
+            rstd[r] = p.rstd[row];
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if (r < pair) {
+                const int row = first + (i + r) * stride;
+                if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage + r), phase, limit)) dead = true;
+                const float2 m = splat(-mean[r]), rs = splat(rstd[r]);
+                float2 a1 = make_float2(0.f, 0.f), a2 = a1;
+#pragma unroll
+                for (int c = 0; c < CHUNKS; ++c) {
+                    float2 dy[PAIRS], s[PAIRS];
+                    load(stage + r, 0, row, c, dy);
+                    load(stage + r, 1, row, c, s);
+#pragma unroll
+                    for (int j = 0; j < PAIRS; ++j) {
+                        const int e = c * PAIRS + j;
+                        const float2 xh = mul2(add2(s[j], m), rs), g = mul2(dy[j], add2(w.pair(e), offset));
+                        a1 = add2(a1, g);
+                        a2 = fma2(g, xh, a2);
+                        acc_g[e] = fma2(dy[j], xh, acc_g[e]);
+                        acc_b[e] = add2(acc_b[e], dy[j]);
+                    }
                 }
+                s1[r] = a1.x + a1.y;
+                s2[r] = a2.x + a2.y;
             }
         }
-        s1 = warp_sum(s1);
-        s2 = warp_sum(s2);
-        if (T > 32) {
-            if (lane == 0) red[flip * 16 + warp] = make_float2(s1, s2);
-            group_sync(group, T);
-            const float2 q = lane < group_warps ? red[flip * 16 + warp0 + lane] : make_float2(0.f, 0.f);
-            s1 = warp_sum(q.x);
-            s2 = warp_sum(q.y);
-        } else {
-            __syncwarp();
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            s1[r] = warp_sum(s1[r]);
+            s2[r] = warp_sum(s2[r]);
         }
-        // the group has left the previous row's slot: refill it
-        if (t == 0 && done > 0 && issued < p.rows && !dead) {
-            fence_proxy_async_smem();
-            fetch(issued, slot == 0 ? p.stages - 1 : slot - 1);
-            issued += stride;
+        if (T > 32) {
+            if (lane == 0) red[flip * 16 + warp] = make_float4(s1[0], s2[0], s1[1], s2[1]);
+            group_sync(group, T);
+            const float4 q = lane < group_warps ? red[flip * 16 + warp0 + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+            s1[0] = warp_sum(q.x);
+            s2[0] = warp_sum(q.y);
+            s1[1] = warp_sum(q.z);
+            s2[1] = warp_sum(q.w);
         }
         if (nc > 1) {
-            if (threadIdx.x == 0) xch[flip] = make_float4(s1, s2, 0.f, 0.f);
-            cluster_sync();
-            const float4 q = lane < static_cast<int>(nc) ? ld_cluster_f4(smem_u32(&xch[flip]), lane)
-                                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-            s1 = warp_sum(q.x);
-            s2 = warp_sum(q.y);
+            float4 q;
+            if (warp == 0) sums.send(lane, flip, make_float4(s1[0], s2[0], s1[1], s2[1]));
+            if (!sums.receive(lane, flip, (i >> 2) & 1, dead ? 0 : limit, q)) dead = true;
+            s1[0] = warp_sum(q.x);
+            s2[0] = warp_sum(q.y);
+            s1[1] = warp_sum(q.z);
+            s2[1] = warp_sum(q.w);
         }
-        s1 *= inv_h;
-        s2 *= inv_h;
-
-        TT* const out = static_cast<TT*>(p.ds) + row * p.hidden + c0;
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int k = D::col(c, t, T);
-            if (k < len) {
-                float dy[VW], s[VW], d[VW];
-                get(0, k, dy);
-                get(1, k, s);
-                if (ntens == 3) {
-                    get(2, k, d);
-                } else {
+        for (int r = 0; r < 2; ++r) {
+            if (r < pair) {
+                const int row = first + (i + r) * stride;
+                const float m1 = s1[r] * inv_h, m2 = s2[r] * inv_h;
+                TT* const out = static_cast<TT*>(p.ds) + static_cast<long long>(row) * p.r.hidden + c0;
+                const float2 m = splat(-mean[r]), rs = splat(rstd[r]), n1 = splat(-m1), n2 = splat(-m2);
 #pragma unroll
-                    for (int j = 0; j < VW; ++j) d[j] = 0.f;
+                for (int c = 0; c < CHUNKS; ++c) {
+                    float2 dy[PAIRS], s[PAIRS], d[PAIRS];
+                    load(stage + r, 0, row, c, dy);
+                    load(stage + r, 1, row, c, s);
+                    if (has_res) {
+                        load(stage + r, 2, row, c, d);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < PAIRS; ++j) d[j] = make_float2(0.f, 0.f);
+                    }
+#pragma unroll
+                    for (int j = 0; j < PAIRS; ++j) {
+                        const float2 xh = mul2(add2(s[j], m), rs), g = mul2(dy[j], add2(w.pair(c * PAIRS + j), offset));
+                        d[j] = fma2(rs, fma2(xh, n2, add2(g, n1)), d[j]);
+                    }
+                    if constexpr (VEC) {
+                        const int k = D::col(c, t, T);
+                        if (k < len) st_v4(out + k, pack_pairs<DT>(d));
+                    } else {
+                        const int k0 = D::col(2 * c, t, T), k1 = D::col(2 * c + 1, t, T);
+                        if (k0 < len) out[k0] = S::put(d[0].x);
+                        if (k1 < len) out[k1] = S::put(d[0].y);
+                    }
                 }
-#pragma unroll
-                for (int j = 0; j < VW; ++j) {
-                    const float xh = (s[j] - mean) * rstd, g = dy[j] * w[c * VW + j];
-                    d[j] = fmaf(rstd, fmaf(-xh, s2, g - s1), d[j]);
-                }
-                if constexpr (VEC) st_v4(out + k, pack_vec<DT>(d));
-                else out[k] = S::put(d[0]);
             }
         }
+        __syncwarp();
+        if (lane == 0) {                          // the warp has read the slots
+            mbar_arrive(ring.empty(stage));
+            if (pair == 2) mbar_arrive(ring.empty(stage + 1));
+        }
         flip ^= 1;
-        ++done;
-        if (++slot == p.stages) {
-            slot = 0;
-            phase ^= 1;
+        stage += 2;
+        if (stage == p.r.stages) {
+            stage = 0;
+            phase ^= 1u;
         }
     }
 
-    if (dead) {
-        if (lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
-        // the copies in flight end before the CTA does
-        if (t == 0) {
-            bool drained = true;
-            long long k = 0;
-            for (long long r = first; r < issued; r += stride, ++k)
-                if (issued - r <= stride * p.stages)
-                    drained &= mbar_wait<SCOPE_CTA>(
-                        smem_u32(&bars[group * kBwdMaxStages + static_cast<int>(k % p.stages)]),
-                        static_cast<uint32_t>(k / p.stages) & 1u, wait_limit(4 * p.timeout_ns));
-            if (!drained) atomicOr(p.err, ERRF_DRAIN_TIMEOUT);
-        }
-    }
+    if (dead && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
 
+    const auto workers_sync = [&]() { asm volatile("bar.sync 15, %0;" ::"r"(workers) : "memory"); };
+    const auto acc = [](const float2* a, int e) { return e & 1 ? a[e / 2].y : a[e / 2].x; };
     // ---- partial rows: the groups' sums in group order, through the ring's memory ----
-    __syncthreads();
-    float* const part = p.part + static_cast<long long>(cluster_id()) * 2 * p.hidden + c0;
+    workers_sync();
+    float* const part = p.part + static_cast<long long>(cluster_id()) * 2 * p.r.hidden + c0;
     if (p.groups == 1) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
@@ -259,12 +243,12 @@ __global__ void __launch_bounds__(kBwdThreads) rmsq_norm_bwd_kernel(const NormBw
 #pragma unroll
             for (int j = 0; j < VW; ++j)
                 if (k < len) {
-                    part[k + j] = acc_g[c * VW + j];
-                    part[p.hidden + k + j] = acc_b[c * VW + j];
+                    part[k + j] = acc(acc_g, c * VW + j);
+                    part[p.r.hidden + k + j] = acc(acc_b, c * VW + j);
                 }
         }
     } else {
-        float* const sum = reinterpret_cast<float*>(ring);
+        float* const sum = reinterpret_cast<float*>(smem + kBwdHead);
         for (int g = 0; g < p.groups; ++g) {
             if (g == group) {
 #pragma unroll
@@ -275,19 +259,19 @@ __global__ void __launch_bounds__(kBwdThreads) rmsq_norm_bwd_kernel(const NormBw
                         if (k < len) {
                             float& a = sum[k + j];
                             float& b = sum[len + k + j];
-                            a = (g == 0 ? 0.f : a) + acc_g[c * VW + j];
-                            b = (g == 0 ? 0.f : b) + acc_b[c * VW + j];
+                            a = (g == 0 ? 0.f : a) + acc(acc_g, c * VW + j);
+                            b = (g == 0 ? 0.f : b) + acc(acc_b, c * VW + j);
                         }
                 }
             }
-            __syncthreads();
+            workers_sync();
         }
-        for (int k = threadIdx.x; k < len; k += blockDim.x) {
+        for (int k = threadIdx.x; k < len; k += workers) {
             part[k] = sum[k];
-            part[p.hidden + k] = sum[len + k];
+            part[p.r.hidden + k] = sum[len + k];
         }
     }
-    if (nc > 1) cluster_sync();   // exchange slots are read by the other CTAs until here
+    if (nc > 1) cluster_sync();                   // nobody sends to a CTA that has left
 }
 
 // dgamma and dbeta from the partial rows: 32 columns per CTA, 16 threads share a column's partials

@@ -27,10 +27,11 @@ cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem,
 
 struct NormPlan {
     int dt;
-    int elems;      // per thread: 8, 16 or 32
+    int elems;      // per thread: 8, 16 or 24
     bool vec;
-    int scope;
+    int scope;      // SCOPE_*
     int threads;
+    int smem;
     unsigned grid;
     int cluster;
 };
@@ -39,40 +40,43 @@ cudaError_t norm_layer(const NormPlan& pl, const NormParams& p, cudaStream_t str
 cudaError_t norm_layer_int8(const NormPlan& pl, const NormParams& p, cudaStream_t stream);
 cudaError_t norm_rms_int8(const NormPlan& pl, const NormParams& p, cudaStream_t stream);
 
-// Backward pass (rmsq_norm_bwd.cu): the row kernel for a type, elements per thread (8 or 16) and
+// Backward pass (rmsq_norm_bwd.cu): the row kernel for a type, elements per thread (8, 16 or 24) and
 // alignment, and the column reduction.
 struct NormBwdParams;
 const void* norm_bwd_fn(int dt, int elems, bool vec);
 const void* norm_bwd_reduce_fn();
 
 #define RMSQ_DEFINE_NORM_DISPATCH(NAME, KIND)                                                     \
-    template <int DT, bool VEC> static const void* NAME##_fn(const NormPlan& pl)                  \
+    template <int DT, bool VEC> static const void* NAME##_scope(const NormPlan& pl)               \
     {                                                                                             \
         switch (pl.scope * 64 + pl.elems) {                                                       \
         case SCOPE_WARP * 64 + 8:                                                                 \
             return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 8, VEC, SCOPE_WARP, KIND>); \
         case SCOPE_WARP * 64 + 16:                                                                \
             return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 16, VEC, SCOPE_WARP, KIND>); \
-        case SCOPE_WARP * 64 + 32:                                                                \
-            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 32, VEC, SCOPE_WARP, KIND>); \
         case SCOPE_CTA * 64 + 16:                                                                 \
             return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 16, VEC, SCOPE_CTA, KIND>); \
-        case SCOPE_CTA * 64 + 32:                                                                 \
-            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 32, VEC, SCOPE_CTA, KIND>); \
-        case SCOPE_CLUSTER * 64 + 32:                                                             \
-            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 32, VEC, SCOPE_CLUSTER, KIND>); \
+        case SCOPE_CTA * 64 + 24:                                                                 \
+            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 24, VEC, SCOPE_CTA, KIND>); \
+        case SCOPE_CLUSTER * 64 + 16:                                                             \
+            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 16, VEC, SCOPE_CLUSTER, KIND>); \
+        case SCOPE_CLUSTER * 64 + 24:                                                             \
+            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 24, VEC, SCOPE_CLUSTER, KIND>); \
         }                                                                                         \
         return nullptr;                                                                           \
     }                                                                                             \
+    template <int DT> static const void* NAME##_fn(const NormPlan& pl)                            \
+    {                                                                                             \
+        return pl.vec ? NAME##_scope<DT, true>(pl) : NAME##_scope<DT, false>(pl);                 \
+    }                                                                                             \
     cudaError_t NAME(const NormPlan& pl, const NormParams& p, cudaStream_t stream)                \
     {                                                                                             \
-        const void* fn = pl.dt == DT_BF16 ? (pl.vec ? NAME##_fn<DT_BF16, true>(pl) : NAME##_fn<DT_BF16, false>(pl)) \
-                       : pl.dt == DT_FP16 ? (pl.vec ? NAME##_fn<DT_FP16, true>(pl) : NAME##_fn<DT_FP16, false>(pl)) \
-                                          : (pl.vec ? NAME##_fn<DT_F32, true>(pl) : NAME##_fn<DT_F32, false>(pl)); \
+        const void* fn = pl.dt == DT_BF16 ? NAME##_fn<DT_BF16>(pl)                                \
+                       : pl.dt == DT_FP16 ? NAME##_fn<DT_FP16>(pl) : NAME##_fn<DT_F32>(pl);       \
         if (fn == nullptr) return cudaErrorInvalidConfiguration;                                  \
         NormParams q = p;                                                                         \
         void* args[] = {&q};                                                                      \
-        return launch_kernel(fn, pl.grid, pl.threads, 0, pl.cluster, stream, args);               \
+        return launch_kernel(fn, pl.grid, pl.threads, pl.smem, pl.cluster, stream, args);         \
     }
 
 }  // namespace rmsq

@@ -3,6 +3,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "rmsq_norm_bwd.cuh"
 #include "rmsq_ops.h"
@@ -30,42 +31,74 @@ static rmsq_status status_of(cudaError_t e)
     return RMSQ_ERR_LAUNCH;
 }
 
-// Elements of a row that one CTA takes: 512 threads of 32 elements forward, of 16 backward (whose
-// threads also hold two column sums per element). Wider rows are split evenly over the smallest
-// cluster of 2, 4, 8 or 16 CTAs, in whole vectors where the row has them.
-static int cluster_slice(int hidden, int most, int vec, int* cluster)
+// How rows are dealt out: wide rows are split evenly over the smallest cluster of 2, 4, 8 or 16 CTAs
+// whose slices hold at most `most` elements, in whole vectors where the row has them; a slice takes
+// T threads of `elems` elements; short rows leave a CTA room for several row groups, of which it
+// takes no more than give every SM a row.
+struct RowGeometry {
+    int cluster, slice, elems, T, groups, slot;
+    bool vec;
+};
+
+static RowGeometry row_geometry(int64_t rows, int hidden, int dtype, int most, int sms)
 {
-    int c = 1;
-    while (static_cast<long long>(c) * most < hidden) c *= 2;
-    *cluster = c;
-    const int slice = (hidden + c - 1) / c;
-    return (slice + vec - 1) / vec * vec;
+    const int es = elem_bytes(dtype), per16 = 16 / es;
+    RowGeometry g;
+    g.vec = hidden % per16 == 0;
+    g.cluster = 1;
+    while (static_cast<long long>(g.cluster) * most < hidden) g.cluster *= 2;
+    const int vec = g.vec ? per16 : 1;
+    g.slice = ((hidden + g.cluster - 1) / g.cluster + vec - 1) / vec * vec;
+    g.elems = g.slice <= 256 ? 8 : g.slice <= row_warps(16) * 32 * 16 ? 16 : 24;
+    g.T = ((g.slice + g.elems - 1) / g.elems + 31) / 32 * 32;
+    g.groups = g.cluster > 1 ? 1 : row_warps(g.elems) * 32 / g.T;
+    const int64_t spread = (rows + sms - 1) / sms;
+    if (g.groups > spread) g.groups = static_cast<int>(spread);
+    // rows off 16-byte boundaries are copied from the boundary below
+    g.slot = g.vec ? g.slice * es : (g.slice * es + 30) / 16 * 16;
+    return g;
 }
 
-// A warp per row up to 1024 elements (no block barrier), a CTA per row up to 16384, a cluster
-// beyond. CTAs take 16 elements per thread up to 8192 elements, then 32.
+// Launch of a forward norm (rmsq_norm_kernel).
 static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormParams&, cudaStream_t),
-                               NormParams& p, int64_t rows, int dtype, cudaStream_t stream)
+                               NormParams& p, int64_t rows, int dtype, const DeviceView& dv, cudaStream_t stream)
 {
-    const int per16 = 16 / elem_bytes(dtype);
+    const RowGeometry g = row_geometry(rows, p.r.hidden, dtype, kRowSlice, dv.sms);
     NormPlan pl;
     pl.dt = dtype;
-    pl.vec = p.hidden % per16 == 0;
-    pl.cluster = 1;
-    p.rows = rows;
-    p.slice = p.hidden;
-    if (p.hidden <= 1024) {
-        pl.scope = SCOPE_WARP;
-        pl.elems = p.hidden <= 256 ? 8 : p.hidden <= 512 ? 16 : 32;
-        pl.threads = 256;
-        pl.grid = static_cast<unsigned>((rows + 7) / 8);
-    } else {
-        p.slice = cluster_slice(p.hidden, 512 * 32, pl.vec ? per16 : 1, &pl.cluster);
-        pl.scope = pl.cluster > 1 ? SCOPE_CLUSTER : SCOPE_CTA;
-        pl.elems = p.slice > 512 * 16 || pl.cluster > 1 ? 32 : 16;
-        pl.threads = ((p.slice + pl.elems - 1) / pl.elems + 31) / 32 * 32;
-        pl.grid = static_cast<unsigned>(rows * pl.cluster);
-    }
+    pl.vec = g.vec;
+    pl.cluster = g.cluster;
+    pl.elems = g.elems;
+    pl.scope = g.cluster > 1 ? SCOPE_CLUSTER : g.T > 32 ? SCOPE_CTA : SCOPE_WARP;
+    pl.threads = g.T * g.groups + 32;
+    p.r.rows = static_cast<int>(rows);
+    p.r.total = rows * p.r.hidden * elem_bytes(dtype);
+    p.r.slice = g.slice;
+    p.r.slot = g.slot;
+    p.T = g.T;
+    p.groups = g.groups;
+    p.err = dv.err;
+    p.timeout_ns = dv.timeout_ns;
+    // CTAs per SM: what the registers hold (32 warps of up to 16 elements a thread, 24 of more), or as
+    // many as leave each two slots a group
+    const int64_t stage = static_cast<int64_t>(g.slot) * p.r.ntens * g.groups, head = kNormHead + 2 * g.slot;
+    const auto slots = [&](int ctas) { return (dv.smem_optin / ctas - 1024 - head) / stage; };
+    static const int env_r = getenv("RMSQ_R") ? atoi(getenv("RMSQ_R")) : 0, env_s = getenv("RMSQ_S") ? atoi(getenv("RMSQ_S")) : 0, env_c = getenv("RMSQ_C") ? atoi(getenv("RMSQ_C")) : 0;
+    int ctas = env_c ? env_c : (g.elems <= 16 ? 32 : 24) * 32 / pl.threads;
+    while (ctas > 1 && slots(ctas) < 2) --ctas;
+    int64_t stages = slots(ctas);
+    if (stages < 1) return RMSQ_ERR_LAUNCH;
+    if (stages > kRingStages) stages = kRingStages;
+    if (env_s) stages = env_s;
+    // rows per group: about four CTAs in turn on every place an SM has for one
+    const int64_t places = static_cast<int64_t>(dv.sms) * ctas / pl.cluster * p.groups;
+    int64_t per = env_r ? env_r : rows / (places * 4);
+    p.rows_per_group = static_cast<int>(per < 1 ? 1 : per > 64 ? 64 : per);
+    if (stages > p.rows_per_group) stages = p.rows_per_group;
+    p.r.stages = static_cast<int>(stages);
+    pl.smem = static_cast<int>(head + stages * stage);
+    const int64_t per_cta = static_cast<int64_t>(p.rows_per_group) * p.groups;
+    pl.grid = static_cast<unsigned>((rows + per_cta - 1) / per_cta * pl.cluster);
     return status_of(go(pl, p, stream));
 }
 
@@ -96,13 +129,14 @@ static NormParams norm_params(const void* input, const void* residual, void* res
                               float weight_offset, void* output)
 {
     NormParams p = {};
-    p.x = input;
-    p.res = residual;
+    p.r.in[0] = input;
+    p.r.in[1] = residual;
+    p.r.ntens = residual != nullptr ? 2 : 1;
     p.res_out = residual_output;
     p.gamma = gamma;
     p.beta = beta;
     p.out = output;
-    p.hidden = static_cast<int>(hidden);
+    p.r.hidden = static_cast<int>(hidden);
     p.eps = epsilon;
     p.offset = weight_offset;
     return p;
@@ -125,7 +159,7 @@ static rmsq_status norm_int8(cudaError_t (*go)(const NormPlan&, const NormParams
     NormParams p = norm_params(input, residual, residual_output, gamma, beta, hidden, epsilon,
                                weight_offset, output);
     p.scale = scale_output;
-    return launch_norm(go, p, rows, dtype, static_cast<cudaStream_t>(stream));
+    return launch_norm(go, p, rows, dtype, dv, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace rmsq
@@ -148,7 +182,7 @@ extern "C" rmsq_status layernorm(const void* input, const void* residual, void* 
                                weight_offset, output);
     p.mean = mean;
     p.rstd = rstd;
-    return launch_norm(&norm_layer, p, rows, dtype, static_cast<cudaStream_t>(stream));
+    return launch_norm(&norm_layer, p, rows, dtype, dv, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" rmsq_status layernorm_quant_int8(const void* input, const void* residual,
@@ -218,38 +252,40 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
 
     if (rows > 0) {
         NormBwdParams p = {};
-        p.in[0] = grad_output;
-        p.in[1] = input;
-        p.in[2] = grad_residual;
+        p.r.in[0] = grad_output;
+        p.r.in[1] = input;
+        p.r.in[2] = grad_residual;
         p.gamma = gamma;
         p.mean = mean;
         p.rstd = rstd;
         p.ds = grad_input;
         p.part = static_cast<float*>(workspace);
         p.err = dv.err;
-        p.rows = rows;
-        p.hidden = static_cast<int>(hidden);
+        p.r.ntens = grad_residual != nullptr ? 3 : 2;
+        p.r.rows = static_cast<int>(rows);
+        p.r.hidden = static_cast<int>(hidden);
+        p.r.total = rows * hidden * elem_bytes(dtype);
         p.offset = weight_offset;
         p.timeout_ns = dv.timeout_ns;
 
-        const int es = elem_bytes(dtype), per16 = 16 / es;
-        const bool vec = hidden % per16 == 0;
-        int cluster = 1;
-        p.slice = cluster_slice(p.hidden, kBwdThreads * 16, vec ? per16 : 1, &cluster);
-        const int elems = p.slice <= 256 ? 8 : 16;
-        p.T = ((p.slice + elems - 1) / elems + 31) / 32 * 32;
-        // Row groups: as many as 512 threads hold, but no more than it takes to give every CTA
-        // of the device a row.
-        p.groups = cluster > 1 ? 1 : kBwdThreads / p.T;
-        const int64_t spread = (rows + dv.sms - 1) / dv.sms;
-        if (p.groups > spread) p.groups = static_cast<int>(spread);
-        p.slot = vec ? p.slice * es : (p.slice * es + 30) / 16 * 16;
-        const int64_t stage = static_cast<int64_t>(p.slot) * (grad_residual ? 3 : 2) * p.groups;
-        int64_t stages = (dv.smem_optin - kBwdHead) / stage;
-        if (stages < 1) return RMSQ_ERR_LAUNCH;
-        p.stages = static_cast<int>(stages > kBwdMaxStages ? kBwdMaxStages : stages);
-        int64_t ring = p.stages * stage;
-        if (p.groups > 1 && ring < 8LL * p.slice) ring = 8LL * p.slice;   // the groups' sums
+        // slices of at most 16 KB: the ring then holds at least four rows of three tensors
+        RowGeometry g = row_geometry(rows, p.r.hidden, dtype, 16384 / elem_bytes(dtype), dv.sms);
+        p.r.slice = g.slice;
+        p.r.slot = g.slot;
+        p.T = g.T;
+        p.groups = g.groups;
+        const int cluster = g.cluster;
+        // at least two pairs of rows in the ring: one is refilled while the other is worked on
+        auto slots = [&]() {
+            return (dv.smem_optin - kBwdHead) / (static_cast<int64_t>(p.r.slot) * p.r.ntens * p.groups);
+        };
+        while (p.groups > 1 && slots() < 4) --p.groups;
+        const int64_t stages = slots();
+        if (stages < 4) return RMSQ_ERR_LAUNCH;
+        p.r.stages = static_cast<int>(stages > kRingStages ? kRingStages : stages) & ~1;
+        const int64_t stage = static_cast<int64_t>(p.r.slot) * p.r.ntens * p.groups;
+        int64_t ring = p.r.stages * stage;
+        if (p.groups > 1 && ring < 8LL * p.r.slice) ring = 8LL * p.r.slice;   // the groups' sums
         int64_t parts = (rows + p.groups - 1) / p.groups;
         const int64_t resident = dv.sms / cluster;
         if (parts > resident) parts = resident;
@@ -258,8 +294,8 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         r.parts = static_cast<int>(parts);
         void* args[] = {&p};
         const rmsq_status e = status_of(launch_kernel(
-            norm_bwd_fn(dtype, elems, vec), static_cast<unsigned>(parts * cluster),
-            static_cast<unsigned>(p.T * p.groups), static_cast<int>(kBwdHead + ring), cluster, st, args));
+            norm_bwd_fn(dtype, g.elems, g.vec), static_cast<unsigned>(parts * cluster),
+            static_cast<unsigned>(p.T * p.groups + 32), static_cast<int>(kBwdHead + ring), cluster, st, args));
         if (e != RMSQ_OK) return e;
     }
     void* args[] = {&r};

@@ -279,6 +279,23 @@ def test_backward_rows(rows, hidden):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hidden", [1000, 1003, 4096, 8192])
+@pytest.mark.parametrize("residual", [False, True])
+def test_backward_many_rows(dtype, hidden, residual):
+    # every slot of the ring is refilled several times
+    check_backward(make_backward(5003, hidden, dtype, hidden, residual=residual))
+
+
+@gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("hidden", [1000, 1003, 4096, 8192, 16384])
+@pytest.mark.parametrize("residual", [False, True])
+def test_forward_many_rows(dtype, hidden, residual):
+    check_forward(make(20011 if hidden < 8000 else 5003, hidden, dtype, hidden, residual=residual))
+
+
+@gpu
 def test_backward_in_place_and_repeatable():
     for hidden in (1000, 1003, 4096, 9001):
         d = make_backward(400, hidden, torch.bfloat16, 6, residual=True)
