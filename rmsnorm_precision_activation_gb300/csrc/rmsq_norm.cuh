@@ -288,6 +288,187 @@ __device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float 
     return __byte_perm(lo, hi, 0x5410);
 }
 
+// A thread's share of a row (in whole vectors) as int8 codes of y * 127 / amax. 127 / amax overflows for
+// rows of tiny y: those are scaled up by 2^100 first (exact).
+template <int DT, int E, bool FULL>
+__device__ __forceinline__ void store_codes(float2 (&v)[E / 2], float amax, signed char* o, int t, int T, int len)
+{
+    using D = Deal<DT, E, true>;
+    constexpr int PV = D::VW / 2;
+    const float pre = amax < 1e-30f ? 0x1p100f : 1.0f;
+    const float2 inv = splat(amax > 0.f ? __fdiv_rn(127.0f, amax * pre) : 0.f);
+    if (pre != 1.0f) {
+#pragma unroll
+        for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], splat(pre));
+    }
+    const float2 magic = splat(12582912.0f);      // code_bits of pairs
+#pragma unroll
+    for (int c = 0; c < D::NC; ++c) {
+        const int k = D::col(c, t, T);
+        if (FULL || k < len) {
+            uint32_t h[PV];
+#pragma unroll
+            for (int j = 0; j < PV; ++j) {
+                const float2 q = add2(mul2(v[c * PV + j], inv), magic);
+                h[j] = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x0040);
+            }
+            if constexpr (PV == 4) st_v2(o + k, __byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
+            else st_u32(o + k, __byte_perm(h[0], h[1], 0x5410));
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------
+// Rows straight into registers
+// ------------------------------------------------------------------------------------------
+
+// A warp (SCOPE_WARP, rows of up to 1024 elements) or a CTA (up to 16384, 32 elements a thread) per row, for
+// rows in whole vectors. FULL: the threads' shares cover the row exactly, so nothing is checked.
+// Every row has its own thread group and no loop: the hardware's CTA scheduler overlaps rows and evens
+// out SMs of unequal bandwidth. Bound by HBM with a residual and by instructions without one: 32
+// elements a thread halve what a row costs in reductions against 16.
+template <int DT, int E, bool FULL, int SCOPE, int KIND>
+__global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512) rmsq_norm_direct_kernel(const __grid_constant__ NormParams p)
+{
+    using D = Deal<DT, E, true>;
+    using S = Scalar<DT>;
+    using TT = typename S::T;
+    constexpr bool RMS = KIND == NORM_RMS_INT8;
+    constexpr bool INT8 = KIND != NORM_LAYER;
+    constexpr int VW = D::VW, NC = D::NC, PV = VW / 2;
+    __shared__ float2 part[16];
+    __shared__ float part_max[16];
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int T = SCOPE == SCOPE_WARP ? 32 : blockDim.x;
+    const int t = SCOPE == SCOPE_WARP ? lane : threadIdx.x;
+    const int nwarps = SCOPE == SCOPE_WARP ? 1 : blockDim.x >> 5;
+    const int len = p.r.hidden;
+    const int row = SCOPE == SCOPE_WARP ? static_cast<int>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+    pdl_wait();
+    if (SCOPE == SCOPE_WARP && row >= p.r.rows) return;
+
+    const long long at = static_cast<long long>(row) * len;
+    const auto in = [&](int c) { return FULL || D::col(c, t, T) < len; };
+
+    // ---- s into registers, fp32 (exact), 0 outside the row ----
+    float2 v[E / 2];
+    {
+        const TT* const x = static_cast<const TT*>(p.r.in[0]) + at;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        uint4 raw[NC];
+#pragma unroll
+        for (int c = 0; c < NC; ++c) raw[c] = in(c) ? ld_stream_v4(reinterpret_cast<const uint4*>(x + D::col(c, t, T))) : zero;
+        if (p.r.ntens == 2) {
+            const TT* const r = static_cast<const TT*>(p.r.in[1]) + at;
+            TT* const ro = static_cast<TT*>(p.res_out) + at;
+            uint4 add[NC];
+#pragma unroll
+            for (int c = 0; c < NC; ++c) add[c] = in(c) ? ld_stream_v4(reinterpret_cast<const uint4*>(r + D::col(c, t, T))) : zero;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                raw[c] = Elem<DT>::add(raw[c], add[c]);
+                if (in(c)) st_v4(ro + D::col(c, t, T), raw[c]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            float2 f[PV];
+            Elem<DT>::pairs(raw[c], f);
+#pragma unroll
+            for (int j = 0; j < PV; ++j) v[c * PV + j] = f[j];
+        }
+    }
+
+    // ---- mean and squares about it ----
+    const int n_w = FULL ? 32 * E : D::count(SCOPE == SCOPE_WARP ? 0 : warp * 32, T, len);
+    float sum = 0.f, m2, mean = 0.f;
+    if constexpr (!RMS) {
+        float2 a = v[0];
+#pragma unroll
+        for (int j = 1; j < E / 2; ++j) a = add2(a, v[j]);
+        sum = warp_sum(a.x + a.y);
+        mean = FULL ? sum * (1.0f / (32 * E)) : n_w > 0 ? __fdividef(sum, static_cast<float>(n_w)) : 0.f;
+    }
+    {
+        const float2 m = splat(-mean);
+        float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            if (in(c)) {
+#pragma unroll
+                for (int j = 0; j < PV; ++j) {
+                    const float2 d = add2(v[c * PV + j], m);
+                    a = fma2(d, d, a);
+                }
+            }
+        }
+        m2 = warp_sum(a.x + a.y);
+    }
+    const float inv_h = __frcp_rn(static_cast<float>(len));
+    if constexpr (SCOPE != SCOPE_WARP) {
+        if (lane == 0) part[warp] = make_float2(sum, m2);
+        __syncthreads();
+        const float2 q = lane < nwarps ? part[lane] : make_float2(0.f, 0.f);
+        float d = 0.f, n_l = 0.f;
+        if constexpr (!RMS) {
+            mean = warp_sum(q.x) * inv_h;
+            if (lane < nwarps) {
+                n_l = FULL ? static_cast<float>(32 * E) : static_cast<float>(D::count(lane * 32, T, len));
+                d = FULL ? q.x * (1.0f / (32 * E)) - mean : n_l > 0.f ? __fdividef(q.x, n_l) - mean : 0.f;
+            }
+        }
+        m2 = warp_sum(fmaf(n_l * d, d, q.y));
+    }
+    const float rstd = __frsqrt_rn(fmaf(m2, inv_h, p.eps));
+
+    // ---- y ----
+    const float2 m = splat(-mean), r2 = splat(rstd), offset = splat(p.offset);
+    const TT* const gamma = static_cast<const TT*>(p.gamma);
+    const TT* const beta = static_cast<const TT*>(p.beta);
+    float amax = 0.f;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        if (in(c)) {
+            const int k = D::col(c, t, T);
+            float2 w[PV], b[PV];
+            Elem<DT>::pairs(ld_v4(gamma + k), w);
+            if (p.offset != 0.f) {
+#pragma unroll
+                for (int j = 0; j < PV; ++j) w[j] = add2(w[j], offset);
+            }
+            if (!RMS && beta != nullptr) {
+                Elem<DT>::pairs(ld_v4(beta + k), b);
+            } else {
+#pragma unroll
+                for (int j = 0; j < PV; ++j) b[j] = make_float2(0.f, 0.f);
+            }
+#pragma unroll
+            for (int j = 0; j < PV; ++j) {
+                float2& y = v[c * PV + j];
+                if constexpr (RMS) y = mul2(mul2(y, r2), w[j]);
+                else y = fma2(mul2(add2(y, m), r2), w[j], b[j]);
+                if constexpr (INT8) amax = max3(amax, fabsf(y.x), fabsf(y.y));
+            }
+            if constexpr (!INT8) st_v4(static_cast<TT*>(p.out) + at + k, pack_pairs<DT>(&v[c * PV]));
+        }
+    }
+    const bool leader = t == 0;
+    if constexpr (INT8) {
+        amax = warp_max(amax);
+        if constexpr (SCOPE != SCOPE_WARP) {
+            if (lane == 0) part_max[warp] = amax;
+            __syncthreads();
+            amax = warp_max(lane < nwarps ? part_max[lane] : 0.f);
+        }
+        store_codes<DT, E, FULL>(v, amax, static_cast<signed char*>(p.out) + at, t, T, len);
+        if (leader) p.scale[row] = amax / 127.0f;
+    } else if (leader) {
+        if (p.mean) p.mean[row] = mean;
+        if (p.rstd) p.rstd[row] = rstd;
+    }
+}
+
 // ------------------------------------------------------------------------------------------
 // Rows through shared memory
 // ------------------------------------------------------------------------------------------

@@ -27,8 +27,10 @@ cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem,
 
 struct NormPlan {
     int dt;
-    int elems;      // per thread: 8, 16 or 24
+    int elems;      // per thread: 8, 16 or 24 (direct: 8, 16 or 32)
     bool vec;
+    bool direct;    // rows straight into registers
+    bool full;      // direct: the threads' shares cover the row exactly
     int scope;      // SCOPE_*
     int threads;
     int smem;
@@ -65,8 +67,19 @@ const void* norm_bwd_reduce_fn();
         }                                                                                         \
         return nullptr;                                                                           \
     }                                                                                             \
+    template <int DT, bool FULL> static const void* NAME##_direct(const NormPlan& pl)             \
+    {                                                                                             \
+        if (pl.scope == SCOPE_CTA)                                                                \
+            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 32, FULL, SCOPE_CTA, KIND>); \
+        if (pl.elems == 8)                                                                        \
+            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 8, FULL, SCOPE_WARP, KIND>); \
+        if (pl.elems == 16)                                                                       \
+            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 16, FULL, SCOPE_WARP, KIND>); \
+        return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 32, FULL, SCOPE_WARP, KIND>); \
+    }                                                                                             \
     template <int DT> static const void* NAME##_fn(const NormPlan& pl)                            \
     {                                                                                             \
+        if (pl.direct) return pl.full ? NAME##_direct<DT, true>(pl) : NAME##_direct<DT, false>(pl); \
         return pl.vec ? NAME##_scope<DT, true>(pl) : NAME##_scope<DT, false>(pl);                 \
     }                                                                                             \
     cudaError_t NAME(const NormPlan& pl, const NormParams& p, cudaStream_t stream)                \

@@ -63,15 +63,31 @@ static RowGeometry row_geometry(int64_t rows, int hidden, int dtype, int most, i
 static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormParams&, cudaStream_t),
                                NormParams& p, int64_t rows, int dtype, const DeviceView& dv, cudaStream_t stream)
 {
-    const RowGeometry g = row_geometry(rows, p.r.hidden, dtype, kRowSlice, dv.sms);
     NormPlan pl;
+    p.r.rows = static_cast<int>(rows);
+    static const int env_d = getenv("RMSQ_D") ? atoi(getenv("RMSQ_D")) : 1;
+    const int hidden = p.r.hidden;
+    pl.direct = env_d && hidden % (16 / elem_bytes(dtype)) == 0 && hidden <= 512 * 32;
+    if (pl.direct) {
+        pl.dt = dtype;
+        pl.vec = true;
+        pl.cluster = 1;
+        pl.smem = 0;
+        pl.elems = hidden <= 256 ? 8 : hidden <= 512 ? 16 : 32;
+        pl.scope = hidden <= 1024 ? SCOPE_WARP : SCOPE_CTA;
+        const int T = pl.scope == SCOPE_WARP ? 32 : (hidden + 1023) / 1024 * 32;
+        pl.full = T * pl.elems == hidden;
+        pl.threads = pl.scope == SCOPE_WARP ? 256 : T;
+        pl.grid = static_cast<unsigned>(pl.scope == SCOPE_WARP ? (rows + 7) / 8 : rows);
+        return status_of(go(pl, p, stream));
+    }
+    const RowGeometry g = row_geometry(rows, p.r.hidden, dtype, kRowSlice, dv.sms);
     pl.dt = dtype;
     pl.vec = g.vec;
     pl.cluster = g.cluster;
     pl.elems = g.elems;
     pl.scope = g.cluster > 1 ? SCOPE_CLUSTER : g.T > 32 ? SCOPE_CTA : SCOPE_WARP;
     pl.threads = g.T * g.groups + 32;
-    p.r.rows = static_cast<int>(rows);
     p.r.total = rows * p.r.hidden * elem_bytes(dtype);
     p.r.slice = g.slice;
     p.r.slot = g.slot;
