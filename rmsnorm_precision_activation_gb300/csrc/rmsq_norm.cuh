@@ -12,13 +12,13 @@
 //   M2 = sum_w M2_w + n_w (mean_w - mean)^2,
 // which costs one block barrier instead of two.
 //
-// Bound by HBM. A row group of T threads (a warp for rows of up to 512 elements, else 16 or 24
-// elements a thread) takes rows in turn; a group's next rows come through a ring of shared-memory slots filled
-// by bulk copies, so that loads run while a row is reduced, and gamma and beta stay in shared memory.
-// (Rows loaded straight into registers, by a CTA each, reached 0.65-0.8 of the copy rate without a
-// residual and 0.14-0.28 at odd widths.) A CTA takes several rows and ends, rather than all of a
-// persistent CTA's share: the hardware's CTA scheduler then evens out SMs of unequal bandwidth. Rows wider
-// than 8192 elements are split over a cluster whose CTAs exchange the row's sums.
+// Bound by HBM. Two kernels:
+//  - rmsq_norm_direct_kernel, rows in whole vectors of up to 16384 elements: straight into registers, each
+//    row by a warp or CTA of its own.
+//  - rmsq_norm_ring_kernel, other widths: rows off 16-byte boundaries, whose direct loads of one element
+//    each reached 0.14 of the copy rate (bf16, 5121 wide), and rows split over a cluster, where gamma and
+//    beta would be read anew with every row. CTAs take several rows, which come through a ring of
+//    shared-memory slots filled by bulk copies, and keep gamma and beta in shared memory.
 #pragma once
 
 #include "rmsq_device.cuh"
@@ -328,7 +328,7 @@ __device__ __forceinline__ void store_codes(float2 (&v)[E / 2], float amax, sign
 // out SMs of unequal bandwidth. Bound by HBM with a residual and by instructions without one: 32
 // elements a thread halve what a row costs in reductions against 16.
 template <int DT, int E, bool FULL, int SCOPE, int KIND>
-__global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512) rmsq_norm_direct_kernel(const __grid_constant__ NormParams p)
+__global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOPE_WARP ? 4 : 2) rmsq_norm_direct_kernel(const __grid_constant__ NormParams p)
 {
     using D = Deal<DT, E, true>;
     using S = Scalar<DT>;
@@ -510,15 +510,30 @@ template <int DT, bool VEC> struct RowRing {
 
     // Vector (element, where VEC is false) k of tensor i of the row in a slot, as raw bits.
     __device__ __forceinline__ uint4 vec(uint32_t stage, int i, int k) const { return ld_shared_v4(at(stage, i) + k * ES); }
-    __device__ __forceinline__ T elem(uint32_t stage, int i, int row, int k) const
+    // Rows off 16-byte boundaries: the slice's first byte in tensor i's part of a slot, and how many of its
+    // elements the copies brought (all, but in the tensors' last row). Elements from there on are read
+    // from the tensor.
+    __device__ __forceinline__ uint32_t start(uint32_t stage, int i, int row) const
     {
-        const long long b0 = byte(row);
-        if (b0 + static_cast<long long>(k) * ES >= (r.total & ~15LL)) return static_cast<const T*>(r.in[i])[b0 / ES + k];
-        const uint32_t a = at(stage, i) + static_cast<uint32_t>(b0 & 15) + k * ES;
+        return at(stage, i) + static_cast<uint32_t>(byte(row) & 15);
+    }
+    __device__ __forceinline__ int have(int row) const
+    {
+        const long long n = ((r.total & ~15LL) - byte(row)) / ES;
+        return n < len ? static_cast<int>(n) : len;
+    }
+    static __device__ __forceinline__ T elem(uint32_t start, int k)
+    {
         T v;
-        if constexpr (ES == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-        else asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+        if constexpr (ES == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(start + k * ES));
+        else asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(start + k * ES));
         return v;
+    }
+    __device__ __forceinline__ T tail(int i, int row, int k) const { return static_cast<const T*>(r.in[i])[byte(row) / ES + k]; }
+    // Element k of tensor i, 0 outside the slice.
+    __device__ __forceinline__ T element(uint32_t start, int i, int row, int k, int have) const
+    {
+        return k < have ? elem(start, k) : k < len ? tail(i, row, k) : T(0);
     }
     // One thread sets the barriers up: a slot is empty when `warps` warps have left it.
     __device__ __forceinline__ void init(int warps) const
@@ -600,41 +615,39 @@ struct ClusterSums {
     }
 };
 
-// Elements of a row per thread: 8, 16 or 24, and the warps of a CTA that work on rows then (one more
-// copies). Registers are dealt to a quarter of the SM's warps each, so 16 warps of 16 elements and 12 of
-// 24 are what two CTAs forward and one backward leave enough of them for.
-constexpr int row_warps(int elems) { return elems <= 16 ? 15 : 11; }
-constexpr int kRowSlice = 8192;               // elements of a row per CTA at most (11 warps of 24)
+constexpr int kRingSlice = 16384;             // bytes of a tensor's row per CTA at most
+constexpr int kRingWorkers = 256;             // threads that work on rows; a warp more copies
 
 // Shared memory before gamma, beta and the ring: barriers, the groups' warp sums and maxima (each for
 // two rows in turn: one barrier a row then keeps a row's from the next but one's), the cluster's sums.
-constexpr int kNormHead = (kRingBars + 2 * 16 * 8 + 2 * 16 * 4 + 2 * ClusterSums::BYTES + 127) / 128 * 128;
+constexpr int kNormHead = (kRingBars + 2 * 8 * 8 + 2 * 8 * 4 + 2 * ClusterSums::BYTES + 127) / 128 * 128;
 
-template <int DT, int E, bool VEC, int SCOPE, int KIND>
-__global__ void __launch_bounds__(32 * row_warps(E) + 32, 2) rmsq_norm_kernel(const __grid_constant__ NormParams p)
+template <int DT, int E, bool VEC, bool FULL, int SCOPE, int KIND>
+__global__ void __launch_bounds__(kRingWorkers + 32, VEC ? 3 : 2) rmsq_norm_ring_kernel(const __grid_constant__ NormParams p)
 {
     using D = Deal<DT, E, VEC>;
     using S = Scalar<DT>;
     using TT = typename S::T;
     constexpr bool RMS = KIND == NORM_RMS_INT8;
     constexpr bool INT8 = KIND != NORM_LAYER;
-    constexpr int VW = D::VW, NC = D::NC;
+    constexpr int VW = D::VW, NC = D::NC, PV = VEC ? VW / 2 : 1;
     extern __shared__ __align__(128) unsigned char smem[];
 
     float2* const part = reinterpret_cast<float2*>(smem + kRingBars);
-    float* const part_max = reinterpret_cast<float*>(part + 32);
-    unsigned char* const cluster_part = reinterpret_cast<unsigned char*>(part_max + 32);
+    float* const part_max = reinterpret_cast<float*>(part + 16);
+    unsigned char* const cluster_part = reinterpret_cast<unsigned char*>(part_max + 16);
 
     const int T = SCOPE == SCOPE_WARP ? 32 : p.T;
     const int group = SCOPE == SCOPE_CLUSTER ? 0 : threadIdx.x / T, groups = p.groups;
-    const int t = threadIdx.x - group * T;
+    const int thread = threadIdx.x - group * T;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group_warps = T >> 5, warp0 = group * group_warps;
     const int nc = SCOPE == SCOPE_CLUSTER ? static_cast<int>(cluster_size()) : 1;
     const int rank = SCOPE == SCOPE_CLUSTER ? static_cast<int>(cluster_rank()) : 0;
 
     const int c0 = rank * p.r.slice, left = p.r.hidden - c0;
-    const int len = left < 0 ? 0 : left < p.r.slice ? left : p.r.slice;
+    const int len = FULL ? p.r.slice : left < 0 ? 0 : left < p.r.slice ? left : p.r.slice;
+    const auto in = [&](int k) { return FULL || k < len; };
     // a warp's lanes of the copying warp stand for the groups they feed
     const bool copies = threadIdx.x >= T * groups;
     const int mine = copies ? (lane < groups ? lane : 0) : group;
@@ -690,17 +703,19 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32, 2) rmsq_norm_kernel(co
     // CTA's of the cluster. A count that is not a power of two makes a mean off by half a step more.
     const uint32_t limit = wait_limit(p.timeout_ns);
     const auto inverse = [](int k) { return k > 0 ? 1.0f / static_cast<float>(k) : 0.f; };
-    const int n_w = D::count((warp - warp0) * 32, T, len);
-    const int n_l = lane < group_warps ? D::count(lane * 32, T, len) : 0;
+    const int n_w = FULL ? 32 * E : D::count((warp - warp0) * 32, T, len);
+    const int n_l = lane >= group_warps ? 0 : FULL ? 32 * E : D::count(lane * 32, T, len);
     const int n_r = SCOPE == SCOPE_CLUSTER && lane < nc ? min(max(p.r.hidden - lane * p.r.slice, 0), p.r.slice) : 0;
-    const bool full = n_w == 32 * E;
     const float inv_w = inverse(n_w), inv_l = inverse(n_l), inv_c = inverse(len), inv_r = inverse(n_r);
     const float inv_h = 1.0f / static_cast<float>(p.r.hidden), f_l = static_cast<float>(n_l), f_r = static_cast<float>(n_r);
-    const float2 offset = splat(p.offset);
     bool dead = false;                            // a wait ran out: finish without waiting again
     int stage = 0, phase = 0;
     int flip = 0;
     for (int i = 0; i < n; ++i) {
+        // made opaque to the compiler again and again, which would keep every element's address and test
+        // in registers from row to row and from phase to phase
+        int t = thread;
+        asm volatile("" : "+r"(t));
         const int row = first + i * groups;
         if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage), phase, limit)) dead = true;
         const long long at = static_cast<long long>(row) * p.r.hidden + c0;
@@ -712,29 +727,29 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32, 2) rmsq_norm_kernel(co
             for (int c = 0; c < NC; ++c) {
                 const int k = D::col(c, t, T);
                 uint4 raw = make_uint4(0, 0, 0, 0);
-                if (k < len) {
+                if (in(k)) {
                     raw = ring.vec(stage, 0, k);
                     if (has_res) {
                         raw = Elem<DT>::add(raw, ring.vec(stage, 1, k));
                         st_v4(static_cast<TT*>(p.res_out) + at + k, raw);
                     }
                 }
-                float2 f[VW / 2];
+                float2 f[PV];
                 Elem<DT>::pairs(raw, f);
 #pragma unroll
-                for (int j = 0; j < VW / 2; ++j) v[c * (VW / 2) + j] = f[j];
+                for (int j = 0; j < PV; ++j) v[c * PV + j] = f[j];
             }
         } else {
+            const int have = ring.have(row);
+            const uint32_t x0 = ring.start(stage, 0, row), r0 = ring.start(stage, 1, row);
+            TT* const ro = static_cast<TT*>(p.res_out) + at;
 #pragma unroll
             for (int c = 0; c < E; ++c) {
                 const int k = D::col(c, t, T);
-                TT raw = TT(0);
-                if (k < len) {
-                    raw = ring.elem(stage, 0, row, k);
-                    if (has_res) {
-                        raw = S::add(raw, ring.elem(stage, 1, row, k));
-                        static_cast<TT*>(p.res_out)[at + k] = raw;
-                    }
+                TT raw = ring.element(x0, 0, row, k, have);
+                if (has_res) {
+                    raw = S::add(raw, ring.element(r0, 1, row, k, have));
+                    if (k < len) ro[k] = raw;
                 }
                 if (c & 1) v[c / 2].y = S::get(raw);
                 else v[c / 2].x = S::get(raw);
@@ -742,6 +757,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32, 2) rmsq_norm_kernel(co
         }
 
         // ---- mean and squares about it ----
+        asm volatile("" : "+r"(t));
         float sum = 0.f, m2, mean = 0.f;
         if constexpr (!RMS) {
             float2 a = v[0];
@@ -753,28 +769,20 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32, 2) rmsq_norm_kernel(co
         {
             const float2 m = splat(-mean);
             float2 a = make_float2(0.f, 0.f);
-            if (full) {
 #pragma unroll
-                for (int j = 0; j < E / 2; ++j) {
-                    const float2 d = add2(v[j], m);
-                    a = fma2(d, d, a);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < E / 2; ++j) {
-                    float2 d = add2(v[j], m);
-                    if (D::col(2 * j / VW, t, T) >= len) d.x = 0.f;
-                    if (D::col((2 * j + 1) / VW, t, T) >= len) d.y = 0.f;
-                    a = fma2(d, d, a);
-                }
+            for (int j = 0; j < E / 2; ++j) {
+                float2 d = add2(v[j], m);
+                if (!in(D::col(2 * j / VW, t, T))) d.x = 0.f;
+                if (!in(D::col((2 * j + 1) / VW, t, T))) d.y = 0.f;
+                a = fma2(d, d, a);
             }
             m2 = warp_sum(a.x + a.y);
         }
         if (lane == 0) mbar_arrive(ring.empty(stage));       // the warp has read the slot
         if constexpr (SCOPE != SCOPE_WARP) {
-            if (lane == 0) part[flip * 16 + warp] = make_float2(sum, m2);
+            if (lane == 0) part[flip * 8 + warp] = make_float2(sum, m2);
             group_sync(group, T);
-            const float2 q = lane < group_warps ? part[flip * 16 + warp0 + lane] : make_float2(0.f, 0.f);
+            const float2 q = lane < group_warps ? part[flip * 8 + warp0 + lane] : make_float2(0.f, 0.f);
             float d = 0.f;
             if constexpr (!RMS) {
                 sum = warp_sum(q.x);
@@ -797,61 +805,57 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32, 2) rmsq_norm_kernel(co
         const float rstd = __frsqrt_rn(m2 * inv_h + p.eps);
 
         // ---- y ----
+        asm volatile("" : "+r"(t));
         const float2 m = splat(-mean), r2 = splat(rstd);
-        if constexpr (VEC) {
+        float amax = 0.f;
+        TT* const o = static_cast<TT*>(p.out) + at;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int k = D::col(c, t, T);
-                if (k < len) {
-                    float2 w[VW / 2], b[VW / 2];
-                    Elem<DT>::pairs(ld_shared_v4(smem_u32(ws + k)), w);
-                    Elem<DT>::pairs(ld_shared_v4(smem_u32(bs + k)), b);
+        for (int c = 0; c < E / 2 / PV; ++c) {
+            const int k0 = D::col(VEC ? c : 2 * c, t, T), k1 = VEC ? k0 : D::col(2 * c + 1, t, T);
+            float2 w[PV], b[PV];
+            if constexpr (VEC) {
+                if (in(k0)) {
+                    Elem<DT>::pairs(ld_shared_v4(smem_u32(ws + k0)), w);
+                    Elem<DT>::pairs(ld_shared_v4(smem_u32(bs + k0)), b);
+                }
+            } else {
+                // outside the slice: any element of it, whose result is not used
+                const int j0 = k0 < len ? k0 : 0, j1 = k1 < len ? k1 : 0;
+                w[0] = make_float2(S::get(ws[j0]), S::get(ws[j1]));
+                b[0] = make_float2(S::get(bs[j0]), S::get(bs[j1]));
+            }
+            if (p.offset != 0.f) {
 #pragma unroll
-                    for (int j = 0; j < VW / 2; ++j) {
-                        float2& y = v[c * (VW / 2) + j];
-                        y = fma2(mul2(add2(y, m), r2), add2(w[j], offset), b[j]);
+                for (int j = 0; j < PV; ++j) w[j] = add2(w[j], splat(p.offset));
+            }
+            if (in(k0)) {
+#pragma unroll
+                for (int j = 0; j < PV; ++j) {
+                    float2& y = v[c * PV + j];
+                    if constexpr (RMS) y = mul2(mul2(y, r2), w[j]);
+                    else y = fma2(mul2(add2(y, m), r2), w[j], b[j]);
+                    if constexpr (INT8) {
+                        amax = fmaxf(amax, fabsf(y.x));
+                        if (in(k1)) amax = fmaxf(amax, fabsf(y.y));
                     }
                 }
             }
-        } else {
-#pragma unroll
-            for (int j = 0; j < E / 2; ++j) {
-                const int k0 = D::col(2 * j, t, T), k1 = D::col(2 * j + 1, t, T);
-                const float2 w = make_float2(k0 < len ? S::get(ws[k0]) : 0.f, k1 < len ? S::get(ws[k1]) : 0.f);
-                const float2 b = make_float2(k0 < len ? S::get(bs[k0]) : 0.f, k1 < len ? S::get(bs[k1]) : 0.f);
-                v[j] = fma2(mul2(add2(v[j], m), r2), add2(w, offset), b);
-            }
-        }
-        if constexpr (!INT8) {
-            TT* const o = static_cast<TT*>(p.out) + at;
-            if constexpr (VEC) {
-#pragma unroll
-                for (int c = 0; c < NC; ++c)
-                    if (D::col(c, t, T) < len) st_v4(o + D::col(c, t, T), pack_pairs<DT>(&v[c * (VW / 2)]));
-            } else {
-#pragma unroll
-                for (int c = 0; c < E; ++c)
-                    if (D::col(c, t, T) < len) o[D::col(c, t, T)] = S::put(c & 1 ? v[c / 2].y : v[c / 2].x);
+            if constexpr (!INT8) {
+                if constexpr (VEC) {
+                    if (in(k0)) st_v4(o + k0, pack_pairs<DT>(&v[c * PV]));
+                } else {
+                    if (k0 < len) o[k0] = S::put(v[c].x);
+                    if (k1 < len) o[k1] = S::put(v[c].y);
+                }
             }
         }
         const bool leader = t == 0 && rank == 0;
         if constexpr (INT8) {
-            float amax = 0.f;
-            if (full) {
-#pragma unroll
-                for (int j = 0; j < E / 2; ++j) amax = max3(amax, fabsf(v[j].x), fabsf(v[j].y));
-            } else {
-#pragma unroll
-                for (int j = 0; j < E / 2; ++j) {
-                    if (D::col(2 * j / VW, t, T) < len) amax = fmaxf(amax, fabsf(v[j].x));
-                    if (D::col((2 * j + 1) / VW, t, T) < len) amax = fmaxf(amax, fabsf(v[j].y));
-                }
-            }
             amax = warp_max(amax);
             if constexpr (SCOPE != SCOPE_WARP) {
-                if (lane == 0) part_max[flip * 16 + warp] = amax;
+                if (lane == 0) part_max[flip * 8 + warp] = amax;
                 group_sync(group, T);
-                amax = warp_max(lane < group_warps ? part_max[flip * 16 + warp0 + lane] : 0.f);
+                amax = warp_max(lane < group_warps ? part_max[flip * 8 + warp0 + lane] : 0.f);
             }
             if constexpr (SCOPE == SCOPE_CLUSTER) {
                 float4 q;
@@ -859,33 +863,17 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32, 2) rmsq_norm_kernel(co
                 if (!maxima.receive(lane, flip, (i >> 1) & 1, dead ? 0 : limit, q)) dead = true;
                 amax = warp_max(q.x);
             }
-            // 127 / amax overflows for rows of tiny y: those are scaled up by 2^100 first (exact).
-            const float pre = amax < 1e-30f ? 0x1p100f : 1.0f;
-            const float2 pre2 = splat(pre), inv = splat(amax > 0.f ? 127.0f / (amax * pre) : 0.f);
-            signed char* const o = static_cast<signed char*>(p.out) + at;
-            if (pre != 1.0f) {
-#pragma unroll
-                for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], pre2);
-            }
-#pragma unroll
-            for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], inv);
+            asm volatile("" : "+r"(t));
+            signed char* const codes = static_cast<signed char*>(p.out) + at;
             if constexpr (VEC) {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int k = D::col(c, t, T);
-                    const float2* const f = &v[c * (VW / 2)];
-                    if (k < len) {
-                        if constexpr (VW == 8)
-                            st_v2(o + k, pack_codes(f[0].x, f[0].y, f[1].x, f[1].y), pack_codes(f[2].x, f[2].y, f[3].x, f[3].y));
-                        else
-                            st_u32(o + k, pack_codes(f[0].x, f[0].y, f[1].x, f[1].y));
-                    }
-                }
+                store_codes<DT, E, FULL>(v, amax, codes, t, T, len);
             } else {
+                const float pre = amax < 1e-30f ? 0x1p100f : 1.0f, inv = amax > 0.f ? __fdiv_rn(127.0f, amax * pre) : 0.f;
 #pragma unroll
-                for (int c = 0; c < E; ++c)
-                    if (D::col(c, t, T) < len)
-                        o[D::col(c, t, T)] = static_cast<signed char>(code_bits(c & 1 ? v[c / 2].y : v[c / 2].x) & 0xFFu);
+                for (int c = 0; c < E; ++c) {
+                    const int k = D::col(c, t, T);
+                    if (k < len) codes[k] = static_cast<signed char>(code_bits((c & 1 ? v[c / 2].y : v[c / 2].x) * pre * inv) & 0xFFu);
+                }
             }
             if (leader) p.scale[row] = amax / 127.0f;
         } else if (leader) {

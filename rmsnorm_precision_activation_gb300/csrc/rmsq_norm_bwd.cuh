@@ -46,6 +46,10 @@ struct NormBwdReduceParams {
 
 // Shared memory before the ring: barriers, the groups' warp sums (of two iterations in turn), the
 // cluster's sums.
+// Elements of a row per thread: 8, 16 or 24, and the warps of a CTA that work on rows then (one more
+// copies). Registers are dealt to a quarter of the SM's warps each: 16 warps get 128, 12 get 168.
+constexpr int row_warps(int elems) { return elems <= 16 ? 15 : 11; }
+
 constexpr int kBwdHead = (kRingBars + 2 * 16 * 16 + ClusterSums::BYTES + 127) / 128 * 128;
 
 template <int DT, int E, bool VEC>
@@ -60,7 +64,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     float4* const red = reinterpret_cast<float4*>(smem + kRingBars);
     unsigned char* const cluster_part = reinterpret_cast<unsigned char*>(red + 32);
 
-    const int T = p.T, group = threadIdx.x / T, t = threadIdx.x % T;
+    const int T = p.T, group = threadIdx.x / T, thread = threadIdx.x % T;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group_warps = T >> 5, warp0 = group * group_warps;
     const int nc = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
@@ -96,7 +100,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
 
     float2 acc_g[E / 2], acc_b[E / 2];
     Held<DT, E, VEC> w;                           // gamma, in its own type
-    w.load(static_cast<const TT*>(p.gamma) + c0, t, T, len);
+    w.load(static_cast<const TT*>(p.gamma) + c0, thread, T, len);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) acc_g[e] = acc_b[e] = make_float2(0.f, 0.f);
 
@@ -106,7 +110,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     int stage = 0, phase = 0;
     int flip = 0;
     // Elements 2 j and 2 j + 1 of the thread's share of tensor i, or all of its vector c (0 outside the slice).
-    auto load = [&](int slot, int i, int row, int c, float2* f) {
+    auto load = [&](int t, int slot, int i, int row, int have, int c, float2* f) {
         if constexpr (VEC) {
             const int k = D::col(c, t, T);
             float2 g[VW / 2];
@@ -114,9 +118,9 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
 #pragma unroll
             for (int j = 0; j < VW / 2; ++j) f[j] = g[j];
         } else {
-            const int k0 = D::col(2 * c, t, T), k1 = D::col(2 * c + 1, t, T);
-            f[0].x = k0 < len ? S::get(ring.elem(slot, i, row, k0)) : 0.f;
-            f[0].y = k1 < len ? S::get(ring.elem(slot, i, row, k1)) : 0.f;
+            const uint32_t s0 = ring.start(slot, i, row);
+            f[0].x = S::get(ring.element(s0, i, row, D::col(2 * c, t, T), have));
+            f[0].y = S::get(ring.element(s0, i, row, D::col(2 * c + 1, t, T), have));
         }
     };
     constexpr int PAIRS = VEC ? VW / 2 : 1, CHUNKS = E / 2 / PAIRS;
@@ -124,6 +128,9 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     // Two rows at a time, so that one barrier and one round of shuffles serve both. Every CTA of a
     // cluster, and every thread of a group, runs the same iterations.
     for (int i = 0; i < n; i += 2) {
+        // opaque to the compiler, which would keep every element's address in registers across rows
+        int t = thread;
+        asm volatile("" : "+r"(t));
         const int pair = n - i < 2 ? 1 : 2;
         w.pin();
         float mean[2], rstd[2], s1[2] = {0.f, 0.f}, s2[2] = {0.f, 0.f};
@@ -138,13 +145,14 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
             if (r < pair) {
                 const int row = first + (i + r) * stride;
                 if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage + r), phase, limit)) dead = true;
+                const int have = VEC ? len : ring.have(row);
                 const float2 m = splat(-mean[r]), rs = splat(rstd[r]);
                 float2 a1 = make_float2(0.f, 0.f), a2 = a1;
 #pragma unroll
                 for (int c = 0; c < CHUNKS; ++c) {
                     float2 dy[PAIRS], s[PAIRS];
-                    load(stage + r, 0, row, c, dy);
-                    load(stage + r, 1, row, c, s);
+                    load(t, stage + r, 0, row, have, c, dy);
+                    load(t, stage + r, 1, row, have, c, s);
 #pragma unroll
                     for (int j = 0; j < PAIRS; ++j) {
                         const int e = c * PAIRS + j;
@@ -186,16 +194,17 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
         for (int r = 0; r < 2; ++r) {
             if (r < pair) {
                 const int row = first + (i + r) * stride;
+                const int have = VEC ? len : ring.have(row);
                 const float m1 = s1[r] * inv_h, m2 = s2[r] * inv_h;
                 TT* const out = static_cast<TT*>(p.ds) + static_cast<long long>(row) * p.r.hidden + c0;
                 const float2 m = splat(-mean[r]), rs = splat(rstd[r]), n1 = splat(-m1), n2 = splat(-m2);
 #pragma unroll
                 for (int c = 0; c < CHUNKS; ++c) {
                     float2 dy[PAIRS], s[PAIRS], d[PAIRS];
-                    load(stage + r, 0, row, c, dy);
-                    load(stage + r, 1, row, c, s);
+                    load(t, stage + r, 0, row, have, c, dy);
+                    load(t, stage + r, 1, row, have, c, s);
                     if (has_res) {
-                        load(stage + r, 2, row, c, d);
+                        load(t, stage + r, 2, row, have, c, d);
                     } else {
 #pragma unroll
                         for (int j = 0; j < PAIRS; ++j) d[j] = make_float2(0.f, 0.f);
@@ -239,7 +248,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     if (p.groups == 1) {
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int k = D::col(c, t, T);
+            const int k = D::col(c, thread, T);
 #pragma unroll
             for (int j = 0; j < VW; ++j)
                 if (k < len) {
@@ -253,7 +262,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
             if (g == group) {
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    const int k = D::col(c, t, T);
+                    const int k = D::col(c, thread, T);
 #pragma unroll
                     for (int j = 0; j < VW; ++j)
                         if (k < len) {

@@ -27,10 +27,10 @@ cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem,
 
 struct NormPlan {
     int dt;
-    int elems;      // per thread: 8, 16 or 24 (direct: 8, 16 or 32)
+    int elems;      // per thread: 8, 16 (direct only) or 32
     bool vec;
     bool direct;    // rows straight into registers
-    bool full;      // direct: the threads' shares cover the row exactly
+    bool full;      // the threads' shares cover the row exactly
     int scope;      // SCOPE_*
     int threads;
     int smem;
@@ -49,21 +49,16 @@ const void* norm_bwd_fn(int dt, int elems, bool vec);
 const void* norm_bwd_reduce_fn();
 
 #define RMSQ_DEFINE_NORM_DISPATCH(NAME, KIND)                                                     \
-    template <int DT, bool VEC> static const void* NAME##_scope(const NormPlan& pl)               \
+    template <int DT, bool VEC, bool FULL> static const void* NAME##_ring(const NormPlan& pl)     \
     {                                                                                             \
-        switch (pl.scope * 64 + pl.elems) {                                                       \
-        case SCOPE_WARP * 64 + 8:                                                                 \
-            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 8, VEC, SCOPE_WARP, KIND>); \
-        case SCOPE_WARP * 64 + 16:                                                                \
-            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 16, VEC, SCOPE_WARP, KIND>); \
-        case SCOPE_CTA * 64 + 16:                                                                 \
-            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 16, VEC, SCOPE_CTA, KIND>); \
-        case SCOPE_CTA * 64 + 24:                                                                 \
-            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 24, VEC, SCOPE_CTA, KIND>); \
-        case SCOPE_CLUSTER * 64 + 16:                                                             \
-            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 16, VEC, SCOPE_CLUSTER, KIND>); \
-        case SCOPE_CLUSTER * 64 + 24:                                                             \
-            return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, 24, VEC, SCOPE_CLUSTER, KIND>); \
+        if (pl.scope == SCOPE_CLUSTER)                                                            \
+            return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, VEC, FULL, SCOPE_CLUSTER, KIND>); \
+        if constexpr (!VEC) {                                                                     \
+            if (pl.scope == SCOPE_CTA)                                                            \
+                return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, VEC, FULL, SCOPE_CTA, KIND>); \
+            if (pl.elems == 8)                                                                    \
+                return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 8, VEC, FULL, SCOPE_WARP, KIND>); \
+            return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, VEC, FULL, SCOPE_WARP, KIND>); \
         }                                                                                         \
         return nullptr;                                                                           \
     }                                                                                             \
@@ -80,7 +75,8 @@ const void* norm_bwd_reduce_fn();
     template <int DT> static const void* NAME##_fn(const NormPlan& pl)                            \
     {                                                                                             \
         if (pl.direct) return pl.full ? NAME##_direct<DT, true>(pl) : NAME##_direct<DT, false>(pl); \
-        return pl.vec ? NAME##_scope<DT, true>(pl) : NAME##_scope<DT, false>(pl);                 \
+        if (!pl.vec) return NAME##_ring<DT, false, false>(pl);                                    \
+        return pl.full ? NAME##_ring<DT, true, true>(pl) : NAME##_ring<DT, true, false>(pl);      \
     }                                                                                             \
     cudaError_t NAME(const NormPlan& pl, const NormParams& p, cudaStream_t stream)                \
     {                                                                                             \

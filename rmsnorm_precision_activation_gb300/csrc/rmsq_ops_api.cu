@@ -31,27 +31,27 @@ static rmsq_status status_of(cudaError_t e)
     return RMSQ_ERR_LAUNCH;
 }
 
-// How rows are dealt out: wide rows are split evenly over the smallest cluster of 2, 4, 8 or 16 CTAs
-// whose slices hold at most `most` elements, in whole vectors where the row has them; a slice takes
-// T threads of `elems` elements; short rows leave a CTA room for several row groups, of which it
-// takes no more than give every SM a row.
+// How rows are dealt out over rings: wide rows are split evenly over the smallest cluster of 2, 4, 8 or
+// 16 CTAs whose slices take at most kRingSlice bytes, in whole vectors where the row has them; a slice
+// takes T threads of `elems` elements; short rows leave a CTA of `workers` threads room for several row
+// groups, of which it takes no more than give every SM a row.
 struct RowGeometry {
     int cluster, slice, elems, T, groups, slot;
     bool vec;
 };
 
-static RowGeometry row_geometry(int64_t rows, int hidden, int dtype, int most, int sms)
+static RowGeometry row_geometry(int64_t rows, int hidden, int dtype, int sms, int (*elems)(int), int (*workers)(int))
 {
     const int es = elem_bytes(dtype), per16 = 16 / es;
     RowGeometry g;
     g.vec = hidden % per16 == 0;
     g.cluster = 1;
-    while (static_cast<long long>(g.cluster) * most < hidden) g.cluster *= 2;
+    while (static_cast<long long>(g.cluster) * (kRingSlice / es) < hidden) g.cluster *= 2;
     const int vec = g.vec ? per16 : 1;
     g.slice = ((hidden + g.cluster - 1) / g.cluster + vec - 1) / vec * vec;
-    g.elems = g.slice <= 256 ? 8 : g.slice <= row_warps(16) * 32 * 16 ? 16 : 24;
+    g.elems = elems(g.slice);
     g.T = ((g.slice + g.elems - 1) / g.elems + 31) / 32 * 32;
-    g.groups = g.cluster > 1 ? 1 : row_warps(g.elems) * 32 / g.T;
+    g.groups = g.cluster > 1 ? 1 : workers(g.elems) / g.T;
     const int64_t spread = (rows + sms - 1) / sms;
     if (g.groups > spread) g.groups = static_cast<int>(spread);
     // rows off 16-byte boundaries are copied from the boundary below
@@ -64,15 +64,13 @@ static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormPara
                                NormParams& p, int64_t rows, int dtype, const DeviceView& dv, cudaStream_t stream)
 {
     NormPlan pl;
-    p.r.rows = static_cast<int>(rows);
-    static const int env_d = getenv("RMSQ_D") ? atoi(getenv("RMSQ_D")) : 1;
     const int hidden = p.r.hidden;
-    pl.direct = env_d && hidden % (16 / elem_bytes(dtype)) == 0 && hidden <= 512 * 32;
+    pl.dt = dtype;
+    pl.cluster = 1;
+    pl.smem = 0;
+    p.r.rows = static_cast<int>(rows);
+    pl.direct = hidden % (16 / elem_bytes(dtype)) == 0 && hidden <= 512 * 32;
     if (pl.direct) {
-        pl.dt = dtype;
-        pl.vec = true;
-        pl.cluster = 1;
-        pl.smem = 0;
         pl.elems = hidden <= 256 ? 8 : hidden <= 512 ? 16 : 32;
         pl.scope = hidden <= 1024 ? SCOPE_WARP : SCOPE_CTA;
         const int T = pl.scope == SCOPE_WARP ? 32 : (hidden + 1023) / 1024 * 32;
@@ -81,26 +79,26 @@ static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormPara
         pl.grid = static_cast<unsigned>(pl.scope == SCOPE_WARP ? (rows + 7) / 8 : rows);
         return status_of(go(pl, p, stream));
     }
-    const RowGeometry g = row_geometry(rows, p.r.hidden, dtype, kRowSlice, dv.sms);
-    pl.dt = dtype;
+    const RowGeometry g = row_geometry(rows, hidden, dtype, dv.sms, [](int slice) { return slice <= 256 ? 8 : 32; },
+                                       [](int) { return kRingWorkers; });
     pl.vec = g.vec;
     pl.cluster = g.cluster;
     pl.elems = g.elems;
     pl.scope = g.cluster > 1 ? SCOPE_CLUSTER : g.T > 32 ? SCOPE_CTA : SCOPE_WARP;
+    pl.full = g.T * g.elems == g.slice && g.slice * g.cluster == hidden;
     pl.threads = g.T * g.groups + 32;
-    p.r.total = rows * p.r.hidden * elem_bytes(dtype);
+    p.r.total = rows * hidden * elem_bytes(dtype);
     p.r.slice = g.slice;
     p.r.slot = g.slot;
     p.T = g.T;
     p.groups = g.groups;
     p.err = dv.err;
     p.timeout_ns = dv.timeout_ns;
-    // CTAs per SM: what the registers hold (32 warps of up to 16 elements a thread, 24 of more), or as
-    // many as leave each two slots a group
+    // CTAs per SM: what the registers hold (27 warps), or as many as leave each two slots a group
     const int64_t stage = static_cast<int64_t>(g.slot) * p.r.ntens * g.groups, head = kNormHead + 2 * g.slot;
     const auto slots = [&](int ctas) { return (dv.smem_optin / ctas - 1024 - head) / stage; };
     static const int env_r = getenv("RMSQ_R") ? atoi(getenv("RMSQ_R")) : 0, env_s = getenv("RMSQ_S") ? atoi(getenv("RMSQ_S")) : 0, env_c = getenv("RMSQ_C") ? atoi(getenv("RMSQ_C")) : 0;
-    int ctas = env_c ? env_c : (g.elems <= 16 ? 32 : 24) * 32 / pl.threads;
+    int ctas = env_c ? env_c : (pl.vec ? 27 : 20) * 32 / pl.threads;
     while (ctas > 1 && slots(ctas) < 2) --ctas;
     int64_t stages = slots(ctas);
     if (stages < 1) return RMSQ_ERR_LAUNCH;
@@ -284,8 +282,9 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         p.offset = weight_offset;
         p.timeout_ns = dv.timeout_ns;
 
-        // slices of at most 16 KB: the ring then holds at least four rows of three tensors
-        RowGeometry g = row_geometry(rows, p.r.hidden, dtype, 16384 / elem_bytes(dtype), dv.sms);
+        RowGeometry g = row_geometry(rows, p.r.hidden, dtype, dv.sms,
+                                     [](int slice) { return slice <= 256 ? 8 : slice <= row_warps(16) * 32 * 16 ? 16 : 24; },
+                                     [](int elems) { return row_warps(elems) * 32; });
         p.r.slice = g.slice;
         p.r.slot = g.slot;
         p.T = g.T;
