@@ -51,7 +51,6 @@ struct NormParams {
     float* rstd;           // or null
     int T;                 // threads per row group
     int groups;            // row groups per CTA
-    int rows_per_group;
     float eps;
     float offset;
     unsigned int* err;
@@ -202,25 +201,48 @@ template <int SCOPE> __device__ __forceinline__ bool mbar_wait(uint32_t bar, uin
     return false;
 }
 
-// The thread's share of a slice of len elements, dealt to T threads. VEC: vector c of a thread is
-// vector c * T + t of the slice (rows start on 16-byte boundaries); otherwise element j is element
-// j * T + t, so that a warp's accesses are contiguous either way.
-template <int DT, int E, bool VEC> struct Deal {
-    static constexpr int VW = VEC ? Elem<DT>::EPV : 1;
-    static constexpr int NC = E / VW;
+// A row in vectors of 16 bytes, dealt to T threads: vector c of a thread is vector c * T + t, so that a
+// warp's accesses are contiguous. Rows whose width is no whole number of vectors start `shift` elements
+// behind a 16-byte boundary; such a row is taken from that boundary on ("columns"), and its elements are
+// columns shift to shift + hidden. All accesses but those of its first and last vector are then whole
+// vectors, as in other rows.
+template <int DT, int E> struct Deal {
+    static constexpr int VW = Elem<DT>::EPV, NC = E / VW, PV = VW / 2;
     static __device__ __forceinline__ int col(int c, int t, int T) { return (c * T + t) * VW; }
-    // how many of the slice's elements the 32 threads from t0 on hold
-    static __device__ __forceinline__ int count(int t0, int T, int len)
+    // how many of the columns lo to hi the 32 threads from t0 on hold
+    static __device__ __forceinline__ int count(int t0, int T, int lo, int hi)
     {
         int n = 0;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            const int left = len - (c * T + t0) * VW;
-            n += left < 0 ? 0 : left < 32 * VW ? left : 32 * VW;
+            const int first = (c * T + t0) * VW;
+            n += max(0, min(hi, first + 32 * VW) - max(lo, first));
         }
         return n;
     }
 };
+
+// Zeros in place of a vector's columns outside lo to hi.
+template <int PV> __device__ __forceinline__ void clear_outside(float2 (&f)[PV], int k, int lo, int hi)
+{
+#pragma unroll
+    for (int j = 0; j < PV; ++j) {
+        if (k + 2 * j < lo || k + 2 * j >= hi) f[j].x = 0.f;
+        if (k + 2 * j + 1 < lo || k + 2 * j + 1 >= hi) f[j].y = 0.f;
+    }
+}
+
+// A vector's columns lo to hi to p + k, element by element.
+template <int DT> __device__ __forceinline__ void store_inside(typename Scalar<DT>::T* p, const uint4& v, int k, int lo, int hi)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < Elem<DT>::EPV; ++j)
+        if (k + j >= lo && k + j < hi) {
+            if constexpr (DT == DT_F32) p[k + j] = __uint_as_float(w[j]);
+            else p[k + j] = static_cast<uint16_t>(j & 1 ? w[j / 2] >> 16 : w[j / 2] & 0xFFFFu);
+        }
+}
 
 // Two 16-bit elements of a word, exact.
 template <int DT> __device__ __forceinline__ float2 unpack2(uint32_t w)
@@ -229,38 +251,37 @@ template <int DT> __device__ __forceinline__ float2 unpack2(uint32_t w)
     else return make_float2(Scalar<DT>::get(static_cast<uint16_t>(w & 0xFFFFu)), Scalar<DT>::get(static_cast<uint16_t>(w >> 16)));
 }
 
-// A thread's share of gamma or beta over all rows, as raw 32-bit words (two 16-bit elements each).
-template <int DT, int E, bool VEC> struct Held {
-    using D = Deal<DT, E, VEC>;
+// A thread's share of gamma over all rows, as raw 32-bit words (two 16-bit elements each).
+template <int DT, int E, bool EDGE> struct Held {
+    using D = Deal<DT, E>;
     using T = typename Scalar<DT>::T;
     static constexpr int PER = 4 / sizeof(T), N = E / PER;
     uint32_t w[N];
 
-    __device__ __forceinline__ void load(const T* p, int t, int threads, int len)     // p may be null: zeros
+    // Column k is p[k - lo] in columns lo to hi, 0 elsewhere.
+    __device__ __forceinline__ void load(const T* p, int t, int threads, int lo, int hi)
     {
-        if constexpr (VEC) {
 #pragma unroll
-            for (int c = 0; c < D::NC; ++c) {
-                const int k = D::col(c, t, threads);
-                const uint4 v = p != nullptr && k < len ? ld_v4(p + k) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < D::NC; ++c) {
+            const int k = D::col(c, t, threads);
+            if constexpr (!EDGE) {
+                const uint4 v = k < hi ? ld_v4(p + k) : make_uint4(0, 0, 0, 0);
                 w[4 * c] = v.x;
                 w[4 * c + 1] = v.y;
                 w[4 * c + 2] = v.z;
                 w[4 * c + 3] = v.w;
-            }
-        } else {
+            } else {
 #pragma unroll
-            for (int e = 0; e < E; e += PER) {
-                uint32_t v = 0;
+                for (int j = 0; j < D::VW; j += PER) {
+                    uint32_t v = 0;
 #pragma unroll
-                for (int j = 0; j < PER; ++j) {
-                    const int k = D::col(e + j, t, threads);
-                    if (p != nullptr && k < len) {
-                        if constexpr (PER == 1) v = __float_as_uint(p[k]);
-                        else v |= static_cast<uint32_t>(p[k]) << (16 * j);
-                    }
+                    for (int q = 0; q < PER; ++q)
+                        if (k + j + q >= lo && k + j + q < hi) {
+                            if constexpr (PER == 1) v = __float_as_uint(p[k + j - lo]);
+                            else v |= static_cast<uint32_t>(p[k + j + q - lo]) << (16 * q);
+                        }
+                    w[(c * D::VW + j) / PER] = v;
                 }
-                w[e / PER] = v;
             }
         }
     }
@@ -277,43 +298,39 @@ template <int DT, int E, bool VEC> struct Held {
     }
 };
 
-// int8 codes of values already scaled to [-127, 127]: adding 1.5 * 2^23 rounds to nearest even
-// and leaves the code in the low byte.
-__device__ __forceinline__ uint32_t code_bits(float v) { return __float_as_uint(__fadd_rn(v, 12582912.0f)); }
-
-__device__ __forceinline__ uint32_t pack_codes(float a, float b, float c, float d)
-{
-    const uint32_t lo = __byte_perm(code_bits(a), code_bits(b), 0x0040);
-    const uint32_t hi = __byte_perm(code_bits(c), code_bits(d), 0x0040);
-    return __byte_perm(lo, hi, 0x5410);
-}
-
-// A thread's share of a row (in whole vectors) as int8 codes of y * 127 / amax. 127 / amax overflows for
+// A thread's share of a row, columns lo to hi, as int8 codes of y * 127 / amax. 127 / amax overflows for
 // rows of tiny y: those are scaled up by 2^100 first (exact).
-template <int DT, int E, bool FULL>
-__device__ __forceinline__ void store_codes(float2 (&v)[E / 2], float amax, signed char* o, int t, int T, int len)
+template <int DT, int E, bool FULL, bool EDGE>
+__device__ __forceinline__ void store_codes(float2 (&v)[E / 2], float amax, signed char* o, int t, int T, int lo, int hi)
 {
-    using D = Deal<DT, E, true>;
-    constexpr int PV = D::VW / 2;
+    using D = Deal<DT, E>;
+    constexpr int PV = D::PV, VW = D::VW;
     const float pre = amax < 1e-30f ? 0x1p100f : 1.0f;
     const float2 inv = splat(amax > 0.f ? __fdiv_rn(127.0f, amax * pre) : 0.f);
     if (pre != 1.0f) {
 #pragma unroll
         for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], splat(pre));
     }
-    const float2 magic = splat(12582912.0f);      // code_bits of pairs
+    // adding 1.5 * 2^23 rounds to nearest even and leaves the code in the low byte
+    const float2 magic = splat(12582912.0f);
 #pragma unroll
     for (int c = 0; c < D::NC; ++c) {
         const int k = D::col(c, t, T);
-        if (FULL || k < len) {
+        if (FULL || k < hi) {
             uint32_t h[PV];
 #pragma unroll
             for (int j = 0; j < PV; ++j) {
                 const float2 q = add2(mul2(v[c * PV + j], inv), magic);
                 h[j] = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x0040);
             }
-            if constexpr (PV == 4) st_v2(o + k, __byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
-            else st_u32(o + k, __byte_perm(h[0], h[1], 0x5410));
+            if (!EDGE || (k >= lo && k + VW <= hi)) {
+                if constexpr (PV == 4) st_v2(o + k, __byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
+                else st_u32(o + k, __byte_perm(h[0], h[1], 0x5410));
+            } else {
+#pragma unroll
+                for (int j = 0; j < VW; ++j)
+                    if (k + j >= lo && k + j < hi) o[k + j] = static_cast<signed char>(h[j / 2] >> (8 * (j & 1)) & 0xFFu);
+            }
         }
     }
 }
@@ -330,12 +347,12 @@ __device__ __forceinline__ void store_codes(float2 (&v)[E / 2], float amax, sign
 template <int DT, int E, bool FULL, int SCOPE, int KIND>
 __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOPE_WARP ? 4 : 2) rmsq_norm_direct_kernel(const __grid_constant__ NormParams p)
 {
-    using D = Deal<DT, E, true>;
+    using D = Deal<DT, E>;
     using S = Scalar<DT>;
     using TT = typename S::T;
     constexpr bool RMS = KIND == NORM_RMS_INT8;
     constexpr bool INT8 = KIND != NORM_LAYER;
-    constexpr int VW = D::VW, NC = D::NC, PV = VW / 2;
+    constexpr int NC = D::NC, PV = D::PV;
     __shared__ float2 part[16];
     __shared__ float part_max[16];
 
@@ -381,7 +398,7 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
     }
 
     // ---- mean and squares about it ----
-    const int n_w = FULL ? 32 * E : D::count(SCOPE == SCOPE_WARP ? 0 : warp * 32, T, len);
+    const int n_w = FULL ? 32 * E : D::count(SCOPE == SCOPE_WARP ? 0 : warp * 32, T, 0, len);
     float sum = 0.f, m2, mean = 0.f;
     if constexpr (!RMS) {
         float2 a = v[0];
@@ -414,7 +431,7 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
         if constexpr (!RMS) {
             mean = warp_sum(q.x) * inv_h;
             if (lane < nwarps) {
-                n_l = FULL ? static_cast<float>(32 * E) : static_cast<float>(D::count(lane * 32, T, len));
+                n_l = FULL ? static_cast<float>(32 * E) : static_cast<float>(D::count(lane * 32, T, 0, len));
                 d = FULL ? q.x * (1.0f / (32 * E)) - mean : n_l > 0.f ? __fdividef(q.x, n_l) - mean : 0.f;
             }
         }
@@ -461,7 +478,7 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
             __syncthreads();
             amax = warp_max(lane < nwarps ? part_max[lane] : 0.f);
         }
-        store_codes<DT, E, FULL>(v, amax, static_cast<signed char*>(p.out) + at, t, T, len);
+        store_codes<DT, E, FULL, false>(v, amax, static_cast<signed char*>(p.out) + at, t, T, 0, len);
         if (leader) p.scale[row] = amax / 127.0f;
     } else if (leader) {
         if (p.mean) p.mean[row] = mean;
@@ -475,66 +492,79 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
 
 constexpr int kRingStages = 8;      // slots per group at most
 constexpr int kRingGroups = 16;     // row groups per CTA at most
+// The rows a group works on: `first`, and every `stride`-th from there. Group g of cluster c starts at
+// row g * clusters + c; the host makes the number of clusters a multiple of the rows after which the shift
+// repeats (or gives every group one row at most), so a CTA's rows have one shift.
+struct Rows {
+    int first, stride, n;
+    __device__ __forceinline__ Rows(int group, int groups, int rows)
+    {
+        const int clusters = static_cast<int>(cluster_count());
+        first = group * clusters + static_cast<int>(cluster_id());
+        stride = clusters * groups;
+        n = first < rows ? (rows - first + stride - 1) / stride : 0;
+    }
+};
+
 constexpr int kRingBars = 2 * kRingStages * kRingGroups * 8;      // bytes of barriers
 
-// A row group's ring of slots: its next rows, brought by bulk copies while the group works. Rows that
-// do not start on 16-byte boundaries (VEC false) are copied from the boundary below; the tensors' last
-// bytes, which no whole 16-byte piece covers, are read directly.
-template <int DT, bool VEC> struct RowRing {
+// A row group's ring of slots: its next rows, brought by bulk copies while the group works. EDGE: rows of
+// a width that is no whole number of vectors, taken from the 16-byte boundary below. The group's rows all
+// have the same shift (Rows). The tensors' last bytes, which no whole 16-byte piece covers, are read
+// directly.
+template <int DT, bool EDGE> struct RowRing {
     using S = Scalar<DT>;
     using T = typename S::T;
-    static constexpr int ES = sizeof(T), VW = VEC ? Elem<DT>::EPV : 1;
+    static constexpr int ES = sizeof(T), VW = Elem<DT>::EPV;
     const RowTensors& r;
-    int c0, len;                   // the CTA's slice of a row
+    int c0;                        // the CTA's first column
+    int lo, hi;                    // its columns that are the row's, from c0 on
+    int shift;                     // of the rows
     uint32_t bars, base;           // shared addresses of the group's barriers (kRingStages full, as many
                                    // empty) and slots
     __device__ __forceinline__ uint32_t full(int stage) const { return bars + 8 * stage; }
     __device__ __forceinline__ uint32_t empty(int stage) const { return bars + 8 * (kRingStages + stage); }
 
     __device__ __forceinline__ uint32_t at(uint32_t stage, int i) const { return base + (stage * r.ntens + i) * r.slot; }
-    // Byte of the row's slice in a tensor.
-    __device__ __forceinline__ long long byte(int row) const { return (static_cast<long long>(row) * r.hidden + c0) * ES; }
+    // Where the CTA's first column of a row is in a tensor, in elements (whole vectors).
+    __device__ __forceinline__ long long origin(int row) const { return static_cast<long long>(row) * r.hidden - shift + c0; }
 
     // One row's pieces of every tensor into a slot (one thread).
     __device__ __forceinline__ void fetch(int row, uint32_t stage, uint64_t policy) const
     {
-        const long long b0 = byte(row), a0 = b0 & ~15LL;
-        long long a1 = (b0 + static_cast<long long>(len) * ES + 15) & ~15LL;
-        if (a1 > (r.total & ~15LL)) a1 = r.total & ~15LL;
-        const uint32_t bytes = len > 0 && a1 > a0 ? static_cast<uint32_t>(a1 - a0) : 0u;
+        const long long a0 = origin(row) * ES;
+        long long a1 = a0 + (hi + VW - 1) / VW * 16;
+        if (EDGE && a1 > (r.total & ~15LL)) a1 = r.total & ~15LL;
+        const uint32_t bytes = hi > lo && a1 > a0 ? static_cast<uint32_t>(a1 - a0) : 0u;
         mbar_arrive_expect_tx(full(stage), bytes * r.ntens);
         if (bytes > 0)
             for (int i = 0; i < r.ntens; ++i)
                 bulk_load(at(stage, i), static_cast<const unsigned char*>(r.in[i]) + a0, bytes, full(stage), policy);
     }
 
-    // Vector (element, where VEC is false) k of tensor i of the row in a slot, as raw bits.
-    __device__ __forceinline__ uint4 vec(uint32_t stage, int i, int k) const { return ld_shared_v4(at(stage, i) + k * ES); }
-    // Rows off 16-byte boundaries: the slice's first byte in tensor i's part of a slot, and how many of its
-    // elements the copies brought (all, but in the tensors' last row). Elements from there on are read
-    // from the tensor.
-    __device__ __forceinline__ uint32_t start(uint32_t stage, int i, int row) const
+    // How many columns of a row's slot the copies can have brought.
+    __device__ __forceinline__ int brought(int row) const
     {
-        return at(stage, i) + static_cast<uint32_t>(byte(row) & 15);
+        if (!EDGE) return hi;
+        const long long n = (r.total & ~15LL) / ES - origin(row);
+        return n < hi + VW ? static_cast<int>(n) : hi + VW;
     }
-    __device__ __forceinline__ int have(int row) const
+    // The vector at column k of tensor i, as raw bits; what is not the row's is not cleared.
+    __device__ __forceinline__ uint4 vec(uint32_t stage, int i, int row, int k, int brought) const
     {
-        const long long n = ((r.total & ~15LL) - byte(row)) / ES;
-        return n < len ? static_cast<int>(n) : len;
+        if (!EDGE || k + VW <= brought) return ld_shared_v4(at(stage, i) + k * ES);
+        const T* const p = static_cast<const T*>(r.in[i]) + origin(row) + k;
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+            if (k + j < hi) {
+                if constexpr (ES == 4) w[j] = __float_as_uint(p[j]);
+                else w[j / 2] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+            }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    static __device__ __forceinline__ T elem(uint32_t start, int k)
-    {
-        T v;
-        if constexpr (ES == 2) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(start + k * ES));
-        else asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(start + k * ES));
-        return v;
-    }
-    __device__ __forceinline__ T tail(int i, int row, int k) const { return static_cast<const T*>(r.in[i])[byte(row) / ES + k]; }
-    // Element k of tensor i, 0 outside the slice.
-    __device__ __forceinline__ T element(uint32_t start, int i, int row, int k, int have) const
-    {
-        return k < have ? elem(start, k) : k < len ? tail(i, row, k) : T(0);
-    }
+    // Whether the vector at column k is the row's as a whole.
+    __device__ __forceinline__ bool whole(int k) const { return !EDGE || (k >= lo && k + VW <= hi); }
     // One thread sets the barriers up: a slot is empty when `warps` warps have left it.
     __device__ __forceinline__ void init(int warps) const
     {
@@ -543,24 +573,24 @@ template <int DT, bool VEC> struct RowRing {
             mbar_init(empty(i), warps);
         }
     }
-    // Brings the group's n rows, first + i * stride (one thread of the CTA's copying warp: issuing a row's
+    // Brings the group's rows (one thread of the CTA's copying warp: issuing a row's
     // copies takes about 1000 cycles, which a working warp would keep its group waiting for). After a
     // wait that ran out, waits (bounded) for the copies in flight, so that they end before the CTA does.
-    __device__ __forceinline__ void feed(int first, int stride, int n, unsigned long long timeout_ns, unsigned int* err) const
+    __device__ __forceinline__ void feed(const Rows& rows, unsigned long long timeout_ns, unsigned int* err) const
     {
         const uint64_t policy = l2_evict_normal_policy();
         const uint32_t limit = wait_limit(timeout_ns);
         int stage = 0, phase = 1, i = 0;
-        for (; i < n; ++i) {
+        for (; i < rows.n; ++i) {
             if (!mbar_wait<SCOPE_CTA>(empty(stage), phase, limit)) break;
             fence_proxy_async_smem();
-            fetch(first + i * stride, stage, policy);
+            fetch(rows.first + i * rows.stride, stage, policy);
             if (++stage == r.stages) {
                 stage = 0;
                 phase ^= 1;
             }
         }
-        if (i < n) {
+        if (i < rows.n) {
             bool drained = true;
             for (int j = i > r.stages ? i - r.stages : 0; j < i; ++j)
                 drained &= mbar_wait<SCOPE_CTA>(full(j % r.stages), (j / r.stages) & 1, wait_limit(4 * timeout_ns));
@@ -622,15 +652,15 @@ constexpr int kRingWorkers = 256;             // threads that work on rows; a wa
 // two rows in turn: one barrier a row then keeps a row's from the next but one's), the cluster's sums.
 constexpr int kNormHead = (kRingBars + 2 * 8 * 8 + 2 * 8 * 4 + 2 * ClusterSums::BYTES + 127) / 128 * 128;
 
-template <int DT, int E, bool VEC, bool FULL, int SCOPE, int KIND>
-__global__ void __launch_bounds__(kRingWorkers + 32, VEC ? 3 : 2) rmsq_norm_ring_kernel(const __grid_constant__ NormParams p)
+template <int DT, int E, bool EDGE, bool FULL, int SCOPE, int KIND>
+__global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(const __grid_constant__ NormParams p)
 {
-    using D = Deal<DT, E, VEC>;
+    using D = Deal<DT, E>;
     using S = Scalar<DT>;
     using TT = typename S::T;
     constexpr bool RMS = KIND == NORM_RMS_INT8;
     constexpr bool INT8 = KIND != NORM_LAYER;
-    constexpr int VW = D::VW, NC = D::NC, PV = VEC ? VW / 2 : 1;
+    constexpr int VW = D::VW, NC = D::NC, PV = D::PV;
     extern __shared__ __align__(128) unsigned char smem[];
 
     float2* const part = reinterpret_cast<float2*>(smem + kRingBars);
@@ -645,21 +675,19 @@ __global__ void __launch_bounds__(kRingWorkers + 32, VEC ? 3 : 2) rmsq_norm_ring
     const int nc = SCOPE == SCOPE_CLUSTER ? static_cast<int>(cluster_size()) : 1;
     const int rank = SCOPE == SCOPE_CLUSTER ? static_cast<int>(cluster_rank()) : 0;
 
-    const int c0 = rank * p.r.slice, left = p.r.hidden - c0;
-    const int len = FULL ? p.r.slice : left < 0 ? 0 : left < p.r.slice ? left : p.r.slice;
-    const auto in = [&](int k) { return FULL || k < len; };
-    // a warp's lanes of the copying warp stand for the groups they feed
+    // a lane of the copying warp stands for the group it feeds
     const bool copies = threadIdx.x >= T * groups;
     const int mine = copies ? (lane < groups ? lane : 0) : group;
-    const RowRing<DT, VEC> ring{p.r, c0, len, smem_u32(smem) + mine * 2 * kRingStages * 8,
-                                smem_u32(smem + kNormHead) + (2 + mine * p.r.stages * p.r.ntens) * p.r.slot};
+    const Rows rows(mine, groups, p.r.rows);
+    const int c0 = rank * p.r.slice;
+    const int shift = EDGE ? static_cast<int>(static_cast<long long>(rows.first) * p.r.hidden % VW) : 0;
+    const int lo = max(shift - c0, 0), hi = FULL ? p.r.slice : max(min(shift + p.r.hidden - c0, p.r.slice), 0);
+    const auto in = [&](int k) { return FULL || k < hi; };
+    const RowRing<DT, EDGE> ring{p.r, c0, lo, hi, shift, smem_u32(smem) + mine * 2 * kRingStages * 8,
+                                 smem_u32(smem + kNormHead) + (2 + mine * p.r.stages * p.r.ntens) * p.r.slot};
     const ClusterSums sums{smem_u32(cluster_part), smem_u32(cluster_part + 16), nc, rank};
     const ClusterSums maxima{sums.bars + ClusterSums::BYTES, sums.slots + ClusterSums::BYTES, nc, rank};
 
-    // this group's rows: every groups-th of the CTA's rows_per_cta * groups
-    const int first = static_cast<int>(SCOPE == SCOPE_CLUSTER ? cluster_id() : blockIdx.x) * p.rows_per_group * groups + mine;
-    int n = first < p.r.rows ? (p.r.rows - first + groups - 1) / groups : 0;
-    if (n > p.rows_per_group) n = p.rows_per_group;
     const bool has_res = p.r.ntens == 2;
 
     if (copies && lane < groups) {
@@ -675,7 +703,7 @@ __global__ void __launch_bounds__(kRingWorkers + 32, VEC ? 3 : 2) rmsq_norm_ring
     if constexpr (SCOPE == SCOPE_CLUSTER) cluster_sync();        // the other CTAs' barriers are set up
     pdl_wait();
     if (copies) {
-        if (lane < groups) ring.feed(first, groups, n, p.timeout_ns, p.err);
+        if (lane < groups) ring.feed(rows, p.timeout_ns, p.err);
         return;
     }
 
@@ -683,16 +711,18 @@ __global__ void __launch_bounds__(kRingWorkers + 32, VEC ? 3 : 2) rmsq_norm_ring
     TT* const ws = reinterpret_cast<TT*>(smem + kNormHead);
     TT* const bs = reinterpret_cast<TT*>(smem + kNormHead + p.r.slot);
     const int workers = T * groups;
-    if constexpr (VEC) {
+    const TT* const gamma = static_cast<const TT*>(p.gamma) + (c0 - shift);
+    const TT* const beta = p.beta != nullptr ? static_cast<const TT*>(p.beta) + (c0 - shift) : nullptr;
+    if constexpr (!EDGE) {
         const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int k = threadIdx.x * VW; k < len; k += workers * VW) {
-            st_shared_v4(smem_u32(ws + k), ld_v4(static_cast<const TT*>(p.gamma) + c0 + k));
-            st_shared_v4(smem_u32(bs + k), p.beta != nullptr ? ld_v4(static_cast<const TT*>(p.beta) + c0 + k) : zero);
+        for (int k = threadIdx.x * VW; k < hi; k += workers * VW) {
+            st_shared_v4(smem_u32(ws + k), ld_v4(gamma + k));
+            st_shared_v4(smem_u32(bs + k), beta != nullptr ? ld_v4(beta + k) : zero);
         }
     } else {
 #pragma unroll 4
-        for (int k = threadIdx.x; k < len; k += workers) {
-            const TT w = static_cast<const TT*>(p.gamma)[c0 + k], b = p.beta != nullptr ? static_cast<const TT*>(p.beta)[c0 + k] : TT(0);
+        for (int k = lo + threadIdx.x; k < hi; k += workers) {
+            const TT w = gamma[k], b = beta != nullptr ? beta[k] : TT(0);
             ws[k] = w;
             bs[k] = b;
         }
@@ -703,56 +733,46 @@ __global__ void __launch_bounds__(kRingWorkers + 32, VEC ? 3 : 2) rmsq_norm_ring
     // CTA's of the cluster. A count that is not a power of two makes a mean off by half a step more.
     const uint32_t limit = wait_limit(p.timeout_ns);
     const auto inverse = [](int k) { return k > 0 ? 1.0f / static_cast<float>(k) : 0.f; };
-    const int n_w = FULL ? 32 * E : D::count((warp - warp0) * 32, T, len);
-    const int n_l = lane >= group_warps ? 0 : FULL ? 32 * E : D::count(lane * 32, T, len);
-    const int n_r = SCOPE == SCOPE_CLUSTER && lane < nc ? min(max(p.r.hidden - lane * p.r.slice, 0), p.r.slice) : 0;
-    const float inv_w = inverse(n_w), inv_l = inverse(n_l), inv_c = inverse(len), inv_r = inverse(n_r);
+    const int n_w = FULL ? 32 * E : D::count((warp - warp0) * 32, T, lo, hi);
+    const int n_l = lane >= group_warps ? 0 : FULL ? 32 * E : D::count(lane * 32, T, lo, hi);
+    const int n_r = SCOPE == SCOPE_CLUSTER && lane < nc
+                        ? max(min(shift + p.r.hidden - lane * p.r.slice, p.r.slice), 0) - (lane == 0 ? shift : 0) : 0;
+    const float inv_w = inverse(n_w), inv_l = inverse(n_l), inv_c = inverse(hi - lo), inv_r = inverse(n_r);
     const float inv_h = 1.0f / static_cast<float>(p.r.hidden), f_l = static_cast<float>(n_l), f_r = static_cast<float>(n_r);
     bool dead = false;                            // a wait ran out: finish without waiting again
     int stage = 0, phase = 0;
     int flip = 0;
-    for (int i = 0; i < n; ++i) {
+    for (int i = 0; i < rows.n; ++i) {
         // made opaque to the compiler again and again, which would keep every element's address and test
         // in registers from row to row and from phase to phase
         int t = thread;
         asm volatile("" : "+r"(t));
-        const int row = first + i * groups;
+        const int row = rows.first + i * rows.stride;
         if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage), phase, limit)) dead = true;
-        const long long at = static_cast<long long>(row) * p.r.hidden + c0;
+        const long long at = ring.origin(row);
 
         // ---- s into registers, fp32 (exact), 0 outside the slice ----
         float2 v[E / 2];
-        if constexpr (VEC) {
+        {
+            const int brought = ring.brought(row);
+            TT* const ro = static_cast<TT*>(p.res_out) + at;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int k = D::col(c, t, T);
                 uint4 raw = make_uint4(0, 0, 0, 0);
                 if (in(k)) {
-                    raw = ring.vec(stage, 0, k);
+                    raw = ring.vec(stage, 0, row, k, brought);
                     if (has_res) {
-                        raw = Elem<DT>::add(raw, ring.vec(stage, 1, k));
-                        st_v4(static_cast<TT*>(p.res_out) + at + k, raw);
+                        raw = Elem<DT>::add(raw, ring.vec(stage, 1, row, k, brought));
+                        if (ring.whole(k)) st_v4(ro + k, raw);
+                        else store_inside<DT>(ro, raw, k, lo, hi);
                     }
                 }
                 float2 f[PV];
                 Elem<DT>::pairs(raw, f);
+                if (!ring.whole(k)) clear_outside(f, k, lo, hi);
 #pragma unroll
                 for (int j = 0; j < PV; ++j) v[c * PV + j] = f[j];
-            }
-        } else {
-            const int have = ring.have(row);
-            const uint32_t x0 = ring.start(stage, 0, row), r0 = ring.start(stage, 1, row);
-            TT* const ro = static_cast<TT*>(p.res_out) + at;
-#pragma unroll
-            for (int c = 0; c < E; ++c) {
-                const int k = D::col(c, t, T);
-                TT raw = ring.element(x0, 0, row, k, have);
-                if (has_res) {
-                    raw = S::add(raw, ring.element(r0, 1, row, k, have));
-                    if (k < len) ro[k] = raw;
-                }
-                if (c & 1) v[c / 2].y = S::get(raw);
-                else v[c / 2].x = S::get(raw);
             }
         }
 
@@ -770,11 +790,16 @@ __global__ void __launch_bounds__(kRingWorkers + 32, VEC ? 3 : 2) rmsq_norm_ring
             const float2 m = splat(-mean);
             float2 a = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int j = 0; j < E / 2; ++j) {
-                float2 d = add2(v[j], m);
-                if (!in(D::col(2 * j / VW, t, T))) d.x = 0.f;
-                if (!in(D::col((2 * j + 1) / VW, t, T))) d.y = 0.f;
-                a = fma2(d, d, a);
+            for (int c = 0; c < NC; ++c) {
+                const int k = D::col(c, t, T);
+                if (in(k)) {
+                    float2 d[PV];
+#pragma unroll
+                    for (int j = 0; j < PV; ++j) d[j] = add2(v[c * PV + j], m);
+                    if (!ring.whole(k)) clear_outside(d, k, lo, hi);
+#pragma unroll
+                    for (int j = 0; j < PV; ++j) a = fma2(d[j], d[j], a);
+                }
             }
             m2 = warp_sum(a.x + a.y);
         }
@@ -810,42 +835,33 @@ __global__ void __launch_bounds__(kRingWorkers + 32, VEC ? 3 : 2) rmsq_norm_ring
         float amax = 0.f;
         TT* const o = static_cast<TT*>(p.out) + at;
 #pragma unroll
-        for (int c = 0; c < E / 2 / PV; ++c) {
-            const int k0 = D::col(VEC ? c : 2 * c, t, T), k1 = VEC ? k0 : D::col(2 * c + 1, t, T);
-            float2 w[PV], b[PV];
-            if constexpr (VEC) {
-                if (in(k0)) {
-                    Elem<DT>::pairs(ld_shared_v4(smem_u32(ws + k0)), w);
-                    Elem<DT>::pairs(ld_shared_v4(smem_u32(bs + k0)), b);
-                }
-            } else {
-                // outside the slice: any element of it, whose result is not used
-                const int j0 = k0 < len ? k0 : 0, j1 = k1 < len ? k1 : 0;
-                w[0] = make_float2(S::get(ws[j0]), S::get(ws[j1]));
-                b[0] = make_float2(S::get(bs[j0]), S::get(bs[j1]));
-            }
-            if (p.offset != 0.f) {
+        for (int c = 0; c < NC; ++c) {
+            const int k = D::col(c, t, T);
+            if (in(k)) {
+                float2 w[PV], b[PV];
+                Elem<DT>::pairs(ld_shared_v4(smem_u32(ws + k)), w);
+                Elem<DT>::pairs(ld_shared_v4(smem_u32(bs + k)), b);
+                if (p.offset != 0.f) {
 #pragma unroll
-                for (int j = 0; j < PV; ++j) w[j] = add2(w[j], splat(p.offset));
-            }
-            if (in(k0)) {
+                    for (int j = 0; j < PV; ++j) w[j] = add2(w[j], splat(p.offset));
+                }
+                float2 y[PV];
 #pragma unroll
                 for (int j = 0; j < PV; ++j) {
-                    float2& y = v[c * PV + j];
-                    if constexpr (RMS) y = mul2(mul2(y, r2), w[j]);
-                    else y = fma2(mul2(add2(y, m), r2), w[j], b[j]);
-                    if constexpr (INT8) {
-                        amax = fmaxf(amax, fabsf(y.x));
-                        if (in(k1)) amax = fmaxf(amax, fabsf(y.y));
-                    }
+                    if constexpr (RMS) y[j] = mul2(mul2(v[c * PV + j], r2), w[j]);
+                    else y[j] = fma2(mul2(add2(v[c * PV + j], m), r2), w[j], b[j]);
                 }
-            }
-            if constexpr (!INT8) {
-                if constexpr (VEC) {
-                    if (in(k0)) st_v4(o + k0, pack_pairs<DT>(&v[c * PV]));
+                if constexpr (INT8) {
+                    if (!ring.whole(k)) clear_outside(y, k, lo, hi);
+#pragma unroll
+                    for (int j = 0; j < PV; ++j) {
+                        amax = max3(amax, fabsf(y[j].x), fabsf(y[j].y));
+                        v[c * PV + j] = y[j];
+                    }
                 } else {
-                    if (k0 < len) o[k0] = S::put(v[c].x);
-                    if (k1 < len) o[k1] = S::put(v[c].y);
+                    const uint4 raw = pack_pairs<DT>(y);
+                    if (ring.whole(k)) st_v4(o + k, raw);
+                    else store_inside<DT>(o, raw, k, lo, hi);
                 }
             }
         }
@@ -865,16 +881,7 @@ __global__ void __launch_bounds__(kRingWorkers + 32, VEC ? 3 : 2) rmsq_norm_ring
             }
             asm volatile("" : "+r"(t));
             signed char* const codes = static_cast<signed char*>(p.out) + at;
-            if constexpr (VEC) {
-                store_codes<DT, E, FULL>(v, amax, codes, t, T, len);
-            } else {
-                const float pre = amax < 1e-30f ? 0x1p100f : 1.0f, inv = amax > 0.f ? __fdiv_rn(127.0f, amax * pre) : 0.f;
-#pragma unroll
-                for (int c = 0; c < E; ++c) {
-                    const int k = D::col(c, t, T);
-                    if (k < len) codes[k] = static_cast<signed char>(code_bits((c & 1 ? v[c / 2].y : v[c / 2].x) * pre * inv) & 0xFFu);
-                }
-            }
+            store_codes<DT, E, FULL, EDGE>(v, amax, codes, t, T, lo, hi);
             if (leader) p.scale[row] = amax / 127.0f;
         } else if (leader) {
             if (p.mean) p.mean[row] = mean;

@@ -4,16 +4,16 @@
 
 namespace rmsq {
 
-template <int DT, bool VEC> static const void* pick(int elems)
+template <int DT, bool EDGE> static const void* pick(int elems)
 {
-    return elems == 8 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 8, VEC>)
-         : elems == 16 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 16, VEC>)
-                       : reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 24, VEC>);
+    return elems == 8 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 8, EDGE>)
+         : elems == 16 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 16, EDGE>)
+                       : reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 24, EDGE>);
 }
 
 template <int DT> static const void* pick(int elems, bool vec)
 {
-    return vec ? pick<DT, true>(elems) : pick<DT, false>(elems);
+    return vec ? pick<DT, false>(elems) : pick<DT, true>(elems);
 }
 
 const void* norm_bwd_fn(int dt, int elems, bool vec)

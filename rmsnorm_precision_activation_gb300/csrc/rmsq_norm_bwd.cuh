@@ -44,21 +44,21 @@ struct NormBwdReduceParams {
     int dt;                  // type of dgamma and dbeta
 };
 
-// Shared memory before the ring: barriers, the groups' warp sums (of two iterations in turn), the
-// cluster's sums.
 // Elements of a row per thread: 8, 16 or 24, and the warps of a CTA that work on rows then (one more
 // copies). Registers are dealt to a quarter of the SM's warps each: 16 warps get 128, 12 get 168.
 constexpr int row_warps(int elems) { return elems <= 16 ? 15 : 11; }
 
+// Shared memory before the ring: barriers, the groups' warp sums (of two iterations in turn), the
+// cluster's sums.
 constexpr int kBwdHead = (kRingBars + 2 * 16 * 16 + ClusterSums::BYTES + 127) / 128 * 128;
 
-template <int DT, int E, bool VEC>
+template <int DT, int E, bool EDGE>
 __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
 {
-    using D = Deal<DT, E, VEC>;
+    using D = Deal<DT, E>;
     using S = Scalar<DT>;
     using TT = typename S::T;
-    constexpr int VW = D::VW, NC = D::NC;
+    constexpr int VW = D::VW, NC = D::NC, PV = D::PV;
     extern __shared__ __align__(128) unsigned char smem[];
 
     float4* const red = reinterpret_cast<float4*>(smem + kRingBars);
@@ -69,19 +69,17 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     const int group_warps = T >> 5, warp0 = group * group_warps;
     const int nc = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
 
-    const int c0 = rank * p.r.slice, left = p.r.hidden - c0;
-    const int len = left < 0 ? 0 : left < p.r.slice ? left : p.r.slice;
     // a lane of the copying warp stands for the group it feeds
     const bool copies = threadIdx.x >= T * p.groups;
     const int mine = copies ? (lane < p.groups ? lane : 0) : group;
-    const RowRing<DT, VEC> ring{p.r, c0, len, smem_u32(smem) + mine * 2 * kRingStages * 8,
-                                smem_u32(smem + kBwdHead) + mine * p.r.stages * p.r.ntens * p.r.slot};
+    const Rows rows(mine, p.groups, p.r.rows);
+    const int c0 = rank * p.r.slice;
+    const int shift = EDGE ? static_cast<int>(static_cast<long long>(rows.first) * p.r.hidden % VW) : 0;
+    const int lo = max(shift - c0, 0), hi = max(min(shift + p.r.hidden - c0, p.r.slice), 0);
+    const RowRing<DT, EDGE> ring{p.r, c0, lo, hi, shift, smem_u32(smem) + mine * 2 * kRingStages * 8,
+                                 smem_u32(smem + kBwdHead) + mine * p.r.stages * p.r.ntens * p.r.slot};
     const ClusterSums sums{smem_u32(cluster_part), smem_u32(cluster_part + 16), nc, rank};
     const bool has_res = p.r.ntens == 3;
-
-    const int first = static_cast<int>(cluster_id()) * p.groups + mine;
-    const int stride = static_cast<int>(cluster_count()) * p.groups;
-    const int n = first < p.r.rows ? (p.r.rows - first + stride - 1) / stride : 0;      // this group's rows
 
     if (copies && lane < p.groups) {
         ring.init(group_warps);
@@ -93,14 +91,14 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     if (nc > 1) cluster_sync();                   // the other CTAs' barriers are set up
     pdl_wait();
     if (copies) {
-        if (lane < p.groups) ring.feed(first, stride, n, p.timeout_ns, p.err);
+        if (lane < p.groups) ring.feed(rows, p.timeout_ns, p.err);
         return;
     }
     const int workers = T * p.groups;
 
     float2 acc_g[E / 2], acc_b[E / 2];
-    Held<DT, E, VEC> w;                           // gamma, in its own type
-    w.load(static_cast<const TT*>(p.gamma) + c0, thread, T, len);
+    Held<DT, E, EDGE> w;                          // gamma, in its own type
+    w.load(static_cast<const TT*>(p.gamma) + (c0 + lo - shift), thread, T, lo, hi);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) acc_g[e] = acc_b[e] = make_float2(0.f, 0.f);
 
@@ -109,53 +107,44 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     bool dead = false;                            // a wait ran out: finish without waiting again
     int stage = 0, phase = 0;
     int flip = 0;
-    // Elements 2 j and 2 j + 1 of the thread's share of tensor i, or all of its vector c (0 outside the slice).
-    auto load = [&](int t, int slot, int i, int row, int have, int c, float2* f) {
-        if constexpr (VEC) {
-            const int k = D::col(c, t, T);
-            float2 g[VW / 2];
-            Elem<DT>::pairs(k < len ? ring.vec(slot, i, k) : make_uint4(0, 0, 0, 0), g);
-#pragma unroll
-            for (int j = 0; j < VW / 2; ++j) f[j] = g[j];
-        } else {
-            const uint32_t s0 = ring.start(slot, i, row);
-            f[0].x = S::get(ring.element(s0, i, row, D::col(2 * c, t, T), have));
-            f[0].y = S::get(ring.element(s0, i, row, D::col(2 * c + 1, t, T), have));
-        }
+    // The vector at column k of tensor i, 0 outside the row.
+    auto load = [&](int slot, int i, int row, int k, int brought, float2 (&f)[PV]) {
+        Elem<DT>::pairs(k < hi ? ring.vec(slot, i, row, k, brought) : make_uint4(0, 0, 0, 0), f);
+        if (!ring.whole(k)) clear_outside(f, k, lo, hi);
     };
-    constexpr int PAIRS = VEC ? VW / 2 : 1, CHUNKS = E / 2 / PAIRS;
     const float2 offset = splat(p.offset);
     // Two rows at a time, so that one barrier and one round of shuffles serve both. Every CTA of a
     // cluster, and every thread of a group, runs the same iterations.
-    for (int i = 0; i < n; i += 2) {
+    for (int i = 0; i < rows.n; i += 2) {
         // opaque to the compiler, which would keep every element's address in registers across rows
         int t = thread;
         asm volatile("" : "+r"(t));
-        const int pair = n - i < 2 ? 1 : 2;
+        const int pair = rows.n - i < 2 ? 1 : 2;
         w.pin();
         float mean[2], rstd[2], s1[2] = {0.f, 0.f}, s2[2] = {0.f, 0.f};
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int row = first + (i + (r < pair ? r : 0)) * stride;
+            const int row = rows.first + (i + (r < pair ? r : 0)) * rows.stride;
             mean[r] = p.mean[row];
             rstd[r] = p.rstd[row];
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             if (r < pair) {
-                const int row = first + (i + r) * stride;
+                const int row = rows.first + (i + r) * rows.stride;
                 if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage + r), phase, limit)) dead = true;
-                const int have = VEC ? len : ring.have(row);
+                const int brought = ring.brought(row);
                 const float2 m = splat(-mean[r]), rs = splat(rstd[r]);
                 float2 a1 = make_float2(0.f, 0.f), a2 = a1;
 #pragma unroll
-                for (int c = 0; c < CHUNKS; ++c) {
-                    float2 dy[PAIRS], s[PAIRS];
-                    load(t, stage + r, 0, row, have, c, dy);
-                    load(t, stage + r, 1, row, have, c, s);
+                for (int c = 0; c < NC; ++c) {
+                    const int k = D::col(c, t, T);
+                    float2 dy[PV], s[PV];
+                    load(stage + r, 0, row, k, brought, dy);
+                    load(stage + r, 1, row, k, brought, s);
 #pragma unroll
-                    for (int j = 0; j < PAIRS; ++j) {
-                        const int e = c * PAIRS + j;
+                    for (int j = 0; j < PV; ++j) {
+                        const int e = c * PV + j;
                         const float2 xh = mul2(add2(s[j], m), rs), g = mul2(dy[j], add2(w.pair(e), offset));
                         a1 = add2(a1, g);
                         a2 = fma2(g, xh, a2);
@@ -193,34 +182,32 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             if (r < pair) {
-                const int row = first + (i + r) * stride;
-                const int have = VEC ? len : ring.have(row);
+                const int row = rows.first + (i + r) * rows.stride;
+                const int brought = ring.brought(row);
                 const float m1 = s1[r] * inv_h, m2 = s2[r] * inv_h;
-                TT* const out = static_cast<TT*>(p.ds) + static_cast<long long>(row) * p.r.hidden + c0;
+                TT* const out = static_cast<TT*>(p.ds) + ring.origin(row);
                 const float2 m = splat(-mean[r]), rs = splat(rstd[r]), n1 = splat(-m1), n2 = splat(-m2);
 #pragma unroll
-                for (int c = 0; c < CHUNKS; ++c) {
-                    float2 dy[PAIRS], s[PAIRS], d[PAIRS];
-                    load(t, stage + r, 0, row, have, c, dy);
-                    load(t, stage + r, 1, row, have, c, s);
-                    if (has_res) {
-                        load(t, stage + r, 2, row, have, c, d);
-                    } else {
+                for (int c = 0; c < NC; ++c) {
+                    const int k = D::col(c, t, T);
+                    if (k < hi) {
+                        float2 dy[PV], s[PV], d[PV];
+                        load(stage + r, 0, row, k, brought, dy);
+                        load(stage + r, 1, row, k, brought, s);
+                        if (has_res) {
+                            load(stage + r, 2, row, k, brought, d);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < PAIRS; ++j) d[j] = make_float2(0.f, 0.f);
-                    }
+                            for (int j = 0; j < PV; ++j) d[j] = make_float2(0.f, 0.f);
+                        }
 #pragma unroll
-                    for (int j = 0; j < PAIRS; ++j) {
-                        const float2 xh = mul2(add2(s[j], m), rs), g = mul2(dy[j], add2(w.pair(c * PAIRS + j), offset));
-                        d[j] = fma2(rs, fma2(xh, n2, add2(g, n1)), d[j]);
-                    }
-                    if constexpr (VEC) {
-                        const int k = D::col(c, t, T);
-                        if (k < len) st_v4(out + k, pack_pairs<DT>(d));
-                    } else {
-                        const int k0 = D::col(2 * c, t, T), k1 = D::col(2 * c + 1, t, T);
-                        if (k0 < len) out[k0] = S::put(d[0].x);
-                        if (k1 < len) out[k1] = S::put(d[0].y);
+                        for (int j = 0; j < PV; ++j) {
+                            const float2 xh = mul2(add2(s[j], m), rs), g = mul2(dy[j], add2(w.pair(c * PV + j), offset));
+                            d[j] = fma2(rs, fma2(xh, n2, add2(g, n1)), d[j]);
+                        }
+                        const uint4 raw = pack_pairs<DT>(d);
+                        if (ring.whole(k)) st_v4(out + k, raw);
+                        else store_inside<DT>(out, raw, k, lo, hi);
                     }
                 }
             }
@@ -244,42 +231,35 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     const auto acc = [](const float2* a, int e) { return e & 1 ? a[e / 2].y : a[e / 2].x; };
     // ---- partial rows: the groups' sums in group order, through the ring's memory ----
     workers_sync();
-    float* const part = p.part + static_cast<long long>(cluster_id()) * 2 * p.r.hidden + c0;
-    if (p.groups == 1) {
+    float* const part = p.part + static_cast<long long>(cluster_id()) * 2 * p.r.hidden + (c0 + lo - shift);
+    float* const sum = reinterpret_cast<float*>(smem + kBwdHead);
+    for (int g = 0; g < p.groups; ++g) {
+        if (g == group) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int k = D::col(c, thread, T);
+            for (int c = 0; c < NC; ++c) {
+                const int k = D::col(c, thread, T);
 #pragma unroll
-            for (int j = 0; j < VW; ++j)
-                if (k < len) {
-                    part[k + j] = acc(acc_g, c * VW + j);
-                    part[p.r.hidden + k + j] = acc(acc_b, c * VW + j);
-                }
-        }
-    } else {
-        float* const sum = reinterpret_cast<float*>(smem + kBwdHead);
-        for (int g = 0; g < p.groups; ++g) {
-            if (g == group) {
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int k = D::col(c, thread, T);
-#pragma unroll
-                    for (int j = 0; j < VW; ++j)
-                        if (k < len) {
-                            float& a = sum[k + j];
-                            float& b = sum[len + k + j];
-                            a = (g == 0 ? 0.f : a) + acc(acc_g, c * VW + j);
-                            b = (g == 0 ? 0.f : b) + acc(acc_b, c * VW + j);
+                for (int j = 0; j < VW; ++j)
+                    if (k + j >= lo && k + j < hi) {
+                        const int e = k + j - lo;
+                        const float a = acc(acc_g, c * VW + j), b = acc(acc_b, c * VW + j);
+                        if (p.groups == 1) {
+                            part[e] = a;
+                            part[p.r.hidden + e] = b;
+                        } else {
+                            sum[e] = (g == 0 ? 0.f : sum[e]) + a;
+                            sum[p.r.slice + e] = (g == 0 ? 0.f : sum[p.r.slice + e]) + b;
                         }
-                }
+                    }
             }
-            workers_sync();
         }
-        for (int k = threadIdx.x; k < len; k += workers) {
-            part[k] = sum[k];
-            part[p.r.hidden + k] = sum[len + k];
-        }
+        if (p.groups > 1) workers_sync();
     }
+    if (p.groups > 1)
+        for (int k = threadIdx.x; k < hi - lo; k += workers) {
+            part[k] = sum[k];
+            part[p.r.hidden + k] = sum[p.r.slice + k];
+        }
     if (nc > 1) cluster_sync();                   // nobody sends to a CTA that has left
 }
 

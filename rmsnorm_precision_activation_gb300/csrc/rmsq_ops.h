@@ -27,7 +27,7 @@ cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem,
 
 struct NormPlan {
     int dt;
-    int elems;      // per thread: 8, 16 (direct only) or 32
+    int elems;      // per thread: 8, 16 (direct only), 32 or 40 (the widest rows)
     bool vec;
     bool direct;    // rows straight into registers
     bool full;      // the threads' shares cover the row exactly
@@ -49,16 +49,18 @@ const void* norm_bwd_fn(int dt, int elems, bool vec);
 const void* norm_bwd_reduce_fn();
 
 #define RMSQ_DEFINE_NORM_DISPATCH(NAME, KIND)                                                     \
-    template <int DT, bool VEC, bool FULL> static const void* NAME##_ring(const NormPlan& pl)     \
+    template <int DT, bool EDGE, bool FULL> static const void* NAME##_ring(const NormPlan& pl)    \
     {                                                                                             \
-        if (pl.scope == SCOPE_CLUSTER)                                                            \
-            return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, VEC, FULL, SCOPE_CLUSTER, KIND>); \
-        if constexpr (!VEC) {                                                                     \
+        if (pl.scope == SCOPE_CLUSTER && pl.elems == 32)                                          \
+            return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, EDGE, FULL, SCOPE_CLUSTER, KIND>); \
+        if constexpr (EDGE) {                                                                     \
+            if (pl.scope == SCOPE_CLUSTER && pl.elems == 40)                                      \
+                return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 40, EDGE, FULL, SCOPE_CLUSTER, KIND>); \
             if (pl.scope == SCOPE_CTA)                                                            \
-                return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, VEC, FULL, SCOPE_CTA, KIND>); \
+                return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, EDGE, FULL, SCOPE_CTA, KIND>); \
             if (pl.elems == 8)                                                                    \
-                return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 8, VEC, FULL, SCOPE_WARP, KIND>); \
-            return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, VEC, FULL, SCOPE_WARP, KIND>); \
+                return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 8, EDGE, FULL, SCOPE_WARP, KIND>); \
+            return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, EDGE, FULL, SCOPE_WARP, KIND>); \
         }                                                                                         \
         return nullptr;                                                                           \
     }                                                                                             \
@@ -75,8 +77,8 @@ const void* norm_bwd_reduce_fn();
     template <int DT> static const void* NAME##_fn(const NormPlan& pl)                            \
     {                                                                                             \
         if (pl.direct) return pl.full ? NAME##_direct<DT, true>(pl) : NAME##_direct<DT, false>(pl); \
-        if (!pl.vec) return NAME##_ring<DT, false, false>(pl);                                    \
-        return pl.full ? NAME##_ring<DT, true, true>(pl) : NAME##_ring<DT, true, false>(pl);      \
+        if (!pl.vec) return NAME##_ring<DT, true, false>(pl);                                     \
+        return pl.full ? NAME##_ring<DT, false, true>(pl) : NAME##_ring<DT, false, false>(pl);    \
     }                                                                                             \
     cudaError_t NAME(const NormPlan& pl, const NormParams& p, cudaStream_t stream)                \
     {                                                                                             \

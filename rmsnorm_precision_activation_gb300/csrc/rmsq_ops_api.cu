@@ -37,25 +37,26 @@ static rmsq_status status_of(cudaError_t e)
 // groups, of which it takes no more than give every SM a row.
 struct RowGeometry {
     int cluster, slice, elems, T, groups, slot;
-    bool vec;
+    int period;      // rows after which the shift off 16-byte boundaries repeats
 };
 
 static RowGeometry row_geometry(int64_t rows, int hidden, int dtype, int sms, int (*elems)(int), int (*workers)(int))
 {
-    const int es = elem_bytes(dtype), per16 = 16 / es;
+    const int es = elem_bytes(dtype), vw = 16 / es;
     RowGeometry g;
-    g.vec = hidden % per16 == 0;
+    g.period = 1;
+    while (static_cast<long long>(g.period) * hidden % vw != 0) ++g.period;
+    const int columns = g.period == 1 ? hidden : hidden + vw - 1;
     g.cluster = 1;
-    while (static_cast<long long>(g.cluster) * (kRingSlice / es) < hidden) g.cluster *= 2;
-    const int vec = g.vec ? per16 : 1;
-    g.slice = ((hidden + g.cluster - 1) / g.cluster + vec - 1) / vec * vec;
+    // (16 slices of the widest rows off 16-byte boundaries are one vector more)
+    while (g.cluster < 16 && static_cast<long long>(g.cluster) * (kRingSlice / es) < columns) g.cluster *= 2;
+    g.slice = ((columns + g.cluster - 1) / g.cluster + vw - 1) / vw * vw;
     g.elems = elems(g.slice);
     g.T = ((g.slice + g.elems - 1) / g.elems + 31) / 32 * 32;
     g.groups = g.cluster > 1 ? 1 : workers(g.elems) / g.T;
     const int64_t spread = (rows + sms - 1) / sms;
     if (g.groups > spread) g.groups = static_cast<int>(spread);
-    // rows off 16-byte boundaries are copied from the boundary below
-    g.slot = g.vec ? g.slice * es : (g.slice * es + 30) / 16 * 16;
+    g.slot = g.slice * es;
     return g;
 }
 
@@ -79,9 +80,9 @@ static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormPara
         pl.grid = static_cast<unsigned>(pl.scope == SCOPE_WARP ? (rows + 7) / 8 : rows);
         return status_of(go(pl, p, stream));
     }
-    const RowGeometry g = row_geometry(rows, hidden, dtype, dv.sms, [](int slice) { return slice <= 256 ? 8 : 32; },
+    const RowGeometry g = row_geometry(rows, hidden, dtype, dv.sms, [](int slice) { return slice <= 256 ? 8 : slice <= kRingWorkers * 32 ? 32 : 40; },
                                        [](int) { return kRingWorkers; });
-    pl.vec = g.vec;
+    pl.vec = g.period == 1;
     pl.cluster = g.cluster;
     pl.elems = g.elems;
     pl.scope = g.cluster > 1 ? SCOPE_CLUSTER : g.T > 32 ? SCOPE_CTA : SCOPE_WARP;
@@ -98,21 +99,25 @@ static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormPara
     const int64_t stage = static_cast<int64_t>(g.slot) * p.r.ntens * g.groups, head = kNormHead + 2 * g.slot;
     const auto slots = [&](int ctas) { return (dv.smem_optin / ctas - 1024 - head) / stage; };
     static const int env_r = getenv("RMSQ_R") ? atoi(getenv("RMSQ_R")) : 0, env_s = getenv("RMSQ_S") ? atoi(getenv("RMSQ_S")) : 0, env_c = getenv("RMSQ_C") ? atoi(getenv("RMSQ_C")) : 0;
-    int ctas = env_c ? env_c : (pl.vec ? 27 : 20) * 32 / pl.threads;
+    int ctas = env_c ? env_c : 27 * 32 / pl.threads;
     while (ctas > 1 && slots(ctas) < 2) --ctas;
     int64_t stages = slots(ctas);
     if (stages < 1) return RMSQ_ERR_LAUNCH;
     if (stages > kRingStages) stages = kRingStages;
     if (env_s) stages = env_s;
-    // rows per group: about four CTAs in turn on every place an SM has for one
+    // About four CTAs in turn on every place an SM has for one, but 8 rows each where that leaves a CTA to
+    // every place; a CTA's rows all have one shift.
     const int64_t places = static_cast<int64_t>(dv.sms) * ctas / pl.cluster * p.groups;
-    int64_t per = env_r ? env_r : rows / (places * 4);
-    p.rows_per_group = static_cast<int>(per < 1 ? 1 : per > 64 ? 64 : per);
-    if (stages > p.rows_per_group) stages = p.rows_per_group;
+    int64_t per = rows / (places * 4), most = rows / places < 8 ? rows / places : 8;
+    if (per < most) per = most;
+    if (per < 1) per = 1;
+    if (env_r) per = env_r;
+    if (stages > per) stages = per;
     p.r.stages = static_cast<int>(stages);
     pl.smem = static_cast<int>(head + stages * stage);
-    const int64_t per_cta = static_cast<int64_t>(p.rows_per_group) * p.groups;
-    pl.grid = static_cast<unsigned>((rows + per_cta - 1) / per_cta * pl.cluster);
+    int64_t clusters = (rows + per * p.groups - 1) / (per * p.groups);
+    if (per > 1 || p.groups > 1) clusters = (clusters + g.period - 1) / g.period * g.period;
+    pl.grid = static_cast<unsigned>(clusters * pl.cluster);
     return status_of(go(pl, p, stream));
 }
 
@@ -301,15 +306,22 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         const int64_t stage = static_cast<int64_t>(p.r.slot) * p.r.ntens * p.groups;
         int64_t ring = p.r.stages * stage;
         if (p.groups > 1 && ring < 8LL * p.r.slice) ring = 8LL * p.r.slice;   // the groups' sums
+        // one partial row per cluster; where a group has several rows or a CTA several groups, as many
+        // clusters as make a CTA's rows have one shift
+        const int64_t most = bwd_parts(rows), resident = dv.sms / cluster;
         int64_t parts = (rows + p.groups - 1) / p.groups;
-        const int64_t resident = dv.sms / cluster;
         if (parts > resident) parts = resident;
-        if (parts > bwd_parts(rows)) parts = bwd_parts(rows);
+        if (parts > most) parts = most;
+        if (parts * p.groups < rows || p.groups > 1) {
+            if (parts >= g.period) parts = parts / g.period * g.period;
+            else parts = g.period;
+            if (parts > most) return RMSQ_ERR_LAUNCH;      // a device of fewer SMs than the period needs
+        }
         if (parts < 1) return RMSQ_ERR_LAUNCH;
         r.parts = static_cast<int>(parts);
         void* args[] = {&p};
         const rmsq_status e = status_of(launch_kernel(
-            norm_bwd_fn(dtype, g.elems, g.vec), static_cast<unsigned>(parts * cluster),
+            norm_bwd_fn(dtype, g.elems, g.period == 1), static_cast<unsigned>(parts * cluster),
             static_cast<unsigned>(p.T * p.groups + 32), static_cast<int>(kBwdHead + ring), cluster, st, args));
         if (e != RMSQ_OK) return e;
     }
