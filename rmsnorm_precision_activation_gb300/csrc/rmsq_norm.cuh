@@ -13,12 +13,11 @@
 // which costs one block barrier instead of two.
 //
 // Bound by HBM. Two kernels:
-//  - rmsq_norm_direct_kernel, rows in whole vectors of up to 16384 elements: straight into registers, each
-//    row by a warp or CTA of its own.
-//  - rmsq_norm_ring_kernel, other widths: rows off 16-byte boundaries, whose direct loads of one element
-//    each reached 0.14 of the copy rate (bf16, 5121 wide), and rows split over a cluster, where gamma and
-//    beta would be read anew with every row. CTAs take several rows, which come through a ring of
-//    shared-memory slots filled by bulk copies, and keep gamma and beta in shared memory.
+//  - rmsq_norm_direct_kernel, rows of up to 16384 columns: straight into registers, each row by a warp or
+//    CTA of its own.
+//  - rmsq_norm_ring_kernel, wider rows: split over a cluster, whose CTAs would read gamma and beta anew with
+//    every row. They take several rows, which come through a ring of shared-memory slots filled by bulk
+//    copies, and keep gamma and beta in shared memory.
 #pragma once
 
 #include "rmsq_device.cuh"
@@ -50,7 +49,6 @@ struct NormParams {
     float* mean;           // or null
     float* rstd;           // or null
     int T;                 // threads per row group
-    int groups;            // row groups per CTA
     float eps;
     float offset;
     unsigned int* err;
@@ -339,12 +337,94 @@ __device__ __forceinline__ void store_codes(float2 (&v)[E / 2], float amax, sign
 // Rows straight into registers
 // ------------------------------------------------------------------------------------------
 
-// A warp (SCOPE_WARP, rows of up to 1024 elements) or a CTA (up to 16384, 32 elements a thread) per row, for
-// rows in whole vectors. FULL: the threads' shares cover the row exactly, so nothing is checked.
+// The vector at column k of a tensor's row, which starts at element at (the row's columns lo to hi);
+// what is not the row's is not cleared. The last vector can reach past the tensor's `total` elements.
+template <int DT, bool EDGE>
+__device__ __forceinline__ uint4 load_columns(const typename Scalar<DT>::T* p, long long at, long long total, int k, int hi)
+{
+    if (!EDGE || at + k + Elem<DT>::EPV <= total) return ld_stream_v4(reinterpret_cast<const uint4*>(p + at + k));
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < Elem<DT>::EPV; ++j)
+        if (k + j < hi) {
+            if constexpr (DT == DT_F32) w[j] = __float_as_uint(p[at + k + j]);
+            else w[j / 2] |= static_cast<uint32_t>(p[at + k + j]) << (16 * (j & 1));
+        }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// gamma's or beta's elements for the vector at column k of a row with the given shift: elements k - shift
+// on, taken out of the two aligned vectors they lie in (shift is the same for the whole row, so its
+// branches are uniform). Elements outside 0 to hidden are any value.
+template <int DT, bool EDGE>
+__device__ __forceinline__ uint4 load_param(const typename Scalar<DT>::T* p, int k, int shift, int hidden)
+{
+    constexpr int VW = Elem<DT>::EPV;
+    if constexpr (!EDGE) {
+        return ld_v4(p + k);
+    } else {
+        uint32_t w[9];
+        w[8] = 0;
+        const uint4 lower = shift > 0 && k >= VW ? ld_v4(p + k - VW) : make_uint4(0, 0, 0, 0);
+        w[0] = lower.x;
+        w[1] = lower.y;
+        w[2] = lower.z;
+        w[3] = lower.w;
+        if (k + VW <= hidden) {
+            const uint4 upper = ld_v4(p + k);
+            w[4] = upper.x;
+            w[5] = upper.y;
+            w[6] = upper.z;
+            w[7] = upper.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[4 + j] = 0;
+#pragma unroll
+            for (int j = 0; j < VW; ++j)
+                if (k + j < hidden) {
+                    if constexpr (DT == DT_F32) w[4 + j] = __float_as_uint(p[k + j]);
+                    else w[4 + j / 2] |= static_cast<uint32_t>(p[k + j]) << (16 * (j & 1));
+                }
+        }
+        // the vector starts (VW - shift) elements into lower, upper: words first, then half a word
+        const int words = DT == DT_F32 ? 4 - shift : 4 - (shift + 1) / 2;
+        uint32_t v[5];
+        switch (words) {
+        case 0:
+#pragma unroll
+            for (int j = 0; j < 5; ++j) v[j] = w[j];
+            break;
+        case 1:
+#pragma unroll
+            for (int j = 0; j < 5; ++j) v[j] = w[j + 1];
+            break;
+        case 2:
+#pragma unroll
+            for (int j = 0; j < 5; ++j) v[j] = w[j + 2];
+            break;
+        case 3:
+#pragma unroll
+            for (int j = 0; j < 5; ++j) v[j] = w[j + 3];
+            break;
+        default:
+#pragma unroll
+            for (int j = 0; j < 5; ++j) v[j] = w[j + 4];
+        }
+        if (DT != DT_F32 && (shift & 1)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = __funnelshift_r(v[j], v[j + 1], 16);
+        }
+        return make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
+
+// A warp (SCOPE_WARP, rows of up to 1024 columns) or a CTA (up to 16384, 32 elements a thread) per row.
+// FULL: the threads' shares cover the row exactly, so nothing is checked. EDGE: rows whose width is no
+// whole number of vectors.
 // Every row has its own thread group and no loop: the hardware's CTA scheduler overlaps rows and evens
 // out SMs of unequal bandwidth. Bound by HBM with a residual and by instructions without one: 32
 // elements a thread halve what a row costs in reductions against 16.
-template <int DT, int E, bool FULL, int SCOPE, int KIND>
+template <int DT, int E, bool FULL, bool EDGE, int SCOPE, int KIND>
 __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOPE_WARP ? 4 : 2) rmsq_norm_direct_kernel(const __grid_constant__ NormParams p)
 {
     using D = Deal<DT, E>;
@@ -352,7 +432,7 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
     using TT = typename S::T;
     constexpr bool RMS = KIND == NORM_RMS_INT8;
     constexpr bool INT8 = KIND != NORM_LAYER;
-    constexpr int NC = D::NC, PV = D::PV;
+    constexpr int NC = D::NC, PV = D::PV, VW = D::VW;
     __shared__ float2 part[16];
     __shared__ float part_max[16];
 
@@ -360,45 +440,53 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
     const int T = SCOPE == SCOPE_WARP ? 32 : blockDim.x;
     const int t = SCOPE == SCOPE_WARP ? lane : threadIdx.x;
     const int nwarps = SCOPE == SCOPE_WARP ? 1 : blockDim.x >> 5;
-    const int len = p.r.hidden;
     const int row = SCOPE == SCOPE_WARP ? static_cast<int>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
     pdl_wait();
     if (SCOPE == SCOPE_WARP && row >= p.r.rows) return;
 
-    const long long at = static_cast<long long>(row) * len;
-    const auto in = [&](int c) { return FULL || D::col(c, t, T) < len; };
+    const int shift = EDGE ? static_cast<int>(static_cast<long long>(row) * p.r.hidden % VW) : 0;
+    const int lo = shift, hi = shift + p.r.hidden;
+    const long long at = static_cast<long long>(row) * p.r.hidden - shift;      // of column 0
+    const long long total = static_cast<long long>(p.r.rows) * p.r.hidden;
+    const auto in = [&](int c) { return FULL || D::col(c, t, T) < hi; };
+    const auto whole = [&](int k) { return !EDGE || (k >= lo && k + VW <= hi); };
 
     // ---- s into registers, fp32 (exact), 0 outside the row ----
     float2 v[E / 2];
     {
-        const TT* const x = static_cast<const TT*>(p.r.in[0]) + at;
         const uint4 zero = make_uint4(0, 0, 0, 0);
         uint4 raw[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c) raw[c] = in(c) ? ld_stream_v4(reinterpret_cast<const uint4*>(x + D::col(c, t, T))) : zero;
+        for (int c = 0; c < NC; ++c)
+            raw[c] = in(c) ? load_columns<DT, EDGE>(static_cast<const TT*>(p.r.in[0]), at, total, D::col(c, t, T), hi) : zero;
         if (p.r.ntens == 2) {
-            const TT* const r = static_cast<const TT*>(p.r.in[1]) + at;
             TT* const ro = static_cast<TT*>(p.res_out) + at;
             uint4 add[NC];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) add[c] = in(c) ? ld_stream_v4(reinterpret_cast<const uint4*>(r + D::col(c, t, T))) : zero;
+            for (int c = 0; c < NC; ++c)
+                add[c] = in(c) ? load_columns<DT, EDGE>(static_cast<const TT*>(p.r.in[1]), at, total, D::col(c, t, T), hi) : zero;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
+                const int k = D::col(c, t, T);
                 raw[c] = Elem<DT>::add(raw[c], add[c]);
-                if (in(c)) st_v4(ro + D::col(c, t, T), raw[c]);
+                if (in(c)) {
+                    if (whole(k)) st_v4(ro + k, raw[c]);
+                    else store_inside<DT>(ro, raw[c], k, lo, hi);
+                }
             }
         }
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             float2 f[PV];
             Elem<DT>::pairs(raw[c], f);
+            if (!whole(D::col(c, t, T))) clear_outside(f, D::col(c, t, T), lo, hi);
 #pragma unroll
             for (int j = 0; j < PV; ++j) v[c * PV + j] = f[j];
         }
     }
 
     // ---- mean and squares about it ----
-    const int n_w = FULL ? 32 * E : D::count(SCOPE == SCOPE_WARP ? 0 : warp * 32, T, 0, len);
+    const int n_w = FULL ? 32 * E : D::count(SCOPE == SCOPE_WARP ? 0 : warp * 32, T, lo, hi);
     float sum = 0.f, m2, mean = 0.f;
     if constexpr (!RMS) {
         float2 a = v[0];
@@ -413,16 +501,17 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             if (in(c)) {
+                float2 d[PV];
 #pragma unroll
-                for (int j = 0; j < PV; ++j) {
-                    const float2 d = add2(v[c * PV + j], m);
-                    a = fma2(d, d, a);
-                }
+                for (int j = 0; j < PV; ++j) d[j] = add2(v[c * PV + j], m);
+                if (!whole(D::col(c, t, T))) clear_outside(d, D::col(c, t, T), lo, hi);
+#pragma unroll
+                for (int j = 0; j < PV; ++j) a = fma2(d[j], d[j], a);
             }
         }
         m2 = warp_sum(a.x + a.y);
     }
-    const float inv_h = __frcp_rn(static_cast<float>(len));
+    const float inv_h = __frcp_rn(static_cast<float>(p.r.hidden));
     if constexpr (SCOPE != SCOPE_WARP) {
         if (lane == 0) part[warp] = make_float2(sum, m2);
         __syncthreads();
@@ -431,7 +520,7 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
         if constexpr (!RMS) {
             mean = warp_sum(q.x) * inv_h;
             if (lane < nwarps) {
-                n_l = FULL ? static_cast<float>(32 * E) : static_cast<float>(D::count(lane * 32, T, 0, len));
+                n_l = FULL ? static_cast<float>(32 * E) : static_cast<float>(D::count(lane * 32, T, lo, hi));
                 d = FULL ? q.x * (1.0f / (32 * E)) - mean : n_l > 0.f ? __fdividef(q.x, n_l) - mean : 0.f;
             }
         }
@@ -449,25 +538,36 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
         if (in(c)) {
             const int k = D::col(c, t, T);
             float2 w[PV], b[PV];
-            Elem<DT>::pairs(ld_v4(gamma + k), w);
+            Elem<DT>::pairs(load_param<DT, EDGE>(gamma, k, shift, p.r.hidden), w);
             if (p.offset != 0.f) {
 #pragma unroll
                 for (int j = 0; j < PV; ++j) w[j] = add2(w[j], offset);
             }
             if (!RMS && beta != nullptr) {
-                Elem<DT>::pairs(ld_v4(beta + k), b);
+                Elem<DT>::pairs(load_param<DT, EDGE>(beta, k, shift, p.r.hidden), b);
             } else {
 #pragma unroll
                 for (int j = 0; j < PV; ++j) b[j] = make_float2(0.f, 0.f);
             }
+            float2 y[PV];
 #pragma unroll
             for (int j = 0; j < PV; ++j) {
-                float2& y = v[c * PV + j];
-                if constexpr (RMS) y = mul2(mul2(y, r2), w[j]);
-                else y = fma2(mul2(add2(y, m), r2), w[j], b[j]);
-                if constexpr (INT8) amax = max3(amax, fabsf(y.x), fabsf(y.y));
+                if constexpr (RMS) y[j] = mul2(mul2(v[c * PV + j], r2), w[j]);
+                else y[j] = fma2(mul2(add2(v[c * PV + j], m), r2), w[j], b[j]);
             }
-            if constexpr (!INT8) st_v4(static_cast<TT*>(p.out) + at + k, pack_pairs<DT>(&v[c * PV]));
+            if constexpr (INT8) {
+                if (!whole(k)) clear_outside(y, k, lo, hi);
+#pragma unroll
+                for (int j = 0; j < PV; ++j) {
+                    amax = max3(amax, fabsf(y[j].x), fabsf(y[j].y));
+                    v[c * PV + j] = y[j];
+                }
+            } else {
+                TT* const o = static_cast<TT*>(p.out) + at;
+                const uint4 raw = pack_pairs<DT>(y);
+                if (whole(k)) st_v4(o + k, raw);
+                else store_inside<DT>(o, raw, k, lo, hi);
+            }
         }
     }
     const bool leader = t == 0;
@@ -478,7 +578,7 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
             __syncthreads();
             amax = warp_max(lane < nwarps ? part_max[lane] : 0.f);
         }
-        store_codes<DT, E, FULL, false>(v, amax, static_cast<signed char*>(p.out) + at, t, T, 0, len);
+        store_codes<DT, E, FULL, EDGE>(v, amax, static_cast<signed char*>(p.out) + at, t, T, lo, hi);
         if (leader) p.scale[row] = amax / 127.0f;
     } else if (leader) {
         if (p.mean) p.mean[row] = mean;
@@ -652,7 +752,7 @@ constexpr int kRingWorkers = 256;             // threads that work on rows; a wa
 // two rows in turn: one barrier a row then keeps a row's from the next but one's), the cluster's sums.
 constexpr int kNormHead = (kRingBars + 2 * 8 * 8 + 2 * 8 * 4 + 2 * ClusterSums::BYTES + 127) / 128 * 128;
 
-template <int DT, int E, bool EDGE, bool FULL, int SCOPE, int KIND>
+template <int DT, int E, bool EDGE, bool FULL, int KIND>
 __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(const __grid_constant__ NormParams p)
 {
     using D = Deal<DT, E>;
@@ -667,75 +767,66 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
     float* const part_max = reinterpret_cast<float*>(part + 16);
     unsigned char* const cluster_part = reinterpret_cast<unsigned char*>(part_max + 16);
 
-    const int T = SCOPE == SCOPE_WARP ? 32 : p.T;
-    const int group = SCOPE == SCOPE_CLUSTER ? 0 : threadIdx.x / T, groups = p.groups;
-    const int thread = threadIdx.x - group * T;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int group_warps = T >> 5, warp0 = group * group_warps;
-    const int nc = SCOPE == SCOPE_CLUSTER ? static_cast<int>(cluster_size()) : 1;
-    const int rank = SCOPE == SCOPE_CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+    const int T = p.T, thread = threadIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = T >> 5;
+    const int nc = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
 
-    // a lane of the copying warp stands for the group it feeds
-    const bool copies = threadIdx.x >= T * groups;
-    const int mine = copies ? (lane < groups ? lane : 0) : group;
-    const Rows rows(mine, groups, p.r.rows);
+    const bool copies = threadIdx.x >= T;
+    const Rows rows(0, 1, p.r.rows);
     const int c0 = rank * p.r.slice;
     const int shift = EDGE ? static_cast<int>(static_cast<long long>(rows.first) * p.r.hidden % VW) : 0;
     const int lo = max(shift - c0, 0), hi = FULL ? p.r.slice : max(min(shift + p.r.hidden - c0, p.r.slice), 0);
     const auto in = [&](int k) { return FULL || k < hi; };
-    const RowRing<DT, EDGE> ring{p.r, c0, lo, hi, shift, smem_u32(smem) + mine * 2 * kRingStages * 8,
-                                 smem_u32(smem + kNormHead) + (2 + mine * p.r.stages * p.r.ntens) * p.r.slot};
+    const RowRing<DT, EDGE> ring{p.r, c0, lo, hi, shift, smem_u32(smem),
+                                 smem_u32(smem + kNormHead) + 2 * p.r.slot};
     const ClusterSums sums{smem_u32(cluster_part), smem_u32(cluster_part + 16), nc, rank};
     const ClusterSums maxima{sums.bars + ClusterSums::BYTES, sums.slots + ClusterSums::BYTES, nc, rank};
 
     const bool has_res = p.r.ntens == 2;
 
-    if (copies && lane < groups) {
-        ring.init(group_warps);
-        if (SCOPE == SCOPE_CLUSTER) {
-            sums.init();
-            maxima.init();
-        }
+    if (copies && lane == 0) {
+        ring.init(warps);
+        sums.init();
+        maxima.init();
         fence_mbar_init();
         fence_proxy_async_smem();
     }
     __syncthreads();
-    if constexpr (SCOPE == SCOPE_CLUSTER) cluster_sync();        // the other CTAs' barriers are set up
+    cluster_sync();                               // the other CTAs' barriers are set up
     pdl_wait();
     if (copies) {
-        if (lane < groups) ring.feed(rows, p.timeout_ns, p.err);
+        if (lane == 0) ring.feed(rows, p.timeout_ns, p.err);
         return;
     }
 
     // gamma and beta of the slice stay in shared memory, in their own type
     TT* const ws = reinterpret_cast<TT*>(smem + kNormHead);
     TT* const bs = reinterpret_cast<TT*>(smem + kNormHead + p.r.slot);
-    const int workers = T * groups;
     const TT* const gamma = static_cast<const TT*>(p.gamma) + (c0 - shift);
     const TT* const beta = p.beta != nullptr ? static_cast<const TT*>(p.beta) + (c0 - shift) : nullptr;
     if constexpr (!EDGE) {
         const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int k = threadIdx.x * VW; k < hi; k += workers * VW) {
+        for (int k = threadIdx.x * VW; k < hi; k += T * VW) {
             st_shared_v4(smem_u32(ws + k), ld_v4(gamma + k));
             st_shared_v4(smem_u32(bs + k), beta != nullptr ? ld_v4(beta + k) : zero);
         }
     } else {
 #pragma unroll 4
-        for (int k = lo + threadIdx.x; k < hi; k += workers) {
+        for (int k = lo + threadIdx.x; k < hi; k += T) {
             const TT w = gamma[k], b = beta != nullptr ? beta[k] : TT(0);
             ws[k] = w;
             bs[k] = b;
         }
     }
-    asm volatile("bar.sync 15, %0;" ::"r"(workers) : "memory");
+    asm volatile("bar.sync 15, %0;" ::"r"(T) : "memory");
 
     // Counts of elements and their reciprocals: this warp's, lane's warp's of the group, the CTA's, lane's
     // CTA's of the cluster. A count that is not a power of two makes a mean off by half a step more.
     const uint32_t limit = wait_limit(p.timeout_ns);
     const auto inverse = [](int k) { return k > 0 ? 1.0f / static_cast<float>(k) : 0.f; };
-    const int n_w = FULL ? 32 * E : D::count((warp - warp0) * 32, T, lo, hi);
-    const int n_l = lane >= group_warps ? 0 : FULL ? 32 * E : D::count(lane * 32, T, lo, hi);
-    const int n_r = SCOPE == SCOPE_CLUSTER && lane < nc
+    const int n_w = FULL ? 32 * E : D::count(warp * 32, T, lo, hi);
+    const int n_l = lane >= warps ? 0 : FULL ? 32 * E : D::count(lane * 32, T, lo, hi);
+    const int n_r = lane < nc
                         ? max(min(shift + p.r.hidden - lane * p.r.slice, p.r.slice), 0) - (lane == 0 ? shift : 0) : 0;
     const float inv_w = inverse(n_w), inv_l = inverse(n_l), inv_c = inverse(hi - lo), inv_r = inverse(n_r);
     const float inv_h = 1.0f / static_cast<float>(p.r.hidden), f_l = static_cast<float>(n_l), f_r = static_cast<float>(n_r);
@@ -804,10 +895,10 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
             m2 = warp_sum(a.x + a.y);
         }
         if (lane == 0) mbar_arrive(ring.empty(stage));       // the warp has read the slot
-        if constexpr (SCOPE != SCOPE_WARP) {
+        {
             if (lane == 0) part[flip * 8 + warp] = make_float2(sum, m2);
-            group_sync(group, T);
-            const float2 q = lane < group_warps ? part[flip * 8 + warp0 + lane] : make_float2(0.f, 0.f);
+            group_sync(0, T);
+            const float2 q = lane < warps ? part[flip * 8 + lane] : make_float2(0.f, 0.f);
             float d = 0.f;
             if constexpr (!RMS) {
                 sum = warp_sum(q.x);
@@ -816,7 +907,7 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
             }
             m2 = warp_sum(fmaf(f_l * d, d, q.y));
         }
-        if constexpr (SCOPE == SCOPE_CLUSTER) {
+        {
             float4 q;
             if (warp == 0) sums.send(lane, flip, make_float4(sum, m2, 0.f, 0.f));
             if (!sums.receive(lane, flip, (i >> 1) & 1, dead ? 0 : limit, q)) dead = true;
@@ -868,12 +959,12 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
         const bool leader = t == 0 && rank == 0;
         if constexpr (INT8) {
             amax = warp_max(amax);
-            if constexpr (SCOPE != SCOPE_WARP) {
+            {
                 if (lane == 0) part_max[flip * 8 + warp] = amax;
-                group_sync(group, T);
-                amax = warp_max(lane < group_warps ? part_max[flip * 8 + warp0 + lane] : 0.f);
+                group_sync(0, T);
+                amax = warp_max(lane < warps ? part_max[flip * 8 + lane] : 0.f);
             }
-            if constexpr (SCOPE == SCOPE_CLUSTER) {
+            {
                 float4 q;
                 if (warp == 0) maxima.send(lane, flip, make_float4(amax, 0.f, 0.f, 0.f));
                 if (!maxima.receive(lane, flip, (i >> 1) & 1, dead ? 0 : limit, q)) dead = true;
@@ -894,7 +985,7 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
         }
     }
     if (dead && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
-    if constexpr (SCOPE == SCOPE_CLUSTER) cluster_sync();        // nobody sends to a CTA that has left
+    cluster_sync();                               // nobody sends to a CTA that has left
 }
 
 }  // namespace rmsq

@@ -49,42 +49,32 @@ const void* norm_bwd_fn(int dt, int elems, bool vec);
 const void* norm_bwd_reduce_fn();
 
 #define RMSQ_DEFINE_NORM_DISPATCH(NAME, KIND)                                                     \
-    template <int DT, bool EDGE, bool FULL> static const void* NAME##_ring(const NormPlan& pl)    \
+    template <int DT, bool EDGE, bool FULL> static const void* NAME##_pick(const NormPlan& pl)    \
     {                                                                                             \
-        if (pl.scope == SCOPE_CLUSTER && pl.elems == 32)                                          \
-            return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, EDGE, FULL, SCOPE_CLUSTER, KIND>); \
-        if constexpr (EDGE) {                                                                     \
-            if (pl.scope == SCOPE_CLUSTER && pl.elems == 40)                                      \
-                return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 40, EDGE, FULL, SCOPE_CLUSTER, KIND>); \
-            if (pl.scope == SCOPE_CTA)                                                            \
-                return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, EDGE, FULL, SCOPE_CTA, KIND>); \
-            if (pl.elems == 8)                                                                    \
-                return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 8, EDGE, FULL, SCOPE_WARP, KIND>); \
-            return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, EDGE, FULL, SCOPE_WARP, KIND>); \
+        if (!pl.direct) {                                                                         \
+            if constexpr (EDGE) {                                                                 \
+                if (pl.elems == 40)                                                               \
+                    return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 40, EDGE, FULL, KIND>); \
+            }                                                                                     \
+            return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, EDGE, FULL, KIND>); \
         }                                                                                         \
-        return nullptr;                                                                           \
-    }                                                                                             \
-    template <int DT, bool FULL> static const void* NAME##_direct(const NormPlan& pl)             \
-    {                                                                                             \
         if (pl.scope == SCOPE_CTA)                                                                \
-            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 32, FULL, SCOPE_CTA, KIND>); \
+            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 32, FULL, EDGE, SCOPE_CTA, KIND>); \
         if (pl.elems == 8)                                                                        \
-            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 8, FULL, SCOPE_WARP, KIND>); \
+            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 8, FULL, EDGE, SCOPE_WARP, KIND>); \
         if (pl.elems == 16)                                                                       \
-            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 16, FULL, SCOPE_WARP, KIND>); \
-        return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 32, FULL, SCOPE_WARP, KIND>); \
+            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 16, FULL, EDGE, SCOPE_WARP, KIND>); \
+        return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 32, FULL, EDGE, SCOPE_WARP, KIND>); \
     }                                                                                             \
     template <int DT> static const void* NAME##_fn(const NormPlan& pl)                            \
     {                                                                                             \
-        if (pl.direct) return pl.full ? NAME##_direct<DT, true>(pl) : NAME##_direct<DT, false>(pl); \
-        if (!pl.vec) return NAME##_ring<DT, true, false>(pl);                                     \
-        return pl.full ? NAME##_ring<DT, false, true>(pl) : NAME##_ring<DT, false, false>(pl);    \
+        if (!pl.vec) return NAME##_pick<DT, true, false>(pl);                                     \
+        return pl.full ? NAME##_pick<DT, false, true>(pl) : NAME##_pick<DT, false, false>(pl);    \
     }                                                                                             \
     cudaError_t NAME(const NormPlan& pl, const NormParams& p, cudaStream_t stream)                \
     {                                                                                             \
         const void* fn = pl.dt == DT_BF16 ? NAME##_fn<DT_BF16>(pl)                                \
                        : pl.dt == DT_FP16 ? NAME##_fn<DT_FP16>(pl) : NAME##_fn<DT_F32>(pl);       \
-        if (fn == nullptr) return cudaErrorInvalidConfiguration;                                  \
         NormParams q = p;                                                                         \
         void* args[] = {&q};                                                                      \
         return launch_kernel(fn, pl.grid, pl.threads, pl.smem, pl.cluster, stream, args);         \

@@ -3,7 +3,6 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 
 #include "rmsq_norm_bwd.cuh"
 #include "rmsq_ops.h"
@@ -65,58 +64,55 @@ static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormPara
                                NormParams& p, int64_t rows, int dtype, const DeviceView& dv, cudaStream_t stream)
 {
     NormPlan pl;
-    const int hidden = p.r.hidden;
+    const int hidden = p.r.hidden, vw = 16 / elem_bytes(dtype);
     pl.dt = dtype;
     pl.cluster = 1;
     pl.smem = 0;
+    pl.vec = hidden % vw == 0;
     p.r.rows = static_cast<int>(rows);
-    pl.direct = hidden % (16 / elem_bytes(dtype)) == 0 && hidden <= 512 * 32;
+    const int columns = pl.vec ? hidden : hidden + vw - 1;
+    pl.direct = columns <= 512 * 32;
     if (pl.direct) {
-        pl.elems = hidden <= 256 ? 8 : hidden <= 512 ? 16 : 32;
-        pl.scope = hidden <= 1024 ? SCOPE_WARP : SCOPE_CTA;
-        const int T = pl.scope == SCOPE_WARP ? 32 : (hidden + 1023) / 1024 * 32;
+        pl.elems = columns <= 256 ? 8 : columns <= 512 ? 16 : 32;
+        pl.scope = columns <= 1024 ? SCOPE_WARP : SCOPE_CTA;
+        const int T = pl.scope == SCOPE_WARP ? 32 : (columns + 1023) / 1024 * 32;
         pl.full = T * pl.elems == hidden;
         pl.threads = pl.scope == SCOPE_WARP ? 256 : T;
         pl.grid = static_cast<unsigned>(pl.scope == SCOPE_WARP ? (rows + 7) / 8 : rows);
         return status_of(go(pl, p, stream));
     }
-    const RowGeometry g = row_geometry(rows, hidden, dtype, dv.sms, [](int slice) { return slice <= 256 ? 8 : slice <= kRingWorkers * 32 ? 32 : 40; },
+    const RowGeometry g = row_geometry(rows, hidden, dtype, dv.sms, [](int slice) { return slice <= kRingWorkers * 32 ? 32 : 40; },
                                        [](int) { return kRingWorkers; });
-    pl.vec = g.period == 1;
     pl.cluster = g.cluster;
     pl.elems = g.elems;
-    pl.scope = g.cluster > 1 ? SCOPE_CLUSTER : g.T > 32 ? SCOPE_CTA : SCOPE_WARP;
+    pl.scope = SCOPE_CLUSTER;
     pl.full = g.T * g.elems == g.slice && g.slice * g.cluster == hidden;
-    pl.threads = g.T * g.groups + 32;
+    pl.threads = g.T + 32;
     p.r.total = rows * hidden * elem_bytes(dtype);
     p.r.slice = g.slice;
     p.r.slot = g.slot;
     p.T = g.T;
-    p.groups = g.groups;
     p.err = dv.err;
     p.timeout_ns = dv.timeout_ns;
-    // CTAs per SM: what the registers hold (27 warps), or as many as leave each two slots a group
-    const int64_t stage = static_cast<int64_t>(g.slot) * p.r.ntens * g.groups, head = kNormHead + 2 * g.slot;
+    // CTAs per SM: what the registers hold (27 warps), or as many as leave each two slots
+    const int64_t stage = static_cast<int64_t>(g.slot) * p.r.ntens, head = kNormHead + 2 * g.slot;
     const auto slots = [&](int ctas) { return (dv.smem_optin / ctas - 1024 - head) / stage; };
-    static const int env_r = getenv("RMSQ_R") ? atoi(getenv("RMSQ_R")) : 0, env_s = getenv("RMSQ_S") ? atoi(getenv("RMSQ_S")) : 0, env_c = getenv("RMSQ_C") ? atoi(getenv("RMSQ_C")) : 0;
-    int ctas = env_c ? env_c : 27 * 32 / pl.threads;
+    int ctas = 27 * 32 / pl.threads;
     while (ctas > 1 && slots(ctas) < 2) --ctas;
     int64_t stages = slots(ctas);
     if (stages < 1) return RMSQ_ERR_LAUNCH;
     if (stages > kRingStages) stages = kRingStages;
-    if (env_s) stages = env_s;
     // About four CTAs in turn on every place an SM has for one, but 8 rows each where that leaves a CTA to
     // every place; a CTA's rows all have one shift.
-    const int64_t places = static_cast<int64_t>(dv.sms) * ctas / pl.cluster * p.groups;
+    const int64_t places = static_cast<int64_t>(dv.sms) * ctas / pl.cluster;
     int64_t per = rows / (places * 4), most = rows / places < 8 ? rows / places : 8;
     if (per < most) per = most;
     if (per < 1) per = 1;
-    if (env_r) per = env_r;
     if (stages > per) stages = per;
     p.r.stages = static_cast<int>(stages);
     pl.smem = static_cast<int>(head + stages * stage);
-    int64_t clusters = (rows + per * p.groups - 1) / (per * p.groups);
-    if (per > 1 || p.groups > 1) clusters = (clusters + g.period - 1) / g.period * g.period;
+    int64_t clusters = (rows + per - 1) / per;
+    if (per > 1) clusters = (clusters + g.period - 1) / g.period * g.period;
     pl.grid = static_cast<unsigned>(clusters * pl.cluster);
     return status_of(go(pl, p, stream));
 }
