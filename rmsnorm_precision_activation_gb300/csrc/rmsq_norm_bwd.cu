@@ -4,22 +4,23 @@
 
 namespace rmsq {
 
-template <int DT, bool EDGE> static const void* pick(int elems)
+template <int DT, bool FULL, bool EDGE> static const void* pick(int elems)
 {
-    return elems == 8 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 8, EDGE>)
-         : elems == 16 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 16, EDGE>)
-                       : reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 24, EDGE>);
+    return elems == 8 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 8, FULL, EDGE>)
+         : elems == 16 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 16, FULL, EDGE>)
+                       : reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 24, FULL, EDGE>);
 }
 
-template <int DT> static const void* pick(int elems, bool vec)
+template <int DT> static const void* pick(int elems, bool full, bool vec)
 {
-    return vec ? pick<DT, false>(elems) : pick<DT, true>(elems);
+    if (!vec) return pick<DT, false, true>(elems);
+    return full ? pick<DT, true, false>(elems) : pick<DT, false, false>(elems);
 }
 
-const void* norm_bwd_fn(int dt, int elems, bool vec)
+const void* norm_bwd_fn(int dt, int elems, bool full, bool vec)
 {
-    return dt == DT_BF16 ? pick<DT_BF16>(elems, vec) : dt == DT_FP16 ? pick<DT_FP16>(elems, vec)
-                                                                     : pick<DT_F32>(elems, vec);
+    return dt == DT_BF16 ? pick<DT_BF16>(elems, full, vec) : dt == DT_FP16 ? pick<DT_FP16>(elems, full, vec)
+                                                                           : pick<DT_F32>(elems, full, vec);
 }
 
 const void* norm_bwd_reduce_fn() { return reinterpret_cast<const void*>(&rmsq_norm_bwd_reduce_kernel); }

@@ -52,7 +52,7 @@ constexpr int row_warps(int elems) { return elems <= 16 ? 15 : 11; }
 // cluster's sums.
 constexpr int kBwdHead = (kRingBars + 2 * 16 * 16 + ClusterSums::BYTES + 127) / 128 * 128;
 
-template <int DT, int E, bool EDGE>
+template <int DT, int E, bool FULL, bool EDGE>
 __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
 {
     using D = Deal<DT, E>;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     const Rows rows(mine, p.groups, p.r.rows);
     const int c0 = rank * p.r.slice;
     const int shift = EDGE ? static_cast<int>(static_cast<long long>(rows.first) * p.r.hidden % VW) : 0;
-    const int lo = max(shift - c0, 0), hi = max(min(shift + p.r.hidden - c0, p.r.slice), 0);
+    const int lo = max(shift - c0, 0), hi = FULL ? p.r.slice : max(min(shift + p.r.hidden - c0, p.r.slice), 0);
     const RowRing<DT, EDGE> ring{p.r, c0, lo, hi, shift, smem_u32(smem) + mine * 2 * kRingStages * 8,
                                  smem_u32(smem + kBwdHead) + mine * p.r.stages * p.r.ntens * p.r.slot};
     const ClusterSums sums{smem_u32(cluster_part), smem_u32(cluster_part + 16), nc, rank};
@@ -109,10 +109,21 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     int flip = 0;
     // The vector at column k of tensor i, 0 outside the row.
     auto load = [&](int slot, int i, int row, int k, int brought, float2 (&f)[PV]) {
-        Elem<DT>::pairs(k < hi ? ring.vec(slot, i, row, k, brought) : make_uint4(0, 0, 0, 0), f);
+        Elem<DT>::pairs(FULL || k < hi ? ring.vec(slot, i, row, k, brought) : make_uint4(0, 0, 0, 0), f);
         if (!ring.whole(k)) clear_outside(f, k, lo, hi);
     };
     const float2 offset = splat(p.offset);
+    // the statistics of the next two rows, loaded an iteration ahead
+    float next_mean[2], next_rstd[2];
+    auto ahead = [&](int i) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = rows.first + min(i + r, rows.n - 1) * rows.stride;
+            next_mean[r] = rows.n > 0 ? p.mean[row] : 0.f;
+            next_rstd[r] = rows.n > 0 ? p.rstd[row] : 0.f;
+        }
+    };
+    ahead(0);
     // Two rows at a time, so that one barrier and one round of shuffles serve both. Every CTA of a
     // cluster, and every thread of a group, runs the same iterations.
     for (int i = 0; i < rows.n; i += 2) {
@@ -120,40 +131,40 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
         int t = thread;
         asm volatile("" : "+r"(t));
         const int pair = rows.n - i < 2 ? 1 : 2;
-        w.pin();
-        float mean[2], rstd[2], s1[2] = {0.f, 0.f}, s2[2] = {0.f, 0.f};
+        const float mean[2] = {next_mean[0], next_mean[1]}, rstd[2] = {next_rstd[0], next_rstd[1]};
+        float s1[2] = {0.f, 0.f}, s2[2] = {0.f, 0.f};
+        ahead(i + 2);
+        // (one row's code, not unrolled: both rows' operands at once take more registers than there are)
+#pragma unroll 1
+        for (int r = 0; r < pair; ++r) {
+            const int row = rows.first + (i + r) * rows.stride;
+            if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage + r), phase, limit)) dead = true;
+            const int brought = ring.brought(row);
+            w.pin();
+            const float2 m = splat(r ? -mean[1] : -mean[0]), rs = splat(r ? rstd[1] : rstd[0]);
+            float2 a1 = make_float2(0.f, 0.f), a2 = a1;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int row = rows.first + (i + (r < pair ? r : 0)) * rows.stride;
-            mean[r] = p.mean[row];
-            rstd[r] = p.rstd[row];
-        }
+            for (int c = 0; c < NC; ++c) {
+                const int k = D::col(c, t, T);
+                float2 dy[PV], s[PV];
+                load(stage + r, 0, row, k, brought, dy);
+                load(stage + r, 1, row, k, brought, s);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            if (r < pair) {
-                const int row = rows.first + (i + r) * rows.stride;
-                if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage + r), phase, limit)) dead = true;
-                const int brought = ring.brought(row);
-                const float2 m = splat(-mean[r]), rs = splat(rstd[r]);
-                float2 a1 = make_float2(0.f, 0.f), a2 = a1;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int k = D::col(c, t, T);
-                    float2 dy[PV], s[PV];
-                    load(stage + r, 0, row, k, brought, dy);
-                    load(stage + r, 1, row, k, brought, s);
-#pragma unroll
-                    for (int j = 0; j < PV; ++j) {
-                        const int e = c * PV + j;
-                        const float2 xh = mul2(add2(s[j], m), rs), g = mul2(dy[j], add2(w.pair(e), offset));
-                        a1 = add2(a1, g);
-                        a2 = fma2(g, xh, a2);
-                        acc_g[e] = fma2(dy[j], xh, acc_g[e]);
-                        acc_b[e] = add2(acc_b[e], dy[j]);
-                    }
+                for (int j = 0; j < PV; ++j) {
+                    const int e = c * PV + j;
+                    const float2 xh = mul2(add2(s[j], m), rs), g = mul2(dy[j], add2(w.pair(e), offset));
+                    a1 = add2(a1, g);
+                    a2 = fma2(g, xh, a2);
+                    acc_g[e] = fma2(dy[j], xh, acc_g[e]);
+                    acc_b[e] = add2(acc_b[e], dy[j]);
                 }
-                s1[r] = a1.x + a1.y;
-                s2[r] = a2.x + a2.y;
+            }
+            if (r) {
+                s1[1] = a1.x + a1.y;
+                s2[1] = a2.x + a2.y;
+            } else {
+                s1[0] = a1.x + a1.y;
+                s2[0] = a2.x + a2.y;
             }
         }
 #pragma unroll
@@ -179,36 +190,35 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
             s1[1] = warp_sum(q.z);
             s2[1] = warp_sum(q.w);
         }
+#pragma unroll 1
+        for (int r = 0; r < pair; ++r) {
+            const int row = rows.first + (i + r) * rows.stride;
+            const int brought = ring.brought(row);
+            w.pin();
+            TT* const out = static_cast<TT*>(p.ds) + ring.origin(row);
+            const float2 m = splat(r ? -mean[1] : -mean[0]), rs = splat(r ? rstd[1] : rstd[0]);
+            const float2 n1 = splat((r ? s1[1] : s1[0]) * -inv_h), n2 = splat((r ? s2[1] : s2[0]) * -inv_h);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            if (r < pair) {
-                const int row = rows.first + (i + r) * rows.stride;
-                const int brought = ring.brought(row);
-                const float m1 = s1[r] * inv_h, m2 = s2[r] * inv_h;
-                TT* const out = static_cast<TT*>(p.ds) + ring.origin(row);
-                const float2 m = splat(-mean[r]), rs = splat(rstd[r]), n1 = splat(-m1), n2 = splat(-m2);
+            for (int c = 0; c < NC; ++c) {
+                const int k = D::col(c, t, T);
+                if (FULL || k < hi) {
+                    float2 dy[PV], s[PV], d[PV];
+                    load(stage + r, 0, row, k, brought, dy);
+                    load(stage + r, 1, row, k, brought, s);
+                    if (has_res) {
+                        load(stage + r, 2, row, k, brought, d);
+                    } else {
 #pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const int k = D::col(c, t, T);
-                    if (k < hi) {
-                        float2 dy[PV], s[PV], d[PV];
-                        load(stage + r, 0, row, k, brought, dy);
-                        load(stage + r, 1, row, k, brought, s);
-                        if (has_res) {
-                            load(stage + r, 2, row, k, brought, d);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < PV; ++j) d[j] = make_float2(0.f, 0.f);
-                        }
-#pragma unroll
-                        for (int j = 0; j < PV; ++j) {
-                            const float2 xh = mul2(add2(s[j], m), rs), g = mul2(dy[j], add2(w.pair(c * PV + j), offset));
-                            d[j] = fma2(rs, fma2(xh, n2, add2(g, n1)), d[j]);
-                        }
-                        const uint4 raw = pack_pairs<DT>(d);
-                        if (ring.whole(k)) st_v4(out + k, raw);
-                        else store_inside<DT>(out, raw, k, lo, hi);
+                        for (int j = 0; j < PV; ++j) d[j] = make_float2(0.f, 0.f);
                     }
+#pragma unroll
+                    for (int j = 0; j < PV; ++j) {
+                        const float2 xh = mul2(add2(s[j], m), rs), g = mul2(dy[j], add2(w.pair(c * PV + j), offset));
+                        d[j] = fma2(rs, fma2(xh, n2, add2(g, n1)), d[j]);
+                    }
+                    const uint4 raw = pack_pairs<DT>(d);
+                    if (ring.whole(k)) st_v4(out + k, raw);
+                    else store_inside<DT>(out, raw, k, lo, hi);
                 }
             }
         }

@@ -42,10 +42,10 @@ cudaError_t norm_layer(const NormPlan& pl, const NormParams& p, cudaStream_t str
 cudaError_t norm_layer_int8(const NormPlan& pl, const NormParams& p, cudaStream_t stream);
 cudaError_t norm_rms_int8(const NormPlan& pl, const NormParams& p, cudaStream_t stream);
 
-// Backward pass (rmsq_norm_bwd.cu): the row kernel for a type, elements per thread (8, 16 or 24) and
-// alignment, and the column reduction.
+// Backward pass (rmsq_norm_bwd.cu): the row kernel for a type, elements per thread (8, 16 or 24),
+// whether the threads cover the slices exactly and whether rows are whole vectors, and the column reduction.
 struct NormBwdParams;
-const void* norm_bwd_fn(int dt, int elems, bool vec);
+const void* norm_bwd_fn(int dt, int elems, bool full, bool vec);
 const void* norm_bwd_reduce_fn();
 
 #define RMSQ_DEFINE_NORM_DISPATCH(NAME, KIND)                                                     \

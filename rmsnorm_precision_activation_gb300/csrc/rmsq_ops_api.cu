@@ -317,7 +317,7 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         r.parts = static_cast<int>(parts);
         void* args[] = {&p};
         const rmsq_status e = status_of(launch_kernel(
-            norm_bwd_fn(dtype, g.elems, g.period == 1), static_cast<unsigned>(parts * cluster),
+            norm_bwd_fn(dtype, g.elems, g.T * g.elems == g.slice && g.slice * g.cluster == hidden, g.period == 1), static_cast<unsigned>(parts * cluster),
             static_cast<unsigned>(p.T * p.groups + 32), static_cast<int>(kBwdHead + ring), cluster, st, args));
         if (e != RMSQ_OK) return e;
     }
