@@ -165,13 +165,13 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                     const bool fresh = left == 0;
                     if (fresh) {
                         left = kTcChunk;
-                        ok = mbar_wait<SCOPE_CLUSTER>(acc_empty + 8 * (chunks & 1u), ((chunks >> 1) & 1u) ^ 1u, limit);
+                        ok = mbar_wait<SCOPE_CTA>(acc_empty + 8 * (chunks & 1u), ((chunks >> 1) & 1u) ^ 1u, limit);
                         ++chunks;
                     }
                     const uint32_t buf = (chunks - 1) & 1u, acc = tmem + buf * kPairTokens;
                     const bool tail = --left == 0 || s == steps - 1;
                     const uint32_t next = slot + 2 == OPS ? 0 : slot + 2, next_phase = slot + 2 == OPS ? phase ^ 1u : phase;
-                    if (!ready0) ok = ok && mbar_wait<SCOPE_CLUSTER>(op_full + 8 * slot, phase, limit);
+                    if (!ready0) ok = ok && mbar_wait<SCOPE_CTA>(op_full + 8 * slot, phase, limit);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc_fence_after();
@@ -180,12 +180,12 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                         tc_commit_pair(op_empty + 8 * slot);
                     }
                     __syncwarp();
-                    if (!ready1) ok = mbar_wait<SCOPE_CLUSTER>(op_full + 8 * slot + 8, phase, limit);
+                    if (!ready1) ok = mbar_wait<SCOPE_CTA>(op_full + 8 * slot + 8, phase, limit);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    const bool peek0 = mbar_test<SCOPE_CLUSTER>(op_full + 8 * next, next_phase);
-                    const bool peek1 = mbar_test<SCOPE_CLUSTER>(op_full + 8 * next + 8, next_phase);
+                    const bool peek0 = mbar_test<SCOPE_CTA>(op_full + 8 * next, next_phase);
+                    const bool peek1 = mbar_test<SCOPE_CTA>(op_full + 8 * next + 8, next_phase);
                     if (one) {
                         tc_mma_step<true>(acc, tmem_a + slot * 32 + 32, desc0 + (slot + 1) * (kPairOp / 16), idesc, false);
                         tc_commit_pair(op_empty + 8 * slot + 8);
