@@ -220,6 +220,27 @@ template <int DT, int E> struct Deal {
     }
 };
 
+// Which of a thread's vectors have columns lo to hi at all, and which of those also have others. EDGE: bits,
+// the same for all rows of one shift, so that testing one is all a row costs.
+template <int DT, int E, bool FULL, bool EDGE> struct Part {
+    uint32_t some = 0, cut = 0;
+    int hi;
+    __device__ __forceinline__ Part(int t, int T, int lo, int hi_) : hi(hi_)
+    {
+        using D = Deal<DT, E>;
+        if (EDGE) {
+#pragma unroll
+            for (int c = 0; c < D::NC; ++c) {
+                const int k = D::col(c, t, T);
+                if (k < hi) some |= 1u << c;
+                if (k < hi && (k < lo || k + D::VW > hi)) cut |= 1u << c;
+            }
+        }
+    }
+    __device__ __forceinline__ bool in(int c, int k) const { return FULL || (EDGE ? (some >> c & 1u) != 0 : k < hi); }
+    __device__ __forceinline__ bool whole(int c) const { return !EDGE || !(cut >> c & 1u); }
+};
+
 // Zeros in place of a vector's columns outside lo to hi.
 template <int PV> __device__ __forceinline__ void clear_outside(float2 (&f)[PV], int k, int lo, int hi)
 {
@@ -610,8 +631,7 @@ constexpr int kRingBars = 2 * kRingStages * kRingGroups * 8;      // bytes of ba
 
 // A row group's ring of slots: its next rows, brought by bulk copies while the group works. EDGE: rows of
 // a width that is no whole number of vectors, taken from the 16-byte boundary below. The group's rows all
-// have the same shift (Rows). The tensors' last bytes, which no whole 16-byte piece covers, are read
-// directly.
+// have the same shift (Rows).
 template <int DT, bool EDGE> struct RowRing {
     using S = Scalar<DT>;
     using T = typename S::T;
@@ -636,35 +656,25 @@ template <int DT, bool EDGE> struct RowRing {
         long long a1 = a0 + (hi + VW - 1) / VW * 16;
         if (EDGE && a1 > (r.total & ~15LL)) a1 = r.total & ~15LL;
         const uint32_t bytes = hi > lo && a1 > a0 ? static_cast<uint32_t>(a1 - a0) : 0u;
+        if (EDGE && hi > lo) {
+            // the tensors' last bytes, which no whole piece covers, by hand (before the arrival below)
+            const long long end = origin(row) + hi;
+            for (long long e = a1 / ES; e < end; ++e)
+                for (int i = 0; i < r.ntens; ++i) {
+                    const uint32_t to = at(stage, i) + static_cast<uint32_t>(e * ES - a0);
+                    const T v = static_cast<const T*>(r.in[i])[e];
+                    if constexpr (ES == 2) asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
+                    else asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+                }
+        }
         mbar_arrive_expect_tx(full(stage), bytes * r.ntens);
         if (bytes > 0)
             for (int i = 0; i < r.ntens; ++i)
                 bulk_load(at(stage, i), static_cast<const unsigned char*>(r.in[i]) + a0, bytes, full(stage), policy);
     }
 
-    // How many columns of a row's slot the copies can have brought.
-    __device__ __forceinline__ int brought(int row) const
-    {
-        if (!EDGE) return hi;
-        const long long n = (r.total & ~15LL) / ES - origin(row);
-        return n < hi + VW ? static_cast<int>(n) : hi + VW;
-    }
     // The vector at column k of tensor i, as raw bits; what is not the row's is not cleared.
-    __device__ __forceinline__ uint4 vec(uint32_t stage, int i, int row, int k, int brought) const
-    {
-        if (!EDGE || k + VW <= brought) return ld_shared_v4(at(stage, i) + k * ES);
-        const T* const p = static_cast<const T*>(r.in[i]) + origin(row) + k;
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < VW; ++j)
-            if (k + j < hi) {
-                if constexpr (ES == 4) w[j] = __float_as_uint(p[j]);
-                else w[j / 2] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
-            }
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    // Whether the vector at column k is the row's as a whole.
-    __device__ __forceinline__ bool whole(int k) const { return !EDGE || (k >= lo && k + VW <= hi); }
+    __device__ __forceinline__ uint4 vec(uint32_t stage, int i, int k) const { return ld_shared_v4(at(stage, i) + k * ES); }
     // One thread sets the barriers up: a slot is empty when `warps` warps have left it.
     __device__ __forceinline__ void init(int warps) const
     {
@@ -776,7 +786,6 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
     const int c0 = rank * p.r.slice;
     const int shift = EDGE ? static_cast<int>(static_cast<long long>(rows.first) * p.r.hidden % VW) : 0;
     const int lo = max(shift - c0, 0), hi = FULL ? p.r.slice : max(min(shift + p.r.hidden - c0, p.r.slice), 0);
-    const auto in = [&](int k) { return FULL || k < hi; };
     const RowRing<DT, EDGE> ring{p.r, c0, lo, hi, shift, smem_u32(smem),
                                  smem_u32(smem + kNormHead) + 2 * p.r.slot};
     const ClusterSums sums{smem_u32(cluster_part), smem_u32(cluster_part + 16), nc, rank};
@@ -824,6 +833,7 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
     // CTA's of the cluster. A count that is not a power of two makes a mean off by half a step more.
     const uint32_t limit = wait_limit(p.timeout_ns);
     const auto inverse = [](int k) { return k > 0 ? 1.0f / static_cast<float>(k) : 0.f; };
+    const Part<DT, E, FULL, EDGE> mine(thread, T, lo, hi);
     const int n_w = FULL ? 32 * E : D::count(warp * 32, T, lo, hi);
     const int n_l = lane >= warps ? 0 : FULL ? 32 * E : D::count(lane * 32, T, lo, hi);
     const int n_r = lane < nc
@@ -845,23 +855,22 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
         // ---- s into registers, fp32 (exact), 0 outside the slice ----
         float2 v[E / 2];
         {
-            const int brought = ring.brought(row);
             TT* const ro = static_cast<TT*>(p.res_out) + at;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int k = D::col(c, t, T);
                 uint4 raw = make_uint4(0, 0, 0, 0);
-                if (in(k)) {
-                    raw = ring.vec(stage, 0, row, k, brought);
+                if (mine.in(c, k)) {
+                    raw = ring.vec(stage, 0, k);
                     if (has_res) {
-                        raw = Elem<DT>::add(raw, ring.vec(stage, 1, row, k, brought));
-                        if (ring.whole(k)) st_v4(ro + k, raw);
+                        raw = Elem<DT>::add(raw, ring.vec(stage, 1, k));
+                        if (mine.whole(c)) st_v4(ro + k, raw);
                         else store_inside<DT>(ro, raw, k, lo, hi);
                     }
                 }
                 float2 f[PV];
                 Elem<DT>::pairs(raw, f);
-                if (!ring.whole(k)) clear_outside(f, k, lo, hi);
+                if (!mine.whole(c)) clear_outside(f, k, lo, hi);
 #pragma unroll
                 for (int j = 0; j < PV; ++j) v[c * PV + j] = f[j];
             }
@@ -883,11 +892,11 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int k = D::col(c, t, T);
-                if (in(k)) {
+                if (mine.in(c, k)) {
                     float2 d[PV];
 #pragma unroll
                     for (int j = 0; j < PV; ++j) d[j] = add2(v[c * PV + j], m);
-                    if (!ring.whole(k)) clear_outside(d, k, lo, hi);
+                    if (!mine.whole(c)) clear_outside(d, k, lo, hi);
 #pragma unroll
                     for (int j = 0; j < PV; ++j) a = fma2(d[j], d[j], a);
                 }
@@ -928,7 +937,7 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int k = D::col(c, t, T);
-            if (in(k)) {
+            if (mine.in(c, k)) {
                 float2 w[PV], b[PV];
                 Elem<DT>::pairs(ld_shared_v4(smem_u32(ws + k)), w);
                 Elem<DT>::pairs(ld_shared_v4(smem_u32(bs + k)), b);
@@ -943,7 +952,7 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
                     else y[j] = fma2(mul2(add2(v[c * PV + j], m), r2), w[j], b[j]);
                 }
                 if constexpr (INT8) {
-                    if (!ring.whole(k)) clear_outside(y, k, lo, hi);
+                    if (!mine.whole(c)) clear_outside(y, k, lo, hi);
 #pragma unroll
                     for (int j = 0; j < PV; ++j) {
                         amax = max3(amax, fabsf(y[j].x), fabsf(y[j].y));
@@ -951,7 +960,7 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
                     }
                 } else {
                     const uint4 raw = pack_pairs<DT>(y);
-                    if (ring.whole(k)) st_v4(o + k, raw);
+                    if (mine.whole(c)) st_v4(o + k, raw);
                     else store_inside<DT>(o, raw, k, lo, hi);
                 }
             }

@@ -107,10 +107,11 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     bool dead = false;                            // a wait ran out: finish without waiting again
     int stage = 0, phase = 0;
     int flip = 0;
-    // The vector at column k of tensor i, 0 outside the row.
-    auto load = [&](int slot, int i, int row, int k, int brought, float2 (&f)[PV]) {
-        Elem<DT>::pairs(FULL || k < hi ? ring.vec(slot, i, row, k, brought) : make_uint4(0, 0, 0, 0), f);
-        if (!ring.whole(k)) clear_outside(f, k, lo, hi);
+    const Part<DT, E, FULL, EDGE> share(thread, T, lo, hi);
+    // The thread's vector c, at column k, of tensor i, 0 outside the row.
+    auto load = [&](int c, int slot, int i, int k, float2 (&f)[PV]) {
+        Elem<DT>::pairs(share.in(c, k) ? ring.vec(slot, i, k) : make_uint4(0, 0, 0, 0), f);
+        if (!share.whole(c)) clear_outside(f, k, lo, hi);
     };
     const float2 offset = splat(p.offset);
     // the statistics of the next two rows, loaded an iteration ahead
@@ -139,7 +140,6 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
         for (int r = 0; r < pair; ++r) {
             const int row = rows.first + (i + r) * rows.stride;
             if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage + r), phase, limit)) dead = true;
-            const int brought = ring.brought(row);
             w.pin();
             const float2 m = splat(r ? -mean[1] : -mean[0]), rs = splat(r ? rstd[1] : rstd[0]);
             float2 a1 = make_float2(0.f, 0.f), a2 = a1;
@@ -147,8 +147,8 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
             for (int c = 0; c < NC; ++c) {
                 const int k = D::col(c, t, T);
                 float2 dy[PV], s[PV];
-                load(stage + r, 0, row, k, brought, dy);
-                load(stage + r, 1, row, k, brought, s);
+                load(c, stage + r, 0, k, dy);
+                load(c, stage + r, 1, k, s);
 #pragma unroll
                 for (int j = 0; j < PV; ++j) {
                     const int e = c * PV + j;
@@ -193,7 +193,6 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
 #pragma unroll 1
         for (int r = 0; r < pair; ++r) {
             const int row = rows.first + (i + r) * rows.stride;
-            const int brought = ring.brought(row);
             w.pin();
             TT* const out = static_cast<TT*>(p.ds) + ring.origin(row);
             const float2 m = splat(r ? -mean[1] : -mean[0]), rs = splat(r ? rstd[1] : rstd[0]);
@@ -201,12 +200,12 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 const int k = D::col(c, t, T);
-                if (FULL || k < hi) {
+                if (share.in(c, k)) {
                     float2 dy[PV], s[PV], d[PV];
-                    load(stage + r, 0, row, k, brought, dy);
-                    load(stage + r, 1, row, k, brought, s);
+                    load(c, stage + r, 0, k, dy);
+                    load(c, stage + r, 1, k, s);
                     if (has_res) {
-                        load(stage + r, 2, row, k, brought, d);
+                        load(c, stage + r, 2, k, d);
                     } else {
 #pragma unroll
                         for (int j = 0; j < PV; ++j) d[j] = make_float2(0.f, 0.f);
@@ -217,7 +216,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
                         d[j] = fma2(rs, fma2(xh, n2, add2(g, n1)), d[j]);
                     }
                     const uint4 raw = pack_pairs<DT>(d);
-                    if (ring.whole(k)) st_v4(out + k, raw);
+                    if (share.whole(c)) st_v4(out + k, raw);
                     else store_inside<DT>(out, raw, k, lo, hi);
                 }
             }
