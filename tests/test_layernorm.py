@@ -105,6 +105,40 @@ def test_forward_far_off_centre():
 
 
 @gpu
+def test_offsets_past_32_bits():
+    # 34000 x 65536 elements: the last rows start past 2^31 elements and 2^32 bytes
+    rows, hidden = 34000, 65536
+    x = torch.empty(rows, hidden, dtype=torch.bfloat16, device="cuda")
+    x[:-3].fill_(1.0)
+    x[-3:].copy_(torch.randn(3, hidden, device="cuda"))
+    gamma = (torch.randn(hidden, device="cuda") * 0.2 + 1.0).bfloat16()
+    y, _, mean, rstd = rq().layernorm(x, gamma, stats=True)
+    few = rq().layernorm(x[-3:].contiguous(), gamma, stats=True)
+    assert torch.equal(y[-3:], few[0]) and torch.equal(mean[-3:], few[2]) and not y[:-3].any()
+    q, scale, _ = rq().rmsnorm_quant_int8(x, gamma)
+    fewq = rq().rmsnorm_quant_int8(x[-3:].contiguous(), gamma)
+    assert torch.equal(q[-3:], fewq[0]) and torch.equal(scale[-3:], fewq[1])
+    del q
+    ds, dg, _ = rq().layernorm_backward(x, x, gamma, mean, rstd, grad_input=y, param_grad_dtype=torch.float32)
+    fewb = rq().layernorm_backward(x[-3:].contiguous(), x[-3:].contiguous(), gamma, mean[-3:].clone(),
+                                   rstd[-3:].clone(), param_grad_dtype=torch.float32)
+    # the rows of ones have xhat = 0, so they add nothing to dgamma; other rows' sums differ in order
+    assert torch.equal(ds[-3:], fewb[0])
+    assert ((dg - fewb[1]).abs() <= 8 * U * (x[-3:].double().abs() * 8).sum(0)).all()
+
+
+@gpu
+def test_backward_far_off_centre():
+    d = make(200, 2000, torch.float32, seed=3, centre=1000.0)
+    d["dy"] = torch.randn_like(d["x"])
+    d["dres"] = None
+    x = d["x"].double()
+    d["mean"] = x.mean(1).float()
+    d["rstd"] = (x.var(1, correction=0) + 1e-5).rsqrt().float()
+    check_backward(d)
+
+
+@gpu
 def test_constant_rows_give_beta():
     x = torch.full((5, 2048), 3.0, dtype=torch.float32, device="cuda")
     g = torch.full((2048,), 2.0, device="cuda")

@@ -107,6 +107,18 @@ def test_large():
 
 
 @gpu
+@pytest.mark.parametrize("m,n", [(70000, 32768), (300, 8000000), (12, 3125000)])
+def test_outputs_and_weights_past_32_bits(m, n):
+    # outputs of over 2^31 elements (first two); rows and channels at the far end against a small call
+    k = 64
+    d = make(m, n, k, seed=6, bias=False)
+    out = rq().matmul_int8(d["a"], d["sa"], d["w"], d["sw"])
+    far = slice(n - 130, n)
+    want = rq().matmul_int8(d["a"][-5:].contiguous(), d["sa"][-5:].clone(), d["w"][far].contiguous(), d["sw"][far].clone())
+    assert torch.equal(out[-5:, far], want)
+
+
+@gpu
 @pytest.mark.parametrize("m", [1, 12, 100, 300])
 def test_guard_bytes_and_leading_dimensions(m):
     d = make(m, 333, 208, seed=9)
