@@ -4,6 +4,8 @@ ragged sizes, and with codes whose sums are as large as they get.
 Tolerance. The integer sum is exact; it is rounded to fp32 once, multiplied by two scales and the
 bias added (four roundings of u = 2^-24), then rounded to the output's type (half a step h):
 |out - exact| <= h |exact| + 4 u (|exact - bias| + |bias|) (1 + h), and half an fp16 subnormal step."""
+import threading
+
 import pytest
 import torch
 
@@ -104,6 +106,28 @@ def test_unit_scales_give_whole_numbers(m):
 def test_large():
     check(make(2048, 4096, 8192, seed=4))
     check(make(4099, 5001, 1232, seed=5, dtype=torch.float16))
+
+
+@gpu
+@pytest.mark.parametrize("m", [1, 12, 24, 60, 100, 300])
+def test_first_call_of_a_thread(m):
+    # a thread with no CUDA call of its own before; every tensor made elsewhere
+    d = make(m, 500, 192, seed=9)
+    want = rq().matmul_int8(d["a"], d["sa"], d["w"], d["sw"], bias=d["bias"])
+    out = torch.zeros_like(want)
+    errors = []
+
+    def call():
+        try:
+            rq().matmul_int8(d["a"], d["sa"], d["w"], d["sw"], bias=d["bias"], output=out)
+        except Exception as e:
+            errors.append(e)
+
+    thread = threading.Thread(target=call)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert not errors and torch.equal(out, want)
 
 
 @gpu
