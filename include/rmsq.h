@@ -196,6 +196,8 @@ rmsq_status rmsnorm_quant_fp8_static_scratch(const void* input, const void* resi
  * RMSQ_MAX_HIDDEN (fp32: half of it), rows at most 2^27 - 1. output may be input, and residual_output
  * may be residual or input (each element is read before it is written).
  * A row with a NaN or an infinity gives NaN in that row alone.
+ * Sums are added in a fixed order, which depends on the row's length and, where rows are no whole number
+ * of 16 bytes, on where the row starts against a 16-byte boundary; not on the number of rows.
  * ------------------------------------------------------------------------------------------- */
 rmsq_status layernorm(const void* input, const void* residual, void* residual_output,
                       const void* gamma, const void* beta, int64_t rows, int64_t hidden, int dtype,
@@ -243,6 +245,7 @@ rmsq_status layernorm_backward(const void* grad_output, const void* grad_residua
  *
  *   output           [rows x hidden] int8
  *   scale_output     [rows] fp32; a row whose y is all zero gets codes 0 and scale 0
+ * A row with a NaN or an infinity gets scale NaN (and any codes), so matmul_int8 gives NaN for it.
  * Other arguments and sizes as for layernorm. Codes are formed with a reciprocal in fp32: one whose
  * y_i / scale lies within 1e-4 of a half may be either neighbour.
  * ------------------------------------------------------------------------------------------- */

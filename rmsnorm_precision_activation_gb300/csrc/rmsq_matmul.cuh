@@ -71,7 +71,7 @@ template <int NB>
 __global__ void __launch_bounds__(kStreamWarps * 32, 2) rmsq_matmul_stream_kernel(const MatmulParams p)
 {
     // steps of 64 elements held in registers: one is multiplied while the loads of the others run
-    constexpr int U = NB == 1 ? 4 : NB == 2 ? 3 : 2;
+    constexpr int U = NB == 1 ? 4 : 3;
     __shared__ int part[kStreamWarps][NB * 8][kStreamRows + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const long long n0 = static_cast<long long>(blockIdx.x) * kStreamRows;

@@ -133,6 +133,20 @@ __device__ __forceinline__ uint4 ld_v4(const void* p)
     return v;
 }
 
+// Maxima that are NaN where one of their operands is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float warp_max_nan(float v)
+{
+    float r;
+    asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 __device__ __forceinline__ void pdl_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -318,7 +332,8 @@ template <int DT, int E, bool EDGE> struct Held {
 };
 
 // A thread's share of a row, columns lo to hi, as int8 codes of y * 127 / amax. 127 / amax overflows for
-// rows of tiny y: those are scaled up by 2^100 first (exact).
+// rows of tiny y: those are scaled up by 2^100 first (exact). amax is NaN for a row with a NaN, and so is
+// the scale; the codes are then any.
 template <int DT, int E, bool FULL, bool EDGE>
 __device__ __forceinline__ void store_codes(float2 (&v)[E / 2], float amax, signed char* o, int t, int T, int lo, int hi)
 {
@@ -580,7 +595,7 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
                 if (!whole(k)) clear_outside(y, k, lo, hi);
 #pragma unroll
                 for (int j = 0; j < PV; ++j) {
-                    amax = max3(amax, fabsf(y[j].x), fabsf(y[j].y));
+                    amax = max3_nan(amax, fabsf(y[j].x), fabsf(y[j].y));
                     v[c * PV + j] = y[j];
                 }
             } else {
@@ -593,11 +608,11 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
     }
     const bool leader = t == 0;
     if constexpr (INT8) {
-        amax = warp_max(amax);
+        amax = warp_max_nan(amax);
         if constexpr (SCOPE != SCOPE_WARP) {
             if (lane == 0) part_max[warp] = amax;
             __syncthreads();
-            amax = warp_max(lane < nwarps ? part_max[lane] : 0.f);
+            amax = warp_max_nan(lane < nwarps ? part_max[lane] : 0.f);
         }
         store_codes<DT, E, FULL, EDGE>(v, amax, static_cast<signed char*>(p.out) + at, t, T, lo, hi);
         if (leader) p.scale[row] = amax / 127.0f;
@@ -633,8 +648,7 @@ constexpr int kRingBars = 2 * kRingStages * kRingGroups * 8;      // bytes of ba
 // a width that is no whole number of vectors, taken from the 16-byte boundary below. The group's rows all
 // have the same shift (Rows).
 template <int DT, bool EDGE> struct RowRing {
-    using S = Scalar<DT>;
-    using T = typename S::T;
+    using T = typename Scalar<DT>::T;
     static constexpr int ES = sizeof(T), VW = Elem<DT>::EPV;
     const RowTensors& r;
     int c0;                        // the CTA's first column
@@ -675,6 +689,7 @@ template <int DT, bool EDGE> struct RowRing {
 
     // The vector at column k of tensor i, as raw bits; what is not the row's is not cleared.
     __device__ __forceinline__ uint4 vec(uint32_t stage, int i, int k) const { return ld_shared_v4(at(stage, i) + k * ES); }
+
     // One thread sets the barriers up: a slot is empty when `warps` warps have left it.
     __device__ __forceinline__ void init(int warps) const
     {
@@ -683,9 +698,10 @@ template <int DT, bool EDGE> struct RowRing {
             mbar_init(empty(i), warps);
         }
     }
-    // Brings the group's rows (one thread of the CTA's copying warp: issuing a row's
-    // copies takes about 1000 cycles, which a working warp would keep its group waiting for). After a
-    // wait that ran out, waits (bounded) for the copies in flight, so that they end before the CTA does.
+
+    // Brings the group's rows (one thread of the CTA's copying warp: issuing a row's copies takes about
+    // 1000 cycles, which a working warp would keep its group waiting for). After a wait that ran out,
+    // waits (bounded) for the copies in flight, so that they end before the CTA does.
     __device__ __forceinline__ void feed(const Rows& rows, unsigned long long timeout_ns, unsigned int* err) const
     {
         const uint64_t policy = l2_evict_normal_policy();
@@ -708,7 +724,6 @@ template <int DT, bool EDGE> struct RowRing {
         }
     }
 };
-
 
 // The threads of a row group (T a multiple of 32).
 __device__ __forceinline__ void group_sync(int group, int T)
@@ -792,7 +807,6 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
     const ClusterSums maxima{sums.bars + ClusterSums::BYTES, sums.slots + ClusterSums::BYTES, nc, rank};
 
     const bool has_res = p.r.ntens == 2;
-
     if (copies && lane == 0) {
         ring.init(warps);
         sums.init();
@@ -904,9 +918,9 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
             m2 = warp_sum(a.x + a.y);
         }
         if (lane == 0) mbar_arrive(ring.empty(stage));       // the warp has read the slot
+        if (lane == 0) part[flip * 8 + warp] = make_float2(sum, m2);
+        group_sync(0, T);
         {
-            if (lane == 0) part[flip * 8 + warp] = make_float2(sum, m2);
-            group_sync(0, T);
             const float2 q = lane < warps ? part[flip * 8 + lane] : make_float2(0.f, 0.f);
             float d = 0.f;
             if constexpr (!RMS) {
@@ -955,7 +969,7 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
                     if (!mine.whole(c)) clear_outside(y, k, lo, hi);
 #pragma unroll
                     for (int j = 0; j < PV; ++j) {
-                        amax = max3(amax, fabsf(y[j].x), fabsf(y[j].y));
+                        amax = max3_nan(amax, fabsf(y[j].x), fabsf(y[j].y));
                         v[c * PV + j] = y[j];
                     }
                 } else {
@@ -967,18 +981,14 @@ __global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(co
         }
         const bool leader = t == 0 && rank == 0;
         if constexpr (INT8) {
-            amax = warp_max(amax);
-            {
-                if (lane == 0) part_max[flip * 8 + warp] = amax;
-                group_sync(0, T);
-                amax = warp_max(lane < warps ? part_max[flip * 8 + lane] : 0.f);
-            }
-            {
-                float4 q;
-                if (warp == 0) maxima.send(lane, flip, make_float4(amax, 0.f, 0.f, 0.f));
-                if (!maxima.receive(lane, flip, (i >> 1) & 1, dead ? 0 : limit, q)) dead = true;
-                amax = warp_max(q.x);
-            }
+            amax = warp_max_nan(amax);
+            if (lane == 0) part_max[flip * 8 + warp] = amax;
+            group_sync(0, T);
+            amax = warp_max_nan(lane < warps ? part_max[flip * 8 + lane] : 0.f);
+            float4 q;
+            if (warp == 0) maxima.send(lane, flip, make_float4(amax, 0.f, 0.f, 0.f));
+            if (!maxima.receive(lane, flip, (i >> 1) & 1, dead ? 0 : limit, q)) dead = true;
+            amax = warp_max_nan(q.x);
             asm volatile("" : "+r"(t));
             signed char* const codes = static_cast<signed char*>(p.out) + at;
             store_codes<DT, E, FULL, EDGE>(v, amax, codes, t, T, lo, hi);

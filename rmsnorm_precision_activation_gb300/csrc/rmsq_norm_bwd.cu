@@ -6,9 +6,12 @@ namespace rmsq {
 
 template <int DT, bool FULL, bool EDGE> static const void* pick(int elems)
 {
+    // (slices of more than 7680 elements are no multiple of 32 x 24, and fp32 slices have 4100 at most)
+    if constexpr (!FULL && DT != DT_F32) {
+        if (elems == 24) return reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 24, FULL, EDGE>);
+    }
     return elems == 8 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 8, FULL, EDGE>)
-         : elems == 16 ? reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 16, FULL, EDGE>)
-                       : reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 24, FULL, EDGE>);
+                      : reinterpret_cast<const void*>(&rmsq_norm_bwd_kernel<DT, 16, FULL, EDGE>);
 }
 
 template <int DT> static const void* pick(int elems, bool full, bool vec)

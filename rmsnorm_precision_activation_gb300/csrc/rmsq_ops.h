@@ -27,7 +27,8 @@ cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem,
 
 struct NormPlan {
     int dt;
-    int elems;      // per thread: 8, 16 (direct only), 32 or 40 (the widest rows)
+    int elems;      // per thread: 8, 16 (direct only), 32 or 40 (16-bit rows of 131065 elements or more,
+                    // off 16-byte boundaries: 16 slices of 8200)
     bool vec;
     bool direct;    // rows straight into registers
     bool full;      // the threads' shares cover the row exactly
@@ -42,8 +43,9 @@ cudaError_t norm_layer(const NormPlan& pl, const NormParams& p, cudaStream_t str
 cudaError_t norm_layer_int8(const NormPlan& pl, const NormParams& p, cudaStream_t stream);
 cudaError_t norm_rms_int8(const NormPlan& pl, const NormParams& p, cudaStream_t stream);
 
-// Backward pass (rmsq_norm_bwd.cu): the row kernel for a type, elements per thread (8, 16 or 24),
-// whether the threads cover the slices exactly and whether rows are whole vectors, and the column reduction.
+// Backward pass (rmsq_norm_bwd.cu): the row kernel for a type, elements per thread (8, 16, or 24 for
+// slices of more than 7680 elements of 16 bits), whether the threads cover the slices exactly and whether
+// rows are whole vectors, and the column reduction.
 struct NormBwdParams;
 const void* norm_bwd_fn(int dt, int elems, bool full, bool vec);
 const void* norm_bwd_reduce_fn();
@@ -52,7 +54,7 @@ const void* norm_bwd_reduce_fn();
     template <int DT, bool EDGE, bool FULL> static const void* NAME##_pick(const NormPlan& pl)    \
     {                                                                                             \
         if (!pl.direct) {                                                                         \
-            if constexpr (EDGE) {                                                                 \
+            if constexpr (EDGE && DT != DT_F32) {                                                 \
                 if (pl.elems == 40)                                                               \
                     return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 40, EDGE, FULL, KIND>); \
             }                                                                                     \

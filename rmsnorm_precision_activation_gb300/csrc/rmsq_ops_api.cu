@@ -30,16 +30,14 @@ static rmsq_status status_of(cudaError_t e)
     return RMSQ_ERR_LAUNCH;
 }
 
-// How rows are dealt out over rings: wide rows are split evenly over the smallest cluster of 2, 4, 8 or
-// 16 CTAs whose slices take at most kRingSlice bytes, in whole vectors where the row has them; a slice
-// takes T threads of `elems` elements; short rows leave a CTA of `workers` threads room for several row
-// groups, of which it takes no more than give every SM a row.
+// How a row is dealt out: split evenly, in whole vectors, over the smallest cluster of 1, 2, 4, 8 or 16
+// CTAs whose slices take at most kRingSlice bytes; a slice takes T threads of `elems` elements.
 struct RowGeometry {
-    int cluster, slice, elems, T, groups, slot;
+    int cluster, slice, elems, T, slot;
     int period;      // rows after which the shift off 16-byte boundaries repeats
 };
 
-static RowGeometry row_geometry(int64_t rows, int hidden, int dtype, int sms, int (*elems)(int), int (*workers)(int))
+static RowGeometry row_geometry(int hidden, int dtype, int (*elems)(int))
 {
     const int es = elem_bytes(dtype), vw = 16 / es;
     RowGeometry g;
@@ -52,14 +50,11 @@ static RowGeometry row_geometry(int64_t rows, int hidden, int dtype, int sms, in
     g.slice = ((columns + g.cluster - 1) / g.cluster + vw - 1) / vw * vw;
     g.elems = elems(g.slice);
     g.T = ((g.slice + g.elems - 1) / g.elems + 31) / 32 * 32;
-    g.groups = g.cluster > 1 ? 1 : workers(g.elems) / g.T;
-    const int64_t spread = (rows + sms - 1) / sms;
-    if (g.groups > spread) g.groups = static_cast<int>(spread);
     g.slot = g.slice * es;
     return g;
 }
 
-// Launch of a forward norm (rmsq_norm_kernel).
+// Launch of a forward norm.
 static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormParams&, cudaStream_t),
                                NormParams& p, int64_t rows, int dtype, const DeviceView& dv, cudaStream_t stream)
 {
@@ -81,8 +76,7 @@ static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormPara
         pl.grid = static_cast<unsigned>(pl.scope == SCOPE_WARP ? (rows + 7) / 8 : rows);
         return status_of(go(pl, p, stream));
     }
-    const RowGeometry g = row_geometry(rows, hidden, dtype, dv.sms, [](int slice) { return slice <= kRingWorkers * 32 ? 32 : 40; },
-                                       [](int) { return kRingWorkers; });
+    const RowGeometry g = row_geometry(hidden, dtype, [](int slice) { return slice <= kRingWorkers * 32 ? 32 : 40; });
     pl.cluster = g.cluster;
     pl.elems = g.elems;
     pl.scope = SCOPE_CLUSTER;
@@ -283,14 +277,17 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         p.offset = weight_offset;
         p.timeout_ns = dv.timeout_ns;
 
-        RowGeometry g = row_geometry(rows, p.r.hidden, dtype, dv.sms,
-                                     [](int slice) { return slice <= 256 ? 8 : slice <= row_warps(16) * 32 * 16 ? 16 : 24; },
-                                     [](int elems) { return row_warps(elems) * 32; });
+        const RowGeometry g = row_geometry(p.r.hidden, dtype, [](int slice) {
+            return slice <= 256 ? 8 : slice <= row_warps(16) * 32 * 16 ? 16 : 24;
+        });
         p.r.slice = g.slice;
         p.r.slot = g.slot;
         p.T = g.T;
-        p.groups = g.groups;
         const int cluster = g.cluster;
+        // short rows leave room for several row groups in a CTA, which takes no more than give every SM a row
+        const int64_t spread = (rows + dv.sms - 1) / dv.sms;
+        p.groups = cluster > 1 ? 1 : row_warps(g.elems) * 32 / g.T;
+        if (p.groups > spread) p.groups = static_cast<int>(spread);
         // at least two pairs of rows in the ring: one is refilled while the other is worked on
         auto slots = [&]() {
             return (dv.smem_optin - kBwdHead) / (static_cast<int64_t>(p.r.slot) * p.r.ntens * p.groups);

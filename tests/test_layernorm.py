@@ -128,6 +128,26 @@ def test_offsets_past_32_bits():
 
 
 @gpu
+@pytest.mark.parametrize("hidden", [96, 1003, 1024, 5121, 16384, 20000, 66001])
+def test_int8_rows_that_are_not_finite_get_scale_nan(hidden):
+    x = torch.randn(9, hidden, device="cuda").bfloat16()
+    x[2, hidden - 1] = float("nan")
+    x[4, hidden // 2] = float("inf")
+    x[7, 0] = -float("inf")
+    gamma = torch.ones(hidden, dtype=torch.bfloat16, device="cuda")
+    bad = torch.tensor([2, 4, 7], device="cuda")
+    good = torch.tensor([0, 1, 3, 5, 6, 8], device="cuda")
+    finite = x.clone()
+    finite[bad] = 1.0
+    for f in (rq().layernorm_quant_int8, rq().rmsnorm_quant_int8):
+        q, scale, _ = f(x, gamma)
+        assert scale[bad].isnan().all()
+        # the same rows at the same places (their order of summing goes by the row's place at odd widths)
+        want = f(finite, gamma)
+        assert torch.equal(q[good], want[0][good]) and torch.equal(scale[good], want[1][good])
+
+
+@gpu
 def test_backward_far_off_centre():
     d = make(200, 2000, torch.float32, seed=3, centre=1000.0)
     d["dy"] = torch.randn_like(d["x"])
