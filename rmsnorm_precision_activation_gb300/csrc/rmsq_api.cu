@@ -229,52 +229,87 @@ bool device_view(DeviceView* v)
 struct ReadyFn {
     const void* fn;
     int dev;
+    int clusters[9];      // clusters of each size that fit on the device at a time; 0: not asked yet
 };
 static ReadyFn g_ready[512];
 static int g_nready = 0;
 
-cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem, int cluster,
-                          cudaStream_t stream, void** args)
+// fn's entry for the current device, with its attributes set (under g_mu); null when the table is full
+// or a call fails (*e).
+static ReadyFn* ready_fn(const void* fn, int smem, cudaError_t* e)
 {
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    {
-        std::lock_guard<std::mutex> lock(g_mu);
-        int i = 0;
-        while (i < g_nready && !(g_ready[i].fn == fn && g_ready[i].dev == dev)) ++i;
-        if (i == g_nready) {
-            cudaFuncAttributes fa;
-            e = cudaFuncGetAttributes(&fa, fn);
-            if (e != cudaSuccess) return e;
-            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     g_dev[dev].smem_optin - static_cast<int>(fa.sharedSizeBytes));
-            // clusters of 16 CTAs are beyond the portable size of 8
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-            // the rings of several CTAs fit on one SM
-            if (e == cudaSuccess && smem > 0)
-                e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                         cudaSharedmemCarveoutMaxShared);
-            if (e != cudaSuccess) return e;
-            if (g_nready < static_cast<int>(sizeof(g_ready) / sizeof(g_ready[0])))
-                g_ready[g_nready++] = ReadyFn{fn, dev};
-        }
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
+    *e = cudaGetDevice(&dev);
+    if (*e != cudaSuccess) return nullptr;
+    for (int i = 0; i < g_nready; ++i)
+        if (g_ready[i].fn == fn && g_ready[i].dev == dev) return &g_ready[i];
+    cudaFuncAttributes fa;
+    *e = cudaFuncGetAttributes(&fa, fn);
+    if (*e == cudaSuccess)
+        *e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  g_dev[dev].smem_optin - static_cast<int>(fa.sharedSizeBytes));
+    // clusters of 16 CTAs are beyond the portable size of 8
+    if (*e == cudaSuccess) *e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    // the rings of several CTAs fit on one SM
+    if (*e == cudaSuccess && smem > 0)
+        *e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (*e != cudaSuccess || g_nready == static_cast<int>(sizeof(g_ready) / sizeof(g_ready[0]))) return nullptr;
+    g_ready[g_nready] = ReadyFn{fn, dev, {}};
+    return &g_ready[g_nready++];
+}
+
+static void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], dim3 grid, unsigned threads, int smem,
+                      int cluster, cudaStream_t stream)
+{
+    *cfg = {};
+    cfg->gridDim = grid;
+    cfg->blockDim = dim3(threads);
+    cfg->dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg->stream = stream;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = g_pdl.load() ? 1 : 0;
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg->attrs = attr;
+    cfg->numAttrs = cluster > 1 ? 2 : 1;
+}
+
+int resident_clusters(const void* fn, unsigned threads, int smem, int cluster)
+{
+    std::lock_guard<std::mutex> lock(g_mu);
+    cudaError_t e;
+    ReadyFn* const r = ready_fn(fn, smem, &e);
+    if (r == nullptr || cluster < 1 || cluster > 8) return 0;
+    if (r->clusters[cluster] == 0) {
+        cudaLaunchConfig_t cfg;
+        cudaLaunchAttribute attr[2];
+        configure(&cfg, attr, dim3(static_cast<unsigned>(cluster)), threads, smem, cluster, nullptr);
+        cfg.attrs = attr + 1;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        r->clusters[cluster] = n;
+    }
+    return r->clusters[cluster];
+}
+
+cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem, int cluster,
+                          cudaStream_t stream, void** args)
+{
+    cudaError_t e;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        ready_fn(fn, smem, &e);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    configure(&cfg, attr, grid, threads, smem, cluster, stream);
     e = cudaLaunchKernelExC(&cfg, fn, args);
     if (e == cudaSuccess) g_launches.fetch_add(1, std::memory_order_relaxed);
     return e;

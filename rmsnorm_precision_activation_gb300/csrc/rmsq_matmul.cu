@@ -56,6 +56,18 @@ static bool encode(CUtensorMap* map, const void* codes, long long rows, int k, i
     return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && make() == CUDA_SUCCESS;
 }
 
+// CTAs that share a tile's k: as many as let all tiles run at a time, each with at least 2 code stages.
+// What fits goes by the device's clusters of SMs, not by SMs alone: 100 x 2400 x 8192 (19 tiles of 128
+// tokens) takes 16.1 us in clusters of 6, of which 23 fit, and 26.2 in clusters of 8, of which 15 do.
+template <int NT> static int tc_cluster(long long tiles, int steps, const DeviceView& dv)
+{
+    const void* fn = reinterpret_cast<const void*>(&rmsq_matmul_tc_kernel<NT>);
+    int best = 1;
+    for (int c = 2; c <= 8 && c * 2 <= steps && c * tiles <= dv.sms * TcShape<NT>::CTAS; ++c)
+        if (tiles <= resident_clusters(fn, TcShape<NT>::THREADS, TcShape<NT>::SMEM, c)) best = c;
+    return best;
+}
+
 template <int NT> static cudaError_t launch_tc(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
 {
     CUtensorMap map_w, map_a;
@@ -64,12 +76,9 @@ template <int NT> static cudaError_t launch_tc(MatmulParams& p, const DeviceView
     t.n_tiles = static_cast<int>((p.n + kTcRows - 1) / kTcRows);
     t.m_tiles = static_cast<int>((p.m + NT - 1) / NT);
     const long long tiles = static_cast<long long>(t.n_tiles) * t.m_tiles;
-    // CTAs that share a tile's k: as many as the SMs hold, each with at least 2 code stages
     const long long slots = static_cast<long long>(dv.sms) * TcShape<NT>::CTAS;
     const int steps = (p.k + kTcCodes - 1) / kTcCodes;
-    long long cluster = slots / tiles < 8 ? slots / tiles : 8;
-    if (cluster > steps / 2) cluster = steps / 2;
-    if (cluster < 1) cluster = 1;
+    const int cluster = tc_cluster<NT>(tiles, steps, dv);
     const long long grid = cluster > 1 ? tiles * cluster : tiles < slots ? tiles : slots;
     void* args[] = {&map_w, &map_a, &p, &t};
     return launch_kernel(reinterpret_cast<const void*>(&rmsq_matmul_tc_kernel<NT>),
@@ -77,11 +86,11 @@ template <int NT> static cudaError_t launch_tc(MatmulParams& p, const DeviceView
                          static_cast<int>(cluster), stream, args);
 }
 
-static cudaError_t launch_pair(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
+template <int TOKENS> static cudaError_t launch_pair(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
 {
     // setmaxnreg moves registers that the launch must have
     static std::atomic<int> regs{0};
-    const void* fn = reinterpret_cast<const void*>(&rmsq_matmul_pair_kernel);
+    const void* fn = reinterpret_cast<const void*>(&rmsq_matmul_pair_kernel<TOKENS>);
     if (regs.load() == 0) {
         cudaFuncAttributes fa;
         const cudaError_t e = cudaFuncGetAttributes(&fa, fn);
@@ -90,24 +99,41 @@ static cudaError_t launch_pair(MatmulParams& p, const DeviceView& dv, cudaStream
     }
     if (regs.load() < kPairRegs) return cudaErrorInvalidConfiguration;
     CUtensorMap map_w, map_a;
-    if (!encode(&map_w, p.w, p.n, p.k, kTcRows) || !encode(&map_a, p.a, p.m, p.k, kPairHalf)) return cudaErrorUnknown;
+    if (!encode(&map_w, p.w, p.n, p.k, kTcRows) || !encode(&map_a, p.a, p.m, p.k, PairShape<TOKENS>::HALF)) return cudaErrorUnknown;
     TcTiles t;
     t.n_tiles = static_cast<int>((p.n + 2 * kTcRows - 1) / (2 * kTcRows));
-    t.m_tiles = static_cast<int>((p.m + kPairTokens - 1) / kPairTokens);
+    t.m_tiles = static_cast<int>((p.m + TOKENS - 1) / TOKENS);
     const long long tiles = static_cast<long long>(t.n_tiles) * t.m_tiles;
     const long long pairs = tiles < dv.sms / 2 ? tiles : dv.sms / 2;
     void* args[] = {&map_w, &map_a, &p, &t};
-    return launch_kernel(fn, dim3(static_cast<unsigned>(2 * pairs)), kTcThreads, kPairSmem, 2, stream, args);
+    return launch_kernel(fn, dim3(static_cast<unsigned>(2 * pairs)), kTcThreads, PairShape<TOKENS>::SMEM, 2, stream, args);
 }
 
+// The kernel, by tokens (GB300, weights from HBM, n x k = 8192 x 8192 where not given):
+//   up to 16: mma.sync, 17.0 us at 16 tokens (tcgen05: 18.4), but 23.9 at 32 (tcgen05: 19.4)
+//   up to 32, up to 64: tiles of 32 and 64 tokens, 19.4 and 21.5 us (of 128: 27.9)
+//   more: what takes least by the time of a step of 128 elements of k in each kernel (hundredths of a
+//   us, with a CTA or pair on every SM) and the steps its CTAs take one after another. Measured, in the
+//   order tiles of 128, pairs of 128, pairs of 192:  128 tokens 28.7, 35.1, 40.9 us;  200 44.9, 36.0, 42.2;
+//   512 83, 63, 74;  768 121, 90, 76;  4096 540, 386, 335;  1024 x 1024 x 8192 27.7, 34.8, 40.4.
 static cudaError_t launch_matmul(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
 {
     if (p.m <= 8) return launch_stream<1>(p, stream);
     if (p.m <= 16) return launch_stream<2>(p, stream);
     if (p.m <= 32) return launch_tc<32>(p, dv, stream);
     if (p.m <= 64) return launch_tc<64>(p, dv, stream);
-    if (p.m <= 256 || p.n <= 128) return launch_tc<128>(p, dv, stream);
-    return launch_pair(p, dv, stream);
+    const int steps = (p.k + kTcCodes - 1) / kTcCodes;
+    const auto tiles = [&](int channels, int tokens) {
+        return (p.n + channels - 1) / channels * ((p.m + tokens - 1) / tokens);
+    };
+    const auto waves = [](long long work, int places) { return (work + places - 1) / places; };
+    const long long one = tiles(kTcRows, 128);
+    const int cluster = tc_cluster<128>(one, steps, dv);
+    const long long t1 = waves(one, dv.sms) * ((steps + cluster - 1) / cluster) * 58;
+    const long long t128 = waves(tiles(2 * kTcRows, 128), dv.sms / 2) * steps * 42;
+    const long long t192 = waves(tiles(2 * kTcRows, 192), dv.sms / 2) * steps * 52;
+    if (t1 < t128 && t1 < t192) return launch_tc<128>(p, dv, stream);
+    return t128 < t192 ? launch_pair<128>(p, dv, stream) : launch_pair<192>(p, dv, stream);
 }
 
 }  // namespace rmsq

@@ -1,39 +1,48 @@
 // rmsq_matmul_pair.cuh -- the int8 product on the tensor cores for many tokens: a CTA pair per tile.
 //
 // As rmsq_matmul_tc_kernel, but two CTAs (a cluster of 2) share one MMA (cta_group::2) of 256 output
-// channels by 192 tokens: each converts its own 128 channels into its TMEM and half of the tokens
-// into its shared memory, and holds the sums of its channels for all 192 tokens. 192 rather than
-// 256, because two accumulators then fit TMEM beside the operand stages, and reading one out (2500
-// cycles per 8192 of MMA at 256, bound by the float-to-integer conversions) overlaps the next. Per product that
-// halves the codes a CTA turns into fp16 and the shared memory the MMA reads, which bound the
-// one-CTA kernel (shared memory moves 16-bit and 8-bit copies of both operands through one port).
+// channels by TOKENS tokens: each converts its own 128 channels into its TMEM and half of the tokens
+// into its shared memory, and holds the sums of its channels for all of the tokens. Per product that
+// halves the codes a CTA turns into fp16 and the shared memory the MMA reads, which bound the one-CTA
+// kernel (shared memory moves 8-bit and 16-bit copies of both operands through one port).
+//
+// Tiles have 192 tokens, or 128 where those fill the SMs better, rather than 256: two accumulators then
+// fit TMEM beside the operand stages, and reading one out (bound by the float-to-integer conversions, at
+// 256 tokens 2500 cycles per 8192 of MMA) overlaps the next one's products. Measured (GB300, boost clock):
+// 8192^3 in 621 us, 1770 TFLOP/s, 0.90 of what a plain fp16 product of the size reaches; pairs of 128
+// tokens 755 us, of 160 679; 256 tokens with one accumulator 863.
 //
 // The leader (rank 0) issues the MMAs. Its op_full and acc_empty barriers count arrivals of both
-// CTAs; its commits arrive in both. Copy rings are each CTA's own. The reading warps hold 96 sums
-// per thread, so registers move to them from the other warps (setmaxnreg).
+// CTAs; its commits arrive in both. Copy rings are each CTA's own. The reading warps hold TOKENS / 2
+// sums per thread, so registers move to them from the other warps (setmaxnreg).
 #pragma once
 
 #include "rmsq_matmul_tc.cuh"
 
 namespace rmsq {
 
-constexpr int kPairTokens = 192, kPairHalf = kPairTokens / 2;
-constexpr int kPairRaws = 6, kPairOps = 4;
-constexpr int kPairRawA = kTcRows * kTcCodes;                     // codes of 128 channels
-constexpr int kPairRaw = kPairRawA + kPairHalf * kTcCodes;        // and of 96 tokens
-constexpr int kPairOp = kPairHalf * kTcStep * 2;                  // 96 tokens in fp16
-static_assert(kPairRaw % 1024 == 0 && kPairOp % 1024 == 0 && kPairRawA % 1024 == 0, "swizzle atoms");
-static_assert(2 * kPairTokens + kPairOps * 32 <= 512, "two accumulators and the operand stages fill TMEM");
-constexpr int kPairSmem = 2048 + kPairRaws * kPairRaw + kPairOps * kPairOp;
-static_assert(kPairSmem > 116 * 1024 && kPairSmem <= 232448, "one CTA per SM");
+// Per tile width in tokens.
+template <int TOKENS> struct PairShape {
+    static constexpr int HALF = TOKENS / 2;                       // tokens whose codes a CTA brings and converts
+    static constexpr int RAWS = 6;                                // code stages
+    static constexpr int OPS = 4;                                 // operand stages
+    static constexpr int RAW_A = kTcRows * kTcCodes;              // codes of 128 channels
+    static constexpr int RAW = RAW_A + HALF * kTcCodes;           // and of half the tokens
+    static constexpr int OP = HALF * kTcStep * 2;                 // half the tokens in fp16
+    static constexpr int SMEM = 2048 + RAWS * RAW + OPS * OP;     // 1024 to align the ring, 1024 for barriers
+    static_assert(RAW % 1024 == 0 && OP % 1024 == 0 && RAW_A % 1024 == 0, "swizzle atoms");
+    static_assert(2 * TOKENS + OPS * 32 <= 512, "two accumulators and the operand stages fit TMEM");
+    static_assert(SMEM > 116 * 1024 && SMEM <= 232448, "one CTA per SM");
+};
 // registers: 12 warps give up what 8 take; the launch has kPairRegs for every thread
 constexpr int kPairRegs = 96, kPairRegsIssue = 32, kPairRegsConvert = 80, kPairRegsRead = 144;
 static_assert(128 * kPairRegsIssue + 256 * (kPairRegsConvert + kPairRegsRead) <= kTcThreads * kPairRegs, "within the launch's registers");
 
 // Arrive on the leader's barrier at this CTA's address bar. What the arrival publishes stays in this
 // CTA's own shared memory and TMEM, where the MMA reads it: fence.proxy.async and tcgen05.fence before
-// the arrival make it visible there, so the arrival need not release at cluster scope (which takes
-// about 1000 cycles behind the converting warps' stores: 863 us against 768 at 8192^3).
+// the arrival make it visible there, so the arrival need not release at cluster scope (which took about
+// 1000 cycles behind the converting warps' stores: 863 us against 768 at 8192^3 when it was tried, in
+// tiles of 256 tokens).
 __device__ __forceinline__ void mbar_arrive_leader(uint32_t bar)
 {
     asm volatile(
@@ -57,19 +66,21 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar)
         ::"r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
 }
 
+template <int TOKENS>
 __global__ void __launch_bounds__(kTcThreads, 1) __cluster_dims__(2, 1, 1)
 rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
                         const MatmulParams p, const TcTiles tiles)
 {
-    constexpr int RAWS = kPairRaws, OPS = kPairOps;
+    using S = PairShape<TOKENS>;
+    constexpr int RAWS = S::RAWS, OPS = S::OPS, HALF = S::HALF;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t tmem_slot;
 
     unsigned char* const smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     unsigned char* const raw = smem;
-    unsigned char* const ops = smem + RAWS * kPairRaw;
-    const uint32_t bars = smem_u32(ops + OPS * kPairOp);
+    unsigned char* const ops = smem + RAWS * S::RAW;
+    const uint32_t bars = smem_u32(ops + OPS * S::OP);
     const uint32_t raw_full = bars, raw_empty = raw_full + 8 * RAWS;
     const uint32_t op_full = raw_empty + 8 * RAWS, op_empty = op_full + 8 * OPS;
     const uint32_t acc_full = op_empty + 8 * OPS, acc_empty = acc_full + 16, drain = acc_empty + 16;
@@ -83,10 +94,10 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
 
     // Code stage s of a tile into this CTA's ring (one thread).
     auto fetch = [&](uint32_t slot, int s, int tn, int tm) {
-        const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw) + slot * kPairRaw;
-        mbar_arrive_expect_tx(full, kPairRaw);
+        const uint32_t full = raw_full + 8 * slot, dst = smem_u32(raw) + slot * S::RAW;
+        mbar_arrive_expect_tx(full, S::RAW);
         tma_load_2d(dst, &map_w, s * kTcCodes, (tn * 2 + rank) * kTcRows, full);
-        tma_load_2d(dst + kPairRawA, &map_a, s * kTcCodes, tm * kPairTokens + rank * kPairHalf, full);
+        tma_load_2d(dst + S::RAW_A, &map_a, s * kTcCodes, tm * TOKENS + rank * HALF, full);
     };
     int started = 0;                          // stages of the first tile fetched ahead
 
@@ -124,7 +135,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
     cluster_sync();                          // the other CTA's barriers are set up
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    const uint32_t tmem_a = tmem + 2 * kPairTokens;      // operand stages of 32 columns behind the accumulators
+    const uint32_t tmem_a = tmem + 2 * TOKENS;      // operand stages of 32 columns behind the accumulators
     pdl_wait();
 
     const uint32_t limit = wait_limit(p.timeout_ns), drain_limit = wait_limit(4 * p.timeout_ns);
@@ -154,7 +165,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                 atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
             }
         } else if (warp == 1 && rank == 0) {
-            constexpr uint32_t idesc = (1u << 4) | ((kPairTokens / 8u) << 17) | ((2u * kTcRows / 16u) << 24);
+            constexpr uint32_t idesc = (1u << 4) | ((TOKENS / 8u) << 17) | ((2u * kTcRows / 16u) << 24);
             const bool one = elect_one();
             const uint32_t desc0 = tc_desc_lo(smem_u32(ops));
             uint32_t slot = 0, phase = 0, chunks = 0;    // a code stage fills operand stages slot and slot + 1
@@ -168,7 +179,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                         ok = mbar_wait<SCOPE_CTA>(acc_empty + 8 * (chunks & 1u), ((chunks >> 1) & 1u) ^ 1u, limit);
                         ++chunks;
                     }
-                    const uint32_t buf = (chunks - 1) & 1u, acc = tmem + buf * kPairTokens;
+                    const uint32_t buf = (chunks - 1) & 1u, acc = tmem + buf * TOKENS;
                     const bool tail = --left == 0 || s == steps - 1;
                     const uint32_t next = slot + 2 == OPS ? 0 : slot + 2, next_phase = slot + 2 == OPS ? phase ^ 1u : phase;
                     if (!ready0) ok = ok && mbar_wait<SCOPE_CTA>(op_full + 8 * slot, phase, limit);
@@ -176,7 +187,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                     if (!ok) break;
                     tc_fence_after();
                     if (one) {
-                        tc_mma_step<true>(acc, tmem_a + slot * 32, desc0 + slot * (kPairOp / 16), idesc, fresh);
+                        tc_mma_step<true>(acc, tmem_a + slot * 32, desc0 + slot * (S::OP / 16), idesc, fresh);
                         tc_commit_pair(op_empty + 8 * slot);
                     }
                     __syncwarp();
@@ -187,7 +198,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                     const bool peek0 = mbar_test<SCOPE_CTA>(op_full + 8 * next, next_phase);
                     const bool peek1 = mbar_test<SCOPE_CTA>(op_full + 8 * next + 8, next_phase);
                     if (one) {
-                        tc_mma_step<true>(acc, tmem_a + slot * 32 + 32, desc0 + (slot + 1) * (kPairOp / 16), idesc, false);
+                        tc_mma_step<true>(acc, tmem_a + slot * 32 + 32, desc0 + (slot + 1) * (S::OP / 16), idesc, false);
                         tc_commit_pair(op_empty + 8 * slot + 8);
                         if (tail) tc_commit_pair(acc_full + 8 * buf);
                     }
@@ -208,6 +219,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
         __syncwarp();
     } else if (warp < 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsConvert));
+        constexpr int PB = (HALF * 4 + 127) / 128;    // a thread's pieces of the tokens' HALF x 4
         const int wg = (warp - 4) >> 2, t = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;     // this warp's TMEM lanes, in bits 16+
         uint32_t rs = 0, rphase = 0, os = wg, ophase = 0;
@@ -216,16 +228,16 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
             for (int s = 0; s < steps; ++s) {
                 if (!ready) ok = mbar_wait<SCOPE_CTA>(raw_full + 8 * rs, rphase, limit);
                 const uint32_t rnext = rs + 1 == RAWS ? 0 : rs + 1, rnext_phase = rs + 1 == RAWS ? rphase ^ 1u : rphase;
-                const uint32_t ra = smem_u32(raw) + rs * kPairRaw, rb = ra + kPairRawA;
-                const uint32_t ob = smem_u32(ops) + os * kPairOp;
-                // thread t: channel t, and three of the 96 x 4 pieces of the tokens; all loads first, to overlap
-                uint4 va[4], vb[3];
+                const uint32_t ra = smem_u32(raw) + rs * S::RAW, rb = ra + S::RAW_A;
+                const uint32_t ob = smem_u32(ops) + os * S::OP;
+                // thread t: channel t, and its pieces of the tokens; all loads first, to overlap
+                uint4 va[4], vb[PB];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) va[c] = ld_shared_v4(ra + t * 128 + (((4 * wg + c) ^ (t & 7)) << 4));
 #pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    const int i = j * 128 + t, r = i % kPairHalf, c = i / kPairHalf;
-                    vb[j] = ld_shared_v4(rb + r * 128 + (((4 * wg + c) ^ (r & 7)) << 4));
+                for (int j = 0; j < PB; ++j) {
+                    const int i = j * 128 + t, r = i % HALF, c = i / HALF;
+                    if (c < 4) vb[j] = ld_shared_v4(rb + r * 128 + (((4 * wg + c) ^ (r & 7)) << 4));
                 }
                 ok = ok && mbar_wait<SCOPE_CTA>(op_empty + 8 * os, ophase ^ 1u, limit);
                 ok = __all_sync(0xFFFFFFFFu, ok);
@@ -245,8 +257,9 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                     tmem_st_x16(tmem_a + lanes + os * 32 + c * 8, h);
                 }
 #pragma unroll
-                for (int j = 0; j < 3; ++j) {
-                    const int i = j * 128 + t, r = i % kPairHalf, c = i / kPairHalf;
+                for (int j = 0; j < PB; ++j) {
+                    const int i = j * 128 + t, r = i % HALF, c = i / HALF;
+                    if (c >= 4) continue;
                     uint4 lo, hi;
                     codes_to_half(vb[j].x, lo.x, lo.y);
                     codes_to_half(vb[j].y, lo.z, lo.w);
@@ -276,7 +289,6 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
         if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsRead));
-        constexpr int HALF = kPairHalf;
         const int wg = (warp - 12) >> 2, row = threadIdx.x & 127;
         const uint32_t base = tmem + (static_cast<uint32_t>(warp & 3) << 21) + wg * HALF;
         uint32_t chunks = 0;
@@ -293,11 +305,12 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
 #pragma unroll
                 for (int c = 0; c < HALF; c += 32) {
                     uint32_t v[32];
-                    tmem_ld_x16(base + buf * kPairTokens + c, v);
-                    tmem_ld_x16(base + buf * kPairTokens + c + 16, v + 16);
+                    tmem_ld_x16(base + buf * TOKENS + c, v);
+                    if (c + 16 < HALF) tmem_ld_x16(base + buf * TOKENS + c + 16, v + 16);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j < HALF) acc[c + j] += __float2int_rn(__uint_as_float(v[j]));
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -306,7 +319,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
             if (!ok) break;
             int tn, tm;
             tc_tile(tile, tiles, tn, tm);
-            const int n = (tn * 2 + rank) * kTcRows + row, m0 = tm * kPairTokens + wg * HALF;
+            const int n = (tn * 2 + rank) * kTcRows + row, m0 = tm * TOKENS + wg * HALF;
             if (n < p.n) {
                 const float ws = p.w_scale[n], b = p.bias ? load_as(p.bias, n, p.dt) : 0.f;
                 const float* const as = p.a_scale + m0;

@@ -109,6 +109,14 @@ def test_large():
 
 
 @gpu
+@pytest.mark.parametrize("m", [65, 100, 150, 200, 260, 500, 700, 1100])
+@pytest.mark.parametrize("n,k", [(2100, 528), (5000, 1040), (11003, 272), (130, 2064)])
+def test_each_kernel_for_many_tokens(m, n, k):
+    # widths at which tiles of 128 (with and without a shared k) and pairs of 128 and 192 tokens are taken
+    check(make(m, n, k, seed=m + n))
+
+
+@gpu
 @pytest.mark.parametrize("m", [1, 12, 24, 60, 100, 300])
 def test_first_call_of_a_thread(m):
     # a thread with no CUDA call of its own before; every tensor made elsewhere
