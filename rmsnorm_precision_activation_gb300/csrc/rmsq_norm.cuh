@@ -12,12 +12,7 @@
 //   M2 = sum_w M2_w + n_w (mean_w - mean)^2,
 // which costs one block barrier instead of two.
 //
-// Bound by HBM. Two kernels:
-//  - rmsq_norm_direct_kernel, rows of up to 16384 columns: straight into registers, each row by a warp or
-//    CTA of its own.
-//  - rmsq_norm_ring_kernel, wider rows: split over a cluster, whose CTAs would read gamma and beta anew with
-//    every row. They take several rows, which come through a ring of shared-memory slots filled by bulk
-//    copies, and keep gamma and beta in shared memory.
+// The kernel is rmsq_norm_kernel; this header also has what the other kernels of these operators share.
 #pragma once
 
 #include "rmsq_device.cuh"
@@ -27,20 +22,9 @@ namespace rmsq {
 enum { SCOPE_WARP = 0, SCOPE_CTA = 1, SCOPE_CLUSTER = 2 };    // threads of a row group, or that a wait acquires from
 enum { NORM_LAYER = 0, NORM_LAYER_INT8 = 1, NORM_RMS_INT8 = 2 };
 
-// The rows a kernel reads through its rings.
-struct RowTensors {
-    const void* in[3];     // tensors [rows x hidden]
-    long long total;       // bytes of one
-    int ntens;
-    int rows;
-    int hidden;
-    int slice;             // elements of a row per CTA
-    int stages;            // ring slots per row group
-    int slot;              // bytes of one tensor's row in a slot (multiple of 16)
-};
-
 struct NormParams {
-    RowTensors r;          // x, and the residual where there is one
+    const void* x;
+    const void* residual;  // or null
     void* res_out;         // or null
     const void* gamma;
     const void* beta;      // or null
@@ -48,11 +32,11 @@ struct NormParams {
     float* scale;          // int8: one per row
     float* mean;           // or null
     float* rstd;           // or null
-    int T;                 // threads per row group
+    int rows;
+    int hidden;
+    int slice;             // columns of a row per CTA of a cluster
     float eps;
     float offset;
-    unsigned int* err;
-    unsigned long long timeout_ns;
 };
 
 // One element of a 16-bit or 32-bit type, by type code.
@@ -234,27 +218,6 @@ template <int DT, int E> struct Deal {
     }
 };
 
-// Which of a thread's vectors have columns lo to hi at all, and which of those also have others. EDGE: bits,
-// the same for all rows of one shift, so that testing one is all a row costs.
-template <int DT, int E, bool FULL, bool EDGE> struct Part {
-    uint32_t some = 0, cut = 0;
-    int hi;
-    __device__ __forceinline__ Part(int t, int T, int lo, int hi_) : hi(hi_)
-    {
-        using D = Deal<DT, E>;
-        if (EDGE) {
-#pragma unroll
-            for (int c = 0; c < D::NC; ++c) {
-                const int k = D::col(c, t, T);
-                if (k < hi) some |= 1u << c;
-                if (k < hi && (k < lo || k + D::VW > hi)) cut |= 1u << c;
-            }
-        }
-    }
-    __device__ __forceinline__ bool in(int c, int k) const { return FULL || (EDGE ? (some >> c & 1u) != 0 : k < hi); }
-    __device__ __forceinline__ bool whole(int c) const { return !EDGE || !(cut >> c & 1u); }
-};
-
 // Zeros in place of a vector's columns outside lo to hi.
 template <int PV> __device__ __forceinline__ void clear_outside(float2 (&f)[PV], int k, int lo, int hi)
 {
@@ -277,101 +240,42 @@ template <int DT> __device__ __forceinline__ void store_inside(typename Scalar<D
         }
 }
 
-// Two 16-bit elements of a word, exact.
-template <int DT> __device__ __forceinline__ float2 unpack2(uint32_t w)
-{
-    if constexpr (DT == DT_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    else return make_float2(Scalar<DT>::get(static_cast<uint16_t>(w & 0xFFFFu)), Scalar<DT>::get(static_cast<uint16_t>(w >> 16)));
-}
-
-// A thread's share of gamma over all rows, as raw 32-bit words (two 16-bit elements each).
-template <int DT, int E, bool EDGE> struct Held {
-    using D = Deal<DT, E>;
-    using T = typename Scalar<DT>::T;
-    static constexpr int PER = 4 / sizeof(T), N = E / PER;
-    uint32_t w[N];
-
-    // Column k is p[k - lo] in columns lo to hi, 0 elsewhere.
-    __device__ __forceinline__ void load(const T* p, int t, int threads, int lo, int hi)
+// int8 codes of a row: y * 127 / amax to the nearest, even at ties. 127 / amax overflows for rows of tiny
+// y: those are scaled up by 2^100 first (exact). amax is NaN for a row with a NaN, and so is the scale;
+// the codes are then any.
+struct Coder {
+    float pre, inv;
+    __device__ __forceinline__ explicit Coder(float amax)
     {
+        pre = amax < 1e-30f ? 0x1p100f : 1.0f;
+        inv = amax > 0.f ? __fdiv_rn(127.0f, amax * pre) : 0.f;
+    }
+    // A vector of y at column k, of which the row has columns lo to hi. EDGE: perhaps not the whole of it.
+    template <bool EDGE, int PV>
+    __device__ __forceinline__ void store(float2 (&y)[PV], signed char* o, int k, int lo, int hi) const
+    {
+        constexpr int VW = 2 * PV;
+        if (pre != 1.0f) {
 #pragma unroll
-        for (int c = 0; c < D::NC; ++c) {
-            const int k = D::col(c, t, threads);
-            if constexpr (!EDGE) {
-                const uint4 v = k < hi ? ld_v4(p + k) : make_uint4(0, 0, 0, 0);
-                w[4 * c] = v.x;
-                w[4 * c + 1] = v.y;
-                w[4 * c + 2] = v.z;
-                w[4 * c + 3] = v.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < D::VW; j += PER) {
-                    uint32_t v = 0;
-#pragma unroll
-                    for (int q = 0; q < PER; ++q)
-                        if (k + j + q >= lo && k + j + q < hi) {
-                            if constexpr (PER == 1) v = __float_as_uint(p[k + j - lo]);
-                            else v |= static_cast<uint32_t>(p[k + j + q - lo]) << (16 * q);
-                        }
-                    w[(c * D::VW + j) / PER] = v;
-                }
-            }
+            for (int j = 0; j < PV; ++j) y[j] = mul2(y[j], splat(pre));
         }
-    }
-    // Keeps the compiler from holding the words unpacked across rows, which the registers do not allow.
-    __device__ __forceinline__ void pin()
-    {
+        // adding 1.5 * 2^23 rounds to nearest even and leaves the code in the low byte
+        uint32_t h[PV];
 #pragma unroll
-        for (int i = 0; i < N; ++i) asm volatile("" : "+r"(w[i]));
-    }
-    __device__ __forceinline__ float2 pair(int i) const          // elements 2 i and 2 i + 1
-    {
-        if constexpr (PER == 1) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
-        else return unpack2<DT>(w[i]);
+        for (int j = 0; j < PV; ++j) {
+            const float2 q = add2(mul2(y[j], splat(inv)), splat(12582912.0f));
+            h[j] = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x0040);
+        }
+        if (!EDGE || (k >= lo && k + VW <= hi)) {
+            if constexpr (PV == 4) st_v2(o + k, __byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
+            else st_u32(o + k, __byte_perm(h[0], h[1], 0x5410));
+        } else {
+#pragma unroll
+            for (int j = 0; j < VW; ++j)
+                if (k + j >= lo && k + j < hi) o[k + j] = static_cast<signed char>(h[j / 2] >> (8 * (j & 1)) & 0xFFu);
+        }
     }
 };
-
-// A thread's share of a row, columns lo to hi, as int8 codes of y * 127 / amax. 127 / amax overflows for
-// rows of tiny y: those are scaled up by 2^100 first (exact). amax is NaN for a row with a NaN, and so is
-// the scale; the codes are then any.
-template <int DT, int E, bool FULL, bool EDGE>
-__device__ __forceinline__ void store_codes(float2 (&v)[E / 2], float amax, signed char* o, int t, int T, int lo, int hi)
-{
-    using D = Deal<DT, E>;
-    constexpr int PV = D::PV, VW = D::VW;
-    const float pre = amax < 1e-30f ? 0x1p100f : 1.0f;
-    const float2 inv = splat(amax > 0.f ? __fdiv_rn(127.0f, amax * pre) : 0.f);
-    if (pre != 1.0f) {
-#pragma unroll
-        for (int j = 0; j < E / 2; ++j) v[j] = mul2(v[j], splat(pre));
-    }
-    // adding 1.5 * 2^23 rounds to nearest even and leaves the code in the low byte
-    const float2 magic = splat(12582912.0f);
-#pragma unroll
-    for (int c = 0; c < D::NC; ++c) {
-        const int k = D::col(c, t, T);
-        if (FULL || k < hi) {
-            uint32_t h[PV];
-#pragma unroll
-            for (int j = 0; j < PV; ++j) {
-                const float2 q = add2(mul2(v[c * PV + j], inv), magic);
-                h[j] = __byte_perm(__float_as_uint(q.x), __float_as_uint(q.y), 0x0040);
-            }
-            if (!EDGE || (k >= lo && k + VW <= hi)) {
-                if constexpr (PV == 4) st_v2(o + k, __byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
-                else st_u32(o + k, __byte_perm(h[0], h[1], 0x5410));
-            } else {
-#pragma unroll
-                for (int j = 0; j < VW; ++j)
-                    if (k + j >= lo && k + j < hi) o[k + j] = static_cast<signed char>(h[j / 2] >> (8 * (j & 1)) & 0xFFu);
-            }
-        }
-    }
-}
-
-// ------------------------------------------------------------------------------------------
-// Rows straight into registers
-// ------------------------------------------------------------------------------------------
 
 // The vector at column k of a tensor's row, which starts at element at (the row's columns lo to hi);
 // what is not the row's is not cleared. The last vector can reach past the tensor's `total` elements.
@@ -454,14 +358,32 @@ __device__ __forceinline__ uint4 load_param(const typename Scalar<DT>::T* p, int
     }
 }
 
-// A warp (SCOPE_WARP, rows of up to 1024 columns) or a CTA (up to 16384, 32 elements a thread) per row.
-// FULL: the threads' shares cover the row exactly, so nothing is checked. EDGE: rows whose width is no
-// whole number of vectors.
+
+// One CTA's v to slot `rank` of every CTA of the cluster (lanes of warp 0), and everybody's read back:
+// lane r of every warp gets rank r's, 0 past the cluster.
+__device__ __forceinline__ float2 cluster_exchange(float2* slots, int warp, int lane, int nc, int rank, float2 v)
+{
+    if (warp == 0 && lane < nc)
+        asm volatile(
+            "{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %0, %1;\n\tst.shared::cluster.v2.f32 [a], {%2, %3};\n\t}"
+            ::"r"(smem_u32(slots + rank)), "r"(lane), "f"(v.x), "f"(v.y) : "memory");
+    cluster_arrive_as(warp == 0);
+    cluster_wait();
+    return lane < nc ? slots[lane] : make_float2(0.f, 0.f);
+}
+
+// A warp, a CTA or a cluster per row, with E elements a thread: as fp32, or, 64 of 16 bits, packed as they
+// were read and unpacked for each use. FULL: the threads' shares cover the row (a CTA's slice of it)
+// exactly, so nothing is checked. EDGE: rows whose width is no whole number of vectors.
 // Every row has its own thread group and no loop: the hardware's CTA scheduler overlaps rows and evens
-// out SMs of unequal bandwidth. Bound by HBM with a residual and by instructions without one: 32
-// elements a thread halve what a row costs in reductions against 16.
+// out SMs of unequal bandwidth (CTAs that walk rows through rings in shared memory: 2048 x 65536 fp16 128
+// us against 108, 4096 x 20000 bf16 89 against 58, 512 x 20000 with residual 26 against 21). Bound by HBM
+// with a residual (16384 x 8192 bf16 154 us, 1.04 of the copy rate), by instructions without one (85 us,
+// 0.94); rows off 16-byte boundaries by instructions (8192 x 5121 bf16 54 us, 0.47: their parameters are
+// shifted into place and their accesses checked, twice the instructions; staging the shifted parameters in
+// shared memory for several rows took 58).
 template <int DT, int E, bool FULL, bool EDGE, int SCOPE, int KIND>
-__global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOPE_WARP ? 4 : 2) rmsq_norm_direct_kernel(const __grid_constant__ NormParams p)
+__global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOPE_WARP ? 4 : 2) rmsq_norm_kernel(const __grid_constant__ NormParams p)
 {
     using D = Deal<DT, E>;
     using S = Scalar<DT>;
@@ -471,66 +393,113 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
     constexpr int NC = D::NC, PV = D::PV, VW = D::VW;
     __shared__ float2 part[16];
     __shared__ float part_max[16];
+    __shared__ float2 cluster_part[2][16];          // sums, maxima
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int T = SCOPE == SCOPE_WARP ? 32 : blockDim.x;
     const int t = SCOPE == SCOPE_WARP ? lane : threadIdx.x;
     const int nwarps = SCOPE == SCOPE_WARP ? 1 : blockDim.x >> 5;
-    const int row = SCOPE == SCOPE_WARP ? static_cast<int>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+    const int nc = SCOPE == SCOPE_CLUSTER ? static_cast<int>(cluster_size()) : 1;
+    const int rank = SCOPE == SCOPE_CLUSTER ? static_cast<int>(cluster_rank()) : 0;
+    const int row = SCOPE == SCOPE_WARP ? static_cast<int>(blockIdx.x) * (blockDim.x >> 5) + warp
+                  : SCOPE == SCOPE_CTA  ? blockIdx.x : static_cast<int>(cluster_id());
+    if (SCOPE == SCOPE_CLUSTER) cluster_arrive_as(false);
     pdl_wait();
-    if (SCOPE == SCOPE_WARP && row >= p.r.rows) return;
+    if (SCOPE == SCOPE_WARP && row >= p.rows) return;
 
-    const int shift = EDGE ? static_cast<int>(static_cast<long long>(row) * p.r.hidden % VW) : 0;
-    const int lo = shift, hi = shift + p.r.hidden;
-    const long long at = static_cast<long long>(row) * p.r.hidden - shift;      // of column 0
-    const long long total = static_cast<long long>(p.r.rows) * p.r.hidden;
+    const int shift = EDGE ? static_cast<int>(static_cast<long long>(row) * p.hidden % VW) : 0;
+    const int c0 = SCOPE == SCOPE_CLUSTER ? rank * p.slice : 0;               // the CTA's first column
+    const int lo = SCOPE == SCOPE_CLUSTER ? max(shift - c0, 0) : shift;
+    const int hi = SCOPE == SCOPE_CLUSTER ? max(min(shift + p.hidden - c0, p.slice), 0) : shift + p.hidden;
+    const long long at = static_cast<long long>(row) * p.hidden - shift + c0; // of the CTA's first column
+    const long long total = static_cast<long long>(p.rows) * p.hidden;
     const auto in = [&](int c) { return FULL || D::col(c, t, T) < hi; };
     const auto whole = [&](int k) { return !EDGE || (k >= lo && k + VW <= hi); };
 
-    // ---- s into registers, fp32 (exact), 0 outside the row ----
-    float2 v[E / 2];
-    {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        uint4 raw[NC];
+    // ---- s into registers, exact, 0 outside the row: as fp32, or packed ----
+    constexpr bool PACKED = E > 32;
+    constexpr int BATCH = NC < 4 || DT == DT_F32 ? NC : 4;          // vectors in flight with a residual's
+    float2 v[PACKED ? 1 : E / 2];
+    uint4 raw[NC];
 #pragma unroll
-        for (int c = 0; c < NC; ++c)
-            raw[c] = in(c) ? load_columns<DT, EDGE>(static_cast<const TT*>(p.r.in[0]), at, total, D::col(c, t, T), hi) : zero;
-        if (p.r.ntens == 2) {
-            TT* const ro = static_cast<TT*>(p.res_out) + at;
-            uint4 add[NC];
+    for (int c = 0; c < NC; ++c)
+        raw[c] = in(c) ? load_columns<DT, EDGE>(static_cast<const TT*>(p.x), at, total, D::col(c, t, T), hi)
+                       : make_uint4(0, 0, 0, 0);
+    if (p.residual != nullptr) {
+        TT* const ro = static_cast<TT*>(p.res_out) + at;
 #pragma unroll
-            for (int c = 0; c < NC; ++c)
-                add[c] = in(c) ? load_columns<DT, EDGE>(static_cast<const TT*>(p.r.in[1]), at, total, D::col(c, t, T), hi) : zero;
+        for (int c0 = 0; c0 < NC; c0 += BATCH) {
+            uint4 add[BATCH];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
+            for (int c = 0; c < BATCH; ++c)
+                add[c] = in(c0 + c) ? load_columns<DT, EDGE>(static_cast<const TT*>(p.residual), at, total,
+                                                             D::col(c0 + c, t, T), hi)
+                                    : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = c0; c < c0 + BATCH; ++c) {
                 const int k = D::col(c, t, T);
-                raw[c] = Elem<DT>::add(raw[c], add[c]);
+                raw[c] = Elem<DT>::add(raw[c], add[c - c0]);
                 if (in(c)) {
                     if (whole(k)) st_v4(ro + k, raw[c]);
                     else store_inside<DT>(ro, raw[c], k, lo, hi);
                 }
             }
         }
+    }
 #pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            float2 f[PV];
-            Elem<DT>::pairs(raw[c], f);
-            if (!whole(D::col(c, t, T))) clear_outside(f, D::col(c, t, T), lo, hi);
+    for (int c = 0; c < NC; ++c) {
+        float2 f[PV];
+        Elem<DT>::pairs(raw[c], f);
+        if (!whole(D::col(c, t, T))) {
+            clear_outside(f, D::col(c, t, T), lo, hi);
+            if constexpr (PACKED) raw[c] = pack_pairs<DT>(f);
+        }
+        if constexpr (!PACKED) {
 #pragma unroll
             for (int j = 0; j < PV; ++j) v[c * PV + j] = f[j];
         }
     }
+    // Keeps the compiler from holding packed vectors unpacked from one use to the next, which the registers
+    // do not allow: 200 bytes of spills without. (It takes a zero that the compiler does not know.)
+    const uint32_t zero = static_cast<uint32_t>(p.hidden >> 31);
+    auto pin = [&]() {
+        if constexpr (PACKED) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                raw[c].x ^= zero;
+                raw[c].y ^= zero;
+                raw[c].z ^= zero;
+                raw[c].w ^= zero;
+                asm volatile("" : "+r"(raw[c].x), "+r"(raw[c].y), "+r"(raw[c].z), "+r"(raw[c].w));
+            }
+        }
+    };
+    // vector c
+    auto held = [&](int c, float2 (&f)[PV]) {
+        if constexpr (PACKED) {
+            Elem<DT>::pairs(raw[c], f);
+        } else {
+#pragma unroll
+            for (int j = 0; j < PV; ++j) f[j] = v[c * PV + j];
+        }
+    };
 
     // ---- mean and squares about it ----
     const int n_w = FULL ? 32 * E : D::count(SCOPE == SCOPE_WARP ? 0 : warp * 32, T, lo, hi);
     float sum = 0.f, m2, mean = 0.f;
     if constexpr (!RMS) {
-        float2 a = v[0];
+        float2 a = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 1; j < E / 2; ++j) a = add2(a, v[j]);
+        for (int c = 0; c < NC; ++c) {
+            float2 f[PV];
+            held(c, f);
+#pragma unroll
+            for (int j = 0; j < PV; ++j) a = add2(a, f[j]);
+        }
         sum = warp_sum(a.x + a.y);
         mean = FULL ? sum * (1.0f / (32 * E)) : n_w > 0 ? __fdividef(sum, static_cast<float>(n_w)) : 0.f;
     }
+    pin();
     {
         const float2 m = splat(-mean);
         float2 a = make_float2(0.f, 0.f);
@@ -538,8 +507,9 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
         for (int c = 0; c < NC; ++c) {
             if (in(c)) {
                 float2 d[PV];
+                held(c, d);
 #pragma unroll
-                for (int j = 0; j < PV; ++j) d[j] = add2(v[c * PV + j], m);
+                for (int j = 0; j < PV; ++j) d[j] = add2(d[j], m);
                 if (!whole(D::col(c, t, T))) clear_outside(d, D::col(c, t, T), lo, hi);
 #pragma unroll
                 for (int j = 0; j < PV; ++j) a = fma2(d[j], d[j], a);
@@ -547,14 +517,15 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
         }
         m2 = warp_sum(a.x + a.y);
     }
-    const float inv_h = __frcp_rn(static_cast<float>(p.r.hidden));
+    const float inv_h = __frcp_rn(static_cast<float>(p.hidden));
     if constexpr (SCOPE != SCOPE_WARP) {
         if (lane == 0) part[warp] = make_float2(sum, m2);
         __syncthreads();
         const float2 q = lane < nwarps ? part[lane] : make_float2(0.f, 0.f);
         float d = 0.f, n_l = 0.f;
         if constexpr (!RMS) {
-            mean = warp_sum(q.x) * inv_h;
+            sum = warp_sum(q.x);
+            mean = sum * (SCOPE == SCOPE_CTA ? inv_h : hi > lo ? 1.0f / static_cast<float>(hi - lo) : 0.f);
             if (lane < nwarps) {
                 n_l = FULL ? static_cast<float>(32 * E) : static_cast<float>(D::count(lane * 32, T, lo, hi));
                 d = FULL ? q.x * (1.0f / (32 * E)) - mean : n_l > 0.f ? __fdividef(q.x, n_l) - mean : 0.f;
@@ -562,449 +533,104 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
         }
         m2 = warp_sum(fmaf(n_l * d, d, q.y));
     }
+    if constexpr (SCOPE == SCOPE_CLUSTER) {
+        cluster_wait();                               // the other CTAs have started
+        const float2 q = cluster_exchange(cluster_part[0], warp, lane, nc, rank, make_float2(sum, m2));
+        float d = 0.f, n_r = 0.f;
+        if constexpr (!RMS) {
+            mean = warp_sum(q.x) * inv_h;
+            if (lane < nc) {
+                n_r = static_cast<float>(max(min(shift + p.hidden - lane * p.slice, p.slice), 0) - (lane == 0 ? shift : 0));
+                d = n_r > 0.f ? __fdividef(q.x, n_r) - mean : 0.f;
+            }
+        }
+        m2 = warp_sum(fmaf(n_r * d, d, q.y));
+    }
     const float rstd = __frsqrt_rn(fmaf(m2, inv_h, p.eps));
 
     // ---- y ----
+    pin();
     const float2 m = splat(-mean), r2 = splat(rstd), offset = splat(p.offset);
     const TT* const gamma = static_cast<const TT*>(p.gamma);
     const TT* const beta = static_cast<const TT*>(p.beta);
-    float amax = 0.f;
+    auto norm = [&](int c, int k, float2 (&y)[PV]) {
+        float2 w[PV], b[PV];
+        Elem<DT>::pairs(load_param<DT, EDGE>(gamma, c0 + k, shift, p.hidden), w);
+        if (p.offset != 0.f) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        if (in(c)) {
+            for (int j = 0; j < PV; ++j) w[j] = add2(w[j], offset);
+        }
+        if (!RMS && beta != nullptr) {
+            Elem<DT>::pairs(load_param<DT, EDGE>(beta, c0 + k, shift, p.hidden), b);
+        } else {
+#pragma unroll
+            for (int j = 0; j < PV; ++j) b[j] = make_float2(0.f, 0.f);
+        }
+        held(c, y);
+#pragma unroll
+        for (int j = 0; j < PV; ++j) {
+            if constexpr (RMS) y[j] = mul2(mul2(y[j], r2), w[j]);
+            else y[j] = fma2(mul2(add2(y[j], m), r2), w[j], b[j]);
+        }
+    };
+    const bool leader = t == 0 && rank == 0;
+    if constexpr (!INT8) {
+        TT* const o = static_cast<TT*>(p.out) + at;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
             const int k = D::col(c, t, T);
-            float2 w[PV], b[PV];
-            Elem<DT>::pairs(load_param<DT, EDGE>(gamma, k, shift, p.r.hidden), w);
-            if (p.offset != 0.f) {
-#pragma unroll
-                for (int j = 0; j < PV; ++j) w[j] = add2(w[j], offset);
+            if (in(c)) {
+                float2 y[PV];
+                norm(c, k, y);
+                const uint4 v4 = pack_pairs<DT>(y);
+                if (whole(k)) st_v4(o + k, v4);
+                else store_inside<DT>(o, v4, k, lo, hi);
             }
-            if (!RMS && beta != nullptr) {
-                Elem<DT>::pairs(load_param<DT, EDGE>(beta, k, shift, p.r.hidden), b);
-            } else {
+        }
+        if (leader) {
+            if (p.mean) p.mean[row] = mean;
+            if (p.rstd) p.rstd[row] = rstd;
+        }
+    } else {
+        // packed rows form y twice, for want of registers
+        float amax = 0.f;
 #pragma unroll
-                for (int j = 0; j < PV; ++j) b[j] = make_float2(0.f, 0.f);
-            }
-            float2 y[PV];
-#pragma unroll
-            for (int j = 0; j < PV; ++j) {
-                if constexpr (RMS) y[j] = mul2(mul2(v[c * PV + j], r2), w[j]);
-                else y[j] = fma2(mul2(add2(v[c * PV + j], m), r2), w[j], b[j]);
-            }
-            if constexpr (INT8) {
+        for (int c = 0; c < NC; ++c) {
+            const int k = D::col(c, t, T);
+            if (in(c)) {
+                float2 y[PV];
+                norm(c, k, y);
                 if (!whole(k)) clear_outside(y, k, lo, hi);
 #pragma unroll
                 for (int j = 0; j < PV; ++j) {
                     amax = max3_nan(amax, fabsf(y[j].x), fabsf(y[j].y));
-                    v[c * PV + j] = y[j];
+                    if constexpr (!PACKED) v[c * PV + j] = y[j];
                 }
-            } else {
-                TT* const o = static_cast<TT*>(p.out) + at;
-                const uint4 raw = pack_pairs<DT>(y);
-                if (whole(k)) st_v4(o + k, raw);
-                else store_inside<DT>(o, raw, k, lo, hi);
+                if constexpr (PACKED) asm volatile("" : "+f"(amax));      // before the next vectors' loads
             }
         }
-    }
-    const bool leader = t == 0;
-    if constexpr (INT8) {
         amax = warp_max_nan(amax);
         if constexpr (SCOPE != SCOPE_WARP) {
             if (lane == 0) part_max[warp] = amax;
             __syncthreads();
             amax = warp_max_nan(lane < nwarps ? part_max[lane] : 0.f);
         }
-        store_codes<DT, E, FULL, EDGE>(v, amax, static_cast<signed char*>(p.out) + at, t, T, lo, hi);
-        if (leader) p.scale[row] = amax / 127.0f;
-    } else if (leader) {
-        if (p.mean) p.mean[row] = mean;
-        if (p.rstd) p.rstd[row] = rstd;
-    }
-}
-
-// ------------------------------------------------------------------------------------------
-// Rows through shared memory
-// ------------------------------------------------------------------------------------------
-
-constexpr int kRingStages = 8;      // slots per group at most
-constexpr int kRingGroups = 16;     // row groups per CTA at most
-// The rows a group works on: `first`, and every `stride`-th from there. Group g of cluster c starts at
-// row g * clusters + c; the host makes the number of clusters a multiple of the rows after which the shift
-// repeats (or gives every group one row at most), so a CTA's rows have one shift.
-struct Rows {
-    int first, stride, n;
-    __device__ __forceinline__ Rows(int group, int groups, int rows)
-    {
-        const int clusters = static_cast<int>(cluster_count());
-        first = group * clusters + static_cast<int>(cluster_id());
-        stride = clusters * groups;
-        n = first < rows ? (rows - first + stride - 1) / stride : 0;
-    }
-};
-
-constexpr int kRingBars = 2 * kRingStages * kRingGroups * 8;      // bytes of barriers
-
-// A row group's ring of slots: its next rows, brought by bulk copies while the group works. EDGE: rows of
-// a width that is no whole number of vectors, taken from the 16-byte boundary below. The group's rows all
-// have the same shift (Rows).
-template <int DT, bool EDGE> struct RowRing {
-    using T = typename Scalar<DT>::T;
-    static constexpr int ES = sizeof(T), VW = Elem<DT>::EPV;
-    const RowTensors& r;
-    int c0;                        // the CTA's first column
-    int lo, hi;                    // its columns that are the row's, from c0 on
-    int shift;                     // of the rows
-    uint32_t bars, base;           // shared addresses of the group's barriers (kRingStages full, as many
-                                   // empty) and slots
-    __device__ __forceinline__ uint32_t full(int stage) const { return bars + 8 * stage; }
-    __device__ __forceinline__ uint32_t empty(int stage) const { return bars + 8 * (kRingStages + stage); }
-
-    __device__ __forceinline__ uint32_t at(uint32_t stage, int i) const { return base + (stage * r.ntens + i) * r.slot; }
-    // Where the CTA's first column of a row is in a tensor, in elements (whole vectors).
-    __device__ __forceinline__ long long origin(int row) const { return static_cast<long long>(row) * r.hidden - shift + c0; }
-
-    // One row's pieces of every tensor into a slot (one thread).
-    __device__ __forceinline__ void fetch(int row, uint32_t stage, uint64_t policy) const
-    {
-        const long long a0 = origin(row) * ES;
-        long long a1 = a0 + (hi + VW - 1) / VW * 16;
-        if (EDGE && a1 > (r.total & ~15LL)) a1 = r.total & ~15LL;
-        const uint32_t bytes = hi > lo && a1 > a0 ? static_cast<uint32_t>(a1 - a0) : 0u;
-        if (EDGE && hi > lo) {
-            // the tensors' last bytes, which no whole piece covers, by hand (before the arrival below)
-            const long long end = origin(row) + hi;
-            for (long long e = a1 / ES; e < end; ++e)
-                for (int i = 0; i < r.ntens; ++i) {
-                    const uint32_t to = at(stage, i) + static_cast<uint32_t>(e * ES - a0);
-                    const T v = static_cast<const T*>(r.in[i])[e];
-                    if constexpr (ES == 2) asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
-                    else asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
-                }
-        }
-        mbar_arrive_expect_tx(full(stage), bytes * r.ntens);
-        if (bytes > 0)
-            for (int i = 0; i < r.ntens; ++i)
-                bulk_load(at(stage, i), static_cast<const unsigned char*>(r.in[i]) + a0, bytes, full(stage), policy);
-    }
-
-    // The vector at column k of tensor i, as raw bits; what is not the row's is not cleared.
-    __device__ __forceinline__ uint4 vec(uint32_t stage, int i, int k) const { return ld_shared_v4(at(stage, i) + k * ES); }
-
-    // One thread sets the barriers up: a slot is empty when `warps` warps have left it.
-    __device__ __forceinline__ void init(int warps) const
-    {
-        for (int i = 0; i < r.stages; ++i) {
-            mbar_init(full(i), 1);
-            mbar_init(empty(i), warps);
-        }
-    }
-
-    // Brings the group's rows (one thread of the CTA's copying warp: issuing a row's copies takes about
-    // 1000 cycles, which a working warp would keep its group waiting for). After a wait that ran out,
-    // waits (bounded) for the copies in flight, so that they end before the CTA does.
-    __device__ __forceinline__ void feed(const Rows& rows, unsigned long long timeout_ns, unsigned int* err) const
-    {
-        const uint64_t policy = l2_evict_normal_policy();
-        const uint32_t limit = wait_limit(timeout_ns);
-        int stage = 0, phase = 1, i = 0;
-        for (; i < rows.n; ++i) {
-            if (!mbar_wait<SCOPE_CTA>(empty(stage), phase, limit)) break;
-            fence_proxy_async_smem();
-            fetch(rows.first + i * rows.stride, stage, policy);
-            if (++stage == r.stages) {
-                stage = 0;
-                phase ^= 1;
-            }
-        }
-        if (i < rows.n) {
-            bool drained = true;
-            for (int j = i > r.stages ? i - r.stages : 0; j < i; ++j)
-                drained &= mbar_wait<SCOPE_CTA>(full(j % r.stages), (j / r.stages) & 1, wait_limit(4 * timeout_ns));
-            atomicOr(err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
-        }
-    }
-};
-
-// The threads of a row group (T a multiple of 32).
-__device__ __forceinline__ void group_sync(int group, int T)
-{
-    if (T == 32) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(T) : "memory");
-}
-
-// A row's sums among the CTAs of a cluster: each writes its own into a slot of every CTA, which counts
-// the bytes on its own barrier. Two sets in turn: a CTA sends a row's sums after it has read those of
-// the row before, so nobody writes a set that is still read. No cluster barrier, which the copying
-// warp would have to join; every wait is bounded.
-struct ClusterSums {
-    uint32_t bars, slots;          // shared addresses: 2 barriers, [2][16] float4
-    int nc, rank;
-    static constexpr int BYTES = 16 + 2 * 16 * 16;
-
-    __device__ __forceinline__ void init() const
-    {
-        mbar_init(bars, 1);
-        mbar_init(bars + 8, 1);
-    }
-    // By the lanes of one warp.
-    __device__ __forceinline__ void send(int lane, int flip, float4 v) const
-    {
-        const uint32_t bar = bars + 8 * flip, slot = slots + (flip * 16 + rank) * 16;
-        if (lane == 0) mbar_arrive_expect_tx(bar, nc * 16);
-        if (lane < nc)
-            asm volatile(
-                "{\n\t.reg .b32 a, b;\n\tmapa.shared::cluster.u32 a, %0, %2;\n\tmapa.shared::cluster.u32 b, %1, %2;\n\t"
-                "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [a], {%3, %4, %5, %6}, [b];\n\t}"
-                ::"r"(slot), "r"(bar), "r"(lane), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-    }
-    // Lane r of every warp gets rank r's (zeros past the cluster); false: the wait ran out.
-    __device__ __forceinline__ bool receive(int lane, int flip, int phase, uint32_t limit_ns, float4& v) const
-    {
-        const bool ok = mbar_wait<SCOPE_CLUSTER>(bars + 8 * flip, phase, limit_ns);
-        v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (lane < nc) {
-            const uint4 w = ld_shared_v4(slots + (flip * 16 + lane) * 16);
-            v = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-        }
-        return ok;
-    }
-};
-
-constexpr int kRingSlice = 16384;             // bytes of a tensor's row per CTA at most
-constexpr int kRingWorkers = 256;             // threads that work on rows; a warp more copies
-
-// Shared memory before gamma, beta and the ring: barriers, the groups' warp sums and maxima (each for
-// two rows in turn: one barrier a row then keeps a row's from the next but one's), the cluster's sums.
-constexpr int kNormHead = (kRingBars + 2 * 8 * 8 + 2 * 8 * 4 + 2 * ClusterSums::BYTES + 127) / 128 * 128;
-
-template <int DT, int E, bool EDGE, bool FULL, int KIND>
-__global__ void __launch_bounds__(kRingWorkers + 32, 3) rmsq_norm_ring_kernel(const __grid_constant__ NormParams p)
-{
-    using D = Deal<DT, E>;
-    using S = Scalar<DT>;
-    using TT = typename S::T;
-    constexpr bool RMS = KIND == NORM_RMS_INT8;
-    constexpr bool INT8 = KIND != NORM_LAYER;
-    constexpr int VW = D::VW, NC = D::NC, PV = D::PV;
-    extern __shared__ __align__(128) unsigned char smem[];
-
-    float2* const part = reinterpret_cast<float2*>(smem + kRingBars);
-    float* const part_max = reinterpret_cast<float*>(part + 16);
-    unsigned char* const cluster_part = reinterpret_cast<unsigned char*>(part_max + 16);
-
-    const int T = p.T, thread = threadIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = T >> 5;
-    const int nc = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-
-    const bool copies = threadIdx.x >= T;
-    const Rows rows(0, 1, p.r.rows);
-    const int c0 = rank * p.r.slice;
-    const int shift = EDGE ? static_cast<int>(static_cast<long long>(rows.first) * p.r.hidden % VW) : 0;
-    const int lo = max(shift - c0, 0), hi = FULL ? p.r.slice : max(min(shift + p.r.hidden - c0, p.r.slice), 0);
-    const RowRing<DT, EDGE> ring{p.r, c0, lo, hi, shift, smem_u32(smem),
-                                 smem_u32(smem + kNormHead) + 2 * p.r.slot};
-    const ClusterSums sums{smem_u32(cluster_part), smem_u32(cluster_part + 16), nc, rank};
-    const ClusterSums maxima{sums.bars + ClusterSums::BYTES, sums.slots + ClusterSums::BYTES, nc, rank};
-
-    const bool has_res = p.r.ntens == 2;
-    if (copies && lane == 0) {
-        ring.init(warps);
-        sums.init();
-        maxima.init();
-        fence_mbar_init();
-        fence_proxy_async_smem();
-    }
-    __syncthreads();
-    cluster_sync();                               // the other CTAs' barriers are set up
-    pdl_wait();
-    if (copies) {
-        if (lane == 0) ring.feed(rows, p.timeout_ns, p.err);
-        return;
-    }
-
-    // gamma and beta of the slice stay in shared memory, in their own type
-    TT* const ws = reinterpret_cast<TT*>(smem + kNormHead);
-    TT* const bs = reinterpret_cast<TT*>(smem + kNormHead + p.r.slot);
-    const TT* const gamma = static_cast<const TT*>(p.gamma) + (c0 - shift);
-    const TT* const beta = p.beta != nullptr ? static_cast<const TT*>(p.beta) + (c0 - shift) : nullptr;
-    if constexpr (!EDGE) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        for (int k = threadIdx.x * VW; k < hi; k += T * VW) {
-            st_shared_v4(smem_u32(ws + k), ld_v4(gamma + k));
-            st_shared_v4(smem_u32(bs + k), beta != nullptr ? ld_v4(beta + k) : zero);
-        }
-    } else {
-#pragma unroll 4
-        for (int k = lo + threadIdx.x; k < hi; k += T) {
-            const TT w = gamma[k], b = beta != nullptr ? beta[k] : TT(0);
-            ws[k] = w;
-            bs[k] = b;
-        }
-    }
-    asm volatile("bar.sync 15, %0;" ::"r"(T) : "memory");
-
-    // Counts of elements and their reciprocals: this warp's, lane's warp's of the group, the CTA's, lane's
-    // CTA's of the cluster. A count that is not a power of two makes a mean off by half a step more.
-    const uint32_t limit = wait_limit(p.timeout_ns);
-    const auto inverse = [](int k) { return k > 0 ? 1.0f / static_cast<float>(k) : 0.f; };
-    const Part<DT, E, FULL, EDGE> mine(thread, T, lo, hi);
-    const int n_w = FULL ? 32 * E : D::count(warp * 32, T, lo, hi);
-    const int n_l = lane >= warps ? 0 : FULL ? 32 * E : D::count(lane * 32, T, lo, hi);
-    const int n_r = lane < nc
-                        ? max(min(shift + p.r.hidden - lane * p.r.slice, p.r.slice), 0) - (lane == 0 ? shift : 0) : 0;
-    const float inv_w = inverse(n_w), inv_l = inverse(n_l), inv_c = inverse(hi - lo), inv_r = inverse(n_r);
-    const float inv_h = 1.0f / static_cast<float>(p.r.hidden), f_l = static_cast<float>(n_l), f_r = static_cast<float>(n_r);
-    bool dead = false;                            // a wait ran out: finish without waiting again
-    int stage = 0, phase = 0;
-    int flip = 0;
-    for (int i = 0; i < rows.n; ++i) {
-        // made opaque to the compiler again and again, which would keep every element's address and test
-        // in registers from row to row and from phase to phase
-        int t = thread;
-        asm volatile("" : "+r"(t));
-        const int row = rows.first + i * rows.stride;
-        if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage), phase, limit)) dead = true;
-        const long long at = ring.origin(row);
-
-        // ---- s into registers, fp32 (exact), 0 outside the slice ----
-        float2 v[E / 2];
-        {
-            TT* const ro = static_cast<TT*>(p.res_out) + at;
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int k = D::col(c, t, T);
-                uint4 raw = make_uint4(0, 0, 0, 0);
-                if (mine.in(c, k)) {
-                    raw = ring.vec(stage, 0, k);
-                    if (has_res) {
-                        raw = Elem<DT>::add(raw, ring.vec(stage, 1, k));
-                        if (mine.whole(c)) st_v4(ro + k, raw);
-                        else store_inside<DT>(ro, raw, k, lo, hi);
-                    }
-                }
-                float2 f[PV];
-                Elem<DT>::pairs(raw, f);
-                if (!mine.whole(c)) clear_outside(f, k, lo, hi);
-#pragma unroll
-                for (int j = 0; j < PV; ++j) v[c * PV + j] = f[j];
-            }
-        }
-
-        // ---- mean and squares about it ----
-        asm volatile("" : "+r"(t));
-        float sum = 0.f, m2, mean = 0.f;
-        if constexpr (!RMS) {
-            float2 a = v[0];
-#pragma unroll
-            for (int j = 1; j < E / 2; ++j) a = add2(a, v[j]);
-            sum = warp_sum(a.x + a.y);
-            mean = sum * inv_w;
-        }
-        {
-            const float2 m = splat(-mean);
-            float2 a = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int k = D::col(c, t, T);
-                if (mine.in(c, k)) {
-                    float2 d[PV];
-#pragma unroll
-                    for (int j = 0; j < PV; ++j) d[j] = add2(v[c * PV + j], m);
-                    if (!mine.whole(c)) clear_outside(d, k, lo, hi);
-#pragma unroll
-                    for (int j = 0; j < PV; ++j) a = fma2(d[j], d[j], a);
-                }
-            }
-            m2 = warp_sum(a.x + a.y);
-        }
-        if (lane == 0) mbar_arrive(ring.empty(stage));       // the warp has read the slot
-        if (lane == 0) part[flip * 8 + warp] = make_float2(sum, m2);
-        group_sync(0, T);
-        {
-            const float2 q = lane < warps ? part[flip * 8 + lane] : make_float2(0.f, 0.f);
-            float d = 0.f;
-            if constexpr (!RMS) {
-                sum = warp_sum(q.x);
-                mean = sum * inv_c;
-                d = f_l > 0.f ? q.x * inv_l - mean : 0.f;
-            }
-            m2 = warp_sum(fmaf(f_l * d, d, q.y));
-        }
-        {
-            float4 q;
-            if (warp == 0) sums.send(lane, flip, make_float4(sum, m2, 0.f, 0.f));
-            if (!sums.receive(lane, flip, (i >> 1) & 1, dead ? 0 : limit, q)) dead = true;
-            float d = 0.f;
-            if constexpr (!RMS) {
-                mean = warp_sum(q.x) * inv_h;
-                d = f_r > 0.f ? q.x * inv_r - mean : 0.f;
-            }
-            m2 = warp_sum(fmaf(f_r * d, d, q.y));
-        }
-        const float rstd = __frsqrt_rn(m2 * inv_h + p.eps);
-
-        // ---- y ----
-        asm volatile("" : "+r"(t));
-        const float2 m = splat(-mean), r2 = splat(rstd);
-        float amax = 0.f;
-        TT* const o = static_cast<TT*>(p.out) + at;
+        if constexpr (SCOPE == SCOPE_CLUSTER)
+            amax = warp_max_nan(cluster_exchange(cluster_part[1], warp, lane, nc, rank, make_float2(amax, 0.f)).x);
+        const Coder coder(amax);
+        pin();
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int k = D::col(c, t, T);
-            if (mine.in(c, k)) {
-                float2 w[PV], b[PV];
-                Elem<DT>::pairs(ld_shared_v4(smem_u32(ws + k)), w);
-                Elem<DT>::pairs(ld_shared_v4(smem_u32(bs + k)), b);
-                if (p.offset != 0.f) {
-#pragma unroll
-                    for (int j = 0; j < PV; ++j) w[j] = add2(w[j], splat(p.offset));
-                }
+            if (in(c)) {
                 float2 y[PV];
-#pragma unroll
-                for (int j = 0; j < PV; ++j) {
-                    if constexpr (RMS) y[j] = mul2(mul2(v[c * PV + j], r2), w[j]);
-                    else y[j] = fma2(mul2(add2(v[c * PV + j], m), r2), w[j], b[j]);
-                }
-                if constexpr (INT8) {
-                    if (!mine.whole(c)) clear_outside(y, k, lo, hi);
-#pragma unroll
-                    for (int j = 0; j < PV; ++j) {
-                        amax = max3_nan(amax, fabsf(y[j].x), fabsf(y[j].y));
-                        v[c * PV + j] = y[j];
-                    }
-                } else {
-                    const uint4 raw = pack_pairs<DT>(y);
-                    if (mine.whole(c)) st_v4(o + k, raw);
-                    else store_inside<DT>(o, raw, k, lo, hi);
-                }
+                if constexpr (PACKED) norm(c, k, y);
+                else held(c, y);
+                coder.store<EDGE>(y, static_cast<signed char*>(p.out) + at, k, lo, hi);
             }
         }
-        const bool leader = t == 0 && rank == 0;
-        if constexpr (INT8) {
-            amax = warp_max_nan(amax);
-            if (lane == 0) part_max[flip * 8 + warp] = amax;
-            group_sync(0, T);
-            amax = warp_max_nan(lane < warps ? part_max[flip * 8 + lane] : 0.f);
-            float4 q;
-            if (warp == 0) maxima.send(lane, flip, make_float4(amax, 0.f, 0.f, 0.f));
-            if (!maxima.receive(lane, flip, (i >> 1) & 1, dead ? 0 : limit, q)) dead = true;
-            amax = warp_max_nan(q.x);
-            asm volatile("" : "+r"(t));
-            signed char* const codes = static_cast<signed char*>(p.out) + at;
-            store_codes<DT, E, FULL, EDGE>(v, amax, codes, t, T, lo, hi);
-            if (leader) p.scale[row] = amax / 127.0f;
-        } else if (leader) {
-            if (p.mean) p.mean[row] = mean;
-            if (p.rstd) p.rstd[row] = rstd;
-        }
-        flip ^= 1;
-        if (++stage == p.r.stages) {
-            stage = 0;
-            phase ^= 1u;
-        }
+        if (leader) p.scale[row] = amax / 127.0f;
     }
-    if (dead && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
-    cluster_sync();                               // nobody sends to a CTA that has left
 }
 
 }  // namespace rmsq

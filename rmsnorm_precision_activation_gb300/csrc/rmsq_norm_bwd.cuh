@@ -21,6 +21,18 @@
 
 namespace rmsq {
 
+// The rows a kernel reads through its rings.
+struct RowTensors {
+    const void* in[3];     // tensors [rows x hidden]
+    long long total;       // bytes of one
+    int ntens;
+    int rows;
+    int hidden;
+    int slice;             // elements of a row per CTA
+    int stages;            // ring slots per row group
+    int slot;              // bytes of one tensor's row in a slot (multiple of 16)
+};
+
 struct NormBwdParams {
     RowTensors r;            // dy, s, and dres where there is one
     const void* gamma;
@@ -43,6 +55,227 @@ struct NormBwdReduceParams {
     int hidden;
     int dt;                  // type of dgamma and dbeta
 };
+
+// Which of a thread's vectors have columns lo to hi at all, and which of those also have others. EDGE: bits,
+// the same for all rows of one shift, so that testing one is all a row costs.
+template <int DT, int E, bool FULL, bool EDGE> struct Part {
+    uint32_t some = 0, cut = 0;
+    int hi;
+    __device__ __forceinline__ Part(int t, int T, int lo, int hi_) : hi(hi_)
+    {
+        using D = Deal<DT, E>;
+        if (EDGE) {
+#pragma unroll
+            for (int c = 0; c < D::NC; ++c) {
+                const int k = D::col(c, t, T);
+                if (k < hi) some |= 1u << c;
+                if (k < hi && (k < lo || k + D::VW > hi)) cut |= 1u << c;
+            }
+        }
+    }
+    __device__ __forceinline__ bool in(int c, int k) const { return FULL || (EDGE ? (some >> c & 1u) != 0 : k < hi); }
+    __device__ __forceinline__ bool whole(int c) const { return !EDGE || !(cut >> c & 1u); }
+};
+
+// Two 16-bit elements of a word, exact.
+template <int DT> __device__ __forceinline__ float2 unpack2(uint32_t w)
+{
+    if constexpr (DT == DT_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else return make_float2(Scalar<DT>::get(static_cast<uint16_t>(w & 0xFFFFu)), Scalar<DT>::get(static_cast<uint16_t>(w >> 16)));
+}
+
+// A thread's share of gamma over all rows, as raw 32-bit words (two 16-bit elements each).
+template <int DT, int E, bool EDGE> struct Held {
+    using D = Deal<DT, E>;
+    using T = typename Scalar<DT>::T;
+    static constexpr int PER = 4 / sizeof(T), N = E / PER;
+    uint32_t w[N];
+
+    // Column k is p[k - lo] in columns lo to hi, 0 elsewhere.
+    __device__ __forceinline__ void load(const T* p, int t, int threads, int lo, int hi)
+    {
+#pragma unroll
+        for (int c = 0; c < D::NC; ++c) {
+            const int k = D::col(c, t, threads);
+            if constexpr (!EDGE) {
+                const uint4 v = k < hi ? ld_v4(p + k) : make_uint4(0, 0, 0, 0);
+                w[4 * c] = v.x;
+                w[4 * c + 1] = v.y;
+                w[4 * c + 2] = v.z;
+                w[4 * c + 3] = v.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < D::VW; j += PER) {
+                    uint32_t v = 0;
+#pragma unroll
+                    for (int q = 0; q < PER; ++q)
+                        if (k + j + q >= lo && k + j + q < hi) {
+                            if constexpr (PER == 1) v = __float_as_uint(p[k + j - lo]);
+                            else v |= static_cast<uint32_t>(p[k + j + q - lo]) << (16 * q);
+                        }
+                    w[(c * D::VW + j) / PER] = v;
+                }
+            }
+        }
+    }
+    // Keeps the compiler from holding the words unpacked across rows, which the registers do not allow.
+    __device__ __forceinline__ void pin()
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) asm volatile("" : "+r"(w[i]));
+    }
+    __device__ __forceinline__ float2 pair(int i) const          // elements 2 i and 2 i + 1
+    {
+        if constexpr (PER == 1) return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return unpack2<DT>(w[i]);
+    }
+};
+
+constexpr int kRingStages = 8;      // slots per group at most
+constexpr int kRingGroups = 16;     // row groups per CTA at most
+// The rows a group works on: `first`, and every `stride`-th from there. Group g of cluster c starts at
+// row g * clusters + c; the host makes the number of clusters a multiple of the rows after which the shift
+// repeats (or gives every group one row at most), so a CTA's rows have one shift.
+struct Rows {
+    int first, stride, n;
+    __device__ __forceinline__ Rows(int group, int groups, int rows)
+    {
+        const int clusters = static_cast<int>(cluster_count());
+        first = group * clusters + static_cast<int>(cluster_id());
+        stride = clusters * groups;
+        n = first < rows ? (rows - first + stride - 1) / stride : 0;
+    }
+};
+
+constexpr int kRingBars = 2 * kRingStages * kRingGroups * 8;      // bytes of barriers
+
+// A row group's ring of slots: its next rows, brought by bulk copies while the group works. EDGE: rows of
+// a width that is no whole number of vectors, taken from the 16-byte boundary below. The group's rows all
+// have the same shift (Rows).
+template <int DT, bool EDGE> struct RowRing {
+    using T = typename Scalar<DT>::T;
+    static constexpr int ES = sizeof(T), VW = Elem<DT>::EPV;
+    const RowTensors& r;
+    int c0;                        // the CTA's first column
+    int lo, hi;                    // its columns that are the row's, from c0 on
+    int shift;                     // of the rows
+    uint32_t bars, base;           // shared addresses of the group's barriers (kRingStages full, as many
+                                   // empty) and slots
+    __device__ __forceinline__ uint32_t full(int stage) const { return bars + 8 * stage; }
+    __device__ __forceinline__ uint32_t empty(int stage) const { return bars + 8 * (kRingStages + stage); }
+
+    __device__ __forceinline__ uint32_t at(uint32_t stage, int i) const { return base + (stage * r.ntens + i) * r.slot; }
+    // Where the CTA's first column of a row is in a tensor, in elements (whole vectors).
+    __device__ __forceinline__ long long origin(int row) const { return static_cast<long long>(row) * r.hidden - shift + c0; }
+
+    // One row's pieces of every tensor into a slot (one thread).
+    __device__ __forceinline__ void fetch(int row, uint32_t stage, uint64_t policy) const
+    {
+        const long long a0 = origin(row) * ES;
+        long long a1 = a0 + (hi + VW - 1) / VW * 16;
+        if (EDGE && a1 > (r.total & ~15LL)) a1 = r.total & ~15LL;
+        const uint32_t bytes = hi > lo && a1 > a0 ? static_cast<uint32_t>(a1 - a0) : 0u;
+        if (EDGE && hi > lo) {
+            // the tensors' last bytes, which no whole piece covers, by hand (before the arrival below)
+            const long long end = origin(row) + hi;
+            for (long long e = a1 / ES; e < end; ++e)
+                for (int i = 0; i < r.ntens; ++i) {
+                    const uint32_t to = at(stage, i) + static_cast<uint32_t>(e * ES - a0);
+                    const T v = static_cast<const T*>(r.in[i])[e];
+                    if constexpr (ES == 2) asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(v) : "memory");
+                    else asm volatile("st.shared.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+                }
+        }
+        mbar_arrive_expect_tx(full(stage), bytes * r.ntens);
+        if (bytes > 0)
+            for (int i = 0; i < r.ntens; ++i)
+                bulk_load(at(stage, i), static_cast<const unsigned char*>(r.in[i]) + a0, bytes, full(stage), policy);
+    }
+
+    // The vector at column k of tensor i, as raw bits; what is not the row's is not cleared.
+    __device__ __forceinline__ uint4 vec(uint32_t stage, int i, int k) const { return ld_shared_v4(at(stage, i) + k * ES); }
+
+    // One thread sets the barriers up: a slot is empty when `warps` warps have left it.
+    __device__ __forceinline__ void init(int warps) const
+    {
+        for (int i = 0; i < r.stages; ++i) {
+            mbar_init(full(i), 1);
+            mbar_init(empty(i), warps);
+        }
+    }
+
+    // Brings the group's rows (one thread of the CTA's copying warp: issuing a row's copies takes about
+    // 1000 cycles, which a working warp would keep its group waiting for). After a wait that ran out,
+    // waits (bounded) for the copies in flight, so that they end before the CTA does.
+    __device__ __forceinline__ void feed(const Rows& rows, unsigned long long timeout_ns, unsigned int* err) const
+    {
+        const uint64_t policy = l2_evict_normal_policy();
+        const uint32_t limit = wait_limit(timeout_ns);
+        int stage = 0, phase = 1, i = 0;
+        for (; i < rows.n; ++i) {
+            if (!mbar_wait<SCOPE_CTA>(empty(stage), phase, limit)) break;
+            fence_proxy_async_smem();
+            fetch(rows.first + i * rows.stride, stage, policy);
+            if (++stage == r.stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        if (i < rows.n) {
+            bool drained = true;
+            for (int j = i > r.stages ? i - r.stages : 0; j < i; ++j)
+                drained &= mbar_wait<SCOPE_CTA>(full(j % r.stages), (j / r.stages) & 1, wait_limit(4 * timeout_ns));
+            atomicOr(err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
+        }
+    }
+};
+
+// The threads of a row group (T a multiple of 32).
+__device__ __forceinline__ void group_sync(int group, int T)
+{
+    if (T == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(T) : "memory");
+}
+
+// A row's sums among the CTAs of a cluster: each writes its own into a slot of every CTA, which counts
+// the bytes on its own barrier. Two sets in turn: a CTA sends a row's sums after it has read those of
+// the row before, so nobody writes a set that is still read. No cluster barrier, which the copying
+// warp would have to join; every wait is bounded.
+struct ClusterSums {
+    uint32_t bars, slots;          // shared addresses: 2 barriers, [2][16] float4
+    int nc, rank;
+    static constexpr int BYTES = 16 + 2 * 16 * 16;
+
+    __device__ __forceinline__ void init() const
+    {
+        mbar_init(bars, 1);
+        mbar_init(bars + 8, 1);
+    }
+    // By the lanes of one warp.
+    __device__ __forceinline__ void send(int lane, int flip, float4 v) const
+    {
+        const uint32_t bar = bars + 8 * flip, slot = slots + (flip * 16 + rank) * 16;
+        if (lane == 0) mbar_arrive_expect_tx(bar, nc * 16);
+        if (lane < nc)
+            asm volatile(
+                "{\n\t.reg .b32 a, b;\n\tmapa.shared::cluster.u32 a, %0, %2;\n\tmapa.shared::cluster.u32 b, %1, %2;\n\t"
+                "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [a], {%3, %4, %5, %6}, [b];\n\t}"
+                ::"r"(slot), "r"(bar), "r"(lane), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+    }
+    // Lane r of every warp gets rank r's (zeros past the cluster); false: the wait ran out.
+    __device__ __forceinline__ bool receive(int lane, int flip, int phase, uint32_t limit_ns, float4& v) const
+    {
+        const bool ok = mbar_wait<SCOPE_CLUSTER>(bars + 8 * flip, phase, limit_ns);
+        v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (lane < nc) {
+            const uint4 w = ld_shared_v4(slots + (flip * 16 + lane) * 16);
+            v = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+        }
+        return ok;
+    }
+};
+
+constexpr int kRingSlice = 16384;             // bytes of a tensor's row per CTA at most
 
 // Elements of a row per thread: 8, 16 or 24, and the warps of a CTA that work on rows then (one more
 // copies). Registers are dealt to a quarter of the SM's warps each: 16 warps get 128, 12 get 168.

@@ -30,14 +30,11 @@ int resident_clusters(const void* fn, unsigned threads, int smem, int cluster);
 
 struct NormPlan {
     int dt;
-    int elems;      // per thread: 8, 16 (direct only), 32 or 40 (16-bit rows of 131065 elements or more,
-                    // off 16-byte boundaries: 16 slices of 8200)
-    bool vec;
-    bool direct;    // rows straight into registers
+    int elems;      // per thread: 8 or 16 (short rows), 32, or 64 (16-bit types, packed)
+    bool vec;       // rows are whole vectors of 16 bytes
     bool full;      // the threads' shares cover the row exactly
     int scope;      // SCOPE_*
     int threads;
-    int smem;
     unsigned grid;
     int cluster;
 };
@@ -54,22 +51,20 @@ const void* norm_bwd_fn(int dt, int elems, bool full, bool vec);
 const void* norm_bwd_reduce_fn();
 
 #define RMSQ_DEFINE_NORM_DISPATCH(NAME, KIND)                                                     \
+    template <int DT, bool EDGE, bool FULL, int E, int SCOPE> static const void* NAME##_at()      \
+    {                                                                                             \
+        return reinterpret_cast<const void*>(&rmsq_norm_kernel<DT, E, FULL, EDGE, SCOPE, KIND>);  \
+    }                                                                                             \
     template <int DT, bool EDGE, bool FULL> static const void* NAME##_pick(const NormPlan& pl)    \
     {                                                                                             \
-        if (!pl.direct) {                                                                         \
-            if constexpr (EDGE && DT != DT_F32) {                                                 \
-                if (pl.elems == 40)                                                               \
-                    return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 40, EDGE, FULL, KIND>); \
-            }                                                                                     \
-            return reinterpret_cast<const void*>(&rmsq_norm_ring_kernel<DT, 32, EDGE, FULL, KIND>); \
-        }                                                                                         \
+        constexpr int WIDE = DT == DT_F32 ? 32 : 64;                                              \
+        if (pl.scope == SCOPE_CLUSTER) return NAME##_at<DT, EDGE, FULL, WIDE, SCOPE_CLUSTER>();   \
         if (pl.scope == SCOPE_CTA)                                                                \
-            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 32, FULL, EDGE, SCOPE_CTA, KIND>); \
-        if (pl.elems == 8)                                                                        \
-            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 8, FULL, EDGE, SCOPE_WARP, KIND>); \
-        if (pl.elems == 16)                                                                       \
-            return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 16, FULL, EDGE, SCOPE_WARP, KIND>); \
-        return reinterpret_cast<const void*>(&rmsq_norm_direct_kernel<DT, 32, FULL, EDGE, SCOPE_WARP, KIND>); \
+            return pl.elems == WIDE ? NAME##_at<DT, EDGE, FULL, WIDE, SCOPE_CTA>()                \
+                                    : NAME##_at<DT, EDGE, FULL, 32, SCOPE_CTA>();                 \
+        return pl.elems == 8    ? NAME##_at<DT, EDGE, FULL, 8, SCOPE_WARP>()                      \
+               : pl.elems == 16 ? NAME##_at<DT, EDGE, FULL, 16, SCOPE_WARP>()                     \
+                                : NAME##_at<DT, EDGE, FULL, 32, SCOPE_WARP>();                    \
     }                                                                                             \
     template <int DT> static const void* NAME##_fn(const NormPlan& pl)                            \
     {                                                                                             \
@@ -82,7 +77,7 @@ const void* norm_bwd_reduce_fn();
                        : pl.dt == DT_FP16 ? NAME##_fn<DT_FP16>(pl) : NAME##_fn<DT_F32>(pl);       \
         NormParams q = p;                                                                         \
         void* args[] = {&q};                                                                      \
-        return launch_kernel(fn, pl.grid, pl.threads, pl.smem, pl.cluster, stream, args);         \
+        return launch_kernel(fn, pl.grid, pl.threads, 0, pl.cluster, stream, args);         \
     }
 
 }  // namespace rmsq

@@ -30,84 +30,34 @@ static rmsq_status status_of(cudaError_t e)
     return RMSQ_ERR_LAUNCH;
 }
 
-// How a row is dealt out: split evenly, in whole vectors, over the smallest cluster of 1, 2, 4, 8 or 16
-// CTAs whose slices take at most kRingSlice bytes; a slice takes T threads of `elems` elements.
-struct RowGeometry {
-    int cluster, slice, elems, T, slot;
-    int period;      // rows after which the shift off 16-byte boundaries repeats
-};
-
-static RowGeometry row_geometry(int hidden, int dtype, int (*elems)(int))
-{
-    const int es = elem_bytes(dtype), vw = 16 / es;
-    RowGeometry g;
-    g.period = 1;
-    while (static_cast<long long>(g.period) * hidden % vw != 0) ++g.period;
-    const int columns = g.period == 1 ? hidden : hidden + vw - 1;
-    g.cluster = 1;
-    // (16 slices of the widest rows off 16-byte boundaries are one vector more)
-    while (g.cluster < 16 && static_cast<long long>(g.cluster) * (kRingSlice / es) < columns) g.cluster *= 2;
-    g.slice = ((columns + g.cluster - 1) / g.cluster + vw - 1) / vw * vw;
-    g.elems = elems(g.slice);
-    g.T = ((g.slice + g.elems - 1) / g.elems + 31) / 32 * 32;
-    g.slot = g.slice * es;
-    return g;
-}
-
-// Launch of a forward norm.
+// Launch of a forward norm. Who takes a row, and in what shares (GB300, rows x hidden, bf16):
+//  - up to 1024 columns a warp, of 8, 16 or 32 elements a thread;
+//  - up to 16384 a CTA, of 32 elements a thread as fp32 (16 elements: 16384 x 8192 117 us, 32: 85);
+//  - wider 16-bit rows a CTA of 64 elements a thread, packed: 4096 x 20000 58.5 us (clusters of fp32
+//    shares: 83), 4096 x 32768 91 us (131); and rows from 8193 on where there are many of them, without a
+//    residual and off no 16-byte boundary: 8192 x 12000 66 us (fp32 shares: 82), but with a residual 123
+//    (118), 8192 x 14001 136 (132), 100 x 12000 4.7 (3.5), to int8 96 (93), which forms y twice then;
+//  - rows wider than a CTA takes a cluster of 4 or 8: 2048 x 65536 106 us, in clusters of 2 some 5 % more.
 static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormParams&, cudaStream_t),
                                NormParams& p, int64_t rows, int dtype, const DeviceView& dv, cudaStream_t stream)
 {
     NormPlan pl;
-    const int hidden = p.r.hidden, vw = 16 / elem_bytes(dtype);
+    const int hidden = p.hidden, vw = 16 / elem_bytes(dtype);
+    p.rows = static_cast<int>(rows);
     pl.dt = dtype;
-    pl.cluster = 1;
-    pl.smem = 0;
     pl.vec = hidden % vw == 0;
-    p.r.rows = static_cast<int>(rows);
-    const int columns = pl.vec ? hidden : hidden + vw - 1;
-    pl.direct = columns <= 512 * 32;
-    if (pl.direct) {
-        pl.elems = columns <= 256 ? 8 : columns <= 512 ? 16 : 32;
-        pl.scope = columns <= 1024 ? SCOPE_WARP : SCOPE_CTA;
-        const int T = pl.scope == SCOPE_WARP ? 32 : (columns + 1023) / 1024 * 32;
-        pl.full = T * pl.elems == hidden;
-        pl.threads = pl.scope == SCOPE_WARP ? 256 : T;
-        pl.grid = static_cast<unsigned>(pl.scope == SCOPE_WARP ? (rows + 7) / 8 : rows);
-        return status_of(go(pl, p, stream));
-    }
-    const RowGeometry g = row_geometry(hidden, dtype, [](int slice) { return slice <= kRingWorkers * 32 ? 32 : 40; });
-    pl.cluster = g.cluster;
-    pl.elems = g.elems;
-    pl.scope = SCOPE_CLUSTER;
-    pl.full = g.T * g.elems == g.slice && g.slice * g.cluster == hidden;
-    pl.threads = g.T + 32;
-    p.r.total = rows * hidden * elem_bytes(dtype);
-    p.r.slice = g.slice;
-    p.r.slot = g.slot;
-    p.T = g.T;
-    p.err = dv.err;
-    p.timeout_ns = dv.timeout_ns;
-    // CTAs per SM: what the registers hold (27 warps), or as many as leave each two slots
-    const int64_t stage = static_cast<int64_t>(g.slot) * p.r.ntens, head = kNormHead + 2 * g.slot;
-    const auto slots = [&](int ctas) { return (dv.smem_optin / ctas - 1024 - head) / stage; };
-    int ctas = 27 * 32 / pl.threads;
-    while (ctas > 1 && slots(ctas) < 2) --ctas;
-    int64_t stages = slots(ctas);
-    if (stages < 1) return RMSQ_ERR_LAUNCH;
-    if (stages > kRingStages) stages = kRingStages;
-    // About four CTAs in turn on every place an SM has for one, but 8 rows each where that leaves a CTA to
-    // every place; a CTA's rows all have one shift.
-    const int64_t places = static_cast<int64_t>(dv.sms) * ctas / pl.cluster;
-    int64_t per = rows / (places * 4), most = rows / places < 8 ? rows / places : 8;
-    if (per < most) per = most;
-    if (per < 1) per = 1;
-    if (stages > per) stages = per;
-    p.r.stages = static_cast<int>(stages);
-    pl.smem = static_cast<int>(head + stages * stage);
-    int64_t clusters = (rows + per - 1) / per;
-    if (per > 1) clusters = (clusters + g.period - 1) / g.period * g.period;
-    pl.grid = static_cast<unsigned>(clusters * pl.cluster);
+    const int columns = pl.vec ? hidden : hidden + vw - 1;      // from a row's 16-byte boundary on
+    const bool many = rows >= 4 * dv.sms && pl.vec && p.residual == nullptr && p.scale == nullptr;
+    const bool packed = dtype != RMSQ_F32 && (columns > 16384 || (columns > 8192 && many));
+    pl.elems = columns <= 256 ? 8 : columns <= 512 ? 16 : packed ? 64 : 32;
+    const int most = 512 * pl.elems;                            // of a CTA
+    pl.cluster = columns <= most ? 1 : columns < 2 * most + vw ? 4 : 8;
+    pl.scope = columns <= 1024 ? SCOPE_WARP : pl.cluster == 1 ? SCOPE_CTA : SCOPE_CLUSTER;
+    p.slice = ((columns + pl.cluster - 1) / pl.cluster + vw - 1) / vw * vw;
+    const int T = (p.slice + 32 * pl.elems - 1) / (32 * pl.elems) * 32;
+    pl.full = T * pl.elems == p.slice && p.slice * pl.cluster == hidden;
+    pl.threads = pl.scope == SCOPE_WARP ? 256 : T;
+    pl.grid = static_cast<unsigned>(pl.scope == SCOPE_WARP ? (rows + 7) / 8 : rows * pl.cluster);
     return status_of(go(pl, p, stream));
 }
 
@@ -138,14 +88,13 @@ static NormParams norm_params(const void* input, const void* residual, void* res
                               float weight_offset, void* output)
 {
     NormParams p = {};
-    p.r.in[0] = input;
-    p.r.in[1] = residual;
-    p.r.ntens = residual != nullptr ? 2 : 1;
+    p.x = input;
+    p.residual = residual;
     p.res_out = residual_output;
     p.gamma = gamma;
     p.beta = beta;
     p.out = output;
-    p.r.hidden = static_cast<int>(hidden);
+    p.hidden = static_cast<int>(hidden);
     p.eps = epsilon;
     p.offset = weight_offset;
     return p;
@@ -212,6 +161,30 @@ extern "C" rmsq_status rmsnorm_quant_int8(const void* input, const void* residua
 {
     return norm_int8(&norm_rms_int8, input, residual, residual_output, gamma, nullptr, rows, hidden,
                      dtype, epsilon, weight_offset, output, scale_output, stream);
+}
+
+// How a row is dealt out: split evenly, in whole vectors, over the smallest cluster of 1, 2, 4, 8 or 16
+// CTAs whose slices take at most kRingSlice bytes; a slice takes T threads of `elems` elements.
+struct RowGeometry {
+    int cluster, slice, elems, T, slot;
+    int period;      // rows after which the shift off 16-byte boundaries repeats
+};
+
+static RowGeometry row_geometry(int hidden, int dtype, int (*elems)(int))
+{
+    const int es = elem_bytes(dtype), vw = 16 / es;
+    RowGeometry g;
+    g.period = 1;
+    while (static_cast<long long>(g.period) * hidden % vw != 0) ++g.period;
+    const int columns = g.period == 1 ? hidden : hidden + vw - 1;
+    g.cluster = 1;
+    // (16 slices of the widest rows off 16-byte boundaries are one vector more)
+    while (g.cluster < 16 && static_cast<long long>(g.cluster) * (kRingSlice / es) < columns) g.cluster *= 2;
+    g.slice = ((columns + g.cluster - 1) / g.cluster + vw - 1) / vw * vw;
+    g.elems = elems(g.slice);
+    g.T = ((g.slice + g.elems - 1) / g.elems + 31) / 32 * 32;
+    g.slot = g.slice * es;
+    return g;
 }
 
 // Partial rows of the column sums: at most one per CTA of a GB300 (152), and no more than rows.
