@@ -229,7 +229,7 @@ bool device_view(DeviceView* v)
 struct ReadyFn {
     const void* fn;
     int dev;
-    int clusters[9];      // clusters of each size that fit on the device at a time; 0: not asked yet
+    int clusters[17];     // clusters of each size that fit on the device at a time; 0: not asked yet
 };
 static ReadyFn g_ready[512];
 static int g_nready = 0;
@@ -281,7 +281,7 @@ int resident_clusters(const void* fn, unsigned threads, int smem, int cluster)
     std::lock_guard<std::mutex> lock(g_mu);
     cudaError_t e;
     ReadyFn* const r = ready_fn(fn, smem, &e);
-    if (r == nullptr || cluster < 1 || cluster > 8) return 0;
+    if (r == nullptr || cluster < 1 || cluster > 16) return 0;
     if (r->clusters[cluster] == 0) {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];

@@ -25,7 +25,7 @@ bool device_view(DeviceView* v);
 cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem, int cluster,
                           cudaStream_t stream, void** args);
 
-// How many clusters of that size (1 to 8 CTAs) the current device runs at a time; 0: not known.
+// How many clusters of that size (1 to 16 CTAs) the current device runs at a time; 0: not known.
 int resident_clusters(const void* fn, unsigned threads, int smem, int cluster);
 
 struct NormPlan {

@@ -274,7 +274,10 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         if (p.groups > 1 && ring < 8LL * p.r.slice) ring = 8LL * p.r.slice;   // the groups' sums
         // one partial row per cluster; where a group has several rows or a CTA several groups, as many
         // clusters as make a CTA's rows have one shift
-        const int64_t most = bwd_parts(rows), resident = dv.sms / cluster;
+        const void* fn = norm_bwd_fn(dtype, g.elems, g.T * g.elems == g.slice && g.slice * cluster == hidden, g.period == 1);
+        const unsigned threads = static_cast<unsigned>(p.T * p.groups + 32);
+        const int smem = static_cast<int>(kBwdHead + ring);
+        const int64_t most = bwd_parts(rows), resident = cluster == 1 ? dv.sms : resident_clusters(fn, threads, smem, cluster);
         int64_t parts = (rows + p.groups - 1) / p.groups;
         if (parts > resident) parts = resident;
         if (parts > most) parts = most;
@@ -287,8 +290,7 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         r.parts = static_cast<int>(parts);
         void* args[] = {&p};
         const rmsq_status e = status_of(launch_kernel(
-            norm_bwd_fn(dtype, g.elems, g.T * g.elems == g.slice && g.slice * g.cluster == hidden, g.period == 1), static_cast<unsigned>(parts * cluster),
-            static_cast<unsigned>(p.T * p.groups + 32), static_cast<int>(kBwdHead + ring), cluster, st, args));
+            fn, static_cast<unsigned>(parts * cluster), threads, smem, cluster, st, args));
         if (e != RMSQ_OK) return e;
     }
     void* args[] = {&r};
