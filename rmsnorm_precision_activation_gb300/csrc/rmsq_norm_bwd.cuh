@@ -15,6 +15,12 @@
 //
 // A CTA holds several row groups of T threads when rows are short; rows wider than 16 KB are split
 // over a cluster whose CTAs exchange the two row sums.
+//
+// Measured (GB300, of the copy rate): 16384 x 8192 fp16 with dres 177 us (0.91), 16384 x 4096 bf16 with
+// dres 96 (0.84), 32768 x 2048 74 (0.81), 8192 x 16384 165 (0.73), 2048 x 65536 210 (0.57), fp32
+// 4096 x 16384 125 (0.96). The cluster's exchange bounds wide rows (an SM holds one CTA, which waits for it
+// once in two rows), the checked and unaligned accesses rows off 16-byte boundaries (5003 x 2051 fp32 33,
+// 0.56). Row groups add their column sums side by side: one after another, 4000 x 512 took 26 us, not 10.
 #pragma once
 
 #include "rmsq_norm.cuh"
@@ -133,6 +139,7 @@ template <int DT, int E, bool EDGE> struct Held {
 
 constexpr int kRingStages = 8;      // slots per group at most
 constexpr int kRingGroups = 16;     // row groups per CTA at most
+
 // The rows a group works on: `first`, and every `stride`-th from there. Group g of cluster c starts at
 // row g * clusters + c; the host makes the number of clusters a multiple of the rows after which the shift
 // repeats (or gives every group one row at most), so a CTA's rows have one shift.
@@ -471,37 +478,32 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
 
     const auto workers_sync = [&]() { asm volatile("bar.sync 15, %0;" ::"r"(workers) : "memory"); };
     const auto acc = [](const float2* a, int e) { return e & 1 ? a[e / 2].y : a[e / 2].x; };
-    // ---- partial rows: the groups' sums in group order, through the ring's memory ----
+    // ---- partial rows: the groups' sums side by side in the ring's memory, then added in group order ----
     workers_sync();
     float* const part = p.part + static_cast<long long>(cluster_id()) * 2 * p.r.hidden + (c0 + lo - shift);
-    float* const sum = reinterpret_cast<float*>(smem + kBwdHead);
-    for (int g = 0; g < p.groups; ++g) {
-        if (g == group) {
+    float* const sums_all = reinterpret_cast<float*>(smem + kBwdHead);
+    float* const own = p.groups == 1 ? part : sums_all + group * 2 * p.r.slice;
+    const int other = p.groups == 1 ? p.r.hidden : p.r.slice;
 #pragma unroll
-            for (int c = 0; c < NC; ++c) {
-                const int k = D::col(c, thread, T);
+    for (int c = 0; c < NC; ++c) {
+        const int k = D::col(c, thread, T);
 #pragma unroll
-                for (int j = 0; j < VW; ++j)
-                    if (k + j >= lo && k + j < hi) {
-                        const int e = k + j - lo;
-                        const float a = acc(acc_g, c * VW + j), b = acc(acc_b, c * VW + j);
-                        if (p.groups == 1) {
-                            part[e] = a;
-                            part[p.r.hidden + e] = b;
-                        } else {
-                            sum[e] = (g == 0 ? 0.f : sum[e]) + a;
-                            sum[p.r.slice + e] = (g == 0 ? 0.f : sum[p.r.slice + e]) + b;
-                        }
-                    }
+        for (int j = 0; j < VW; ++j)
+            if (k + j >= lo && k + j < hi) {
+                own[k + j - lo] = acc(acc_g, c * VW + j);
+                own[other + k + j - lo] = acc(acc_b, c * VW + j);
             }
-        }
-        if (p.groups > 1) workers_sync();
     }
-    if (p.groups > 1)
-        for (int k = threadIdx.x; k < hi - lo; k += workers) {
-            part[k] = sum[k];
-            part[p.r.hidden + k] = sum[p.r.slice + k];
+    if (p.groups > 1) {
+        workers_sync();
+        for (int k = threadIdx.x; k < 2 * (hi - lo); k += workers) {
+            const bool beta = k >= hi - lo;
+            const int e = beta ? k - (hi - lo) : k, at = beta ? p.r.slice + e : e;
+            float a = 0.f;
+            for (int g = 0; g < p.groups; ++g) a += sums_all[g * 2 * p.r.slice + at];
+            part[beta ? p.r.hidden + e : e] = a;
         }
+    }
     if (nc > 1) cluster_sync();                   // nobody sends to a CTA that has left
 }
 

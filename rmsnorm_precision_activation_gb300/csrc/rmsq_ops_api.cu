@@ -271,7 +271,7 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         p.r.stages = static_cast<int>(stages > kRingStages ? kRingStages : stages) & ~1;
         const int64_t stage = static_cast<int64_t>(p.r.slot) * p.r.ntens * p.groups;
         int64_t ring = p.r.stages * stage;
-        if (p.groups > 1 && ring < 8LL * p.r.slice) ring = 8LL * p.r.slice;   // the groups' sums
+        if (p.groups > 1 && ring < 8LL * p.r.slice * p.groups) ring = 8LL * p.r.slice * p.groups;   // the groups' sums
         // one partial row per cluster; where a group has several rows or a CTA several groups, as many
         // clusters as make a CTA's rows have one shift
         const void* fn = norm_bwd_fn(dtype, g.elems, g.T * g.elems == g.slice && g.slice * cluster == hidden, g.period == 1);
