@@ -26,6 +26,10 @@
  *          -- the same file, phase 3 with the UE8M0 scale format (block 32),
  *          cvt_f32_to_ue8m0 and ue8m0_to_output_scale.
  *
+ * Next to these it has layer norm and its gradients, layer norm and RMS norm to int8 codes with one
+ * scale per row, and the product of such codes: layernorm, layernorm_backward, layernorm_quant_int8,
+ * rmsnorm_quant_int8, matmul_int8, described with their declarations.
+ *
  * All E4M3 / E2M1 conversions round to nearest even and saturate finite values ("satfinite").
  * A row whose FP8 scale is 0 (an all-zero y) gets codes 0 and scale 0.
  *
@@ -39,7 +43,8 @@
  *   - Arguments are checked on the host before anything is launched; on an error nothing is
  *     launched and no output is touched.
  *   - residual and residual_output are both NULL (no residual) or both non-NULL.
- *   - Inputs must be finite; NaN / Inf inputs give unspecified codes.
+ *   - Inputs must be finite; NaN / Inf inputs give unspecified codes (but see layernorm and the int8
+ *     norms).
  *   - Calls on one stream are ordered; outputs of concurrent calls must not overlap.
  */
 #ifndef RMSQ_H
