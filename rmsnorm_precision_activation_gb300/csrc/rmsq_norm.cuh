@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
     constexpr bool RMS = KIND == NORM_RMS_INT8;
     constexpr bool INT8 = KIND != NORM_LAYER;
     constexpr int NC = D::NC, PV = D::PV, VW = D::VW;
-    __shared__ float2 part[16];
+    __shared__ float4 part[16];                     // sum, squares, elements
     __shared__ float part_max[16];
     __shared__ float2 cluster_part[2][16];          // sums, maxima
 
@@ -519,17 +519,15 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
     }
     const float inv_h = __frcp_rn(static_cast<float>(p.hidden));
     if constexpr (SCOPE != SCOPE_WARP) {
-        if (lane == 0) part[warp] = make_float2(sum, m2);
+        if (lane == 0) part[warp] = make_float4(sum, m2, static_cast<float>(n_w), 0.f);
         __syncthreads();
-        const float2 q = lane < nwarps ? part[lane] : make_float2(0.f, 0.f);
-        float d = 0.f, n_l = 0.f;
+        const float4 q = lane < nwarps ? part[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float n_l = FULL ? (lane < nwarps ? static_cast<float>(32 * E) : 0.f) : q.z;
+        float d = 0.f;
         if constexpr (!RMS) {
             sum = warp_sum(q.x);
             mean = sum * (SCOPE == SCOPE_CTA ? inv_h : hi > lo ? 1.0f / static_cast<float>(hi - lo) : 0.f);
-            if (lane < nwarps) {
-                n_l = FULL ? static_cast<float>(32 * E) : static_cast<float>(D::count(lane * 32, T, lo, hi));
-                d = FULL ? q.x * (1.0f / (32 * E)) - mean : n_l > 0.f ? __fdividef(q.x, n_l) - mean : 0.f;
-            }
+            if (lane < nwarps) d = FULL ? q.x * (1.0f / (32 * E)) - mean : n_l > 0.f ? __fdividef(q.x, n_l) - mean : 0.f;
         }
         m2 = warp_sum(fmaf(n_l * d, d, q.y));
     }
