@@ -9,12 +9,20 @@ namespace rmsq {
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <int NB> static cudaError_t launch_stream(MatmulParams& p, cudaStream_t stream)
+template <int NB, int ROWS> static cudaError_t launch_stream(MatmulParams& p, cudaStream_t stream)
 {
     void* args[] = {&p};
-    return launch_kernel(reinterpret_cast<const void*>(&rmsq_matmul_stream_kernel<NB>),
-                         dim3(static_cast<unsigned>((p.n + kStreamRows - 1) / kStreamRows)), kStreamWarps * 32, 0, 1,
-                         stream, args);
+    return launch_kernel(reinterpret_cast<const void*>(&rmsq_matmul_stream_kernel<NB, ROWS>),
+                         dim3(static_cast<unsigned>((p.n + ROWS - 1) / ROWS)), kStreamWarps * 32, 0, 1, stream, args);
+}
+
+// 16 channels per CTA where all of the CTAs run at a time then, else 32 (GB300, 1 token, n x k: 7168 x 8192
+// 12.1 us against 13.2, 1024 x 4096 3.3 against 4.3, 300 x 16384 7.4 against 10.6; 8192 x 8192, which
+// takes more than one wave of 16, 15.9 against 14.1; 16 tokens 5000 x 8192 14.7 against 15.5).
+template <int NB> static cudaError_t launch_stream(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
+{
+    if (p.n <= static_cast<long long>(dv.sms) * kStreamHalves * 16) return launch_stream<NB, 16>(p, stream);
+    return launch_stream<NB, 32>(p, stream);
 }
 
 // cuTensorMapEncodeTiled from the driver (the library does not link it).
@@ -118,8 +126,8 @@ template <int TOKENS> static cudaError_t launch_pair(MatmulParams& p, const Devi
 //   512 83, 63, 74;  768 121, 90, 76;  4096 540, 386, 335;  1024 x 1024 x 8192 27.7, 34.8, 40.4.
 static cudaError_t launch_matmul(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
 {
-    if (p.m <= 8) return launch_stream<1>(p, stream);
-    if (p.m <= 16) return launch_stream<2>(p, stream);
+    if (p.m <= 8) return launch_stream<1>(p, dv, stream);
+    if (p.m <= 16) return launch_stream<2>(p, dv, stream);
     if (p.m <= 32) return launch_tc<32>(p, dv, stream);
     if (p.m <= 64) return launch_tc<64>(p, dv, stream);
     const int steps = (p.k + kTcCodes - 1) / kTcCodes;

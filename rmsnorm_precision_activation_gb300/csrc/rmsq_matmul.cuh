@@ -54,31 +54,32 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t
     asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
 }
 
-// Single tokens and decode batches (NB x 8 tokens): bound by the weight's bytes. A CTA takes 32
+// Single tokens and decode batches (NB x 8 tokens): bound by the weight's bytes. A CTA takes 16 or 32
 // channels; its 8 warps take k in turn, 64 bytes of every row at a time, load the codes straight into
 // registers, turn them into fp16 there and multiply with mma.sync (fp32 sums of up to 1024 products
 // are exact, then they go to integers). No shared memory or barrier stands between a load and its
 // use, so a short call costs little more than its bytes, where the tcgen05 kernels' hand-overs cost
-// about 8 us. Measured (GB300, weights from HBM): 1 to 8 tokens x 7168 x 8192 13 us, 4.5 TB/s (a dp4a
-// kernel: 13 us for 1 token, 28 for 8; tcgen05: 16.6); 16 x 8192 x 8192 16.7 us (tcgen05: 18.4);
-// 32 tokens 23.9 us (tcgen05: 19.8, so those go there).
+// about 8 us. Measured (GB300, weights from HBM): 1 to 8 tokens x 7168 x 8192 12.1 us, 4.8 TB/s (a dp4a
+// kernel: 13 us for 1 token, 28 for 8; tcgen05: 16.6); x 28672 x 8192 38.9 us, 6.0 TB/s;
+// 16 x 8192 x 8192 16.8 us (tcgen05: 18.4); 32 tokens 23.9 us (tcgen05: 19.8, so those go there).
 // A fragment's k order is free as long as both operands share it: lane (g, t) loads 16 bytes of row
 // g at 16 t, and the j-th four of them are its elements in the j-th of four MMAs.
 constexpr int kStreamWarps = 8;
-constexpr int kStreamRows = 32;
+constexpr int kStreamHalves = 3;         // CTAs of 16 channels on an SM
 
-template <int NB>
-__global__ void __launch_bounds__(kStreamWarps * 32, 2) rmsq_matmul_stream_kernel(const MatmulParams p)
+template <int NB, int ROWS>
+__global__ void __launch_bounds__(kStreamWarps * 32, ROWS == 16 ? kStreamHalves : 2) rmsq_matmul_stream_kernel(const MatmulParams p)
 {
     // steps of 64 elements held in registers: one is multiplied while the loads of the others run
     constexpr int U = NB == 1 ? 4 : 3;
-    __shared__ int part[kStreamWarps][NB * 8][kStreamRows + 1];
+    __shared__ int part[kStreamWarps][NB * 8][ROWS + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const long long n0 = static_cast<long long>(blockIdx.x) * kStreamRows;
-    const signed char* wp[4];
+    const long long n0 = static_cast<long long>(blockIdx.x) * ROWS;
+    constexpr int I = ROWS / 16, R = ROWS / 8;      // MMAs of 16 rows, loads of 8
+    const signed char* wp[R];
     const signed char* ap[NB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
         const long long n = n0 + 8 * i + g;
         wp[i] = p.w + (n < p.n ? n : p.n - 1) * p.k + 16 * t;
     }
@@ -89,9 +90,9 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 2) rmsq_matmul_stream_kerne
     }
     pdl_wait();
 
-    float c[2][NB][4];
+    float c[I][NB][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < I; ++i)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 2) rmsq_matmul_stream_kerne
     bool fresh = true;                                     // nothing in part yet
     auto flush = [&]() {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < I; ++i)
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -111,12 +112,12 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 2) rmsq_matmul_stream_kerne
         fresh = false;
     };
 
-    uint4 wv[U][4], av[U][NB];
+    uint4 wv[U][R], av[U][NB];
     auto load = [&](int u, int step) {                     // past the end: zeros, nothing is read
         const int k = step * 64;
         const bool in = k + 16 * t < p.k;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
             wv[u][i] = in ? ld_stream_v4(reinterpret_cast<const uint4*>(wp[i] + k)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int b = 0; b < NB; ++b) av[u][b] = in ? ld_v4(ap[b] + k) : make_uint4(0, 0, 0, 0);
@@ -128,22 +129,26 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 2) rmsq_matmul_stream_kerne
     for (int s = warp; s < steps; s += U * kStreamWarps) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t w[4][4] = {{wv[u][0].x, wv[u][0].y, wv[u][0].z, wv[u][0].w},
-                                      {wv[u][1].x, wv[u][1].y, wv[u][1].z, wv[u][1].w},
-                                      {wv[u][2].x, wv[u][2].y, wv[u][2].z, wv[u][2].w},
-                                      {wv[u][3].x, wv[u][3].y, wv[u][3].z, wv[u][3].w}};
+            uint32_t w[R][4];
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                w[i][0] = wv[u][i].x;
+                w[i][1] = wv[u][i].y;
+                w[i][2] = wv[u][i].z;
+                w[i][3] = wv[u][i].w;
+            }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint32_t lo[4], hi[4];
+                uint32_t lo[R], hi[R];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) codes_to_half(w[i][j], lo[i], hi[i]);
+                for (int i = 0; i < R; ++i) codes_to_half(w[i][j], lo[i], hi[i]);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
                     const uint32_t a[4] = {av[u][b].x, av[u][b].y, av[u][b].z, av[u][b].w};
                     uint32_t b0, b1;
                     codes_to_half(a[j], b0, b1);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < I; ++i)
                         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
                             "{%8, %9}, {%0, %1, %2, %3};"
                             : "+f"(c[i][b][0]), "+f"(c[i][b][1]), "+f"(c[i][b][2]), "+f"(c[i][b][3])
@@ -159,8 +164,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 2) rmsq_matmul_stream_kerne
     }
     flush();
     __syncthreads();
-    for (int e = threadIdx.x; e < NB * 8 * kStreamRows; e += kStreamWarps * 32) {
-        const int row = e % kStreamRows, m = e / kStreamRows;
+    for (int e = threadIdx.x; e < NB * 8 * ROWS; e += kStreamWarps * 32) {
+        const int row = e % ROWS, m = e / ROWS;
         const long long n = n0 + row;
         if (n < p.n && m < p.m) {
             int v = 0;

@@ -109,6 +109,13 @@ def test_large():
 
 
 @gpu
+@pytest.mark.parametrize("m", [1, 8, 11, 16])
+@pytest.mark.parametrize("n", [1, 17, 7296, 7297, 12007])
+def test_few_tokens_around_a_wave_of_narrow_ctas(m, n):
+    check(make(m, n, 1104, seed=m + n))
+
+
+@gpu
 @pytest.mark.parametrize("m", [65, 100, 150, 200, 260, 500, 700, 1100])
 @pytest.mark.parametrize("n,k", [(2100, 528), (5000, 1040), (11003, 272), (130, 2064)])
 def test_each_kernel_for_many_tokens(m, n, k):
