@@ -201,8 +201,9 @@ rmsq_status rmsnorm_quant_fp8_static_scratch(const void* input, const void* resi
  * RMSQ_MAX_HIDDEN (fp32: half of it), rows at most 2^27 - 1. output may be input, and residual_output
  * may be residual or input (each element is read before it is written).
  * A row with a NaN or an infinity gives NaN in that row alone.
- * Sums are added in a fixed order, which depends on the row's length and, where rows are no whole number
- * of 16 bytes, on where the row starts against a 16-byte boundary; not on the number of rows.
+ * Sums are added in a fixed order, which goes by the row's length and type, by whether there is a
+ * residual and, where rows are no whole number of 16 bytes, by where the row starts against a 16-byte
+ * boundary; not by the other rows or their number.
  * ------------------------------------------------------------------------------------------- */
 rmsq_status layernorm(const void* input, const void* residual, void* residual_output,
                       const void* gamma, const void* beta, int64_t rows, int64_t hidden, int dtype,

@@ -34,12 +34,13 @@ static rmsq_status status_of(cudaError_t e)
 //  - up to 1024 columns a warp, of 8, 16 or 32 elements a thread;
 //  - up to 16384 a CTA, of 32 elements a thread as fp32 (16 elements: 16384 x 8192 117 us, 32: 85);
 //  - wider 16-bit rows a CTA of 64 elements a thread, packed: 4096 x 20000 58.5 us (clusters of fp32
-//    shares: 83), 4096 x 32768 91 us (131); and rows from 8193 on where there are many of them, without a
-//    residual and off no 16-byte boundary: 8192 x 12000 66 us (fp32 shares: 82), but with a residual 123
-//    (118), 8192 x 14001 136 (132), 100 x 12000 4.7 (3.5), to int8 96 (93), which forms y twice then;
+//    shares: 83), 4096 x 32768 91 us (131); and rows from 8193 on without a residual and off no 16-byte
+//    boundary: 8192 x 12000 66 us (fp32 shares: 82), but with a residual 123 (118), 8192 x 14001 136 (132),
+//    to int8 96 (93), which forms y twice then. (100 x 12000 takes 4.7 us packed, 3.5 not; the choice does
+//    not go by the number of rows, so that a row's bits do not depend on the others.)
 //  - rows wider than a CTA takes a cluster of 4 or 8: 2048 x 65536 106 us, in clusters of 2 some 5 % more.
 static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormParams&, cudaStream_t),
-                               NormParams& p, int64_t rows, int dtype, const DeviceView& dv, cudaStream_t stream)
+                               NormParams& p, int64_t rows, int dtype, cudaStream_t stream)
 {
     NormPlan pl;
     const int hidden = p.hidden, vw = 16 / elem_bytes(dtype);
@@ -47,8 +48,8 @@ static rmsq_status launch_norm(cudaError_t (*go)(const NormPlan&, const NormPara
     pl.dt = dtype;
     pl.vec = hidden % vw == 0;
     const int columns = pl.vec ? hidden : hidden + vw - 1;      // from a row's 16-byte boundary on
-    const bool many = rows >= 4 * dv.sms && pl.vec && p.residual == nullptr && p.scale == nullptr;
-    const bool packed = dtype != RMSQ_F32 && (columns > 16384 || (columns > 8192 && many));
+    const bool packed = dtype != RMSQ_F32 &&
+                        (columns > 16384 || (columns > 8192 && pl.vec && p.residual == nullptr && p.scale == nullptr));
     pl.elems = columns <= 256 ? 8 : columns <= 512 ? 16 : packed ? 64 : 32;
     const int most = 512 * pl.elems;                            // of a CTA
     pl.cluster = columns <= most ? 1 : columns < 2 * most + vw ? 4 : 8;
@@ -117,7 +118,7 @@ static rmsq_status norm_int8(cudaError_t (*go)(const NormPlan&, const NormParams
     NormParams p = norm_params(input, residual, residual_output, gamma, beta, hidden, epsilon,
                                weight_offset, output);
     p.scale = scale_output;
-    return launch_norm(go, p, rows, dtype, dv, static_cast<cudaStream_t>(stream));
+    return launch_norm(go, p, rows, dtype, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace rmsq
@@ -140,7 +141,7 @@ extern "C" rmsq_status layernorm(const void* input, const void* residual, void* 
                                weight_offset, output);
     p.mean = mean;
     p.rstd = rstd;
-    return launch_norm(&norm_layer, p, rows, dtype, dv, static_cast<cudaStream_t>(stream));
+    return launch_norm(&norm_layer, p, rows, dtype, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" rmsq_status layernorm_quant_int8(const void* input, const void* residual,

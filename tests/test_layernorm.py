@@ -3,8 +3,8 @@ formulas in 64 bits, at the widths where the row's owner changes (a warp to 1024
 16384, 8192 backward, then clusters), at widths that are no whole vectors, and at degenerate rows.
 
 Tolerances. u = 2^-24 is half a step of fp32, h = finfo(t).eps / 2 half a step of the output type.
-A sum over a row is at most 32 terms in a thread, then at most 12 levels of pairwise adds, so its
-error is at most 44 u times the sum of magnitudes; the few products behind it keep it under K = 64.
+A sum over a row is at most 32 terms in a thread, then at most 14 levels of pairwise adds, so its
+error is at most 46 u times the sum of magnitudes; the few products behind it keep it under K = 64.
  - y: an error of the mean (64 u mean|s|) and of rstd (64 u relative) reach y through rstd |w|, so
    |y - exact| <= h |exact| + K u (rstd |w| (mean|s| + |s - mean|) + |beta|) + one fp16 subnormal step.
  - ds: the same with |g| + mean|g| + |xhat| mean|g xhat| in place of the norm's terms; xhat is formed
@@ -95,6 +95,32 @@ def test_forward_widest(hidden):
 @pytest.mark.parametrize("hidden", [96, 2048])
 def test_forward_rows(rows, hidden):
     check_forward(make(rows, hidden, torch.bfloat16, seed=rows, beta=rows % 2 == 0), offset=1.0)
+
+
+@gpu
+@pytest.mark.parametrize("hidden", [8193, 9000, 12000, 16377, 16376, 16384, 32761, 32769, 32776, 65529, 65537, 65544])
+def test_forward_around_each_plan(hidden):
+    # where rows are packed, take a cluster of 4, of 8; with and without a residual
+    check_forward(make(6, hidden, torch.bfloat16, seed=hidden))
+    check_forward(make(6, hidden, torch.float16, seed=hidden, residual=True))
+
+
+@gpu
+@pytest.mark.parametrize("hidden", [16381, 16382, 32765, 32766, 32772, 65533, 65535])
+def test_forward_around_each_plan_fp32(hidden):
+    check_forward(make(6, hidden, torch.float32, seed=hidden))
+
+
+@gpu
+@pytest.mark.parametrize("hidden", [96, 1024, 4096, 12000, 16384, 20000, 65536])
+@pytest.mark.parametrize("residual", [False, True])
+def test_a_rows_bits_do_not_depend_on_the_other_rows(hidden, residual):
+    d = make(700, hidden, torch.bfloat16, seed=hidden, residual=residual)
+    cut = lambda t, n: None if t is None else t[:n].contiguous()  # noqa: E731
+    for f in (rq().layernorm, rq().layernorm_quant_int8):
+        many = f(d["x"], d["gamma"], d["beta"], residual=d["residual"])
+        one = f(cut(d["x"], 3), d["gamma"], d["beta"], residual=cut(d["residual"], 3))
+        assert all(torch.equal(a[:3], b) for a, b in zip(many, one) if a is not None)
 
 
 @gpu
@@ -245,7 +271,8 @@ def check_int8(d, rms, offset=0.0, eps=1e-5):
 @gpu
 @pytest.mark.parametrize("rms", [False, True])
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("hidden", [1, 8, 63, 256, 400, 1000, 1024, 1026, 4096, 5121, 8192, 12000, 16384, 20000, 33333])
+@pytest.mark.parametrize("hidden", [1, 8, 63, 256, 400, 1000, 1024, 1026, 4096, 5121, 8192, 12000, 16384, 20000, 33333,
+                                    32761, 32776, 65535, 65536])
 def test_int8_rows(rms, dtype, hidden):
     check_int8(make(19, hidden, dtype, seed=hidden + 1, residual=hidden % 2 == 0), rms, offset=1.0)
 
@@ -316,6 +343,13 @@ def test_backward_widths(dtype, hidden):
 @pytest.mark.parametrize("hidden", [8200, 8193, 16384, 22761, 40008, 65536])
 def test_backward_clusters(dtype, hidden):
     check_backward(make_backward(45, hidden, dtype, hidden, residual=hidden % 2 == 0))
+
+
+@gpu
+@pytest.mark.parametrize("hidden", [8191, 8193, 8200, 16383, 16393, 16401, 32767, 32793, 65543, 65544])
+def test_backward_around_each_cluster(hidden):
+    # enough rows that every CTA has several
+    check_backward(make_backward(600, hidden, torch.bfloat16, hidden, residual=False))
 
 
 @gpu
