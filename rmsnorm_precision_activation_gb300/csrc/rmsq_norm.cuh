@@ -56,12 +56,6 @@ template <> struct Scalar<DT_BF16> {
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
         return r;
     }
-    static __device__ __forceinline__ T add(T a, T b)
-    {
-        T r;
-        asm("add.rn.bf16 %0, %1, %2;" : "=h"(r) : "h"(a), "h"(b));
-        return r;
-    }
 };
 template <> struct Scalar<DT_FP16> {
     using T = uint16_t;
@@ -83,18 +77,11 @@ template <> struct Scalar<DT_FP16> {
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
         return r;
     }
-    static __device__ __forceinline__ T add(T a, T b)
-    {
-        T r;
-        asm("add.rn.f16 %0, %1, %2;" : "=h"(r) : "h"(a), "h"(b));
-        return r;
-    }
 };
 template <> struct Scalar<DT_F32> {
     using T = float;
     static __device__ __forceinline__ float get(T v) { return v; }
     static __device__ __forceinline__ T put(float f) { return f; }
-    static __device__ __forceinline__ T add(T a, T b) { return __fadd_rn(a, b); }
 };
 
 // fp32 pairs -> one 16-byte vector of the type.

@@ -1,6 +1,5 @@
 // rmsq_ops_api.cu -- C ABI of layer norm, its gradient and the norms to int8: argument checks,
 // launch plans and entry points (declared in include/rmsq.h).
-#include <climits>
 #include <cmath>
 #include <cstdint>
 
