@@ -17,10 +17,12 @@
 // over a cluster whose CTAs exchange the two row sums.
 //
 // Measured (GB300, of the copy rate): 16384 x 8192 fp16 with dres 177 us (0.91), 16384 x 4096 bf16 with
-// dres 96 (0.84), 32768 x 2048 74 (0.81), 8192 x 16384 165 (0.73), 2048 x 65536 210 (0.57), fp32
-// 4096 x 16384 125 (0.96). The cluster's exchange bounds wide rows (an SM holds one CTA, which waits for it
-// once in two rows), the checked and unaligned accesses rows off 16-byte boundaries (5003 x 2051 fp32 33,
-// 0.56). Row groups add their column sums side by side: one after another, 4000 x 512 took 26 us, not 10.
+// dres 92 (0.87), 32768 x 2048 72 (0.84), 8192 x 16384 165 (0.73), 2048 x 65536 210 (0.57), fp32
+// 4096 x 16384 125 (0.96). Wide rows are bound by the SMs that clusters of 8 leave idle (120 of 152 work)
+// and by the latency of a pair of rows in 11 warps: sums formed a pair ahead of the exchange gave 3 % at
+// 65536 and cost 4 % at 8192. Rows off 16-byte boundaries are bound by checked and unaligned accesses
+// (5003 x 2051 fp32 32, 0.57). Row groups add their column sums side by side: one after another, 4000 x 512
+// took 26 us, not 10.
 #pragma once
 
 #include "rmsq_norm.cuh"
@@ -292,7 +294,10 @@ constexpr int row_warps(int elems) { return elems <= 16 ? 15 : 11; }
 // cluster's sums.
 constexpr int kBwdHead = (kRingBars + 2 * 16 * 16 + ClusterSums::BYTES + 127) / 128 * 128;
 
-template <int DT, int E, bool FULL, bool EDGE>
+// CLUSTER: the row may be split over a cluster. (Leaving its code out where it cannot be gives 3 % with 16
+// elements a thread: 16384 x 4096 bf16 with dres 92 us against 95. With 24 the registers are dealt out worse
+// without it, 16384 x 8192 fp16 with dres 193 us against 176, so those have it always.)
+template <int DT, int E, bool FULL, bool EDGE, bool CLUSTER>
 __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(const __grid_constant__ NormBwdParams p)
 {
     using D = Deal<DT, E>;
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     const int T = p.T, group = threadIdx.x / T, thread = threadIdx.x % T;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group_warps = T >> 5, warp0 = group * group_warps;
-    const int nc = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+    const int nc = CLUSTER ? static_cast<int>(cluster_size()) : 1, rank = CLUSTER ? static_cast<int>(cluster_rank()) : 0;
 
     // a lane of the copying warp stands for the group it feeds
     const bool copies = threadIdx.x >= T * p.groups;
@@ -323,12 +328,12 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
 
     if (copies && lane < p.groups) {
         ring.init(group_warps);
-        sums.init();
+        if (CLUSTER) sums.init();
         fence_mbar_init();
         fence_proxy_async_smem();
     }
     __syncthreads();
-    if (nc > 1) cluster_sync();                   // the other CTAs' barriers are set up
+    if (CLUSTER && nc > 1) cluster_sync();                   // the other CTAs' barriers are set up
     pdl_wait();
     if (copies) {
         if (lane < p.groups) ring.feed(rows, p.timeout_ns, p.err);
@@ -421,7 +426,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
             s1[1] = warp_sum(q.z);
             s2[1] = warp_sum(q.w);
         }
-        if (nc > 1) {
+        if (CLUSTER && nc > 1) {
             float4 q;
             if (warp == 0) sums.send(lane, flip, make_float4(s1[0], s2[0], s1[1], s2[1]));
             if (!sums.receive(lane, flip, (i >> 2) & 1, dead ? 0 : limit, q)) dead = true;
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
             part[beta ? p.r.hidden + e : e] = a;
         }
     }
-    if (nc > 1) cluster_sync();                   // nobody sends to a CTA that has left
+    if (CLUSTER && nc > 1) cluster_sync();                   // nobody sends to a CTA that has left
 }
 
 // dgamma and dbeta from the partial rows: 32 columns per CTA, 16 threads share a column's partials

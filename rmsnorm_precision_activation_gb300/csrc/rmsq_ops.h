@@ -44,10 +44,10 @@ cudaError_t norm_layer_int8(const NormPlan& pl, const NormParams& p, cudaStream_
 cudaError_t norm_rms_int8(const NormPlan& pl, const NormParams& p, cudaStream_t stream);
 
 // Backward pass (rmsq_norm_bwd.cu): the row kernel for a type, elements per thread (8, 16, or 24 for
-// slices of more than 7680 elements of 16 bits), whether the threads cover the slices exactly and whether
-// rows are whole vectors, and the column reduction.
+// slices of more than 7680 elements of 16 bits), whether the threads cover the slices exactly, whether
+// rows are whole vectors and whether they are split over clusters, and the column reduction.
 struct NormBwdParams;
-const void* norm_bwd_fn(int dt, int elems, bool full, bool vec);
+const void* norm_bwd_fn(int dt, int elems, bool full, bool vec, bool cluster);
 const void* norm_bwd_reduce_fn();
 
 #define RMSQ_DEFINE_NORM_DISPATCH(NAME, KIND)                                                     \

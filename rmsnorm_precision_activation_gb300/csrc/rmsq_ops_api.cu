@@ -274,7 +274,8 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         if (p.groups > 1 && ring < 8LL * p.r.slice * p.groups) ring = 8LL * p.r.slice * p.groups;   // the groups' sums
         // one partial row per cluster; where a group has several rows or a CTA several groups, as many
         // clusters as make a CTA's rows have one shift
-        const void* fn = norm_bwd_fn(dtype, g.elems, g.T * g.elems == g.slice && g.slice * cluster == hidden, g.period == 1);
+        const void* fn = norm_bwd_fn(dtype, g.elems, g.T * g.elems == g.slice && g.slice * cluster == hidden, g.period == 1,
+                                     cluster > 1);
         const unsigned threads = static_cast<unsigned>(p.T * p.groups + 32);
         const int smem = static_cast<int>(kBwdHead + ring);
         const int64_t most = bwd_parts(rows), resident = cluster == 1 ? dv.sms : resident_clusters(fn, threads, smem, cluster);
