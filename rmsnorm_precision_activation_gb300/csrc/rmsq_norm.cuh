@@ -16,6 +16,7 @@
 #pragma once
 
 #include "rmsq_device.cuh"
+#include "rmsq_param.h"
 
 namespace rmsq {
 
@@ -280,71 +281,36 @@ __device__ __forceinline__ uint4 load_columns(const typename Scalar<DT>::T* p, l
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// gamma's or beta's elements for the vector at column k of a row with the given shift: elements k - shift
-// on, taken out of the two aligned vectors they lie in (shift is the same for the whole row, so its
-// branches are uniform). Elements outside 0 to hidden are any value.
+// A parameter in device memory, as param_words reads it.
+template <int DT> struct ParamReader {
+    const typename Scalar<DT>::T* p;
+    __device__ __forceinline__ void vector(int k, uint32_t* w) const
+    {
+        const uint4 v = ld_v4(p + k);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+    __device__ __forceinline__ uint32_t element(int k) const
+    {
+        if constexpr (DT == DT_F32) return __float_as_uint(p[k]);
+        else return p[k];
+    }
+};
+
+// gamma's or beta's elements for the vector at column k of a row with the given shift (param_words).
 template <int DT, bool EDGE>
 __device__ __forceinline__ uint4 load_param(const typename Scalar<DT>::T* p, int k, int shift, int hidden)
 {
-    constexpr int VW = Elem<DT>::EPV;
     if constexpr (!EDGE) {
         return ld_v4(p + k);
     } else {
-        uint32_t w[9];
-        w[8] = 0;
-        const uint4 lower = shift > 0 && k >= VW ? ld_v4(p + k - VW) : make_uint4(0, 0, 0, 0);
-        w[0] = lower.x;
-        w[1] = lower.y;
-        w[2] = lower.z;
-        w[3] = lower.w;
-        if (k + VW <= hidden) {
-            const uint4 upper = ld_v4(p + k);
-            w[4] = upper.x;
-            w[5] = upper.y;
-            w[6] = upper.z;
-            w[7] = upper.w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[4 + j] = 0;
-#pragma unroll
-            for (int j = 0; j < VW; ++j)
-                if (k + j < hidden) {
-                    if constexpr (DT == DT_F32) w[4 + j] = __float_as_uint(p[k + j]);
-                    else w[4 + j / 2] |= static_cast<uint32_t>(p[k + j]) << (16 * (j & 1));
-                }
-        }
-        // the vector starts (VW - shift) elements into lower, upper: words first, then half a word
-        const int words = DT == DT_F32 ? 4 - shift : 4 - (shift + 1) / 2;
-        uint32_t v[5];
-        switch (words) {
-        case 0:
-#pragma unroll
-            for (int j = 0; j < 5; ++j) v[j] = w[j];
-            break;
-        case 1:
-#pragma unroll
-            for (int j = 0; j < 5; ++j) v[j] = w[j + 1];
-            break;
-        case 2:
-#pragma unroll
-            for (int j = 0; j < 5; ++j) v[j] = w[j + 2];
-            break;
-        case 3:
-#pragma unroll
-            for (int j = 0; j < 5; ++j) v[j] = w[j + 3];
-            break;
-        default:
-#pragma unroll
-            for (int j = 0; j < 5; ++j) v[j] = w[j + 4];
-        }
-        if (DT != DT_F32 && (shift & 1)) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = __funnelshift_r(v[j], v[j + 1], 16);
-        }
+        uint32_t v[4];
+        param_words<Elem<DT>::EPV>(ParamReader<DT>{p}, k, shift, hidden, v);
         return make_uint4(v[0], v[1], v[2], v[3]);
     }
 }
-
 
 // One CTA's v to slot `rank` of every CTA of the cluster (lanes of warp 0), and everybody's read back:
 // lane r of every warp gets rank r's, 0 past the cluster.
