@@ -291,9 +291,10 @@ const char* rmsq_status_string(rmsq_status status);
 /* ---------------------------------------------------------------------------------------------
  * rmsq_device_status -- errors raised on the device since the last call, for the current device.
  * Every wait inside a kernel on a bulk-copy (mbarrier) phase is bounded in time; a wait that runs
- * out sets a flag and the CTA stops, after waiting (for four times the bound) for the copies it
- * has in flight. After RMSQ_ERR_TIMEOUT the outputs of the launches since the last call are not
- * to be trusted. If one of those drain waits ran out as well (a second flag, reported the same
+ * out sets a flag and the CTA stops, after waiting (for four times the bound; in layernorm_backward
+ * and matmul_int8 for a second at least) for the copies it has in flight. After RMSQ_ERR_TIMEOUT the
+ * outputs of the launches since the last call are not to be trusted. If one of those drain waits ran
+ * out as well (a second flag, reported the same
  * way), a CTA may have exited with a copy into its shared memory still pending; treat the CUDA
  * context as unreliable then. The cluster barrier of the cluster schedule is a hardware barrier
  * that cannot be bounded: every CTA of a cluster makes the same barrier calls (a timed-out wait
@@ -336,7 +337,8 @@ rmsq_status rmsq_device_status(void);
  *                    launch may be scheduled while the previous kernel on the stream finishes; it
  *                    waits for that kernel before touching global memory). 0 turns this off for
  *                    later calls. Returns the previous setting.
- * rmsq_set_wait_timeout_ns  bound of every device-side wait (default 2e9 ns).
+ * rmsq_set_wait_timeout_ns  bound of every device-side wait (default 2e9 ns). layernorm_backward and
+ *                    matmul_int8 count it in units of 1024 ns, up to 2^40 ns (18 minutes).
  * rmsq_selftest_wait_timeout  launches one CTA that waits on a barrier nothing will complete,
  *                    bounded by timeout_ns, so a test can check that the bound fires and is
  *                    reported by rmsq_device_status without hanging the GPU.

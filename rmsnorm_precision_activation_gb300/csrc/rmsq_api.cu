@@ -222,7 +222,9 @@ bool device_view(DeviceView* v)
     v->sms = di->sms;
     v->smem_optin = di->smem_optin;
     v->err = di->err;
-    v->timeout_ns = g_timeout_ns.load();
+    const unsigned long long timeout_ns = g_timeout_ns.load();
+    v->wait = wait_units(timeout_ns);
+    v->drain = drain_units(timeout_ns);
     return true;
 }
 
@@ -926,7 +928,9 @@ extern "C" int rmsq_set_pdl(int enable)
 
 extern "C" void rmsq_set_wait_timeout_ns(uint64_t timeout_ns)
 {
-    g_timeout_ns = timeout_ns > 0 ? timeout_ns : 1;
+    // (four times it, the bound of a stopping CTA's copies, has to fit 64 bits)
+    const uint64_t most = UINT64_MAX / 4;
+    g_timeout_ns = timeout_ns == 0 ? 1 : timeout_ns < most ? timeout_ns : most;
 }
 
 extern "C" rmsq_status rmsq_selftest_wait_timeout(uint64_t timeout_ns, void* stream)

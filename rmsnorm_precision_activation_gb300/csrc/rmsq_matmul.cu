@@ -176,7 +176,8 @@ extern "C" rmsq_status matmul_int8(const void* input, const float* input_scale, 
     p.n = n;
     p.k = static_cast<int>(k);
     p.dt = output_dtype;
-    p.timeout_ns = dv.timeout_ns;
+    p.wait = dv.wait;
+    p.drain = dv.drain;
     const cudaError_t e = launch_matmul(p, dv, static_cast<cudaStream_t>(stream));
     if (e == cudaSuccess) return RMSQ_OK;
     cudaGetLastError();

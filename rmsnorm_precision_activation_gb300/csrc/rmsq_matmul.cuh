@@ -20,7 +20,7 @@ struct MatmulParams {
     long long m, n;
     int k;
     int dt;                    // output's type
-    unsigned long long timeout_ns;
+    uint32_t wait, drain;      // bounds of waits, and of what a stopping CTA has in flight (rmsq_ops_plan.h)
 };
 
 __device__ __forceinline__ float load_as(const void* p, long long i, int dt)

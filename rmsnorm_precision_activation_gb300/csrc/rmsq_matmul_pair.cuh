@@ -138,7 +138,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
     const uint32_t tmem_a = tmem + 2 * TOKENS;      // operand stages of 32 columns behind the accumulators
     pdl_wait();
 
-    const uint32_t limit = wait_limit(p.timeout_ns), drain_limit = wait_limit(4 * p.timeout_ns);
+    const uint32_t limit = p.wait, drain_limit = p.drain;
     bool ok = true;
 
     if (warp < 4) {

@@ -233,7 +233,7 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
     const uint32_t tmem_a = tmem + S::ACC;   // operand stages of 32 columns behind the accumulator
     pdl_wait();
 
-    const uint32_t limit = wait_limit(p.timeout_ns), drain_limit = wait_limit(4 * p.timeout_ns);
+    const uint32_t limit = p.wait, drain_limit = p.drain;
     bool ok = true;
 
     if (warp == 0) {

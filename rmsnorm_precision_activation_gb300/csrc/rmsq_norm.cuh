@@ -160,28 +160,23 @@ template <int SCOPE> __device__ __forceinline__ bool mbar_test(uint32_t bar, uin
     return ok != 0;
 }
 
-// A timeout as mbar_wait takes it: 32 bits of nanoseconds (registers are scarce where it waits).
-__device__ __forceinline__ uint32_t wait_limit(unsigned long long timeout_ns)
+// Time in units of 1024 ns, as bounds are given (rmsq_ops_plan.h).
+__device__ __forceinline__ uint32_t time_units()
 {
-    return timeout_ns < 4000000000ull ? static_cast<uint32_t>(timeout_ns) : 4000000000u;
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return static_cast<uint32_t>(t >> 10);
 }
 
-__device__ __forceinline__ uint32_t globaltimer_lo()
-{
-    uint32_t t;
-    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-    return t;
-}
-
-template <int SCOPE> __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t limit_ns)
+template <int SCOPE> __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint32_t limit)
 {
     if (mbar_test<SCOPE>(bar, parity)) return true;
     if (mbar_try_wait_long<SCOPE>(bar, parity)) return true;
-    const uint32_t t0 = globaltimer_lo();
+    const uint32_t t0 = time_units();
 #pragma unroll 1
     do {
         if (mbar_try_wait_long<SCOPE>(bar, parity)) return true;
-    } while (globaltimer_lo() - t0 <= limit_ns);
+    } while (time_units() - t0 <= limit);
     return false;
 }
 

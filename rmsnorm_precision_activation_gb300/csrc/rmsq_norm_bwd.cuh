@@ -52,7 +52,7 @@ struct NormBwdParams {
     float offset;
     int T;                   // threads per row group
     int groups;              // row groups per CTA
-    unsigned long long timeout_ns;
+    uint32_t wait, drain;    // bounds of waits, and of what a stopping CTA has in flight (rmsq_ops_plan.h)
 };
 
 struct NormBwdReduceParams {
@@ -216,10 +216,9 @@ template <int DT, bool EDGE> struct RowRing {
     // Brings the group's rows (one thread of the CTA's copying warp: issuing a row's copies takes about
     // 1000 cycles, which a working warp would keep its group waiting for). After a wait that ran out,
     // waits (bounded) for the copies in flight, so that they end before the CTA does.
-    __device__ __forceinline__ void feed(const Rows& rows, unsigned long long timeout_ns, unsigned int* err) const
+    __device__ __forceinline__ void feed(const Rows& rows, uint32_t limit, uint32_t drain, unsigned int* err) const
     {
         const uint64_t policy = l2_evict_normal_policy();
-        const uint32_t limit = wait_limit(timeout_ns);
         int stage = 0, phase = 1, i = 0;
         for (; i < rows.n; ++i) {
             if (!mbar_wait<SCOPE_CTA>(empty(stage), phase, limit)) break;
@@ -233,7 +232,7 @@ template <int DT, bool EDGE> struct RowRing {
         if (i < rows.n) {
             bool drained = true;
             for (int j = i > r.stages ? i - r.stages : 0; j < i; ++j)
-                drained &= mbar_wait<SCOPE_CTA>(full(j % r.stages), (j / r.stages) & 1, wait_limit(4 * timeout_ns));
+                drained &= mbar_wait<SCOPE_CTA>(full(j % r.stages), (j / r.stages) & 1, drain);
             atomicOr(err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
         }
     }
@@ -272,9 +271,9 @@ struct ClusterSums {
                 ::"r"(slot), "r"(bar), "r"(lane), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
     }
     // Lane r of every warp gets rank r's (zeros past the cluster); false: the wait ran out.
-    __device__ __forceinline__ bool receive(int lane, int flip, int phase, uint32_t limit_ns, float4& v) const
+    __device__ __forceinline__ bool receive(int lane, int flip, int phase, uint32_t limit, float4& v) const
     {
-        const bool ok = mbar_wait<SCOPE_CLUSTER>(bars + 8 * flip, phase, limit_ns);
+        const bool ok = mbar_wait<SCOPE_CLUSTER>(bars + 8 * flip, phase, limit);
         v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (lane < nc) {
             const uint4 w = ld_shared_v4(slots + (flip * 16 + lane) * 16);
@@ -336,7 +335,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
     if (CLUSTER && nc > 1) cluster_sync();                   // the other CTAs' barriers are set up
     pdl_wait();
     if (copies) {
-        if (lane < p.groups) ring.feed(rows, p.timeout_ns, p.err);
+        if (lane < p.groups) ring.feed(rows, p.wait, p.drain, p.err);
         return;
     }
     const int workers = T * p.groups;
@@ -347,7 +346,7 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) acc_g[e] = acc_b[e] = make_float2(0.f, 0.f);
 
-    const uint32_t limit = wait_limit(p.timeout_ns);
+    const uint32_t limit = p.wait;
     const float inv_h = 1.0f / static_cast<float>(p.r.hidden);
     bool dead = false;                            // a wait ran out: finish without waiting again
     int stage = 0, phase = 0;

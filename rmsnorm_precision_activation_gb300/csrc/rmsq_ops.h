@@ -6,6 +6,7 @@
 
 #include "rmsq.h"
 #include "rmsq_norm.cuh"
+#include "rmsq_ops_plan.h"
 
 namespace rmsq {
 
@@ -14,7 +15,7 @@ struct DeviceView {
     int sms;
     int smem_optin;
     unsigned int* err;                // device error word
-    unsigned long long timeout_ns;    // bound of device-side waits
+    uint32_t wait, drain;             // bounds of device-side waits (rmsq_ops_plan.h)
 };
 // False: no usable device.
 bool device_view(DeviceView* v);

@@ -250,7 +250,8 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         p.r.hidden = static_cast<int>(hidden);
         p.r.total = rows * hidden * elem_bytes(dtype);
         p.offset = weight_offset;
-        p.timeout_ns = dv.timeout_ns;
+        p.wait = dv.wait;
+        p.drain = dv.drain;
 
         const RowGeometry g = row_geometry(p.r.hidden, dtype);
         p.r.slice = g.slice;
