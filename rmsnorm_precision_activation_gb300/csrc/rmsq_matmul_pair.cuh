@@ -156,14 +156,12 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                     fetch(slot, s, tn, tm);
                 }
             }
-            if (!ok) {
-                // the copies in flight end before the CTA does
-                bool drained = true;
-                for (long long i = it > RAWS ? it - RAWS : 0; i < it; ++i)
-                    drained &= mbar_wait<SCOPE_CTA>(raw_full + 8 * static_cast<int>(i % RAWS),
-                                                 static_cast<uint32_t>(i / RAWS) & 1u, drain_limit);
-                atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
-            }
+            // the copies in flight end before the CTA does, whichever role stopped waiting
+            bool drained = true;
+            for (long long i = it > RAWS ? it - RAWS : 0; i < it; ++i)
+                drained &= mbar_wait<SCOPE_CTA>(raw_full + 8 * static_cast<int>(i % RAWS),
+                                             static_cast<uint32_t>(i / RAWS) & 1u, drain_limit);
+            if (!ok || !drained) atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
         } else if (warp == 1 && rank == 0) {
             constexpr uint32_t idesc = (1u << 4) | ((TOKENS / 8u) << 17) | ((2u * kTcRows / 16u) << 24);
             const bool one = elect_one();
@@ -209,11 +207,9 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
                     phase = next_phase;
                 }
             }
-            if (!ok && one) {
-                // the MMAs in flight end before either CTA frees its TMEM (the barrier below)
+            if (one) {
                 tc_commit_pair(drain);
-                const bool drained = mbar_wait<SCOPE_CTA>(drain, 0, drain_limit);
-                atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
+                if (!ok) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
             }
         }
         __syncwarp();
@@ -336,6 +332,10 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
 
     tc_fence_before();
     __syncthreads();
+    // the MMAs in flight end, and their arrivals come, before either CTA frees its TMEM or leaves,
+    // whichever role stopped waiting
+    if (threadIdx.x == 0 && !mbar_wait<SCOPE_CTA>(drain, 0, drain_limit))
+        atomicOr(p.err, ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
     cluster_sync();                          // no CTA leaves while the other arrives on its barriers
     if (warp == 1) {
         tc_fence_after();

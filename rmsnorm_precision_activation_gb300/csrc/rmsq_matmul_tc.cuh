@@ -17,8 +17,9 @@
 // The weight is read as codes, so a call with few tokens streams one byte per weight; CTAs of a
 // cluster then share a tile's k and add their integer sums through distributed shared memory.
 //
-// Every wait is bounded: a role whose wait runs out leaves its loop, the MMA and copy roles wait
-// (bounded again) for what they have in flight, and the CTA frees its TMEM and ends.
+// Every wait is bounded: a role whose wait runs out leaves its loop, and so then do the others. At their
+// end the MMA and copy roles always wait (bounded again) for what they have in flight, because they can
+// have issued everything when another role's wait runs out; then the CTA frees its TMEM and ends.
 #pragma once
 
 #include <cuda.h>
@@ -250,14 +251,12 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                     fetch(slot, s, tn, tm);
                 }
             }
-            if (!ok) {
-                // the copies in flight end before the CTA does
-                bool drained = true;
-                for (long long i = it > RAWS ? it - RAWS : 0; i < it; ++i)
-                    drained &= mbar_wait<SCOPE_CTA>(raw_full + 8 * static_cast<int>(i % RAWS),
-                                                 static_cast<uint32_t>(i / RAWS) & 1u, drain_limit);
-                atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
-            }
+            // the copies in flight end before the CTA does, whichever role stopped waiting
+            bool drained = true;
+            for (long long i = it > RAWS ? it - RAWS : 0; i < it; ++i)
+                drained &= mbar_wait<SCOPE_CTA>(raw_full + 8 * static_cast<int>(i % RAWS),
+                                             static_cast<uint32_t>(i / RAWS) & 1u, drain_limit);
+            if (!ok || !drained) atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -306,11 +305,11 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
                 phase = next_phase;
             }
         }
-        if (!ok && one) {
-            // the MMAs in flight end before TMEM is freed
+        if (one) {
+            // the MMAs in flight end before TMEM is freed, whichever role stopped waiting
             tc_commit(drain);
             const bool drained = mbar_wait<SCOPE_CTA>(drain, 0, drain_limit);
-            atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
+            if (!ok || !drained) atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
         }
         __syncwarp();
     } else if (warp >= 4 && warp < 12) {

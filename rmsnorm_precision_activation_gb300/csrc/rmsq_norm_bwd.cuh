@@ -214,8 +214,8 @@ template <int DT, bool EDGE> struct RowRing {
     }
 
     // Brings the group's rows (one thread of the CTA's copying warp: issuing a row's copies takes about
-    // 1000 cycles, which a working warp would keep its group waiting for). After a wait that ran out,
-    // waits (bounded) for the copies in flight, so that they end before the CTA does.
+    // 1000 cycles, which a working warp would keep its group waiting for). At its end it waits (bounded)
+    // for the copies in flight, so that they end before the CTA does, whichever thread's wait ran out.
     __device__ __forceinline__ void feed(const Rows& rows, uint32_t limit, uint32_t drain, unsigned int* err) const
     {
         const uint64_t policy = l2_evict_normal_policy();
@@ -229,12 +229,10 @@ template <int DT, bool EDGE> struct RowRing {
                 phase ^= 1;
             }
         }
-        if (i < rows.n) {
-            bool drained = true;
-            for (int j = i > r.stages ? i - r.stages : 0; j < i; ++j)
-                drained &= mbar_wait<SCOPE_CTA>(full(j % r.stages), (j / r.stages) & 1, drain);
-            atomicOr(err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
-        }
+        bool drained = true;
+        for (int j = i > r.stages ? i - r.stages : 0; j < i; ++j)
+            drained &= mbar_wait<SCOPE_CTA>(full(j % r.stages), (j / r.stages) & 1, drain);
+        if (i < rows.n || !drained) atomicOr(err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
     }
 };
 
