@@ -246,7 +246,8 @@ __device__ __forceinline__ void group_sync(int group, int T)
 // A row's sums among the CTAs of a cluster: each writes its own into a slot of every CTA, which counts
 // the bytes on its own barrier. Two sets in turn: a CTA sends a row's sums after it has read those of
 // the row before, so nobody writes a set that is still read. No cluster barrier, which the copying
-// warp would have to join; every wait is bounded.
+// warp would have to join; every wait is bounded. A CTA whose wait ran out sends no more, so the others'
+// waits run out too, and it stays (linger) until what they had sent it has landed.
 struct ClusterSums {
     uint32_t bars, slots;          // shared addresses: 2 barriers, [2][16] float4
     int nc, rank;
@@ -278,6 +279,13 @@ struct ClusterSums {
             v = make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
         }
         return ok;
+    }
+    // After the cluster's last barrier, when nobody sends any more: time for what was sent to land, which
+    // takes about a microsecond. A CTA that received every row's sums has nothing under way to it.
+    static __device__ __forceinline__ void linger()
+    {
+        const uint32_t t0 = time_units();
+        while (time_units() - t0 < 1000) __nanosleep(100000);
     }
 };
 
@@ -425,7 +433,8 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
         }
         if (CLUSTER && nc > 1) {
             float4 q;
-            if (warp == 0) sums.send(lane, flip, make_float4(s1[0], s2[0], s1[1], s2[1]));
+            // (a warp whose wait ran out sends no more: its arrival could fall into the phase it did not see end)
+            if (warp == 0 && !__any_sync(0xFFFFFFFFu, dead)) sums.send(lane, flip, make_float4(s1[0], s2[0], s1[1], s2[1]));
             if (!sums.receive(lane, flip, (i >> 2) & 1, dead ? 0 : limit, q)) dead = true;
             s1[0] = warp_sum(q.x);
             s2[0] = warp_sum(q.y);
@@ -506,7 +515,10 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
             part[beta ? p.r.hidden + e : e] = a;
         }
     }
-    if (CLUSTER && nc > 1) cluster_sync();                   // nobody sends to a CTA that has left
+    if (CLUSTER && nc > 1) {
+        cluster_sync();                                      // nobody sends to a CTA that has left
+        if (dead) ClusterSums::linger();
+    }
 }
 
 // dgamma and dbeta from the partial rows: 32 columns per CTA, 16 threads share a column's partials
