@@ -273,22 +273,13 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         const int64_t stage = static_cast<int64_t>(p.r.slot) * p.r.ntens * p.groups;
         int64_t ring = p.r.stages * stage;
         if (p.groups > 1 && ring < 8LL * p.r.slice * p.groups) ring = 8LL * p.r.slice * p.groups;   // the groups' sums
-        // one partial row per cluster; where a group has several rows or a CTA several groups, as many
-        // clusters as make a CTA's rows have one shift
         const void* fn = norm_bwd_fn(dtype, g.elems, g.T * g.elems == g.slice && g.slice * cluster == hidden, g.period == 1,
                                      cluster > 1);
         const unsigned threads = static_cast<unsigned>(p.T * p.groups + 32);
         const int smem = static_cast<int>(kBwdHead + ring);
-        const int64_t most = bwd_parts(rows), resident = cluster == 1 ? dv.sms : resident_clusters(fn, threads, smem, cluster);
-        int64_t parts = (rows + p.groups - 1) / p.groups;
-        if (parts > resident) parts = resident;
-        if (parts > most) parts = most;
-        if (parts * p.groups < rows || p.groups > 1) {
-            if (parts >= g.period) parts = parts / g.period * g.period;
-            else parts = g.period;
-            if (parts > most) return RMSQ_ERR_LAUNCH;      // a device of fewer SMs than the period needs
-        }
-        if (parts < 1) return RMSQ_ERR_LAUNCH;
+        int64_t resident = cluster == 1 ? dv.sms : resident_clusters(fn, threads, smem, cluster);
+        if (resident < 1) resident = dv.sms / cluster;                  // not known
+        const int64_t parts = bwd_clusters(rows, p.groups, g.period, resident, bwd_parts(rows));
         r.parts = static_cast<int>(parts);
         void* args[] = {&p};
         const rmsq_status e = status_of(launch_kernel(

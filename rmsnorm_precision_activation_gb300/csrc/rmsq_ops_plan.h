@@ -28,4 +28,21 @@ inline uint32_t drain_units(uint64_t timeout_ns)
     return 4 * units < second ? second : 4 * units;
 }
 
+// Clusters (CTAs where a cluster is one) that walk the rows of layer norm's backward pass, each with
+// `groups` row groups and one partial row of the column sums: group g of cluster c takes row
+// g * clusters + c and every (clusters * groups)-th from there. At most `most`, and otherwise as many as
+// run at a time (`resident`), but a CTA's rows have to start at the same place against a 16-byte boundary,
+// which rows do that are a multiple of `period` apart (1 to 8). So the clusters are a multiple of the period,
+// unless nobody has more than one row; more than are resident run one after another, which they may, as
+// clusters do not wait for each other. most >= min(rows, period).
+inline int64_t bwd_clusters(int64_t rows, int groups, int period, int64_t resident, int64_t most)
+{
+    if (rows < period) return rows;
+    int64_t n = (rows + groups - 1) / groups;
+    if (n > resident) n = resident;
+    if (n > most) n = most;
+    if (groups == 1 && n == rows) return n;
+    return n < period ? period : n / period * period;
+}
+
 }  // namespace rmsq
