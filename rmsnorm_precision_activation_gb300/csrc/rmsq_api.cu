@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <new>
 
 #include "rmsq.h"
 #include "rmsq_host.h"
@@ -231,33 +232,30 @@ bool device_view(DeviceView* v)
 struct ReadyFn {
     const void* fn;
     int dev;
-    int clusters[17];     // clusters of each size that fit on the device at a time; 0: not asked yet
 };
 static ReadyFn g_ready[512];
 static int g_nready = 0;
 
-// fn's entry for the current device, with its attributes set (under g_mu); null when the table is full
-// or a call fails (*e).
-static ReadyFn* ready_fn(const void* fn, int smem, cudaError_t* e)
+// Sets fn's attributes for the current device (under g_mu), once while the table has room.
+static cudaError_t ready_fn(const void* fn, int smem, int* dev)
 {
-    int dev = 0;
-    *e = cudaGetDevice(&dev);
-    if (*e != cudaSuccess) return nullptr;
+    cudaError_t e = cudaGetDevice(dev);
+    if (e != cudaSuccess) return e;
     for (int i = 0; i < g_nready; ++i)
-        if (g_ready[i].fn == fn && g_ready[i].dev == dev) return &g_ready[i];
+        if (g_ready[i].fn == fn && g_ready[i].dev == *dev) return cudaSuccess;
     cudaFuncAttributes fa;
-    *e = cudaFuncGetAttributes(&fa, fn);
-    if (*e == cudaSuccess)
-        *e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  g_dev[dev].smem_optin - static_cast<int>(fa.sharedSizeBytes));
+    e = cudaFuncGetAttributes(&fa, fn);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 g_dev[*dev].smem_optin - static_cast<int>(fa.sharedSizeBytes));
     // clusters of 16 CTAs are beyond the portable size of 8
-    if (*e == cudaSuccess) *e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     // the rings of several CTAs fit on one SM
-    if (*e == cudaSuccess && smem > 0)
-        *e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (*e != cudaSuccess || g_nready == static_cast<int>(sizeof(g_ready) / sizeof(g_ready[0]))) return nullptr;
-    g_ready[g_nready] = ReadyFn{fn, dev, {}};
-    return &g_ready[g_nready++];
+    if (e == cudaSuccess && smem > 0)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e == cudaSuccess && g_nready < static_cast<int>(sizeof(g_ready) / sizeof(g_ready[0])))
+        g_ready[g_nready++] = ReadyFn{fn, *dev};
+    return e;
 }
 
 static void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], dim3 grid, unsigned threads, int smem,
@@ -278,26 +276,33 @@ static void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], d
     cfg->numAttrs = cluster > 1 ? 2 : 1;
 }
 
+// (never destroyed: a thread may still launch while the process ends)
+static ResidentClusters& resident_table()
+{
+    alignas(ResidentClusters) static unsigned char store[sizeof(ResidentClusters)];
+    static ResidentClusters* const table = new (store) ResidentClusters;
+    return *table;
+}
+
 int resident_clusters(const void* fn, unsigned threads, int smem, int cluster)
 {
     std::lock_guard<std::mutex> lock(g_mu);
-    cudaError_t e;
-    ReadyFn* const r = ready_fn(fn, smem, &e);
-    if (r == nullptr || cluster < 1 || cluster > 16) return 0;
-    if (r->clusters[cluster] == 0) {
+    int dev = 0;
+    if (ready_fn(fn, smem, &dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return resident_table().get({fn, dev, threads, smem, cluster}, [&]() {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         configure(&cfg, attr, dim3(static_cast<unsigned>(cluster)), threads, smem, cluster, nullptr);
         cfg.attrs = attr + 1;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
-        }
-        r->clusters[cluster] = n;
-    }
-    return r->clusters[cluster];
+        if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess) return n;
+        cudaGetLastError();
+        return 0;
+    });
 }
 
 cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem, int cluster,
@@ -306,7 +311,8 @@ cudaError_t launch_kernel(const void* fn, dim3 grid, unsigned threads, int smem,
     cudaError_t e;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        ready_fn(fn, smem, &e);
+        int dev = 0;
+        e = ready_fn(fn, smem, &dev);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg;

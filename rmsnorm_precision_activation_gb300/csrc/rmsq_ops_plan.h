@@ -3,8 +3,34 @@
 #pragma once
 
 #include <cstdint>
+#include <map>
+#include <tuple>
 
 namespace rmsq {
+
+// How many clusters of a launch a device runs at a time, as the driver was asked once: it goes by the
+// kernel, the device and the whole shape of the launch. Not synchronised.
+class ResidentClusters {
+public:
+    using Key = std::tuple<const void*, int, unsigned, int, int>;     // kernel, device, threads, smem, cluster
+
+    // query() gives the number, or less than 1 where it cannot be had; that is not kept.
+    template <class Query> int get(const Key& key, Query query)
+    {
+        const auto it = known_.find(key);
+        if (it != known_.end()) return it->second;
+        const int n = query();
+        if (n >= 1) {
+            try {
+                known_.emplace(key, n);
+            } catch (...) {}                                          // no memory: asked again next time
+        }
+        return n;
+    }
+
+private:
+    std::map<Key, int> known_;
+};
 
 // Device-side waits count in units of 1024 ns: 32 bits of those last 73 minutes (registers are scarce
 // where the kernels wait, and a bound in nanoseconds would be 4 s at most). At least one unit, so that a
