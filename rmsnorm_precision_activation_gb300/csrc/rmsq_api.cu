@@ -229,20 +229,20 @@ bool device_view(DeviceView* v)
     return true;
 }
 
-struct ReadyFn {
-    const void* fn;
-    int dev;
-};
-static ReadyFn g_ready[512];
-static int g_nready = 0;
+// (the tables are never destroyed: a thread may still launch while the process ends)
+template <class Table> static Table& kept()
+{
+    alignas(Table) static unsigned char store[sizeof(Table)];
+    static Table* const table = new (store) Table;
+    return *table;
+}
 
-// Sets fn's attributes for the current device (under g_mu), once while the table has room.
+// Sets fn's attributes for the current device (under g_mu), once.
 static cudaError_t ready_fn(const void* fn, int smem, int* dev)
 {
     cudaError_t e = cudaGetDevice(dev);
     if (e != cudaSuccess) return e;
-    for (int i = 0; i < g_nready; ++i)
-        if (g_ready[i].fn == fn && g_ready[i].dev == *dev) return cudaSuccess;
+    if (kept<PreparedKernels>().has(fn, *dev)) return cudaSuccess;
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, fn);
     if (e == cudaSuccess)
@@ -253,8 +253,7 @@ static cudaError_t ready_fn(const void* fn, int smem, int* dev)
     // the rings of several CTAs fit on one SM
     if (e == cudaSuccess && smem > 0)
         e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    if (e == cudaSuccess && g_nready < static_cast<int>(sizeof(g_ready) / sizeof(g_ready[0])))
-        g_ready[g_nready++] = ReadyFn{fn, *dev};
+    if (e == cudaSuccess) kept<PreparedKernels>().add(fn, *dev);
     return e;
 }
 
@@ -276,14 +275,6 @@ static void configure(cudaLaunchConfig_t* cfg, cudaLaunchAttribute (&attr)[2], d
     cfg->numAttrs = cluster > 1 ? 2 : 1;
 }
 
-// (never destroyed: a thread may still launch while the process ends)
-static ResidentClusters& resident_table()
-{
-    alignas(ResidentClusters) static unsigned char store[sizeof(ResidentClusters)];
-    static ResidentClusters* const table = new (store) ResidentClusters;
-    return *table;
-}
-
 int resident_clusters(const void* fn, unsigned threads, int smem, int cluster)
 {
     std::lock_guard<std::mutex> lock(g_mu);
@@ -292,7 +283,7 @@ int resident_clusters(const void* fn, unsigned threads, int smem, int cluster)
         cudaGetLastError();
         return 0;
     }
-    return resident_table().get({fn, dev, threads, smem, cluster}, [&]() {
+    return kept<ResidentClusters>().get({fn, dev, threads, smem, cluster}, [&]() {
         cudaLaunchConfig_t cfg;
         cudaLaunchAttribute attr[2];
         configure(&cfg, attr, dim3(static_cast<unsigned>(cluster)), threads, smem, cluster, nullptr);

@@ -4,7 +4,9 @@
 
 #include <cstdint>
 #include <map>
+#include <set>
 #include <tuple>
+#include <utility>
 
 namespace rmsq {
 
@@ -30,6 +32,21 @@ public:
 
 private:
     std::map<Key, int> known_;
+};
+
+// Kernels whose attributes are set on a device. Not synchronised.
+class PreparedKernels {
+public:
+    bool has(const void* fn, int dev) const { return set_.count({fn, dev}) != 0; }
+    void add(const void* fn, int dev)
+    {
+        try {
+            set_.insert({fn, dev});
+        } catch (...) {}                                              // no memory: set again next time
+    }
+
+private:
+    std::set<std::pair<const void*, int>> set_;
 };
 
 // Device-side waits count in units of 1024 ns: 32 bits of those last 73 minutes (registers are scarce

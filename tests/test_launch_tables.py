@@ -1,5 +1,6 @@
 """What the library keeps of a launch between calls, on the CPU: the number of clusters that run at a time
-goes by the whole shape of the launch, and one that cannot be had is asked again."""
+goes by the whole shape of the launch, and one that cannot be had is asked again; kernels are prepared once per
+device, however many there are."""
 import host_program
 
 
@@ -27,6 +28,29 @@ int main()
     // a failed question is not kept
     wrong += get(0, 0, 64, 0, 2, 0) != 0 || get(0, 0, 64, 0, 2, 60) != 60 || get(0, 0, 64, 0, 2, 99) != 60;
     std::printf("%d\\n", wrong);
+}
+""", tmp_path)
+    assert out.strip() == "0"
+
+
+def test_more_prepared_kernels_than_any_process_has(tmp_path):
+    # 200 kernels on each of 64 devices
+    out = host_program.run("""
+#include <cstdio>
+#include "rmsq_ops_plan.h"
+static char kernels[200];
+int main()
+{
+    rmsq::PreparedKernels table;
+    int wrong = 0;
+    for (int dev = 0; dev < 64; ++dev)
+        for (char& k : kernels) {
+            wrong += table.has(&k, dev);
+            table.add(&k, dev);
+        }
+    for (int dev = 0; dev < 64; ++dev)
+        for (char& k : kernels) wrong += !table.has(&k, dev);
+    std::printf("%d\\n", wrong + table.has(kernels, 64));
 }
 """, tmp_path)
     assert out.strip() == "0"
