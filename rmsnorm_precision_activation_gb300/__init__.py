@@ -252,7 +252,12 @@ def _elsewhere(input, stream):
     """Whether the call needs another device or stream to be current (_queue)."""
     if not input.is_cuda:
         raise ValueError("input must be a CUDA tensor")
-    return stream is not None or input.get_device() != torch.cuda.current_device()
+    if stream is not None:
+        # (making a stream current makes its device current, where the call would look for another stream)
+        if stream.device_index != input.get_device():
+            raise ValueError("stream must be a stream of the input's device")
+        return True
+    return input.get_device() != torch.cuda.current_device()
 
 
 @contextlib.contextmanager
