@@ -289,6 +289,16 @@ def _count(name, t, n, dtype, index):
     return t.data_ptr()
 
 
+def _vector(name, t, n, dtype, index):
+    """_count for a vector that is only read, one element at a time: (what is read, its pointer). A slice
+    off 16-byte boundaries, as a program makes that splits its tokens or channels, is read from a copy."""
+    p = _count(name, t, n, dtype, index)
+    if p & 15:
+        t = t.clone()
+        p = t.data_ptr()
+    return t, p
+
+
 def _norm_inputs(input, gamma, beta, residual, residual_output):
     """Checks a norm's inputs; (device index, shape, rows, H, the C call's first pointers,
     residual_output)."""
@@ -353,7 +363,8 @@ def layernorm_backward(grad_output, input, gamma, mean, rstd, *, grad_residual=N
     had a residual); grad_residual: the gradient that reaches residual_output from elsewhere.
     param_grad_dtype: type of grad_gamma and grad_beta, the input's (default) or torch.float32.
     workspace: a CUDA uint8 tensor of layernorm_backward_workspace(rows, H) bytes, allocated when
-    not passed.
+    not passed. mean and rstd may be slices off 16-byte boundaries (they are copied then); every other
+    tensor starts on one.
 
     Returns (grad_input [..., H], grad_gamma [H], grad_beta [H])."""
     if _elsewhere(input, stream):
@@ -366,8 +377,8 @@ def layernorm_backward(grad_output, input, gamma, mean, rstd, *, grad_residual=N
     dtype = input.dtype
     dy = _same("grad_output", grad_output, shape, dtype, index)
     dr = None if grad_residual is None else _same("grad_residual", grad_residual, shape, dtype, index)
-    mp = _count("mean", mean, rows, torch.float32, index)
-    rp = _count("rstd", rstd, rows, torch.float32, index)
+    mean, mp = _vector("mean", mean, rows, torch.float32, index)
+    rstd, rp = _vector("rstd", rstd, rows, torch.float32, index)
     pdt = dtype if param_grad_dtype is None else param_grad_dtype
     if pdt is not dtype and pdt is not torch.float32:
         raise TypeError("param_grad_dtype must be the input's dtype or float32")
@@ -457,7 +468,8 @@ def matmul_int8(input, input_scale, weight, weight_scale, *, bias=None, out_dtyp
     """(input @ weight.T) * input_scale * weight_scale + bias on int8 codes, integer sums exact.
 
     input int8 [..., K] with one fp32 scale per row, weight int8 [N, K] with one fp32 scale per
-    output channel, bias [N] of out_dtype. K must be a multiple of 16.
+    output channel, bias [N] of out_dtype. K must be a multiple of 16. The codes and the output start on
+    16-byte boundaries; scales and bias may be slices that do not (they are copied then).
 
     Returns output [..., N] of out_dtype."""
     if _elsewhere(input, stream):
@@ -477,9 +489,9 @@ def matmul_int8(input, input_scale, weight, weight_scale, *, bias=None, out_dtyp
         raise ValueError("weight must have shape (N, %d)" % K)
     N = weight.shape[0]
     w = _same("weight", weight, (N, K), torch.int8, index)
-    sa = _count("input_scale", input_scale, M, torch.float32, index)
-    sw = _count("weight_scale", weight_scale, N, torch.float32, index)
-    b = None if bias is None else _count("bias", bias, N, out_dtype, index)
+    input_scale, sa = _vector("input_scale", input_scale, M, torch.float32, index)
+    weight_scale, sw = _vector("weight_scale", weight_scale, N, torch.float32, index)
+    bias, b = (None, None) if bias is None else _vector("bias", bias, N, out_dtype, index)
     oshape = shape[:-1] + (N,)
     if output is None:
         output = torch.empty(oshape, dtype=out_dtype, device=input.device)
