@@ -433,8 +433,8 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
         }
         if (CLUSTER && nc > 1) {
             float4 q;
-            // (a warp whose wait ran out sends no more: its arrival could fall into the phase it did not see end)
-            if (warp == 0 && !__any_sync(0xFFFFFFFFu, dead)) sums.send(lane, flip, make_float4(s1[0], s2[0], s1[1], s2[1]));
+            // (a lane whose wait ran out sends no more: its arrival could fall into the phase it did not see end)
+            if (warp == 0 && !dead) sums.send(lane, flip, make_float4(s1[0], s2[0], s1[1], s2[1]));
             if (!sums.receive(lane, flip, (i >> 2) & 1, dead ? 0 : limit, q)) dead = true;
             s1[0] = warp_sum(q.x);
             s2[0] = warp_sum(q.y);
