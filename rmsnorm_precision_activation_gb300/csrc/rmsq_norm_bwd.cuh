@@ -388,7 +388,6 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
         // (one row's code, not unrolled: both rows' operands at once take more registers than there are)
 #pragma unroll 1
         for (int r = 0; r < pair; ++r) {
-            const int row = rows.first + (i + r) * rows.stride;
             if (!dead && !mbar_wait<SCOPE_CTA>(ring.full(stage + r), phase, limit)) dead = true;
             w.pin();
             const float2 m = splat(r ? -mean[1] : -mean[0]), rs = splat(r ? rstd[1] : rstd[0]);

@@ -270,9 +270,8 @@ extern "C" rmsq_status layernorm_backward(const void* grad_output, const void* g
         const int64_t stages = slots();
         if (stages < 4) return RMSQ_ERR_LAUNCH;
         p.r.stages = static_cast<int>(stages > kRingStages ? kRingStages : stages) & ~1;
-        const int64_t stage = static_cast<int64_t>(p.r.slot) * p.r.ntens * p.groups;
-        int64_t ring = p.r.stages * stage;
-        if (p.groups > 1 && ring < 8LL * p.r.slice * p.groups) ring = 8LL * p.r.slice * p.groups;   // the groups' sums
+        // (4 stages of 2 tensors at least, so the groups' sums, 8 bytes an element, fit where the ring was)
+        const int64_t ring = static_cast<int64_t>(p.r.stages) * p.r.slot * p.r.ntens * p.groups;
         const void* fn = norm_bwd_fn(dtype, g.elems, g.T * g.elems == g.slice && g.slice * cluster == hidden, g.period == 1,
                                      cluster > 1);
         const unsigned threads = static_cast<unsigned>(p.T * p.groups + 32);
