@@ -6,6 +6,7 @@
 #pragma once
 
 #include "rmsq_norm.cuh"
+#include "rmsq_ops_plan.h"
 
 namespace rmsq {
 

@@ -26,6 +26,7 @@
 #pragma once
 
 #include "rmsq_norm.cuh"
+#include "rmsq_ops_plan.h"
 
 namespace rmsq {
 
@@ -352,7 +353,9 @@ __global__ void __launch_bounds__(32 * row_warps(E) + 32) rmsq_norm_bwd_kernel(c
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) acc_g[e] = acc_b[e] = make_float2(0.f, 0.f);
 
-    const uint32_t limit = p.wait;
+    // (the minimum changes nothing but keeps the limit in a register: read from the parameters where it is
+    // used, 16384 x 4096 bf16 with dres takes 94.2 us, so 92.5)
+    const uint32_t limit = min(p.wait, kWaitMost);
     const float inv_h = 1.0f / static_cast<float>(p.r.hidden);
     bool dead = false;                            // a wait ran out: finish without waiting again
     int stage = 0, phase = 0;
