@@ -120,7 +120,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
         fence_mbar_init();
         fence_proxy_async_smem();
         // the first loads run while the pair sets itself up
-        pdl_wait();
+        pdl_wait_alone();
         int tn, tm;
         tc_tile(first, tiles, tn, tm);
         for (; started < RAWS && started < steps; ++started) fetch(started, started, tn, tm);

@@ -216,7 +216,7 @@ rmsq_matmul_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_co
         fence_mbar_init();
         fence_proxy_async_smem();
         // the first loads run while the CTA sets itself up
-        pdl_wait();
+        pdl_wait_alone();
         int tn, tm;
         tc_tile(first, tiles, tn, tm);
         for (; started < RAWS && started < steps; ++started) fetch(started, started, tn, tm);

@@ -119,9 +119,14 @@ __device__ __forceinline__ float warp_max_nan(float v)
     return r;
 }
 
+// The kernels before this one on the stream are done and their writes visible.
+__device__ __forceinline__ void pdl_wait_alone() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The same, and the next kernel's CTAs may come as soon as every CTA has got here. A CTA that allocates
+// TMEM does so first: a CTA of the next kernel could take the columns and then wait for this kernel.
 __device__ __forceinline__ void pdl_wait()
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    pdl_wait_alone();
     asm volatile("griddepcontrol.launch_dependents;");
 }
 
