@@ -18,7 +18,7 @@ template <int NB, int ROWS> static cudaError_t launch_stream(MatmulParams& p, cu
 
 // 16 channels per CTA where all of the CTAs run at a time then, else 32 (GB300, 1 token, n x k: 7168 x 8192
 // 12.1 us against 13.2, 1024 x 4096 3.3 against 4.3, 300 x 16384 7.4 against 10.6; 8192 x 8192, which
-// takes more than one wave of 16, 15.9 against 14.1; 16 tokens 5000 x 8192 14.7 against 15.5).
+// takes more than one wave of 16, 15.9 against 14.0; 16 tokens 5000 x 8192 14.6 against 15.5).
 template <int NB> static cudaError_t launch_stream(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
 {
     if (p.n <= static_cast<long long>(dv.sms) * kStreamHalves * 16) return launch_stream<NB, 16>(p, stream);
@@ -66,7 +66,7 @@ static bool encode(CUtensorMap* map, const void* codes, long long rows, int k, i
 
 // CTAs that share a tile's k: as many as let all tiles run at a time, each with at least 2 code stages.
 // What fits goes by the device's clusters of SMs, not by SMs alone: 100 x 2400 x 8192 (19 tiles of 128
-// tokens) takes 16.1 us in clusters of 6, of which 23 fit, and 26.2 in clusters of 8, of which 15 do.
+// tokens) takes 15.9 us in clusters of 6, of which 23 fit, and 26.2 in clusters of 8, of which 15 do.
 template <int NT> static int tc_cluster(long long tiles, int steps, const DeviceView& dv)
 {
     const void* fn = reinterpret_cast<const void*>(&rmsq_matmul_tc_kernel<NT>);
@@ -118,12 +118,12 @@ template <int TOKENS> static cudaError_t launch_pair(MatmulParams& p, const Devi
 }
 
 // The kernel, by tokens (GB300, weights from HBM, n x k = 8192 x 8192 where not given):
-//   up to 16: mma.sync, 17.0 us at 16 tokens (tcgen05: 18.4), but 23.9 at 32 (tcgen05: 19.4)
-//   up to 32, up to 64: tiles of 32 and 64 tokens, 19.4 and 21.5 us (of 128: 27.9)
+//   up to 16: mma.sync, 16.8 us at 16 tokens (tcgen05: 20.4), but 23.9 at 32 (tcgen05: 20.7)
+//   up to 32, up to 64: tiles of 32 and 64 tokens, 20.7 and 21.8 us (of 128: 27.8)
 //   more: what takes least by the time of a step of 128 elements of k in each kernel (hundredths of a
 //   us, with a CTA or pair on every SM) and the steps its CTAs take one after another. Measured, in the
-//   order tiles of 128, pairs of 128, pairs of 192:  128 tokens 28.7, 35.1, 40.9 us;  200 44.9, 36.0, 42.2;
-//   512 83, 63, 74;  768 121, 90, 76;  4096 540, 386, 335;  1024 x 1024 x 8192 27.7, 34.8, 40.4.
+//   order tiles of 128, pairs of 128, pairs of 192:  128 tokens 29.3, 33.3, 40.9 us;  200 47.0, 34.2, 42.3;
+//   512 87, 60, 74;  768 128, 87, 76;  4096 570, 376, 337;  1024 x 1024 x 8192 28.5, 32.9, 40.2.
 static cudaError_t launch_matmul(MatmulParams& p, const DeviceView& dv, cudaStream_t stream)
 {
     if (p.m <= 8) return launch_stream<1>(p, dv, stream);

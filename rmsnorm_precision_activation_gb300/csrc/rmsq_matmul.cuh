@@ -60,9 +60,10 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t
 // registers, turn them into fp16 there and multiply with mma.sync (fp32 sums of up to 1024 products
 // are exact, then they go to integers). No shared memory or barrier stands between a load and its
 // use, so a short call costs little more than its bytes, where the tcgen05 kernels' hand-overs cost
-// about 8 us. Measured (GB300, weights from HBM): 1 to 8 tokens x 7168 x 8192 12.1 us, 4.8 TB/s (a dp4a
-// kernel: 13 us for 1 token, 28 for 8; tcgen05: 16.6); x 28672 x 8192 38.9 us, 6.0 TB/s;
-// 16 x 8192 x 8192 16.8 us (tcgen05: 18.4); 32 tokens 23.9 us (tcgen05: 19.8, so those go there).
+// about 8 us. Measured (GB300, weights from HBM, calls in a captured graph): 1 to 8 tokens x 7168 x 8192
+// 12.1 us, 4.9 TB/s (tcgen05: 20.2; a dp4a kernel took 18.7 us a call for 1 token, 28 for 8); x 28672 x 8192
+// 39.0 us, 6.0 TB/s; 16 x 8192 x 8192 16.8 us (tcgen05: 20.4); 32 tokens 23.9 us (tcgen05: 20.7, so those go
+// there).
 // A fragment's k order is free as long as both operands share it: lane (g, t) loads 16 bytes of row
 // g at 16 t, and the j-th four of them are its elements in the j-th of four MMAs.
 constexpr int kStreamWarps = 8;

@@ -9,8 +9,9 @@
 // Tiles have 192 tokens, or 128 where those fill the SMs better, rather than 256: two accumulators then
 // fit TMEM beside the operand stages, and reading one out (bound by the float-to-integer conversions, at
 // 256 tokens 2500 cycles per 8192 of MMA) overlaps the next one's products. Measured (GB300, boost clock):
-// 8192^3 in 621 us, 1770 TFLOP/s, 0.93 of the measured rate of a library product in bf16 (0.86 under
-// the power cap, 668 us); pairs of 128 tokens 755 us, of 160 679; 256 tokens with one accumulator 863.
+// 8192^3 in 622 to 634 us, 1770 to 1735 TFLOP/s, 0.93 to 0.91 of the measured burst rate of a library product
+// in bf16 (665 us, 1650, under the power cap: 0.97 of its sustained rate); pairs of 128 tokens 720 us, of 160
+// 679; 256 tokens with one accumulator 863.
 //
 // The leader (rank 0) issues the MMAs. Its op_full and acc_empty barriers count arrivals of both
 // CTAs; its commits arrive in both. Copy rings are each CTA's own. The reading warps hold TOKENS / 2
@@ -139,7 +140,7 @@ rmsq_matmul_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_
     pdl_wait();
 
     // (the minima change nothing but keep the limits in registers: read from the parameters where they are
-    // used, 512 x 8192 x 8192 takes 63.9 us, so 60.8)
+    // used, 512 x 8192 x 8192 takes 63.9 us, so 60.5)
     const uint32_t limit = min(p.wait, kWaitMost), drain_limit = min(p.drain, 2 * kWaitMost);
     bool ok = true;
 

@@ -330,11 +330,15 @@ __device__ __forceinline__ float2 cluster_exchange(float2* slots, int warp, int 
 // exactly, so nothing is checked. EDGE: rows whose width is no whole number of vectors.
 // Every row has its own thread group and no loop: the hardware's CTA scheduler overlaps rows and evens
 // out SMs of unequal bandwidth (CTAs that walk rows through rings in shared memory: 2048 x 65536 fp16 128
-// us against 108, 4096 x 20000 bf16 89 against 58, 512 x 20000 with residual 26 against 21). Bound by HBM
-// with a residual (16384 x 8192 bf16 154 us, 1.04 of the copy rate), by instructions without one (85 us,
-// 0.94); rows off 16-byte boundaries by instructions (8192 x 5121 bf16 54 us, 0.47: their parameters are
-// shifted into place and their accesses checked, twice the instructions; staging the shifted parameters in
-// shared memory for several rows took 58).
+// us against 107, 4096 x 20000 bf16 89 against 58, 512 x 20000 with residual 26 against 21). Bound by HBM
+// with a residual (16384 x 8192 bf16 155 us, 1.02 of the copy rate of 6787 GB/s), by instructions without
+// one (85.6 us, 0.92; to int8 87.6, 0.68); rows off 16-byte boundaries by instructions (8192 x 5121 bf16
+// 54.6 us, 0.45: their parameters are shifted into place and their accesses checked, twice the instructions;
+// staging the shifted parameters in shared memory for several rows took 58).
+// The launch bounds leave 64 registers, which not every form fits. What each thread stores and reloads,
+// in bytes: fp32 to 44 (fp32 rows of no whole vectors 100 to 164); to int8 fp32 16 to 96 (96 to 228, a warp
+// per row the most), packed 72 to 140, 16-bit rows of no whole vectors up to 100; other forms under 40 or
+// none. Wide rows to int8 lose most by it (2048 x 65536 158 us, 0.38).
 template <int DT, int E, bool FULL, bool EDGE, int SCOPE, int KIND>
 __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOPE_WARP ? 4 : 2) rmsq_norm_kernel(const __grid_constant__ NormParams p)
 {
@@ -413,7 +417,8 @@ __global__ void __launch_bounds__(SCOPE == SCOPE_WARP ? 256 : 512, SCOPE == SCOP
         }
     }
     // Keeps the compiler from holding packed vectors unpacked from one use to the next, which the registers
-    // do not allow: 200 bytes of spills without. (It takes a zero that the compiler does not know.)
+    // do not allow: 200 bytes of spills without it, none to 28 with it (to int8 up to 140: the comment at the
+    // kernel). It takes a zero that the compiler does not know.
     const uint32_t zero = static_cast<uint32_t>(p.hidden >> 31);
     auto pin = [&]() {
         if constexpr (PACKED) {

@@ -16,13 +16,13 @@
 // A CTA holds several row groups of T threads when rows are short; rows wider than 16 KB are split
 // over a cluster whose CTAs exchange the two row sums.
 //
-// Measured (GB300, of the copy rate): 16384 x 8192 fp16 with dres 177 us (0.91), 16384 x 4096 bf16 with
-// dres 92 (0.87), 32768 x 2048 72 (0.84), 8192 x 16384 165 (0.73), 2048 x 65536 210 (0.57), fp32
-// 4096 x 16384 125 (0.96). Wide rows are bound by the SMs that clusters of 8 leave idle (120 of 152 work)
-// and by the latency of a pair of rows in 11 warps: sums formed a pair ahead of the exchange gave 3 % at
-// 65536 and cost 4 % at 8192. Rows off 16-byte boundaries are bound by checked and unaligned accesses
-// (5003 x 2051 fp32 32, 0.57). Row groups add their column sums side by side: one after another, 4000 x 512
-// took 26 us, not 10.
+// Measured (GB300, of the copy rate of 6787 GB/s; with dres where it says so): 16384 x 8192 fp16 with dres
+// 175 us (0.90), 16384 x 4096 bf16 with dres 92.4 (0.86), 32768 x 2048 72.5 (0.82), 8192 x 16384 164 (0.72),
+// 2048 x 65536 209 (0.57), fp32 4096 x 16384 124 (0.95). Wide rows are bound by the SMs that clusters of 8
+// leave idle (120 of 152 work) and by the latency of a pair of rows in 11 warps: sums formed a pair ahead of
+// the exchange gave 3 % at 65536 and cost 4 % at 8192. Rows off 16-byte boundaries are bound by checked and
+// unaligned accesses (5003 x 2051 fp32 32, 0.57). Row groups add their column sums side by side: one after
+// another, 4000 x 512 took 26 us, not 10.
 #pragma once
 
 #include "rmsq_norm.cuh"

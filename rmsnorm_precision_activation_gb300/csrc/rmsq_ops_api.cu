@@ -31,10 +31,10 @@ static rmsq_status status_of(cudaError_t e)
 
 // Launch of a forward norm. Who takes a row, and in what shares (GB300, rows x hidden, bf16):
 //  - up to 1024 columns a warp, of 8, 16 or 32 elements a thread;
-//  - up to 16384 a CTA, of 32 elements a thread as fp32 (16 elements: 16384 x 8192 117 us, 32: 85);
+//  - up to 16384 a CTA, of 32 elements a thread as fp32 (16 elements: 16384 x 8192 117 us, 32: 86);
 //  - wider 16-bit rows a CTA of 64 elements a thread, packed: 4096 x 20000 58.5 us (clusters of fp32
-//    shares: 83), 4096 x 32768 91 us (131); and rows from 8193 on without a residual and off no 16-byte
-//    boundary: 8192 x 12000 66 us (fp32 shares: 82), but with a residual 123 (118), 8192 x 14001 136 (132),
+//    shares: 83), 4096 x 32768 89 us (131); and rows from 8193 on without a residual and off no 16-byte
+//    boundary: 8192 x 12000 65 us (fp32 shares: 82), but with a residual 123 (118), 8192 x 14001 136 (132),
 //    to int8 96 (93), which forms y twice then. (100 x 12000 takes 4.7 us packed, 3.5 not; the choice does
 //    not go by the number of rows, so that a row's bits do not depend on the others.)
 //  - rows wider than a CTA takes a cluster of 4 or 8: 2048 x 65536 106 us, in clusters of 2 some 5 % more.
@@ -166,7 +166,7 @@ extern "C" rmsq_status rmsnorm_quant_int8(const void* input, const void* residua
 // How a row is dealt out in the backward pass: split evenly, in whole vectors, over the smallest cluster of
 // 1, 2, 4, 8 or 16 CTAs whose slices take at most kRingSlice bytes (off 16-byte boundaries a vector more); a
 // slice takes T threads of `elems` elements. (Clusters of other sizes fill the SMs worse: 4096 x 20000 bf16
-// 135 us in clusters of 4, 191 of 3. Halved slices and two CTAs on an SM: 8192 x 16384 236 us against 165.)
+// 137 us in clusters of 4, 191 of 3. Halved slices and two CTAs on an SM: 8192 x 16384 236 us against 164.)
 struct RowGeometry {
     int cluster, slice, elems, T, slot;
     int period;      // rows after which the shift off 16-byte boundaries repeats
