@@ -411,6 +411,9 @@ def layernorm_backward(grad_output, input, gamma, mean, rstd, *, grad_residual=N
 
 
 def _int8_outputs(input, index, shape, rows, output, scale_output):
+    """(output, scale_output, their pointers, staged): staged is what the scales are written to, to be
+    copied to scale_output after the call, where that is a slice off 16-byte boundaries; else None."""
+    staged = None
     if output is None:
         output = torch.empty(shape, dtype=torch.int8, device=input.device)
         out = output.data_ptr()
@@ -421,12 +424,16 @@ def _int8_outputs(input, index, shape, rows, output, scale_output):
         scale = scale_output.data_ptr()
     else:
         scale = _count("scale_output", scale_output, rows, torch.float32, index)
-    return output, scale_output, out, scale
+        if scale & 15:
+            staged = torch.empty_like(scale_output)
+            scale = staged.data_ptr()
+    return output, scale_output, out, scale, staged
 
 
 def layernorm_quant_int8(input, gamma, beta=None, *, residual=None, residual_output=None,
                          epsilon=1e-5, weight_offset=0.0, output=None, scale_output=None, stream=None):
-    """Residual add + layer norm + int8 codes with one fp32 scale per row (max |y| / 127).
+    """Residual add + layer norm + int8 codes with one fp32 scale per row (max |y| / 127). scale_output may be
+    a slice off 16-byte boundaries (it is copied to then); every other tensor starts on one.
 
     Returns (output int8 [..., H], scale_output float32 [...], residual_output)."""
     if _elsewhere(input, stream):
@@ -437,16 +444,19 @@ def layernorm_quant_int8(input, gamma, beta=None, *, residual=None, residual_out
                                         scale_output=scale_output)
     index, shape, rows, H, head, residual_output = _norm_inputs(input, gamma, beta, residual,
                                                                 residual_output)
-    output, scale_output, out, scale = _int8_outputs(input, index, shape, rows, output, scale_output)
+    output, scale_output, out, scale, staged = _int8_outputs(input, index, shape, rows, output, scale_output)
     _check((_lib or lib()).layernorm_quant_int8(*head, rows, H, _DT[input.dtype], float(epsilon),
                                                 float(weight_offset), out, scale, _raw_stream(index)),
            "layernorm_quant_int8")
+    if staged is not None:
+        scale_output.copy_(staged)
     return output, scale_output, residual_output
 
 
 def rmsnorm_quant_int8(input, gamma, *, residual=None, residual_output=None, epsilon=1e-6,
                        weight_offset=0.0, output=None, scale_output=None, stream=None):
-    """Residual add + RMSNorm + int8 codes with one fp32 scale per row (max |y| / 127).
+    """Residual add + RMSNorm + int8 codes with one fp32 scale per row (max |y| / 127). scale_output may be a
+    slice off 16-byte boundaries (it is copied to then); every other tensor starts on one.
 
     Returns (output int8 [..., H], scale_output float32 [...], residual_output)."""
     if _elsewhere(input, stream):
@@ -456,10 +466,12 @@ def rmsnorm_quant_int8(input, gamma, *, residual=None, residual_output=None, eps
                                       scale_output=scale_output)
     index, shape, rows, H, head, residual_output = _norm_inputs(input, gamma, None, residual,
                                                                 residual_output)
-    output, scale_output, out, scale = _int8_outputs(input, index, shape, rows, output, scale_output)
+    output, scale_output, out, scale, staged = _int8_outputs(input, index, shape, rows, output, scale_output)
     _check((_lib or lib()).rmsnorm_quant_int8(*head[:4], rows, H, _DT[input.dtype], float(epsilon),
                                               float(weight_offset), out, scale, _raw_stream(index)),
            "rmsnorm_quant_int8")
+    if staged is not None:
+        scale_output.copy_(staged)
     return output, scale_output, residual_output
 
 

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_common import rq
-from test_layernorm import make_backward
+from test_layernorm import make as make_norm, make_backward
 from test_matmul_int8 import make
 
 gpu = pytest.mark.gpu
@@ -67,3 +67,32 @@ def test_backward_on_some_rows(hidden):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
         assert torch.equal(got[0], whole[0][some])
     assert rq().rmsq_device_status() == 0
+
+
+@gpu
+@pytest.mark.parametrize("name", ["layernorm_quant_int8", "rmsnorm_quant_int8"])
+@pytest.mark.parametrize("hidden", [64, 2048])
+def test_int8_rows_written_in_pieces(name, hidden):
+    call = getattr(rq(), name)
+    d = make_norm(50, hidden, torch.bfloat16, seed=hidden)
+    want = call(d["x"], d["gamma"])
+    q = torch.zeros(50, hidden, dtype=torch.int8, device="cuda")
+    scale = torch.full((52,), 7.0, device="cuda")
+    ends = [0, 1, 3, 4, 9, 30, 50]
+    for a, b in zip(ends, ends[1:]):
+        call(d["x"][a:b], d["gamma"], output=q[a:b], scale_output=scale[a:b])
+    assert torch.equal(q, want[0]) and torch.equal(scale[:50], want[1]) and bool((scale[50:] == 7.0).all())
+    # on a side stream, and captured and replayed on new inputs
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = call(d["x"][1:30], d["gamma"], output=q[1:30], scale_output=scale[1:30], stream=side)
+    side.synchronize()
+    assert torch.equal(got[1], want[1][1:30]) and got[1].data_ptr() == scale[1:30].data_ptr()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(d["x"][1:30], d["gamma"], output=q[1:30], scale_output=scale[1:30])
+    for f in (2.0, 0.5):
+        d["x"].mul_(f)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(scale[1:30], call(d["x"], d["gamma"])[1][1:30])
