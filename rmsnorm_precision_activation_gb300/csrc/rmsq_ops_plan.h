@@ -10,7 +10,7 @@
 
 namespace rmsq {
 
-// How many clusters of a launch a device runs at a time, as the driver was asked once: it goes by the
+// How many clusters of a launch a device runs at a time, as CUDA was asked once: it goes by the
 // kernel, the device and the whole shape of the launch. Not synchronised.
 class ResidentClusters {
 public:
