@@ -285,6 +285,150 @@ rmsq_status matmul_int8(const void* input, const float* input_scale, const void*
                         const float* weight_scale, const void* bias, int64_t m, int64_t n, int64_t k,
                         void* output, int output_dtype, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * quant_nvfp4, quant_mxfp4 -- quantisation of a tensor that comes from no norm (an attention's output, an
+ * activation in front of a projection, a weight), in the formats of rmsnorm_quant_nvfp4 / rmsnorm_quant_mxfp4.
+ *
+ *   input            [rows x hidden] of `dtype`; hidden a multiple of 16 (NVFP4) or 32 (MXFP4), at most
+ *                    RMSQ_QUANT_MAX_HIDDEN; rows at most RMSQ_QUANT_MAX_ROWS
+ *   global_scale     DEVICE pointer to one fp32 gs (4-byte aligned), finite and above 0, read by the kernel;
+ *                    NULL for 1
+ *   output           [rows x hidden / 2] bytes, two E2M1 codes per byte (element 2k low nibble)
+ *   block_scale      E4M3 / UE8M0 codes in `scale_layout`
+ * Codes are the formula's, exact ties to the even code; an element whose exact quotient is within 2e-6 of a
+ * rounding boundary, but not on it, may be either neighbour (NVFP4). A block with a NaN or an infinity gets scale
+ * NaN (E4M3 0x7F, UE8M0 255) and any codes, so a product gives NaN for its row. Zeros may have either sign.
+ * ------------------------------------------------------------------------------------------- */
+#define RMSQ_QUANT_MAX_HIDDEN 1073741824
+#define RMSQ_QUANT_MAX_ROWS 1073741824
+rmsq_status quant_nvfp4(const void* input, int64_t rows, int64_t hidden, int dtype,
+                        const float* global_scale, void* output, void* block_scale, int scale_layout,
+                        void* stream);
+rmsq_status quant_mxfp4(const void* input, int64_t rows, int64_t hidden, int dtype, void* output,
+                        void* block_scale, int scale_layout, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * nvfp4_global_scale -- gs = 448 * 6 / max |input| over `count` elements, for quant_nvfp4: the largest block scale
+ * lands on the largest E4M3 value. All zeros, or count == 0, give gs = 1; a maximum so small that gs would
+ * overflow gives the largest fp32; a NaN gives NaN.
+ *
+ *   gs_out           DEVICE pointer to one fp32 (4-byte aligned)
+ *   workspace        device memory of at least nvfp4_global_scale_workspace(count) bytes, 16-byte aligned, used
+ *                    by this call alone until it ends on the stream. Its contents before do not matter.
+ * ------------------------------------------------------------------------------------------- */
+#define RMSQ_GLOBAL_SCALE_PARTS 608
+int64_t nvfp4_global_scale_workspace(int64_t count);
+rmsq_status nvfp4_global_scale(const void* input, int64_t count, int dtype, float* gs_out, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * matmul_nvfp4, matmul_mxfp4 -- product of 4-bit codes with a scale per block of both operands.
+ *
+ *   output[i][j] = RN(sum_c a_ic w_jc / (input_gs * weight_gs) + bias[j])
+ *   a_ic = decode(input code) * decode(its block's scale), w_jc likewise; MXFP4 has no global scales
+ *
+ *   input            [m x k / 2] bytes, two E2M1 codes per byte (element 2k low nibble): the codes of
+ *                    rmsnorm_quant_nvfp4 / quant_nvfp4 (or _mxfp4), or any others
+ *   weight           [n x k / 2] bytes, a row per output channel
+ *   input_scale, weight_scale   their block scales in the layout RMSQ_SCALE_SWIZZLED_128x4; what the padding
+ *                    holds does not matter
+ *   input_gs, weight_gs   DEVICE pointers to one fp32 each (4-byte aligned), the global scales that the codes were
+ *                    formed with, read by the kernel; NULL for 1
+ *   bias             [n] of `output_dtype`, or NULL
+ *   output           [m x n] of `output_dtype` (an rmsq_dtype)
+ * k is a multiple of 32 up to RMSQ_MATMUL_FP4_MAX_K; m and n are at most RMSQ_MATMUL_MAX_ROWS, any numbers;
+ * RMSQ_ERR_SHAPE otherwise. m == 0 or n == 0 launches nothing. Sums are held in fp32 and rounded once to the
+ * output's type; how they are split goes by m, n and k, so the same call gives the same bits, and a token's row
+ * may differ in its last bits between batches of different sizes.
+ * ------------------------------------------------------------------------------------------- */
+#define RMSQ_MATMUL_FP4_MAX_K 131072
+rmsq_status matmul_nvfp4(const void* input, const void* input_scale, const float* input_gs, const void* weight,
+                         const void* weight_scale, const float* weight_gs, const void* bias, int64_t m,
+                         int64_t n, int64_t k, void* output, int output_dtype, void* stream);
+rmsq_status matmul_mxfp4(const void* input, const void* input_scale, const void* weight,
+                         const void* weight_scale, const void* bias, int64_t m, int64_t n, int64_t k,
+                         void* output, int output_dtype, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * rmsnorm_rope -- RMS norm of every head's query and key, and the rotation by the token's position.
+ *
+ *   xhat = x / sqrt(sum_i x_i^2 / dim + epsilon);  z_i = xhat_i * (gamma_i + weight_offset)     (fp32)
+ *   for i < rotated / 2, with the angle's cosine c and sine s of frequency i at the token's position:
+ *     (y_a, y_b) = RN_dtype(z_a c - z_b s, z_b c + z_a s)
+ *   (a, b) = (i, i + rotated / 2), or (2 i, 2 i + 1) with `neighbours`; elements from `rotated` on are RN_dtype(z).
+ *
+ *   query, key       rmsq_heads: elements of `dtype` at data[t * token_stride + h * head_stride + i] (strides in
+ *                    elements, from 0 to 2^31 - 1, so heads may lie inside a projection's output), heads from 1
+ *                    to 65536
+ *   query_gamma, key_gamma   [dim] of `dtype`
+ *   rotation         rmsq_rotation: cos and sin [places x rotated / 2] fp32; positions [axes x tokens], 32 or 64
+ *                    bits (position_bits); with axes > 1 (at most 4) the first sections[0] frequencies go by the
+ *                    positions of the first axis, the next sections[1] by the second's, and so on (they add
+ *                    up to rotated / 2). A position outside 0 to places - 1 reads nothing, and the elements it
+ *                    rotates come out as NaN.
+ *   query_output, key_output   rmsq_heads like query and key, their elements apart from one another; may be
+ *                    query and key themselves (same data and strides), and must not overlap them otherwise
+ * Pointers here need only be aligned to an element; rows that all start on 16-byte boundaries are read fastest.
+ * dim is even, from 2 to RMSQ_ROPE_MAX_DIM; rotated is even, from 2 to dim; tokens from 0 to
+ * RMSQ_ROPE_MAX_TOKENS. A head that is not finite gives NaN in that head alone (an infinity: NaN or 0).
+ * ------------------------------------------------------------------------------------------- */
+#define RMSQ_ROPE_MAX_DIM 512
+#define RMSQ_ROPE_MAX_TOKENS 134217727
+
+typedef struct {
+    void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+    int64_t heads;
+} rmsq_heads;
+
+typedef struct {
+    const float* cos;
+    const float* sin;
+    const void* positions;
+    int64_t places;
+    int position_bits;       /* 32 or 64 */
+    int rotated;
+    int neighbours;          /* 0: halves are rotated against each other, otherwise neighbours */
+    int axes;
+    int sections[4];         /* read where axes > 1 */
+} rmsq_rotation;
+
+rmsq_status rmsnorm_rope(const rmsq_heads* query, const rmsq_heads* key, const void* query_gamma,
+                         const void* key_gamma, const rmsq_rotation* rotation, int64_t tokens,
+                         int64_t dim, int dtype, float epsilon, float weight_offset,
+                         const rmsq_heads* query_output, const rmsq_heads* key_output, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * rmsnorm_rope_backward -- the gradients of rmsnorm_rope.
+ *
+ *   g = the rotation of grad by the opposite angle;  u = g * (gamma + weight_offset)
+ *   output = RN_dtype(rstd * (u - xhat * <u * xhat>))                         (<.>: mean over dim)
+ *   grad_gamma = sum over tokens and heads of g * xhat
+ *
+ *   grad_query, grad_key   the gradients of rmsnorm_rope's outputs, rmsq_heads like query and key
+ *   query, key             rmsnorm_rope's inputs (not what it wrote in place of them)
+ *   query_output, key_output   receive the gradients of query and key; they may be grad_query and grad_key, or
+ *                    query and key, themselves
+ *   grad_query_gamma, grad_key_gamma   [dim] of `param_grad_dtype` (`dtype` or RMSQ_F32)
+ *   workspace        device memory of at least rmsnorm_rope_backward_workspace(tokens, dim) bytes, 16-byte
+ *                    aligned, used by this call alone until it ends on the stream. Its contents before do
+ *                    not matter.
+ * Sums are held in fp32 and added in a fixed order: the same inputs give the same bits. tokens == 0 writes zeros
+ * to grad_query_gamma and grad_key_gamma. Other arguments and sizes as for rmsnorm_rope; RMSQ_ERR_SHAPE also for a
+ * workspace that is too small.
+ * ------------------------------------------------------------------------------------------- */
+#define RMSQ_ROPE_PARTS 304
+int64_t rmsnorm_rope_backward_workspace(int64_t tokens, int64_t dim);
+rmsq_status rmsnorm_rope_backward(const rmsq_heads* grad_query, const rmsq_heads* grad_key,
+                                  const rmsq_heads* query, const rmsq_heads* key,
+                                  const void* query_gamma, const void* key_gamma,
+                                  const rmsq_rotation* rotation, int64_t tokens, int64_t dim, int dtype,
+                                  float epsilon, float weight_offset, const rmsq_heads* query_output,
+                                  const rmsq_heads* key_output, void* grad_query_gamma,
+                                  void* grad_key_gamma, int param_grad_dtype, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
 /* Human-readable name of a status code (static storage; never NULL). */
 const char* rmsq_status_string(rmsq_status status);
 

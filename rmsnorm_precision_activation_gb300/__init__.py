@@ -48,6 +48,15 @@ SIGNATURES = {
     "layernorm_quant_int8": ([_P, _P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _P], _I),
     "rmsnorm_quant_int8": ([_P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _P], _I),
     "matmul_int8": ([_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _P], _I),
+    "quant_nvfp4": ([_P, _I64, _I64, _I, _P, _P, _P, _I, _P], _I),
+    "quant_mxfp4": ([_P, _I64, _I64, _I, _P, _P, _I, _P], _I),
+    "nvfp4_global_scale_workspace": ([_I64], _I64),
+    "nvfp4_global_scale": ([_P, _I64, _I, _P, _P, _I64, _P], _I),
+    "matmul_nvfp4": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _P], _I),
+    "matmul_mxfp4": ([_P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _I, _P], _I),
+    "rmsnorm_rope": ([_P, _P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _P], _I),
+    "rmsnorm_rope_backward_workspace": ([_I64, _I64], _I64),
+    "rmsnorm_rope_backward": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I, _F, _F, _P, _P, _P, _P, _I, _P, _I64, _P], _I),
     "rmsq_status_string": ([_I], ctypes.c_char_p),
     "rmsq_device_status": ([], _I),
     "rmsq_set_schedule": ([_I], _I),
@@ -72,6 +81,16 @@ GB300_SMEM = (232448, 233472, 1024)
 class PlanInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("schedule", "vectors_per_thread", "threads", "stages",
                                             "cluster", "smem_bytes", "ctas_per_sm", "w16")]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", _I64), ("head_stride", _I64), ("heads", _I64)]
+
+
+class Rotation(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("places", _I64),
+                ("position_bits", _I), ("rotated", _I), ("neighbours", _I), ("axes", _I), ("sections", _I * 4)]
+
 
 _lib = None
 
@@ -513,6 +532,313 @@ def matmul_int8(input, input_scale, weight, weight_scale, *, bias=None, out_dtyp
     _check((_lib or lib()).matmul_int8(input.data_ptr(), sa, w, sw, b, M, N, K, out, _DT[out_dtype],
                                        _raw_stream(index)), "matmul_int8")
     return output
+
+
+def _one(name, t, index):
+    """Pointer to a device scalar, None for none."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() != 1 or t.get_device() != index:
+        raise ValueError("%s must be a float32 tensor of one element on the input's device" % name)
+    return t.data_ptr()
+
+
+def nvfp4_global_scale(input, *, out=None, workspace=None, stream=None):
+    """gs = 448 * 6 / max |input|, computed on the device (quant_nvfp4's global_scale). workspace: a CUDA uint8
+    tensor of nvfp4_global_scale_workspace(input.numel()) bytes, allocated when not passed.
+
+    Returns a CUDA float32 tensor of one element."""
+    if _elsewhere(input, stream):
+        with _queue(input, stream):
+            return nvfp4_global_scale(input, out=out, workspace=workspace)
+    if input.dtype not in _DT:
+        raise TypeError("input dtype must be bfloat16, float16 or float32")
+    if not input.is_contiguous():
+        raise ValueError("input must be a contiguous tensor")
+    index, count = input.get_device(), input.numel()
+    if out is None:
+        out = torch.empty((1,), dtype=torch.float32, device=input.device)
+    o = _one("out", out, index)
+    if workspace is None:
+        size = nvfp4_global_scale_workspace(count)
+        workspace = torch.empty((size,), dtype=torch.uint8, device=input.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the input's device")
+    else:
+        size = workspace.numel() * workspace.element_size()
+    _check((_lib or lib()).nvfp4_global_scale(input.data_ptr(), count, _DT[input.dtype], o, workspace.data_ptr(), size,
+                                              _raw_stream(index)), "nvfp4_global_scale")
+    return out
+
+
+def nvfp4_global_scale_workspace(count: int) -> int:
+    """Bytes of workspace nvfp4_global_scale needs."""
+    return lib().nvfp4_global_scale_workspace(int(count))
+
+
+def _bytes(name, t, n, index):
+    if t.element_size() != 1 or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError("%s must be a contiguous tensor of %d bytes on the input's device" % (name, n))
+    return t.data_ptr()
+
+
+def _quant_fp4(input, block, scale_dtype, output, block_scale, swizzled):
+    """Checks a 4-bit quantisation's tensors; (device index, rows, H, output, block_scale, their pointers)."""
+    if input.dtype not in _DT:
+        raise TypeError("input dtype must be bfloat16, float16 or float32")
+    shape, index = input.shape, input.get_device()
+    if not shape or not input.is_contiguous():
+        raise ValueError("input must be a contiguous tensor of at least one dimension")
+    H = shape[-1]
+    if H == 0 or H % block:
+        raise ValueError("the last dimension must be a multiple of %d" % block)
+    rows = input.numel() // H
+    if output is None:
+        output = torch.empty(shape[:-1] + (H // 2,), dtype=torch.uint8, device=input.device)
+        out = output.data_ptr()
+    else:
+        out = _same("output", output, shape[:-1] + (H // 2,), torch.uint8, index)
+    if block_scale is None:
+        sshape = (swizzled_scale_numel(rows, H, block),) if swizzled else shape[:-1] + (H // block,)
+        block_scale = torch.empty(sshape, dtype=scale_dtype, device=input.device)
+        scale = block_scale.data_ptr()
+    else:
+        scale = _bytes("block_scale", block_scale, swizzled_scale_numel(rows, H, block) if swizzled else rows * (H // block),
+                       index)
+    return index, rows, H, output, block_scale, out, scale
+
+
+def quant_nvfp4(input, *, global_scale=None, output=None, block_scale=None, swizzled=False, stream=None):
+    """NVFP4 (packed E2M1, E4M3 scale per 16 elements) of a tensor that comes from no norm. global_scale: a CUDA
+    float32 tensor of one element, read on the device (nvfp4_global_scale's; default 1.0).
+
+    Returns (output uint8 [..., H/2], block_scale float8_e4m3fn)."""
+    if _elsewhere(input, stream):
+        with _queue(input, stream):
+            return quant_nvfp4(input, global_scale=global_scale, output=output, block_scale=block_scale, swizzled=swizzled)
+    index, rows, H, output, block_scale, out, scale = _quant_fp4(input, 16, torch.float8_e4m3fn, output, block_scale, swizzled)
+    gs = _one("global_scale", global_scale, index)
+    _check((_lib or lib()).quant_nvfp4(input.data_ptr(), rows, H, _DT[input.dtype], gs, out, scale,
+                                       SCALE_SWIZZLED_128x4 if swizzled else SCALE_ROW_MAJOR, _raw_stream(index)),
+           "quant_nvfp4")
+    return output, block_scale
+
+
+def quant_mxfp4(input, *, output=None, block_scale=None, swizzled=False, stream=None):
+    """MXFP4 (packed E2M1, UE8M0 scale per 32 elements) of a tensor that comes from no norm.
+
+    Returns (output uint8 [..., H/2], block_scale uint8 (UE8M0 codes))."""
+    if _elsewhere(input, stream):
+        with _queue(input, stream):
+            return quant_mxfp4(input, output=output, block_scale=block_scale, swizzled=swizzled)
+    index, rows, H, output, block_scale, out, scale = _quant_fp4(input, 32, torch.uint8, output, block_scale, swizzled)
+    _check((_lib or lib()).quant_mxfp4(input.data_ptr(), rows, H, _DT[input.dtype], out, scale,
+                                       SCALE_SWIZZLED_128x4 if swizzled else SCALE_ROW_MAJOR, _raw_stream(index)),
+           "quant_mxfp4")
+    return output, block_scale
+
+
+def _matmul_fp4(input, input_scale, weight, weight_scale, block, bias, out_dtype, output):
+    """Checks a 4-bit product's tensors; (device index, M, N, K, pointers of the four operands, the bias that is read,
+    its pointer, output, its pointer)."""
+    if input.dtype is not torch.uint8 or weight.dtype is not torch.uint8:
+        raise TypeError("input and weight must be uint8 (two codes per byte)")
+    if out_dtype not in _DT:
+        raise TypeError("out_dtype must be bfloat16, float16 or float32")
+    index, shape = input.get_device(), input.shape
+    if not shape or not input.is_contiguous():
+        raise ValueError("input must be a contiguous tensor of at least one dimension")
+    half = shape[-1]
+    M = input.numel() // half if half else 0
+    if weight.dim() != 2:
+        raise ValueError("weight must have shape (N, %d)" % half)
+    N = weight.shape[0]
+    w = _same("weight", weight, (N, half), torch.uint8, index)
+    K = 2 * half
+    sa = _bytes("input_scale", input_scale, swizzled_scale_numel(M, K, block), index)
+    sw = _bytes("weight_scale", weight_scale, swizzled_scale_numel(N, K, block), index)
+    bias, b = (None, None) if bias is None else _vector("bias", bias, N, out_dtype, index)
+    oshape = shape[:-1] + (N,)
+    if output is None:
+        output = torch.empty(oshape, dtype=out_dtype, device=input.device)
+        out = output.data_ptr()
+    else:
+        out = _same("output", output, oshape, out_dtype, index)
+    return index, M, N, K, (input.data_ptr(), sa, w, sw), bias, b, output, out
+
+
+def matmul_nvfp4(input, input_scale, weight, weight_scale, *, input_global_scale=None, weight_global_scale=None, bias=None,
+                 out_dtype=torch.bfloat16, output=None, stream=None):
+    """input @ weight.T / (input_global_scale * weight_global_scale) + bias on NVFP4 codes.
+
+    input uint8 [..., K/2] and weight uint8 [N, K/2] as rmsnorm_quant_nvfp4 and quant_nvfp4 give them with
+    swizzled=True, with their block scales; the global scales they were formed with (CUDA float32 tensors of one
+    element, read on the device; default 1.0); bias [N] of out_dtype. K must be a multiple of 32. Tensors start on
+    16-byte boundaries; bias may be a slice that does not (it is copied then).
+
+    Returns output [..., N] of out_dtype."""
+    if _elsewhere(input, stream):
+        with _queue(input, stream):
+            return matmul_nvfp4(input, input_scale, weight, weight_scale, input_global_scale=input_global_scale,
+                                weight_global_scale=weight_global_scale, bias=bias, out_dtype=out_dtype, output=output)
+    index, M, N, K, (a, sa, w, sw), bias, b, output, out = _matmul_fp4(input, input_scale, weight, weight_scale, 16, bias,
+                                                                       out_dtype, output)
+    ga = _one("input_global_scale", input_global_scale, index)
+    gw = _one("weight_global_scale", weight_global_scale, index)
+    _check((_lib or lib()).matmul_nvfp4(a, sa, ga, w, sw, gw, b, M, N, K, out, _DT[out_dtype], _raw_stream(index)),
+           "matmul_nvfp4")
+    return output
+
+
+def matmul_mxfp4(input, input_scale, weight, weight_scale, *, bias=None, out_dtype=torch.bfloat16, output=None, stream=None):
+    """input @ weight.T + bias on MXFP4 codes.
+
+    input uint8 [..., K/2] and weight uint8 [N, K/2] as rmsnorm_quant_mxfp4 and quant_mxfp4 give them with
+    swizzled=True, with their block scales; bias [N] of out_dtype. K must be a multiple of 32. Tensors start on 16-byte
+    boundaries; bias may be a slice that does not (it is copied then).
+
+    Returns output [..., N] of out_dtype."""
+    if _elsewhere(input, stream):
+        with _queue(input, stream):
+            return matmul_mxfp4(input, input_scale, weight, weight_scale, bias=bias, out_dtype=out_dtype, output=output)
+    index, M, N, K, (a, sa, w, sw), bias, b, output, out = _matmul_fp4(input, input_scale, weight, weight_scale, 32, bias,
+                                                                       out_dtype, output)
+    _check((_lib or lib()).matmul_mxfp4(a, sa, w, sw, b, M, N, K, out, _DT[out_dtype], _raw_stream(index)), "matmul_mxfp4")
+    return output
+
+
+def _heads(name, t, shape, dtype, index):
+    """The C view of [..., heads, D], whose leading dimensions count as tokens."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or t.stride(-1) != 1:
+        raise ValueError("%s must be a %s tensor of shape %s on the input's device, its last dimension contiguous"
+                         % (name, dtype, tuple(shape)))
+    if t.dim() != 3:
+        try:
+            t = t.view((-1 if t.numel() else 0,) + tuple(shape[-2:]))
+        except RuntimeError:
+            raise ValueError("%s: its leading dimensions must lie behind each other" % name) from None
+    tokens, heads, _ = t.shape
+    ts, hs, _ = t.stride()
+    return Heads(t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0, heads)
+
+
+def _rope(query, key, query_gamma, key_gamma, cos, sin, positions, sections, interleaved):
+    """Checks the inputs of rmsnorm_rope; (device index, dtype, tokens, D, query, key, gammas, rotation)."""
+    dtype, index = query.dtype, query.get_device()
+    if dtype not in _DT:
+        raise TypeError("query dtype must be bfloat16, float16 or float32")
+    if query.dim() < 3 or key.dim() != query.dim() or key.shape[:-2] != query.shape[:-2] or key.shape[-1] != query.shape[-1]:
+        raise ValueError("query and key must have shapes [..., heads, D] with the same tokens and D")
+    lead, D = query.shape[:-2], query.shape[-1]
+    tokens = lead.numel()
+    q = _heads("query", query, query.shape, dtype, index)
+    k = _heads("key", key, key.shape, dtype, index)
+    gq = _count("query_gamma", query_gamma, D, dtype, index)
+    gk = _count("key_gamma", key_gamma, D, dtype, index)
+    if cos.dim() != 2:
+        raise ValueError("cos must have shape (positions, rotated / 2)")
+    c = _same("cos", cos, cos.shape, torch.float32, index)
+    s = _same("sin", sin, cos.shape, torch.float32, index)
+    axes = 1 if sections is None else len(sections)
+    if not 1 <= axes <= 4:
+        raise ValueError("sections must have 1 to 4 entries")
+    if sections is not None and sum(sections) != cos.shape[1]:
+        raise ValueError("sections must add up to rotated / 2")
+    want = lead if sections is None else (axes,) + lead
+    if positions.dtype is torch.int64:
+        bits = 64
+    elif positions.dtype is torch.int32:
+        bits = 32
+    else:
+        raise TypeError("positions must be int32 or int64")
+    at = _same("positions", positions, want, positions.dtype, index)
+    r = Rotation(c, s, at, cos.shape[0], bits, 2 * cos.shape[1], int(bool(interleaved)), axes)
+    if axes > 1:
+        r.sections[:axes] = sections
+    return index, dtype, tokens, D, q, k, gq, gk, r
+
+
+def _like(name, t, of, dtype, index):
+    """(tensor, its C view) of an output like `of`; a contiguous one where none is given."""
+    if t is None:
+        t = torch.empty(of.shape, dtype=dtype, device=of.device)
+    return t, _heads(name, t, of.shape, dtype, index)
+
+
+def rmsnorm_rope(query, key, query_gamma, key_gamma, cos, sin, positions, *, sections=None, interleaved=False, epsilon=1e-6,
+                 weight_offset=0.0, query_output=None, key_output=None, stream=None):
+    """RMS norm of every head's query and key, then the rotation by the token's position.
+
+    query [..., heads, D] and key [..., kv_heads, D], the last dimension contiguous, otherwise with any strides (slices
+    of a projection's output); gammas [D]; cos and sin float32 [places, R / 2], R <= D elements of a head being rotated;
+    positions int32 or int64 [...], or [axes, ...] with sections, which says how many of the R / 2 frequencies go by
+    each axis. interleaved: neighbours are rotated together, instead of the halves of the R elements. A position outside
+    the table gives NaN. query_output and key_output may be query and key themselves.
+
+    Returns (query_output [..., heads, D], key_output [..., kv_heads, D])."""
+    if _elsewhere(query, stream):
+        with _queue(query, stream):
+            return rmsnorm_rope(query, key, query_gamma, key_gamma, cos, sin, positions, sections=sections,
+                                interleaved=interleaved, epsilon=epsilon, weight_offset=weight_offset,
+                                query_output=query_output, key_output=key_output)
+    index, dtype, tokens, D, q, k, gq, gk, r = _rope(query, key, query_gamma, key_gamma, cos, sin, positions, sections,
+                                                     interleaved)
+    query_output, qo = _like("query_output", query_output, query, dtype, index)
+    key_output, ko = _like("key_output", key_output, key, dtype, index)
+    ref = ctypes.byref
+    _check((_lib or lib()).rmsnorm_rope(ref(q), ref(k), gq, gk, ref(r), tokens, D, _DT[dtype], float(epsilon),
+                                        float(weight_offset), ref(qo), ref(ko), _raw_stream(index)), "rmsnorm_rope")
+    return query_output, key_output
+
+
+def rmsnorm_rope_backward_workspace(tokens: int, dim: int) -> int:
+    """Bytes of workspace rmsnorm_rope_backward needs."""
+    return lib().rmsnorm_rope_backward_workspace(int(tokens), int(dim))
+
+
+def rmsnorm_rope_backward(grad_query, grad_key, query, key, query_gamma, key_gamma, cos, sin, positions, *, sections=None,
+                          interleaved=False, epsilon=1e-6, weight_offset=0.0, query_grad=None, key_grad=None,
+                          query_gamma_grad=None, key_gamma_grad=None, param_grad_dtype=None, workspace=None, stream=None):
+    """The gradients of rmsnorm_rope. grad_query, grad_key: the gradients of its outputs; query, key and the rest: its
+    inputs. param_grad_dtype: type of the gammas' gradients, the input's (default) or torch.float32. query_grad and
+    key_grad may be grad_query and grad_key themselves. workspace: a CUDA uint8 tensor of
+    rmsnorm_rope_backward_workspace(tokens, D) bytes, allocated when not passed.
+
+    Returns (query_grad [..., heads, D], key_grad [..., kv_heads, D], query_gamma_grad [D], key_gamma_grad [D])."""
+    if _elsewhere(query, stream):
+        with _queue(query, stream):
+            return rmsnorm_rope_backward(grad_query, grad_key, query, key, query_gamma, key_gamma, cos, sin, positions,
+                                         sections=sections, interleaved=interleaved, epsilon=epsilon,
+                                         weight_offset=weight_offset, query_grad=query_grad, key_grad=key_grad,
+                                         query_gamma_grad=query_gamma_grad, key_gamma_grad=key_gamma_grad,
+                                         param_grad_dtype=param_grad_dtype, workspace=workspace)
+    index, dtype, tokens, D, q, k, gq, gk, r = _rope(query, key, query_gamma, key_gamma, cos, sin, positions, sections,
+                                                     interleaved)
+    dq = _heads("grad_query", grad_query, query.shape, dtype, index)
+    dk = _heads("grad_key", grad_key, key.shape, dtype, index)
+    pdt = dtype if param_grad_dtype is None else param_grad_dtype
+    if pdt is not dtype and pdt is not torch.float32:
+        raise TypeError("param_grad_dtype must be the input's dtype or float32")
+    query_grad, qo = _like("query_grad", query_grad, query, dtype, index)
+    key_grad, ko = _like("key_grad", key_grad, key, dtype, index)
+    if query_gamma_grad is None:
+        query_gamma_grad = torch.empty((D,), dtype=pdt, device=query.device)
+    if key_gamma_grad is None:
+        key_gamma_grad = torch.empty((D,), dtype=pdt, device=query.device)
+    pq = _count("query_gamma_grad", query_gamma_grad, D, pdt, index)
+    pk = _count("key_gamma_grad", key_gamma_grad, D, pdt, index)
+    if workspace is None:
+        size = rmsnorm_rope_backward_workspace(tokens, D)
+        workspace = torch.empty((size,), dtype=torch.uint8, device=query.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the input's device")
+    else:
+        size = workspace.numel() * workspace.element_size()
+    ref = ctypes.byref
+    _check((_lib or lib()).rmsnorm_rope_backward(ref(dq), ref(dk), ref(q), ref(k), gq, gk, ref(r), tokens, D, _DT[dtype],
+                                                 float(epsilon), float(weight_offset), ref(qo), ref(ko), pq, pk, _DT[pdt],
+                                                 workspace.data_ptr(), size, _raw_stream(index)), "rmsnorm_rope_backward")
+    return query_grad, key_grad, query_gamma_grad, key_gamma_grad
 
 
 def rmsq_device_status() -> int:

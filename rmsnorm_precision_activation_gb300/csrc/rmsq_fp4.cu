@@ -1,0 +1,108 @@
+// rmsq_fp4.cu -- C ABI of the 4-bit products: argument checks and the choice of kernel.
+#include <cstdint>
+
+#include "rmsq_fp4.cuh"
+#include "rmsq_ops.h"
+#include "rmsq_tensor_map.h"
+
+namespace rmsq {
+
+static bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
+
+struct Fp4Operands {
+    const void *a, *sa, *w, *sw;
+};
+
+// Codes [rows x k] in boxes of box_rows x 256 elements, and their scales in boxes of a stage's tiles of box_tiles x 128 rows.
+template <bool NV>
+static bool encode(CUtensorMap* codes_map, CUtensorMap* scales_map, const void* codes, const void* scales, long long rows, int k,
+                   int box_rows, int box_tiles)
+{
+    const long long k_tiles = (k / (NV ? 16 : 32) + 3) / 4;
+    return encode_map(codes_map, codes, 1, rows, k / 2, box_rows, kFp4Step / 2, CU_TENSOR_MAP_SWIZZLE_128B) &&
+           encode_map(scales_map, scales, 8, (rows + 127) / 128, k_tiles * (kFp4ScaleTile / 8), box_tiles,
+                      fp4_tiles<NV>() * kFp4ScaleTile / 8, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <bool NV, int NT> static cudaError_t launch_tile(Fp4Params& p, const Fp4Operands& o, const DeviceView& dv, cudaStream_t stream)
+{
+    using S = Fp4Shape<NV, NT>;
+    const void* fn = reinterpret_cast<const void*>(&rmsq_fp4_tile_kernel<NV, NT>);
+    CUtensorMap map_w, map_a, map_sw, map_sa;
+    if (!encode<NV>(&map_w, &map_sw, o.w, o.sw, p.n, p.k, kFp4Rows, 1) ||
+        !encode<NV>(&map_a, &map_sa, o.a, o.sa, p.m, p.k, NT, S::ROW_TILES))
+        return cudaErrorUnknown;
+    TcTiles t;
+    t.n_tiles = static_cast<int>((p.n + kFp4Rows - 1) / kFp4Rows);
+    t.m_tiles = static_cast<int>((p.m + NT - 1) / NT);
+    const long long tiles = static_cast<long long>(t.n_tiles) * t.m_tiles;
+    const int steps = (p.k + kFp4Step - 1) / kFp4Step;
+    // CTAs that share a tile's k: as many as let all tiles run at a time
+    int cluster = 1;
+    for (int c = 2; c <= 8 && c <= steps && c * tiles <= dv.sms * S::CTAS; ++c)
+        if (tiles <= resident_clusters(fn, kFp4Threads, S::SMEM, c)) cluster = c;
+    if (tiles * cluster > INT32_MAX) return cudaErrorInvalidConfiguration;
+    void* args[] = {&map_w, &map_a, &map_sw, &map_sa, &p, &t};
+    return launch_kernel(fn, dim3(static_cast<unsigned>(tiles * cluster)), kFp4Threads, S::SMEM, cluster, stream, args);
+}
+
+template <bool NV> static cudaError_t launch_fp4(Fp4Params& p, const Fp4Operands& o, const DeviceView& dv, cudaStream_t stream)
+{
+    if (p.m <= 16) return launch_tile<NV, 16>(p, o, dv, stream);
+    if (p.m <= 32) return launch_tile<NV, 32>(p, o, dv, stream);
+    if (p.m <= 64) return launch_tile<NV, 64>(p, o, dv, stream);
+    return launch_tile<NV, 128>(p, o, dv, stream);
+}
+
+template <bool NV>
+static rmsq_status matmul_fp4(const Fp4Operands& o, const float* a_gs, const float* w_gs, const void* bias, int64_t m, int64_t n,
+                              int64_t k, void* output, int output_dtype, void* stream)
+{
+    if (output_dtype != RMSQ_BF16 && output_dtype != RMSQ_FP16 && output_dtype != RMSQ_F32) return RMSQ_ERR_DTYPE;
+    if (m < 0 || n < 0 || m > RMSQ_MATMUL_MAX_ROWS || n > RMSQ_MATMUL_MAX_ROWS || k < 32 || k % 32 != 0 ||
+        k > RMSQ_MATMUL_FP4_MAX_K)
+        return RMSQ_ERR_SHAPE;
+    if (m == 0 || n == 0) return RMSQ_OK;
+    if (!o.a || !o.sa || !o.w || !o.sw || !output) return RMSQ_ERR_NULL;
+    if (!aligned(o.a, 16) || !aligned(o.sa, 16) || !aligned(o.w, 16) || !aligned(o.sw, 16) || !aligned(a_gs, 4) ||
+        !aligned(w_gs, 4) || !aligned(bias, 16) || !aligned(output, 16))
+        return RMSQ_ERR_ALIGN;
+    DeviceView dv;
+    if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
+    Fp4Params p = {};
+    p.a_gs = a_gs;
+    p.w_gs = w_gs;
+    p.bias = bias;
+    p.out = output;
+    p.err = dv.err;
+    p.m = m;
+    p.n = n;
+    p.k = static_cast<int>(k);
+    p.dt = output_dtype;
+    p.wait = dv.wait;
+    p.drain = dv.drain;
+    const cudaError_t e = launch_fp4<NV>(p, o, dv, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) return RMSQ_OK;
+    cudaGetLastError();
+    return RMSQ_ERR_LAUNCH;
+}
+
+}  // namespace rmsq
+
+using namespace rmsq;
+
+extern "C" rmsq_status matmul_nvfp4(const void* input, const void* input_scale, const float* input_gs, const void* weight,
+                                    const void* weight_scale, const float* weight_gs, const void* bias, int64_t m, int64_t n,
+                                    int64_t k, void* output, int output_dtype, void* stream)
+{
+    return matmul_fp4<true>({input, input_scale, weight, weight_scale}, input_gs, weight_gs, bias, m, n, k, output,
+                            output_dtype, stream);
+}
+
+extern "C" rmsq_status matmul_mxfp4(const void* input, const void* input_scale, const void* weight, const void* weight_scale,
+                                    const void* bias, int64_t m, int64_t n, int64_t k, void* output, int output_dtype,
+                                    void* stream)
+{
+    return matmul_fp4<false>({input, input_scale, weight, weight_scale}, nullptr, nullptr, bias, m, n, k, output,
+                             output_dtype, stream);
+}

@@ -1,0 +1,339 @@
+// rmsq_fp4.cuh -- product of 4-bit codes with block scales on the tensor cores, a CTA per tile.
+//
+//   out[m][n] = RN(sum_k (a[m][k] sa[m][k / B]) (w[n][k] sw[n][k / B]) / (gs_a gs_w) + bias[n])
+//   NVFP4: B = 16, scales E4M3;  MXFP4: B = 32, scales UE8M0
+//
+// tcgen05.mma's block-scaled kinds take the codes as they are, K-major in shared memory, and the scales from TMEM. The
+// swizzled 128x4 scale layout is made for that: a tile of 128 rows x 4 scales is 512 bytes, [row % 32][row / 32][4],
+// which tcgen05.cp (32x128b.warpx4) puts into 4 TMEM columns, each the scales of 32 rows. So nothing stands between
+// memory and the tensor cores but TMA and that copy.
+//
+// A CTA takes 128 output channels (the MMA's rows) and NT tokens (its columns); with few tokens, CTAs of a cluster
+// share a tile's k and add their sums through distributed shared memory in rank order.
+//   warps 0-3   read the accumulator and write the output (a lane is a channel: 32 neighbours of a token's row)
+//   warp 4      TMA loads codes and scales of both tiles into a ring, 256 elements of k per stage
+//   warp 5      one thread issues the copies of the scales and the MMAs, four of 64 elements per stage
+//
+// k is a multiple of 32, so the last MMA's 64 elements may end half way: TMA fills the codes behind the end with zeros,
+// but the scales there are the padding's, which may be a NaN; they are cleared in shared memory before the copy.
+//
+// Every wait is bounded: a role whose wait runs out leaves its loop, and so then do the others. At their end the MMA and
+// copy roles always wait (bounded again) for what they have in flight; then the CTA frees its TMEM and ends.
+#pragma once
+
+#include "rmsq_matmul_tc.cuh"
+
+namespace rmsq {
+
+struct Fp4Params {
+    const float* a_gs;         // or null (1)
+    const float* w_gs;
+    const void* bias;          // [n] of the output's type, or null
+    void* out;                 // [m x n]
+    unsigned int* err;
+    long long m, n;
+    int k;
+    int dt;                    // output's type
+    uint32_t wait, drain;      // bounds of waits, and of what a stopping CTA has in flight (rmsq_ops_plan.h)
+};
+
+constexpr int kFp4Step = 256;                    // elements of k per stage: 128 bytes of codes a row
+constexpr int kFp4Rows = 128;                    // output channels per CTA
+constexpr int kFp4ScaleTile = 512;               // bytes of 128 rows x 4 scales
+
+// Tiles of scales per 128 rows and stage.
+template <bool NV> __host__ __device__ constexpr int fp4_tiles() { return NV ? 4 : 2; }
+
+template <bool NV, int NT> struct Fp4Shape {
+    static constexpr int ROW_TILES = (NT + 127) / 128;
+    static constexpr int CODES_W = kFp4Rows * kFp4Step / 2, CODES_A = NT * kFp4Step / 2;
+    static constexpr int SCALES_W = fp4_tiles<NV>() * kFp4ScaleTile, SCALES_A = ROW_TILES * SCALES_W;
+    static constexpr int AT_A = CODES_W, AT_SW = AT_A + CODES_A, AT_SA = AT_SW + SCALES_W;
+    static constexpr int STAGE = AT_SA + SCALES_A;
+    static constexpr int CTAS = NT <= 32 ? 2 : 1;                     // on an SM
+    static constexpr int MOST = (CTAS == 2 ? 113 : 226) * 1024;
+    static constexpr int STAGES = (MOST - 2048) / STAGE;
+    static constexpr int SMEM = 2048 + STAGES * STAGE;                // 1024 to align the ring, 1024 for barriers
+    // TMEM: the accumulator, then two buffers of scales (the channels', the tokens')
+    static constexpr int ACC = NT < 32 ? 32 : NT;
+    static constexpr int COLS_S = 4 * fp4_tiles<NV>() * (1 + ROW_TILES);
+    static constexpr int NEED = ACC + 2 * COLS_S;
+    static constexpr int COLS = NEED <= 128 ? 128 : NEED <= 256 ? 256 : 512;
+    static_assert(STAGE % 1024 == 0 && AT_A % 1024 == 0 && AT_SW % 1024 == 0, "swizzle atoms");
+    static_assert(SMEM <= 232448 && COLS * CTAS <= 512, "fits the SM");
+    static_assert(SMEM * (CTAS + 1) > 233472 - 1024 * CTAS, "no more CTAs on an SM than TMEM has columns for");
+    static_assert(STAGES * STAGE >= NT * kFp4Rows * 4, "the cluster's sums reuse the ring");
+};
+
+constexpr int kFp4Threads = 192;
+
+// Scales from shared memory to 4 TMEM columns (all four lane quarters).
+template <bool PAIR> __device__ __forceinline__ void fp4_copy_scales(uint32_t tmem, uint32_t smem)
+{
+    const uint64_t desc = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// d (+)= a b^T over 64 elements of k, with scales at sa and sb in TMEM.
+template <bool NV, bool PAIR>
+__device__ __forceinline__ void fp4_mma(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t sa, uint32_t sb, uint32_t add)
+{
+    constexpr uint32_t hi = 64u | (1u << 14) | (2u << 29);            // as in tc_mma_step
+#define RMSQ_FP4_MMA(GROUP, KIND)                                                                              \
+    asm volatile(                                                                                              \
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %7, 0;\n\tmov.b64 a, {%1, %3};\n\t"            \
+        "mov.b64 b, {%2, %3};\n\ttcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], a, b, %4, [%5], [%6], p;\n\t}" \
+        ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(sa), "r"(sb), "r"(add) : "memory")
+    if constexpr (NV && PAIR) RMSQ_FP4_MMA("2", "mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (NV) RMSQ_FP4_MMA("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (PAIR) RMSQ_FP4_MMA("2", "mxf4.block_scale.scale_vec::2X");
+    else RMSQ_FP4_MMA("1", "mxf4.block_scale.scale_vec::2X");
+#undef RMSQ_FP4_MMA
+}
+
+// Instruction descriptor: both operands E2M1, K-major; E4M3 or UE8M0 scales.
+template <bool NV> __host__ __device__ constexpr uint32_t fp4_idesc(int rows, int cols)
+{
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(cols / 8) << 17) | (NV ? 0u : 1u << 23) |
+           (static_cast<uint32_t>(rows / 16) << 24);
+}
+
+// A stage: the copies of its scales and up to four MMAs (`quarters` of 64 elements have codes). stage: its address;
+// scales: TMEM columns of this stage's scales, the channels' first. The codes' descriptors advance by 32 bytes an MMA.
+template <bool NV, int ROW_TILES, int AT_A, int AT_SW, int AT_SA, bool PAIR>
+__device__ __forceinline__ void fp4_stage(uint32_t d, uint32_t stage, uint32_t scales, uint32_t idesc, int quarters, bool fresh)
+{
+    constexpr int T = fp4_tiles<NV>(), PER = 4 / T;                   // MMAs per tile of scales
+    const uint32_t sa = scales + 4 * T;                               // the tokens': per MMA the row tiles' columns
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+        fp4_copy_scales<PAIR>(scales + 4 * i, stage + AT_SW + i * kFp4ScaleTile);
+#pragma unroll
+        for (int r = 0; r < ROW_TILES; ++r)
+            fp4_copy_scales<PAIR>(sa + 4 * (i * ROW_TILES + r), stage + AT_SA + (r * T + i) * kFp4ScaleTile);
+    }
+    const uint32_t a_lo = tc_desc_lo(stage), b_lo = tc_desc_lo(stage + AT_A);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j >= quarters) break;
+        const uint32_t id = j % PER * 2;                              // MXFP4: which two of a tile's four scales
+        fp4_mma<NV, PAIR>(d, a_lo + 2 * j, b_lo + 2 * j, idesc | (id << 29) | (id << 4), scales + 4 * (j / PER),
+                          sa + 4 * ROW_TILES * (j / PER), j > 0 || !fresh);
+    }
+}
+
+// Clears the scales behind the end of k in the last stage (one warp, after the stage's copies have landed).
+template <bool NV, int ROW_TILES, int AT_SW, int AT_SA>
+__device__ __forceinline__ void fp4_clear_tail(uint32_t stage, int k, int lane)
+{
+    constexpr int T = fp4_tiles<NV>(), B = NV ? 16 : 32;
+    const int held = (k % kFp4Step + B - 1) / B, tile = held / 4;     // scales of the stage; the tile that ends early
+    const uint32_t keep = (1u << (8 * (held % 4))) - 1u;              // held % 4 > 0: k % 64 is 32
+#pragma unroll
+    for (int r = 0; r < 1 + ROW_TILES; ++r) {
+        const uint32_t at = stage + (r == 0 ? AT_SW : AT_SA + (r - 1) * T * kFp4ScaleTile) + tile * kFp4ScaleTile + lane * 16;
+        uint4 v = ld_shared_v4(at);
+        v.x &= keep;
+        v.y &= keep;
+        v.z &= keep;
+        v.w &= keep;
+        st_shared_v4(at, v);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+__device__ __forceinline__ float fp4_factor(const float* gs) { return gs != nullptr ? __fdiv_rn(1.0f, *gs) : 1.0f; }
+
+// A sum to the output's fp32 value.
+__device__ __forceinline__ float fp4_value(float sum, float fa, float fw, float bias)
+{
+    return fmaf(__fmul_rn(sum, fa), fw, bias);
+}
+
+template <bool NV, int NT>
+__global__ void __launch_bounds__(kFp4Threads, Fp4Shape<NV, NT>::CTAS)
+rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
+                     const __grid_constant__ CUtensorMap map_sw, const __grid_constant__ CUtensorMap map_sa, const Fp4Params p,
+                     const TcTiles tiles)
+{
+    using S = Fp4Shape<NV, NT>;
+    constexpr int STAGES = S::STAGES;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint32_t tmem_slot;
+
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t bars = ring + STAGES * S::STAGE;
+    const uint32_t full = bars, empty = full + 8 * STAGES, acc_full = empty + 8 * STAGES, drain = acc_full + 8;
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t nc = cluster_size(), rank = cluster_rank();
+    int tn, tm;
+    tc_tile(cluster_id(), tiles, tn, tm);
+
+    // this CTA's stages of k
+    const int steps_all = (p.k + kFp4Step - 1) / kFp4Step;
+    const int s0 = static_cast<int>(static_cast<long long>(steps_all) * rank / nc);
+    const int steps = static_cast<int>(static_cast<long long>(steps_all) * (rank + 1) / nc) - s0;
+
+    auto fetch = [&](uint32_t slot, int s) {
+        const uint32_t bar = full + 8 * slot, dst = ring + slot * S::STAGE;
+        mbar_arrive_expect_tx(bar, S::STAGE);
+        tma_load_2d(dst, &map_w, (s0 + s) * (kFp4Step / 2), tn * kFp4Rows, bar);
+        tma_load_2d(dst + S::AT_SW, &map_sw, (s0 + s) * (S::SCALES_W / 8), tn, bar);
+        tma_load_2d(dst + S::AT_A, &map_a, (s0 + s) * (kFp4Step / 2), tm * NT, bar);
+        tma_load_2d(dst + S::AT_SA, &map_sa, (s0 + s) * (S::SCALES_W / 8), tm * NT / 128, bar);
+    };
+    int started = 0;                          // stages fetched ahead
+
+    if (threadIdx.x == 128) {
+        prefetch_map(&map_w);
+        prefetch_map(&map_a);
+        prefetch_map(&map_sw);
+        prefetch_map(&map_sa);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(drain, 1);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        // the first loads run while the CTA sets itself up
+        pdl_wait_alone();
+        for (; started < STAGES && started < steps; ++started) fetch(started, started);
+    }
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
+                     "r"(S::COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    pdl_wait();
+
+    const uint32_t limit = p.wait, drain_limit = p.drain;
+    bool ok = true;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            int s = started;
+            for (; s < steps; ++s) {
+                const uint32_t slot = static_cast<uint32_t>(s % STAGES);
+                ok = mbar_wait<SCOPE_CTA>(empty + 8 * slot, (static_cast<uint32_t>(s / STAGES) & 1u) ^ 1u, limit);
+                if (!ok) break;
+                fetch(slot, s);
+            }
+            // the copies in flight end before the CTA does, whichever role stopped waiting
+            bool drained = true;
+            for (int i = s > STAGES ? s - STAGES : 0; i < s; ++i)
+                drained &= mbar_wait<SCOPE_CTA>(full + 8 * (i % STAGES), static_cast<uint32_t>(i / STAGES) & 1u, drain_limit);
+            if (!ok || !drained) atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        constexpr uint32_t idesc = fp4_idesc<NV>(kFp4Rows, NT);
+        const bool one = elect_one();
+        uint32_t slot = 0, phase = 0;
+        for (int s = 0; s < steps; ++s) {
+            ok = mbar_wait<SCOPE_CTA>(full + 8 * slot, phase, limit);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            const uint32_t stage = ring + slot * S::STAGE;
+            const int left = p.k - (s0 + s) * kFp4Step;               // elements of k from this stage on
+            if (left < kFp4Step && left % 64 != 0) fp4_clear_tail<NV, S::ROW_TILES, S::AT_SW, S::AT_SA>(stage, p.k, lane);
+            tc_fence_after();
+            if (one) {
+                fp4_stage<NV, S::ROW_TILES, S::AT_A, S::AT_SW, S::AT_SA, false>(
+                    tmem, stage, tmem + S::ACC + (s & 1) * S::COLS_S, idesc, left >= kFp4Step ? 4 : (left + 63) / 64, s == 0);
+                tc_commit(empty + 8 * slot);
+                if (s == steps - 1) tc_commit(acc_full);
+            }
+            __syncwarp();
+            if (++slot == STAGES) {
+                slot = 0;
+                phase ^= 1u;
+            }
+        }
+        if (one) {
+            // the MMAs in flight end before TMEM is freed, whichever role stopped waiting
+            tc_commit(drain);
+            const bool drained = mbar_wait<SCOPE_CTA>(drain, 0, drain_limit);
+            if (!ok || !drained) atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
+        const uint32_t acc = tmem + (static_cast<uint32_t>(warp) << 21);
+        const int row = threadIdx.x;
+        const long long n = static_cast<long long>(tn) * kFp4Rows + row;
+        const float fa = fp4_factor(p.a_gs), fw = fp4_factor(p.w_gs);
+        const float bias = p.bias != nullptr && n < p.n ? load_as(p.bias, n, p.dt) : 0.f;
+        ok = mbar_wait<SCOPE_CTA>(acc_full, 0, limit);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (ok) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < NT; c += 16) {
+                uint32_t v[16];
+                tmem_ld_x16(acc + c, v);
+                tmem_wait_ld();
+                if (nc == 1) {
+                    if (n < p.n) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const long long m = static_cast<long long>(tm) * NT + c + i;
+                            if (m < p.m) store_as(p.out, m * p.n + n, p.dt, fp4_value(__uint_as_float(v[i]), fa, fw, bias));
+                        }
+                    }
+                } else {
+                    // every copy into the ring has been read: it takes the sums, [token][channel]
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(ring + ((c + i) * kFp4Rows + row) * 4), "r"(v[i]) : "memory");
+                }
+            }
+        } else if (lane == 0) {
+            atomicOr(p.err, ERRF_WAIT_TIMEOUT);
+        }
+    }
+
+    if (nc > 1) {
+        // tokens rank, rank + nc, ... of the tile: add the CTAs' sums and write
+        cluster_sync();
+        const float fa = fp4_factor(p.a_gs), fw = fp4_factor(p.w_gs);
+        for (int e = threadIdx.x; e < (NT + static_cast<int>(nc) - 1) / static_cast<int>(nc) * 32; e += kFp4Threads) {
+            const int i = (e >> 5) * static_cast<int>(nc) + static_cast<int>(rank);
+            const long long m = static_cast<long long>(tm) * NT + i, n = static_cast<long long>(tn) * kFp4Rows + lane * 4;
+            if (i >= NT || m >= p.m || n >= p.n) continue;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (uint32_t r = 0; r < nc; ++r) {
+                const float4 o = ld_cluster_f4(ring + (i * kFp4Rows + lane * 4) * 4, r);
+                v.x += o.x;
+                v.y += o.y;
+                v.z += o.z;
+                v.w += o.w;
+            }
+            const float a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < p.n)
+                    store_as(p.out, m * p.n + n + j, p.dt,
+                             fp4_value(a[j], fa, fw, p.bias != nullptr ? load_as(p.bias, n + j, p.dt) : 0.f));
+        }
+        cluster_sync();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::COLS));
+    }
+}
+
+}  // namespace rmsq

@@ -4,6 +4,7 @@
 
 #include "rmsq_matmul_pair.cuh"
 #include "rmsq_ops.h"
+#include "rmsq_tensor_map.h"
 
 namespace rmsq {
 
@@ -25,43 +26,10 @@ template <int NB> static cudaError_t launch_stream(MatmulParams& p, const Device
     return launch_stream<NB, 32>(p, stream);
 }
 
-// cuTensorMapEncodeTiled from the driver (the library does not link it).
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeFn encode_fn()
-{
-    static std::atomic<void*> fn{nullptr};
-    void* f = fn.load();
-    if (f == nullptr) {
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess || found != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn.store(f);
-    }
-    return reinterpret_cast<EncodeFn>(f);
-}
-
-// Codes [rows x k], read in boxes of box_rows x 128 elements; what lies outside reads as 0.
+// Codes [rows x k], read in boxes of box_rows x 128 elements.
 static bool encode(CUtensorMap* map, const void* codes, long long rows, int k, int box_rows)
 {
-    const EncodeFn fn = encode_fn();
-    if (fn == nullptr) return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k)};
-    const cuuint32_t box[2] = {kTcCodes, static_cast<cuuint32_t>(box_rows)}, step[2] = {1, 1};
-    const auto make = [&]() {
-        return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    };
-    const CUresult r = make();
-    if (r != CUDA_ERROR_INVALID_CONTEXT) return r == CUDA_SUCCESS;
-    // a thread that has made no runtime call that binds the device's context yet
-    int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && make() == CUDA_SUCCESS;
+    return encode_map(map, codes, 1, rows, k, box_rows, kTcCodes, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // CTAs that share a tile's k: as many as let all tiles run at a time, each with at least 2 code stages.

@@ -1,0 +1,303 @@
+// rmsq_quant.cu -- quantisation to NVFP4 and MXFP4 without a norm, and NVFP4's global scale (declared in
+// include/rmsq.h).
+//
+//   NVFP4  per 16 elements: s_b = E4M3(min(gs amax_b / 6, 448));  q = E2M1(x gs / s_b);  gs = 2688 / max |x|
+//   MXFP4  per 32 elements: e_b = clamp(ceil(log2(amax_b / 6)) + 127, 0, 255);  q = E2M1(x 2^(127 - e_b))
+//
+// Bound by HBM: an element of 16 bits is read once and leaves as 4 bits and its part of a scale. A thread takes 16
+// neighbours, so a block's maximum needs no more than one exchange, and codes leave as 8 bytes a thread.
+#include <cstdint>
+
+#include "rmsq_norm.cuh"
+#include "rmsq_ops.h"
+
+namespace rmsq {
+
+struct QuantParams {
+    const void* x;
+    const float* gs;                 // or null (1)
+    unsigned char* out;
+    unsigned char* scale;
+    long long units;                 // of 16 elements
+    long long row_units;             // per row
+    int swizzled;
+    int k_tiles;                     // swizzled: tiles of 4 scales per row
+    int words;                       // swizzled: a row is whole tiles of 4 scales
+};
+
+constexpr int kQuantThreads = 256;
+
+// 16 elements as fp32 pairs.
+template <int DT> __device__ __forceinline__ void load16(const void* x, long long unit, float2 (&f)[8])
+{
+    constexpr int N = DT == DT_F32 ? 4 : 2;
+    const uint4* const p = static_cast<const uint4*>(x) + unit * N;
+    uint4 v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = ld_stream_v4(p + i);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float2 t[8 / N];
+        Elem<DT>::pairs(v[i], t);
+#pragma unroll
+        for (int j = 0; j < 8 / N; ++j) f[i * (8 / N) + j] = t[j];
+    }
+}
+
+// max |f|, NaN where one of them is.
+__device__ __forceinline__ float amax16(const float2 (&f)[8])
+{
+    float a = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = max3_nan(a, fabsf(f[j].x), fabsf(f[j].y));
+    return a;
+}
+
+template <int DT, bool NV> __global__ void __launch_bounds__(kQuantThreads) rmsq_quant_kernel(const QuantParams p)
+{
+    pdl_wait();
+    const long long first = static_cast<long long>(blockIdx.x) * kQuantThreads, unit = first + threadIdx.x;
+    const bool in = unit < p.units;
+    float2 f[8];
+    if (in) load16<DT>(p.x, unit, f);
+    else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = make_float2(0.f, 0.f);
+    }
+    float a = amax16(f);
+    uint32_t code;
+    float q[16];
+    if (NV) {
+        const float gs = p.gs != nullptr ? __ldg(p.gs) : 1.0f;
+        code = cvt_e4m3x2(__fdiv_rn(__fmul_rn(gs, a), 6.0f), 0.f) & 0xFFu;
+        if (!(a < __int_as_float(0x7F800000))) code = 0x7Fu;           // a NaN or an infinity: scale NaN
+        const float s = e4m3_value(code);
+        const float inv = s > 0.f ? __fdiv_rn(gs, s) : 0.f;
+        // The quotient in multiples of 2^-19 (24 is in [16, 32), and |x inv| is at most 6.4 unless it
+        // saturates): exact ties, frequent with 16-bit elements, stay ties in spite of inv's rounding.
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 t = add2(fma2(f[j], splat(inv), splat(24.f)), splat(-24.f));
+            q[2 * j] = t.x;
+            q[2 * j + 1] = t.y;
+        }
+    } else {
+        a = max3_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1), 0.f);
+        code = a < __int_as_float(0x7F800000) ? ue8m0_code(a) : 255u;
+        const float inv = code < 255u ? ue8m0_inv_factor(code) : 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 t = mul2(f[j], splat(inv));
+            q[2 * j] = t.x;
+            q[2 * j + 1] = t.y;
+        }
+    }
+    if (in) {
+        float lo[8], hi[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            lo[j] = q[j];
+            hi[j] = q[8 + j];
+        }
+        st_v2(p.out + unit * 8, cvt_e2m1x8(lo), cvt_e2m1x8(hi));
+    }
+    constexpr int PER = NV ? 1 : 2;                                     // units per scale
+    if (!p.swizzled) {
+        if (in && threadIdx.x % PER == 0) p.scale[unit / PER] = static_cast<unsigned char>(code);
+        return;
+    }
+    const long long row0 = first / p.row_units;
+    const unsigned in_row = static_cast<unsigned>(first - row0 * p.row_units) + threadIdx.x;
+    const unsigned down = in_row / static_cast<unsigned>(p.row_units);
+    const long long row = row0 + down;
+    const int sf = static_cast<int>((in_row - down * static_cast<unsigned>(p.row_units)) / PER);
+    unsigned char* const at = p.scale + (row / 128 * p.k_tiles + sf / 4) * 512 + row % 32 * 16 + row % 128 / 32 * 4;
+    if (p.words) {
+        // the four scales of a tile's row come from neighbouring lanes
+        uint32_t w = code << (8 * (sf & 3));
+        w |= __shfl_xor_sync(0xFFFFFFFFu, w, PER);
+        w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2 * PER);
+        if (in && threadIdx.x % (4 * PER) == 0) st_u32(at, w);
+    } else if (in && threadIdx.x % PER == 0) {
+        at[sf & 3] = static_cast<unsigned char>(code);
+    }
+}
+
+// The global scale, in two steps: the maxima of parts of the tensor, one per CTA, then their maximum. A tensor that one
+// CTA reads in about the time of a launch takes one step.
+struct AmaxParams {
+    const void* x;
+    long long vectors, count;        // whole vectors of 16 bytes, elements
+    float* part;                     // or null: out is written
+    float* out;
+};
+
+constexpr int kAmaxThreads = 512;
+
+__device__ __forceinline__ float gs_of(float a)
+{
+    return a == 0.f ? 1.0f : a != a ? a : fminf(__fdiv_rn(448.0f * 6.0f, a), 3.402823466e38f);
+}
+
+// Maximum over the CTA, in thread 0; NaN where one is.
+__device__ __forceinline__ float cta_max_nan(float a)
+{
+    __shared__ float w[kAmaxThreads / 32];
+    a = warp_max_nan(a);
+    if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = a;
+    __syncthreads();
+    if (threadIdx.x < 32) a = warp_max_nan(threadIdx.x < kAmaxThreads / 32 ? w[threadIdx.x] : 0.f);
+    return a;
+}
+
+template <int DT> __global__ void __launch_bounds__(kAmaxThreads) rmsq_amax_kernel(const AmaxParams p)
+{
+    constexpr int VW = Elem<DT>::EPV, U = 4;
+    pdl_wait();
+    float a = 0.f;
+    const long long stride = static_cast<long long>(gridDim.x) * kAmaxThreads;
+    const uint4* const x = static_cast<const uint4*>(p.x);
+    for (long long i = static_cast<long long>(blockIdx.x) * kAmaxThreads + threadIdx.x; i < p.vectors; i += U * stride) {
+        uint4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = i + u * stride < p.vectors ? ld_v4(x + i + u * stride) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float2 f[VW / 2];
+            Elem<DT>::pairs(v[u], f);
+#pragma unroll
+            for (int j = 0; j < VW / 2; ++j) a = max3_nan(a, fabsf(f[j].x), fabsf(f[j].y));
+        }
+    }
+    if (blockIdx.x == 0 && threadIdx.x < p.count - p.vectors * VW) {
+        const typename Scalar<DT>::T e = static_cast<const typename Scalar<DT>::T*>(p.x)[p.vectors * VW + threadIdx.x];
+        a = max3_nan(a, fabsf(Scalar<DT>::get(e)), 0.f);
+    }
+    a = cta_max_nan(a);
+    if (threadIdx.x == 0) {
+        if (p.part != nullptr) p.part[blockIdx.x] = a;
+        else *p.out = gs_of(a);
+    }
+}
+
+static __global__ void __launch_bounds__(kAmaxThreads) rmsq_amax_join_kernel(const float* part, int parts, float* out)
+{
+    pdl_wait();
+    float a = 0.f;
+    for (int i = threadIdx.x; i < parts; i += kAmaxThreads) a = max3_nan(a, part[i], 0.f);
+    a = cta_max_nan(a);
+    if (threadIdx.x == 0) *out = gs_of(a);
+}
+
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+static bool known_dtype(int dtype) { return dtype == RMSQ_BF16 || dtype == RMSQ_FP16 || dtype == RMSQ_F32; }
+
+static rmsq_status status_of(cudaError_t e)
+{
+    if (e == cudaSuccess) return RMSQ_OK;
+    cudaGetLastError();
+    return RMSQ_ERR_LAUNCH;
+}
+
+template <bool NV> static const void* quant_fn(int dtype)
+{
+    return dtype == RMSQ_BF16   ? reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_BF16, NV>)
+           : dtype == RMSQ_FP16 ? reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_FP16, NV>)
+                                : reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_F32, NV>);
+}
+
+static rmsq_status quantise(bool nv, const void* input, int64_t rows, int64_t hidden, int dtype, const float* global_scale,
+                            void* output, void* block_scale, int scale_layout, void* stream)
+{
+    const int block = nv ? 16 : 32;
+    if (!known_dtype(dtype)) return RMSQ_ERR_DTYPE;
+    if (scale_layout != RMSQ_SCALE_ROW_MAJOR && scale_layout != RMSQ_SCALE_SWIZZLED_128x4) return RMSQ_ERR_DTYPE;
+    if (rows < 0 || hidden < block || hidden % block != 0 || hidden > RMSQ_QUANT_MAX_HIDDEN || rows > RMSQ_QUANT_MAX_ROWS)
+        return RMSQ_ERR_SHAPE;
+    if (rows == 0) return RMSQ_OK;
+    if (!input || !output || !block_scale) return RMSQ_ERR_NULL;
+    if (!aligned16(input) || !aligned16(output) || !aligned16(block_scale) || reinterpret_cast<uintptr_t>(global_scale) % 4 != 0)
+        return RMSQ_ERR_ALIGN;
+    QuantParams p = {};
+    p.x = input;
+    p.gs = global_scale;
+    p.out = static_cast<unsigned char*>(output);
+    p.scale = static_cast<unsigned char*>(block_scale);
+    p.row_units = hidden / 16;
+    p.units = rows * p.row_units;
+    p.swizzled = scale_layout == RMSQ_SCALE_SWIZZLED_128x4;
+    p.k_tiles = static_cast<int>((hidden / block + 3) / 4);
+    p.words = hidden % (4 * block) == 0;
+    const long long grid = (p.units + kQuantThreads - 1) / kQuantThreads;
+    if (grid > INT32_MAX) return RMSQ_ERR_SHAPE;
+    DeviceView dv;
+    if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
+    void* args[] = {&p};
+    return status_of(launch_kernel(nv ? quant_fn<true>(dtype) : quant_fn<false>(dtype), dim3(static_cast<unsigned>(grid)),
+                                   kQuantThreads, 0, 1, static_cast<cudaStream_t>(stream), args));
+}
+
+}  // namespace rmsq
+
+using namespace rmsq;
+
+extern "C" rmsq_status quant_nvfp4(const void* input, int64_t rows, int64_t hidden, int dtype, const float* global_scale,
+                                   void* output, void* block_scale, int scale_layout, void* stream)
+{
+    return quantise(true, input, rows, hidden, dtype, global_scale, output, block_scale, scale_layout, stream);
+}
+
+extern "C" rmsq_status quant_mxfp4(const void* input, int64_t rows, int64_t hidden, int dtype, void* output,
+                                   void* block_scale, int scale_layout, void* stream)
+{
+    return quantise(false, input, rows, hidden, dtype, nullptr, output, block_scale, scale_layout, stream);
+}
+
+// Bytes that one CTA takes alone.
+constexpr int64_t kAmaxAlone = 128 * 1024;
+
+extern "C" int64_t nvfp4_global_scale_workspace(int64_t count)
+{
+    return count > 0 ? RMSQ_GLOBAL_SCALE_PARTS * static_cast<int64_t>(sizeof(float)) : 0;
+}
+
+extern "C" rmsq_status nvfp4_global_scale(const void* input, int64_t count, int dtype, float* gs_out, void* workspace,
+                                          int64_t workspace_bytes, void* stream)
+{
+    if (!known_dtype(dtype)) return RMSQ_ERR_DTYPE;
+    if (count < 0) return RMSQ_ERR_SHAPE;
+    if (!gs_out) return RMSQ_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(gs_out) % 4 != 0) return RMSQ_ERR_ALIGN;
+    if (count > 0) {
+        if (!input || !workspace) return RMSQ_ERR_NULL;
+        if (!aligned16(input) || !aligned16(workspace)) return RMSQ_ERR_ALIGN;
+        if (workspace_bytes < nvfp4_global_scale_workspace(count)) return RMSQ_ERR_SHAPE;
+    }
+    DeviceView dv;
+    if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    AmaxParams p = {};
+    p.x = input;
+    p.count = count;
+    p.out = gs_out;
+    const int es = dtype == RMSQ_F32 ? 4 : 2;
+    p.vectors = count / (16 / es);
+    long long grid = 1;
+    if (count * es > kAmaxAlone) {
+        grid = (p.vectors + 4 * kAmaxThreads - 1) / (4 * kAmaxThreads);
+        if (grid > 4LL * dv.sms) grid = 4LL * dv.sms;
+        if (grid > RMSQ_GLOBAL_SCALE_PARTS) grid = RMSQ_GLOBAL_SCALE_PARTS;
+        p.part = static_cast<float*>(workspace);
+    }
+    const void* fn = dtype == RMSQ_BF16   ? reinterpret_cast<const void*>(&rmsq_amax_kernel<DT_BF16>)
+                     : dtype == RMSQ_FP16 ? reinterpret_cast<const void*>(&rmsq_amax_kernel<DT_FP16>)
+                                          : reinterpret_cast<const void*>(&rmsq_amax_kernel<DT_F32>);
+    void* args[] = {&p};
+    const rmsq_status s = status_of(launch_kernel(fn, dim3(static_cast<unsigned>(grid)), kAmaxThreads, 0, 1, st, args));
+    if (s != RMSQ_OK || p.part == nullptr) return s;
+    const float* part = p.part;
+    int parts = static_cast<int>(grid);
+    void* join[] = {&part, &parts, &gs_out};
+    return status_of(launch_kernel(reinterpret_cast<const void*>(&rmsq_amax_join_kernel), dim3(1), kAmaxThreads, 0, 1, st, join));
+}

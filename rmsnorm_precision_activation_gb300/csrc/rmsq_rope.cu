@@ -1,0 +1,260 @@
+// rmsq_rope.cu -- C ABI of the per-head norm with rotation and of its gradient: argument checks, the choice of
+// vectors and the launches (declared in include/rmsq.h).
+#include <cmath>
+#include <cstdint>
+
+#include "rmsq_norm_bwd.cuh"
+#include "rmsq_ops.h"
+#include "rmsq_rope.cuh"
+
+namespace rmsq {
+
+static bool aligned(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(bytes) == 0; }
+
+// Whether [tokens][heads][dim] elements with these strides lie apart from one another.
+static bool apart(long long tokens, long long heads, long long dim, long long st, long long sh)
+{
+    if (tokens == 1) st = 0;
+    if (heads == 1) sh = 0;
+    if ((tokens > 1 && st < dim) || (heads > 1 && sh < dim)) return false;
+    return tokens == 1 || heads == 1 || st >= (heads - 1) * sh + dim || sh >= (tokens - 1) * st + dim;
+}
+
+// Strides past this would leave 64 bits once multiplied by a count of heads or tokens.
+constexpr long long kMostStride = 1LL << 31;
+
+static rmsq_status check_side(const rmsq_heads* s, int64_t tokens, int64_t dim, int es, bool output, int* vec)
+{
+    if (s == nullptr) return RMSQ_ERR_NULL;
+    if (s->heads < 1 || s->heads > 65536 || s->token_stride < 0 || s->head_stride < 0 || s->token_stride >= kMostStride ||
+        s->head_stride >= kMostStride)
+        return RMSQ_ERR_SHAPE;
+    if (tokens == 0) return RMSQ_OK;
+    if (s->data == nullptr) return RMSQ_ERR_NULL;
+    if (!aligned(s->data, es)) return RMSQ_ERR_ALIGN;
+    if (output && !apart(tokens, s->heads, dim, s->token_stride, s->head_stride)) return RMSQ_ERR_SHAPE;
+    // elements that every row starts at a multiple of, in memory
+    while (*vec > 1 && (!aligned(s->data, *vec * es) || (tokens > 1 && s->token_stride % *vec != 0) ||
+                        (s->heads > 1 && s->head_stride % *vec != 0)))
+        *vec /= 2;
+    return RMSQ_OK;
+}
+
+template <int DT, int V, bool INTER> static const void* rope_at(bool backward)
+{
+    return backward ? reinterpret_cast<const void*>(&rmsq_rope_bwd_kernel<DT, V, INTER>)
+                    : reinterpret_cast<const void*>(&rmsq_rope_kernel<DT, V, INTER>);
+}
+
+template <int DT> static const void* rope_fn(int vec, bool inter, bool backward)
+{
+    if constexpr (DT != DT_F32)
+        if (vec == 8) return inter ? rope_at<DT, 8, true>(backward) : rope_at<DT, 8, false>(backward);
+    if (vec == 4) return inter ? rope_at<DT, 4, true>(backward) : rope_at<DT, 4, false>(backward);
+    if (vec == 2) return inter ? rope_at<DT, 2, true>(backward) : rope_at<DT, 2, false>(backward);
+    return inter ? rope_at<DT, 1, true>(backward) : rope_at<DT, 1, false>(backward);
+}
+
+struct RopeCall {
+    const rmsq_heads *dq, *dk;                   // backward: gradients that come
+    const rmsq_heads *q, *k;
+    const void *gq, *gk;
+    const rmsq_rotation* rot;
+    int64_t tokens, dim;
+    int dtype;
+    float eps, offset;
+    const rmsq_heads *oq, *ok;
+};
+
+// Checks a call and fills in everything but the launch; *vec: the elements a vector holds.
+static rmsq_status prepare_rope(const RopeCall& c, RopeParams* p, int* vec)
+{
+    if (c.dtype != RMSQ_BF16 && c.dtype != RMSQ_FP16 && c.dtype != RMSQ_F32) return RMSQ_ERR_DTYPE;
+    if (c.rot == nullptr || c.q == nullptr || c.k == nullptr || c.oq == nullptr || c.ok == nullptr) return RMSQ_ERR_NULL;
+    const rmsq_rotation& r = *c.rot;
+    if (r.position_bits != 32 && r.position_bits != 64) return RMSQ_ERR_DTYPE;
+    if (c.tokens < 0 || c.tokens > RMSQ_ROPE_MAX_TOKENS || c.dim < 2 || c.dim > RMSQ_ROPE_MAX_DIM || c.dim % 2 != 0 ||
+        r.rotated < 2 || r.rotated > c.dim || r.rotated % 2 != 0 || r.places < 1 || r.axes < 1 || r.axes > kRopeAxes)
+        return RMSQ_ERR_SHAPE;
+    int sum = 0;
+    for (int a = 0; a < r.axes && r.axes > 1; ++a) {
+        if (r.sections[a] < 0 || r.sections[a] > r.rotated / 2) return RMSQ_ERR_SHAPE;
+        sum += r.sections[a];
+    }
+    if (r.axes > 1 && sum != r.rotated / 2) return RMSQ_ERR_SHAPE;
+    if (!(c.eps >= 0.0f) || !std::isfinite(c.eps) || !std::isfinite(c.offset)) return RMSQ_ERR_VALUE;
+    if (c.q->heads != c.oq->heads || c.k->heads != c.ok->heads) return RMSQ_ERR_SHAPE;
+    const int es = c.dtype == RMSQ_F32 ? 4 : 2, half = r.rotated / 2;
+    *vec = 16 / es;
+    rmsq_status st = check_side(c.q, c.tokens, c.dim, es, false, vec);
+    if (st == RMSQ_OK) st = check_side(c.k, c.tokens, c.dim, es, false, vec);
+    if (st == RMSQ_OK) st = check_side(c.oq, c.tokens, c.dim, es, true, vec);
+    if (st == RMSQ_OK) st = check_side(c.ok, c.tokens, c.dim, es, true, vec);
+    if (st != RMSQ_OK) return st;
+    if (c.tokens > 0) {
+        if (!c.gq || !c.gk || !r.cos || !r.sin || !r.positions) return RMSQ_ERR_NULL;
+        if (!aligned(c.gq, es) || !aligned(c.gk, es) || !aligned(r.cos, 4) || !aligned(r.sin, 4) ||
+            !aligned(r.positions, r.position_bits / 8))
+            return RMSQ_ERR_ALIGN;
+        while (*vec > 1 && (!aligned(c.gq, *vec * es) || !aligned(c.gk, *vec * es))) *vec /= 2;
+    }
+    // vectors end where the pairs' halves and the rotation do
+    const auto whole = [&](int v) {
+        return r.neighbours ? c.dim % v == 0 && r.rotated % v == 0 : half % v == 0 && (c.dim / 2 - half) % v == 0;
+    };
+    while (*vec > 1 && !whole(*vec)) *vec /= 2;
+    *p = {};
+    const rmsq_heads* in[2] = {c.q, c.k};
+    const rmsq_heads* out[2] = {c.oq, c.ok};
+    const void* gamma[2] = {c.gq, c.gk};
+    for (int s = 0; s < 2; ++s) {
+        RopeSide& d = p->side[s];
+        d.x = in[s]->data;
+        d.xt = in[s]->token_stride;
+        d.xh = in[s]->head_stride;
+        d.out = out[s]->data;
+        d.ot = out[s]->token_stride;
+        d.oh = out[s]->head_stride;
+        d.gamma = gamma[s];
+        d.heads = static_cast<int>(in[s]->heads);
+    }
+    p->cos = r.cos;
+    p->sin = r.sin;
+    p->positions = r.positions;
+    p->tokens = c.tokens;
+    p->places = r.places;
+    p->dim = static_cast<int>(c.dim);
+    p->half = half;
+    p->wide = r.position_bits == 64;
+    p->axes = r.axes;
+    for (int a = 0, end = 0; a < kRopeAxes; ++a) {
+        end += r.axes > 1 && a < r.axes ? r.sections[a] : 0;
+        p->until[a] = a < r.axes - 1 ? end : half;
+    }
+    p->vec_table = half % 4 == 0 && aligned(r.cos, 16) && aligned(r.sin, 16);
+    p->eps = c.eps;
+    p->offset = c.offset;
+    p->inv_dim = 1.0f / static_cast<float>(c.dim);
+    return RMSQ_OK;
+}
+
+// Lanes per row, and turns of rows that a warp takes on one token: as many as still leave every SM `warps`.
+static void deal_rope(RopeParams* p, int vec, bool neighbours, int sms, int warps, int most)
+{
+    // a lane holds 8 pairs, in steps of a vector (neighbours: of a pair at least)
+    const int step = neighbours ? (vec > 2 ? vec / 2 : 1) : vec;
+    const int units = (p->dim / 2 / step + 8 / step - 1) / (8 / step);
+    p->lanes = 1;
+    while (p->lanes < units) p->lanes *= 2;
+    const int rows = 32 / p->lanes;
+    const long long turns = (p->side[0].heads + rows - 1) / rows + (p->side[1].heads + rows - 1) / rows;
+    p->run = most;
+    while (p->run > 1 && p->tokens * turns / p->run < static_cast<long long>(sms) * warps) p->run /= 2;
+    for (RopeSide& s : p->side) s.items = (s.heads + rows * p->run - 1) / (rows * p->run);
+}
+
+static const void* rope_kernel(int dtype, int vec, bool neighbours, bool backward)
+{
+    return dtype == RMSQ_BF16   ? rope_fn<DT_BF16>(vec, neighbours, backward)
+           : dtype == RMSQ_FP16 ? rope_fn<DT_FP16>(vec, neighbours, backward)
+                                : rope_fn<DT_F32>(vec, neighbours, backward);
+}
+
+static rmsq_status status_of(cudaError_t e)
+{
+    if (e == cudaSuccess) return RMSQ_OK;
+    cudaGetLastError();
+    return RMSQ_ERR_LAUNCH;
+}
+
+// Partial rows of the gammas' gradients: one per CTA.
+static int64_t rope_parts(int64_t tokens) { return tokens < RMSQ_ROPE_PARTS ? tokens : RMSQ_ROPE_PARTS; }
+
+}  // namespace rmsq
+
+using namespace rmsq;
+
+extern "C" rmsq_status rmsnorm_rope(const rmsq_heads* query, const rmsq_heads* key, const void* query_gamma,
+                                    const void* key_gamma, const rmsq_rotation* rotation, int64_t tokens, int64_t dim,
+                                    int dtype, float epsilon, float weight_offset, const rmsq_heads* query_output,
+                                    const rmsq_heads* key_output, void* stream)
+{
+    RopeParams p;
+    int vec = 0;
+    const rmsq_status st = prepare_rope({nullptr, nullptr, query, key, query_gamma, key_gamma, rotation, tokens, dim, dtype,
+                                         epsilon, weight_offset, query_output, key_output}, &p, &vec);
+    if (st != RMSQ_OK || tokens == 0) return st;
+    DeviceView dv;
+    if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
+    const bool neighbours = rotation->neighbours != 0;
+    deal_rope(&p, vec, neighbours, dv.sms, 16, 8);
+    const long long items = tokens * (static_cast<long long>(p.side[0].items) + p.side[1].items);
+    const long long grid = (items + kRopeWarps - 1) / kRopeWarps;
+    if (grid > INT32_MAX) return RMSQ_ERR_SHAPE;
+    void* args[] = {&p};
+    return status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, false), dim3(static_cast<unsigned>(grid)), kRopeWarps * 32,
+                                   0, 1, static_cast<cudaStream_t>(stream), args));
+}
+
+extern "C" int64_t rmsnorm_rope_backward_workspace(int64_t tokens, int64_t dim)
+{
+    if (tokens <= 0 || dim <= 0 || dim > RMSQ_ROPE_MAX_DIM) return 0;
+    return rope_parts(tokens) * 2 * dim * static_cast<int64_t>(sizeof(float));
+}
+
+extern "C" rmsq_status rmsnorm_rope_backward(const rmsq_heads* grad_query, const rmsq_heads* grad_key,
+                                             const rmsq_heads* query, const rmsq_heads* key, const void* query_gamma,
+                                             const void* key_gamma, const rmsq_rotation* rotation, int64_t tokens,
+                                             int64_t dim, int dtype, float epsilon, float weight_offset,
+                                             const rmsq_heads* query_output, const rmsq_heads* key_output,
+                                             void* grad_query_gamma, void* grad_key_gamma, int param_grad_dtype,
+                                             void* workspace, int64_t workspace_bytes, void* stream)
+{
+    RopeParams p;
+    int vec = 0;
+    rmsq_status st = prepare_rope({grad_query, grad_key, query, key, query_gamma, key_gamma, rotation, tokens, dim, dtype,
+                                   epsilon, weight_offset, query_output, key_output}, &p, &vec);
+    if (st != RMSQ_OK) return st;
+    if (param_grad_dtype != dtype && param_grad_dtype != RMSQ_F32) return RMSQ_ERR_DTYPE;
+    const int es = dtype == RMSQ_F32 ? 4 : 2;
+    const rmsq_heads* grads[2] = {grad_query, grad_key};
+    for (int s = 0; s < 2; ++s) {
+        st = check_side(grads[s], tokens, dim, es, false, &vec);
+        if (st != RMSQ_OK) return st;
+        if (grads[s]->heads != p.side[s].heads) return RMSQ_ERR_SHAPE;
+        p.side[s].dy = grads[s]->data;
+        p.side[s].dt = grads[s]->token_stride;
+        p.side[s].dh = grads[s]->head_stride;
+    }
+    if (!grad_query_gamma || !grad_key_gamma) return RMSQ_ERR_NULL;
+    if (!aligned(grad_query_gamma, 16) || !aligned(grad_key_gamma, 16)) return RMSQ_ERR_ALIGN;
+    if (tokens > 0) {
+        if (!workspace) return RMSQ_ERR_NULL;
+        if (!aligned(workspace, 16)) return RMSQ_ERR_ALIGN;
+        if (workspace_bytes < rmsnorm_rope_backward_workspace(tokens, dim)) return RMSQ_ERR_SHAPE;
+    }
+    DeviceView dv;
+    if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
+    NormBwdReduceParams r = {};
+    r.part = static_cast<const float*>(workspace);
+    r.dgamma = grad_query_gamma;
+    r.dbeta = grad_key_gamma;
+    r.hidden = static_cast<int>(dim);
+    r.dt = param_grad_dtype;
+    if (tokens > 0) {
+        const bool neighbours = rotation->neighbours != 0;
+        deal_rope(&p, vec, neighbours, dv.sms, 16, 8);
+        p.part = static_cast<float*>(workspace);
+        const long long most = p.side[0].items > p.side[1].items ? p.side[0].items : p.side[1].items;
+        long long grid = (tokens * most + kRopeWarps - 1) / kRopeWarps;
+        if (grid > rope_parts(tokens)) grid = rope_parts(tokens);
+        r.parts = static_cast<int>(grid);
+        void* args[] = {&p};
+        st = status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, true), dim3(static_cast<unsigned>(grid)),
+                                     kRopeWarps * 32, 0, 1, static_cast<cudaStream_t>(stream), args));
+        if (st != RMSQ_OK) return st;
+    }
+    void* args[] = {&r};
+    return status_of(launch_kernel(norm_bwd_reduce_fn(), dim3(static_cast<unsigned>((2 * dim + 31) / 32)), 512, 0, 1,
+                                   static_cast<cudaStream_t>(stream), args));
+}
