@@ -1,7 +1,7 @@
 // rmsq_fp4.cu -- C ABI of the 4-bit products: argument checks and the choice of kernel.
 #include <cstdint>
 
-#include "rmsq_fp4.cuh"
+#include "rmsq_fp4_pair.cuh"
 #include "rmsq_ops.h"
 #include "rmsq_tensor_map.h"
 
@@ -46,12 +46,31 @@ template <bool NV, int NT> static cudaError_t launch_tile(Fp4Params& p, const Fp
     return launch_kernel(fn, dim3(static_cast<unsigned>(tiles * cluster)), kFp4Threads, S::SMEM, cluster, stream, args);
 }
 
+template <bool NV> static cudaError_t launch_pair(Fp4Params& p, const Fp4Operands& o, const DeviceView& dv, cudaStream_t stream)
+{
+    using S = Fp4PairShape<NV>;
+    CUtensorMap map_w, map_a, map_sw, map_sa;
+    if (!encode<NV>(&map_w, &map_sw, o.w, o.sw, p.n, p.k, kFp4Rows, 1) ||
+        !encode<NV>(&map_a, &map_sa, o.a, o.sa, p.m, p.k, kFp4PairTokens / 2, 2))
+        return cudaErrorUnknown;
+    TcTiles t;
+    t.n_tiles = static_cast<int>((p.n + 2 * kFp4Rows - 1) / (2 * kFp4Rows));
+    t.m_tiles = static_cast<int>((p.m + kFp4PairTokens - 1) / kFp4PairTokens);
+    const long long tiles = static_cast<long long>(t.n_tiles) * t.m_tiles;
+    const long long pairs = tiles < dv.sms / 2 ? tiles : dv.sms / 2;
+    const void *sw = o.sw, *sa = o.sa;
+    void* args[] = {&map_w, &map_a, &map_sw, &map_sa, &p, &t, &sw, &sa};
+    return launch_kernel(reinterpret_cast<const void*>(&rmsq_fp4_pair_kernel<NV>), dim3(static_cast<unsigned>(2 * pairs)),
+                         kFp4PairThreads, S::SMEM, 2, stream, args);
+}
+
 template <bool NV> static cudaError_t launch_fp4(Fp4Params& p, const Fp4Operands& o, const DeviceView& dv, cudaStream_t stream)
 {
     if (p.m <= 16) return launch_tile<NV, 16>(p, o, dv, stream);
     if (p.m <= 32) return launch_tile<NV, 32>(p, o, dv, stream);
     if (p.m <= 64) return launch_tile<NV, 64>(p, o, dv, stream);
-    return launch_tile<NV, 128>(p, o, dv, stream);
+    if (p.m <= 128) return launch_tile<NV, 128>(p, o, dv, stream);
+    return launch_pair<NV>(p, o, dv, stream);
 }
 
 template <bool NV>

@@ -67,14 +67,21 @@ template <bool NV, int NT> struct Fp4Shape {
 
 constexpr int kFp4Threads = 192;
 
-// Scales from shared memory to 4 TMEM columns (all four lane quarters).
-template <bool PAIR> __device__ __forceinline__ void fp4_copy_scales(uint32_t tmem, uint32_t smem)
+// The low word of a descriptor of what lies at a shared-memory address (the high words are constant; both kinds of
+// operand take the same low word, and 16 bytes on are one more).
+__device__ __forceinline__ uint32_t fp4_desc(uint32_t addr) { return tc_desc_lo(addr); }
+
+// 512 bytes of scales from shared memory to 4 TMEM columns (all four lane quarters): no swizzle, groups of 8 rows of 16
+// bytes 128 bytes apart.
+template <bool PAIR> __device__ __forceinline__ void fp4_copy_scales(uint32_t tmem, uint32_t lo)
 {
-    const uint64_t desc = static_cast<uint64_t>((smem & 0x3FFFFu) >> 4) | (1ull << 16) | (8ull << 32) | (1ull << 46);
+    constexpr uint32_t hi = 8u | (1u << 14);
     if constexpr (PAIR)
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\ttcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}"
+                     ::"r"(tmem), "r"(lo), "r"(hi) : "memory");
     else
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+        asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\ttcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}"
+                     ::"r"(tmem), "r"(lo), "r"(hi) : "memory");
 }
 
 // d (+)= a b^T over 64 elements of k, with scales at sa and sb in TMEM.
@@ -101,46 +108,78 @@ template <bool NV> __host__ __device__ constexpr uint32_t fp4_idesc(int rows, in
            (static_cast<uint32_t>(rows / 16) << 24);
 }
 
-// A stage: the copies of its scales and up to four MMAs (`quarters` of 64 elements have codes). stage: its address;
-// scales: TMEM columns of this stage's scales, the channels' first. The codes' descriptors advance by 32 bytes an MMA.
-template <bool NV, int ROW_TILES, int AT_A, int AT_SW, int AT_SA, bool PAIR>
-__device__ __forceinline__ void fp4_stage(uint32_t d, uint32_t stage, uint32_t scales, uint32_t idesc, int quarters, bool fresh)
+// The copies of a stage's scales. weight, tokens: low words of the descriptors of their tiles in shared memory; to: the TMEM
+// columns, the channels' first. The tokens' row tiles lie T tiles apart.
+template <bool NV, int ROW_TILES, bool PAIR>
+__device__ __forceinline__ void fp4_scales(uint32_t weight, uint32_t tokens, uint32_t to)
 {
-    constexpr int T = fp4_tiles<NV>(), PER = 4 / T;                   // MMAs per tile of scales
-    const uint32_t sa = scales + 4 * T;                               // the tokens': per MMA the row tiles' columns
+    constexpr int T = fp4_tiles<NV>(), D = kFp4ScaleTile / 16;
 #pragma unroll
     for (int i = 0; i < T; ++i) {
-        fp4_copy_scales<PAIR>(scales + 4 * i, stage + AT_SW + i * kFp4ScaleTile);
+        fp4_copy_scales<PAIR>(to + 4 * i, weight + i * D);
 #pragma unroll
-        for (int r = 0; r < ROW_TILES; ++r)
-            fp4_copy_scales<PAIR>(sa + 4 * (i * ROW_TILES + r), stage + AT_SA + (r * T + i) * kFp4ScaleTile);
-    }
-    const uint32_t a_lo = tc_desc_lo(stage), b_lo = tc_desc_lo(stage + AT_A);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (j >= quarters) break;
-        const uint32_t id = j % PER * 2;                              // MXFP4: which two of a tile's four scales
-        fp4_mma<NV, PAIR>(d, a_lo + 2 * j, b_lo + 2 * j, idesc | (id << 29) | (id << 4), scales + 4 * (j / PER),
-                          sa + 4 * ROW_TILES * (j / PER), j > 0 || !fresh);
+        for (int r = 0; r < ROW_TILES; ++r) fp4_copy_scales<PAIR>(to + 4 * (T + i * ROW_TILES + r), tokens + (r * T + i) * D);
     }
 }
+
+// The same where the last stage's tile `end` is taken from elsewhere: the channels' at `tail`, then the tokens' row tiles.
+template <bool NV, int ROW_TILES, bool PAIR>
+__device__ __forceinline__ void fp4_scales_cut(uint32_t weight, uint32_t tokens, uint32_t to, int end, uint32_t tail)
+{
+    constexpr int T = fp4_tiles<NV>(), D = kFp4ScaleTile / 16;
+#pragma unroll 1
+    for (int i = 0; i < T; ++i) {
+        fp4_copy_scales<PAIR>(to + 4 * i, i == end ? tail : weight + i * D);
+#pragma unroll
+        for (int r = 0; r < ROW_TILES; ++r)
+            fp4_copy_scales<PAIR>(to + 4 * (T + i * ROW_TILES + r), i == end ? tail + (1 + r) * D : tokens + (r * T + i) * D);
+    }
+}
+
+// A stage's MMAs: `quarters` of 64 elements have codes; a whole stage's four are issued without a test. a, b: low words of
+// the descriptors of the codes, which advance by 32 bytes an MMA.
+template <bool NV, int ROW_TILES, bool PAIR>
+__device__ __forceinline__ void fp4_mmas(uint32_t d, uint32_t a, uint32_t b, uint32_t scales, uint32_t idesc, int quarters, bool fresh)
+{
+    constexpr int T = fp4_tiles<NV>(), PER = 4 / T;                   // MMAs per tile of scales
+    const auto mma = [&](int j) {
+        const uint32_t id = j % PER * 2;                              // MXFP4: which two of a tile's four scales
+        fp4_mma<NV, PAIR>(d, a + 2 * j, b + 2 * j, idesc | (id << 29) | (id << 4), scales + 4 * (j / PER),
+                          scales + 4 * (T + ROW_TILES * (j / PER)), j > 0 || !fresh);
+    };
+    if (quarters >= 4) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma(j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (j < quarters) mma(j);
+    }
+}
+
+// Scales in the tile of four that k ends in, and which tile of its stage that is (k % 64 == 32: there are 1 to 3).
+template <bool NV> struct Fp4Tail {
+    int tile;
+    uint32_t keep;
+    __device__ __forceinline__ explicit Fp4Tail(int k)
+    {
+        const int held = (k % kFp4Step + (NV ? 15 : 31)) / (NV ? 16 : 32);
+        tile = held / 4;
+        keep = (1u << (8 * (held % 4))) - 1u;
+    }
+    __device__ __forceinline__ uint4 cut(uint4 v) const { return make_uint4(v.x & keep, v.y & keep, v.z & keep, v.w & keep); }
+};
 
 // Clears the scales behind the end of k in the last stage (one warp, after the stage's copies have landed).
 template <bool NV, int ROW_TILES, int AT_SW, int AT_SA>
 __device__ __forceinline__ void fp4_clear_tail(uint32_t stage, int k, int lane)
 {
-    constexpr int T = fp4_tiles<NV>(), B = NV ? 16 : 32;
-    const int held = (k % kFp4Step + B - 1) / B, tile = held / 4;     // scales of the stage; the tile that ends early
-    const uint32_t keep = (1u << (8 * (held % 4))) - 1u;              // held % 4 > 0: k % 64 is 32
+    constexpr int T = fp4_tiles<NV>();
+    const Fp4Tail<NV> tail(k);
 #pragma unroll
     for (int r = 0; r < 1 + ROW_TILES; ++r) {
-        const uint32_t at = stage + (r == 0 ? AT_SW : AT_SA + (r - 1) * T * kFp4ScaleTile) + tile * kFp4ScaleTile + lane * 16;
-        uint4 v = ld_shared_v4(at);
-        v.x &= keep;
-        v.y &= keep;
-        v.z &= keep;
-        v.w &= keep;
-        st_shared_v4(at, v);
+        const uint32_t at = stage + (r == 0 ? AT_SW : AT_SA + (r - 1) * T * kFp4ScaleTile) + tail.tile * kFp4ScaleTile + lane * 16;
+        st_shared_v4(at, tail.cut(ld_shared_v4(at)));
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -250,8 +289,9 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
             if (left < kFp4Step && left % 64 != 0) fp4_clear_tail<NV, S::ROW_TILES, S::AT_SW, S::AT_SA>(stage, p.k, lane);
             tc_fence_after();
             if (one) {
-                fp4_stage<NV, S::ROW_TILES, S::AT_A, S::AT_SW, S::AT_SA, false>(
-                    tmem, stage, tmem + S::ACC + (s & 1) * S::COLS_S, idesc, left >= kFp4Step ? 4 : (left + 63) / 64, s == 0);
+                const uint32_t desc = fp4_desc(stage), scales = tmem + S::ACC + (s & 1) * S::COLS_S;
+                fp4_scales<NV, S::ROW_TILES, false>(desc + S::AT_SW / 16, desc + S::AT_SA / 16, scales);
+                fp4_mmas<NV, S::ROW_TILES, false>(tmem, desc, desc + S::AT_A / 16, scales, idesc, (left + 63) / 64, s == 0);
                 tc_commit(empty + 8 * slot);
                 if (s == steps - 1) tc_commit(acc_full);
             }
