@@ -39,11 +39,12 @@ template <bool NV, int NT> static cudaError_t launch_tile(Fp4Params& p, const Fp
     const int steps = (p.k + kFp4Step - 1) / kFp4Step;
     // CTAs that share a tile's k: as many as let all tiles run at a time
     int cluster = 1;
+    const int tokens = p.m < NT ? static_cast<int>(p.m) : NT;
     for (int c = 2; c <= 8 && c <= steps && c * tiles <= dv.sms * S::CTAS; ++c)
-        if (tiles <= resident_clusters(fn, kFp4Threads, S::SMEM, c)) cluster = c;
+        if (c * fp4_share(tokens, c) <= S::SUM_ROWS && tiles <= resident_clusters(fn, S::THREADS, S::SMEM, c)) cluster = c;
     if (tiles * cluster > INT32_MAX) return cudaErrorInvalidConfiguration;
     void* args[] = {&map_w, &map_a, &map_sw, &map_sa, &p, &t};
-    return launch_kernel(fn, dim3(static_cast<unsigned>(tiles * cluster)), kFp4Threads, S::SMEM, cluster, stream, args);
+    return launch_kernel(fn, dim3(static_cast<unsigned>(tiles * cluster)), S::THREADS, S::SMEM, cluster, stream, args);
 }
 
 template <bool NV> static cudaError_t launch_pair(Fp4Params& p, const Fp4Operands& o, const DeviceView& dv, cudaStream_t stream)

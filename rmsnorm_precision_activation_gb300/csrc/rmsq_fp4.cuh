@@ -9,10 +9,13 @@
 // memory and the tensor cores but TMA and that copy.
 //
 // A CTA takes 128 output channels (the MMA's rows) and NT tokens (its columns); with few tokens, CTAs of a cluster
-// share a tile's k and add their sums through distributed shared memory in rank order.
-//   warps 0-3   read the accumulator and write the output (a lane is a channel: 32 neighbours of a token's row)
-//   warp 4      TMA loads codes and scales of both tiles into a ring, 256 elements of k per stage
-//   warp 5      one thread issues the copies of the scales and the MMAs, four of 64 elements per stage
+// share a tile's k. Each token's sums then go to one of them, which adds them up in rank order: a thread sends its value
+// straight into that CTA's shared memory, whose barrier counts the bytes (sums left in shared memory for others to read
+// between two cluster barriers took 2 us, 3.5 at 128 tokens).
+//   warps 0-3 (0-7 from 64 tokens on)   read the accumulator and write the output (a lane is a channel: 32 neighbours
+//               of a token's row)
+//   the next    TMA loads codes and scales of both tiles into a ring, 256 elements of k per stage
+//   the last    one thread issues the copies of the scales and the MMAs, four of 64 elements per stage
 //
 // k is a multiple of 32, so the last MMA's 64 elements may end half way: TMA fills the codes behind the end with zeros,
 // but the scales there are the padding's, which may be a NaN; they are cleared in shared memory before the copy.
@@ -51,9 +54,13 @@ template <bool NV, int NT> struct Fp4Shape {
     static constexpr int AT_A = CODES_W, AT_SW = AT_A + CODES_A, AT_SA = AT_SW + SCALES_W;
     static constexpr int STAGE = AT_SA + SCALES_A;
     static constexpr int CTAS = NT <= 32 ? 2 : 1;                     // on an SM
+    static constexpr int READERS = NT <= 32 ? 4 : 8;                  // warps that read the accumulator
+    static constexpr int THREADS = 32 * (READERS + 2);
+    // sums from the cluster's CTAs, [rank][four tokens][channel][4]
+    static constexpr int SUM_ROWS = NT + 16, SUMS = SUM_ROWS * kFp4Rows * 4;
     static constexpr int MOST = (CTAS == 2 ? 113 : 226) * 1024;
-    static constexpr int STAGES = (MOST - 2048) / STAGE;
-    static constexpr int SMEM = 2048 + STAGES * STAGE;                // 1024 to align the ring, 1024 for barriers
+    static constexpr int STAGES = (MOST - 2048 - SUMS) / STAGE;
+    static constexpr int SMEM = 2048 + STAGES * STAGE + SUMS;         // 1024 to align the ring, 1024 for barriers
     // TMEM: the accumulator, then two buffers of scales (the channels', the tokens')
     static constexpr int ACC = NT < 32 ? 32 : NT;
     static constexpr int COLS_S = 4 * fp4_tiles<NV>() * (1 + ROW_TILES);
@@ -62,10 +69,7 @@ template <bool NV, int NT> struct Fp4Shape {
     static_assert(STAGE % 1024 == 0 && AT_A % 1024 == 0 && AT_SW % 1024 == 0, "swizzle atoms");
     static_assert(SMEM <= 232448 && COLS * CTAS <= 512, "fits the SM");
     static_assert(SMEM * (CTAS + 1) > 233472 - 1024 * CTAS, "no more CTAs on an SM than TMEM has columns for");
-    static_assert(STAGES * STAGE >= NT * kFp4Rows * 4, "the cluster's sums reuse the ring");
 };
-
-constexpr int kFp4Threads = 192;
 
 // The low word of a descriptor of what lies at a shared-memory address (the high words are constant; both kinds of
 // operand take the same low word, and 16 bytes on are one more).
@@ -193,20 +197,37 @@ __device__ __forceinline__ float fp4_value(float sum, float fa, float fw, float 
     return fmaf(__fmul_rn(sum, fa), fw, bias);
 }
 
+// Tokens that each CTA of a cluster of nc adds up: whole fours, which a thread sends together.
+__host__ __device__ constexpr int fp4_share(int tokens, int nc) { return (tokens + 4 * nc - 1) / (4 * nc) * 4; }
+
+// Four values to another CTA's shared memory (both addresses in the cluster); its barrier counts the 16 bytes.
+__device__ __forceinline__ void fp4_send(uint32_t addr, uint32_t bar, const uint32_t* v)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+                 ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint32_t fp4_peer(uint32_t addr, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+
 template <bool NV, int NT>
-__global__ void __launch_bounds__(kFp4Threads, Fp4Shape<NV, NT>::CTAS)
+__global__ void __launch_bounds__(Fp4Shape<NV, NT>::THREADS, Fp4Shape<NV, NT>::CTAS)
 rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_sw, const __grid_constant__ CUtensorMap map_sa, const Fp4Params p,
                      const TcTiles tiles)
 {
     using S = Fp4Shape<NV, NT>;
-    constexpr int STAGES = S::STAGES;
+    constexpr int STAGES = S::STAGES, LOADER = S::READERS, ISSUER = LOADER + 1;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t tmem_slot;
 
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t bars = ring + STAGES * S::STAGE;
-    const uint32_t full = bars, empty = full + 8 * STAGES, acc_full = empty + 8 * STAGES, drain = acc_full + 8;
+    const uint32_t sums = ring + STAGES * S::STAGE, full = sums + S::SUMS;
+    const uint32_t empty = full + 8 * STAGES, acc_full = empty + 8 * STAGES, drain = acc_full + 8, received = drain + 8;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t nc = cluster_size(), rank = cluster_rank();
@@ -217,6 +238,10 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
     const int steps_all = (p.k + kFp4Step - 1) / kFp4Step;
     const int s0 = static_cast<int>(static_cast<long long>(steps_all) * rank / nc);
     const int steps = static_cast<int>(static_cast<long long>(steps_all) * (rank + 1) / nc) - s0;
+    // the tile's tokens, and those of them that this CTA adds up: per from first on
+    const int tokens = static_cast<int>(min(static_cast<long long>(NT), p.m - static_cast<long long>(tm) * NT));
+    const int per = fp4_share(tokens, static_cast<int>(nc)), fours = per / 4;
+    const int own = max(0, min(per, tokens - static_cast<int>(rank) * per)), own_fours = (own + 3) / 4;
 
     auto fetch = [&](uint32_t slot, int s) {
         const uint32_t bar = full + 8 * slot, dst = ring + slot * S::STAGE;
@@ -228,24 +253,33 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
     };
     int started = 0;                          // stages fetched ahead
 
-    if (threadIdx.x == 128) {
-        prefetch_map(&map_w);
-        prefetch_map(&map_a);
-        prefetch_map(&map_sw);
-        prefetch_map(&map_sa);
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(full + 8 * i, 1);
-            mbar_init(empty + 8 * i, 1);
+    if (warp == LOADER) {
+        // (the whole warp runs the loop and one lane issues: a stage's loads take 120 cycles then, from divergent code 330)
+        const bool one = elect_one();
+        if (one) {
+            prefetch_map(&map_w);
+            prefetch_map(&map_a);
+            prefetch_map(&map_sw);
+            prefetch_map(&map_sa);
+            for (int i = 0; i < STAGES; ++i) {
+                mbar_init(full + 8 * i, 1);
+                mbar_init(empty + 8 * i, 1);
+            }
+            mbar_init(acc_full, 1);
+            mbar_init(drain, 1);
+            mbar_init(received, 1);
+            fence_mbar_init();
+            fence_proxy_async_smem();
+            if (nc > 1) mbar_arrive_expect_tx(received, (nc - 1) * static_cast<uint32_t>(own_fours * kFp4Rows * 16));
         }
-        mbar_init(acc_full, 1);
-        mbar_init(drain, 1);
-        fence_mbar_init();
-        fence_proxy_async_smem();
+        __syncwarp();
         // the first loads run while the CTA sets itself up
         pdl_wait_alone();
-        for (; started < STAGES && started < steps; ++started) fetch(started, started);
+        for (; started < STAGES && started < steps; ++started)
+            if (one) fetch(static_cast<uint32_t>(started), started);
+        __syncwarp();
     }
-    if (warp == 5) {
+    if (warp == ISSUER) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_slot)),
                      "r"(S::COLS)
                      : "memory");
@@ -253,6 +287,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
         tc_fence_before();
     }
     __syncthreads();
+    if (nc > 1) cluster_arrive_as(false);     // this CTA's barriers are set up
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     pdl_wait();
@@ -260,15 +295,18 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
     const uint32_t limit = p.wait, drain_limit = p.drain;
     bool ok = true;
 
-    if (warp == 4) {
+    if (warp == LOADER) {
+        const bool one = elect_one();
+        int s = started;
+        for (; s < steps; ++s) {
+            const uint32_t slot = static_cast<uint32_t>(s % STAGES);
+            ok = mbar_wait<SCOPE_CTA>(empty + 8 * slot, (static_cast<uint32_t>(s / STAGES) & 1u) ^ 1u, limit);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (one) fetch(slot, s);
+            __syncwarp();
+        }
         if (lane == 0) {
-            int s = started;
-            for (; s < steps; ++s) {
-                const uint32_t slot = static_cast<uint32_t>(s % STAGES);
-                ok = mbar_wait<SCOPE_CTA>(empty + 8 * slot, (static_cast<uint32_t>(s / STAGES) & 1u) ^ 1u, limit);
-                if (!ok) break;
-                fetch(slot, s);
-            }
             // the copies in flight end before the CTA does, whichever role stopped waiting
             bool drained = true;
             for (int i = s > STAGES ? s - STAGES : 0; i < s; ++i)
@@ -276,7 +314,11 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
             if (!ok || !drained) atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
         }
         __syncwarp();
-    } else if (warp == 5) {
+        if (nc > 1) {
+            cluster_wait();
+            cluster_arrive_as(false);
+        }
+    } else if (warp == ISSUER) {
         constexpr uint32_t idesc = fp4_idesc<NV>(kFp4Rows, NT);
         const bool one = elect_one();
         uint32_t slot = 0, phase = 0;
@@ -308,69 +350,87 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
             if (!ok || !drained) atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
         }
         __syncwarp();
+        if (nc > 1) {
+            cluster_wait();
+            cluster_arrive_as(false);
+        }
     } else {
-        const uint32_t acc = tmem + (static_cast<uint32_t>(warp) << 21);
-        const int row = threadIdx.x;
-        const long long n = static_cast<long long>(tn) * kFp4Rows + row;
+        const uint32_t acc = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        constexpr int PARTS = S::READERS / 4;                         // of the columns
+        const int row = threadIdx.x & 127, part = warp >> 2;
+        const long long n = static_cast<long long>(tn) * kFp4Rows + row, m0 = static_cast<long long>(tm) * NT;
         const float fa = fp4_factor(p.a_gs), fw = fp4_factor(p.w_gs);
         const float bias = p.bias != nullptr && n < p.n ? load_as(p.bias, n, p.dt) : 0.f;
+        if (nc > 1) cluster_wait();
         ok = mbar_wait<SCOPE_CTA>(acc_full, 0, limit);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (ok) {
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
+            for (int c = part * (NT / PARTS); c < (part + 1) * (NT / PARTS) && c < tokens; c += 16) {
                 uint32_t v[16];
                 tmem_ld_x16(acc + c, v);
                 tmem_wait_ld();
                 if (nc == 1) {
                     if (n < p.n) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const long long m = static_cast<long long>(tm) * NT + c + i;
-                            if (m < p.m) store_as(p.out, m * p.n + n, p.dt, fp4_value(__uint_as_float(v[i]), fa, fw, bias));
-                        }
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < tokens)
+                                store_as(p.out, (m0 + c + i) * p.n + n, p.dt, fp4_value(__uint_as_float(v[i]), fa, fw, bias));
                     }
                 } else {
-                    // every copy into the ring has been read: it takes the sums, [token][channel]
+                    // each four tokens' sums to the CTA that adds them up
+                    int to = c / 4 / fours, at = c / 4 - to * fours;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        asm volatile("st.shared.u32 [%0], %1;" ::"r"(ring + ((c + i) * kFp4Rows + row) * 4), "r"(v[i]) : "memory");
+                    for (int i = 0; i < 4; ++i) {
+                        if (c + 4 * i < tokens) {
+                            const uint32_t addr = sums + ((rank * fours + at) * kFp4Rows + row) * 16;
+                            if (to == static_cast<int>(rank)) st_shared_v4(addr, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+                            else fp4_send(fp4_peer(addr, to), fp4_peer(received, to), v + 4 * i);
+                        }
+                        if (++at == fours) {
+                            at = 0;
+                            ++to;
+                        }
+                    }
                 }
             }
-        } else if (lane == 0) {
-            atomicOr(p.err, ERRF_WAIT_TIMEOUT);
         }
+        if (nc > 1) {
+            cluster_arrive_as(false);                                 // this thread sends no more
+            if (own > 0) {
+                ok = ok && mbar_wait<SCOPE_CLUSTER>(received, 0, limit);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (PARTS > 1) asm volatile("bar.sync 1, %0;" ::"n"(32 * S::READERS) : "memory");   // this CTA's own
+                for (int i = part; ok && i < own_fours; i += PARTS) {
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (uint32_t r = 0; r < nc; ++r) {
+                        const uint4 o = ld_shared_v4(sums + ((r * fours + i) * kFp4Rows + row) * 16);
+                        v.x += __uint_as_float(o.x);
+                        v.y += __uint_as_float(o.y);
+                        v.z += __uint_as_float(o.z);
+                        v.w += __uint_as_float(o.w);
+                    }
+                    const float four[4] = {v.x, v.y, v.z, v.w};
+                    const long long m = m0 + static_cast<int>(rank) * per + 4 * i;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (n < p.n && 4 * i + j < own) store_as(p.out, (m + j) * p.n + n, p.dt, fp4_value(four[j], fa, fw, bias));
+                }
+            }
+        }
+        if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
     }
 
-    if (nc > 1) {
-        // tokens rank, rank + nc, ... of the tile: add the CTAs' sums and write
-        cluster_sync();
-        const float fa = fp4_factor(p.a_gs), fw = fp4_factor(p.w_gs);
-        for (int e = threadIdx.x; e < (NT + static_cast<int>(nc) - 1) / static_cast<int>(nc) * 32; e += kFp4Threads) {
-            const int i = (e >> 5) * static_cast<int>(nc) + static_cast<int>(rank);
-            const long long m = static_cast<long long>(tm) * NT + i, n = static_cast<long long>(tn) * kFp4Rows + lane * 4;
-            if (i >= NT || m >= p.m || n >= p.n) continue;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (uint32_t r = 0; r < nc; ++r) {
-                const float4 o = ld_cluster_f4(ring + (i * kFp4Rows + lane * 4) * 4, r);
-                v.x += o.x;
-                v.y += o.y;
-                v.z += o.z;
-                v.w += o.w;
-            }
-            const float a[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n + j < p.n)
-                    store_as(p.out, m * p.n + n + j, p.dt,
-                             fp4_value(a[j], fa, fw, p.bias != nullptr ? load_as(p.bias, n + j, p.dt) : 0.f));
-        }
-        cluster_sync();
-    }
+    if (nc > 1) cluster_wait();                                       // nobody sends to a CTA that has left
     tc_fence_before();
-    __syncthreads();
-    if (warp == 5) {
+    if (__syncthreads_or(!ok) && nc > 1) {
+        // what was sent here lands before the CTA leaves, which takes about a microsecond
+        const uint32_t t0 = time_units();
+        while (time_units() - t0 < 1000) __nanosleep(100000);
+    }
+    if (warp == ISSUER) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(S::COLS));
     }
