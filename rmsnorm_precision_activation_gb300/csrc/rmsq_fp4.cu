@@ -24,10 +24,9 @@ static bool encode(CUtensorMap* codes_map, CUtensorMap* scales_map, const void* 
                       fp4_tiles<NV>() * kFp4ScaleTile / 8, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <bool NV, int NT> static cudaError_t launch_tile(Fp4Params& p, const Fp4Operands& o, const DeviceView& dv, cudaStream_t stream)
+template <bool NV, int NT> static cudaError_t launch_tile(Fp4Params& p, const Fp4Operands& o, int cluster, cudaStream_t stream)
 {
     using S = Fp4Shape<NV, NT>;
-    const void* fn = reinterpret_cast<const void*>(&rmsq_fp4_tile_kernel<NV, NT>);
     CUtensorMap map_w, map_a, map_sw, map_sa;
     if (!encode<NV>(&map_w, &map_sw, o.w, o.sw, p.n, p.k, kFp4Rows, 1) ||
         !encode<NV>(&map_a, &map_sa, o.a, o.sa, p.m, p.k, NT, S::ROW_TILES))
@@ -35,16 +34,11 @@ template <bool NV, int NT> static cudaError_t launch_tile(Fp4Params& p, const Fp
     TcTiles t;
     t.n_tiles = static_cast<int>((p.n + kFp4Rows - 1) / kFp4Rows);
     t.m_tiles = static_cast<int>((p.m + NT - 1) / NT);
-    const long long tiles = static_cast<long long>(t.n_tiles) * t.m_tiles;
-    const int steps = (p.k + kFp4Step - 1) / kFp4Step;
-    // CTAs that share a tile's k: as many as let all tiles run at a time
-    int cluster = 1;
-    const int tokens = p.m < NT ? static_cast<int>(p.m) : NT;
-    for (int c = 2; c <= 8 && c <= steps && c * tiles <= dv.sms * S::CTAS; ++c)
-        if (c * fp4_share(tokens, c) <= S::SUM_ROWS && tiles <= resident_clusters(fn, S::THREADS, S::SMEM, c)) cluster = c;
-    if (tiles * cluster > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const long long ctas = static_cast<long long>(t.n_tiles) * t.m_tiles * cluster;
+    if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
     void* args[] = {&map_w, &map_a, &map_sw, &map_sa, &p, &t};
-    return launch_kernel(fn, dim3(static_cast<unsigned>(tiles * cluster)), S::THREADS, S::SMEM, cluster, stream, args);
+    return launch_kernel(reinterpret_cast<const void*>(&rmsq_fp4_tile_kernel<NV, NT>), dim3(static_cast<unsigned>(ctas)), S::THREADS,
+                         S::SMEM, cluster, stream, args);
 }
 
 template <bool NV> static cudaError_t launch_pair(Fp4Params& p, const Fp4Operands& o, const DeviceView& dv, cudaStream_t stream)
@@ -65,13 +59,67 @@ template <bool NV> static cudaError_t launch_pair(Fp4Params& p, const Fp4Operand
                          kFp4PairThreads, S::SMEM, 2, stream, args);
 }
 
+// What a call takes in each kernel, in cycles, by the parts of its time that were measured (GB300, 2.07 GHz), and with
+// it the choice of kernel, tile and cluster. Sizes only: the same call always takes the same one.
+//   - Before the first product and after the last 2500 to 3000 cycles pass in every wave of CTAs (pairs 9500).
+//   - A stage takes as long as its bytes (76 a cycle and SM), as its issue (400; pairs 600), or as a load's latency under
+//     load over the stages in flight (3600, so three stages of 32 tokens are slower than six of 64).
+//   - The weight comes from HBM at 3200 bytes a cycle at most.
+//   - CTAs that share a tile's k spend 1500 cycles on joining their sums, and 24 for every token they send.
+// Measured, in us, NVFP4, tokens x channels x k, tokens of a tile / CTAs that share its k:
+//   1 x 1024 x 4096: 16/8 2.9, 16/4 3.4, 16/1 6.7;  1 x 7168 x 8192: 16/2 9.0, 16/1 12.3
+//   24 x 7168 x 8192: 64/2 9.2, 32/2 10.3;  24 x 28672 x 8192: 32/1 23.4, 64/1 28.5
+//   128 x 1024 x 4096: 64/6 4.4, 128/6 5.2, pair 8.8;  128 x 7168 x 8192: 128/2 11.4, 64/1 12.9, pair 14.1
+//   128 x 28672 x 8192: pair 30.0, 128/1 33.5;  512 x 1024 x 4096: 64/2 6.5, pair 9.0;  512 x 7168 x 8192: pair 15.0, 128/1 27.0
+struct Fp4Plan {
+    long long cycles;
+    int tokens, cluster;              // tokens of a tile; 0: none yet
+};
+
+static long long most(long long a, long long b) { return a > b ? a : b; }
+
+static long long weight_cycles(const Fp4Params& p, bool nv) { return p.n * (p.k / 2 + p.k / (nv ? 16 : 32)) / 3200; }
+
+template <bool NV, int NT> static void plan_tile(const Fp4Params& p, const DeviceView& dv, Fp4Plan* best)
+{
+    using S = Fp4Shape<NV, NT>;
+    const void* fn = reinterpret_cast<const void*>(&rmsq_fp4_tile_kernel<NV, NT>);
+    const long long tiles = (p.n + kFp4Rows - 1) / kFp4Rows * ((p.m + NT - 1) / NT), slots = static_cast<long long>(dv.sms) * S::CTAS;
+    const int steps = (p.k + kFp4Step - 1) / kFp4Step, tokens = p.m < NT ? static_cast<int>(p.m) : NT;
+    for (int c = 1; c <= 8 && c <= steps && (c == 1 || c * tiles <= slots); ++c) {
+        if (c > 1 && c * fp4_share(tokens, c) > S::SUM_ROWS) continue;
+        const long long waves = (tiles * c + slots - 1) / slots, each = (tiles * c + dv.sms - 1) / dv.sms;   // CTAs of an SM
+        const long long stage = most(most(S::STAGE * (each < S::CTAS ? each : S::CTAS) / 76, 400), 3600 / S::STAGES);
+        const long long join = c > 1 ? 1500 + 24LL * tokens * (c - 1) / c : 8LL * tokens;
+        const long long cycles = (NT < 64 ? 2500 : 3000) * waves + most(waves * ((steps + c - 1) / c) * stage, weight_cycles(p, NV)) + join;
+        if (best->tokens != 0 && cycles >= best->cycles) continue;
+        // (what fits goes by the device's clusters of SMs, not by SMs alone)
+        if (c > 1 && tiles > resident_clusters(fn, S::THREADS, S::SMEM, c)) continue;
+        *best = {cycles, NT, c};
+    }
+}
+
 template <bool NV> static cudaError_t launch_fp4(Fp4Params& p, const Fp4Operands& o, const DeviceView& dv, cudaStream_t stream)
 {
-    if (p.m <= 16) return launch_tile<NV, 16>(p, o, dv, stream);
-    if (p.m <= 32) return launch_tile<NV, 32>(p, o, dv, stream);
-    if (p.m <= 64) return launch_tile<NV, 64>(p, o, dv, stream);
-    if (p.m <= 128) return launch_tile<NV, 128>(p, o, dv, stream);
-    return launch_pair<NV>(p, o, dv, stream);
+    Fp4Plan t = {0, 0, 0};
+    // (tiles of 16 and 32 tokens are for the only tile: the kernel says why)
+    if (p.m <= 16) plan_tile<NV, 16>(p, dv, &t);
+    else {
+        if (p.m <= 32) plan_tile<NV, 32>(p, dv, &t);
+        plan_tile<NV, 64>(p, dv, &t);
+        if (p.m > 64) plan_tile<NV, 128>(p, dv, &t);
+    }
+    if (p.m > 64) {
+        const long long tiles = (p.n + 2 * kFp4Rows - 1) / (2 * kFp4Rows) * ((p.m + kFp4PairTokens - 1) / kFp4PairTokens);
+        const long long waves = (tiles + dv.sms / 2 - 1) / (dv.sms / 2), steps = (p.k + kFp4Step - 1) / kFp4Step;
+        if (9500 + most(waves * steps * 600, weight_cycles(p, NV)) < t.cycles) return launch_pair<NV>(p, o, dv, stream);
+    }
+    switch (t.tokens) {
+    case 16: return launch_tile<NV, 16>(p, o, t.cluster, stream);
+    case 32: return launch_tile<NV, 32>(p, o, t.cluster, stream);
+    case 64: return launch_tile<NV, 64>(p, o, t.cluster, stream);
+    default: return launch_tile<NV, 128>(p, o, t.cluster, stream);
+    }
 }
 
 template <bool NV>

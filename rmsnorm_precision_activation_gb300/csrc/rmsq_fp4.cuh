@@ -9,8 +9,8 @@
 // memory and the tensor cores but TMA and that copy.
 //
 // A CTA takes 128 output channels (the MMA's rows) and NT tokens (its columns); with few tokens, CTAs of a cluster
-// share a tile's k. Each token's sums then go to one of them, which adds them up in rank order: a thread sends its value
-// straight into that CTA's shared memory, whose barrier counts the bytes (sums left in shared memory for others to read
+// share a tile's k. Each token's sums then go to one of them, which adds them up in rank order: threads send four tokens'
+// values at a time straight into that CTA's shared memory, whose barrier counts the bytes (sums left in shared memory for others to read
 // between two cluster barriers took 2 us, 3.5 at 128 tokens).
 //   warps 0-3 (0-7 from 64 tokens on)   read the accumulator and write the output (a lane is a channel: 32 neighbours
 //               of a token's row)
@@ -141,15 +141,17 @@ __device__ __forceinline__ void fp4_scales_cut(uint32_t weight, uint32_t tokens,
 }
 
 // A stage's MMAs: `quarters` of 64 elements have codes; a whole stage's four are issued without a test. a, b: low words of
-// the descriptors of the codes, which advance by 32 bytes an MMA.
+// the descriptors of the codes, which advance by 32 bytes an MMA. tokens_from: the column of the tokens' scales that the tile
+// starts at (a column holds 32 tokens').
 template <bool NV, int ROW_TILES, bool PAIR>
-__device__ __forceinline__ void fp4_mmas(uint32_t d, uint32_t a, uint32_t b, uint32_t scales, uint32_t idesc, int quarters, bool fresh)
+__device__ __forceinline__ void fp4_mmas(uint32_t d, uint32_t a, uint32_t b, uint32_t scales, uint32_t tokens_from, uint32_t idesc,
+                                         int quarters, bool fresh)
 {
     constexpr int T = fp4_tiles<NV>(), PER = 4 / T;                   // MMAs per tile of scales
     const auto mma = [&](int j) {
         const uint32_t id = j % PER * 2;                              // MXFP4: which two of a tile's four scales
         fp4_mma<NV, PAIR>(d, a + 2 * j, b + 2 * j, idesc | (id << 29) | (id << 4), scales + 4 * (j / PER),
-                          scales + 4 * (T + ROW_TILES * (j / PER)), j > 0 || !fresh);
+                          scales + 4 * (T + ROW_TILES * (j / PER)) + tokens_from, j > 0 || !fresh);
     };
     if (quarters >= 4) {
 #pragma unroll
@@ -320,6 +322,8 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
         }
     } else if (warp == ISSUER) {
         constexpr uint32_t idesc = fp4_idesc<NV>(kFp4Rows, NT);
+        // 0 or 2: an MMA takes the scales from even columns only, so tiles of fewer tokens are for the first alone
+        const uint32_t tokens_from = NT == 64 ? (static_cast<uint32_t>(tm) & 1u) * 2u : 0u;
         const bool one = elect_one();
         uint32_t slot = 0, phase = 0;
         for (int s = 0; s < steps; ++s) {
@@ -333,7 +337,8 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
             if (one) {
                 const uint32_t desc = fp4_desc(stage), scales = tmem + S::ACC + (s & 1) * S::COLS_S;
                 fp4_scales<NV, S::ROW_TILES, false>(desc + S::AT_SW / 16, desc + S::AT_SA / 16, scales);
-                fp4_mmas<NV, S::ROW_TILES, false>(tmem, desc, desc + S::AT_A / 16, scales, idesc, (left + 63) / 64, s == 0);
+                fp4_mmas<NV, S::ROW_TILES, false>(tmem, desc, desc + S::AT_A / 16, scales, tokens_from, idesc, (left + 63) / 64,
+                                                  s == 0);
                 tc_commit(empty + 8 * slot);
                 if (s == steps - 1) tc_commit(acc_full);
             }
@@ -361,28 +366,31 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
         const long long n = static_cast<long long>(tn) * kFp4Rows + row, m0 = static_cast<long long>(tm) * NT;
         const float fa = fp4_factor(p.a_gs), fw = fp4_factor(p.w_gs);
         const float bias = p.bias != nullptr && n < p.n ? load_as(p.bias, n, p.dt) : 0.f;
+        const int es = p.dt == DT_F32 ? 4 : 2;
         if (nc > 1) cluster_wait();
         ok = mbar_wait<SCOPE_CTA>(acc_full, 0, limit);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (ok) {
             tc_fence_after();
+            constexpr int COLS = NT / PARTS, LD = COLS < 32 ? COLS : 32;       // of a part, and of one read
+            // the CTA that adds up the next four tokens, and their place there
+            int to = part * (COLS / 4) / fours, at = part * (COLS / 4) - to * fours;
 #pragma unroll 1
-            for (int c = part * (NT / PARTS); c < (part + 1) * (NT / PARTS) && c < tokens; c += 16) {
-                uint32_t v[16];
+            for (int c = part * COLS; c < (part + 1) * COLS && c < tokens; c += LD) {
+                uint32_t v[LD];
                 tmem_ld_x16(acc + c, v);
+                if constexpr (LD == 32) tmem_ld_x16(acc + c + 16, v + 16);
                 tmem_wait_ld();
                 if (nc == 1) {
                     if (n < p.n) {
+                        char* out = static_cast<char*>(p.out) + ((m0 + c) * p.n + n) * es;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c + i < tokens)
-                                store_as(p.out, (m0 + c + i) * p.n + n, p.dt, fp4_value(__uint_as_float(v[i]), fa, fw, bias));
+                        for (int i = 0; i < LD; ++i, out += p.n * es)
+                            if (c + i < tokens) store_as(out, 0, p.dt, fp4_value(__uint_as_float(v[i]), fa, fw, bias));
                     }
                 } else {
-                    // each four tokens' sums to the CTA that adds them up
-                    int to = c / 4 / fours, at = c / 4 - to * fours;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
+                    for (int i = 0; i < LD / 4; ++i) {
                         if (c + 4 * i < tokens) {
                             const uint32_t addr = sums + ((rank * fours + at) * kFp4Rows + row) * 16;
                             if (to == static_cast<int>(rank)) st_shared_v4(addr, make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
@@ -402,21 +410,25 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                 ok = ok && mbar_wait<SCOPE_CLUSTER>(received, 0, limit);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (PARTS > 1) asm volatile("bar.sync 1, %0;" ::"n"(32 * S::READERS) : "memory");   // this CTA's own
+                const uint32_t stride = static_cast<uint32_t>(fours) * kFp4Rows * 16;
                 for (int i = part; ok && i < own_fours; i += PARTS) {
+                    uint4 o[8];
+#pragma unroll
+                    for (uint32_t r = 0; r < 8; ++r)
+                        o[r] = r < nc ? ld_shared_v4(sums + r * stride + (i * kFp4Rows + row) * 16) : make_uint4(0, 0, 0, 0);
                     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (uint32_t r = 0; r < nc; ++r) {
-                        const uint4 o = ld_shared_v4(sums + ((r * fours + i) * kFp4Rows + row) * 16);
-                        v.x += __uint_as_float(o.x);
-                        v.y += __uint_as_float(o.y);
-                        v.z += __uint_as_float(o.z);
-                        v.w += __uint_as_float(o.w);
+#pragma unroll
+                    for (uint32_t r = 0; r < 8; ++r) {
+                        v.x += __uint_as_float(o[r].x);
+                        v.y += __uint_as_float(o[r].y);
+                        v.z += __uint_as_float(o[r].z);
+                        v.w += __uint_as_float(o[r].w);
                     }
                     const float four[4] = {v.x, v.y, v.z, v.w};
-                    const long long m = m0 + static_cast<int>(rank) * per + 4 * i;
+                    char* const out = static_cast<char*>(p.out) + ((m0 + static_cast<int>(rank) * per + 4 * i) * p.n + n) * es;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (n < p.n && 4 * i + j < own) store_as(p.out, (m + j) * p.n + n, p.dt, fp4_value(four[j], fa, fw, bias));
+                        if (n < p.n && 4 * i + j < own) store_as(out + j * p.n * es, 0, p.dt, fp4_value(four[j], fa, fw, bias));
                 }
             }
         }

@@ -194,7 +194,7 @@ rmsq_fp4_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                         fp4_scales<NV, 2, true>(from, from + S::SCALES_W / 16, to);
                     tc_commit_pair(empty + 8 * before);
                     const uint32_t a = codes + slot * (S::CODES / 16);
-                    fp4_mmas<NV, 2, true>(acc, a, a + S::CODES_W / 16, to, idesc, (left + 63) / 64, left == p.k);
+                    fp4_mmas<NV, 2, true>(acc, a, a + S::CODES_W / 16, to, 0, idesc, (left + 63) / 64, left == p.k);
                     if (left <= kFp4Step) tc_commit_pair(acc_full + 8 * (done & 1u));
                 }
                 __syncwarp();
