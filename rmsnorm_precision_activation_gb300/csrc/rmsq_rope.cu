@@ -3,7 +3,6 @@
 #include <cmath>
 #include <cstdint>
 
-#include "rmsq_norm_bwd.cuh"
 #include "rmsq_ops.h"
 #include "rmsq_rope.cuh"
 
@@ -138,8 +137,9 @@ static rmsq_status prepare_rope(const RopeCall& c, RopeParams* p, int* vec)
     return RMSQ_OK;
 }
 
-// Lanes per row, and turns of rows that a warp takes on one token: as many as still leave every SM `warps`.
-static void deal_rope(RopeParams* p, int vec, bool neighbours, int sms, int warps, int most)
+// Lanes per row, turns that a warp takes of one token, and the CTAs: `ctas` on every SM at most, those of the queries and of
+// the keys by their turns. Fewer turns per item where there would be too few items for the warps.
+static unsigned deal_rope(RopeParams* p, int vec, bool neighbours, int sms, int ctas)
 {
     // a lane holds 8 pairs, in steps of a vector (neighbours: of a pair at least)
     const int step = neighbours ? (vec > 2 ? vec / 2 : 1) : vec;
@@ -147,10 +147,29 @@ static void deal_rope(RopeParams* p, int vec, bool neighbours, int sms, int warp
     p->lanes = 1;
     while (p->lanes < units) p->lanes *= 2;
     const int rows = 32 / p->lanes;
-    const long long turns = (p->side[0].heads + rows - 1) / rows + (p->side[1].heads + rows - 1) / rows;
-    p->run = most;
-    while (p->run > 1 && p->tokens * turns / p->run < static_cast<long long>(sms) * warps) p->run /= 2;
-    for (RopeSide& s : p->side) s.items = (s.heads + rows * p->run - 1) / (rows * p->run);
+    for (RopeSide& s : p->side) s.turns = (s.heads + rows - 1) / rows;
+    const long long turns[2] = {p->tokens * p->side[0].turns, p->tokens * p->side[1].turns};
+    const long long warps = static_cast<long long>(sms) * ctas * kRopeWarps;
+    p->run = 8;
+    while (p->run > 1 && (turns[0] + turns[1]) / p->run < 4 * warps) p->run /= 2;
+    for (RopeSide& s : p->side) s.items = (s.turns + p->run - 1) / p->run;
+    // CTAs that leave no warp without an item
+    const auto all = [&](int s) {
+        const long long n = (p->tokens * p->side[s].items + kRopeWarps - 1) / kRopeWarps;
+        return n < sms * ctas ? n : sms * ctas;
+    };
+    const long long total = static_cast<long long>(sms) * ctas;
+    long long q = all(0), k = all(1);
+    if (q + k > total) {
+        const long long share = (total * turns[0] + (turns[0] + turns[1]) / 2) / (turns[0] + turns[1]);
+        long long nq = share < 1 ? 1 : share > total - 1 ? total - 1 : share;
+        if (nq > q) nq = q;
+        if (total - nq > k) nq = total - k;
+        q = nq;
+        k = total - nq;
+    }
+    p->split = static_cast<int>(q);
+    return static_cast<unsigned>(q + k);
 }
 
 static const void* rope_kernel(int dtype, int vec, bool neighbours, bool backward)
@@ -167,8 +186,16 @@ static rmsq_status status_of(cudaError_t e)
     return RMSQ_ERR_LAUNCH;
 }
 
-// Partial rows of the gammas' gradients: one per CTA.
-static int64_t rope_parts(int64_t tokens) { return tokens < RMSQ_ROPE_PARTS ? tokens : RMSQ_ROPE_PARTS; }
+// CTAs on an SM, by the shared memory and registers of the kernels, and their shared memory.
+static int rope_ctas(int dtype, int vec, bool backward)
+{
+    return backward ? (dtype == RMSQ_F32 ? 1 : 2) : dtype == RMSQ_F32 || vec < 8 ? 2 : 3;
+}
+static int rope_smem(int dtype, bool backward)
+{
+    return (dtype == RMSQ_F32 ? (backward ? RopeStages<DT_F32, true>::N * 128 : RopeStages<DT_F32, false>::N * 64)
+                              : (backward ? RopeStages<DT_BF16, true>::N * 64 : RopeStages<DT_BF16, false>::N * 32)) * kRopeThreads;
+}
 
 }  // namespace rmsq
 
@@ -187,19 +214,16 @@ extern "C" rmsq_status rmsnorm_rope(const rmsq_heads* query, const rmsq_heads* k
     DeviceView dv;
     if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
     const bool neighbours = rotation->neighbours != 0;
-    deal_rope(&p, vec, neighbours, dv.sms, 16, 8);
-    const long long items = tokens * (static_cast<long long>(p.side[0].items) + p.side[1].items);
-    const long long grid = (items + kRopeWarps - 1) / kRopeWarps;
-    if (grid > INT32_MAX) return RMSQ_ERR_SHAPE;
+    const unsigned grid = deal_rope(&p, vec, neighbours, dv.sms, rope_ctas(dtype, vec, false));
     void* args[] = {&p};
-    return status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, false), dim3(static_cast<unsigned>(grid)), kRopeWarps * 32,
-                                   0, 1, static_cast<cudaStream_t>(stream), args));
+    return status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, false), dim3(grid), kRopeThreads, rope_smem(dtype, false), 1,
+                                   static_cast<cudaStream_t>(stream), args));
 }
 
 extern "C" int64_t rmsnorm_rope_backward_workspace(int64_t tokens, int64_t dim)
 {
     if (tokens <= 0 || dim <= 0 || dim > RMSQ_ROPE_MAX_DIM) return 0;
-    return rope_parts(tokens) * 2 * dim * static_cast<int64_t>(sizeof(float));
+    return RMSQ_ROPE_PARTS * dim * static_cast<int64_t>(sizeof(float));
 }
 
 extern "C" rmsq_status rmsnorm_rope_backward(const rmsq_heads* grad_query, const rmsq_heads* grad_key,
@@ -235,26 +259,27 @@ extern "C" rmsq_status rmsnorm_rope_backward(const rmsq_heads* grad_query, const
     }
     DeviceView dv;
     if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
-    NormBwdReduceParams r = {};
+    RopeReduceParams r = {};
     r.part = static_cast<const float*>(workspace);
-    r.dgamma = grad_query_gamma;
-    r.dbeta = grad_key_gamma;
-    r.hidden = static_cast<int>(dim);
+    r.out[0] = grad_query_gamma;
+    r.out[1] = grad_key_gamma;
+    r.dim = static_cast<int>(dim);
     r.dt = param_grad_dtype;
     if (tokens > 0) {
         const bool neighbours = rotation->neighbours != 0;
-        deal_rope(&p, vec, neighbours, dv.sms, 16, 8);
+        int ctas = rope_ctas(dtype, vec, true);
+        while (dv.sms * ctas > RMSQ_ROPE_PARTS) --ctas;
+        if (ctas < 1) return RMSQ_ERR_LAUNCH;
+        const unsigned grid = deal_rope(&p, vec, neighbours, dv.sms, ctas);
         p.part = static_cast<float*>(workspace);
-        const long long most = p.side[0].items > p.side[1].items ? p.side[0].items : p.side[1].items;
-        long long grid = (tokens * most + kRopeWarps - 1) / kRopeWarps;
-        if (grid > rope_parts(tokens)) grid = rope_parts(tokens);
-        r.parts = static_cast<int>(grid);
+        r.rows[0] = p.split;
+        r.rows[1] = static_cast<int>(grid) - p.split;
         void* args[] = {&p};
-        st = status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, true), dim3(static_cast<unsigned>(grid)),
-                                     kRopeWarps * 32, 0, 1, static_cast<cudaStream_t>(stream), args));
+        st = status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, true), dim3(grid), kRopeThreads, rope_smem(dtype, true), 1,
+                                     static_cast<cudaStream_t>(stream), args));
         if (st != RMSQ_OK) return st;
     }
     void* args[] = {&r};
-    return status_of(launch_kernel(norm_bwd_reduce_fn(), dim3(static_cast<unsigned>((2 * dim + 31) / 32)), 512, 0, 1,
-                                   static_cast<cudaStream_t>(stream), args));
+    return status_of(launch_kernel(reinterpret_cast<const void*>(&rmsq_rope_reduce_kernel),
+                                   dim3(static_cast<unsigned>((dim + 31) / 32), 2), 1024, 0, 1, static_cast<cudaStream_t>(stream), args));
 }
