@@ -137,9 +137,9 @@ static rmsq_status prepare_rope(const RopeCall& c, RopeParams* p, int* vec)
     return RMSQ_OK;
 }
 
-// Lanes per row, turns that a warp takes of one token, and the CTAs: `ctas` on every SM at most, those of the queries and of
-// the keys by their turns. Fewer turns per item where there would be too few items for the warps.
-static unsigned deal_rope(RopeParams* p, int vec, bool neighbours, int sms, int ctas)
+// Lanes per row, turns that a warp takes of one token, and the CTAs: `most` at most, those of the queries and of the keys by
+// their turns, and no more than have an item for every warp. Fewer turns per item where there would be too few items.
+static unsigned deal_rope(RopeParams* p, int vec, bool neighbours, long long most, int warps)
 {
     // a lane holds 8 pairs, in steps of a vector (neighbours: of a pair at least)
     const int step = neighbours ? (vec > 2 ? vec / 2 : 1) : vec;
@@ -147,29 +147,25 @@ static unsigned deal_rope(RopeParams* p, int vec, bool neighbours, int sms, int 
     p->lanes = 1;
     while (p->lanes < units) p->lanes *= 2;
     const int rows = 32 / p->lanes;
-    for (RopeSide& s : p->side) s.turns = (s.heads + rows - 1) / rows;
-    const long long turns[2] = {p->tokens * p->side[0].turns, p->tokens * p->side[1].turns};
-    const long long warps = static_cast<long long>(sms) * ctas * kRopeWarps;
-    p->run = 8;
-    while (p->run > 1 && (turns[0] + turns[1]) / p->run < 4 * warps) p->run /= 2;
-    for (RopeSide& s : p->side) s.items = (s.turns + p->run - 1) / p->run;
-    // CTAs that leave no warp without an item
-    const auto all = [&](int s) {
-        const long long n = (p->tokens * p->side[s].items + kRopeWarps - 1) / kRopeWarps;
-        return n < sms * ctas ? n : sms * ctas;
-    };
-    const long long total = static_cast<long long>(sms) * ctas;
-    long long q = all(0), k = all(1);
-    if (q + k > total) {
-        const long long share = (total * turns[0] + (turns[0] + turns[1]) / 2) / (turns[0] + turns[1]);
-        long long nq = share < 1 ? 1 : share > total - 1 ? total - 1 : share;
-        if (nq > q) nq = q;
-        if (total - nq > k) nq = total - k;
-        q = nq;
-        k = total - nq;
+    for (RopeSide& s : p->side) s.turns = (s.heads + kRopeRows * rows - 1) / (kRopeRows * rows);
+    const long long turns[2] = {p->tokens * p->side[0].turns, p->tokens * p->side[1].turns}, all = turns[0] + turns[1];
+    p->run = 4;
+    while (p->run > 1 && all / p->run < 4 * most * warps) p->run /= 2;
+    long long need[2];
+    for (int s = 0; s < 2; ++s) {
+        p->side[s].items = (p->side[s].turns + p->run - 1) / p->run;
+        need[s] = (p->tokens * p->side[s].items + warps - 1) / warps;
+    }
+    long long q = need[0];
+    if (need[0] + need[1] > most) {
+        q = (most * turns[0] + all / 2) / all;
+        q = q < 1 ? 1 : q > most - 1 ? most - 1 : q;
+        if (q > need[0]) q = need[0];
+        if (q < most - need[1]) q = most - need[1];
+        need[1] = most - q;
     }
     p->split = static_cast<int>(q);
-    return static_cast<unsigned>(q + k);
+    return static_cast<unsigned>(q + need[1]);
 }
 
 static const void* rope_kernel(int dtype, int vec, bool neighbours, bool backward)
@@ -186,15 +182,11 @@ static rmsq_status status_of(cudaError_t e)
     return RMSQ_ERR_LAUNCH;
 }
 
-// CTAs on an SM, by the shared memory and registers of the kernels, and their shared memory.
-static int rope_ctas(int dtype, int vec, bool backward)
+template <bool BACKWARD> static int rope_smem(const RopeParams& p, int dtype)
 {
-    return backward ? (dtype == RMSQ_F32 ? 1 : 2) : dtype == RMSQ_F32 || vec < 8 ? 2 : 3;
-}
-static int rope_smem(int dtype, bool backward)
-{
-    return (dtype == RMSQ_F32 ? (backward ? RopeStages<DT_F32, true>::N * 128 : RopeStages<DT_F32, false>::N * 64)
-                              : (backward ? RopeStages<DT_BF16, true>::N * 64 : RopeStages<DT_BF16, false>::N * 32)) * kRopeThreads;
+    using S = RopeShape<BACKWARD>;
+    return S::STAGES * 16 * (dtype == RMSQ_F32 ? 4 : 2) * S::THREADS * kRopeRows * (BACKWARD ? 2 : 1) +
+           S::THREADS / 32 * RopeAngles<S::STAGES>::bytes(p.half) + (p.dim + 3) / 4 * 16;
 }
 
 }  // namespace rmsq
@@ -214,9 +206,10 @@ extern "C" rmsq_status rmsnorm_rope(const rmsq_heads* query, const rmsq_heads* k
     DeviceView dv;
     if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
     const bool neighbours = rotation->neighbours != 0;
-    const unsigned grid = deal_rope(&p, vec, neighbours, dv.sms, rope_ctas(dtype, vec, false));
+    using S = RopeShape<false>;
+    const unsigned grid = deal_rope(&p, vec, neighbours, dv.sms * S::CTAS, S::THREADS / 32);
     void* args[] = {&p};
-    return status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, false), dim3(grid), kRopeThreads, rope_smem(dtype, false), 1,
+    return status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, false), dim3(grid), S::THREADS, rope_smem<false>(p, dtype), 1,
                                    static_cast<cudaStream_t>(stream), args));
 }
 
@@ -267,15 +260,14 @@ extern "C" rmsq_status rmsnorm_rope_backward(const rmsq_heads* grad_query, const
     r.dt = param_grad_dtype;
     if (tokens > 0) {
         const bool neighbours = rotation->neighbours != 0;
-        int ctas = rope_ctas(dtype, vec, true);
-        while (dv.sms * ctas > RMSQ_ROPE_PARTS) --ctas;
-        if (ctas < 1) return RMSQ_ERR_LAUNCH;
-        const unsigned grid = deal_rope(&p, vec, neighbours, dv.sms, ctas);
+        using S = RopeShape<true>;
+        const int ctas = dv.sms * S::CTAS < RMSQ_ROPE_PARTS ? dv.sms * S::CTAS : RMSQ_ROPE_PARTS;
+        const unsigned grid = deal_rope(&p, vec, neighbours, ctas, S::THREADS / 32);
         p.part = static_cast<float*>(workspace);
         r.rows[0] = p.split;
         r.rows[1] = static_cast<int>(grid) - p.split;
         void* args[] = {&p};
-        st = status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, true), dim3(grid), kRopeThreads, rope_smem(dtype, true), 1,
+        st = status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, true), dim3(grid), S::THREADS, rope_smem<true>(p, dtype), 1,
                                      static_cast<cudaStream_t>(stream), args));
         if (st != RMSQ_OK) return st;
     }

@@ -159,41 +159,48 @@ template <int DT, int V> struct RopeVec {
     }
 };
 
-constexpr int kRopeWarps = 8, kRopeThreads = 32 * kRopeWarps;
+// Threads of a CTA and CTAs on an SM: 16 warps of 128 registers a thread, backward 12 of 168 (16 of 128 spill: 138 us,
+// 16384 tokens of 40 heads of 128 in bf16, against 84). Two slots in a ring, one turn ahead: deeper rings are slower (forward 59.2 us
+// with 2, 61.0 with 3, 65.6 with 4; backward 84.3 and 93.1), as if reads and writes got into each other's way in HBM.
+template <bool BACKWARD> struct RopeShape {
+    static constexpr int THREADS = BACKWARD ? 192 : 128, CTAS = BACKWARD ? 2 : 4, STAGES = 2;
+};
 
-// A lane's rings: TENSORS rows of 16 elements in each of STAGES slots, vector i of thread t at (i * threads + t) vectors.
-template <int DT, int V, bool INTER, int TENSORS, int STAGES> struct RopeRing {
+// A lane's ring: ROWS rows of 16 elements in each of STAGES slots, vector i of thread t at (i * threads + t) vectors. Where
+// a lane has no elements its slots stay zero; where it has no row they keep what an earlier row left.
+template <int DT, int V, bool INTER, int ROWS, int STAGES, int THREADS> struct RopeRing {
     using Vec = RopeVec<DT, V>;
     using Lane = RopeLane<V, INTER>;
-    static constexpr int ES = DT == DT_F32 ? 4 : 2, ROW = 16 * ES * kRopeThreads, BYTES = TENSORS * STAGES * ROW;
+    static constexpr int ES = DT == DT_F32 ? 4 : 2, ROW = 16 * ES * THREADS, BYTES = ROWS * STAGES * ROW;
     uint32_t base;
 
-    __device__ __forceinline__ uint32_t at(int stage, int tensor, int i) const
+    __device__ __forceinline__ uint32_t at(int stage, int row, int i) const
     {
-        return base + static_cast<uint32_t>((stage * TENSORS + tensor) * ROW + (i * kRopeThreads) * Vec::BYTES);
+        return base + static_cast<uint32_t>((stage * ROWS + row) * ROW + (i * THREADS) * Vec::BYTES);
     }
-    // Starts the copies of a row (in: the lane has one).
-    __device__ __forceinline__ void fetch(int stage, int tensor, const char* row, const Lane& lane, bool in) const
+    __device__ __forceinline__ void clear() const
+    {
+        for (uint32_t i = threadIdx.x * 16; i < BYTES; i += THREADS * 16) st_shared_v4(base + i, make_uint4(0, 0, 0, 0));
+    }
+    // Starts the copies of a row.
+    __device__ __forceinline__ void fetch(int stage, int row, const char* from, const Lane& lane) const
     {
 #pragma unroll
         for (int i = 0; i < Lane::NV; ++i)
-            if (in && lane.at[i] >= 0) Vec::copy(at(stage, tensor, i), row + static_cast<long long>(lane.at[i]) * ES);
+            if (lane.at[i] >= 0) Vec::copy(at(stage, row, i), from + static_cast<long long>(lane.at[i]) * ES);
     }
-    // Zeros where the lane has nothing.
-    __device__ __forceinline__ void get(int stage, int tensor, const Lane& lane, bool in, float (&f)[16]) const
+    __device__ __forceinline__ void get(int stage, int row, float (&f)[16]) const
     {
 #pragma unroll
         for (int i = 0; i < Lane::NV; ++i) {
             uint32_t w[Vec::W];
-#pragma unroll
-            for (int j = 0; j < Vec::W; ++j) w[j] = 0;
-            if (in && lane.at[i] >= 0) Vec::get(at(stage, tensor, i), w);
+            Vec::get(at(stage, row, i), w);
             Vec::unpack(w, f + i * V);
         }
     }
 };
 
-// A row to memory, and gamma from it.
+// A row to memory.
 template <int DT, int V, bool INTER>
 __device__ __forceinline__ void rope_store(char* row, const RopeLane<V, INTER>& lane, const float (&f)[16])
 {
@@ -202,31 +209,48 @@ __device__ __forceinline__ void rope_store(char* row, const RopeLane<V, INTER>& 
         if (lane.at[i] >= 0) RopeVec<DT, V>::store(row + static_cast<long long>(lane.at[i]) * (DT == DT_F32 ? 4 : 2), f + i * V);
 }
 
-template <int DT, int V, bool INTER>
-__device__ __forceinline__ void rope_gamma(const void* gamma, const RopeLane<V, INTER>& lane, float offset, float (&g)[16])
+// L floats from shared memory.
+template <int L> __device__ __forceinline__ void rope_read(uint32_t from, float* f)
 {
-#pragma unroll
-    for (int i = 0; i < RopeLane<V, INTER>::NV; ++i) {
-        uint32_t w[RopeVec<DT, V>::W];
-#pragma unroll
-        for (int j = 0; j < RopeVec<DT, V>::W; ++j) w[j] = 0;
-        if (lane.at[i] >= 0)
-            RopeVec<DT, V>::load(static_cast<const char*>(gamma) + static_cast<long long>(lane.at[i]) * (DT == DT_F32 ? 4 : 2), w);
-        RopeVec<DT, V>::unpack(w, g + i * V);
-    }
-#pragma unroll
-    for (int j = 0; j < 16; ++j) g[j] += offset;
+    if constexpr (L == 4)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3]) : "r"(from) : "memory");
+    else if constexpr (L == 2)
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f[0]), "=f"(f[1]) : "r"(from) : "memory");
+    else
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f[0]) : "r"(from) : "memory");
 }
 
+// gamma + offset in fp32, a CTA's together: registers go to the rows instead.
+template <int DT> struct RopeGamma {
+    uint32_t base;
+    __device__ __forceinline__ void load(const void* gamma, int dim, float offset) const
+    {
+        for (int i = threadIdx.x; i < dim; i += blockDim.x) {
+            const float v = Scalar<DT>::get(static_cast<const typename Scalar<DT>::T*>(gamma)[i]) + offset;
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + i * 4), "f"(v) : "memory");
+        }
+    }
+    template <int V, bool INTER> __device__ __forceinline__ void get(const RopeLane<V, INTER>& lane, float (&g)[16]) const
+    {
+        constexpr int L = V < 4 ? V : 4;
+#pragma unroll
+        for (int i = 0; i < RopeLane<V, INTER>::NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; j += L) rope_read<L>(base + (max(lane.at[i], 0) + j) * 4, g + i * V + j);
+    }
+};
+
 // The turns of a warp, one after another: items w, w + W, ... of a side's tokens * items, each of up to `run` turns of
-// `rows` heads of one token.
+// kRopeRows * rows heads of one token (a lane has heads `rows` apart).
+constexpr int kRopeRows = 2;
+
 struct RopeCursor {
     long long t;
     int item, left, head;            // within the token; turns left of the item; this lane's head
     __device__ __forceinline__ void enter(const RopeParams& p, const RopeSide& sd, int rows, int mine)
     {
         left = min(p.run, sd.turns - item * p.run);
-        head = item * p.run * rows + mine;
+        head = item * p.run * kRopeRows * rows + mine;
     }
     __device__ __forceinline__ void start(const RopeParams& p, const RopeSide& sd, int rows, int mine, int w)
     {
@@ -237,7 +261,7 @@ struct RopeCursor {
     // dt, di: the warps' stride in items, as tokens and items. True where an item begins.
     __device__ __forceinline__ bool next(const RopeParams& p, const RopeSide& sd, int rows, int mine, int dt, int di)
     {
-        head += rows;
+        head += kRopeRows * rows;
         if (--left > 0) return false;
         t += dt;
         item += di;
@@ -259,68 +283,90 @@ struct RopeAt {
     }
 };
 
-__device__ __forceinline__ long long rope_place(const RopeParams& p, int axis, long long t)
-{
-    const long long i = axis * p.tokens + t;
-    return p.wide ? static_cast<const long long*>(p.positions)[i] : static_cast<const int*>(p.positions)[i];
-}
+// A warp's cosines and sines, [slot][cosines, then sines][half]: those of the items whose rows are in the ring, so as many slots
+// as that. The warp copies a token's row of both tables together, when it starts on the rows of its first turn. Lane a
+// holds the token's place on axis a, read an item before it is needed.
+template <int STAGES> struct RopeAngles {
+    uint32_t base;                       // this warp's
+    long long place;
+    int ahead = 0, now = 0;              // slots
 
-// Cosines and sines of the lane's 8 pairs for token t. A place outside the table reads nothing and gives NaN.
-template <int V, bool INTER>
-__device__ __forceinline__ void rope_angles(const RopeParams& p, const RopeLane<V, INTER>& lane, long long t,
-                                            float (&c)[8], float (&s)[8])
-{
-    using Lane = RopeLane<V, INTER>;
-    constexpr int PV = !INTER ? V : V > 2 ? V / 2 : 1, N = 8 / PV;     // pairs read together
-    const float nan = __int_as_float(0x7FFFFFFF);
-    const long long place0 = rope_place(p, 0, t);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int q = lane.pair[Lane::of(i * PV)];
-#pragma unroll
-        for (int j = 0; j < PV; ++j) {
-            c[i * PV + j] = nan;
-            s[i * PV + j] = nan;
-        }
-        if (q < 0) continue;
-        if (p.axes == 1) {
-            if (place0 < 0 || place0 >= p.places) continue;
-            const float* const cr = p.cos + place0 * p.half + q;
-            const float* const sr = p.sin + place0 * p.half + q;
-            if (PV % 4 == 0 && p.vec_table) {
-#pragma unroll
-                for (int j = 0; j < PV; j += 4) {
-                    const float4 a = __ldg(reinterpret_cast<const float4*>(cr + j));
-                    const float4 b = __ldg(reinterpret_cast<const float4*>(sr + j));
-                    c[i * PV + j] = a.x, c[i * PV + j + 1] = a.y, c[i * PV + j + 2] = a.z, c[i * PV + j + 3] = a.w;
-                    s[i * PV + j] = b.x, s[i * PV + j + 1] = b.y, s[i * PV + j + 2] = b.z, s[i * PV + j + 3] = b.w;
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < PV; ++j) {
-                    c[i * PV + j] = __ldg(cr + j);
-                    s[i * PV + j] = __ldg(sr + j);
-                }
+    static __host__ __device__ constexpr int bytes(int half) { return STAGES * 2 * ((half + 3) / 4 * 4) * 4; }
+    __device__ __forceinline__ uint32_t at(const RopeParams& p, int slot, int sine) const
+    {
+        return base + static_cast<uint32_t>((slot * 2 + sine) * ((p.half + 3) / 4 * 4) * 4);
+    }
+    __device__ __forceinline__ void look(const RopeParams& p, long long t)
+    {
+        const int lane = threadIdx.x & 31;
+        if (lane >= p.axes || t >= p.tokens) return;
+        const long long i = lane * p.tokens + t;
+        place = p.wide ? static_cast<const long long*>(p.positions)[i] : static_cast<const int*>(p.positions)[i];
+    }
+    // Starts the copies for the item whose token look() was given. A place outside the table reads nothing and gives NaN.
+    __device__ __forceinline__ void fetch(const RopeParams& p)
+    {
+        const int lane = threadIdx.x & 31;
+        const uint32_t c = at(p, ahead, 0), s = at(p, ahead, 1);
+        if (p.axes == 1 && p.vec_table) {
+            const long long row = __shfl_sync(0xFFFFFFFFu, place, 0);
+            const bool in = row >= 0 && row < p.places;
+            for (int i = lane; i < p.half / 2; i += 32) {                 // the cosines' vectors, then the sines'
+                const int sine = i >= p.half / 4, v = 4 * (i - sine * (p.half / 4));
+                const uint32_t to = (sine ? s : c) + v * 4;
+                if (in)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"((sine ? p.sin : p.cos) + row * p.half + v) : "memory");
+                else
+                    st_shared_v4(to, make_uint4(0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu, 0x7FFFFFFFu));
             }
         } else {
-#pragma unroll
-            for (int j = 0; j < PV; ++j) {
+            for (int i0 = 0; i0 < p.half; i0 += 32) {
+                const int i = i0 + lane;
                 int axis = 0;
 #pragma unroll
-                for (int a = 0; a < kRopeAxes - 1; ++a) axis += q + j >= p.until[a];
-                const long long place = axis == 0 ? place0 : rope_place(p, axis, t);
-                if (place < 0 || place >= p.places) continue;
-                c[i * PV + j] = __ldg(p.cos + place * p.half + q + j);
-                s[i * PV + j] = __ldg(p.sin + place * p.half + q + j);
+                for (int a = 0; a < kRopeAxes - 1; ++a) axis += i >= p.until[a];
+                const long long row = __shfl_sync(0xFFFFFFFFu, place, axis);
+                if (i >= p.half) continue;
+                if (row >= 0 && row < p.places) {
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(c + i * 4), "l"(p.cos + row * p.half + i) : "memory");
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(s + i * 4), "l"(p.sin + row * p.half + i) : "memory");
+                } else {
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(c + i * 4), "r"(0x7FFFFFFFu) : "memory");
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(s + i * 4), "r"(0x7FFFFFFFu) : "memory");
+                }
+            }
+        }
+        if (++ahead == STAGES) ahead = 0;
+    }
+    // Cosines and sines of the lane's 8 pairs (any where it has none).
+    template <int V, bool INTER>
+    __device__ __forceinline__ void get(const RopeParams& p, const RopeLane<V, INTER>& lane, float (&c)[8], float (&s)[8]) const
+    {
+        using Lane = RopeLane<V, INTER>;
+        constexpr int PV = !INTER ? V : V > 2 ? V / 2 : 1, N = 8 / PV, L = PV < 4 ? PV : 4;     // pairs together; floats of a read
+        const uint32_t ca = at(p, now, 0), sa = at(p, now, 1);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int q = max(lane.pair[Lane::of(i * PV)], 0);
+#pragma unroll
+            for (int j = 0; j < PV; j += L) {
+                rope_read<L>(ca + (q + j) * 4, c + i * PV + j);
+                rope_read<L>(sa + (q + j) * 4, s + i * PV + j);
             }
         }
     }
-}
+    __device__ __forceinline__ void pass() { if (++now == STAGES) now = 0; }
+};
 
-__device__ __forceinline__ float rope_row_sum(float v, int lanes)
+// Sums over the lanes of a row, of every row of a lane.
+__device__ __forceinline__ void rope_row_sums(float (&v)[2], int lanes)
 {
-    for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        if (o >= lanes) continue;
+        v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+        v[1] += __shfl_xor_sync(0xFFFFFFFFu, v[1], o);
+    }
 }
 
 __device__ __forceinline__ float rope_rstd(float squares, const RopeParams& p) { return rsqrtf(fmaf(squares, p.inv_dim, p.eps)); }
@@ -356,24 +402,25 @@ __device__ __forceinline__ void rope_turn(float (&f)[16], const RopeLane<V, INTE
     }
 }
 
-// Slots of the rings: 64 KB a CTA, of which two or three run on an SM (32-bit gradients: 128 KB, one).
-template <int DT, bool BACKWARD> struct RopeStages {
-    static constexpr int N = DT != DT_F32 && !BACKWARD ? 8 : 4;
-};
-
-// What the kernels do with a side's turns: fetch several ahead, then body(stage, cursor, an item begins, the lane has a row).
-// fetch(stage, cursor, an item begins, the lane has a row) starts the copies.
+// What the kernels do with a side's turns: fetch(stage, cursor, an item begins) starts the copies several turns ahead of
+// body(stage, cursor, an item begins); the angles of body's item are there.
 template <int STAGES, class Fetch, class Body>
-__device__ __forceinline__ void rope_turns(const RopeParams& p, const RopeSide& sd, int rows, int mine, int w, int W, Fetch fetch, Body body)
+__device__ __forceinline__ void rope_turns(const RopeParams& p, const RopeSide& sd, int rows, int mine, int w, int W,
+                                           RopeAngles<STAGES>& angles, Fetch fetch, Body body)
 {
     const int dt = W / sd.items, di = W - dt * sd.items;
     RopeCursor ahead, now;
     ahead.start(p, sd, rows, mine, w);
     now = ahead;
     bool begins = true, begins_ahead = true;
+    angles.look(p, ahead.t);
     const auto bring = [&](int stage) {
         if (ahead.t < p.tokens) {
-            fetch(stage, ahead, begins_ahead, ahead.head < sd.heads);
+            if (begins_ahead) {
+                angles.fetch(p);
+                angles.look(p, ahead.t + dt + (ahead.item + di >= sd.items));
+            }
+            fetch(stage, ahead, begins_ahead);
             begins_ahead = ahead.next(p, sd, rows, mine, dt, di);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -383,66 +430,26 @@ __device__ __forceinline__ void rope_turns(const RopeParams& p, const RopeSide& 
     int stage = 0;
 #pragma unroll 1
     while (now.t < p.tokens) {
-        bring((stage + STAGES - 1) & (STAGES - 1));
+        bring(stage == 0 ? STAGES - 1 : stage - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-        body(stage, now, begins, now.head < sd.heads);
+        __syncwarp();                                     // the angles are the warp's together
+        body(stage, now, begins);
         begins = now.next(p, sd, rows, mine, dt, di);
-        stage = (stage + 1) & (STAGES - 1);
+        if (begins) angles.pass();
+        __syncwarp();
+        if (++stage == STAGES) stage = 0;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
+// Two rows of a lane at a time: two chains of dependent instructions in flight, and half the bookkeeping.
 template <int DT, int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, DT == DT_F32 || V < 8 ? 2 : 3) rmsq_rope_kernel(const __grid_constant__ RopeParams p)
+__global__ void __launch_bounds__(RopeShape<false>::THREADS, RopeShape<false>::CTAS) rmsq_rope_kernel(const __grid_constant__ RopeParams p)
 {
     using Lane = RopeLane<V, INTER>;
-    constexpr int STAGES = RopeStages<DT, false>::N;
-    using Ring = RopeRing<DT, V, INTER, 1, STAGES>;
-    extern __shared__ __align__(16) unsigned char smem[];
-    const int l = threadIdx.x & (p.lanes - 1), rows = 32 / p.lanes, mine = (threadIdx.x & 31) / p.lanes;
-    const bool key = static_cast<int>(blockIdx.x) >= p.split;
-    const RopeSide& sd = p.side[key];
-    const int cta = static_cast<int>(blockIdx.x) - (key ? p.split : 0), ctas = key ? static_cast<int>(gridDim.x) - p.split : p.split;
-    Lane lane;
-    lane.init(l, p.lanes, p.dim, p.half);
-    const Ring ring = {smem_u32(smem)};
-    pdl_wait();
-    float cs[8], sn[8], g[16];
-    rope_gamma<DT, V, INTER>(sd.gamma, lane, p.offset, g);
-    RopeAt x, y;
-    const long long xs = rows * sd.xh * Ring::ES, ys = rows * sd.oh * Ring::ES;          // a turn's heads on
-    rope_turns<STAGES>(
-        p, sd, rows, mine, cta * kRopeWarps + (threadIdx.x >> 5), ctas * kRopeWarps,
-        [&](int stage, const RopeCursor& c, bool begins, bool in) {
-            if (begins) x.enter(sd.x, c.t, sd.xt, c.head, sd.xh, Ring::ES);
-            ring.fetch(stage, 0, x.p, lane, in);
-            x.p += xs;
-        },
-        [&](int stage, const RopeCursor& c, bool begins, bool in) {
-            if (begins) {
-                rope_angles<V, INTER>(p, lane, c.t, cs, sn);
-                y.enter(sd.out, c.t, sd.ot, c.head, sd.oh, Ring::ES);
-            }
-            float f[16];
-            ring.get(stage, 0, lane, in, f);
-            const float2 rstd = splat(rope_rstd(rope_row_sum(rope_dot(f, f), p.lanes), p));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) rope_put(f, j, mul2(mul2(rope_two(f, j), rstd), rope_two(g, j)));
-            rope_turn<false>(f, lane, cs, sn);
-            if (in) rope_store<DT, V, INTER>(const_cast<char*>(y.p), lane, f);
-            y.p += ys;
-        });
-}
-
-// A lane has the same elements in every row and adds their part of gamma's gradient in registers. The row groups of a warp
-// are joined by exchanges, the warps of a CTA through shared memory, the CTAs by rmsq_rope_reduce_kernel, all in a
-// fixed order.
-template <int DT, int V, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads, DT == DT_F32 ? 1 : 2) rmsq_rope_bwd_kernel(const __grid_constant__ RopeParams p)
-{
-    using Lane = RopeLane<V, INTER>;
-    constexpr int STAGES = RopeStages<DT, true>::N;
-    using Ring = RopeRing<DT, V, INTER, 2, STAGES>;
+    using Shape = RopeShape<false>;
+    constexpr int STAGES = Shape::STAGES, WARPS = Shape::THREADS / 32, R = kRopeRows;
+    using Ring = RopeRing<DT, V, INTER, R, STAGES, Shape::THREADS>;
     extern __shared__ __align__(16) unsigned char smem[];
     const int l = threadIdx.x & (p.lanes - 1), rows = 32 / p.lanes, mine = (threadIdx.x & 31) / p.lanes, warp = threadIdx.x >> 5;
     const bool key = static_cast<int>(blockIdx.x) >= p.split;
@@ -451,48 +458,140 @@ __global__ void __launch_bounds__(kRopeThreads, DT == DT_F32 ? 1 : 2) rmsq_rope_
     Lane lane;
     lane.init(l, p.lanes, p.dim, p.half);
     const Ring ring = {smem_u32(smem)};
+    RopeAngles<STAGES> angles;
+    angles.base = smem_u32(smem) + Ring::BYTES + warp * RopeAngles<STAGES>::bytes(p.half);
+    const RopeGamma<DT> gamma = {smem_u32(smem) + Ring::BYTES + WARPS * RopeAngles<STAGES>::bytes(p.half)};
+    ring.clear();
     pdl_wait();
-    float cs[8], sn[8], g[16], acc[16];
-    rope_gamma<DT, V, INTER>(sd.gamma, lane, p.offset, g);
+    gamma.load(sd.gamma, p.dim, p.offset);
+    __syncthreads();
+    RopeAt x, y;
+    const long long xs = rows * sd.xh * Ring::ES, ys = rows * sd.oh * Ring::ES;          // `rows` heads on
+    rope_turns<STAGES>(
+        p, sd, rows, mine, cta * WARPS + warp, ctas * WARPS, angles,
+        [&](int stage, const RopeCursor& c, bool begins) {
+            if (begins) x.enter(sd.x, c.t, sd.xt, c.head, sd.xh, Ring::ES);
+#pragma unroll
+            for (int r = 0; r < R; ++r, x.p += xs)
+                if (c.head + r * rows < sd.heads) ring.fetch(stage, r, x.p, lane);
+        },
+        [&](int stage, const RopeCursor& c, bool begins) {
+            if (begins) y.enter(sd.out, c.t, sd.ot, c.head, sd.oh, Ring::ES);
+            float f[R][16], ss[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                ring.get(stage, r, f[r]);
+                ss[r] = rope_dot(f[r], f[r]);
+            }
+            rope_row_sums(ss, p.lanes);
+            {
+                float g[16];
+                gamma.get(lane, g);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float2 rstd = splat(rope_rstd(ss[r], p));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) rope_put(f[r], j, mul2(mul2(rope_two(f[r], j), rstd), rope_two(g, j)));
+                }
+            }
+            float cs[8], sn[8];
+            angles.get(p, lane, cs, sn);
+#pragma unroll
+            for (int r = 0; r < R; ++r, y.p += ys) {
+                rope_turn<false>(f[r], lane, cs, sn);
+                if (c.head + r * rows < sd.heads) rope_store<DT, V, INTER>(const_cast<char*>(y.p), lane, f[r]);
+            }
+        });
+}
+
+// A lane has the same elements in every row and adds their part of gamma's gradient in registers. The row groups of a warp
+// are joined by exchanges, the warps of a CTA through shared memory, the CTAs by rmsq_rope_reduce_kernel, all in a
+// fixed order.
+template <int DT, int V, bool INTER>
+__global__ void __launch_bounds__(RopeShape<true>::THREADS, RopeShape<true>::CTAS) rmsq_rope_bwd_kernel(const __grid_constant__ RopeParams p)
+{
+    using Lane = RopeLane<V, INTER>;
+    using Shape = RopeShape<true>;
+    constexpr int STAGES = Shape::STAGES, WARPS = Shape::THREADS / 32, R = kRopeRows;
+    using Ring = RopeRing<DT, V, INTER, 2 * R, STAGES, Shape::THREADS>;                  // rows of x, then of dy
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int l = threadIdx.x & (p.lanes - 1), rows = 32 / p.lanes, mine = (threadIdx.x & 31) / p.lanes, warp = threadIdx.x >> 5;
+    const bool key = static_cast<int>(blockIdx.x) >= p.split;
+    const RopeSide& sd = p.side[key];
+    const int cta = static_cast<int>(blockIdx.x) - (key ? p.split : 0), ctas = key ? static_cast<int>(gridDim.x) - p.split : p.split;
+    Lane lane;
+    lane.init(l, p.lanes, p.dim, p.half);
+    const Ring ring = {smem_u32(smem)};
+    RopeAngles<STAGES> angles;
+    angles.base = smem_u32(smem) + Ring::BYTES + warp * RopeAngles<STAGES>::bytes(p.half);
+    const RopeGamma<DT> gamma = {smem_u32(smem) + Ring::BYTES + WARPS * RopeAngles<STAGES>::bytes(p.half)};
+    ring.clear();
+    pdl_wait();
+    gamma.load(sd.gamma, p.dim, p.offset);
+    __syncthreads();
+    float acc[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[j] = 0.f;
     RopeAt x, dy, dx;
-    const long long xs = rows * sd.xh * Ring::ES, ds = rows * sd.dh * Ring::ES, os = rows * sd.oh * Ring::ES;   // a turn's heads on
+    const long long xs = rows * sd.xh * Ring::ES, ds = rows * sd.dh * Ring::ES, os = rows * sd.oh * Ring::ES;   // `rows` heads on
     rope_turns<STAGES>(
-        p, sd, rows, mine, cta * kRopeWarps + warp, ctas * kRopeWarps,
-        [&](int stage, const RopeCursor& c, bool begins, bool in) {
+        p, sd, rows, mine, cta * WARPS + warp, ctas * WARPS, angles,
+        [&](int stage, const RopeCursor& c, bool begins) {
             if (begins) {
                 x.enter(sd.x, c.t, sd.xt, c.head, sd.xh, Ring::ES);
                 dy.enter(sd.dy, c.t, sd.dt, c.head, sd.dh, Ring::ES);
             }
-            ring.fetch(stage, 0, x.p, lane, in);
-            ring.fetch(stage, 1, dy.p, lane, in);
-            x.p += xs;
-            dy.p += ds;
+#pragma unroll
+            for (int r = 0; r < R; ++r, x.p += xs, dy.p += ds)
+                if (c.head + r * rows < sd.heads) {
+                    ring.fetch(stage, r, x.p, lane);
+                    ring.fetch(stage, R + r, dy.p, lane);
+                }
         },
-        [&](int stage, const RopeCursor& c, bool begins, bool in) {
-            if (begins) {
-                rope_angles<V, INTER>(p, lane, c.t, cs, sn);
-                dx.enter(sd.out, c.t, sd.ot, c.head, sd.oh, Ring::ES);
-            }
-            float f[16], d[16];
-            ring.get(stage, 0, lane, in, f);
-            ring.get(stage, 1, lane, in, d);
-            const float rstd = rope_rstd(rope_row_sum(rope_dot(f, f), p.lanes), p);
-            rope_turn<true>(d, lane, cs, sn);
+        [&](int stage, const RopeCursor& c, bool begins) {
+            if (begins) dx.enter(sd.out, c.t, sd.ot, c.head, sd.oh, Ring::ES);
+            float f[R][16], d[R][16], ss[R], dot[R];
+            {
+                float cs[8], sn[8];
+                angles.get(p, lane, cs, sn);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 xhat = mul2(rope_two(f, j), splat(rstd));
-                // (a lane without a row has NaN here where its group has no place in the table)
-                if (in) rope_put(acc, j, fma2(rope_two(d, j), xhat, rope_two(acc, j)));
-                rope_put(f, j, xhat);
-                rope_put(d, j, mul2(rope_two(d, j), rope_two(g, j)));
+                for (int r = 0; r < R; ++r) {
+                    ring.get(stage, r, f[r]);
+                    ring.get(stage, R + r, d[r]);
+                    ss[r] = rope_dot(f[r], f[r]);
+                    rope_turn<true>(d[r], lane, cs, sn);
+                }
             }
-            const float2 dot = splat(-rope_row_sum(rope_dot(f, d), p.lanes) * p.inv_dim);
+            rope_row_sums(ss, p.lanes);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) rope_put(d, j, mul2(fma2(rope_two(f, j), dot, rope_two(d, j)), splat(rstd)));
-            if (in) rope_store<DT, V, INTER>(const_cast<char*>(dx.p), lane, d);
-            dx.p += os;
+            for (int r = 0; r < R; ++r) {
+                ss[r] = rope_rstd(ss[r], p);
+                const bool in = c.head + r * rows < sd.heads;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    rope_put(f[r], j, mul2(rope_two(f[r], j), splat(ss[r])));
+                    // (a lane without a row has anything here)
+                    if (in) rope_put(acc, j, fma2(rope_two(d[r], j), rope_two(f[r], j), rope_two(acc, j)));
+                }
+            }
+            {
+                float g[16];
+                gamma.get(lane, g);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) rope_put(d[r], j, mul2(rope_two(d[r], j), rope_two(g, j)));
+                    dot[r] = rope_dot(f[r], d[r]);
+                }
+            }
+            rope_row_sums(dot, p.lanes);
+#pragma unroll
+            for (int r = 0; r < R; ++r, dx.p += os) {
+                const float2 back = splat(-dot[r] * p.inv_dim);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) rope_put(d[r], j, mul2(fma2(rope_two(f[r], j), back, rope_two(d[r], j)), splat(ss[r])));
+                if (c.head + r * rows < sd.heads) rope_store<DT, V, INTER>(const_cast<char*>(dx.p), lane, d[r]);
+            }
         });
     __syncthreads();                                       // the rings are free: they take the warps' sums
     float* const sums = reinterpret_cast<float*>(smem);
@@ -507,10 +606,10 @@ __global__ void __launch_bounds__(kRopeThreads, DT == DT_F32 ? 1 : 2) rmsq_rope_
                 if (lane.at[i] >= 0) sums[warp * p.dim + lane.at[i] + j] = acc[i * V + j];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.dim; e += kRopeThreads) {
+    for (int e = threadIdx.x; e < p.dim; e += Shape::THREADS) {
         float a = 0.f;
 #pragma unroll
-        for (int w = 0; w < kRopeWarps; ++w) a += sums[w * p.dim + e];
+        for (int w = 0; w < WARPS; ++w) a += sums[w * p.dim + e];
         p.part[static_cast<long long>(blockIdx.x) * p.dim + e] = a;
     }
 }
