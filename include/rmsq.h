@@ -313,8 +313,9 @@ rmsq_status quant_mxfp4(const void* input, int64_t rows, int64_t hidden, int dty
  * overflow gives the largest fp32; a NaN gives NaN.
  *
  *   gs_out           DEVICE pointer to one fp32 (4-byte aligned)
- *   workspace        device memory of at least nvfp4_global_scale_workspace(count) bytes, 16-byte aligned, used
- *                    by this call alone until it ends on the stream. Its contents before do not matter.
+ *   workspace        device memory of at least nvfp4_global_scale_workspace(count) bytes (none for small tensors:
+ *                    NULL will do), 16-byte aligned, used by this call alone until it ends on the stream.
+ *                    Its contents before do not matter.
  * ------------------------------------------------------------------------------------------- */
 #define RMSQ_GLOBAL_SCALE_PARTS 608
 int64_t nvfp4_global_scale_workspace(int64_t count);

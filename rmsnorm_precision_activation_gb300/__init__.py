@@ -15,6 +15,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -83,13 +84,9 @@ class PlanInfo(ctypes.Structure):
                                             "cluster", "smem_bytes", "ctas_per_sm", "w16")]
 
 
-class Heads(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", _I64), ("head_stride", _I64), ("heads", _I64)]
-
-
-class Rotation(ctypes.Structure):
-    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("places", _I64),
-                ("position_bits", _I), ("rotated", _I), ("neighbours", _I), ("axes", _I), ("sections", _I * 4)]
+# rmsq_heads (data, token_stride, head_stride, heads) and rmsq_rotation (cos, sin, positions, places, position_bits,
+# rotated, neighbours, axes, sections[4]) as bytes: packing takes a third of what filling a ctypes structure does.
+HEADS, ROTATION = struct.Struct("Pqqq"), struct.Struct("PPPq8i")
 
 
 _lib = None
@@ -123,9 +120,15 @@ def _check(status: int, where: str):
 
 
 def _stream(device, stream):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+    return ctypes.c_void_p(_raw_stream(device.index) if stream is None else stream.cuda_stream)
+
+
+def _on(device):
+    """Makes the device current; nothing to do, and to undo, where it is (a context costs 3 us a call)."""
+    return _NOTHING if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+_NOTHING = contextlib.nullcontext()
 
 
 def _ptr(t):
@@ -175,7 +178,7 @@ def rmsnorm_quant_fp8(input, gamma, *, residual=None, residual_output=None, epsi
         output = torch.empty(input.shape, dtype=torch.float8_e4m3fn, device=input.device)
     if scale_output is None:
         scale_output = torch.empty(lead, dtype=scale_dtype, device=input.device)
-    with torch.cuda.device(input.device):
+    with _on(input.device):
         st = lib().rmsnorm_quant_fp8(_ptr(x), _ptr(r), _ptr(ro), _ptr(gamma), x.shape[0], H,
                                      _DT[input.dtype], float(epsilon), float(weight_offset),
                                      float(scale_ub), _ptr(output), _ptr(scale_output),
@@ -216,7 +219,7 @@ def rmsnorm_quant_nvfp4(input, gamma, *, global_scale=None, residual=None, resid
     if global_scale.dtype != torch.float32 or global_scale.numel() != 1 or not global_scale.is_cuda:
         raise ValueError("global_scale must be a CUDA float32 tensor with one element")
     output, block_scale = _fp4_outputs(input, H, 16, output, block_scale, swizzled, torch.float8_e4m3fn)
-    with torch.cuda.device(input.device):
+    with _on(input.device):
         st = lib().rmsnorm_quant_nvfp4(_ptr(x), _ptr(r), _ptr(ro), _ptr(gamma), x.shape[0], H,
                                        _DT[input.dtype], float(epsilon), float(weight_offset),
                                        _ptr(global_scale), _ptr(output), _ptr(block_scale),
@@ -234,7 +237,7 @@ def rmsnorm_quant_mxfp4(input, gamma, *, residual=None, residual_output=None, ep
     Returns (output uint8 [..., H/2], block_scale uint8 (UE8M0 codes), residual_output)."""
     x, r, ro, residual_output, H = _prepare(input, gamma, residual, residual_output)
     output, block_scale = _fp4_outputs(input, H, 32, output, block_scale, swizzled, torch.uint8)
-    with torch.cuda.device(input.device):
+    with _on(input.device):
         st = lib().rmsnorm_quant_mxfp4(_ptr(x), _ptr(r), _ptr(ro), _ptr(gamma), x.shape[0], H,
                                        _DT[input.dtype], float(epsilon), float(weight_offset),
                                        _ptr(output), _ptr(block_scale),
@@ -253,7 +256,7 @@ def rmsnorm_nvfp4_global_scale(input, gamma, *, residual=None, epsilon=1e-6, wei
     r = None if residual is None else _flat(residual, H)
     if out is None:
         out = torch.empty(1, dtype=torch.float32, device=input.device)
-    with torch.cuda.device(input.device):
+    with _on(input.device):
         st = lib().rmsnorm_nvfp4_global_scale(_ptr(x), _ptr(r), _ptr(gamma), x.shape[0], H,
                                               _DT[input.dtype], float(epsilon),
                                               float(weight_offset), _ptr(out),
@@ -558,16 +561,21 @@ def nvfp4_global_scale(input, *, out=None, workspace=None, stream=None):
     index, count = input.get_device(), input.numel()
     if out is None:
         out = torch.empty((1,), dtype=torch.float32, device=input.device)
-    o = _one("out", out, index)
+        o = out.data_ptr()
+    else:
+        o = _one("out", out, index)
+    ws = None
     if workspace is None:
-        size = nvfp4_global_scale_workspace(count)
-        workspace = torch.empty((size,), dtype=torch.uint8, device=input.device)
+        size = (_lib or lib()).nvfp4_global_scale_workspace(count)
+        if size:
+            workspace = torch.empty((size,), dtype=torch.uint8, device=input.device)
+            ws = workspace.data_ptr()
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the input's device")
     else:
-        size = workspace.numel() * workspace.element_size()
-    _check((_lib or lib()).nvfp4_global_scale(input.data_ptr(), count, _DT[input.dtype], o, workspace.data_ptr(), size,
-                                              _raw_stream(index)), "nvfp4_global_scale")
+        size, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    _check((_lib or lib()).nvfp4_global_scale(input.data_ptr(), count, _DT[input.dtype], o, ws, size, _raw_stream(index)),
+           "nvfp4_global_scale")
     return out
 
 
@@ -712,57 +720,57 @@ def _heads(name, t, shape, dtype, index):
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or t.stride(-1) != 1:
         raise ValueError("%s must be a %s tensor of shape %s on the input's device, its last dimension contiguous"
                          % (name, dtype, tuple(shape)))
-    if t.dim() != 3:
+    if len(shape) != 3:
         try:
             t = t.view((-1 if t.numel() else 0,) + tuple(shape[-2:]))
         except RuntimeError:
             raise ValueError("%s: its leading dimensions must lie behind each other" % name) from None
     tokens, heads, _ = t.shape
     ts, hs, _ = t.stride()
-    return Heads(t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0, heads)
+    return HEADS.pack(t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0, heads)
 
 
 def _rope(query, key, query_gamma, key_gamma, cos, sin, positions, sections, interleaved):
     """Checks the inputs of rmsnorm_rope; (device index, dtype, tokens, D, query, key, gammas, rotation)."""
-    dtype, index = query.dtype, query.get_device()
+    dtype, index, shape, kshape = query.dtype, query.get_device(), query.shape, key.shape
     if dtype not in _DT:
         raise TypeError("query dtype must be bfloat16, float16 or float32")
-    if query.dim() < 3 or key.dim() != query.dim() or key.shape[:-2] != query.shape[:-2] or key.shape[-1] != query.shape[-1]:
+    lead, D = shape[:-2], shape[-1] if shape else 0
+    if len(shape) < 3 or len(kshape) != len(shape) or kshape[:-2] != lead or kshape[-1] != D:
         raise ValueError("query and key must have shapes [..., heads, D] with the same tokens and D")
-    lead, D = query.shape[:-2], query.shape[-1]
-    tokens = lead.numel()
-    q = _heads("query", query, query.shape, dtype, index)
-    k = _heads("key", key, key.shape, dtype, index)
+    q = _heads("query", query, shape, dtype, index)
+    k = _heads("key", key, kshape, dtype, index)
     gq = _count("query_gamma", query_gamma, D, dtype, index)
     gk = _count("key_gamma", key_gamma, D, dtype, index)
-    if cos.dim() != 2:
+    table = cos.shape
+    if len(table) != 2:
         raise ValueError("cos must have shape (positions, rotated / 2)")
-    c = _same("cos", cos, cos.shape, torch.float32, index)
-    s = _same("sin", sin, cos.shape, torch.float32, index)
-    axes = 1 if sections is None else len(sections)
-    if not 1 <= axes <= 4:
-        raise ValueError("sections must have 1 to 4 entries")
-    if sections is not None and sum(sections) != cos.shape[1]:
-        raise ValueError("sections must add up to rotated / 2")
-    want = lead if sections is None else (axes,) + lead
-    if positions.dtype is torch.int64:
-        bits = 64
-    elif positions.dtype is torch.int32:
-        bits = 32
+    c = _same("cos", cos, table, torch.float32, index)
+    s = _same("sin", sin, table, torch.float32, index)
+    if sections is None:
+        axes, parts, want = 1, (0, 0, 0, 0), lead
     else:
+        axes, want = len(sections), (len(sections),) + tuple(lead)
+        if not 1 <= axes <= 4:
+            raise ValueError("sections must have 1 to 4 entries")
+        if sum(sections) != table[1] or min(sections) < 0:
+            raise ValueError("sections must not be negative, and add up to rotated / 2")
+        parts = tuple(sections) + (0,) * (4 - axes)
+    pdtype = positions.dtype
+    if pdtype is not torch.int64 and pdtype is not torch.int32:
         raise TypeError("positions must be int32 or int64")
-    at = _same("positions", positions, want, positions.dtype, index)
-    r = Rotation(c, s, at, cos.shape[0], bits, 2 * cos.shape[1], int(bool(interleaved)), axes)
-    if axes > 1:
-        r.sections[:axes] = sections
-    return index, dtype, tokens, D, q, k, gq, gk, r
+    at = _same("positions", positions, want, pdtype, index)
+    r = ROTATION.pack(c, s, at, table[0], 64 if pdtype is torch.int64 else 32, 2 * table[1], 1 if interleaved else 0, axes, *parts)
+    return index, dtype, lead.numel(), D, q, k, gq, gk, r
 
 
 def _like(name, t, of, dtype, index):
     """(tensor, its C view) of an output like `of`; a contiguous one where none is given."""
-    if t is None:
-        t = torch.empty(of.shape, dtype=dtype, device=of.device)
-    return t, _heads(name, t, of.shape, dtype, index)
+    if t is not None:
+        return t, _heads(name, t, of.shape, dtype, index)
+    shape = of.shape
+    t = torch.empty(shape, dtype=dtype, device=of.device)
+    return t, HEADS.pack(t.data_ptr(), shape[-2] * shape[-1], shape[-1], shape[-2])
 
 
 def rmsnorm_rope(query, key, query_gamma, key_gamma, cos, sin, positions, *, sections=None, interleaved=False, epsilon=1e-6,
@@ -785,9 +793,8 @@ def rmsnorm_rope(query, key, query_gamma, key_gamma, cos, sin, positions, *, sec
                                                      interleaved)
     query_output, qo = _like("query_output", query_output, query, dtype, index)
     key_output, ko = _like("key_output", key_output, key, dtype, index)
-    ref = ctypes.byref
-    _check((_lib or lib()).rmsnorm_rope(ref(q), ref(k), gq, gk, ref(r), tokens, D, _DT[dtype], float(epsilon),
-                                        float(weight_offset), ref(qo), ref(ko), _raw_stream(index)), "rmsnorm_rope")
+    _check((_lib or lib()).rmsnorm_rope(q, k, gq, gk, r, tokens, D, _DT[dtype], float(epsilon), float(weight_offset),
+                                        qo, ko, _raw_stream(index)), "rmsnorm_rope")
     return query_output, key_output
 
 
@@ -823,10 +830,14 @@ def rmsnorm_rope_backward(grad_query, grad_key, query, key, query_gamma, key_gam
     key_grad, ko = _like("key_grad", key_grad, key, dtype, index)
     if query_gamma_grad is None:
         query_gamma_grad = torch.empty((D,), dtype=pdt, device=query.device)
+        pq = query_gamma_grad.data_ptr()
+    else:
+        pq = _count("query_gamma_grad", query_gamma_grad, D, pdt, index)
     if key_gamma_grad is None:
         key_gamma_grad = torch.empty((D,), dtype=pdt, device=query.device)
-    pq = _count("query_gamma_grad", query_gamma_grad, D, pdt, index)
-    pk = _count("key_gamma_grad", key_gamma_grad, D, pdt, index)
+        pk = key_gamma_grad.data_ptr()
+    else:
+        pk = _count("key_gamma_grad", key_gamma_grad, D, pdt, index)
     if workspace is None:
         size = rmsnorm_rope_backward_workspace(tokens, D)
         workspace = torch.empty((size,), dtype=torch.uint8, device=query.device)
@@ -834,10 +845,9 @@ def rmsnorm_rope_backward(grad_query, grad_key, query, key, query_gamma, key_gam
         raise ValueError("workspace must be a contiguous tensor on the input's device")
     else:
         size = workspace.numel() * workspace.element_size()
-    ref = ctypes.byref
-    _check((_lib or lib()).rmsnorm_rope_backward(ref(dq), ref(dk), ref(q), ref(k), gq, gk, ref(r), tokens, D, _DT[dtype],
-                                                 float(epsilon), float(weight_offset), ref(qo), ref(ko), pq, pk, _DT[pdt],
-                                                 workspace.data_ptr(), size, _raw_stream(index)), "rmsnorm_rope_backward")
+    _check((_lib or lib()).rmsnorm_rope_backward(dq, dk, q, k, gq, gk, r, tokens, D, _DT[dtype], float(epsilon),
+                                                 float(weight_offset), qo, ko, pq, pk, _DT[pdt], workspace.data_ptr(), size, _raw_stream(index)),
+           "rmsnorm_rope_backward")
     return query_grad, key_grad, query_gamma_grad, key_gamma_grad
 
 

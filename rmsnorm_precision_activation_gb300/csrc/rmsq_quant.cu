@@ -254,12 +254,12 @@ extern "C" rmsq_status quant_mxfp4(const void* input, int64_t rows, int64_t hidd
     return quantise(false, input, rows, hidden, dtype, nullptr, output, block_scale, scale_layout, stream);
 }
 
-// Bytes that one CTA takes alone.
-constexpr int64_t kAmaxAlone = 128 * 1024;
+// Elements that one CTA takes alone.
+constexpr int64_t kAmaxAlone = 65536;
 
 extern "C" int64_t nvfp4_global_scale_workspace(int64_t count)
 {
-    return count > 0 ? RMSQ_GLOBAL_SCALE_PARTS * static_cast<int64_t>(sizeof(float)) : 0;
+    return count > kAmaxAlone ? RMSQ_GLOBAL_SCALE_PARTS * static_cast<int64_t>(sizeof(float)) : 0;
 }
 
 extern "C" rmsq_status nvfp4_global_scale(const void* input, int64_t count, int dtype, float* gs_out, void* workspace,
@@ -270,9 +270,10 @@ extern "C" rmsq_status nvfp4_global_scale(const void* input, int64_t count, int 
     if (!gs_out) return RMSQ_ERR_NULL;
     if (reinterpret_cast<uintptr_t>(gs_out) % 4 != 0) return RMSQ_ERR_ALIGN;
     if (count > 0) {
-        if (!input || !workspace) return RMSQ_ERR_NULL;
+        const int64_t need = nvfp4_global_scale_workspace(count);
+        if (!input || (need > 0 && !workspace)) return RMSQ_ERR_NULL;
         if (!aligned16(input) || !aligned16(workspace)) return RMSQ_ERR_ALIGN;
-        if (workspace_bytes < nvfp4_global_scale_workspace(count)) return RMSQ_ERR_SHAPE;
+        if (workspace_bytes < need) return RMSQ_ERR_SHAPE;
     }
     DeviceView dv;
     if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
@@ -284,7 +285,7 @@ extern "C" rmsq_status nvfp4_global_scale(const void* input, int64_t count, int 
     const int es = dtype == RMSQ_F32 ? 4 : 2;
     p.vectors = count / (16 / es);
     long long grid = 1;
-    if (count * es > kAmaxAlone) {
+    if (count > kAmaxAlone) {
         grid = (p.vectors + 4 * kAmaxThreads - 1) / (4 * kAmaxThreads);
         if (grid > 4LL * dv.sms) grid = 4LL * dv.sms;
         if (grid > RMSQ_GLOBAL_SCALE_PARTS) grid = RMSQ_GLOBAL_SCALE_PARTS;

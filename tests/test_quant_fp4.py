@@ -250,13 +250,13 @@ def test_refusals_without_a_gpu():
         assert f(rows=0, x=None) == 0
     assert nv(gs=A + 2) == 3 and mx(hidden=48) == 2
 
-    def gs(x=A, n=64, dt=0, out=A, ws=A, size=1 << 20):
+    def gs(x=A, n=100000, dt=0, out=A, ws=A, size=1 << 20):
         return lib.nvfp4_global_scale(x, n, dt, out, ws, size, None)
 
     assert all(gs(**{a: None}) == 1 for a in ("x", "out", "ws"))
-    assert gs(n=-1) == 2 and gs(size=lib.nvfp4_global_scale_workspace(64) - 1) == 2 and gs(dt=7) == 4
+    assert gs(n=-1) == 2 and gs(size=lib.nvfp4_global_scale_workspace(100000) - 1) == 2 and gs(dt=7) == 4
     assert gs(x=A + 4) == 3 and gs(ws=A + 4) == 3 and gs(out=A + 2) == 3
-    assert lib.nvfp4_global_scale_workspace(0) == 0
+    assert lib.nvfp4_global_scale_workspace(0) == 0 and lib.nvfp4_global_scale_workspace(64) == 0
 
 
 @gpu
@@ -275,4 +275,4 @@ def test_python_refusals():
         with pytest.raises(TypeError):
             call()
     with pytest.raises(q.RmsqError):
-        q.nvfp4_global_scale(x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        q.nvfp4_global_scale(torch.ones(100000, device="cuda"), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

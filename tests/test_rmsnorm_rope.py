@@ -351,19 +351,14 @@ def test_empty_calls():
 
 
 def test_refusals_without_a_gpu():
-    import ctypes
-
     import rmsnorm_precision_activation_gb300 as m
     lib, A = rq().lib(), 1 << 20      # fake addresses: never dereferenced here
-    ref = ctypes.byref
 
     def call(q=(A, 512, 64, 8), k=(A, 128, 64, 2), gq=A, gk=A, rot=(A, A, A, 100, 64, 64, 0, 1), sections=(), tokens=4, dim=64,
              dt=0, eps=1e-6, off=0.0, oq=(A, 512, 64, 8), ok=(A, 128, 64, 2), back=None):
-        r = None if rot is None else m.Rotation(*rot)
-        for i, n in enumerate(sections):
-            r.sections[i] = n
-        h = lambda t: None if t is None else ref(m.Heads(*t))  # noqa: E731
-        r = None if r is None else ref(r)
+        parts = tuple(sections) + (0,) * (4 - len(sections))
+        r = None if rot is None else m.ROTATION.pack(*(p or 0 for p in rot[:3]), *rot[3:], *parts)
+        h = lambda t: None if t is None else m.HEADS.pack(t[0] or 0, *t[1:])  # noqa: E731
         if back is None:
             return lib.rmsnorm_rope(h(q), h(k), gq, gk, r, tokens, dim, dt, eps, off, h(oq), h(ok), None)
         b = dict(dq=(A, 512, 64, 8), dk=(A, 128, 64, 2), pq=A, pk=A, pdt=dt, ws=A, size=1 << 30)
