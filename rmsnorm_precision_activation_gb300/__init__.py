@@ -584,8 +584,11 @@ def nvfp4_global_scale_workspace(count: int) -> int:
     return lib().nvfp4_global_scale_workspace(int(count))
 
 
+_BYTES = {torch.uint8, torch.int8, torch.float8_e4m3fn, getattr(torch, "float8_e8m0fnu", torch.uint8)}
+
+
 def _bytes(name, t, n, index):
-    if t.element_size() != 1 or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
+    if t.dtype not in _BYTES or t.numel() != n or not t.is_contiguous() or t.get_device() != index:
         raise ValueError("%s must be a contiguous tensor of %d bytes on the input's device" % (name, n))
     return t.data_ptr()
 
@@ -649,30 +652,36 @@ def quant_mxfp4(input, *, output=None, block_scale=None, swizzled=False, stream=
 def _matmul_fp4(input, input_scale, weight, weight_scale, block, bias, out_dtype, output):
     """Checks a 4-bit product's tensors; (device index, M, N, K, pointers of the four operands, the bias that is read,
     its pointer, output, its pointer)."""
-    if input.dtype is not torch.uint8 or weight.dtype is not torch.uint8:
+    u8 = torch.uint8
+    if input.dtype is not u8 or weight.dtype is not u8:
         raise TypeError("input and weight must be uint8 (two codes per byte)")
     if out_dtype not in _DT:
         raise TypeError("out_dtype must be bfloat16, float16 or float32")
-    index, shape = input.get_device(), input.shape
+    index, shape, wshape = input.get_device(), input.shape, weight.shape
     if not shape or not input.is_contiguous():
         raise ValueError("input must be a contiguous tensor of at least one dimension")
     half = shape[-1]
-    M = input.numel() // half if half else 0
-    if weight.dim() != 2:
-        raise ValueError("weight must have shape (N, %d)" % half)
-    N = weight.shape[0]
-    w = _same("weight", weight, (N, half), torch.uint8, index)
-    K = 2 * half
-    sa = _bytes("input_scale", input_scale, swizzled_scale_numel(M, K, block), index)
-    sw = _bytes("weight_scale", weight_scale, swizzled_scale_numel(N, K, block), index)
-    bias, b = (None, None) if bias is None else _vector("bias", bias, N, out_dtype, index)
-    oshape = shape[:-1] + (N,)
+    if len(wshape) != 2 or wshape[1] != half or not weight.is_contiguous() or weight.get_device() != index:
+        raise ValueError("weight must be a contiguous uint8 tensor of shape (N, %d) on the input's device" % half)
+    N, K = wshape[0], 2 * half
+    if len(shape) == 2:
+        M = shape[0]
+        oshape = (M, N)
+    else:
+        M = input.numel() // half if half else 0
+        oshape = shape[:-1] + (N,)
+    row = (K // block + 3) // 4 * 512                     # bytes of 128 rows' scales
+    sa = _bytes("input_scale", input_scale, (M + 127) // 128 * row, index)
+    sw = _bytes("weight_scale", weight_scale, (N + 127) // 128 * row, index)
+    b = None
+    if bias is not None:
+        bias, b = _vector("bias", bias, N, out_dtype, index)
     if output is None:
         output = torch.empty(oshape, dtype=out_dtype, device=input.device)
         out = output.data_ptr()
     else:
         out = _same("output", output, oshape, out_dtype, index)
-    return index, M, N, K, (input.data_ptr(), sa, w, sw), bias, b, output, out
+    return index, M, N, K, (input.data_ptr(), sa, weight.data_ptr(), sw), bias, b, output, out
 
 
 def matmul_nvfp4(input, input_scale, weight, weight_scale, *, input_global_scale=None, weight_global_scale=None, bias=None,
