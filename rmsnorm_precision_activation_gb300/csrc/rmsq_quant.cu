@@ -18,11 +18,10 @@ struct QuantParams {
     const float* gs;                 // or null (1)
     unsigned char* out;
     unsigned char* scale;
-    long long units;                 // of 16 elements
+    long long rows, units;           // rows, and units of 16 elements in all
     long long row_units;             // per row
-    int swizzled;
+    int chunks;                      // swizzled: of 32 units per row
     int k_tiles;                     // swizzled: tiles of 4 scales per row
-    int words;                       // swizzled: a row is whole tiles of 4 scales
 };
 
 constexpr int kQuantThreads = 256;
@@ -53,22 +52,13 @@ __device__ __forceinline__ float amax16(const float2 (&f)[8])
     return a;
 }
 
-template <int DT, bool NV> __global__ void __launch_bounds__(kQuantThreads) rmsq_quant_kernel(const QuantParams p)
+// Scale code and E2M1 codes of a thread's unit (MXFP4: of half a block, the other half being the neighbour's).
+template <bool NV> __device__ __forceinline__ uint32_t quantise16(const float2 (&f)[8], float gs, uint2& codes)
 {
-    pdl_wait();
-    const long long first = static_cast<long long>(blockIdx.x) * kQuantThreads, unit = first + threadIdx.x;
-    const bool in = unit < p.units;
-    float2 f[8];
-    if (in) load16<DT>(p.x, unit, f);
-    else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = make_float2(0.f, 0.f);
-    }
     float a = amax16(f);
     uint32_t code;
     float q[16];
     if (NV) {
-        const float gs = p.gs != nullptr ? __ldg(p.gs) : 1.0f;
         code = cvt_e4m3x2(__fdiv_rn(__fmul_rn(gs, a), 6.0f), 0.f) & 0xFFu;
         if (!(a < __int_as_float(0x7F800000))) code = 0x7Fu;           // a NaN or an infinity: scale NaN
         const float s = e4m3_value(code);
@@ -92,35 +82,73 @@ template <int DT, bool NV> __global__ void __launch_bounds__(kQuantThreads) rmsq
             q[2 * j + 1] = t.y;
         }
     }
-    if (in) {
-        float lo[8], hi[8];
+    float lo[8], hi[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            lo[j] = q[j];
-            hi[j] = q[8 + j];
-        }
-        st_v2(p.out + unit * 8, cvt_e2m1x8(lo), cvt_e2m1x8(hi));
+    for (int j = 0; j < 8; ++j) {
+        lo[j] = q[j];
+        hi[j] = q[8 + j];
     }
+    codes = make_uint2(cvt_e2m1x8(lo), cvt_e2m1x8(hi));
+    return code;
+}
+
+// CTAs go through the tensor from its end: what was written or read last before, by the kernel that made it or by
+// nvfp4_global_scale, is still in L2.
+//
+// Row-major scales: units in their order. Swizzled ones: a CTA takes 32 units of 8 rows, 2 r and 2 r + 1 of each of the four
+// groups of 32 rows that a tile of scales has, so that its scales are whole sectors: 32 bytes of each of its tiles
+// (16384 x 8192 bf16 in units of their order, 4 bytes of a tile at a time: 72 us).
+template <int DT, bool NV, bool SWIZZLED> __global__ void __launch_bounds__(kQuantThreads) rmsq_quant_kernel(const QuantParams p)
+{
     constexpr int PER = NV ? 1 : 2;                                     // units per scale
-    if (!p.swizzled) {
+    __shared__ uint32_t words[8 * 8];                                   // [tile][row of two][group]: a row's four scales
+    const unsigned block = gridDim.x - 1 - blockIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long unit, row = 0;
+    int in_row = 0;                                                     // swizzled: unit within its row
+    bool in;
+    if (SWIZZLED) {
+        const unsigned strip = block / static_cast<unsigned>(p.chunks), chunk = block - strip * static_cast<unsigned>(p.chunks);
+        row = static_cast<long long>(strip / 16) * 128 + (warp & 3) * 32 + strip % 16 * 2 + (warp >> 2);
+        in_row = static_cast<int>(chunk) * 32 + lane;
+        unit = row * p.row_units + in_row;
+        in = row < p.rows && in_row < p.row_units;
+    } else {
+        unit = static_cast<long long>(block) * kQuantThreads + threadIdx.x;
+        in = unit < p.units;
+    }
+    pdl_wait();
+    float2 f[8];
+    if (in) load16<DT>(p.x, unit, f);
+    else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = make_float2(0.f, 0.f);
+    }
+    uint2 codes;
+    const uint32_t code = quantise16<NV>(f, NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, codes);
+    if (in) st_v2(p.out + unit * 8, codes.x, codes.y);
+    if (!SWIZZLED) {
         if (in && threadIdx.x % PER == 0) p.scale[unit / PER] = static_cast<unsigned char>(code);
         return;
     }
-    const long long row0 = first / p.row_units;
-    const unsigned in_row = static_cast<unsigned>(first - row0 * p.row_units) + threadIdx.x;
-    const unsigned down = in_row / static_cast<unsigned>(p.row_units);
-    const long long row = row0 + down;
-    const int sf = static_cast<int>((in_row - down * static_cast<unsigned>(p.row_units)) / PER);
-    unsigned char* const at = p.scale + (row / 128 * p.k_tiles + sf / 4) * 512 + row % 32 * 16 + row % 128 / 32 * 4;
-    if (p.words) {
-        // the four scales of a tile's row come from neighbouring lanes
-        uint32_t w = code << (8 * (sf & 3));
-        w |= __shfl_xor_sync(0xFFFFFFFFu, w, PER);
-        w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2 * PER);
-        if (in && threadIdx.x % (4 * PER) == 0) st_u32(at, w);
-    } else if (in && threadIdx.x % PER == 0) {
-        at[sf & 3] = static_cast<unsigned char>(code);
-    }
+    // the four scales of a tile's row come from neighbouring lanes
+    uint32_t w = code << (8 * (lane / PER & 3));
+    w |= __shfl_xor_sync(0xFFFFFFFFu, w, PER);
+    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2 * PER);
+    constexpr int TILES = 32 / (4 * PER);
+    if (lane % (4 * PER) == 0) words[lane / (4 * PER) * 8 + (warp >> 2) * 4 + (warp & 3)] = w;
+    __syncthreads();
+    if (threadIdx.x >= TILES * 8) return;
+    const int tile = threadIdx.x / 8, two = threadIdx.x / 4 & 1, group = threadIdx.x & 3;
+    const unsigned strip = block / static_cast<unsigned>(p.chunks), chunk = block - strip * static_cast<unsigned>(p.chunks);
+    const long long r = static_cast<long long>(strip / 16) * 128 + group * 32 + strip % 16 * 2 + two;
+    const int first = static_cast<int>(chunk) * (32 / PER) + tile * 4, scales = static_cast<int>(p.row_units) / PER - first;
+    if (r >= p.rows || scales <= 0) return;
+    unsigned char* const at = p.scale + (r / 128 * p.k_tiles + first / 4) * 512 + r % 32 * 16 + group * 4;
+    w = words[threadIdx.x];
+    if (scales >= 4) st_u32(at, w);
+    else
+        for (int i = 0; i < scales; ++i) at[i] = static_cast<unsigned char>(w >> (8 * i));   // the padding stays
 }
 
 // The global scale, in two steps: the maxima of parts of the tensor, one per CTA, then their maximum. A tensor that one
@@ -200,11 +228,15 @@ static rmsq_status status_of(cudaError_t e)
     return RMSQ_ERR_LAUNCH;
 }
 
-template <bool NV> static const void* quant_fn(int dtype)
+template <bool NV, bool SWIZZLED> static const void* quant_fn(int dtype)
 {
-    return dtype == RMSQ_BF16   ? reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_BF16, NV>)
-           : dtype == RMSQ_FP16 ? reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_FP16, NV>)
-                                : reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_F32, NV>);
+    return dtype == RMSQ_BF16   ? reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_BF16, NV, SWIZZLED>)
+           : dtype == RMSQ_FP16 ? reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_FP16, NV, SWIZZLED>)
+                                : reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_F32, NV, SWIZZLED>);
+}
+template <bool NV> static const void* quant_fn(int dtype, bool swizzled)
+{
+    return swizzled ? quant_fn<NV, true>(dtype) : quant_fn<NV, false>(dtype);
 }
 
 static rmsq_status quantise(bool nv, const void* input, int64_t rows, int64_t hidden, int dtype, const float* global_scale,
@@ -224,17 +256,18 @@ static rmsq_status quantise(bool nv, const void* input, int64_t rows, int64_t hi
     p.gs = global_scale;
     p.out = static_cast<unsigned char*>(output);
     p.scale = static_cast<unsigned char*>(block_scale);
+    const bool swizzled = scale_layout == RMSQ_SCALE_SWIZZLED_128x4;
+    p.rows = rows;
     p.row_units = hidden / 16;
     p.units = rows * p.row_units;
-    p.swizzled = scale_layout == RMSQ_SCALE_SWIZZLED_128x4;
+    p.chunks = static_cast<int>((p.row_units + 31) / 32);
     p.k_tiles = static_cast<int>((hidden / block + 3) / 4);
-    p.words = hidden % (4 * block) == 0;
-    const long long grid = (p.units + kQuantThreads - 1) / kQuantThreads;
+    const long long grid = swizzled ? (rows + 127) / 128 * 16 * p.chunks : (p.units + kQuantThreads - 1) / kQuantThreads;
     if (grid > INT32_MAX) return RMSQ_ERR_SHAPE;
     DeviceView dv;
     if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
     void* args[] = {&p};
-    return status_of(launch_kernel(nv ? quant_fn<true>(dtype) : quant_fn<false>(dtype), dim3(static_cast<unsigned>(grid)),
+    return status_of(launch_kernel(nv ? quant_fn<true>(dtype, swizzled) : quant_fn<false>(dtype, swizzled), dim3(static_cast<unsigned>(grid)),
                                    kQuantThreads, 0, 1, static_cast<cudaStream_t>(stream), args));
 }
 
