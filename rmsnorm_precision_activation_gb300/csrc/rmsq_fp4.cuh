@@ -216,6 +216,49 @@ __device__ __forceinline__ uint32_t fp4_peer(uint32_t addr, uint32_t rank)
     return a;
 }
 
+// N columns (tokens) of a lane's channel to the output: out is where the first goes, pitch the bytes to the next token's
+// row, `left` the tokens that there are, in: the channel is one. Neighbouring lanes have neighbouring channels, so
+// where their two 16-bit values are a word (the output's width is even) lanes of a pair exchange halves and each writes one
+// token's: half the stores.
+template <int DT, int N>
+__device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, long long pitch, int left, float fa, float fw, float bias, bool in, bool words)
+{
+    float f[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = fp4_value(__uint_as_float(v[i]), fa, fw, bias);
+    if constexpr (DT != DT_F32) {
+        if (words) {
+            const bool odd = threadIdx.x & 1;
+            char* at = odd ? out + pitch - 2 : out;
+#pragma unroll
+            for (int i = 0; i < N; i += 2, at += 2 * pitch) {
+                const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? f[i] : f[i + 1], 1);
+                const uint32_t w = odd ? Scalar<DT>::put2(other, f[i + 1]) : Scalar<DT>::put2(f[i], other);
+                if (in && i + odd < left) st_u32(at, w);
+            }
+            return;
+        }
+    }
+    if (!in) return;
+#pragma unroll
+    for (int i = 0; i < N; ++i, out += pitch) {
+        if (i >= left) return;
+        if constexpr (DT == DT_F32) st_u32(out, __float_as_uint(f[i]));
+        else st_u16(out, Scalar<DT>::put(f[i]));
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void fp4_store(const Fp4Params& p, const uint32_t* v, long long m, long long n, int left, float fa, float fw, float bias)
+{
+    const long long pitch = p.n * (p.dt == DT_F32 ? 4 : 2);
+    char* const out = static_cast<char*>(p.out) + (m * p.n + n) * (p.dt == DT_F32 ? 4 : 2);
+    const bool in = n < p.n, words = p.n % 2 == 0;
+    if (p.dt == DT_BF16) fp4_store<DT_BF16, N>(v, out, pitch, left, fa, fw, bias, in, words);
+    else if (p.dt == DT_FP16) fp4_store<DT_FP16, N>(v, out, pitch, left, fa, fw, bias, in, words);
+    else fp4_store<DT_F32, N>(v, out, pitch, left, fa, fw, bias, in, words);
+}
+
 template <bool NV, int NT>
 __global__ void __launch_bounds__(Fp4Shape<NV, NT>::THREADS, Fp4Shape<NV, NT>::CTAS)
 rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
@@ -366,7 +409,6 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
         const long long n = static_cast<long long>(tn) * kFp4Rows + row, m0 = static_cast<long long>(tm) * NT;
         const float fa = fp4_factor(p.a_gs), fw = fp4_factor(p.w_gs);
         const float bias = p.bias != nullptr && n < p.n ? load_as(p.bias, n, p.dt) : 0.f;
-        const int es = p.dt == DT_F32 ? 4 : 2;
         if (nc > 1) cluster_wait();
         ok = mbar_wait<SCOPE_CTA>(acc_full, 0, limit);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -382,12 +424,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                 if constexpr (LD == 32) tmem_ld_x16(acc + c + 16, v + 16);
                 tmem_wait_ld();
                 if (nc == 1) {
-                    if (n < p.n) {
-                        char* out = static_cast<char*>(p.out) + ((m0 + c) * p.n + n) * es;
-#pragma unroll
-                        for (int i = 0; i < LD; ++i, out += p.n * es)
-                            if (c + i < tokens) store_as(out, 0, p.dt, fp4_value(__uint_as_float(v[i]), fa, fw, bias));
-                    }
+                    fp4_store<LD>(p, v, m0 + c, n, tokens - c, fa, fw, bias);
                 } else {
 #pragma unroll
                     for (int i = 0; i < LD / 4; ++i) {
@@ -424,11 +461,8 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                         v.z += __uint_as_float(o[r].z);
                         v.w += __uint_as_float(o[r].w);
                     }
-                    const float four[4] = {v.x, v.y, v.z, v.w};
-                    char* const out = static_cast<char*>(p.out) + ((m0 + static_cast<int>(rank) * per + 4 * i) * p.n + n) * es;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (n < p.n && 4 * i + j < own) store_as(out + j * p.n * es, 0, p.dt, fp4_value(four[j], fa, fw, bias));
+                    const uint32_t four[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
+                    fp4_store<4>(p, four, m0 + static_cast<int>(rank) * per + 4 * i, n, own - 4 * i, fa, fw, bias);
                 }
             }
         }

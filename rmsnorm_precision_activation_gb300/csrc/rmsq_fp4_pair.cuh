@@ -266,19 +266,10 @@ rmsq_fp4_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                     __syncwarp();
                     if (lane == 0) mbar_arrive_leader_relaxed(acc_free);
                 }
-                if (n < p.n) {
-                    const int es = p.dt == DT_F32 ? 4 : 2;
-                    const long long pitch = p.n * es;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const long long m0 = static_cast<long long>(tm) * kFp4PairTokens + 32 * (h == 0 ? c0 : c1);
-                        const int left = static_cast<int>(min(static_cast<long long>(32), p.m - m0));
-                        char* out = static_cast<char*>(p.out) + (m0 * p.n + n) * es;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j, out += pitch)
-                            if (j < left) store_as(out, 0, p.dt, fp4_value(__uint_as_float(v[32 * h + j]), fa, fw, bias));
-                    }
-                }
+                const long long m0 = static_cast<long long>(tm) * kFp4PairTokens;
+                const int left = static_cast<int>(min(static_cast<long long>(kFp4PairTokens), p.m - m0));
+                fp4_store<32>(p, v, m0 + 32 * c0, n, left - 32 * c0, fa, fw, bias);
+                fp4_store<32>(p, v + 32, m0 + 32 * c1, n, left - 32 * c1, fa, fw, bias);
             }
         }
         if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);

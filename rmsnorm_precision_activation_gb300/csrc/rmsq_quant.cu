@@ -20,7 +20,7 @@ struct QuantParams {
     unsigned char* scale;
     long long rows, units;           // rows, and units of 16 elements in all
     long long row_units;             // per row
-    int chunks;                      // swizzled: of 32 units per row
+    int chunks;                      // swizzled: of kQuantChunk units per row
     int k_tiles;                     // swizzled: tiles of 4 scales per row
 };
 
@@ -95,28 +95,17 @@ template <bool NV> __device__ __forceinline__ uint32_t quantise16(const float2 (
 // CTAs go through the tensor from its end: what was written or read last before, by the kernel that made it or by
 // nvfp4_global_scale, is still in L2.
 //
-// Row-major scales: units in their order. Swizzled ones: a CTA takes 32 units of 8 rows, 2 r and 2 r + 1 of each of the four
-// groups of 32 rows that a tile of scales has, so that its scales are whole sectors: 32 bytes of each of its tiles
-// (16384 x 8192 bf16 in units of their order, 4 bytes of a tile at a time: 72 us).
-template <int DT, bool NV, bool SWIZZLED> __global__ void __launch_bounds__(kQuantThreads) rmsq_quant_kernel(const QuantParams p)
+// Row-major scales: units in their order. Swizzled ones: a CTA takes kQuantChunk units of 8 rows, 2 r and 2 r + 1 of each of the
+// four groups of 32 rows that a tile of scales has, so that its scales are whole sectors: 32 bytes of each of its tiles. Measured,
+// 16384 x 8192 bf16, NVFP4 / MXFP4: 63 / 53 us in chunks of 32, 68 / 67 of 16, 68 / 55 of 64; units in their order, 4 bytes
+// of a tile at a time: 72 / 63; a warp on a tile's 8 rows, whose reads are 128 bytes of a row then: 74 / 57.
+constexpr int kQuantChunk = 32, kSwizzledThreads = 8 * kQuantChunk;
+
+template <int DT, bool NV> __global__ void __launch_bounds__(kQuantThreads) rmsq_quant_kernel(const QuantParams p)
 {
     constexpr int PER = NV ? 1 : 2;                                     // units per scale
-    __shared__ uint32_t words[8 * 8];                                   // [tile][row of two][group]: a row's four scales
-    const unsigned block = gridDim.x - 1 - blockIdx.x;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long unit, row = 0;
-    int in_row = 0;                                                     // swizzled: unit within its row
-    bool in;
-    if (SWIZZLED) {
-        const unsigned strip = block / static_cast<unsigned>(p.chunks), chunk = block - strip * static_cast<unsigned>(p.chunks);
-        row = static_cast<long long>(strip / 16) * 128 + (warp & 3) * 32 + strip % 16 * 2 + (warp >> 2);
-        in_row = static_cast<int>(chunk) * 32 + lane;
-        unit = row * p.row_units + in_row;
-        in = row < p.rows && in_row < p.row_units;
-    } else {
-        unit = static_cast<long long>(block) * kQuantThreads + threadIdx.x;
-        in = unit < p.units;
-    }
+    const long long unit = static_cast<long long>(gridDim.x - 1 - blockIdx.x) * kQuantThreads + threadIdx.x;
+    const bool in = unit < p.units;
     pdl_wait();
     float2 f[8];
     if (in) load16<DT>(p.x, unit, f);
@@ -127,28 +116,46 @@ template <int DT, bool NV, bool SWIZZLED> __global__ void __launch_bounds__(kQua
     uint2 codes;
     const uint32_t code = quantise16<NV>(f, NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, codes);
     if (in) st_v2(p.out + unit * 8, codes.x, codes.y);
-    if (!SWIZZLED) {
-        if (in && threadIdx.x % PER == 0) p.scale[unit / PER] = static_cast<unsigned char>(code);
-        return;
+    if (in && threadIdx.x % PER == 0) p.scale[unit / PER] = static_cast<unsigned char>(code);
+}
+
+template <int DT, bool NV> __global__ void __launch_bounds__(kSwizzledThreads) rmsq_quant_swizzled_kernel(const QuantParams p)
+{
+    constexpr int PER = NV ? 1 : 2, SPAN = 4 * PER;                     // units per scale, per four scales
+    constexpr int TILES = kQuantChunk / SPAN;
+    __shared__ uint32_t words[TILES * 8];                               // [tile][row of two][group]: a row's four scales
+    const unsigned block = gridDim.x - 1 - blockIdx.x;
+    const unsigned strip = block / static_cast<unsigned>(p.chunks), chunk = block - strip * static_cast<unsigned>(p.chunks);
+    const int u = threadIdx.x % kQuantChunk, which = threadIdx.x / kQuantChunk;      // unit of the chunk; of the 8 rows
+    const long long row0 = static_cast<long long>(strip / 16) * 128 + strip % 16 * 2, row = row0 + (which >> 1) * 32 + (which & 1);
+    const int in_row = static_cast<int>(chunk) * kQuantChunk + u;
+    const bool in = row < p.rows && in_row < p.row_units;
+    const long long unit = row * p.row_units + in_row;
+    pdl_wait();
+    float2 f[8];
+    if (in) load16<DT>(p.x, unit, f);
+    else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = make_float2(0.f, 0.f);
     }
+    uint2 codes;
+    uint32_t w = quantise16<NV>(f, NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, codes) << (8 * (u / PER & 3));
+    if (in) st_v2(p.out + unit * 8, codes.x, codes.y);
     // the four scales of a tile's row come from neighbouring lanes
-    uint32_t w = code << (8 * (lane / PER & 3));
     w |= __shfl_xor_sync(0xFFFFFFFFu, w, PER);
     w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2 * PER);
-    constexpr int TILES = 32 / (4 * PER);
-    if (lane % (4 * PER) == 0) words[lane / (4 * PER) * 8 + (warp >> 2) * 4 + (warp & 3)] = w;
+    if (u % SPAN == 0) words[u / SPAN * 8 + (which & 1) * 4 + (which >> 1)] = w;
     __syncthreads();
     if (threadIdx.x >= TILES * 8) return;
     const int tile = threadIdx.x / 8, two = threadIdx.x / 4 & 1, group = threadIdx.x & 3;
-    const unsigned strip = block / static_cast<unsigned>(p.chunks), chunk = block - strip * static_cast<unsigned>(p.chunks);
-    const long long r = static_cast<long long>(strip / 16) * 128 + group * 32 + strip % 16 * 2 + two;
-    const int first = static_cast<int>(chunk) * (32 / PER) + tile * 4, scales = static_cast<int>(p.row_units) / PER - first;
-    if (r >= p.rows || scales <= 0) return;
-    unsigned char* const at = p.scale + (r / 128 * p.k_tiles + first / 4) * 512 + r % 32 * 16 + group * 4;
+    const long long r = row0 + group * 32 + two;
+    const int scale = static_cast<int>(chunk) * (kQuantChunk / PER) + tile * 4, left = static_cast<int>(p.row_units) / PER - scale;
+    if (r >= p.rows || left <= 0) return;
+    unsigned char* const at = p.scale + (r / 128 * p.k_tiles + scale / 4) * 512 + r % 32 * 16 + group * 4;
     w = words[threadIdx.x];
-    if (scales >= 4) st_u32(at, w);
+    if (left >= 4) st_u32(at, w);
     else
-        for (int i = 0; i < scales; ++i) at[i] = static_cast<unsigned char>(w >> (8 * i));   // the padding stays
+        for (int i = 0; i < left; ++i) at[i] = static_cast<unsigned char>(w >> (8 * i));     // the padding stays
 }
 
 // The global scale, in two steps: the maxima of parts of the tensor, one per CTA, then their maximum. A tensor that one
@@ -228,15 +235,16 @@ static rmsq_status status_of(cudaError_t e)
     return RMSQ_ERR_LAUNCH;
 }
 
-template <bool NV, bool SWIZZLED> static const void* quant_fn(int dtype)
+template <int DT, bool NV> static const void* quant_fn(bool swizzled)
 {
-    return dtype == RMSQ_BF16   ? reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_BF16, NV, SWIZZLED>)
-           : dtype == RMSQ_FP16 ? reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_FP16, NV, SWIZZLED>)
-                                : reinterpret_cast<const void*>(&rmsq_quant_kernel<DT_F32, NV, SWIZZLED>);
+    return swizzled ? reinterpret_cast<const void*>(&rmsq_quant_swizzled_kernel<DT, NV>)
+                    : reinterpret_cast<const void*>(&rmsq_quant_kernel<DT, NV>);
 }
 template <bool NV> static const void* quant_fn(int dtype, bool swizzled)
 {
-    return swizzled ? quant_fn<NV, true>(dtype) : quant_fn<NV, false>(dtype);
+    return dtype == RMSQ_BF16   ? quant_fn<DT_BF16, NV>(swizzled)
+           : dtype == RMSQ_FP16 ? quant_fn<DT_FP16, NV>(swizzled)
+                                : quant_fn<DT_F32, NV>(swizzled);
 }
 
 static rmsq_status quantise(bool nv, const void* input, int64_t rows, int64_t hidden, int dtype, const float* global_scale,
@@ -260,7 +268,7 @@ static rmsq_status quantise(bool nv, const void* input, int64_t rows, int64_t hi
     p.rows = rows;
     p.row_units = hidden / 16;
     p.units = rows * p.row_units;
-    p.chunks = static_cast<int>((p.row_units + 31) / 32);
+    p.chunks = static_cast<int>((p.row_units + kQuantChunk - 1) / kQuantChunk);
     p.k_tiles = static_cast<int>((hidden / block + 3) / 4);
     const long long grid = swizzled ? (rows + 127) / 128 * 16 * p.chunks : (p.units + kQuantThreads - 1) / kQuantThreads;
     if (grid > INT32_MAX) return RMSQ_ERR_SHAPE;
@@ -268,7 +276,7 @@ static rmsq_status quantise(bool nv, const void* input, int64_t rows, int64_t hi
     if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
     void* args[] = {&p};
     return status_of(launch_kernel(nv ? quant_fn<true>(dtype, swizzled) : quant_fn<false>(dtype, swizzled), dim3(static_cast<unsigned>(grid)),
-                                   kQuantThreads, 0, 1, static_cast<cudaStream_t>(stream), args));
+                                   swizzled ? kSwizzledThreads : kQuantThreads, 0, 1, static_cast<cudaStream_t>(stream), args));
 }
 
 }  // namespace rmsq
