@@ -193,12 +193,6 @@ __device__ __forceinline__ void fp4_clear_tail(uint32_t stage, int k, int lane)
 
 __device__ __forceinline__ float fp4_factor(const float* gs) { return gs != nullptr ? __fdiv_rn(1.0f, *gs) : 1.0f; }
 
-// A sum to the output's fp32 value.
-__device__ __forceinline__ float fp4_value(float sum, float fa, float fw, float bias)
-{
-    return fmaf(__fmul_rn(sum, fa), fw, bias);
-}
-
 // Tokens that each CTA of a cluster of nc adds up: whole fours, which a thread sends together.
 __host__ __device__ constexpr int fp4_share(int tokens, int nc) { return (tokens + 4 * nc - 1) / (4 * nc) * 4; }
 
@@ -218,45 +212,50 @@ __device__ __forceinline__ uint32_t fp4_peer(uint32_t addr, uint32_t rank)
 
 // N columns (tokens) of a lane's channel to the output: out is where the first goes, pitch the bytes to the next token's
 // row, `left` the tokens that there are, in: the channel is one. Neighbouring lanes have neighbouring channels, so
-// where their two 16-bit values are a word (the output's width is even) lanes of a pair exchange halves and each writes one
-// token's: half the stores.
-template <int DT, int N>
-__device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, long long pitch, int left, float fa, float fw, float bias, bool in, bool words)
+// where their two 16-bit values are a word (the output's width is even) lanes of a pair exchange two tokens' values and each
+// writes one token's: half the stores. (An accumulator's 128 columns a warp take longer here than short products' MMAs,
+// so instructions count: two columns at a time in packed arithmetic.)
+template <int DT, int N, bool ALL>
+__device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t pitch, int left, float2 fa, float2 fw, float2 bias, bool in, bool words)
 {
-    float f[N];
+    const bool odd = threadIdx.x & 1;
+    const uint32_t half = odd ? 0x3276u : 0x5410u;
+    char* const pair = odd ? out + pitch - 2 : out;
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = fp4_value(__uint_as_float(v[i]), fa, fw, bias);
-    if constexpr (DT != DT_F32) {
-        if (words) {
-            const bool odd = threadIdx.x & 1;
-            char* at = odd ? out + pitch - 2 : out;
-#pragma unroll
-            for (int i = 0; i < N; i += 2, at += 2 * pitch) {
-                const float other = __shfl_xor_sync(0xFFFFFFFFu, odd ? f[i] : f[i + 1], 1);
-                const uint32_t w = odd ? Scalar<DT>::put2(other, f[i + 1]) : Scalar<DT>::put2(f[i], other);
-                if (in && i + odd < left) st_u32(at, w);
+    for (int i = 0; i < N; i += 2) {
+        const float2 f = fma2(mul2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), fa), fw, bias);
+        if constexpr (DT == DT_F32) {
+            if (in && (ALL || i < left)) st_u32(out + static_cast<unsigned long long>(pitch) * i, __float_as_uint(f.x));
+            if (in && (ALL || i + 1 < left)) st_u32(out + static_cast<unsigned long long>(pitch) * (i + 1), __float_as_uint(f.y));
+        } else {
+            const uint32_t w = Scalar<DT>::put2(f.x, f.y);
+            if (words) {
+                const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, w, 1);
+                if (in && (ALL || i + odd < left)) st_u32(pair + static_cast<unsigned long long>(pitch) * i, __byte_perm(w, other, half));
+            } else {
+                if (in && (ALL || i < left)) st_u16(out + static_cast<unsigned long long>(pitch) * i, static_cast<uint16_t>(w));
+                if (in && (ALL || i + 1 < left)) st_u16(out + static_cast<unsigned long long>(pitch) * (i + 1), static_cast<uint16_t>(w >> 16));
             }
-            return;
         }
     }
-    if (!in) return;
-#pragma unroll
-    for (int i = 0; i < N; ++i, out += pitch) {
-        if (i >= left) return;
-        if constexpr (DT == DT_F32) st_u32(out, __float_as_uint(f[i]));
-        else st_u16(out, Scalar<DT>::put(f[i]));
-    }
+}
+
+template <int DT, int N>
+__device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t pitch, int left, float2 fa, float2 fw, float2 bias, bool in, bool words)
+{
+    if (left >= N && words) fp4_store<DT, N, true>(v, out, pitch, left, fa, fw, bias, in, true);
+    else fp4_store<DT, N, false>(v, out, pitch, left, fa, fw, bias, in, words);
 }
 
 template <int N>
 __device__ __forceinline__ void fp4_store(const Fp4Params& p, const uint32_t* v, long long m, long long n, int left, float fa, float fw, float bias)
 {
-    const long long pitch = p.n * (p.dt == DT_F32 ? 4 : 2);
-    char* const out = static_cast<char*>(p.out) + (m * p.n + n) * (p.dt == DT_F32 ? 4 : 2);
+    const uint32_t es = p.dt == DT_F32 ? 4 : 2, pitch = static_cast<uint32_t>(p.n) * es;
+    char* const out = static_cast<char*>(p.out) + (m * p.n + n) * es;
     const bool in = n < p.n, words = p.n % 2 == 0;
-    if (p.dt == DT_BF16) fp4_store<DT_BF16, N>(v, out, pitch, left, fa, fw, bias, in, words);
-    else if (p.dt == DT_FP16) fp4_store<DT_FP16, N>(v, out, pitch, left, fa, fw, bias, in, words);
-    else fp4_store<DT_F32, N>(v, out, pitch, left, fa, fw, bias, in, words);
+    if (p.dt == DT_BF16) fp4_store<DT_BF16, N>(v, out, pitch, left, splat(fa), splat(fw), splat(bias), in, words);
+    else if (p.dt == DT_FP16) fp4_store<DT_FP16, N>(v, out, pitch, left, splat(fa), splat(fw), splat(bias), in, words);
+    else fp4_store<DT_F32, N>(v, out, pitch, left, splat(fa), splat(fw), splat(bias), in, words);
 }
 
 template <bool NV, int NT>

@@ -166,12 +166,8 @@ rmsq_fp4_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
         uint32_t slot = 0, phase = 0, scale_slot = 0, before = SLOTS - 1, done = 0, buffer = 0;    // done: tiles
         bool there = false;                                          // the next stage, asked ahead
         for (long long tile = first; tile < ntiles && ok; tile += stride, ++done) {
-            if (done > 0) {
-                ok = mbar_wait<SCOPE_CTA>(acc_free, (done - 1) & 1u, limit);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-            }
             const uint32_t acc = tmem + (done & 1u) * S::SECOND;
-            for (int left = ok ? p.k : 0; left > 0; left -= kFp4Step) {
+            for (int left = p.k; left > 0; left -= kFp4Step) {
                 if (!there) {
                     ok = mbar_wait<SCOPE_CTA>(full + 8 * slot, phase, limit);
                     ok = __all_sync(0xFFFFFFFFu, ok);
@@ -185,17 +181,32 @@ rmsq_fp4_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     if (!ok) break;
                 }
-                tc_fence_after();
-                if (one) {
+                const auto copy = [&]() {
                     const uint32_t from = scales + scale_slot * (S::SCALES / 16), to = tmem + S::COL_S + buffer * S::COLS_S;
                     if (cut)
                         fp4_scales_cut<NV, 2, true>(from, from + S::SCALES_W / 16, to, Fp4Tail<NV>(p.k).tile, fp4_desc(base + S::AT_TAIL));
                     else
                         fp4_scales<NV, 2, true>(from, from + S::SCALES_W / 16, to);
                     tc_commit_pair(empty + 8 * before);
+                };
+                const auto multiply = [&]() {
                     const uint32_t a = codes + slot * (S::CODES / 16);
-                    fp4_mmas<NV, 2, true>(acc, a, a + S::CODES_W / 16, to, 0, idesc, (left + 63) / 64, left == p.k);
+                    fp4_mmas<NV, 2, true>(acc, a, a + S::CODES_W / 16, tmem + S::COL_S + buffer * S::COLS_S, 0, idesc, (left + 63) / 64, left == p.k);
                     if (left <= kFp4Step) tc_commit_pair(acc_full + 8 * (done & 1u));
+                };
+                tc_fence_after();
+                if (left == p.k && done > 0) {
+                    // a tile's first scales are copied while the shared columns of the last accumulator are read
+                    if (one) copy();
+                    __syncwarp();
+                    ok = mbar_wait<SCOPE_CTA>(acc_free, (done - 1) & 1u, limit);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (one) multiply();
+                } else if (one) {
+                    copy();
+                    multiply();
                 }
                 __syncwarp();
                 there = __all_sync(0xFFFFFFFFu, peek);
