@@ -295,8 +295,8 @@ rmsq_status matmul_int8(const void* input, const float* input_scale, const void*
  *                    NULL for 1
  *   output           [rows x hidden / 2] bytes, two E2M1 codes per byte (element 2k low nibble)
  *   block_scale      E4M3 / UE8M0 codes in `scale_layout`
- * Codes are the formula's, exact ties to the even code; an element whose exact quotient is within 2e-6 of a
- * rounding boundary, but not on it, may be either neighbour (NVFP4). A block with a NaN or an infinity gets scale
+ * Codes are the formula's exactly: the nearest to the exact quotient, ties to the even code, with the block's scale as
+ * stored. (That is formed from the fp32 nearest to gs * amax_b / 6.) A block with a NaN or an infinity gets scale
  * NaN (E4M3 0x7F, UE8M0 255) and any codes, so a product gives NaN for its row. Zeros may have either sign.
  * ------------------------------------------------------------------------------------------- */
 #define RMSQ_QUANT_MAX_HIDDEN 1073741824

@@ -191,7 +191,16 @@ __device__ __forceinline__ void fp4_clear_tail(uint32_t stage, int k, int lane)
     __syncwarp();
 }
 
-__device__ __forceinline__ float fp4_factor(const float* gs) { return gs != nullptr ? __fdiv_rn(1.0f, *gs) : 1.0f; }
+// 1 / (gs_a gs_w) as a sum of two floats, so that the product of a sum with it is rounded once, in effect. (Plain factors
+// where the product of the two leaves the range in which its remainder is exact.)
+__device__ __forceinline__ float2 fp4_factor(const float* a_gs, const float* w_gs)
+{
+    const float a = a_gs != nullptr ? *a_gs : 1.0f, w = w_gs != nullptr ? *w_gs : 1.0f, p = __fmul_rn(a, w);
+    if (!(fabsf(p) > 1e-30f && fabsf(p) < 1e30f)) return make_float2(__fmul_rn(__fdiv_rn(1.0f, a), __fdiv_rn(1.0f, w)), 0.f);
+    const float high = __fdiv_rn(1.0f, p);
+    const float rest = __fsub_rn(__fmaf_rn(-high, p, 1.0f), __fmul_rn(high, __fmaf_rn(a, w, -p)));
+    return make_float2(high, __fmul_rn(high, rest));
+}
 
 // Tokens that each CTA of a cluster of nc adds up: whole fours, which a thread sends together.
 __host__ __device__ constexpr int fp4_share(int tokens, int nc) { return (tokens + 4 * nc - 1) / (4 * nc) * 4; }
@@ -216,14 +225,15 @@ __device__ __forceinline__ uint32_t fp4_peer(uint32_t addr, uint32_t rank)
 // writes one token's: half the stores. (An accumulator's 128 columns a warp take longer here than short products' MMAs,
 // so instructions count: two columns at a time in packed arithmetic.)
 template <int DT, int N, bool ALL>
-__device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t pitch, int left, float2 fa, float2 fw, float2 bias, bool in, bool words)
+__device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t pitch, int left, float2 high, float2 low, float2 bias, bool in, bool words)
 {
     const bool odd = threadIdx.x & 1;
     const uint32_t half = odd ? 0x3276u : 0x5410u;
     char* const pair = odd ? out + pitch - 2 : out;
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-        const float2 f = fma2(mul2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), fa), fw, bias);
+        const float2 sum = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+        const float2 f = add2(fma2(sum, high, mul2(sum, low)), bias);
         if constexpr (DT == DT_F32) {
             if (in && (ALL || i < left)) st_u32(out + static_cast<unsigned long long>(pitch) * i, __float_as_uint(f.x));
             if (in && (ALL || i + 1 < left)) st_u32(out + static_cast<unsigned long long>(pitch) * (i + 1), __float_as_uint(f.y));
@@ -241,21 +251,21 @@ __device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t
 }
 
 template <int DT, int N>
-__device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t pitch, int left, float2 fa, float2 fw, float2 bias, bool in, bool words)
+__device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t pitch, int left, float2 high, float2 low, float2 bias, bool in, bool words)
 {
-    if (left >= N && words) fp4_store<DT, N, true>(v, out, pitch, left, fa, fw, bias, in, true);
-    else fp4_store<DT, N, false>(v, out, pitch, left, fa, fw, bias, in, words);
+    if (left >= N && words) fp4_store<DT, N, true>(v, out, pitch, left, high, low, bias, in, true);
+    else fp4_store<DT, N, false>(v, out, pitch, left, high, low, bias, in, words);
 }
 
 template <int N>
-__device__ __forceinline__ void fp4_store(const Fp4Params& p, const uint32_t* v, long long m, long long n, int left, float fa, float fw, float bias)
+__device__ __forceinline__ void fp4_store(const Fp4Params& p, const uint32_t* v, long long m, long long n, int left, float2 factor, float bias)
 {
     const uint32_t es = p.dt == DT_F32 ? 4 : 2, pitch = static_cast<uint32_t>(p.n) * es;
     char* const out = static_cast<char*>(p.out) + (m * p.n + n) * es;
     const bool in = n < p.n, words = p.n % 2 == 0;
-    if (p.dt == DT_BF16) fp4_store<DT_BF16, N>(v, out, pitch, left, splat(fa), splat(fw), splat(bias), in, words);
-    else if (p.dt == DT_FP16) fp4_store<DT_FP16, N>(v, out, pitch, left, splat(fa), splat(fw), splat(bias), in, words);
-    else fp4_store<DT_F32, N>(v, out, pitch, left, splat(fa), splat(fw), splat(bias), in, words);
+    if (p.dt == DT_BF16) fp4_store<DT_BF16, N>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
+    else if (p.dt == DT_FP16) fp4_store<DT_FP16, N>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
+    else fp4_store<DT_F32, N>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
 }
 
 template <bool NV, int NT>
@@ -406,7 +416,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
         constexpr int PARTS = S::READERS / 4;                         // of the columns
         const int row = threadIdx.x & 127, part = warp >> 2;
         const long long n = static_cast<long long>(tn) * kFp4Rows + row, m0 = static_cast<long long>(tm) * NT;
-        const float fa = fp4_factor(p.a_gs), fw = fp4_factor(p.w_gs);
+        const float2 factor = fp4_factor(p.a_gs, p.w_gs);
         const float bias = p.bias != nullptr && n < p.n ? load_as(p.bias, n, p.dt) : 0.f;
         if (nc > 1) cluster_wait();
         ok = mbar_wait<SCOPE_CTA>(acc_full, 0, limit);
@@ -423,7 +433,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                 if constexpr (LD == 32) tmem_ld_x16(acc + c + 16, v + 16);
                 tmem_wait_ld();
                 if (nc == 1) {
-                    fp4_store<LD>(p, v, m0 + c, n, tokens - c, fa, fw, bias);
+                    fp4_store<LD>(p, v, m0 + c, n, tokens - c, factor, bias);
                 } else {
 #pragma unroll
                     for (int i = 0; i < LD / 4; ++i) {
@@ -461,7 +471,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                         v.w += __uint_as_float(o[r].w);
                     }
                     const uint32_t four[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
-                    fp4_store<4>(p, four, m0 + static_cast<int>(rank) * per + 4 * i, n, own - 4 * i, fa, fw, bias);
+                    fp4_store<4>(p, four, m0 + static_cast<int>(rank) * per + 4 * i, n, own - 4 * i, factor, bias);
                 }
             }
         }

@@ -52,42 +52,87 @@ __device__ __forceinline__ float amax16(const float2 (&f)[8])
     return a;
 }
 
+// E4M3 code of gs a / 6: the quotient is formed as the nearest fp32 to the exact one (a near one and the remainders of both
+// steps), because with 16-bit elements it lies on a boundary of E4M3, or a rounding of gs away from one, far more
+// often than chance would have it.
+__device__ __forceinline__ uint32_t nvfp4_scale(float gs, float a)
+{
+    if (!(a < __int_as_float(0x7F800000))) return 0x7Fu;               // a NaN or an infinity: scale NaN
+    const float p = __fmul_rn(gs, a), q = __fmul_rn(p, 1.0f / 6.0f);
+    const float rest = __fadd_rn(__fmaf_rn(-6.0f, q, p), __fmaf_rn(gs, a, -p));
+    const float sum = __fmaf_rn(rest, 1.0f / 6.0f, q);
+    return cvt_e4m3x2(p < 3000.0f ? sum : 448.0f, 0.f) & 0xFFu;        // (above 2688 it saturates; p may be an infinity)
+}
+
+// The nearest E2M1 value to T = x gs / s, exactly, ties to even. T is first formed with a rounded factor and brought to a
+// multiple of 2^-19 by adding 24 (which is in [16, 32); |T| is at most 6.4 unless it saturates): t, off by less than 2^-19, so
+// on T's side of every boundary (a multiple of 1/4) that it is not on. Where it is on one, the sign of x gs - t s tells T's
+// side. With 16-bit elements that is frequent: boundaries are hit, or missed by a rounding of gs, whenever gs is
+// near a ratio of small numbers.
+constexpr float kNudge = 2.384185791015625e-7f;                        // 2^-22
+
+// bf16 elements: one sign for all of a tensor's. An element whose t is on a boundary m has gs within 2^-17 of m s / x, a
+// quotient of N, the odd parts of m (1, 3, 5, 7) times the significand of s (8 to 15), and one of x (128 to 255), times a
+// power of two. Different ones are at least 1 / (105 255) = 2^-14.7 apart, so there is one such quotient at most, and gs is
+// above or below it for all. Each lane tries one N with the bf16 that comes nearest. Returns what t is multiplied by: 1,
+// or 1 +- 2^-22, which moves t off the boundary to its side and, by 1.5e-6 at most, over no other (2^-19 = 1.9e-6 away).
+__device__ __forceinline__ float bf16_side(float gs)
+{
+    const int lane = threadIdx.x & 31;
+    const float n = static_cast<float>((2 * (lane & 3) + 1) * (8 + (lane >> 2)));
+    const float g = __uint_as_float((__float_as_uint(gs) & 0x7FFFFFu) | 0x3F800000u);
+    const float x = Scalar<DT_BF16>::get(Scalar<DT_BF16>::put(__fdividef(n, g)));      // (near enough: 2^-8 apart)
+    const float r = __fmaf_rn(x, g, -n);                               // its sign is exact
+    const uint32_t near = __ballot_sync(0xFFFFFFFFu, fabsf(r) <= n * 7.62939453125e-6f);          // 2^-17
+    if (near == 0) return 1.0f;
+    const float side = __shfl_sync(0xFFFFFFFFu, r, __ffs(near) - 1);
+    return side > 0.f ? 1.0f + kNudge : side < 0.f ? 1.0f - kNudge : 1.0f;
+}
+
+// Other elements: each its own sign, from a fused product and difference (t s is exact where t is on a boundary).
+__device__ __forceinline__ float2 beside(float2 t, float2 x, float gs, float s)
+{
+    const float2 r = fma2(x, splat(gs), mul2(t, splat(-s)));
+    const float step = 9.5367431640625e-7f;                            // 2^-20
+    return add2(t, make_float2(r.x == 0.f ? 0.f : copysignf(step, r.x), r.y == 0.f ? 0.f : copysignf(step, r.y)));
+}
+
 // Scale code and E2M1 codes of a thread's unit (MXFP4: of half a block, the other half being the neighbour's).
-template <bool NV> __device__ __forceinline__ uint32_t quantise16(const float2 (&f)[8], float gs, uint2& codes)
+template <int DT, bool NV> __device__ __forceinline__ uint32_t quantise16(const float2 (&f)[8], float gs, uint2& codes)
 {
     float a = amax16(f);
     uint32_t code;
-    float q[16];
+    float2 t[8];
     if (NV) {
-        code = cvt_e4m3x2(__fdiv_rn(__fmul_rn(gs, a), 6.0f), 0.f) & 0xFFu;
-        if (!(a < __int_as_float(0x7F800000))) code = 0x7Fu;           // a NaN or an infinity: scale NaN
+        code = nvfp4_scale(gs, a);
         const float s = e4m3_value(code);
         const float inv = s > 0.f ? __fdiv_rn(gs, s) : 0.f;
-        // The quotient in multiples of 2^-19 (24 is in [16, 32), and |x inv| is at most 6.4 unless it
-        // saturates): exact ties, frequent with 16-bit elements, stay ties in spite of inv's rounding.
+        if (DT == DT_BF16) {
+            const float c = bf16_side(gs);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 t = add2(fma2(f[j], splat(inv), splat(24.f)), splat(-24.f));
-            q[2 * j] = t.x;
-            q[2 * j + 1] = t.y;
+            for (int j = 0; j < 8; ++j) t[j] = fma2(fma2(f[j], splat(inv), splat(24.f)), splat(c), splat(-24.f * c));     // (24 c is exact)
+        } else {
+            uint32_t low = 0xFFFFFFFFu;                                // 0: some t is a multiple of 1/4
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 u = fma2(f[j], splat(inv), splat(24.f));
+                low = min(min(low, __float_as_uint(u.x) & 0x1FFFFu), __float_as_uint(u.y) & 0x1FFFFu);
+                t[j] = add2(u, splat(-24.f));
+            }
+            if (low == 0) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) t[j] = beside(t[j], f[j], gs, s);
+            }
         }
     } else {
         a = max3_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1), 0.f);
         code = a < __int_as_float(0x7F800000) ? ue8m0_code(a) : 255u;
         const float inv = code < 255u ? ue8m0_inv_factor(code) : 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 t = mul2(f[j], splat(inv));
-            q[2 * j] = t.x;
-            q[2 * j + 1] = t.y;
-        }
+        for (int j = 0; j < 8; ++j) t[j] = mul2(f[j], splat(inv));
     }
-    float lo[8], hi[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        lo[j] = q[j];
-        hi[j] = q[8 + j];
-    }
+    const float lo[8] = {t[0].x, t[0].y, t[1].x, t[1].y, t[2].x, t[2].y, t[3].x, t[3].y};
+    const float hi[8] = {t[4].x, t[4].y, t[5].x, t[5].y, t[6].x, t[6].y, t[7].x, t[7].y};
     codes = make_uint2(cvt_e2m1x8(lo), cvt_e2m1x8(hi));
     return code;
 }
@@ -114,7 +159,7 @@ template <int DT, bool NV> __global__ void __launch_bounds__(kQuantThreads) rmsq
         for (int j = 0; j < 8; ++j) f[j] = make_float2(0.f, 0.f);
     }
     uint2 codes;
-    const uint32_t code = quantise16<NV>(f, NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, codes);
+    const uint32_t code = quantise16<DT, NV>(f, NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, codes);
     if (in) st_v2(p.out + unit * 8, codes.x, codes.y);
     if (in && threadIdx.x % PER == 0) p.scale[unit / PER] = static_cast<unsigned char>(code);
 }
@@ -139,7 +184,7 @@ template <int DT, bool NV> __global__ void __launch_bounds__(kSwizzledThreads) r
         for (int j = 0; j < 8; ++j) f[j] = make_float2(0.f, 0.f);
     }
     uint2 codes;
-    uint32_t w = quantise16<NV>(f, NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, codes) << (8 * (u / PER & 3));
+    uint32_t w = quantise16<DT, NV>(f, NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, codes) << (8 * (u / PER & 3));
     if (in) st_v2(p.out + unit * 8, codes.x, codes.y);
     // the four scales of a tile's row come from neighbouring lanes
     w |= __shfl_xor_sync(0xFFFFFFFFu, w, PER);

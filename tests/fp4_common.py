@@ -39,11 +39,9 @@ def decoded(packed, scale, fmt):
 
 
 def nearest(t):
-    """E2M1 value nearest to t (ties to the even code), and whether t is within 2e-6 of a midpoint but not on it."""
+    """E2M1 value nearest to t, ties to the even code."""
     a, value = t.abs(), torch.zeros_like(t)
-    near = torch.zeros(t.shape, dtype=torch.bool, device=t.device)
     for i, (low, high) in enumerate(zip(VALUES, VALUES[1:])):
         mid = (low + high) / 2
         value += (high - low) * ((a >= mid) if i % 2 else (a > mid))
-        near |= ((a - mid).abs() < 2e-6) & (a != mid)
-    return torch.copysign(value, t), near
+    return torch.copysign(value, t)
