@@ -120,7 +120,7 @@ def _check(status: int, where: str):
 
 
 def _stream(device, stream):
-    return ctypes.c_void_p(_raw_stream(device.index) if stream is None else stream.cuda_stream)
+    return _raw_stream(device.index) if stream is None else stream.cuda_stream
 
 
 def _on(device):
@@ -132,7 +132,7 @@ _NOTHING = contextlib.nullcontext()
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _flat(t, H):
@@ -142,23 +142,24 @@ def _flat(t, H):
 def _prepare(input, gamma, residual, residual_output):
     if not input.is_cuda:
         raise ValueError("input must be a CUDA tensor")
-    if input.dtype not in _DT:
+    dtype, shape, index = input.dtype, input.shape, input.get_device()
+    if dtype not in _DT:
         raise TypeError("input dtype must be bfloat16, float16 or float32")
-    H = input.shape[-1]
-    x = _flat(input, H)
+    H = shape[-1]
+    x = input if len(shape) == 2 else input.reshape(-1, H)
     for name, t in (("input", x), ("gamma", gamma), ("residual", residual)):
-        if t is not None and (not t.is_contiguous() or t.dtype != input.dtype or t.device != input.device):
-            raise ValueError("%s must be a contiguous %s tensor on %s" % (name, input.dtype, input.device))
+        if t is not None and (not t.is_contiguous() or t.dtype is not dtype or t.get_device() != index):
+            raise ValueError("%s must be a contiguous %s tensor on %s" % (name, dtype, input.device))
     if gamma.shape != (H,):
         raise ValueError("gamma must have shape (%d,)" % H)
     r = None
     if residual is not None:
-        r = _flat(residual, H)
+        r = residual if residual.dim() == 2 else residual.reshape(-1, H)
         if r.shape != x.shape:
             raise ValueError("residual must have the input's shape")
         if residual_output is None:
             residual_output = torch.empty_like(input)
-        if residual_output.shape != input.shape or not residual_output.is_contiguous():
+        if residual_output.shape != shape or not residual_output.is_contiguous():
             raise ValueError("residual_output must be a contiguous tensor of the input's shape")
     elif residual_output is not None:
         raise ValueError("residual_output given without residual")
