@@ -26,22 +26,28 @@ struct QuantParams {
 
 constexpr int kQuantThreads = 256;
 
-// 16 elements as fp32 pairs.
-template <int DT> __device__ __forceinline__ void load16(const void* x, long long unit, float2 (&f)[8])
-{
-    constexpr int N = DT == DT_F32 ? 4 : 2;
-    const uint4* const p = static_cast<const uint4*>(x) + unit * N;
+// 16 elements, as they are in memory and as fp32 pairs.
+template <int DT> struct Unit {
+    static constexpr int N = DT == DT_F32 ? 4 : 2;
     uint4 v[N];
+
+    __device__ __forceinline__ void load(const void* x, long long unit, bool in)
+    {
+        const uint4* const p = static_cast<const uint4*>(x) + unit * N;
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = ld_stream_v4(p + i);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float2 t[8 / N];
-        Elem<DT>::pairs(v[i], t);
-#pragma unroll
-        for (int j = 0; j < 8 / N; ++j) f[i * (8 / N) + j] = t[j];
+        for (int i = 0; i < N; ++i) v[i] = in ? ld_stream_v4(p + i) : make_uint4(0, 0, 0, 0);
     }
-}
+    __device__ __forceinline__ void pairs(float2 (&f)[8]) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            float2 t[8 / N];
+            Elem<DT>::pairs(v[i], t);
+#pragma unroll
+            for (int j = 0; j < 8 / N; ++j) f[i * (8 / N) + j] = t[j];
+        }
+    }
+};
 
 // max |f|, NaN where one of them is.
 __device__ __forceinline__ float amax16(const float2 (&f)[8])
@@ -98,17 +104,18 @@ __device__ __forceinline__ float2 beside(float2 t, float2 x, float gs, float s)
 }
 
 // Scale code and E2M1 codes of a thread's unit (MXFP4: of half a block, the other half being the neighbour's).
-template <int DT, bool NV> __device__ __forceinline__ uint32_t quantise16(const float2 (&f)[8], float gs, uint2& codes)
+template <int DT, bool NV> __device__ __forceinline__ uint32_t quantise16(const Unit<DT>& unit, float gs, float c, uint2& codes)
 {
+    float2 f[8];
+    unit.pairs(f);
     float a = amax16(f);
     uint32_t code;
     float2 t[8];
     if (NV) {
         code = nvfp4_scale(gs, a);
         const float s = e4m3_value(code);
-        const float inv = s > 0.f ? __fdiv_rn(gs, s) : 0.f;
+        const float inv = s > 0.f ? __fmul_rn(gs, __frcp_rn(s)) : 0.f;
         if (DT == DT_BF16) {
-            const float c = bf16_side(gs);
 #pragma unroll
             for (int j = 0; j < 8; ++j) t[j] = fma2(fma2(f[j], splat(inv), splat(24.f)), splat(c), splat(-24.f * c));     // (24 c is exact)
         } else {
@@ -140,64 +147,69 @@ template <int DT, bool NV> __device__ __forceinline__ uint32_t quantise16(const 
 // CTAs go through the tensor from its end: what was written or read last before, by the kernel that made it or by
 // nvfp4_global_scale, is still in L2.
 //
-// Row-major scales: units in their order. Swizzled ones: a CTA takes kQuantChunk units of 8 rows, 2 r and 2 r + 1 of each of the
-// four groups of 32 rows that a tile of scales has, so that its scales are whole sectors: 32 bytes of each of its tiles. Measured,
-// 16384 x 8192 bf16, NVFP4 / MXFP4: 63 / 53 us in chunks of 32, 68 / 67 of 16, 68 / 55 of 64; units in their order, 4 bytes
-// of a tile at a time: 72 / 63; a warp on a tile's 8 rows, whose reads are 128 bytes of a row then: 74 / 57.
-constexpr int kQuantChunk = 32, kSwizzledThreads = 8 * kQuantChunk;
+// A thread's units are all on their way before the first is used. Row-major scales: two units, in their order. Swizzled ones:
+// four units (fp32: two); a CTA takes kQuantChunk units of 8 (4) neighbouring rows of each of the four groups of 32 rows that a
+// tile of scales has, so that its scales leave as 128 (64) neighbouring bytes of each of its tiles. Measured, 16384 x 8192 bf16
+// to NVFP4: row-major 50 us (one unit a thread: 52, four: 50); swizzled 52 us, MXFP4 49 (two units a thread: 55 / 49, one:
+// 71 / 54; chunks of 8 units instead of 16: 51 / 49, of 32: 55 / 49); fp32 to NVFP4 88 us with two units, 89 with four.
+constexpr int kQuantChunk = 16, kSwizzledThreads = 8 * kQuantChunk, kRowMajorUnits = 2;
+template <int DT> constexpr int kSwizzledUnits = DT == DT_F32 ? 2 : 4;
 
 template <int DT, bool NV> __global__ void __launch_bounds__(kQuantThreads) rmsq_quant_kernel(const QuantParams p)
 {
-    constexpr int PER = NV ? 1 : 2;                                     // units per scale
-    const long long unit = static_cast<long long>(gridDim.x - 1 - blockIdx.x) * kQuantThreads + threadIdx.x;
-    const bool in = unit < p.units;
+    constexpr int PER = NV ? 1 : 2, U = kRowMajorUnits;                 // units per scale, per thread
+    const long long first = static_cast<long long>(gridDim.x - 1 - blockIdx.x) * (U * kQuantThreads) + threadIdx.x;
     pdl_wait();
-    float2 f[8];
-    if (in) load16<DT>(p.x, unit, f);
-    else {
+    Unit<DT> x[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = make_float2(0.f, 0.f);
+    for (int i = 0; i < U; ++i) x[i].load(p.x, first + i * kQuantThreads, first + i * kQuantThreads < p.units);
+    const float gs = NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, c = NV && DT == DT_BF16 ? bf16_side(gs) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        const long long unit = first + i * kQuantThreads;
+        uint2 codes;
+        const uint32_t code = quantise16<DT, NV>(x[i], gs, c, codes);
+        if (unit >= p.units) continue;
+        st_v2(p.out + unit * 8, codes.x, codes.y);
+        if (threadIdx.x % PER == 0) p.scale[unit / PER] = static_cast<unsigned char>(code);
     }
-    uint2 codes;
-    const uint32_t code = quantise16<DT, NV>(f, NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, codes);
-    if (in) st_v2(p.out + unit * 8, codes.x, codes.y);
-    if (in && threadIdx.x % PER == 0) p.scale[unit / PER] = static_cast<unsigned char>(code);
 }
 
 template <int DT, bool NV> __global__ void __launch_bounds__(kSwizzledThreads) rmsq_quant_swizzled_kernel(const QuantParams p)
 {
     constexpr int PER = NV ? 1 : 2, SPAN = 4 * PER;                     // units per scale, per four scales
-    constexpr int TILES = kQuantChunk / SPAN;
-    __shared__ uint32_t words[TILES * 8];                               // [tile][row of two][group]: a row's four scales
+    constexpr int TILES = kQuantChunk / SPAN, U = kSwizzledUnits<DT>, NEXT = 2 * U;       // neighbouring rows of a group
+    __shared__ uint32_t words[TILES * 8 * U];                           // [tile][row of a group][group]: a row's four scales
     const unsigned block = gridDim.x - 1 - blockIdx.x;
     const unsigned strip = block / static_cast<unsigned>(p.chunks), chunk = block - strip * static_cast<unsigned>(p.chunks);
-    const int u = threadIdx.x % kQuantChunk, which = threadIdx.x / kQuantChunk;      // unit of the chunk; of the 8 rows
-    const long long row0 = static_cast<long long>(strip / 16) * 128 + strip % 16 * 2, row = row0 + (which >> 1) * 32 + (which & 1);
+    const int u = threadIdx.x % kQuantChunk, which = threadIdx.x / kQuantChunk;      // unit of the chunk; of 8 rows
+    const long long row0 = static_cast<long long>(strip / (32 / NEXT)) * 128 + strip % (32 / NEXT) * NEXT;
+    const long long row = row0 + (which >> 1) * 32 + (which & 1);
     const int in_row = static_cast<int>(chunk) * kQuantChunk + u;
-    const bool in = row < p.rows && in_row < p.row_units;
     const long long unit = row * p.row_units + in_row;
     pdl_wait();
-    float2 f[8];
-    if (in) load16<DT>(p.x, unit, f);
-    else {
+    Unit<DT> x[U];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = make_float2(0.f, 0.f);
+    for (int i = 0; i < U; ++i) x[i].load(p.x, unit + 2 * i * p.row_units, row + 2 * i < p.rows && in_row < p.row_units);
+    const float gs = NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, c = NV && DT == DT_BF16 ? bf16_side(gs) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        uint2 codes;
+        uint32_t w = quantise16<DT, NV>(x[i], gs, c, codes) << (8 * (u / PER & 3));
+        if (row + 2 * i < p.rows && in_row < p.row_units) st_v2(p.out + (unit + 2 * i * p.row_units) * 8, codes.x, codes.y);
+        // the four scales of a tile's row come from neighbouring lanes
+        w |= __shfl_xor_sync(0xFFFFFFFFu, w, PER);
+        w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2 * PER);
+        if (u % SPAN == 0) words[(u / SPAN * NEXT + 2 * i + (which & 1)) * 4 + (which >> 1)] = w;
     }
-    uint2 codes;
-    uint32_t w = quantise16<DT, NV>(f, NV && p.gs != nullptr ? __ldg(p.gs) : 1.0f, codes) << (8 * (u / PER & 3));
-    if (in) st_v2(p.out + unit * 8, codes.x, codes.y);
-    // the four scales of a tile's row come from neighbouring lanes
-    w |= __shfl_xor_sync(0xFFFFFFFFu, w, PER);
-    w |= __shfl_xor_sync(0xFFFFFFFFu, w, 2 * PER);
-    if (u % SPAN == 0) words[u / SPAN * 8 + (which & 1) * 4 + (which >> 1)] = w;
     __syncthreads();
-    if (threadIdx.x >= TILES * 8) return;
-    const int tile = threadIdx.x / 8, two = threadIdx.x / 4 & 1, group = threadIdx.x & 3;
-    const long long r = row0 + group * 32 + two;
+    if (threadIdx.x >= TILES * 8 * U) return;
+    const int tile = threadIdx.x / (4 * NEXT), of = threadIdx.x / 4 % NEXT, group = threadIdx.x & 3;
+    const long long r = row0 + group * 32 + of;
     const int scale = static_cast<int>(chunk) * (kQuantChunk / PER) + tile * 4, left = static_cast<int>(p.row_units) / PER - scale;
     if (r >= p.rows || left <= 0) return;
     unsigned char* const at = p.scale + (r / 128 * p.k_tiles + scale / 4) * 512 + r % 32 * 16 + group * 4;
-    w = words[threadIdx.x];
+    const uint32_t w = words[threadIdx.x];
     if (left >= 4) st_u32(at, w);
     else
         for (int i = 0; i < left; ++i) at[i] = static_cast<unsigned char>(w >> (8 * i));     // the padding stays
@@ -315,7 +327,8 @@ static rmsq_status quantise(bool nv, const void* input, int64_t rows, int64_t hi
     p.units = rows * p.row_units;
     p.chunks = static_cast<int>((p.row_units + kQuantChunk - 1) / kQuantChunk);
     p.k_tiles = static_cast<int>((hidden / block + 3) / 4);
-    const long long grid = swizzled ? (rows + 127) / 128 * 16 * p.chunks : (p.units + kQuantThreads - 1) / kQuantThreads;
+    const long long grid = swizzled ? (rows + 127) / 128 * (16 / (dtype == RMSQ_F32 ? kSwizzledUnits<DT_F32> : kSwizzledUnits<DT_BF16>)) * p.chunks
+                                    : (p.units + kRowMajorUnits * kQuantThreads - 1) / (kRowMajorUnits * kQuantThreads);
     if (grid > INT32_MAX) return RMSQ_ERR_SHAPE;
     DeviceView dv;
     if (!device_view(&dv)) return RMSQ_ERR_DEVICE;
