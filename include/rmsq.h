@@ -28,7 +28,11 @@
  *
  * Next to these it has layer norm and its gradients, layer norm and RMS norm to int8 codes with one
  * scale per row, and the product of such codes: layernorm, layernorm_backward, layernorm_quant_int8,
- * rmsnorm_quant_int8, matmul_int8, described with their declarations.
+ * rmsnorm_quant_int8, matmul_int8, described with their declarations. And it has what stands around
+ * the 4-bit norms in a model: quantisation to NVFP4 and MXFP4 without a norm and the global scale of
+ * such a tensor, the products of 4-bit codes, and the RMS norm of every head's query and key with the
+ * rotation by the token's position, and its gradients: quant_nvfp4, quant_mxfp4, nvfp4_global_scale,
+ * matmul_nvfp4, matmul_mxfp4, rmsnorm_rope, rmsnorm_rope_backward.
  *
  * All E4M3 / E2M1 conversions round to nearest even and saturate finite values ("satfinite").
  * A row whose FP8 scale is 0 (an all-zero y) gets codes 0 and scale 0.
@@ -43,8 +47,8 @@
  *   - Arguments are checked on the host before anything is launched; on an error nothing is
  *     launched and no output is touched.
  *   - residual and residual_output are both NULL (no residual) or both non-NULL.
- *   - Inputs must be finite; NaN / Inf inputs give unspecified codes (but see layernorm and the int8
- *     norms).
+ *   - Inputs must be finite; NaN / Inf inputs give unspecified codes (but see layernorm, the int8
+ *     norms and the entry points without a row norm).
  *   - Calls on one stream are ordered; outputs of concurrent calls must not overlap.
  */
 #ifndef RMSQ_H

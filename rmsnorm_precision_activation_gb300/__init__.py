@@ -9,6 +9,11 @@ raises.
     out, scale, res_out = rmsnorm_quant_fp8(x, gamma, residual=r, scale_ub=1200.0)
     q, block_scale, res_out = rmsnorm_quant_nvfp4(x, gamma, global_scale=gs)
     q, block_scale, res_out = rmsnorm_quant_mxfp4(x, gamma, residual=r)
+
+    gs = nvfp4_global_scale(w)
+    w4, w_scale = quant_nvfp4(w, global_scale=gs, swizzled=True)
+    out = matmul_nvfp4(q, block_scale, w4, w_scale, weight_global_scale=gs)      # (q with swizzled=True)
+    query, key = rmsnorm_rope(query, key, query_gamma, key_gamma, cos, sin, positions)
 """
 from __future__ import annotations
 
@@ -561,7 +566,7 @@ def nvfp4_global_scale(input, *, out=None, workspace=None, stream=None):
         raise ValueError("input must be a contiguous tensor")
     index, count = input.get_device(), input.numel()
     if out is None:
-        out = torch.empty((1,), dtype=torch.float32, device=input.device)
+        out = input.new_empty((1,), dtype=torch.float32)
         o = out.data_ptr()
     else:
         o = _one("out", out, index)
@@ -569,7 +574,7 @@ def nvfp4_global_scale(input, *, out=None, workspace=None, stream=None):
     if workspace is None:
         size = (_lib or lib()).nvfp4_global_scale_workspace(count)
         if size:
-            workspace = torch.empty((size,), dtype=torch.uint8, device=input.device)
+            workspace = input.new_empty((size,), dtype=torch.uint8)
             ws = workspace.data_ptr()
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the input's device")
@@ -606,13 +611,13 @@ def _quant_fp4(input, block, scale_dtype, output, block_scale, swizzled):
         raise ValueError("the last dimension must be a multiple of %d" % block)
     rows = input.numel() // H
     if output is None:
-        output = torch.empty(shape[:-1] + (H // 2,), dtype=torch.uint8, device=input.device)
+        output = input.new_empty(shape[:-1] + (H // 2,), dtype=torch.uint8)
         out = output.data_ptr()
     else:
         out = _same("output", output, shape[:-1] + (H // 2,), torch.uint8, index)
     if block_scale is None:
         sshape = (swizzled_scale_numel(rows, H, block),) if swizzled else shape[:-1] + (H // block,)
-        block_scale = torch.empty(sshape, dtype=scale_dtype, device=input.device)
+        block_scale = input.new_empty(sshape, dtype=scale_dtype)
         scale = block_scale.data_ptr()
     else:
         scale = _bytes("block_scale", block_scale, swizzled_scale_numel(rows, H, block) if swizzled else rows * (H // block),
@@ -678,7 +683,7 @@ def _matmul_fp4(input, input_scale, weight, weight_scale, block, bias, out_dtype
     if bias is not None:
         bias, b = _vector("bias", bias, N, out_dtype, index)
     if output is None:
-        output = torch.empty(oshape, dtype=out_dtype, device=input.device)
+        output = input.new_empty(oshape, dtype=out_dtype)
         out = output.data_ptr()
     else:
         out = _same("output", output, oshape, out_dtype, index)
@@ -727,7 +732,8 @@ def matmul_mxfp4(input, input_scale, weight, weight_scale, *, bias=None, out_dty
 
 def _heads(name, t, shape, dtype, index):
     """The C view of [..., heads, D], whose leading dimensions count as tokens."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or t.stride(-1) != 1:
+    stride = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or stride[-1] != 1:
         raise ValueError("%s must be a %s tensor of shape %s on the input's device, its last dimension contiguous"
                          % (name, dtype, tuple(shape)))
     if len(shape) != 3:
@@ -735,9 +741,9 @@ def _heads(name, t, shape, dtype, index):
             t = t.view((-1 if t.numel() else 0,) + tuple(shape[-2:]))
         except RuntimeError:
             raise ValueError("%s: its leading dimensions must lie behind each other" % name) from None
-    tokens, heads, _ = t.shape
-    ts, hs, _ = t.stride()
-    return HEADS.pack(t.data_ptr(), ts if tokens > 1 else 0, hs if heads > 1 else 0, heads)
+        shape, stride = t.shape, t.stride()
+    tokens, heads, _ = shape
+    return HEADS.pack(t.data_ptr(), stride[0] if tokens > 1 else 0, stride[1] if heads > 1 else 0, heads)
 
 
 def _rope(query, key, query_gamma, key_gamma, cos, sin, positions, sections, interleaved):
@@ -779,8 +785,9 @@ def _like(name, t, of, dtype, index):
     if t is not None:
         return t, _heads(name, t, of.shape, dtype, index)
     shape = of.shape
-    t = torch.empty(shape, dtype=dtype, device=of.device)
-    return t, HEADS.pack(t.data_ptr(), shape[-2] * shape[-1], shape[-1], shape[-2])
+    t = of.new_empty(shape)
+    heads, D = shape[-2:]
+    return t, HEADS.pack(t.data_ptr(), heads * D, D, heads)
 
 
 def rmsnorm_rope(query, key, query_gamma, key_gamma, cos, sin, positions, *, sections=None, interleaved=False, epsilon=1e-6,
@@ -839,18 +846,18 @@ def rmsnorm_rope_backward(grad_query, grad_key, query, key, query_gamma, key_gam
     query_grad, qo = _like("query_grad", query_grad, query, dtype, index)
     key_grad, ko = _like("key_grad", key_grad, key, dtype, index)
     if query_gamma_grad is None:
-        query_gamma_grad = torch.empty((D,), dtype=pdt, device=query.device)
+        query_gamma_grad = query.new_empty((D,), dtype=pdt)
         pq = query_gamma_grad.data_ptr()
     else:
         pq = _count("query_gamma_grad", query_gamma_grad, D, pdt, index)
     if key_gamma_grad is None:
-        key_gamma_grad = torch.empty((D,), dtype=pdt, device=query.device)
+        key_gamma_grad = query.new_empty((D,), dtype=pdt)
         pk = key_gamma_grad.data_ptr()
     else:
         pk = _count("key_gamma_grad", key_gamma_grad, D, pdt, index)
     if workspace is None:
         size = rmsnorm_rope_backward_workspace(tokens, D)
-        workspace = torch.empty((size,), dtype=torch.uint8, device=query.device)
+        workspace = query.new_empty((size,), dtype=torch.uint8)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the input's device")
     else:
