@@ -95,7 +95,6 @@ static rmsq_status prepare_rope(const RopeCall& c, RopeParams* p, int* vec)
         if (!aligned(c.gq, es) || !aligned(c.gk, es) || !aligned(r.cos, 4) || !aligned(r.sin, 4) ||
             !aligned(r.positions, r.position_bits / 8))
             return RMSQ_ERR_ALIGN;
-        while (*vec > 1 && (!aligned(c.gq, *vec * es) || !aligned(c.gk, *vec * es))) *vec /= 2;
     }
     // vectors end where the pairs' halves and the rotation do
     const auto whole = [&](int v) {
@@ -137,8 +136,8 @@ static rmsq_status prepare_rope(const RopeCall& c, RopeParams* p, int* vec)
     return RMSQ_OK;
 }
 
-// Lanes per row, turns that a warp takes of one token, and the CTAs: `most` at most, those of the queries and of the keys by
-// their turns, and no more than have an item for every warp. Fewer turns per item where there would be too few items.
+// Lanes per row, a token's turns, and the CTAs: `most` at most, those of the queries and of the keys by their turns, and no more
+// than have a turn for every warp.
 static unsigned deal_rope(RopeParams* p, int vec, bool neighbours, long long most, int warps)
 {
     // a lane holds 8 pairs, in steps of a vector (neighbours: of a pair at least)
@@ -149,13 +148,7 @@ static unsigned deal_rope(RopeParams* p, int vec, bool neighbours, long long mos
     const int rows = 32 / p->lanes;
     for (RopeSide& s : p->side) s.turns = (s.heads + kRopeRows * rows - 1) / (kRopeRows * rows);
     const long long turns[2] = {p->tokens * p->side[0].turns, p->tokens * p->side[1].turns}, all = turns[0] + turns[1];
-    p->run = 4;
-    while (p->run > 1 && all / p->run < 4 * most * warps) p->run /= 2;
-    long long need[2];
-    for (int s = 0; s < 2; ++s) {
-        p->side[s].items = (p->side[s].turns + p->run - 1) / p->run;
-        need[s] = (p->tokens * p->side[s].items + warps - 1) / warps;
-    }
+    long long need[2] = {(turns[0] + warps - 1) / warps, (turns[1] + warps - 1) / warps};
     long long q = need[0];
     if (need[0] + need[1] > most) {
         q = (most * turns[0] + all / 2) / all;

@@ -8,10 +8,10 @@
 //             dx = rstd (u - xhat <u xhat>),  dgamma = sum over tokens and heads of g xhat    (<.>: mean over D)
 //
 // A head is a short row (64 to 256 elements), so a few lanes take one: every lane holds 8 pairs (16 elements)
-// as both of their halves, and the rotation needs no exchange between lanes. A warp has 32 / lanes rows at
-// a time (a turn) and keeps its token's cosines and sines, and gamma, in registers over the heads it goes through.
+// as both of their halves, and the rotation needs no exchange between lanes. A warp has twice 32 / lanes rows of a token at
+// a time (a turn); gamma and the token's cosines and sines come to the lanes by way of shared memory.
 // Bound by HBM: each element is read and written once. Registers hold too few rows for that, so a lane's vectors come
-// through a ring of its own in shared memory by asynchronous copies, several turns ahead; nobody else reads them, so
+// through a ring of its own in shared memory by asynchronous copies, a turn ahead; nobody else reads them, so
 // nothing waits but the lane.
 #pragma once
 
@@ -28,7 +28,7 @@ struct RopeSide {                    // queries or keys: [tokens][heads][D], str
     const void* gamma;
     long long xt, xh, ot, oh, dt, dh;
     int heads;
-    int turns, items;                // per token: of heads, and runs of `run` of them
+    int turns;                       // of heads, per token
 };
 
 struct RopeParams {
@@ -42,7 +42,6 @@ struct RopeParams {
     long long places;
     int dim, half, wide;             // wide: positions are 64-bit
     int lanes;                       // per row, a power of two
-    int run;                         // turns of rows per item
     int axes;
     int until[kRopeAxes];            // frequencies below until[a] go by axis a (or one before it)
     int vec_table;                   // table rows are whole vectors of 16 bytes
@@ -159,9 +158,9 @@ template <int DT, int V> struct RopeVec {
     }
 };
 
-// Threads of a CTA and CTAs on an SM: 16 warps of 128 registers a thread, backward 12 of 168 (16 of 128 spill: 138 us,
-// 16384 tokens of 40 heads of 128 in bf16, against 84). Two slots in a ring, one turn ahead: deeper rings are slower (forward 59.2 us
-// with 2, 61.0 with 3, 65.6 with 4; backward 84.3 and 93.1), as if reads and writes got into each other's way in HBM.
+// Threads of a CTA and CTAs on an SM: 16 warps of 128 registers a thread, backward 12 of 168 (16 of 128 spill: 146 us,
+// 16384 tokens of 40 heads of 128 in bf16, against 81). Two slots in a ring, one turn ahead: with three, forward takes 53 us there
+// instead of 54, 4099 tokens of 14 heads of 80 in fp32 10.7 instead of 10.4.
 template <bool BACKWARD> struct RopeShape {
     static constexpr int THREADS = BACKWARD ? 192 : 128, CTAS = BACKWARD ? 2 : 4, STAGES = 2;
 };
@@ -240,56 +239,45 @@ template <int DT> struct RopeGamma {
     }
 };
 
-// The turns of a warp, one after another: items w, w + W, ... of a side's tokens * items, each of up to `run` turns of
-// kRopeRows * rows heads of one token (a lane has heads `rows` apart).
+// The turns of a warp, one after another: w, w + W, ... of a side's tokens * turns, each of kRopeRows * rows heads of one token
+// (a lane has heads `rows` apart). Neighbouring warps have neighbouring turns, so what an SM reads and writes at a time lies
+// together: forward takes 59 us where a warp takes four turns in a row, 56.5 with two and 54.5 so, though angles are copied for
+// every turn (16384 tokens of 40 heads of 128 in bf16, 6.3 TB/s; backward 84, 83 and 81 us, 6.3 TB/s). Heads of 192, where a
+// quarter of the lanes has nothing, lose by it: 95 and 101 us, backward 146 and 156.
 constexpr int kRopeRows = 2;
 
 struct RopeCursor {
     long long t;
-    int item, left, head;            // within the token; turns left of the item; this lane's head
-    __device__ __forceinline__ void enter(const RopeParams& p, const RopeSide& sd, int rows, int mine)
+    int turn, head;                  // of the token; this lane's first head
+    __device__ __forceinline__ void start(const RopeSide& sd, int rows, int mine, int w)
     {
-        left = min(p.run, sd.turns - item * p.run);
-        head = item * p.run * kRopeRows * rows + mine;
+        t = w / sd.turns;
+        turn = static_cast<int>(w - t * sd.turns);
+        head = turn * kRopeRows * rows + mine;
     }
-    __device__ __forceinline__ void start(const RopeParams& p, const RopeSide& sd, int rows, int mine, int w)
+    // dt, di: the warps' stride in turns, as tokens and turns.
+    __device__ __forceinline__ void next(const RopeSide& sd, int rows, int mine, int dt, int di)
     {
-        t = w / sd.items;
-        item = static_cast<int>(w - t * sd.items);
-        enter(p, sd, rows, mine);
-    }
-    // dt, di: the warps' stride in items, as tokens and items. True where an item begins.
-    __device__ __forceinline__ bool next(const RopeParams& p, const RopeSide& sd, int rows, int mine, int dt, int di)
-    {
-        head += kRopeRows * rows;
-        if (--left > 0) return false;
         t += dt;
-        item += di;
-        if (item >= sd.items) {
-            item -= sd.items;
+        turn += di;
+        if (turn >= sd.turns) {
+            turn -= sd.turns;
             ++t;
         }
-        enter(p, sd, rows, mine);
-        return true;
+        head = turn * kRopeRows * rows + mine;
     }
-};
-
-// Where a lane's row of a tensor lies: found at the start of an item, and a turn's heads on from there.
-struct RopeAt {
-    const char* p;
-    __device__ __forceinline__ void enter(const void* base, long long t, long long st, int head, long long sh, int es)
+    // Where the lane's first row of a tensor lies.
+    __device__ __forceinline__ const char* row(const void* base, long long st, long long sh, int es) const
     {
-        p = static_cast<const char*>(base) + (t * st + head * sh) * es;
+        return static_cast<const char*>(base) + (t * st + head * sh) * es;
     }
 };
 
-// A warp's cosines and sines, [slot][cosines, then sines][half]: those of the items whose rows are in the ring, so as many slots
-// as that. The warp copies a token's row of both tables together, when it starts on the rows of its first turn. Lane a
-// holds the token's place on axis a, read an item before it is needed.
+// A warp's cosines and sines, [slot][cosines, then sines][half], a slot for each turn whose rows are in the ring. The warp copies
+// its token's row of both tables together. Lane a holds the token's place on axis a, read a turn before it is needed.
 template <int STAGES> struct RopeAngles {
     uint32_t base;                       // this warp's
     long long place;
-    int ahead = 0, now = 0;              // slots
 
     static __host__ __device__ constexpr int bytes(int half) { return STAGES * 2 * ((half + 3) / 4 * 4) * 4; }
     __device__ __forceinline__ uint32_t at(const RopeParams& p, int slot, int sine) const
@@ -303,11 +291,11 @@ template <int STAGES> struct RopeAngles {
         const long long i = lane * p.tokens + t;
         place = p.wide ? static_cast<const long long*>(p.positions)[i] : static_cast<const int*>(p.positions)[i];
     }
-    // Starts the copies for the item whose token look() was given. A place outside the table reads nothing and gives NaN.
-    __device__ __forceinline__ void fetch(const RopeParams& p)
+    // Starts the copies for the turn whose token look() was given. A place outside the table reads nothing and gives NaN.
+    __device__ __forceinline__ void fetch(const RopeParams& p, int slot)
     {
         const int lane = threadIdx.x & 31;
-        const uint32_t c = at(p, ahead, 0), s = at(p, ahead, 1);
+        const uint32_t c = at(p, slot, 0), s = at(p, slot, 1);
         if (p.axes == 1 && p.vec_table) {
             const long long row = __shfl_sync(0xFFFFFFFFu, place, 0);
             const bool in = row >= 0 && row < p.places;
@@ -336,15 +324,14 @@ template <int STAGES> struct RopeAngles {
                 }
             }
         }
-        if (++ahead == STAGES) ahead = 0;
     }
     // Cosines and sines of the lane's 8 pairs (any where it has none).
     template <int V, bool INTER>
-    __device__ __forceinline__ void get(const RopeParams& p, const RopeLane<V, INTER>& lane, float (&c)[8], float (&s)[8]) const
+    __device__ __forceinline__ void get(const RopeParams& p, int slot, const RopeLane<V, INTER>& lane, float (&c)[8], float (&s)[8]) const
     {
         using Lane = RopeLane<V, INTER>;
         constexpr int PV = !INTER ? V : V > 2 ? V / 2 : 1, N = 8 / PV, L = PV < 4 ? PV : 4;     // pairs together; floats of a read
-        const uint32_t ca = at(p, now, 0), sa = at(p, now, 1);
+        const uint32_t ca = at(p, slot, 0), sa = at(p, slot, 1);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int q = max(lane.pair[Lane::of(i * PV)], 0);
@@ -355,7 +342,6 @@ template <int STAGES> struct RopeAngles {
             }
         }
     }
-    __device__ __forceinline__ void pass() { if (++now == STAGES) now = 0; }
 };
 
 // Sums over the lanes of a row, of every row of a lane.
@@ -402,26 +388,23 @@ __device__ __forceinline__ void rope_turn(float (&f)[16], const RopeLane<V, INTE
     }
 }
 
-// What the kernels do with a side's turns: fetch(stage, cursor, an item begins) starts the copies several turns ahead of
-// body(stage, cursor, an item begins); the angles of body's item are there.
+// What the kernels do with a side's turns: fetch(stage, cursor) starts the copies of a turn ahead of body(stage, cursor), when
+// they and the angles are there.
 template <int STAGES, class Fetch, class Body>
 __device__ __forceinline__ void rope_turns(const RopeParams& p, const RopeSide& sd, int rows, int mine, int w, int W,
                                            RopeAngles<STAGES>& angles, Fetch fetch, Body body)
 {
-    const int dt = W / sd.items, di = W - dt * sd.items;
+    const int dt = W / sd.turns, di = W - dt * sd.turns;
     RopeCursor ahead, now;
-    ahead.start(p, sd, rows, mine, w);
+    ahead.start(sd, rows, mine, w);
     now = ahead;
-    bool begins = true, begins_ahead = true;
     angles.look(p, ahead.t);
     const auto bring = [&](int stage) {
         if (ahead.t < p.tokens) {
-            if (begins_ahead) {
-                angles.fetch(p);
-                angles.look(p, ahead.t + dt + (ahead.item + di >= sd.items));
-            }
-            fetch(stage, ahead, begins_ahead);
-            begins_ahead = ahead.next(p, sd, rows, mine, dt, di);
+            angles.fetch(p, stage);
+            fetch(stage, ahead);
+            ahead.next(sd, rows, mine, dt, di);
+            angles.look(p, ahead.t);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -433,9 +416,8 @@ __device__ __forceinline__ void rope_turns(const RopeParams& p, const RopeSide& 
         bring(stage == 0 ? STAGES - 1 : stage - 1);
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
         __syncwarp();                                     // the angles are the warp's together
-        body(stage, now, begins);
-        begins = now.next(p, sd, rows, mine, dt, di);
-        if (begins) angles.pass();
+        body(stage, now);
+        now.next(sd, rows, mine, dt, di);
         __syncwarp();
         if (++stage == STAGES) stage = 0;
     }
@@ -465,18 +447,16 @@ __global__ void __launch_bounds__(RopeShape<false>::THREADS, RopeShape<false>::C
     pdl_wait();
     gamma.load(sd.gamma, p.dim, p.offset);
     __syncthreads();
-    RopeAt x, y;
     const long long xs = rows * sd.xh * Ring::ES, ys = rows * sd.oh * Ring::ES;          // `rows` heads on
     rope_turns<STAGES>(
         p, sd, rows, mine, cta * WARPS + warp, ctas * WARPS, angles,
-        [&](int stage, const RopeCursor& c, bool begins) {
-            if (begins) x.enter(sd.x, c.t, sd.xt, c.head, sd.xh, Ring::ES);
+        [&](int stage, const RopeCursor& c) {
+            const char* x = c.row(sd.x, sd.xt, sd.xh, Ring::ES);
 #pragma unroll
-            for (int r = 0; r < R; ++r, x.p += xs)
-                if (c.head + r * rows < sd.heads) ring.fetch(stage, r, x.p, lane);
+            for (int r = 0; r < R; ++r, x += xs)
+                if (c.head + r * rows < sd.heads) ring.fetch(stage, r, x, lane);
         },
-        [&](int stage, const RopeCursor& c, bool begins) {
-            if (begins) y.enter(sd.out, c.t, sd.ot, c.head, sd.oh, Ring::ES);
+        [&](int stage, const RopeCursor& c) {
             float f[R][16], ss[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
@@ -495,11 +475,12 @@ __global__ void __launch_bounds__(RopeShape<false>::THREADS, RopeShape<false>::C
                 }
             }
             float cs[8], sn[8];
-            angles.get(p, lane, cs, sn);
+            angles.get(p, stage, lane, cs, sn);
+            char* y = const_cast<char*>(c.row(sd.out, sd.ot, sd.oh, Ring::ES));
 #pragma unroll
-            for (int r = 0; r < R; ++r, y.p += ys) {
+            for (int r = 0; r < R; ++r, y += ys) {
                 rope_turn<false>(f[r], lane, cs, sn);
-                if (c.head + r * rows < sd.heads) rope_store<DT, V, INTER>(const_cast<char*>(y.p), lane, f[r]);
+                if (c.head + r * rows < sd.heads) rope_store<DT, V, INTER>(y, lane, f[r]);
             }
         });
 }
@@ -532,28 +513,23 @@ __global__ void __launch_bounds__(RopeShape<true>::THREADS, RopeShape<true>::CTA
     float acc[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-    RopeAt x, dy, dx;
     const long long xs = rows * sd.xh * Ring::ES, ds = rows * sd.dh * Ring::ES, os = rows * sd.oh * Ring::ES;   // `rows` heads on
     rope_turns<STAGES>(
         p, sd, rows, mine, cta * WARPS + warp, ctas * WARPS, angles,
-        [&](int stage, const RopeCursor& c, bool begins) {
-            if (begins) {
-                x.enter(sd.x, c.t, sd.xt, c.head, sd.xh, Ring::ES);
-                dy.enter(sd.dy, c.t, sd.dt, c.head, sd.dh, Ring::ES);
-            }
+        [&](int stage, const RopeCursor& c) {
+            const char *x = c.row(sd.x, sd.xt, sd.xh, Ring::ES), *dy = c.row(sd.dy, sd.dt, sd.dh, Ring::ES);
 #pragma unroll
-            for (int r = 0; r < R; ++r, x.p += xs, dy.p += ds)
+            for (int r = 0; r < R; ++r, x += xs, dy += ds)
                 if (c.head + r * rows < sd.heads) {
-                    ring.fetch(stage, r, x.p, lane);
-                    ring.fetch(stage, R + r, dy.p, lane);
+                    ring.fetch(stage, r, x, lane);
+                    ring.fetch(stage, R + r, dy, lane);
                 }
         },
-        [&](int stage, const RopeCursor& c, bool begins) {
-            if (begins) dx.enter(sd.out, c.t, sd.ot, c.head, sd.oh, Ring::ES);
+        [&](int stage, const RopeCursor& c) {
             float f[R][16], d[R][16], ss[R], dot[R];
             {
                 float cs[8], sn[8];
-                angles.get(p, lane, cs, sn);
+                angles.get(p, stage, lane, cs, sn);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
                     ring.get(stage, r, f[r]);
@@ -585,12 +561,13 @@ __global__ void __launch_bounds__(RopeShape<true>::THREADS, RopeShape<true>::CTA
                 }
             }
             rope_row_sums(dot, p.lanes);
+            char* dx = const_cast<char*>(c.row(sd.out, sd.ot, sd.oh, Ring::ES));
 #pragma unroll
-            for (int r = 0; r < R; ++r, dx.p += os) {
+            for (int r = 0; r < R; ++r, dx += os) {
                 const float2 back = splat(-dot[r] * p.inv_dim);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) rope_put(d[r], j, mul2(fma2(rope_two(f[r], j), back, rope_two(d[r], j)), splat(ss[r])));
-                if (c.head + r * rows < sd.heads) rope_store<DT, V, INTER>(const_cast<char*>(dx.p), lane, d[r]);
+                if (c.head + r * rows < sd.heads) rope_store<DT, V, INTER>(dx, lane, d[r]);
             }
         });
     __syncthreads();                                       // the rings are free: they take the warps' sums
