@@ -223,8 +223,8 @@ __device__ __forceinline__ uint32_t fp4_peer(uint32_t addr, uint32_t rank)
 // row, `left` the tokens that there are, in: the channel is one. Neighbouring lanes have neighbouring channels, so
 // where their two 16-bit values are a word (the output's width is even) lanes of a pair exchange two tokens' values and each
 // writes one token's: half the stores. (An accumulator's 128 columns a warp take longer here than short products' MMAs,
-// so instructions count: two columns at a time in packed arithmetic.)
-template <int DT, int N, bool ALL>
+// so instructions count: two columns at a time in packed arithmetic. MXFP4 has no factor.)
+template <int DT, int N, bool NV, bool ALL>
 __device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t pitch, int left, float2 high, float2 low, float2 bias, bool in, bool words)
 {
     const bool odd = threadIdx.x & 1;
@@ -233,7 +233,7 @@ __device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
         const float2 sum = make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-        const float2 f = add2(fma2(sum, high, mul2(sum, low)), bias);
+        const float2 f = add2(NV ? fma2(sum, high, mul2(sum, low)) : sum, bias);
         if constexpr (DT == DT_F32) {
             if (in && (ALL || i < left)) st_u32(out + static_cast<unsigned long long>(pitch) * i, __float_as_uint(f.x));
             if (in && (ALL || i + 1 < left)) st_u32(out + static_cast<unsigned long long>(pitch) * (i + 1), __float_as_uint(f.y));
@@ -250,22 +250,22 @@ __device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t
     }
 }
 
-template <int DT, int N>
+template <int DT, int N, bool NV>
 __device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t pitch, int left, float2 high, float2 low, float2 bias, bool in, bool words)
 {
-    if (left >= N && words) fp4_store<DT, N, true>(v, out, pitch, left, high, low, bias, in, true);
-    else fp4_store<DT, N, false>(v, out, pitch, left, high, low, bias, in, words);
+    if (left >= N && words) fp4_store<DT, N, NV, true>(v, out, pitch, left, high, low, bias, in, true);
+    else fp4_store<DT, N, NV, false>(v, out, pitch, left, high, low, bias, in, words);
 }
 
-template <int N>
+template <int N, bool NV>
 __device__ __forceinline__ void fp4_store(const Fp4Params& p, const uint32_t* v, long long m, long long n, int left, float2 factor, float bias)
 {
     const uint32_t es = p.dt == DT_F32 ? 4 : 2, pitch = static_cast<uint32_t>(p.n) * es;
     char* const out = static_cast<char*>(p.out) + (m * p.n + n) * es;
     const bool in = n < p.n, words = p.n % 2 == 0;
-    if (p.dt == DT_BF16) fp4_store<DT_BF16, N>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
-    else if (p.dt == DT_FP16) fp4_store<DT_FP16, N>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
-    else fp4_store<DT_F32, N>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
+    if (p.dt == DT_BF16) fp4_store<DT_BF16, N, NV>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
+    else if (p.dt == DT_FP16) fp4_store<DT_FP16, N, NV>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
+    else fp4_store<DT_F32, N, NV>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
 }
 
 template <bool NV, int NT>
@@ -416,7 +416,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
         constexpr int PARTS = S::READERS / 4;                         // of the columns
         const int row = threadIdx.x & 127, part = warp >> 2;
         const long long n = static_cast<long long>(tn) * kFp4Rows + row, m0 = static_cast<long long>(tm) * NT;
-        const float2 factor = fp4_factor(p.a_gs, p.w_gs);
+        const float2 factor = NV ? fp4_factor(p.a_gs, p.w_gs) : make_float2(1.f, 0.f);
         const float bias = p.bias != nullptr && n < p.n ? load_as(p.bias, n, p.dt) : 0.f;
         if (nc > 1) cluster_wait();
         ok = mbar_wait<SCOPE_CTA>(acc_full, 0, limit);
@@ -433,7 +433,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                 if constexpr (LD == 32) tmem_ld_x16(acc + c + 16, v + 16);
                 tmem_wait_ld();
                 if (nc == 1) {
-                    fp4_store<LD>(p, v, m0 + c, n, tokens - c, factor, bias);
+                    fp4_store<LD, NV>(p, v, m0 + c, n, tokens - c, factor, bias);
                 } else {
 #pragma unroll
                     for (int i = 0; i < LD / 4; ++i) {
@@ -471,7 +471,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                         v.w += __uint_as_float(o[r].w);
                     }
                     const uint32_t four[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
-                    fp4_store<4>(p, four, m0 + static_cast<int>(rank) * per + 4 * i, n, own - 4 * i, factor, bias);
+                    fp4_store<4, NV>(p, four, m0 + static_cast<int>(rank) * per + 4 * i, n, own - 4 * i, factor, bias);
                 }
             }
         }

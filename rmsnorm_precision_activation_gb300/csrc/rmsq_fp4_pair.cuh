@@ -249,7 +249,7 @@ rmsq_fp4_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
     } else if (warp >= 4) {
         const int wg = (warp - 4) >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-        const float2 factor = fp4_factor(p.a_gs, p.w_gs);
+        const float2 factor = NV ? fp4_factor(p.a_gs, p.w_gs) : make_float2(1.f, 0.f);
         uint32_t done = 0;
         for (long long tile = first; tile < ntiles && ok; tile += stride, ++done) {
             const uint32_t b = done & 1u;
@@ -279,8 +279,8 @@ rmsq_fp4_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                 }
                 const long long m0 = static_cast<long long>(tm) * kFp4PairTokens;
                 const int left = static_cast<int>(min(static_cast<long long>(kFp4PairTokens), p.m - m0));
-                fp4_store<32>(p, v, m0 + 32 * c0, n, left - 32 * c0, factor, bias);
-                fp4_store<32>(p, v + 32, m0 + 32 * c1, n, left - 32 * c1, factor, bias);
+                fp4_store<32, NV>(p, v, m0 + 32 * c0, n, left - 32 * c0, factor, bias);
+                fp4_store<32, NV>(p, v + 32, m0 + 32 * c1, n, left - 32 * c1, factor, bias);
             }
         }
         if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);

@@ -158,6 +158,22 @@ def test_scales_at_the_ends_of_their_range():
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("m", [1, 40, 130, 400])
+def test_sums_past_the_range_of_float(m, dtype):
+    """Scales of 2^100: every sum is 2^200 or more, of one sign per token."""
+    d = make(m, 200, 512, "mxfp4", seed=m, dtype=dtype)
+    d["w"] = (d["w"] | 0x11) & 0x77                        # at least 0.5, and positive
+    d["a"] = (d["a"] | 0x11) & 0x77
+    d["a"][::2] |= 0x88
+    d["sa"].fill_(227)
+    d["sw"].fill_(227)
+    d["ta"], d["tw"] = F.tiled(d["sa"], 255), F.tiled(d["sw"], 255)
+    out = call(d).float()
+    assert (out[::2] == float("-inf")).all() and (out[1::2] == float("inf")).all()
+
+
+@gpu
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_large(fmt):
     check(make(2048, 4096, 4096, fmt, seed=4))
