@@ -301,7 +301,8 @@ rmsq_status matmul_int8(const void* input, const float* input_scale, const void*
  *   block_scale      E4M3 / UE8M0 codes in `scale_layout`
  * Codes are the formula's exactly: the nearest to the exact quotient, ties to the even code, with the block's scale as
  * stored. (That is formed from the fp32 nearest to gs * amax_b / 6.) A block with a NaN or an infinity gets scale
- * NaN (E4M3 0x7F, UE8M0 255) and any codes, so a product gives NaN for its row. Zeros may have either sign.
+ * NaN (E4M3 0x7F, UE8M0 255) and any codes, so a product gives NaN for its row; so does every block where gs is a NaN
+ * (a tensor's that has one). Zeros may have either sign.
  * ------------------------------------------------------------------------------------------- */
 #define RMSQ_QUANT_MAX_HIDDEN 1073741824
 #define RMSQ_QUANT_MAX_ROWS 1073741824
@@ -441,7 +442,7 @@ const char* rmsq_status_string(rmsq_status status);
  * rmsq_device_status -- errors raised on the device since the last call, for the current device.
  * Every wait inside a kernel on a bulk-copy (mbarrier) phase is bounded in time; a wait that runs
  * out sets a flag and the CTA stops, after waiting (for four times the bound; in layernorm_backward
- * and matmul_int8 for a second at least) for the copies it has in flight. After RMSQ_ERR_TIMEOUT the
+ * and the products for a second at least) for the copies it has in flight. After RMSQ_ERR_TIMEOUT the
  * outputs of the launches since the last call are not to be trusted. If one of those drain waits ran
  * out as well (a second flag, reported the same
  * way), a CTA may have exited with a copy into its shared memory still pending; treat the CUDA

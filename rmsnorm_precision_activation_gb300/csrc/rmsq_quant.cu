@@ -67,7 +67,7 @@ __device__ __forceinline__ uint32_t nvfp4_scale(float gs, float a)
     const float p = __fmul_rn(gs, a), q = __fmul_rn(p, 1.0f / 6.0f);
     const float rest = __fadd_rn(__fmaf_rn(-6.0f, q, p), __fmaf_rn(gs, a, -p));
     const float sum = __fmaf_rn(rest, 1.0f / 6.0f, q);
-    return cvt_e4m3x2(p < 3000.0f ? sum : 448.0f, 0.f) & 0xFFu;        // (above 2688 it saturates; p may be an infinity)
+    return cvt_e4m3x2(p > 3000.0f ? 448.0f : sum, 0.f) & 0xFFu;        // (above 2688 it saturates; p may be an infinity, or NaN)
 }
 
 // The nearest E2M1 value to T = x gs / s, exactly, ties to even. T is first formed with a rounded factor and brought to a

@@ -136,6 +136,17 @@ def test_blocks_that_are_not_finite(fmt, dtype, swizzled):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_the_global_scale_of_a_tensor_with_a_nan(dtype):
+    x = make(40, 256, dtype, 4)
+    x[7, 9] = float("nan")
+    gs = rq().nvfp4_global_scale(x)
+    assert torch.isnan(gs).all()
+    s = rq().quant_nvfp4(x, global_scale=gs)[1]
+    assert bool((s.view(torch.uint8) == 0x7F).all())
+
+
+@gpu
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("rows,blocks", [(5, 3), (130, 6), (128, 8)])
 def test_nothing_else_is_written(fmt, rows, blocks):
