@@ -160,7 +160,8 @@ template <int DT, int V> struct RopeVec {
 
 // Threads of a CTA and CTAs on an SM: 16 warps of 128 registers a thread, backward 12 of 168 (16 of 128 spill: 146 us,
 // 16384 tokens of 40 heads of 128 in bf16, against 81). Two slots in a ring, one turn ahead: with three, forward takes 53 us there
-// instead of 54, 4099 tokens of 14 heads of 80 in fp32 10.7 instead of 10.4.
+// instead of 54, 4099 tokens of 14 heads of 80 in fp32 10.7 instead of 10.2. Forward with 20 warps of 96 registers: heads of 96 47 us
+// instead of 49.5, but 32 + 32 heads of 128 93 instead of 85 and of 256 112 instead of 108.
 template <bool BACKWARD> struct RopeShape {
     static constexpr int THREADS = BACKWARD ? 192 : 128, CTAS = BACKWARD ? 2 : 4, STAGES = 2;
 };
