@@ -86,7 +86,8 @@ __device__ __forceinline__ float bf16_side(float gs)
 {
     const int lane = threadIdx.x & 31;
     const float n = static_cast<float>((2 * (lane & 3) + 1) * (8 + (lane >> 2)));
-    const float g = __uint_as_float((__float_as_uint(gs) & 0x7FFFFFu) | 0x3F800000u);
+    const float normal = gs < 1e-37f ? gs * 1.8446744073709552e19f : gs;               // (2^64)
+    const float g = __uint_as_float((__float_as_uint(normal) & 0x7FFFFFu) | 0x3F800000u);
     const float x = Scalar<DT_BF16>::get(Scalar<DT_BF16>::put(__fdividef(n, g)));      // (near enough: 2^-8 apart)
     const float r = __fmaf_rn(x, g, -n);                               // its sign is exact
     const uint32_t near = __ballot_sync(0xFFFFFFFFu, fabsf(r) <= n * 7.62939453125e-6f);          // 2^-17
@@ -114,6 +115,12 @@ template <int DT, bool NV> __device__ __forceinline__ uint32_t quantise16(const 
     if (NV) {
         code = nvfp4_scale(gs, a);
         const float s = e4m3_value(code);
+        // (a block below the normal floats, under the gs of a tensor as small: gs / s would leave their range at the top)
+        if (a < 1e-30f && s > 0.f) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = mul2(f[j], splat(1.099511627776e12f));            // 2^40
+            gs *= 9.094947017729282379e-13f;
+        }
         const float inv = s > 0.f ? __fmul_rn(gs, __frcp_rn(s)) : 0.f;
         if (DT == DT_BF16) {
 #pragma unroll

@@ -136,6 +136,30 @@ def test_blocks_that_are_not_finite(fmt, dtype, swizzled):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("power", [-105, -118, -124, -128])
+def test_tensors_at_the_small_end_of_float(dtype, power):
+    """Their global scale is as large as a float can be, and blocks below the normal floats have zeros among their elements."""
+    g = torch.Generator(device="cuda").manual_seed(-power)
+    x = torch.randn((64, 512), generator=g, device="cuda", dtype=torch.float64)
+    x = x * torch.exp2(-8.0 * torch.rand((64, 32), generator=g, device="cuda", dtype=torch.float64)).repeat_interleave(16, 1)
+    x[:, ::5] = 0.0
+    x = (x * 2.0 ** power).float().to(dtype)
+    assert bool((x != 0).any())
+    check(x, "nvfp4", float(rq().nvfp4_global_scale(x)))
+    check(x, "nvfp4", float(rq().nvfp4_global_scale(x)), swizzled=True)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_global_scale_below_the_normal_floats(dtype):
+    x = make(64, 512, torch.float32, 6)
+    x = (x / x.abs().max() * 2.0 ** 127).to(dtype)
+    for gs in (1e-38, 3e-39, 2.0 ** -130 * 1.25):
+        check(x, "nvfp4", gs)
+
+
+@gpu
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_the_global_scale_of_a_tensor_with_a_nan(dtype):
     x = make(40, 256, dtype, 4)
