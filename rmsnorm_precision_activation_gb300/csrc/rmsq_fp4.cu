@@ -38,7 +38,7 @@ template <bool NV, int NT> static cudaError_t launch_tile(Fp4Params& p, const Fp
     if (ctas > INT32_MAX) return cudaErrorInvalidConfiguration;
     void* args[] = {&map_w, &map_a, &map_sw, &map_sa, &p, &t};
     return launch_kernel(reinterpret_cast<const void*>(&rmsq_fp4_tile_kernel<NV, NT>), dim3(static_cast<unsigned>(ctas)), S::THREADS,
-                         S::SMEM, cluster, stream, args);
+                         S::smem(cluster == 1), cluster, stream, args);
 }
 
 template <bool NV> static cudaError_t launch_pair(Fp4Params& p, const Fp4Operands& o, const DeviceView& dv, cudaStream_t stream)
@@ -89,12 +89,12 @@ template <bool NV, int NT> static void plan_tile(const Fp4Params& p, const Devic
     for (int c = 1; c <= 8 && c <= steps && (c == 1 || c * tiles <= slots); ++c) {
         if (c > 1 && c * fp4_share(tokens, c) > S::SUM_ROWS) continue;
         const long long waves = (tiles * c + slots - 1) / slots, each = (tiles * c + dv.sms - 1) / dv.sms;   // CTAs of an SM
-        const long long stage = most(most(S::STAGE * (each < S::CTAS ? each : S::CTAS) / 76, 400), 3600 / S::STAGES);
+        const long long stage = most(most(S::STAGE * (each < S::CTAS ? each : S::CTAS) / 76, 400), 3600 / S::stages(c == 1));
         const long long join = c > 1 ? 1500 + 24LL * tokens * (c - 1) / c : 8LL * tokens;
         const long long cycles = (NT < 64 ? 2500 : 3000) * waves + most(waves * ((steps + c - 1) / c) * stage, weight_cycles(p, NV)) + join;
         if (best->tokens != 0 && cycles >= best->cycles) continue;
         // (what fits goes by the device's clusters of SMs, not by SMs alone)
-        if (c > 1 && tiles > resident_clusters(fn, S::THREADS, S::SMEM, c)) continue;
+        if (c > 1 && tiles > resident_clusters(fn, S::THREADS, S::smem(false), c)) continue;
         *best = {cycles, NT, c};
     }
 }

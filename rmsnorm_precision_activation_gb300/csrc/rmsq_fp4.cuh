@@ -59,16 +59,19 @@ template <bool NV, int NT> struct Fp4Shape {
     // sums from the cluster's CTAs, [rank][four tokens][channel][4]
     static constexpr int SUM_ROWS = NT + 16, SUMS = SUM_ROWS * kFp4Rows * 4;
     static constexpr int MOST = (CTAS == 2 ? 113 : 226) * 1024;
-    static constexpr int STAGES = (MOST - 2048 - SUMS) / STAGE;
-    static constexpr int SMEM = 2048 + STAGES * STAGE + SUMS;         // 1024 to align the ring, 1024 for barriers
+    // stages of the ring, and shared memory in all (1024 to align the ring, 1024 for barriers): a CTA that has a tile's k
+    // to itself needs no room for sums
+    static __host__ __device__ constexpr int stages(bool alone) { return (MOST - 2048 - (alone ? 0 : SUMS)) / STAGE; }
+    static __host__ __device__ constexpr int smem(bool alone) { return 2048 + stages(alone) * STAGE + (alone ? 0 : SUMS); }
     // TMEM: the accumulator, then two buffers of scales (the channels', the tokens')
     static constexpr int ACC = NT < 32 ? 32 : NT;
     static constexpr int COLS_S = 4 * fp4_tiles<NV>() * (1 + ROW_TILES);
     static constexpr int NEED = ACC + 2 * COLS_S;
     static constexpr int COLS = NEED <= 128 ? 128 : NEED <= 256 ? 256 : 512;
     static_assert(STAGE % 1024 == 0 && AT_A % 1024 == 0 && AT_SW % 1024 == 0, "swizzle atoms");
-    static_assert(SMEM <= 232448 && COLS * CTAS <= 512, "fits the SM");
-    static_assert(SMEM * (CTAS + 1) > 233472 - 1024 * CTAS, "no more CTAs on an SM than TMEM has columns for");
+    static_assert(MOST <= 232448 && COLS * CTAS <= 512, "fits the SM");
+    static_assert((smem(true) < smem(false) ? smem(true) : smem(false)) * (CTAS + 1) > 233472 - 1024 * CTAS,
+                  "no more CTAs on an SM than TMEM has columns for");
 };
 
 // The low word of a descriptor of what lies at a shared-memory address (the high words are constant; both kinds of
@@ -268,6 +271,11 @@ __device__ __forceinline__ void fp4_store(const Fp4Params& p, const uint32_t* v,
     else fp4_store<DT_F32, N, NV>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
 }
 
+// This thread's warp, from a lane of it: a number that the compiler knows to be the warp's own. What a warp does alone then stays
+// in its uniform registers, which descriptors and barriers are taken from (by threadIdx alone every operand is moved
+// there first: 610 cycles instead of 530 to issue a stage at 128 tokens, 8192^3 155 us instead of 151).
+__device__ __forceinline__ int fp4_warp() { return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0); }
+
 template <bool NV, int NT>
 __global__ void __launch_bounds__(Fp4Shape<NV, NT>::THREADS, Fp4Shape<NV, NT>::CTAS)
 rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
@@ -275,16 +283,19 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                      const TcTiles tiles)
 {
     using S = Fp4Shape<NV, NT>;
-    constexpr int STAGES = S::STAGES, LOADER = S::READERS, ISSUER = LOADER + 1;
+    constexpr int LOADER = S::READERS, ISSUER = LOADER + 1;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t tmem_slot;
 
-    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const uint32_t sums = ring + STAGES * S::STAGE, full = sums + S::SUMS;
-    const uint32_t empty = full + 8 * STAGES, acc_full = empty + 8 * STAGES, drain = acc_full + 8, received = drain + 8;
-
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = fp4_warp();
     const uint32_t nc = cluster_size(), rank = cluster_rank();
+    constexpr int joined = S::stages(false), alone = S::stages(true);
+    const int stages = nc == 1 ? alone : joined;
+
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t sums = ring + stages * S::STAGE, full = sums + (nc == 1 ? 0 : S::SUMS);
+    const uint32_t empty = full + 8 * stages, acc_full = empty + 8 * stages, drain = acc_full + 8, received = drain + 8;
+
     int tn, tm;
     tc_tile(cluster_id(), tiles, tn, tm);
 
@@ -315,7 +326,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
             prefetch_map(&map_a);
             prefetch_map(&map_sw);
             prefetch_map(&map_sa);
-            for (int i = 0; i < STAGES; ++i) {
+            for (int i = 0; i < stages; ++i) {
                 mbar_init(full + 8 * i, 1);
                 mbar_init(empty + 8 * i, 1);
             }
@@ -329,7 +340,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
         __syncwarp();
         // the first loads run while the CTA sets itself up
         pdl_wait_alone();
-        for (; started < STAGES && started < steps; ++started)
+        for (; started < stages && started < steps; ++started)
             if (one) fetch(static_cast<uint32_t>(started), started);
         __syncwarp();
     }
@@ -351,20 +362,24 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
 
     if (warp == LOADER) {
         const bool one = elect_one();
-        int s = started;
-        for (; s < steps; ++s) {
-            const uint32_t slot = static_cast<uint32_t>(s % STAGES);
-            ok = mbar_wait<SCOPE_CTA>(empty + 8 * slot, (static_cast<uint32_t>(s / STAGES) & 1u) ^ 1u, limit);
+        int s = started, slot = 0;
+        uint32_t phase = 0;
+        for (; s < steps; ++s) {                                       // (only where the first loads filled the ring)
+            ok = mbar_wait<SCOPE_CTA>(empty + 8 * slot, phase, limit);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok) break;
             if (one) fetch(slot, s);
             __syncwarp();
+            if (++slot == stages) {
+                slot = 0;
+                phase ^= 1u;
+            }
         }
         if (lane == 0) {
             // the copies in flight end before the CTA does, whichever role stopped waiting
             bool drained = true;
-            for (int i = s > STAGES ? s - STAGES : 0; i < s; ++i)
-                drained &= mbar_wait<SCOPE_CTA>(full + 8 * (i % STAGES), static_cast<uint32_t>(i / STAGES) & 1u, drain_limit);
+            for (int i = s > stages ? s - stages : 0; i < s; ++i)
+                drained &= mbar_wait<SCOPE_CTA>(full + 8 * (i % stages), static_cast<uint32_t>(i / stages) & 1u, drain_limit);
             if (!ok || !drained) atomicOr(p.err, drained ? ERRF_WAIT_TIMEOUT : ERRF_WAIT_TIMEOUT | ERRF_DRAIN_TIMEOUT);
         }
         __syncwarp();
@@ -377,11 +392,18 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
         // 0 or 2: an MMA takes the scales from even columns only, so tiles of fewer tokens are for the first alone
         const uint32_t tokens_from = NT == 64 ? (static_cast<uint32_t>(tm) & 1u) * 2u : 0u;
         const bool one = elect_one();
-        uint32_t slot = 0, phase = 0;
+        int slot = 0;
+        uint32_t phase = 0;
+        bool there = false;                                           // the next stage, asked ahead
         for (int s = 0; s < steps; ++s) {
-            ok = mbar_wait<SCOPE_CTA>(full + 8 * slot, phase, limit);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
+            if (!there) {
+                ok = mbar_wait<SCOPE_CTA>(full + 8 * slot, phase, limit);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+            }
+            const int next = slot + 1 == stages ? 0 : slot + 1;
+            const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+            const bool peek = mbar_test<SCOPE_CTA>(full + 8 * next, next_phase);
             const uint32_t stage = ring + slot * S::STAGE;
             const int left = p.k - (s0 + s) * kFp4Step;               // elements of k from this stage on
             if (left < kFp4Step && left % 64 != 0) fp4_clear_tail<NV, S::ROW_TILES, S::AT_SW, S::AT_SA>(stage, p.k, lane);
@@ -395,10 +417,9 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                 if (s == steps - 1) tc_commit(acc_full);
             }
             __syncwarp();
-            if (++slot == STAGES) {
-                slot = 0;
-                phase ^= 1u;
-            }
+            there = __all_sync(0xFFFFFFFFu, peek);
+            slot = next;
+            phase = next_phase;
         }
         if (one) {
             // the MMAs in flight end before TMEM is freed, whichever role stopped waiting

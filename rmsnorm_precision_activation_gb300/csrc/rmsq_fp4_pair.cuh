@@ -78,7 +78,7 @@ rmsq_fp4_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
     const uint32_t full = base + S::AT_BARS, empty = full + 8 * SLOTS, acc_full = empty + 8 * SLOTS;
     const uint32_t acc_free = acc_full + 16, tail_full = acc_free + 8, drain = tail_full + 8;
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = fp4_warp();
     const int rank = static_cast<int>(cluster_rank());
 
     const int steps = (p.k + kFp4Step - 1) / kFp4Step;
