@@ -4,11 +4,13 @@
 // each brings its own 128 channels, half of the tokens, its channels' scales and all of the tokens' (both
 // tensor cores multiply by all columns), and holds the sums of its channels for all of the tokens.
 //
-// What bounds it is how far the loads run ahead: a stage (256 elements of k, 38 KB a CTA) is 512 cycles of MMA, and from
+// What bounds it is the power that the GPU may take (8192^3 runs at 1.8 GHz instead of 2.07, and at 1.6 where products follow
+// one another), then how far the loads run ahead: a stage (256 elements of k, 38 KB a CTA) is 512 cycles of MMA, and from
 // the MMAs that free a slot to the next ones that can use it pass about 2500 (word to the loading warps, the load, word
-// to the MMA warp, its queue). So
+// to the MMA warp, its queue). 8192^3 takes 270 000 cycles, the MMAs alone 229 000. With five slots instead of six: 155 us instead
+// of 150, with four 178; with three quarters of the MMAs 132. So
 //   - the copies of both CTAs arrive on the leader's barrier themselves (passed on by a warp of the other CTA instead:
-//     160 us at 8192^3; that warp's arrival with release at cluster scope takes 1400 cycles: 357 us);
+//     5 us more at 8192^3; that warp's arrival with release at cluster scope takes 1400 cycles: 357 us);
 //   - codes have six slots, which leaves room for five of scales. Those are free earlier, once copied to TMEM: the
 //     commit that follows a stage's scale copies and precedes its MMAs frees the codes of the stage before and the scales of
 //     this one, so one barrier serves both;
