@@ -29,7 +29,7 @@ template <bool NV, int NT> static cudaError_t launch_tile(Fp4Params& p, const Fp
     using S = Fp4Shape<NV, NT>;
     CUtensorMap map_w, map_a, map_sw, map_sa;
     if (!encode<NV>(&map_w, &map_sw, o.w, o.sw, p.n, p.k, kFp4Rows, 1) ||
-        !encode<NV>(&map_a, &map_sa, o.a, o.sa, p.m, p.k, NT, S::ROW_TILES))
+        !encode<NV>(&map_a, &map_sa, o.a, o.sa, p.m, p.k, p.m < NT ? static_cast<int>(p.m) : NT, S::ROW_TILES))
         return cudaErrorUnknown;
     TcTiles t;
     t.n_tiles = static_cast<int>((p.n + kFp4Rows - 1) / kFp4Rows);
@@ -61,18 +61,19 @@ template <bool NV> static cudaError_t launch_pair(Fp4Params& p, const Fp4Operand
 
 // What a call takes in each kernel, in cycles, by the parts of its time that were measured (GB300, 2.07 GHz), and with
 // it the choice of kernel, tile and cluster. Sizes only: the same call always takes the same one.
-//   - Before the first product and after the last 2500 to 3000 cycles pass in every wave of CTAs (pairs 9500).
-//   - A stage takes as long as its bytes (76 a cycle and SM), as its issue (400; pairs 600), or as a load's latency under
-//     load over the stages in flight (3600, so three stages of 32 tokens are slower than six of 64).
-//   - The weight comes from HBM at 3200 bytes a cycle at most.
+//   - Before the first product and after the last 2500 to 3500 cycles pass in every wave of CTAs (pairs 9500).
+//   - A stage takes as long as its bytes (60 a cycle and SM), as its issue (450; pairs 600), or, where there are more than
+//     the ring has slots, as a load's latency under load over the stages in flight (3600, so three stages of 32 tokens are
+//     slower than six of 64).
+//   - The weight comes from HBM at 3200 bytes a cycle at most, and at 32 to an SM.
 //   - CTAs that share a tile's k spend 1500 cycles on joining their sums, and 24 for every token they send.
 // Measured, in us, NVFP4, tokens x channels x k, tokens of a tile / CTAs that share its k:
-//   1 x 1024 x 4096: 16/8 2.8, 16/4 3.2, 16/1 5.6;  1 x 8192 x 8192: 16/2 9.4, 16/1 10.8
-//   24 x 8192 x 8192: 64/2 9.3, 32/2 10.4;  24 x 28672 x 8192: 32/1 23.1, 64/1 27.8
+//   1 x 1024 x 4096: 16/8 2.8, 16/4 3.2, 16/1 5.6;  1 x 7168 x 8192: 16/4 7.9, 16/2 8.9, 16/1 10.6
+//   24 x 8192 x 8192: 64/2 9.1, 32/2 10.3;  24 x 28672 x 8192: 32/1 22.9, 64/1 26.9
 //   128 x 1024 x 4096: 64/6 4.3, 128/6 5.0, pair 9.2;  128 x 8192 x 8192: 64/1 10.9, 128/2 11.8, pair 14.5
 //   256 x 8192 x 8192: 128/1 11.6, pair 13.7, 64/1 20.6;  256 x 28672 x 8192: pair 30.9, 128/1 37.3
 //   512 x 1024 x 4096: 64/2 6.0, pair 8.4;  512 x 8192 x 8192: pair 14.5, 128/1 21.8
-// Over 182 such sizes in both formats the choice takes 1 % longer than the best one on average, 10 % at most.
+// Over 154 such sizes in both formats the choice takes 1 % longer than the best one on average, 10 % at most.
 struct Fp4Plan {
     long long cycles;
     int tokens, cluster;              // tokens of a tile; 0: none yet
@@ -91,12 +92,15 @@ template <bool NV, int NT> static void plan_tile(const Fp4Params& p, const Devic
     for (int c = 1; c <= 8 && c <= steps && (c == 1 || c * tiles <= slots); ++c) {
         if (c > 1 && c * fp4_share(tokens, c) > S::SUM_ROWS) continue;
         const long long waves = (tiles * c + slots - 1) / slots, each = (tiles * c + dv.sms - 1) / dv.sms;   // CTAs of an SM
-        const long long stage = most(most(S::STAGE * (each < S::CTAS ? each : S::CTAS) / 76, 400), 3600 / S::stages(c == 1));
+        const int mine = (steps + c - 1) / c, ring = S::stages(c == 1);
+        const long long stage = most(most(S::STAGE * (each < S::CTAS ? each : S::CTAS) / 60, 450), mine > ring ? 3600 / ring : 0);
         const long long join = c > 1 ? 1500 + 24LL * tokens * (c - 1) / c : 8LL * tokens;
-        const long long cycles = (NT < 64 ? 2500 : 3000) * waves + most(waves * ((steps + c - 1) / c) * stage, weight_cycles(p, NV)) + join;
+        // (tiles of other tokens find the weight in L2)
+        const long long weight = most(weight_cycles(p, NV), p.m <= NT ? each * mine * (S::CODES_W + S::SCALES_W) / 32 : 0);
+        const long long cycles = (NT < 64 ? 2500 : NT < 128 ? 3000 : 3500) * waves + most(waves * mine * stage, weight) + join;
         if (best->tokens != 0 && cycles >= best->cycles) continue;
-        // (what fits goes by the device's clusters of SMs, not by SMs alone)
-        if (c > 1 && tiles > resident_clusters(fn, S::THREADS, S::smem(false), c)) continue;
+        // (what fits goes by the device's clusters of SMs, not by SMs alone; they are counted with one CTA on an SM)
+        if (c > 1 && tiles > static_cast<long long>(S::CTAS) * resident_clusters(fn, S::THREADS, S::smem(false), c)) continue;
         *best = {cycles, NT, c};
     }
 }
