@@ -566,7 +566,7 @@ def nvfp4_global_scale(input, *, out=None, workspace=None, stream=None):
         raise ValueError("input must be a contiguous tensor")
     index, count = input.get_device(), input.numel()
     if out is None:
-        out = input.new_empty((1,), dtype=torch.float32)
+        out = torch.empty((1,), dtype=torch.float32, device=input.device)
         o = out.data_ptr()
     else:
         o = _one("out", out, index)
@@ -574,7 +574,7 @@ def nvfp4_global_scale(input, *, out=None, workspace=None, stream=None):
     if workspace is None:
         size = (_lib or lib()).nvfp4_global_scale_workspace(count)
         if size:
-            workspace = input.new_empty((size,), dtype=torch.uint8)
+            workspace = torch.empty((size,), dtype=torch.uint8, device=input.device)
             ws = workspace.data_ptr()
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the input's device")
@@ -611,13 +611,13 @@ def _quant_fp4(input, block, scale_dtype, output, block_scale, swizzled):
         raise ValueError("the last dimension must be a multiple of %d" % block)
     rows = input.numel() // H
     if output is None:
-        output = input.new_empty(shape[:-1] + (H // 2,), dtype=torch.uint8)
+        output = torch.empty(shape[:-1] + (H // 2,), dtype=torch.uint8, device=input.device)
         out = output.data_ptr()
     else:
         out = _same("output", output, shape[:-1] + (H // 2,), torch.uint8, index)
     if block_scale is None:
         sshape = (swizzled_scale_numel(rows, H, block),) if swizzled else shape[:-1] + (H // block,)
-        block_scale = input.new_empty(sshape, dtype=scale_dtype)
+        block_scale = torch.empty(sshape, dtype=scale_dtype, device=input.device)
         scale = block_scale.data_ptr()
     else:
         scale = _bytes("block_scale", block_scale, swizzled_scale_numel(rows, H, block) if swizzled else rows * (H // block),
@@ -683,7 +683,7 @@ def _matmul_fp4(input, input_scale, weight, weight_scale, block, bias, out_dtype
     if bias is not None:
         bias, b = _vector("bias", bias, N, out_dtype, index)
     if output is None:
-        output = input.new_empty(oshape, dtype=out_dtype)
+        output = torch.empty(oshape, dtype=out_dtype, device=input.device)
         out = output.data_ptr()
     else:
         out = _same("output", output, oshape, out_dtype, index)
@@ -785,7 +785,7 @@ def _like(name, t, of, dtype, index):
     if t is not None:
         return t, _heads(name, t, of.shape, dtype, index)
     shape = of.shape
-    t = of.new_empty(shape)
+    t = torch.empty(shape, dtype=dtype, device=of.device)
     heads, D = shape[-2:]
     return t, HEADS.pack(t.data_ptr(), heads * D, D, heads)
 
@@ -846,18 +846,18 @@ def rmsnorm_rope_backward(grad_query, grad_key, query, key, query_gamma, key_gam
     query_grad, qo = _like("query_grad", query_grad, query, dtype, index)
     key_grad, ko = _like("key_grad", key_grad, key, dtype, index)
     if query_gamma_grad is None:
-        query_gamma_grad = query.new_empty((D,), dtype=pdt)
+        query_gamma_grad = torch.empty((D,), dtype=pdt, device=query.device)
         pq = query_gamma_grad.data_ptr()
     else:
         pq = _count("query_gamma_grad", query_gamma_grad, D, pdt, index)
     if key_gamma_grad is None:
-        key_gamma_grad = query.new_empty((D,), dtype=pdt)
+        key_gamma_grad = torch.empty((D,), dtype=pdt, device=query.device)
         pk = key_gamma_grad.data_ptr()
     else:
         pk = _count("key_gamma_grad", key_gamma_grad, D, pdt, index)
     if workspace is None:
         size = rmsnorm_rope_backward_workspace(tokens, D)
-        workspace = query.new_empty((size,), dtype=torch.uint8)
+        workspace = torch.empty((size,), dtype=torch.uint8, device=query.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the input's device")
     else:
