@@ -39,19 +39,22 @@ static rmsq_status check_side(const rmsq_heads* s, int64_t tokens, int64_t dim, 
     return RMSQ_OK;
 }
 
-template <int DT, int V, bool INTER> static const void* rope_at(bool backward)
+template <int DT, int V, bool BOTH> static const void* rope_at(bool inter, bool backward)
 {
-    return backward ? reinterpret_cast<const void*>(&rmsq_rope_bwd_kernel<DT, V, INTER>)
-                    : reinterpret_cast<const void*>(&rmsq_rope_kernel<DT, V, INTER>);
+    if (inter)
+        return backward ? reinterpret_cast<const void*>(&rmsq_rope_bwd_kernel<DT, V, true, BOTH>)
+                        : reinterpret_cast<const void*>(&rmsq_rope_kernel<DT, V, true, BOTH>);
+    return backward ? reinterpret_cast<const void*>(&rmsq_rope_bwd_kernel<DT, V, false, BOTH>)
+                    : reinterpret_cast<const void*>(&rmsq_rope_kernel<DT, V, false, BOTH>);
 }
 
-template <int DT> static const void* rope_fn(int vec, bool inter, bool backward)
+template <int DT, bool BOTH> static const void* rope_fn(int vec, bool inter, bool backward)
 {
     if constexpr (DT != DT_F32)
-        if (vec == 8) return inter ? rope_at<DT, 8, true>(backward) : rope_at<DT, 8, false>(backward);
-    if (vec == 4) return inter ? rope_at<DT, 4, true>(backward) : rope_at<DT, 4, false>(backward);
-    if (vec == 2) return inter ? rope_at<DT, 2, true>(backward) : rope_at<DT, 2, false>(backward);
-    return inter ? rope_at<DT, 1, true>(backward) : rope_at<DT, 1, false>(backward);
+        if (vec == 8) return rope_at<DT, 8, BOTH>(inter, backward);
+    if (vec == 4) return rope_at<DT, 4, BOTH>(inter, backward);
+    // (narrow vectors, of odd sizes and places, are slow for other reasons)
+    return vec == 2 ? rope_at<DT, 2, true>(inter, backward) : rope_at<DT, 1, true>(inter, backward);
 }
 
 struct RopeCall {
@@ -108,18 +111,18 @@ static rmsq_status prepare_rope(const RopeCall& c, RopeParams* p, int* vec)
     for (int s = 0; s < 2; ++s) {
         RopeSide& d = p->side[s];
         d.x = in[s]->data;
-        d.xt = in[s]->token_stride;
-        d.xh = in[s]->head_stride;
+        d.xt = static_cast<unsigned>(in[s]->token_stride);
+        d.xh = static_cast<unsigned>(in[s]->head_stride);
         d.out = out[s]->data;
-        d.ot = out[s]->token_stride;
-        d.oh = out[s]->head_stride;
+        d.ot = static_cast<unsigned>(out[s]->token_stride);
+        d.oh = static_cast<unsigned>(out[s]->head_stride);
         d.gamma = gamma[s];
         d.heads = static_cast<int>(in[s]->heads);
     }
     p->cos = r.cos;
     p->sin = r.sin;
     p->positions = r.positions;
-    p->tokens = c.tokens;
+    p->tokens = static_cast<int>(c.tokens);
     p->places = r.places;
     p->dim = static_cast<int>(c.dim);
     p->half = half;
@@ -136,7 +139,7 @@ static rmsq_status prepare_rope(const RopeCall& c, RopeParams* p, int* vec)
     return RMSQ_OK;
 }
 
-// Lanes per row, a token's turns, and the CTAs: `most` at most, those of the queries and of the keys by their turns, and no more
+// Lanes per row, a token's groups, and the CTAs: `most` at most, those of the queries and of the keys by their turns, and no more
 // than have a turn for every warp.
 static unsigned deal_rope(RopeParams* p, int vec, bool neighbours, long long most, int warps)
 {
@@ -146,8 +149,13 @@ static unsigned deal_rope(RopeParams* p, int vec, bool neighbours, long long mos
     p->lanes = 1;
     while (p->lanes < units) p->lanes *= 2;
     const int rows = 32 / p->lanes;
-    for (RopeSide& s : p->side) s.turns = (s.heads + kRopeRows * rows - 1) / (kRopeRows * rows);
-    const long long turns[2] = {p->tokens * p->side[0].turns, p->tokens * p->side[1].turns}, all = turns[0] + turns[1];
+    long long turns[2];
+    for (int s = 0; s < 2; ++s) {
+        RopeSide& d = p->side[s];
+        d.groups = (d.heads + rows - 1) / rows;
+        turns[s] = (static_cast<long long>(p->tokens) * d.groups + kRopeRows - 1) / kRopeRows;
+    }
+    const long long all = turns[0] + turns[1];
     long long need[2] = {(turns[0] + warps - 1) / warps, (turns[1] + warps - 1) / warps};
     long long q = need[0];
     if (need[0] + need[1] > most) {
@@ -161,11 +169,19 @@ static unsigned deal_rope(RopeParams* p, int vec, bool neighbours, long long mos
     return static_cast<unsigned>(q + need[1]);
 }
 
-static const void* rope_kernel(int dtype, int vec, bool neighbours, bool backward)
+template <bool BOTH> static const void* rope_kernel(int dtype, int vec, bool neighbours, bool backward)
 {
-    return dtype == RMSQ_BF16   ? rope_fn<DT_BF16>(vec, neighbours, backward)
-           : dtype == RMSQ_FP16 ? rope_fn<DT_FP16>(vec, neighbours, backward)
-                                : rope_fn<DT_F32>(vec, neighbours, backward);
+    return dtype == RMSQ_BF16   ? rope_fn<DT_BF16, BOTH>(vec, neighbours, backward)
+           : dtype == RMSQ_FP16 ? rope_fn<DT_FP16, BOTH>(vec, neighbours, backward)
+                                : rope_fn<DT_F32, BOTH>(vec, neighbours, backward);
+}
+
+// Whether a turn may have rows of two tokens, or the kernel allows for it.
+static bool two_tokens(const RopeParams& p, int vec) { return vec < 4 || p.side[0].groups % 2 != 0 || p.side[1].groups % 2 != 0; }
+
+static const void* rope_kernel(const RopeParams& p, int dtype, int vec, bool neighbours, bool backward)
+{
+    return two_tokens(p, vec) ? rope_kernel<true>(dtype, vec, neighbours, backward) : rope_kernel<false>(dtype, vec, neighbours, backward);
 }
 
 static rmsq_status status_of(cudaError_t e)
@@ -175,11 +191,12 @@ static rmsq_status status_of(cudaError_t e)
     return RMSQ_ERR_LAUNCH;
 }
 
-template <bool BACKWARD> static int rope_smem(const RopeParams& p, int dtype)
+template <bool BACKWARD> static int rope_smem(const RopeParams& p, int dtype, int vec)
 {
     using S = RopeShape<BACKWARD>;
     return S::STAGES * 16 * (dtype == RMSQ_F32 ? 4 : 2) * S::THREADS * kRopeRows * (BACKWARD ? 2 : 1) +
-           S::THREADS / 32 * RopeAngles<S::STAGES>::bytes(p.half) + (p.dim + 3) / 4 * 16;
+           S::THREADS / 32 * (two_tokens(p, vec) ? RopeAngles<S::STAGES, true>::bytes(p.half) : RopeAngles<S::STAGES, false>::bytes(p.half)) +
+           (p.dim + 3) / 4 * 16;
 }
 
 }  // namespace rmsq
@@ -202,7 +219,7 @@ extern "C" rmsq_status rmsnorm_rope(const rmsq_heads* query, const rmsq_heads* k
     using S = RopeShape<false>;
     const unsigned grid = deal_rope(&p, vec, neighbours, dv.sms * S::CTAS, S::THREADS / 32);
     void* args[] = {&p};
-    return status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, false), dim3(grid), S::THREADS, rope_smem<false>(p, dtype), 1,
+    return status_of(launch_kernel(rope_kernel(p, dtype, vec, neighbours, false), dim3(grid), S::THREADS, rope_smem<false>(p, dtype, vec), 1,
                                    static_cast<cudaStream_t>(stream), args));
 }
 
@@ -233,8 +250,8 @@ extern "C" rmsq_status rmsnorm_rope_backward(const rmsq_heads* grad_query, const
         if (st != RMSQ_OK) return st;
         if (grads[s]->heads != p.side[s].heads) return RMSQ_ERR_SHAPE;
         p.side[s].dy = grads[s]->data;
-        p.side[s].dt = grads[s]->token_stride;
-        p.side[s].dh = grads[s]->head_stride;
+        p.side[s].dt = static_cast<unsigned>(grads[s]->token_stride);
+        p.side[s].dh = static_cast<unsigned>(grads[s]->head_stride);
     }
     if (!grad_query_gamma || !grad_key_gamma) return RMSQ_ERR_NULL;
     if (!aligned(grad_query_gamma, 16) || !aligned(grad_key_gamma, 16)) return RMSQ_ERR_ALIGN;
@@ -260,7 +277,7 @@ extern "C" rmsq_status rmsnorm_rope_backward(const rmsq_heads* grad_query, const
         r.rows[0] = p.split;
         r.rows[1] = static_cast<int>(grid) - p.split;
         void* args[] = {&p};
-        st = status_of(launch_kernel(rope_kernel(dtype, vec, neighbours, true), dim3(grid), S::THREADS, rope_smem<true>(p, dtype), 1,
+        st = status_of(launch_kernel(rope_kernel(p, dtype, vec, neighbours, true), dim3(grid), S::THREADS, rope_smem<true>(p, dtype, vec), 1,
                                      static_cast<cudaStream_t>(stream), args));
         if (st != RMSQ_OK) return st;
     }

@@ -8,7 +8,7 @@
 //             dx = rstd (u - xhat <u xhat>),  dgamma = sum over tokens and heads of g xhat    (<.>: mean over D)
 //
 // A head is a short row (64 to 256 elements), so a few lanes take one: every lane holds 8 pairs (16 elements)
-// as both of their halves, and the rotation needs no exchange between lanes. A warp has twice 32 / lanes rows of a token at
+// as both of their halves, and the rotation needs no exchange between lanes. A warp has two groups of 32 / lanes rows at
 // a time (a turn); gamma and the token's cosines and sines come to the lanes by way of shared memory.
 // Bound by HBM: each element is read and written once. Registers hold too few rows for that, so a lane's vectors come
 // through a ring of its own in shared memory by asynchronous copies, a turn ahead; nobody else reads them, so
@@ -26,9 +26,9 @@ struct RopeSide {                    // queries or keys: [tokens][heads][D], str
     void* out;                       // y, or dx
     const void* dy;                  // backward
     const void* gamma;
-    long long xt, xh, ot, oh, dt, dh;
+    unsigned xt, xh, ot, oh, dt, dh; // (below 2^31)
     int heads;
-    int turns;                       // of heads, per token
+    int groups;                      // of heads that a warp takes at a time, per token
 };
 
 struct RopeParams {
@@ -38,7 +38,7 @@ struct RopeParams {
     const void* positions;           // [axes][tokens]
     float* part;                     // backward: [CTAs][D]
     int split;                       // CTAs that take queries; the others take keys
-    long long tokens;
+    int tokens;
     long long places;
     int dim, half, wide;             // wide: positions are 64-bit
     int lanes;                       // per row, a power of two
@@ -160,8 +160,8 @@ template <int DT, int V> struct RopeVec {
 
 // Threads of a CTA and CTAs on an SM: 16 warps of 128 registers a thread, backward 12 of 168 (16 of 128 spill: 146 us,
 // 16384 tokens of 40 heads of 128 in bf16, against 81). Two slots in a ring, one turn ahead: with three, forward takes 53 us there
-// instead of 54, 4099 tokens of 14 heads of 80 in fp32 10.7 instead of 10.2. Forward with 20 warps of 96 registers: heads of 96 47 us
-// instead of 49.5, but 32 + 32 heads of 128 93 instead of 85 and of 256 112 instead of 108.
+// instead of 54, 4099 tokens of 14 heads of 80 in fp32 10.7 instead of 10.2 (two groups of one token a turn). Forward with 20 warps of 96
+// registers: heads of 96 47 us instead of 49.5, but 32 + 32 heads of 128 93 instead of 85 and of 256 112 instead of 108.
 template <bool BACKWARD> struct RopeShape {
     static constexpr int THREADS = BACKWARD ? 192 : 128, CTAS = BACKWARD ? 2 : 4, STAGES = 2;
 };
@@ -240,65 +240,90 @@ template <int DT> struct RopeGamma {
     }
 };
 
-// The turns of a warp, one after another: w, w + W, ... of a side's tokens * turns, each of kRopeRows * rows heads of one token
-// (a lane has heads `rows` apart). Neighbouring warps have neighbouring turns, so what an SM reads and writes at a time lies
-// together: forward takes 59 us where a warp takes four turns in a row, 56.5 with two and 54.5 so, though angles are copied for
-// every turn (16384 tokens of 40 heads of 128 in bf16, 6.3 TB/s; backward 84, 83 and 81 us, 6.3 TB/s). Heads of 192, where a
-// quarter of the lanes has nothing, lose by it: 95 and 101 us, backward 146 and 156.
+// The turns of a warp, one after another: w, w + W, ... of a side's, each two of its tokens * groups groups of heads, which follow one
+// another: the second is the next token's first where the first is its token's last, so that few heads, or an odd
+// number of groups, leave no half of a turn empty (4099 tokens of 12 + 2 heads of 80 in fp32: 9.0 us, with two groups of one
+// token a turn 10.1). Kernels of their own do that (BOTH): where both sides' groups are even no turn has two tokens, and
+// allowing for it takes 56.5 us instead of 54.5 below. Neighbouring warps have neighbouring turns, so what an SM reads and writes at a time
+// lies together: forward takes 59 us where a warp takes four turns in a row, 56.5 with two and 54.5 so, though angles are
+// copied for every turn (16384 tokens of 40 heads of 128 in bf16, 6.3 TB/s; backward 84, 83 and 80 us, 6.4 TB/s). Heads of 192,
+// where a quarter of the lanes has nothing, lose by it: 95 and 98 us, backward 146 and 156.
 constexpr int kRopeRows = 2;
 
 struct RopeCursor {
-    long long t;
-    int turn, head;                  // of the token; this lane's first head
-    __device__ __forceinline__ void start(const RopeSide& sd, int rows, int mine, int w)
+    int t, group;                    // of the first group
+    __device__ __forceinline__ void start(const RopeSide& sd, int w)
     {
-        t = w / sd.turns;
-        turn = static_cast<int>(w - t * sd.turns);
-        head = turn * kRopeRows * rows + mine;
+        t = 2 * w / sd.groups;
+        group = 2 * w - t * sd.groups;
     }
-    // dt, di: the warps' stride in turns, as tokens and turns.
-    __device__ __forceinline__ void next(const RopeSide& sd, int rows, int mine, int dt, int di)
+    // dt, di: the warps' stride, as tokens and groups.
+    __device__ __forceinline__ void next(const RopeSide& sd, int dt, int di)
     {
         t += dt;
-        turn += di;
-        if (turn >= sd.turns) {
-            turn -= sd.turns;
+        group += di;
+        if (group >= sd.groups) {
+            group -= sd.groups;
             ++t;
         }
-        head = turn * kRopeRows * rows + mine;
     }
-    // Where the lane's first row of a tensor lies.
-    __device__ __forceinline__ const char* row(const void* base, long long st, long long sh, int es) const
+    // Whether the second group is the next token's.
+    __device__ __forceinline__ bool splits(const RopeSide& sd) const { return group + 1 == sd.groups; }
+};
+
+// A lane's rows of a turn. Where a tensor's lie: first() and, `rows` heads on or in the next token, second().
+template <bool BOTH> struct RopeRows {
+    int t, head, mine;
+    bool split, in[2];
+    __device__ __forceinline__ RopeRows(const RopeParams& p, const RopeSide& sd, const RopeCursor& c, int rows, int mine_)
     {
-        return static_cast<const char*>(base) + (t * st + head * sh) * es;
+        t = c.t;
+        mine = mine_;
+        head = c.group * rows + mine;
+        split = BOTH && c.splits(sd);
+        in[0] = head < sd.heads;
+        in[1] = split ? mine < sd.heads && t + 1 < p.tokens : head + rows < sd.heads;
+    }
+    static __device__ __forceinline__ char* at(const void* base, int t, int head, unsigned st, unsigned sh, int es)
+    {
+        const unsigned long long e = static_cast<unsigned long long>(static_cast<unsigned>(t)) * st +
+                                     static_cast<unsigned long long>(static_cast<unsigned>(head)) * sh;
+        return const_cast<char*>(static_cast<const char*>(base)) + e * static_cast<unsigned>(es);
+    }
+    __device__ __forceinline__ char* first(const void* base, unsigned st, unsigned sh, int es) const { return at(base, t, head, st, sh, es); }
+    __device__ __forceinline__ char* second(char* first, unsigned long long step, const void* base, unsigned st, unsigned sh, int es) const
+    {
+        return split ? at(base, t + 1, mine, st, sh, es) : first + step;
     }
 };
 
-// A warp's cosines and sines, [slot][cosines, then sines][half], a slot for each turn whose rows are in the ring. The warp copies
-// its token's row of both tables together. Lane a holds the token's place on axis a, read a turn before it is needed.
-template <int STAGES> struct RopeAngles {
+// A warp's cosines and sines, [slot][token of a turn][cosines, then sines][half], a slot for each turn whose rows are in the ring. The
+// warp copies its tokens' rows of both tables together. Lane a holds the first token's place on axis a, lane 16 + a
+// the second's, read a turn before it is needed.
+template <int STAGES, bool BOTH> struct RopeAngles {
     uint32_t base;                       // this warp's
     long long place;
 
-    static __host__ __device__ constexpr int bytes(int half) { return STAGES * 2 * ((half + 3) / 4 * 4) * 4; }
-    __device__ __forceinline__ uint32_t at(const RopeParams& p, int slot, int sine) const
+    static __host__ __device__ constexpr int bytes(int half) { return STAGES * (1 + BOTH) * 2 * ((half + 3) / 4 * 4) * 4; }
+    __device__ __forceinline__ uint32_t at(const RopeParams& p, int slot, int second, int sine) const
     {
-        return base + static_cast<uint32_t>((slot * 2 + sine) * ((p.half + 3) / 4 * 4) * 4);
+        return base + static_cast<uint32_t>(((slot * (1 + BOTH) + second) * 2 + sine) * ((p.half + 3) / 4 * 4) * 4);
     }
-    __device__ __forceinline__ void look(const RopeParams& p, long long t)
+    __device__ __forceinline__ void look(const RopeParams& p, int t)
     {
-        const int lane = threadIdx.x & 31;
-        if (lane >= p.axes || t >= p.tokens) return;
-        const long long i = lane * p.tokens + t;
+        const int lane = threadIdx.x & 31, axis = lane & 15;
+        if (BOTH) t += lane >> 4;
+        if (axis >= p.axes || t >= p.tokens) return;
+        const long long i = static_cast<long long>(axis) * p.tokens + t;
         place = p.wide ? static_cast<const long long*>(p.positions)[i] : static_cast<const int*>(p.positions)[i];
     }
-    // Starts the copies for the turn whose token look() was given. A place outside the table reads nothing and gives NaN.
-    __device__ __forceinline__ void fetch(const RopeParams& p, int slot)
+    // Starts the copies for a token of the turn whose first token look() was given. A place outside the table reads nothing and gives NaN.
+    __device__ __forceinline__ void fetch(const RopeParams& p, int slot, int second)
     {
         const int lane = threadIdx.x & 31;
-        const uint32_t c = at(p, slot, 0), s = at(p, slot, 1);
+        const uint32_t c = at(p, slot, second, 0), s = at(p, slot, second, 1);
         if (p.axes == 1 && p.vec_table) {
-            const long long row = __shfl_sync(0xFFFFFFFFu, place, 0);
+            const long long row = __shfl_sync(0xFFFFFFFFu, place, 16 * second);
             const bool in = row >= 0 && row < p.places;
             for (int i = lane; i < p.half / 2; i += 32) {                 // the cosines' vectors, then the sines'
                 const int sine = i >= p.half / 4, v = 4 * (i - sine * (p.half / 4));
@@ -314,7 +339,7 @@ template <int STAGES> struct RopeAngles {
                 int axis = 0;
 #pragma unroll
                 for (int a = 0; a < kRopeAxes - 1; ++a) axis += i >= p.until[a];
-                const long long row = __shfl_sync(0xFFFFFFFFu, place, axis);
+                const long long row = __shfl_sync(0xFFFFFFFFu, place, 16 * second + axis);
                 if (i >= p.half) continue;
                 if (row >= 0 && row < p.places) {
                     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(c + i * 4), "l"(p.cos + row * p.half + i) : "memory");
@@ -328,11 +353,11 @@ template <int STAGES> struct RopeAngles {
     }
     // Cosines and sines of the lane's 8 pairs (any where it has none).
     template <int V, bool INTER>
-    __device__ __forceinline__ void get(const RopeParams& p, int slot, const RopeLane<V, INTER>& lane, float (&c)[8], float (&s)[8]) const
+    __device__ __forceinline__ void get(const RopeParams& p, int slot, int second, const RopeLane<V, INTER>& lane, float (&c)[8], float (&s)[8]) const
     {
         using Lane = RopeLane<V, INTER>;
         constexpr int PV = !INTER ? V : V > 2 ? V / 2 : 1, N = 8 / PV, L = PV < 4 ? PV : 4;     // pairs together; floats of a read
-        const uint32_t ca = at(p, slot, 0), sa = at(p, slot, 1);
+        const uint32_t ca = at(p, slot, second, 0), sa = at(p, slot, second, 1);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int q = max(lane.pair[Lane::of(i * PV)], 0);
@@ -391,20 +416,20 @@ __device__ __forceinline__ void rope_turn(float (&f)[16], const RopeLane<V, INTE
 
 // What the kernels do with a side's turns: fetch(stage, cursor) starts the copies of a turn ahead of body(stage, cursor), when
 // they and the angles are there.
-template <int STAGES, class Fetch, class Body>
-__device__ __forceinline__ void rope_turns(const RopeParams& p, const RopeSide& sd, int rows, int mine, int w, int W,
-                                           RopeAngles<STAGES>& angles, Fetch fetch, Body body)
+template <int STAGES, bool BOTH, class Fetch, class Body>
+__device__ __forceinline__ void rope_turns(const RopeParams& p, const RopeSide& sd, int w, int W, RopeAngles<STAGES, BOTH>& angles, Fetch fetch, Body body)
 {
-    const int dt = W / sd.turns, di = W - dt * sd.turns;
+    const int dt = 2 * W / sd.groups, di = 2 * W - dt * sd.groups;
     RopeCursor ahead, now;
-    ahead.start(sd, rows, mine, w);
+    ahead.start(sd, w);
     now = ahead;
     angles.look(p, ahead.t);
     const auto bring = [&](int stage) {
         if (ahead.t < p.tokens) {
-            angles.fetch(p, stage);
+            angles.fetch(p, stage, 0);
+            if (BOTH && ahead.splits(sd) && ahead.t + 1 < p.tokens) angles.fetch(p, stage, 1);
             fetch(stage, ahead);
-            ahead.next(sd, rows, mine, dt, di);
+            ahead.next(sd, dt, di);
             angles.look(p, ahead.t);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -418,7 +443,7 @@ __device__ __forceinline__ void rope_turns(const RopeParams& p, const RopeSide& 
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
         __syncwarp();                                     // the angles are the warp's together
         body(stage, now);
-        now.next(sd, rows, mine, dt, di);
+        now.next(sd, dt, di);
         __syncwarp();
         if (++stage == STAGES) stage = 0;
     }
@@ -426,7 +451,7 @@ __device__ __forceinline__ void rope_turns(const RopeParams& p, const RopeSide& 
 }
 
 // Two rows of a lane at a time: two chains of dependent instructions in flight, and half the bookkeeping.
-template <int DT, int V, bool INTER>
+template <int DT, int V, bool INTER, bool BOTH>
 __global__ void __launch_bounds__(RopeShape<false>::THREADS, RopeShape<false>::CTAS) rmsq_rope_kernel(const __grid_constant__ RopeParams p)
 {
     using Lane = RopeLane<V, INTER>;
@@ -441,21 +466,22 @@ __global__ void __launch_bounds__(RopeShape<false>::THREADS, RopeShape<false>::C
     Lane lane;
     lane.init(l, p.lanes, p.dim, p.half);
     const Ring ring = {smem_u32(smem)};
-    RopeAngles<STAGES> angles;
-    angles.base = smem_u32(smem) + Ring::BYTES + warp * RopeAngles<STAGES>::bytes(p.half);
-    const RopeGamma<DT> gamma = {smem_u32(smem) + Ring::BYTES + WARPS * RopeAngles<STAGES>::bytes(p.half)};
+    RopeAngles<STAGES, BOTH> angles;
+    angles.base = smem_u32(smem) + Ring::BYTES + warp * RopeAngles<STAGES, BOTH>::bytes(p.half);
+    const RopeGamma<DT> gamma = {smem_u32(smem) + Ring::BYTES + WARPS * RopeAngles<STAGES, BOTH>::bytes(p.half)};
     ring.clear();
     pdl_wait();
     gamma.load(sd.gamma, p.dim, p.offset);
     __syncthreads();
-    const long long xs = rows * sd.xh * Ring::ES, ys = rows * sd.oh * Ring::ES;          // `rows` heads on
-    rope_turns<STAGES>(
-        p, sd, rows, mine, cta * WARPS + warp, ctas * WARPS, angles,
+    const unsigned long long xs = 1ull * rows * sd.xh * Ring::ES, ys = 1ull * rows * sd.oh * Ring::ES;      // `rows` heads on
+    rope_turns<STAGES, BOTH>(
+        p, sd, cta * WARPS + warp, ctas * WARPS, angles,
         [&](int stage, const RopeCursor& c) {
-            const char* x = c.row(sd.x, sd.xt, sd.xh, Ring::ES);
-#pragma unroll
-            for (int r = 0; r < R; ++r, x += xs)
-                if (c.head + r * rows < sd.heads) ring.fetch(stage, r, x, lane);
+            const RopeRows<BOTH> row(p, sd, c, rows, mine);
+            char* x = row.first(sd.x, sd.xt, sd.xh, Ring::ES);
+            if (row.in[0]) ring.fetch(stage, 0, x, lane);
+            x = row.second(x, xs, sd.x, sd.xt, sd.xh, Ring::ES);
+            if (row.in[1]) ring.fetch(stage, 1, x, lane);
         },
         [&](int stage, const RopeCursor& c) {
             float f[R][16], ss[R];
@@ -476,20 +502,22 @@ __global__ void __launch_bounds__(RopeShape<false>::THREADS, RopeShape<false>::C
                 }
             }
             float cs[8], sn[8];
-            angles.get(p, stage, lane, cs, sn);
-            char* y = const_cast<char*>(c.row(sd.out, sd.ot, sd.oh, Ring::ES));
-#pragma unroll
-            for (int r = 0; r < R; ++r, y += ys) {
-                rope_turn<false>(f[r], lane, cs, sn);
-                if (c.head + r * rows < sd.heads) rope_store<DT, V, INTER>(y, lane, f[r]);
-            }
+            const RopeRows<BOTH> row(p, sd, c, rows, mine);
+            char* y = row.first(sd.out, sd.ot, sd.oh, Ring::ES);
+            angles.get(p, stage, 0, lane, cs, sn);
+            rope_turn<false>(f[0], lane, cs, sn);
+            if (row.in[0]) rope_store<DT, V, INTER>(y, lane, f[0]);
+            if (row.split) angles.get(p, stage, 1, lane, cs, sn);
+            y = row.second(y, ys, sd.out, sd.ot, sd.oh, Ring::ES);
+            rope_turn<false>(f[1], lane, cs, sn);
+            if (row.in[1]) rope_store<DT, V, INTER>(y, lane, f[1]);
         });
 }
 
 // A lane has the same elements in every row and adds their part of gamma's gradient in registers. The row groups of a warp
 // are joined by exchanges, the warps of a CTA through shared memory, the CTAs by rmsq_rope_reduce_kernel, all in a
 // fixed order.
-template <int DT, int V, bool INTER>
+template <int DT, int V, bool INTER, bool BOTH>
 __global__ void __launch_bounds__(RopeShape<true>::THREADS, RopeShape<true>::CTAS) rmsq_rope_bwd_kernel(const __grid_constant__ RopeParams p)
 {
     using Lane = RopeLane<V, INTER>;
@@ -504,9 +532,9 @@ __global__ void __launch_bounds__(RopeShape<true>::THREADS, RopeShape<true>::CTA
     Lane lane;
     lane.init(l, p.lanes, p.dim, p.half);
     const Ring ring = {smem_u32(smem)};
-    RopeAngles<STAGES> angles;
-    angles.base = smem_u32(smem) + Ring::BYTES + warp * RopeAngles<STAGES>::bytes(p.half);
-    const RopeGamma<DT> gamma = {smem_u32(smem) + Ring::BYTES + WARPS * RopeAngles<STAGES>::bytes(p.half)};
+    RopeAngles<STAGES, BOTH> angles;
+    angles.base = smem_u32(smem) + Ring::BYTES + warp * RopeAngles<STAGES, BOTH>::bytes(p.half);
+    const RopeGamma<DT> gamma = {smem_u32(smem) + Ring::BYTES + WARPS * RopeAngles<STAGES, BOTH>::bytes(p.half)};
     ring.clear();
     pdl_wait();
     gamma.load(sd.gamma, p.dim, p.offset);
@@ -514,25 +542,31 @@ __global__ void __launch_bounds__(RopeShape<true>::THREADS, RopeShape<true>::CTA
     float acc[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) acc[j] = 0.f;
-    const long long xs = rows * sd.xh * Ring::ES, ds = rows * sd.dh * Ring::ES, os = rows * sd.oh * Ring::ES;   // `rows` heads on
-    rope_turns<STAGES>(
-        p, sd, rows, mine, cta * WARPS + warp, ctas * WARPS, angles,
+    const unsigned long long xs = 1ull * rows * sd.xh * Ring::ES, ds = 1ull * rows * sd.dh * Ring::ES, os = 1ull * rows * sd.oh * Ring::ES;
+    rope_turns<STAGES, BOTH>(
+        p, sd, cta * WARPS + warp, ctas * WARPS, angles,
         [&](int stage, const RopeCursor& c) {
-            const char *x = c.row(sd.x, sd.xt, sd.xh, Ring::ES), *dy = c.row(sd.dy, sd.dt, sd.dh, Ring::ES);
-#pragma unroll
-            for (int r = 0; r < R; ++r, x += xs, dy += ds)
-                if (c.head + r * rows < sd.heads) {
-                    ring.fetch(stage, r, x, lane);
-                    ring.fetch(stage, R + r, dy, lane);
-                }
+            const RopeRows<BOTH> row(p, sd, c, rows, mine);
+            char *x = row.first(sd.x, sd.xt, sd.xh, Ring::ES), *dy = row.first(sd.dy, sd.dt, sd.dh, Ring::ES);
+            if (row.in[0]) {
+                ring.fetch(stage, 0, x, lane);
+                ring.fetch(stage, R, dy, lane);
+            }
+            x = row.second(x, xs, sd.x, sd.xt, sd.xh, Ring::ES);
+            dy = row.second(dy, ds, sd.dy, sd.dt, sd.dh, Ring::ES);
+            if (row.in[1]) {
+                ring.fetch(stage, 1, x, lane);
+                ring.fetch(stage, R + 1, dy, lane);
+            }
         },
         [&](int stage, const RopeCursor& c) {
+            const RopeRows<BOTH> row(p, sd, c, rows, mine);
             float f[R][16], d[R][16], ss[R], dot[R];
             {
                 float cs[8], sn[8];
-                angles.get(p, stage, lane, cs, sn);
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
+                    if (r == 0 || row.split) angles.get(p, stage, r, lane, cs, sn);
                     ring.get(stage, r, f[r]);
                     ring.get(stage, R + r, d[r]);
                     ss[r] = rope_dot(f[r], f[r]);
@@ -543,12 +577,11 @@ __global__ void __launch_bounds__(RopeShape<true>::THREADS, RopeShape<true>::CTA
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 ss[r] = rope_rstd(ss[r], p);
-                const bool in = c.head + r * rows < sd.heads;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     rope_put(f[r], j, mul2(rope_two(f[r], j), splat(ss[r])));
                     // (a lane without a row has anything here)
-                    if (in) rope_put(acc, j, fma2(rope_two(d[r], j), rope_two(f[r], j), rope_two(acc, j)));
+                    if (row.in[r]) rope_put(acc, j, fma2(rope_two(d[r], j), rope_two(f[r], j), rope_two(acc, j)));
                 }
             }
             {
@@ -562,13 +595,14 @@ __global__ void __launch_bounds__(RopeShape<true>::THREADS, RopeShape<true>::CTA
                 }
             }
             rope_row_sums(dot, p.lanes);
-            char* dx = const_cast<char*>(c.row(sd.out, sd.ot, sd.oh, Ring::ES));
+            char* dx = nullptr;
 #pragma unroll
-            for (int r = 0; r < R; ++r, dx += os) {
+            for (int r = 0; r < R; ++r) {
                 const float2 back = splat(-dot[r] * p.inv_dim);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) rope_put(d[r], j, mul2(fma2(rope_two(f[r], j), back, rope_two(d[r], j)), splat(ss[r])));
-                if (c.head + r * rows < sd.heads) rope_store<DT, V, INTER>(dx, lane, d[r]);
+                dx = r == 0 ? row.first(sd.out, sd.ot, sd.oh, Ring::ES) : row.second(dx, os, sd.out, sd.ot, sd.oh, Ring::ES);
+                if (row.in[r]) rope_store<DT, V, INTER>(dx, lane, d[r]);
             }
         });
     __syncthreads();                                       // the rings are free: they take the warps' sums

@@ -199,6 +199,15 @@ def test_slices_of_tables_gammas_and_broadcast_inputs(inter):
 
 
 @gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens", [1, 2, 3, 4, 33, 1000])
+@pytest.mark.parametrize("heads,kv,dim,sections", [(12, 2, 80, (10, 10, 20)), (28, 4, 128, None), (9, 3, 64, None), (1, 1, 256, (64, 64))])
+def test_turns_of_two_tokens(dtype, tokens, heads, kv, dim, sections):
+    """Heads in an odd number of the groups that a warp takes at a time: groups of two tokens, with places of their own, lie together."""
+    both(make(tokens, heads, kv, dim, dtype, seed=tokens + dim, sections=sections, inter=sections is not None, layout="packed"))
+
+
+@gpu
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("inter", [False, True])
 def test_in_place(dtype, inter):
