@@ -314,7 +314,8 @@ rmsq_status quant_mxfp4(const void* input, int64_t rows, int64_t hidden, int dty
 
 /* ---------------------------------------------------------------------------------------------
  * nvfp4_global_scale -- gs = 448 * 6 / max |input| over `count` elements, for quant_nvfp4: the largest block scale
- * lands on the largest E4M3 value. All zeros, or count == 0, give gs = 1; a maximum so small that gs would
+ * lands on the largest E4M3 value. It is 2688 times the reciprocal, each rounded to fp32 (as PyTorch forms a number
+ * over a tensor), so off by a unit in the last place at most. All zeros, or count == 0, give gs = 1; a maximum so small that gs would
  * overflow gives the largest fp32; a NaN gives NaN.
  *
  *   gs_out           DEVICE pointer to one fp32 (4-byte aligned)

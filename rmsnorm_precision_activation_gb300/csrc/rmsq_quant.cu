@@ -233,9 +233,11 @@ struct AmaxParams {
 
 constexpr int kAmaxThreads = 512;
 
+// The reciprocal's product, both rounded: the value that a number over a tensor has in PyTorch, and so in programs that form it
+// there. (A step of the quotient's last place would decide other ties: 0.4 % of the codes where the maximum is 52.)
 __device__ __forceinline__ float gs_of(float a)
 {
-    return a == 0.f ? 1.0f : a != a ? a : fminf(__fdiv_rn(448.0f * 6.0f, a), 3.402823466e38f);
+    return a == 0.f ? 1.0f : a != a ? a : fminf(__fmul_rn(448.0f * 6.0f, __frcp_rn(a)), 3.402823466e38f);
 }
 
 // Maximum over the CTA, in thread 0; NaN where one is.

@@ -97,10 +97,11 @@ def test_quotients_a_rounding_of_the_global_scale_off_a_boundary(dtype, top):
     x = make(256, 2048, torch.bfloat16, 11).float().clamp(-top, top)
     x[0, 0] = top
     x = x.to(dtype)
-    gs = rq().nvfp4_global_scale(x)
-    assert float(gs) == float(torch.tensor(2688.0) / top)
-    check(x, "nvfp4", gs=float(gs))
-    check(x, "nvfp4", gs=float(gs), swizzled=True)
+    gs = float(rq().nvfp4_global_scale(x))
+    assert gs == float(2688.0 * (torch.tensor(1.0) / top))
+    for g in {gs, float(torch.tensor(2688.0) / torch.tensor(top))}:
+        check(x, "nvfp4", gs=g)
+        check(x, "nvfp4", gs=g, swizzled=True)
 
 
 @gpu
@@ -212,7 +213,7 @@ def test_global_scale(dtype, count):
     x[-1] = 80.0
     for _ in range(2):
         gs = rq().nvfp4_global_scale(x)
-        assert float(gs) == float(torch.tensor(2688.0) / x.float().abs().max().cpu())
+        assert float(gs) == float(2688.0 * (torch.tensor(1.0) / x.float().abs().max().cpu()))
         x[-1] = 0.5
 
 
