@@ -340,7 +340,8 @@ rmsq_status nvfp4_global_scale(const void* input, int64_t count, int dtype, floa
  *   input_scale, weight_scale   their block scales in the layout RMSQ_SCALE_SWIZZLED_128x4; what the padding
  *                    holds does not matter
  *   input_gs, weight_gs   DEVICE pointers to one fp32 each (4-byte aligned), the global scales that the codes were
- *                    formed with, read by the kernel; NULL for 1
+ *                    formed with, read by the kernel; NULL for 1. Any finite ones but 0, subnormal or the largest
+ *                    (their product may leave fp32's range: a sum of 0 gives 0 all the same); 0 gives NaN or infinities
  *   bias             [n] of `output_dtype`, or NULL
  *   output           [m x n] of `output_dtype` (an rmsq_dtype)
  * k is a multiple of 32 up to RMSQ_MATMUL_FP4_MAX_K; m and n are at most RMSQ_MATMUL_MAX_ROWS, any numbers;

@@ -194,15 +194,55 @@ __device__ __forceinline__ void fp4_clear_tail(uint32_t stage, int k, int lane)
     __syncwarp();
 }
 
-// 1 / (gs_a gs_w) as a sum of two floats, so that the product of a sum with it is rounded once, in effect. (Plain factors
-// where the product of the two leaves the range in which its remainder is exact.)
-__device__ __forceinline__ float2 fp4_factor(const float* a_gs, const float* w_gs)
+// 1 / (gs_a gs_w) as a sum of two floats, high + low, so that the product of a sum with it is rounded once, in effect. Where it is past
+// 2^99 or below 2^-98 a factor before it, first + rest, takes a part: below, the power of two that is left of 2^-100, which is
+// exact (a sum is 0, or between 2^-20 and 2^41 in size); past, all but 2^100, so that the two parts of a product are never infinite
+// with opposite signs. So a sum of 0 stays 0, and no bits are lost but where results are subnormal. (Powers past 2^200 need not
+// be told from it: results are infinite, or 0.) Scales that are 0 or not finite: the plain quotients.
+struct Fp4Factor {
+    float high, low, first, rest;
+    // (from high alone: first and rest are formed again where they are needed, and take no registers elsewhere)
+    __device__ __forceinline__ bool split() const { return !(fabsf(high) > 1.6e-30f && fabsf(high) < 1.2e30f); }
+};
+
+// A float's significand, in [1, 2) and with its sign, and its power of two (a finite float other than 0).
+__device__ __forceinline__ float fp4_significand(float v, int& power)
 {
-    const float a = a_gs != nullptr ? *a_gs : 1.0f, w = w_gs != nullptr ? *w_gs : 1.0f, p = __fmul_rn(a, w);
-    if (!(fabsf(p) > 1e-30f && fabsf(p) < 1e30f)) return make_float2(__fmul_rn(__fdiv_rn(1.0f, a), __fdiv_rn(1.0f, w)), 0.f);
+    if (fabsf(v) < 1.17549435e-38f) {
+        v *= 16777216.0f;
+        power -= 24;
+    }
+    power += static_cast<int>((__float_as_uint(v) >> 23) & 0xFFu) - 127;
+    return __uint_as_float((__float_as_uint(v) & 0x807FFFFFu) | 0x3F800000u);
+}
+
+__device__ __forceinline__ float fp4_power(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+__device__ __forceinline__ Fp4Factor fp4_factor(const float* a_gs, const float* w_gs)
+{
+    const float a = a_gs != nullptr ? *a_gs : 1.0f, w = w_gs != nullptr ? *w_gs : 1.0f;
+    const float most = 3.402823466e38f;
+    if (!(fabsf(a) > 0.f && fabsf(a) <= most && fabsf(w) > 0.f && fabsf(w) <= most))
+        return {__fmul_rn(__fdiv_rn(1.0f, a), __fdiv_rn(1.0f, w)), 0.f, 1.0f, 0.f};
+    int power = 0;
+    const float ma = fp4_significand(a, power), mw = fp4_significand(w, power), p = __fmul_rn(ma, mw);
     const float high = __fdiv_rn(1.0f, p);
-    const float rest = __fsub_rn(__fmaf_rn(-high, p, 1.0f), __fmul_rn(high, __fmaf_rn(a, w, -p)));
-    return make_float2(high, __fmul_rn(high, rest));
+    const float low = __fmul_rn(high, __fsub_rn(__fmaf_rn(-high, p, 1.0f), __fmul_rn(high, __fmaf_rn(ma, mw, -p))));
+    power = max(-200, min(200, -power));
+    if (power > 99) return {fp4_power(100), 0.f, __fmul_rn(high, fp4_power(power - 100)), __fmul_rn(low, fp4_power(power - 100))};
+    const int left = power < -96 ? power + 100 : 0;
+    return {__fmul_rn(high, fp4_power(power - left)), __fmul_rn(low, fp4_power(power - left)), fp4_power(left), 0.f};
+}
+
+// Sums times the factor before the factor, where it is split.
+template <int N> __device__ __forceinline__ void fp4_first(uint32_t* v, const float* a_gs, const float* w_gs)
+{
+    const Fp4Factor f = fp4_factor(a_gs, w_gs);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float sum = __uint_as_float(v[i]);
+        v[i] = __float_as_uint(__fmaf_rn(sum, f.first, __fmul_rn(sum, f.rest)));
+    }
 }
 
 // Tokens that each CTA of a cluster of nc adds up: whole fours, which a thread sends together.
@@ -261,14 +301,14 @@ __device__ __forceinline__ void fp4_store(const uint32_t* v, char* out, uint32_t
 }
 
 template <int N, bool NV>
-__device__ __forceinline__ void fp4_store(const Fp4Params& p, const uint32_t* v, long long m, long long n, int left, float2 factor, float bias)
+__device__ __forceinline__ void fp4_store(const Fp4Params& p, const uint32_t* v, long long m, long long n, int left, Fp4Factor factor, float bias)
 {
     const uint32_t es = p.dt == DT_F32 ? 4 : 2, pitch = static_cast<uint32_t>(p.n) * es;
     char* const out = static_cast<char*>(p.out) + (m * p.n + n) * es;
     const bool in = n < p.n, words = p.n % 2 == 0;
-    if (p.dt == DT_BF16) fp4_store<DT_BF16, N, NV>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
-    else if (p.dt == DT_FP16) fp4_store<DT_FP16, N, NV>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
-    else fp4_store<DT_F32, N, NV>(v, out, pitch, left, splat(factor.x), splat(factor.y), splat(bias), in, words);
+    if (p.dt == DT_BF16) fp4_store<DT_BF16, N, NV>(v, out, pitch, left, splat(factor.high), splat(factor.low), splat(bias), in, words);
+    else if (p.dt == DT_FP16) fp4_store<DT_FP16, N, NV>(v, out, pitch, left, splat(factor.high), splat(factor.low), splat(bias), in, words);
+    else fp4_store<DT_F32, N, NV>(v, out, pitch, left, splat(factor.high), splat(factor.low), splat(bias), in, words);
 }
 
 // This thread's warp, from a lane of it: a number that the compiler knows to be the warp's own. What a warp does alone then stays
@@ -441,7 +481,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
         constexpr int PARTS = S::READERS / 4;                         // of the columns
         const int row = threadIdx.x & 127, part = warp >> 2;
         const long long n = static_cast<long long>(tn) * kFp4Rows + row, m0 = static_cast<long long>(tm) * NT;
-        const float2 factor = NV ? fp4_factor(p.a_gs, p.w_gs) : make_float2(1.f, 0.f);
+        const Fp4Factor factor = NV ? fp4_factor(p.a_gs, p.w_gs) : Fp4Factor{1.f, 0.f, 1.f, 0.f};
         const float bias = p.bias != nullptr && n < p.n ? load_as(p.bias, n, p.dt) : 0.f;
         if (nc > 1) cluster_wait();
         ok = mbar_wait<SCOPE_CTA>(acc_full, 0, limit);
@@ -458,6 +498,7 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                 if constexpr (LD == 32) tmem_ld_x16(acc + c + 16, v + 16);
                 tmem_wait_ld();
                 if (nc == 1) {
+                    if (NV && factor.split()) fp4_first<LD>(v, p.a_gs, p.w_gs);
                     fp4_store<LD, NV>(p, v, m0 + c, n, tokens - c, factor, bias);
                 } else {
 #pragma unroll
@@ -495,7 +536,8 @@ rmsq_fp4_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
                         v.z += __uint_as_float(o[r].z);
                         v.w += __uint_as_float(o[r].w);
                     }
-                    const uint32_t four[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
+                    uint32_t four[4] = {__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z), __float_as_uint(v.w)};
+                    if (NV && factor.split()) fp4_first<4>(four, p.a_gs, p.w_gs);
                     fp4_store<4, NV>(p, four, m0 + static_cast<int>(rank) * per + 4 * i, n, own - 4 * i, factor, bias);
                 }
             }

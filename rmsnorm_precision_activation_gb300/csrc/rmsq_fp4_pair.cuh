@@ -27,6 +27,8 @@
 //   warps 4-11   read the accumulator and write the output: two warps per 32 channels, taking every other 32 tokens
 #pragma once
 
+#include <type_traits>
+
 #include "rmsq_fp4.cuh"
 #include "rmsq_matmul_pair.cuh"
 
@@ -251,40 +253,47 @@ rmsq_fp4_pair_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_con
     } else if (warp >= 4) {
         const int wg = (warp - 4) >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-        const float2 factor = NV ? fp4_factor(p.a_gs, p.w_gs) : make_float2(1.f, 0.f);
-        uint32_t done = 0;
-        for (long long tile = first; tile < ntiles && ok; tile += stride, ++done) {
-            const uint32_t b = done & 1u;
-            int tn, tm;
-            tc_tile(tile, tiles, tn, tm);
-            const long long n = (static_cast<long long>(tn) * 2 + rank) * kFp4Rows + row;
-            const float bias = p.bias != nullptr && n < p.n ? load_as(p.bias, n, p.dt) : 0.f;
-            ok = mbar_wait<SCOPE_CTA>(acc_full + 8 * b, (done >> 1) & 1u, limit);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            // 32 columns at a time, the shared ones first: the first accumulator's last 96, the second's first 96
+        const Fp4Factor factor = NV ? fp4_factor(p.a_gs, p.w_gs) : Fp4Factor{1.f, 0.f, 1.f, 0.f};
+        // (twice, for the few calls whose factor is split: a test for each 32 columns takes 2 % longer at 8192 x 8192 x 1024)
+        const auto read = [&](auto split) {
+            constexpr bool SPLIT = decltype(split)::value;
+            uint32_t done = 0;
+            for (long long tile = first; tile < ntiles && ok; tile += stride, ++done) {
+                const uint32_t b = done & 1u;
+                int tn, tm;
+                tc_tile(tile, tiles, tn, tm);
+                const long long n = (static_cast<long long>(tn) * 2 + rank) * kFp4Rows + row;
+                const float bias = p.bias != nullptr && n < p.n ? load_as(p.bias, n, p.dt) : 0.f;
+                ok = mbar_wait<SCOPE_CTA>(acc_full + 8 * b, (done >> 1) & 1u, limit);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                tc_fence_after();
+                // 32 columns at a time, the shared ones first: the first accumulator's last 96, the second's first 96
 #pragma unroll 1
-            for (int i = 0; i < 4; i += 2) {
-                const int c0 = b == 0 ? 6 + wg - 2 * i : wg + 2 * i, c1 = b == 0 ? c0 - 2 : c0 + 2;
-                uint32_t v[64];
-                const uint32_t at = lanes + b * S::SECOND;
-                tmem_ld_x16(at + 32 * c0, v);
-                tmem_ld_x16(at + 32 * c0 + 16, v + 16);
-                tmem_ld_x16(at + 32 * c1, v + 32);
-                tmem_ld_x16(at + 32 * c1 + 16, v + 48);
-                tmem_wait_ld();
-                if (i == 0) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_leader_relaxed(acc_free);
+                for (int i = 0; i < 4; i += 2) {
+                    const int c0 = b == 0 ? 6 + wg - 2 * i : wg + 2 * i, c1 = b == 0 ? c0 - 2 : c0 + 2;
+                    uint32_t v[64];
+                    const uint32_t at = lanes + b * S::SECOND;
+                    tmem_ld_x16(at + 32 * c0, v);
+                    tmem_ld_x16(at + 32 * c0 + 16, v + 16);
+                    tmem_ld_x16(at + 32 * c1, v + 32);
+                    tmem_ld_x16(at + 32 * c1 + 16, v + 48);
+                    tmem_wait_ld();
+                    if (i == 0) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_leader_relaxed(acc_free);
+                    }
+                    const long long m0 = static_cast<long long>(tm) * kFp4PairTokens;
+                    const int left = static_cast<int>(min(static_cast<long long>(kFp4PairTokens), p.m - m0));
+                    if constexpr (SPLIT) fp4_first<64>(v, p.a_gs, p.w_gs);
+                    fp4_store<32, NV>(p, v, m0 + 32 * c0, n, left - 32 * c0, factor, bias);
+                    fp4_store<32, NV>(p, v + 32, m0 + 32 * c1, n, left - 32 * c1, factor, bias);
                 }
-                const long long m0 = static_cast<long long>(tm) * kFp4PairTokens;
-                const int left = static_cast<int>(min(static_cast<long long>(kFp4PairTokens), p.m - m0));
-                fp4_store<32, NV>(p, v, m0 + 32 * c0, n, left - 32 * c0, factor, bias);
-                fp4_store<32, NV>(p, v + 32, m0 + 32 * c1, n, left - 32 * c1, factor, bias);
             }
-        }
+        };
+        if (NV && factor.split()) read(std::true_type());
+        else read(std::false_type());
         if (!ok && lane == 0) atomicOr(p.err, ERRF_WAIT_TIMEOUT);
     }
 
