@@ -1,0 +1,46 @@
+"""nvfp4_global_scale and the 4-bit quantisation at the ends of float's range, as include/rmsq.h states them."""
+from fractions import Fraction
+
+import pytest
+import torch
+
+import fp4_common as F
+from gpu_common import rq
+
+gpu = pytest.mark.gpu
+
+
+def global_scales(tops, dtype, count):
+    """The global scale of a tensor of `count` elements whose largest magnitude is tops[i], for every i."""
+    x = torch.zeros((len(tops), count), dtype=dtype, device="cuda")
+    x[:, count // 3] = torch.tensor(tops, dtype=torch.float64).to(dtype).cuda()
+    got = torch.cat([rq().nvfp4_global_scale(row) for row in x]).cpu()
+    return x[:, count // 3].float().cpu(), got
+
+
+def units_off(top, gs):
+    """How far gs is from 2688 / top, in units of the exact quotient's last place (a float's)."""
+    exact = Fraction(2688) / Fraction(top)
+    e = 0
+    while Fraction(2) ** (e + 1) <= exact:
+        e += 1
+    while Fraction(2) ** e > exact:
+        e -= 1
+    return abs(Fraction(gs) - exact) / Fraction(2) ** (max(e, -126) - 23)
+
+
+@gpu
+@pytest.mark.parametrize("count", [40, 70000])
+def test_the_global_scale_is_near_the_quotient(count):
+    """Two roundings: half a unit of the last place, and the reciprocal's half unit times the ratio of the two mantissas, which is
+    1.3125 at most (2688 = 1.3125 2^11): 1.16 units. One rounding where the reciprocal would be a subnormal float: half a unit."""
+    g = torch.Generator().manual_seed(5)
+    mantissas = [1.0, 1.0 + 2.0 ** -23, 1.3125, 1.5, 2.0 - 2.0 ** -23] + (1 + torch.rand(40, generator=g)).tolist()
+    for power in (-100, -20, 0, 7, 60, 125, 126, 127):
+        top, got = global_scales([m * 2.0 ** power for m in mantissas], torch.float32, count)
+        off = [units_off(a, b) for a, b in zip(top.tolist(), got.tolist())]
+        assert max(off) <= (Fraction(1, 2) if power > 126 else Fraction(116, 100)), (power, float(max(off)))
+    for dtype in (torch.bfloat16, torch.float32):
+        m = torch.finfo(dtype).max
+        top, got = global_scales([m, m / 2, m / 4], dtype, count)
+        assert max(units_off(a, b) for a, b in zip(top.tolist(), got.tolist())) <= Fraction(116, 100)
