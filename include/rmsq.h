@@ -316,7 +316,9 @@ rmsq_status quant_mxfp4(const void* input, int64_t rows, int64_t hidden, int dty
  * nvfp4_global_scale -- gs = 448 * 6 / max |input| over `count` elements, for quant_nvfp4: the largest block scale
  * lands on the largest E4M3 value. It is 2688 times the reciprocal, each rounded to fp32 (as PyTorch forms a number
  * over a tensor), so off by 1.16 units in the last place at most; for maxima above 2^126 the quotient rounded once. All zeros,
- * or count == 0, give gs = 1; a maximum so small that gs would overflow gives the largest fp32; a NaN gives NaN.
+ * or count == 0, give gs = 1; a maximum so small that gs would overflow gives the largest fp32; a NaN gives NaN. An infinity
+ * gives 0, which is no global scale: under it every finite block has scale 0, and a product is NaN throughout, not in that row
+ * alone. A program that may meet one checks for it, or keeps a calibrated scale.
  *
  *   gs_out           DEVICE pointer to one fp32 (4-byte aligned)
  *   workspace        device memory of at least nvfp4_global_scale_workspace(count) bytes (none for small tensors:

@@ -556,7 +556,8 @@ def nvfp4_global_scale(input, *, out=None, workspace=None, stream=None):
     """gs = 448 * 6 / max |input|, computed on the device (quant_nvfp4's global_scale). workspace: a CUDA uint8
     tensor of nvfp4_global_scale_workspace(input.numel()) bytes, allocated when not passed.
 
-    Returns a CUDA float32 tensor of one element."""
+    Returns a CUDA float32 tensor of one element: 1 for zeros, NaN where the input has a NaN, 0 (no scale to quantise by)
+    where it has an infinity."""
     if _elsewhere(input, stream):
         with _queue(input, stream):
             return nvfp4_global_scale(input, out=out, workspace=workspace)

@@ -44,3 +44,21 @@ def test_the_global_scale_is_near_the_quotient(count):
         m = torch.finfo(dtype).max
         top, got = global_scales([m, m / 2, m / 4], dtype, count)
         assert max(units_off(a, b) for a, b in zip(top.tolist(), got.tolist())) <= Fraction(116, 100)
+
+
+@gpu
+@pytest.mark.parametrize("swizzled", [False, True])
+def test_a_tensor_with_an_infinity_has_no_global_scale(swizzled):
+    """It is 0; under it every block has scale 0 but the infinity's, and a product is NaN throughout."""
+    q, g = rq(), torch.Generator(device="cuda").manual_seed(2)
+    x, w = (torch.randn((n, 64), generator=g, device="cuda").bfloat16() for n in (6, 32))
+    x[2, 40] = float("-inf")
+    gs = q.nvfp4_global_scale(x)
+    assert float(gs) == 0.0
+    c, s = q.quant_nvfp4(x, global_scale=gs, swizzled=True)
+    rows = F.untiled(s.view(torch.uint8), 6, 4)[0]
+    hit = torch.zeros_like(rows, dtype=torch.bool)
+    hit[2, 2] = True
+    assert bool((rows[hit] == 0x7F).all()) and bool((rows[~hit] == 0).all())
+    w4, ws = q.quant_nvfp4(w, swizzled=True)
+    assert torch.isnan(q.matmul_nvfp4(c, s, w4, ws, input_global_scale=gs)).all()
