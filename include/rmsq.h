@@ -300,7 +300,8 @@ rmsq_status matmul_int8(const void* input, const float* input_scale, const void*
  *   output           [rows x hidden / 2] bytes, two E2M1 codes per byte (element 2k low nibble)
  *   block_scale      E4M3 / UE8M0 codes in `scale_layout`
  * Codes are the formula's exactly: the nearest to the exact quotient, ties to the even code, with the block's scale as
- * stored. (That is formed from the fp32 nearest to gs * amax_b / 6.) A block with a NaN or an infinity gets scale
+ * stored; but MXFP4 blocks of scale code 0, whose elements are at most 6 * 2^-127, get codes 0, as the norms' do (first lines of
+ * this header), although code 0 stands for 2^-127. (That is formed from the fp32 nearest to gs * amax_b / 6.) A block with a NaN or an infinity gets scale
  * NaN (E4M3 0x7F, UE8M0 255) and any codes, so a product gives NaN for its row; so does every block where gs is a NaN
  * (a tensor's that has one). Zeros may have either sign.
  * ------------------------------------------------------------------------------------------- */

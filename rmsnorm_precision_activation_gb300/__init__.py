@@ -643,7 +643,8 @@ def quant_nvfp4(input, *, global_scale=None, output=None, block_scale=None, swiz
 
 
 def quant_mxfp4(input, *, output=None, block_scale=None, swizzled=False, stream=None):
-    """MXFP4 (packed E2M1, UE8M0 scale per 32 elements) of a tensor that comes from no norm.
+    """MXFP4 (packed E2M1, UE8M0 scale per 32 elements) of a tensor that comes from no norm. Blocks whose elements are at most
+    6 * 2^-127 become zeros.
 
     Returns (output uint8 [..., H/2], block_scale uint8 (UE8M0 codes))."""
     if _elsewhere(input, stream):

@@ -2,7 +2,7 @@
 // include/rmsq.h).
 //
 //   NVFP4  per 16 elements: s_b = E4M3(min(gs amax_b / 6, 448));  q = E2M1(x gs / s_b);  gs = 2688 / max |x|
-//   MXFP4  per 32 elements: e_b = clamp(ceil(log2(amax_b / 6)) + 127, 0, 255);  q = E2M1(x 2^(127 - e_b))
+//   MXFP4  per 32 elements: e_b = clamp(ceil(log2(amax_b / 6)) + 127, 0, 255);  q = E2M1(x 2^(127 - e_b)), 0 where e_b = 0
 //
 // Bound by HBM: an element of 16 bits is read once and leaves as 4 bits and its part of a scale. A thread takes 16
 // neighbours, so a block's maximum needs no more than one exchange, and codes leave as 8 bytes a thread.

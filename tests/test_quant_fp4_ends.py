@@ -62,3 +62,22 @@ def test_a_tensor_with_an_infinity_has_no_global_scale(swizzled):
     assert bool((rows[hit] == 0x7F).all()) and bool((rows[~hit] == 0).all())
     w4, ws = q.quant_nvfp4(w, swizzled=True)
     assert torch.isnan(q.matmul_nvfp4(c, s, w4, ws, input_global_scale=gs)).all()
+
+
+@gpu
+@pytest.mark.parametrize("swizzled", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_mxfp4_blocks_of_the_smallest_scale_are_zeros(dtype, swizzled):
+    """Blocks up to 6 2^-127, whose scale code is 0; one step above the code is 1 and the values stay."""
+    top = torch.tensor(6.0 * 2.0 ** -127, dtype=torch.float64).to(dtype).cuda()
+    above = torch.nextafter(top, torch.tensor(1.0, dtype=dtype, device="cuda"))
+    x = torch.zeros((5, 64), dtype=dtype, device="cuda")
+    x[0, 3], x[1, 3], x[2, 3], x[3, 40] = top, above, -top, -above
+    x[4, :32] = 1.0
+    c, s = rq().quant_mxfp4(x, swizzled=swizzled)
+    s = F.untiled(s, 5, 2)[0] if swizzled else s
+    assert s.tolist() == [[0, 0], [1, 0], [0, 0], [0, 1], [125, 0]]
+    want = torch.zeros((5, 64), dtype=torch.float64, device="cuda")
+    want[1, 3], want[3, 40] = 3.0 * 2.0 ** -126, -3.0 * 2.0 ** -126
+    want[4, :32] = 1.0
+    assert torch.equal(F.decoded(c, s, "mxfp4"), want)
