@@ -160,6 +160,8 @@ rmsq_status rmsnorm_quant_mxfp4(const void* input, const void* residual, void* r
  * One kernel launch: its last CTA turns the launch's running maximum into gs, using two words of
  * a per-launch slot of the library's scratch pool (4096 slots, taken in turn, left at zero), so
  * launches on different streams that run at the same time stay apart unless 4096 launches apart.
+ * gs is the quotient rounded once. (nvfp4_global_scale, of a tensor as it is, forms it in two roundings: for the same maximum
+ * the two may differ in the last place, which decides ties. Pass a product the very gs that the codes were formed with.)
  * Arguments as for rmsnorm_quant_nvfp4 (no outputs besides gs_out).
  * ------------------------------------------------------------------------------------------- */
 rmsq_status rmsnorm_nvfp4_global_scale(const void* input, const void* residual,
@@ -316,7 +318,9 @@ rmsq_status quant_mxfp4(const void* input, int64_t rows, int64_t hidden, int dty
 /* ---------------------------------------------------------------------------------------------
  * nvfp4_global_scale -- gs = 448 * 6 / max |input| over `count` elements, for quant_nvfp4: the largest block scale
  * lands on the largest E4M3 value. It is 2688 times the reciprocal, each rounded to fp32 (as PyTorch forms a number
- * over a tensor), so off by 1.16 units in the last place at most; for maxima above 2^126 the quotient rounded once. All zeros,
+ * over a tensor), so off by 1.16 units in the last place at most; for maxima above 2^126 the quotient rounded once.
+ * (rmsnorm_nvfp4_global_scale rounds the quotient once throughout; see there. The codes differ likewise at boundaries: these
+ * are the formula's exactly, rmsnorm_quant_nvfp4's are formed with a rounded factor.) All zeros,
  * or count == 0, give gs = 1; a maximum so small that gs would overflow gives the largest fp32; a NaN gives NaN. An infinity
  * gives 0, which is no global scale: under it every finite block has scale 0, and a product is NaN throughout, not in that row
  * alone. A program that may meet one checks for it, or keeps a calibrated scale.
