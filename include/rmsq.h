@@ -429,6 +429,9 @@ rmsq_status rmsnorm_rope(const rmsq_heads* query, const rmsq_heads* key, const v
  *   workspace        device memory of at least rmsnorm_rope_backward_workspace(tokens, dim) bytes, 16-byte
  *                    aligned, used by this call alone until it ends on the stream. Its contents before do
  *                    not matter.
+ * A position outside 0 to places - 1 (padding marked by -1, for instance) reads nothing; the gradients of the heads that it
+ * rotates are NaN, and so are the gammas' gradients of the elements it rotates, whose sums they are part of: leave such
+ * tokens out, or give them a place in the table and gradients of 0.
  * Sums are held in fp32 and added in a fixed order: the same inputs give the same bits. tokens == 0 writes zeros
  * to grad_query_gamma and grad_key_gamma. Other arguments and sizes as for rmsnorm_rope; RMSQ_ERR_SHAPE also for a
  * workspace that is too small.

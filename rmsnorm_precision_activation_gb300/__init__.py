@@ -827,7 +827,8 @@ def rmsnorm_rope_backward(grad_query, grad_key, query, key, query_gamma, key_gam
                           query_gamma_grad=None, key_gamma_grad=None, param_grad_dtype=None, workspace=None, stream=None):
     """The gradients of rmsnorm_rope. grad_query, grad_key: the gradients of its outputs; query, key and the rest: its
     inputs. param_grad_dtype: type of the gammas' gradients, the input's (default) or torch.float32. query_grad and
-    key_grad may be grad_query and grad_key themselves. workspace: a CUDA uint8 tensor of
+    key_grad may be grad_query and grad_key themselves. A position outside the table gives NaN in its token's gradients and
+    in the gammas' rotated elements (for padding: a place in the table, and gradients of 0). workspace: a CUDA uint8 tensor of
     rmsnorm_rope_backward_workspace(tokens, D) bytes, allocated when not passed.
 
     Returns (query_grad [..., heads, D], key_grad [..., kv_heads, D], query_gamma_grad [D], key_gamma_grad [D])."""
