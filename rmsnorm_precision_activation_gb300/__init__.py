@@ -796,8 +796,9 @@ def rmsnorm_rope(query, key, query_gamma, key_gamma, cos, sin, positions, *, sec
                  weight_offset=0.0, query_output=None, key_output=None, stream=None):
     """RMS norm of every head's query and key, then the rotation by the token's position.
 
-    query [..., heads, D] and key [..., kv_heads, D], the last dimension contiguous, otherwise with any strides (slices
-    of a projection's output); gammas [D]; cos and sin float32 [places, R / 2], R <= D elements of a head being rotated;
+    query [..., heads, D] and key [..., kv_heads, D], the last dimension contiguous, the heads and the tokens with any stride
+    each (slices of a projection's output; [heads, tokens, D] transposed); several leading dimensions must lie behind each other
+    as one does, which a transposed batch of [batch, heads, tokens, D] does not: ValueError. gammas [D]; cos and sin float32 [places, R / 2], R <= D elements of a head being rotated;
     positions int32 or int64 [...], or [axes, ...] with sections, which says how many of the R / 2 frequencies go by
     each axis. interleaved: neighbours are rotated together, instead of the halves of the R elements. A position outside
     the table gives NaN. query_output and key_output may be query and key themselves.
