@@ -386,6 +386,8 @@ rmsq_status matmul_mxfp4(const void* input, const void* input_scale, const void*
  * Pointers here need only be aligned to an element; rows that all start on 16-byte boundaries are read fastest.
  * dim is even, from 2 to RMSQ_ROPE_MAX_DIM; rotated is even, from 2 to dim; tokens from 0 to
  * RMSQ_ROPE_MAX_TOKENS. A head that is not finite gives NaN in that head alone (an infinity: NaN or 0).
+ * Squares are added in fp32: a finite head whose sum of them passes fp32's range (elements of 2^60 or so) comes out as 0,
+ * with gradients of 0.
  * ------------------------------------------------------------------------------------------- */
 #define RMSQ_ROPE_MAX_DIM 512
 #define RMSQ_ROPE_MAX_TOKENS 134217727
